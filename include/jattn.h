@@ -51,7 +51,8 @@ typedef uint16_t jattn_bf16; /* bfloat16 bit pattern */
 typedef enum {
   JATTN_OK = 0,
   JATTN_ERR_INVALID_ARG = 1, /* null pointer, B/H/d <= 0, N_img/N_txt < 0, N < 1, size overflow */
-  JATTN_ERR_UNSUPPORTED = 2, /* d not in {64, 128}; jattn_qkv_norm: C not a multiple of 8 */
+  JATTN_ERR_UNSUPPORTED = 2, /* d not in {64, 128}; jattn_qkv_norm, token rows: C not a multiple of 8 (token rows:
+                                or above JATTN_MAX_WIDTH) */
   JATTN_ERR_MISALIGNED = 3,  /* a pointer is not 16-byte aligned */
   JATTN_ERR_ALIAS = 4,       /* an output buffer overlaps an input or another output */
   JATTN_ERR_CUDA = 5,        /* a CUDA launch or allocation failed */
@@ -209,6 +210,58 @@ int jattn_fwd_saved(const jattn_bf16* v, int B, int H, int N_img, int N_txt, int
                     void* saved, void* stream);
 
 /*
+ * Token rows: the residual's addition with RMSNorm over the model width, and
+ * rows in 8 bits with scales.  (The steps before the QKV projection; the pages
+ * name no code for them.)  For T rows of C values, row-major and contiguous:
+ *
+ *   h = bf16(x + res)                       (without res: h is x)
+ *   r = (mean_c h_c^2 + eps)^(-1/2)         fp32
+ *   z = g * h * r                           fp32
+ *   y = bf16(z), or 8 bits: m = max(max_c |z_c|, 2^-80), s = m / 448 (fp32),
+ *                           y8 = e4m3(448 z / m)
+ *
+ * e4m3 is 1 sign, 4 exponent and 3 mantissa bits, largest finite value 448,
+ * one byte a value; a row stands for s * y8.  The sum of squares is fp32: a
+ * row whose mean square passes the fp32 range comes out as zeros.  A row with
+ * a NaN comes out as NaN (jattn_quant_rows: the NaN values stay NaN and do not
+ * enter the row's maximum); 8-bit rows with an infinite z read NaN.
+ *   x     : [T, C] bf16
+ *   res   : [T, C] bf16 or NULL
+ *   g     : [C] float32
+ *   T, C  : T >= 1 rows; C a multiple of 8, at most JATTN_MAX_WIDTH (else
+ *           JATTN_ERR_UNSUPPORTED).  T * C may pass 2^31.
+ *   eps   : > 0 and finite
+ *   h     : [T, C] bf16, overwritten; it may be res itself (the residual
+ *           stream updated in place), and is NULL exactly if res is
+ *   y, y8 : [T, C] bf16, or bytes
+ *   s     : [T] float32
+ *   r     : [T] float32, or NULL when no backward will run
+ * jattn_quant_rows does the last step alone on z = x (weights once when they
+ * are loaded, or tokens that another norm made).
+ *
+ * jattn_add_norm_bwd: with n = h r and u = g dy, for the gradients dy of y and
+ * dh of h (or NULL: none),
+ *
+ *   dx = dh + r (u - n mean_c(u n)),    dg = sum_t dy n
+ *
+ * dx [T, C] bf16 is the gradient of x and of res alike, and may be dh itself;
+ * dg [C] float32 is summed in a fixed order that T and C alone set, so both
+ * repeat bit for bit.  h and r are the forward's (without res, h is x).
+ *   work  : jattn_add_norm_bwd_bytes(T, C) bytes, contents of no meaning
+ *           before or after; calls that overlap on the GPU need one each.
+ * jattn_add_norm_bwd_bytes returns 0 for sizes the call would reject.
+ */
+#define JATTN_MAX_WIDTH 16384
+int jattn_add_norm(const jattn_bf16* x, const jattn_bf16* res, const float* g, int T, int C, float eps,
+                   jattn_bf16* h, jattn_bf16* y, float* r, void* stream);
+int jattn_add_norm_fp8(const jattn_bf16* x, const jattn_bf16* res, const float* g, int T, int C, float eps,
+                       jattn_bf16* h, uint8_t* y8, float* s, float* r, void* stream);
+int jattn_quant_rows(const jattn_bf16* x, int T, int C, uint8_t* x8, float* s, void* stream);
+size_t jattn_add_norm_bwd_bytes(int T, int C);
+int jattn_add_norm_bwd(const jattn_bf16* dy, const jattn_bf16* dh, const jattn_bf16* h, const float* r,
+                       const float* g, int T, int C, jattn_bf16* dx, float* dg, void* work, void* stream);
+
+/*
  * Forward without any device allocation.  (No counterpart on the pages: an
  * integration entry point.)  Same arguments, layout and results as jattn_fwd,
  * but the scratch it needs (the normalised q_hat and k_hat, 2 * 2 * B*H*N*d
@@ -276,6 +329,17 @@ typedef enum {
   JATTN_KERNEL_QKV_NORM = 5,     /* QKV projection of both streams with the QK-RMSNorm epilogue */
   JATTN_KERNEL_COUNT = 6
 } jattn_kernel_kind;
+
+/* Kinds of the token-row kernels, numbered apart from the attention path's
+ * (jattn_profile_read and jattn_kernel_name take both). */
+typedef enum {
+  JATTN_TOKEN_KERNEL_FIRST = 16,
+  JATTN_KERNEL_ADD_NORM = 16,      /* residual + RMSNorm, either output */
+  JATTN_KERNEL_ADD_NORM_BWD = 17,  /* its backward: dx and partial sums of dg */
+  JATTN_KERNEL_ADD_NORM_DG = 18,   /* dg from the partial sums */
+  JATTN_KERNEL_QUANT_ROWS = 19,    /* rows to 8 bits */
+  JATTN_TOKEN_KERNEL_END = 20
+} jattn_token_kernel_kind;
 
 int jattn_profile_enable(int on);
 int jattn_profile_reset(void);

@@ -11,7 +11,9 @@ from ._binding import (KERNEL_KINDS, STATUS, STATUS_CODE, JattnError, declared_s
                        jattn_set_deterministic, jattn_kernel_name, jattn_last_device_error, jattn_last_error_message, jattn_profile_enable, jattn_profile_read,
                        jattn_profile_reset, jattn_status_string, jattn_version, load_library, profile_snapshot,
                        jattn_saved_bytes, jattn_saved_bytes_varlen, jattn_fwd_train, jattn_bwd_train,
-                       jattn_fwd_train_varlen, jattn_bwd_train_varlen, jattn_qkv_norm, jattn_fwd_saved)
+                       jattn_fwd_train_varlen, jattn_bwd_train_varlen, jattn_qkv_norm, jattn_fwd_saved,
+                       TOKEN_KERNEL_KINDS, jattn_add_norm, jattn_add_norm_fp8, jattn_quant_rows,
+                       jattn_add_norm_bwd_bytes, jattn_add_norm_bwd)
 
 __all__ = ["STATUS", "STATUS_CODE", "JattnError", "declared_symbols", "jattn_bwd", "jattn_fwd",
            "jattn_last_device_error", "jattn_status_string", "jattn_version", "load_library", "forward",
@@ -21,7 +23,9 @@ __all__ = ["STATUS", "STATUS_CODE", "JattnError", "declared_symbols", "jattn_bwd
            "jattn_selftest_wait_timeout", "jattn_set_sm_limit", "jattn_set_deterministic", "jattn_saved_bytes",
            "jattn_saved_bytes_varlen", "jattn_fwd_train", "jattn_bwd_train", "jattn_fwd_train_varlen",
            "jattn_bwd_train_varlen", "forward_train", "backward_train", "jattn_qkv_norm", "jattn_fwd_saved",
-           "qkv_norm"]
+           "qkv_norm", "TOKEN_KERNEL_KINDS", "jattn_add_norm", "jattn_add_norm_fp8", "jattn_quant_rows",
+           "jattn_add_norm_bwd_bytes", "jattn_add_norm_bwd", "add_norm", "add_norm_fp8", "add_norm_backward",
+           "quant_rows"]
 
 
 def forward(q, k, v, gq, gk, n_txt: int, stream=None):
@@ -114,3 +118,73 @@ def qkv_norm(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, H: int, stream=No
     jattn_qkv_norm(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, B, H, N_img, N_txt, d, C, q, k, v, saved,
                    stream)
     return q, k, v, saved
+
+
+def _outputs_on(stream, *tensors):
+    """Context in which a call's outputs are allocated: the launching stream's, so that the allocator
+    orders their reuse by it.  The call runs on the current device, where its tensors must be."""
+    import contextlib
+
+    import torch
+
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def add_norm(x, g, residual=None, eps: float = 1e-6, stream=None):
+    """y, h, r: RMSNorm of the token rows h = x + residual (h is x without a residual) over their
+    last axis with gain g [C] fp32.  x, residual, h, y [..., C] bf16; r [...] fp32, the rows' 1/rms
+    for add_norm_backward."""
+    import torch
+
+    C = g.numel()
+    with _outputs_on(stream, x, g, residual):
+        y = torch.empty_like(x)
+        h = x if residual is None else torch.empty_like(x)
+        r = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    jattn_add_norm(x, residual, g, r.numel(), C, eps, None if residual is None else h, y, r, stream)
+    return y, h, r
+
+
+def add_norm_fp8(x, g, residual=None, eps: float = 1e-6, stream=None):
+    """y8, scale, h, r: add_norm with 8-bit rows: y8 [..., C] float8_e4m3fn and scale [...] fp32, a row
+    standing for scale * y8 (what qkv_norm_fp8 reads)."""
+    import torch
+
+    C = g.numel()
+    with _outputs_on(stream, x, g, residual):
+        y8 = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        h = x if residual is None else torch.empty_like(x)
+        r = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        scale = torch.empty_like(r)
+    jattn_add_norm_fp8(x, residual, g, r.numel(), C, eps, None if residual is None else h, y8, scale, r, stream)
+    return y8, scale, h, r
+
+
+def add_norm_backward(dy, h, r, g, dh=None, stream=None):
+    """dx, dg from add_norm's h and r: dx is the gradient of x and of the residual alike; dh is the
+    gradient of h from later uses of it (None: none)."""
+    import torch
+
+    T, C = r.numel(), g.numel()
+    with _outputs_on(stream, dy, h, r, g, dh):
+        dx, dg = torch.empty_like(dy), torch.empty_like(g)
+        work = torch.empty(jattn_add_norm_bwd_bytes(T, C), dtype=torch.uint8, device=dy.device)
+    jattn_add_norm_bwd(dy, dh, h, r, g, T, C, dx, dg, work, stream)
+    return dx, dg
+
+
+def quant_rows(x, stream=None):
+    """x8, scale: rows of the last axis in 8 bits (float8_e4m3fn), a row standing for scale * x8."""
+    import torch
+
+    with _outputs_on(stream, x):
+        x8 = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    jattn_quant_rows(x, scale.numel(), x.shape[-1], x8, scale, stream)
+    return x8, scale

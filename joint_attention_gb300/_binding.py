@@ -104,12 +104,24 @@ def load_library(path: str | None = None, build_if_missing: bool = False) -> cty
     lib.jattn_qkv_norm.restype = i32
     lib.jattn_fwd_saved.argtypes = [vp] + [i32] * 5 + [vp] * 4
     lib.jattn_fwd_saved.restype = i32
+    f32c = ctypes.c_float
+    lib.jattn_add_norm.argtypes = [vp] * 3 + [i32, i32, f32c] + [vp] * 4
+    lib.jattn_add_norm.restype = i32
+    lib.jattn_add_norm_fp8.argtypes = [vp] * 3 + [i32, i32, f32c] + [vp] * 5
+    lib.jattn_add_norm_fp8.restype = i32
+    lib.jattn_quant_rows.argtypes = [vp, i32, i32] + [vp] * 3
+    lib.jattn_quant_rows.restype = i32
+    lib.jattn_add_norm_bwd_bytes.argtypes = [i32, i32]
+    lib.jattn_add_norm_bwd_bytes.restype = sz
+    lib.jattn_add_norm_bwd.argtypes = [vp] * 5 + [i32, i32] + [vp] * 4
+    lib.jattn_add_norm_bwd.restype = i32
     if path is None:
         _lib = lib
     return lib
 
 
 KERNEL_KINDS = 6
+TOKEN_KERNEL_KINDS = range(16, 20)  # the token-row kernels' kinds, numbered apart
 
 
 def jattn_profile_enable(on: bool = True) -> int:
@@ -135,7 +147,7 @@ def jattn_kernel_name(kind: int) -> str:
 
 def profile_snapshot() -> dict:
     """{kernel name: (launches, total ms)} for every kernel kind."""
-    return {jattn_kernel_name(k): jattn_profile_read(k) for k in range(KERNEL_KINDS)}
+    return {jattn_kernel_name(k): jattn_profile_read(k) for k in (*range(KERNEL_KINDS), *TOKEN_KERNEL_KINDS)}
 
 
 def declared_symbols(header: str = HEADER) -> list[str]:
@@ -413,6 +425,80 @@ def jattn_fwd_saved(v, B: int, H: int, N_img: int, N_txt: int, d: int, out, lse,
                              _ptr(lse, "lse", f32, r), _saved_ptr(saved, nb), _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_fwd_saved")
+    return rc
+
+
+def jattn_add_norm(x, res, g, T: int, C: int, eps: float, h, y, r, stream=None, check: bool = True) -> int:
+    """C ABI jattn_add_norm.  x / res / h / y [T, C] bf16 (res and h both or neither; h may be res),
+    g [C] fp32, r [T] fp32 or None."""
+    import torch
+
+    bf, f32, e = torch.bfloat16, torch.float32, T * C
+    rc = load_library().jattn_add_norm(_ptr(x, "x", bf, e), _ptr(res, "res", bf, e), _ptr(g, "g", f32, C), T, C, eps,
+                                       _ptr(h, "h", bf, e), _ptr(y, "y", bf, e), _ptr(r, "r", f32, T),
+                                       _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_add_norm")
+    return rc
+
+
+def jattn_add_norm_fp8(x, res, g, T: int, C: int, eps: float, h, y8, s, r, stream=None, check: bool = True) -> int:
+    """C ABI jattn_add_norm_fp8: jattn_add_norm with y8 [T, C] float8_e4m3fn and the rows' scales s [T] fp32."""
+    import torch
+
+    bf, f32, e = torch.bfloat16, torch.float32, T * C
+    rc = load_library().jattn_add_norm_fp8(_ptr(x, "x", bf, e), _ptr(res, "res", bf, e), _ptr(g, "g", f32, C), T, C,
+                                           eps, _ptr(h, "h", bf, e), _ptr(y8, "y8", torch.float8_e4m3fn, e),
+                                           _ptr(s, "s", f32, T), _ptr(r, "r", f32, T), _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_add_norm_fp8")
+    return rc
+
+
+def jattn_quant_rows(x, T: int, C: int, x8, s, stream=None, check: bool = True) -> int:
+    """C ABI jattn_quant_rows.  x [T, C] bf16 to x8 [T, C] float8_e4m3fn and s [T] fp32."""
+    import torch
+
+    e = T * C
+    rc = load_library().jattn_quant_rows(_ptr(x, "x", torch.bfloat16, e), T, C,
+                                         _ptr(x8, "x8", torch.float8_e4m3fn, e), _ptr(s, "s", torch.float32, T),
+                                         _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_quant_rows")
+    return rc
+
+
+def jattn_add_norm_bwd_bytes(T: int, C: int) -> int:
+    """C ABI jattn_add_norm_bwd_bytes: size of the work buffer of jattn_add_norm_bwd (0: it rejects the sizes)."""
+    return int(load_library().jattn_add_norm_bwd_bytes(T, C))
+
+
+def _work_ptr(work, nbytes: int):
+    """Raw pointer of a work buffer of at least nbytes bytes (any dtype)."""
+    import torch
+
+    if work is None or isinstance(work, int):
+        return work
+    if not isinstance(work, torch.Tensor) or not work.is_cuda or not work.is_contiguous():
+        raise ValueError("work: expected a contiguous CUDA tensor")
+    if work.numel() * work.element_size() < nbytes:
+        raise ValueError(f"work: needs {nbytes} bytes, got {work.numel() * work.element_size()}")
+    return work.data_ptr()
+
+
+def jattn_add_norm_bwd(dy, dh, h, r, g, T: int, C: int, dx, dg, work, stream=None, check: bool = True) -> int:
+    """C ABI jattn_add_norm_bwd.  dy / dh (or None) / h / dx [T, C] bf16 (dx may be dh), r [T] fp32,
+    g / dg [C] fp32, work jattn_add_norm_bwd_bytes(T, C) bytes."""
+    import torch
+
+    bf, f32, e = torch.bfloat16, torch.float32, T * C
+    lib = load_library()
+    rc = lib.jattn_add_norm_bwd(_ptr(dy, "dy", bf, e), _ptr(dh, "dh", bf, e), _ptr(h, "h", bf, e),
+                                _ptr(r, "r", f32, T), _ptr(g, "g", f32, C), T, C, _ptr(dx, "dx", bf, e),
+                                _ptr(dg, "dg", f32, C), _work_ptr(work, lib.jattn_add_norm_bwd_bytes(T, C)),
+                                _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_add_norm_bwd")
     return rc
 
 

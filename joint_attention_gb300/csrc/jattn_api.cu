@@ -80,8 +80,8 @@ struct Prof {
   };
   std::vector<Rec> pending;
   std::vector<cudaEvent_t> pool;
-  long long launches[JATTN_KERNEL_COUNT] = {0};
-  double ms[JATTN_KERNEL_COUNT] = {0};
+  long long launches[JATTN_TOKEN_KERNEL_END] = {0};  // by kind (both ranges of kinds)
+  double ms[JATTN_TOKEN_KERNEL_END] = {0};
 
   cudaEvent_t get() {
     if (!pool.empty()) {
@@ -779,6 +779,109 @@ extern "C" int jattn_fwd_saved(const jattn_bf16* v, int B, int H, int N_img, int
   return JATTN_OK;
 }
 
+namespace {
+
+int check_rows(int T, int C) {
+  if (T <= 0 || C <= 0) return JATTN_ERR_INVALID_ARG;
+  return C % 8 != 0 || C > JATTN_MAX_WIDTH ? JATTN_ERR_UNSUPPORTED : JATTN_OK;
+}
+
+// Any output over an input or another output; `same` (an output) may be
+// exactly `as` (an input): those elements are read by the thread that
+// overwrites them, before it does.
+template <size_t I, size_t O>
+bool any_alias(const Range (&ins)[I], const Range (&outs)[O], Range same, Range as) {
+  auto equal = [](Range a, Range b) { return a.lo == b.lo && a.hi == b.hi; };
+  for (size_t a = 0; a < O; ++a) {
+    for (const Range& i : ins)
+      if (overlaps(outs[a], i) && !(equal(outs[a], same) && equal(i, as) && equal(outs[a], i))) return true;
+    for (size_t b = a + 1; b < O; ++b)
+      if (overlaps(outs[a], outs[b])) return true;
+  }
+  return false;
+}
+
+// y (bf16) or y8 and s, exactly one of the two; g null: jattn_quant_rows.
+int add_norm_body(const jattn_bf16* x, const jattn_bf16* res, const float* g, int T, int C, float eps, jattn_bf16* h,
+                  jattn_bf16* y, uint8_t* y8, float* s, float* r, int kind, void* stream) {
+  const int rc = check_rows(T, C);
+  if (rc != JATTN_OK) return rc;
+  const void* ptrs[] = {x, res, g, h, y, y8, s, r};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return JATTN_ERR_MISALIGNED;
+  const size_t n = static_cast<size_t>(T) * C, rows = static_cast<size_t>(T) * 4;
+  const Range ins[] = {range_of(x, n * 2), range_of(res, res ? n * 2 : 0), range_of(g, g ? C * sizeof(float) : 0)};
+  const Range outs[] = {range_of(h, h ? n * 2 : 0), range_of(y, y ? n * 2 : 0), range_of(y8, y8 ? n : 0),
+                        range_of(s, s ? rows : 0), range_of(r, r ? rows : 0)};
+  if (any_alias(ins, outs, outs[0], ins[1])) return JATTN_ERR_ALIAS;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t ce;
+  {
+    Timed t(kind, st);
+    ce = launch_add_norm(TokenNorm{x, res, g, T, C, eps, h, y, y8, s, r}, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "token row kernel launch", ce);
+  return JATTN_OK;
+}
+
+bool eps_ok(float eps) { return eps > 0.f && eps <= 3.402823466e38f; }
+
+}  // namespace
+
+extern "C" int jattn_add_norm(const jattn_bf16* x, const jattn_bf16* res, const float* g, int T, int C, float eps,
+                              jattn_bf16* h, jattn_bf16* y, float* r, void* stream) {
+  if (!x || !g || !y || (res == nullptr) != (h == nullptr) || !eps_ok(eps)) return JATTN_ERR_INVALID_ARG;
+  return add_norm_body(x, res, g, T, C, eps, h, y, nullptr, nullptr, r, JATTN_KERNEL_ADD_NORM, stream);
+}
+
+extern "C" int jattn_add_norm_fp8(const jattn_bf16* x, const jattn_bf16* res, const float* g, int T, int C,
+                                  float eps, jattn_bf16* h, uint8_t* y8, float* s, float* r, void* stream) {
+  if (!x || !g || !y8 || !s || (res == nullptr) != (h == nullptr) || !eps_ok(eps)) return JATTN_ERR_INVALID_ARG;
+  return add_norm_body(x, res, g, T, C, eps, h, nullptr, y8, s, r, JATTN_KERNEL_ADD_NORM, stream);
+}
+
+extern "C" int jattn_quant_rows(const jattn_bf16* x, int T, int C, uint8_t* x8, float* s, void* stream) {
+  if (!x || !x8 || !s) return JATTN_ERR_INVALID_ARG;
+  return add_norm_body(x, nullptr, nullptr, T, C, 0.f, nullptr, nullptr, x8, s, nullptr, JATTN_KERNEL_QUANT_ROWS,
+                       stream);
+}
+
+extern "C" size_t jattn_add_norm_bwd_bytes(int T, int C) {
+  if (check_rows(T, C) != JATTN_OK) return 0;
+  return static_cast<size_t>(add_norm_bwd_parts(T, C)) * C * sizeof(float);
+}
+
+extern "C" int jattn_add_norm_bwd(const jattn_bf16* dy, const jattn_bf16* dh, const jattn_bf16* h, const float* r,
+                                  const float* g, int T, int C, jattn_bf16* dx, float* dg, void* work,
+                                  void* stream) {
+  if (!dy || !h || !r || !g || !dx || !dg || !work) return JATTN_ERR_INVALID_ARG;
+  const int rc = check_rows(T, C);
+  if (rc != JATTN_OK) return rc;
+  const void* ptrs[] = {dy, dh, h, r, g, dx, dg, work};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return JATTN_ERR_MISALIGNED;
+  const size_t tb = static_cast<size_t>(T) * C * 2, gb = static_cast<size_t>(C) * 4;
+  const Range ins[] = {range_of(dy, tb), range_of(dh, dh ? tb : 0), range_of(h, tb),
+                       range_of(r, static_cast<size_t>(T) * 4), range_of(g, gb)};
+  const Range outs[] = {range_of(dx, tb), range_of(dg, gb), range_of(work, jattn_add_norm_bwd_bytes(T, C))};
+  if (any_alias(ins, outs, outs[0], ins[1])) return JATTN_ERR_ALIAS;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* part = static_cast<float*>(work);
+  const int parts = add_norm_bwd_parts(T, C);
+  cudaError_t ce;
+  {
+    Timed t(JATTN_KERNEL_ADD_NORM_BWD, st);
+    ce = launch_add_norm_bwd(dy, dh, h, r, g, T, C, dx, part, parts, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "add_norm_bwd launch", ce);
+  {
+    Timed t(JATTN_KERNEL_ADD_NORM_DG, st);
+    ce = launch_dg_sum(part, parts, C, dg, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "add_norm_dg launch", ce);
+  return JATTN_OK;
+}
+
 namespace jattn {
 
 // One thread waits on an mbarrier that nothing arrives at, through the same
@@ -836,7 +939,7 @@ extern "C" int jattn_profile_reset(void) {
     p.pool.push_back(r.b);
   }
   p.pending.clear();
-  for (int i = 0; i < JATTN_KERNEL_COUNT; ++i) {
+  for (int i = 0; i < JATTN_TOKEN_KERNEL_END; ++i) {
     p.launches[i] = 0;
     p.ms[i] = 0;
   }
@@ -844,7 +947,9 @@ extern "C" int jattn_profile_reset(void) {
 }
 
 extern "C" int jattn_profile_read(int kind, int* launches, double* total_ms) {
-  if (kind < 0 || kind >= JATTN_KERNEL_COUNT || !launches || !total_ms) return JATTN_ERR_INVALID_ARG;
+  const bool known = (kind >= 0 && kind < JATTN_KERNEL_COUNT) ||
+                     (kind >= JATTN_TOKEN_KERNEL_FIRST && kind < JATTN_TOKEN_KERNEL_END);
+  if (!known || !launches || !total_ms) return JATTN_ERR_INVALID_ARG;
   Prof& p = prof();
   std::lock_guard<std::mutex> lock(p.mu);
   int status = JATTN_OK;
@@ -884,6 +989,10 @@ extern "C" const char* jattn_kernel_name(int kind) {
     case JATTN_KERNEL_ATTN_BWD: return "attn_bwd";
     case JATTN_KERNEL_Q_NORM_BWD: return "q_norm_bwd";
     case JATTN_KERNEL_QKV_NORM: return "qkv_norm";
+    case JATTN_KERNEL_ADD_NORM: return "add_norm";
+    case JATTN_KERNEL_ADD_NORM_BWD: return "add_norm_bwd";
+    case JATTN_KERNEL_ADD_NORM_DG: return "add_norm_dg";
+    case JATTN_KERNEL_QUANT_ROWS: return "quant_rows";
     default: return "unknown";
   }
 }
@@ -893,7 +1002,7 @@ extern "C" const char* jattn_status_string(int status) {
     case JATTN_OK: return "ok";
     case JATTN_ERR_INVALID_ARG: return "invalid argument (null pointer, non-positive or overflowing size)";
     case JATTN_ERR_UNSUPPORTED:
-      return "unsupported size (d must be 64 or 128; jattn_qkv_norm: C a multiple of 8)";
+      return "unsupported size (d must be 64 or 128; C a multiple of 8, and for token rows at most 16384)";
     case JATTN_ERR_MISALIGNED: return "pointer not 16-byte aligned";
     case JATTN_ERR_ALIAS: return "an output buffer overlaps another buffer";
     case JATTN_ERR_CUDA: return "CUDA launch or allocation failed";

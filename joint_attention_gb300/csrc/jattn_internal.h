@@ -93,6 +93,27 @@ int q_norm_bwd_parts(int d);
 int device_sm_count();
 void set_sm_limit(int n);  // n <= 0: no limit
 
+// --- token-row norm kernels (HBM-bound) ---------------------------------------
+// h = bf16(x + res), r = (mean h^2 + eps)^(-1/2), z = g h r; y = bf16(z), or
+// y8 = e4m3(z / s) with the rows' scales s.  g null (and y null): z = x.
+struct TokenNorm {
+  const uint16_t *x, *res;  // res: or null (then h is null)
+  const float* g;
+  int T, C;  // C a multiple of 8, at most JATTN_MAX_WIDTH
+  float eps;
+  uint16_t *h, *y;
+  uint8_t* y8;
+  float *s, *r;  // r: or null
+};
+cudaError_t launch_add_norm(const TokenNorm& t, cudaStream_t st);
+// add_norm_bwd_parts(T, C) blocks, each writing C partial sums of dg to part;
+// launch_dg_sum adds them in a fixed order.
+int add_norm_bwd_parts(int T, int C);
+cudaError_t launch_add_norm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const float* r,
+                                const float* g, int T, int C, uint16_t* dx, float* part, int parts,
+                                cudaStream_t st);
+cudaError_t launch_dg_sum(const float* part, int parts, int C, float* dg, cudaStream_t st);
+
 // --- tensor-core attention kernels ------------------------------------------
 struct AttnShape {
   int BH;        // heads (B*H, or H for a packed variable-length call)
