@@ -51,8 +51,8 @@ typedef uint16_t jattn_bf16; /* bfloat16 bit pattern */
 typedef enum {
   JATTN_OK = 0,
   JATTN_ERR_INVALID_ARG = 1, /* null pointer, B/H/d <= 0, N_img/N_txt < 0, N < 1, size overflow */
-  JATTN_ERR_UNSUPPORTED = 2, /* d not in {64, 128}; jattn_qkv_norm, token rows: C not a multiple of 8 (token rows:
-                                or above JATTN_MAX_WIDTH) */
+  JATTN_ERR_UNSUPPORTED = 2, /* d not in {64, 128}; projections and token rows: C not a multiple of 8 (8-bit tokens:
+                                of 16; token rows: or above JATTN_MAX_WIDTH), rank not as jattn_qkv_norm_lora says */
   JATTN_ERR_MISALIGNED = 3,  /* a pointer is not 16-byte aligned */
   JATTN_ERR_ALIAS = 4,       /* an output buffer overlaps an input or another output */
   JATTN_ERR_CUDA = 5,        /* a CUDA launch or allocation failed */
@@ -262,6 +262,66 @@ int jattn_add_norm_bwd(const jattn_bf16* dy, const jattn_bf16* dh, const jattn_b
                        const float* g, int T, int C, jattn_bf16* dx, float* dg, void* work, void* stream);
 
 /*
+ * The projection from 8-bit tokens and weights (serving; 8-bit tokens carry
+ * no gradient).  jattn_qkv_norm with rows in e4m3 and their fp32 scales, as
+ * jattn_add_norm_fp8 and jattn_quant_rows write them:
+ *
+ *   Y = bf16(sx_t sw_o sum_c x8_tc w8_oc + b_o)     fp32 accumulation
+ *
+ *   x_img, x_txt   : [B, N_img, C] and [B, N_txt, C] bytes
+ *   sx_img, sx_txt : [B, N_img] and [B, N_txt] float32
+ *   w_img, w_txt   : [3 H d, C] bytes
+ *   sw_img, sw_txt : [3 H d] float32
+ *   C              : a multiple of 16 (else JATTN_ERR_UNSUPPORTED)
+ * Everything else is jattn_qkv_norm's.
+ */
+int jattn_qkv_norm_fp8(const uint8_t* x_img, const float* sx_img, const uint8_t* w_img, const float* sw_img,
+                       const float* b_img, const uint8_t* x_txt, const float* sx_txt, const uint8_t* w_txt,
+                       const float* sw_txt, const float* b_txt, const float* gq, const float* gk, int B, int H,
+                       int N_img, int N_txt, int d, int C, jattn_bf16* q, jattn_bf16* k, jattn_bf16* v, void* saved,
+                       void* stream);
+
+/*
+ * The projection with low-rank adapters of the batch items' own (serving
+ * many requests, each with its adapter, in one batch).  For item b with a =
+ * index[b], per stream and part p of (q, k, v):
+ *
+ *   U_p = bf16(scale[a] X A_ap^T)                   fp32 accumulation
+ *   Y_p = bf16(X W_p^T + U_p B_ap^T + b_p)          fp32 accumulation, one rounding
+ *
+ * and for an item whose index is outside 0 .. n_adapters - 1, jattn_qkv_norm's
+ * Y.  The rest (heads, joint layout, q_hat, k_hat, 1/rms in `saved`) is
+ * jattn_qkv_norm's.
+ *   down_img, down_txt : [n_adapters, 3 rank, C] bf16, rows p rank .. p rank +
+ *                        rank - 1 of adapter a are A_ap
+ *   up_img, up_txt     : [n_adapters, 3 H d, rank] bf16, rows p H d .. of
+ *                        adapter a are B_ap; a stream may have neither (both
+ *                        NULL): no adapters there
+ *   scale              : [n_adapters] float32
+ *   index              : [B] int32, read on the device by each call (a captured
+ *                        graph replays with what it then holds); any value is
+ *                        allowed, and any items may share an adapter
+ *   n_adapters         : >= 1
+ *   rank               : a multiple of 8, 8 .. JATTN_MAX_RANK (else
+ *                        JATTN_ERR_UNSUPPORTED); adapters of lower rank are
+ *                        padded with zeros by the caller
+ *   work               : jattn_qkv_norm_lora_bytes(...) bytes for U, contents of
+ *                        no meaning before or after; calls that overlap on the
+ *                        GPU need one each
+ * Items that share an adapter are cheapest next to each other in the batch:
+ * a tile of 128 tokens takes each run of equal index values in turn.
+ * jattn_qkv_norm_lora_bytes returns 0 for sizes the call would reject.
+ */
+#define JATTN_MAX_RANK 128
+size_t jattn_qkv_norm_lora_bytes(int B, int H, int N_img, int N_txt, int d, int rank);
+int jattn_qkv_norm_lora(const jattn_bf16* x_img, const jattn_bf16* w_img, const float* b_img,
+                        const jattn_bf16* x_txt, const jattn_bf16* w_txt, const float* b_txt, const float* gq,
+                        const float* gk, const jattn_bf16* down_img, const jattn_bf16* up_img,
+                        const jattn_bf16* down_txt, const jattn_bf16* up_txt, const float* scale, const int* index,
+                        int n_adapters, int rank, int B, int H, int N_img, int N_txt, int d, int C, jattn_bf16* q,
+                        jattn_bf16* k, jattn_bf16* v, void* saved, void* work, void* stream);
+
+/*
  * Forward without any device allocation.  (No counterpart on the pages: an
  * integration entry point.)  Same arguments, layout and results as jattn_fwd,
  * but the scratch it needs (the normalised q_hat and k_hat, 2 * 2 * B*H*N*d
@@ -338,7 +398,8 @@ typedef enum {
   JATTN_KERNEL_ADD_NORM_BWD = 17,  /* its backward: dx and partial sums of dg */
   JATTN_KERNEL_ADD_NORM_DG = 18,   /* dg from the partial sums */
   JATTN_KERNEL_QUANT_ROWS = 19,    /* rows to 8 bits */
-  JATTN_TOKEN_KERNEL_END = 20
+  JATTN_KERNEL_LORA_DOWN = 20,     /* the adapters' first product (the projections themselves: QKV_NORM) */
+  JATTN_TOKEN_KERNEL_END = 21
 } jattn_token_kernel_kind;
 
 int jattn_profile_enable(int on);

@@ -13,7 +13,8 @@ from ._binding import (KERNEL_KINDS, STATUS, STATUS_CODE, JattnError, declared_s
                        jattn_saved_bytes, jattn_saved_bytes_varlen, jattn_fwd_train, jattn_bwd_train,
                        jattn_fwd_train_varlen, jattn_bwd_train_varlen, jattn_qkv_norm, jattn_fwd_saved,
                        TOKEN_KERNEL_KINDS, jattn_add_norm, jattn_add_norm_fp8, jattn_quant_rows,
-                       jattn_add_norm_bwd_bytes, jattn_add_norm_bwd)
+                       jattn_add_norm_bwd_bytes, jattn_add_norm_bwd, jattn_qkv_norm_fp8, jattn_qkv_norm_lora,
+                       jattn_qkv_norm_lora_bytes)
 
 __all__ = ["STATUS", "STATUS_CODE", "JattnError", "declared_symbols", "jattn_bwd", "jattn_fwd",
            "jattn_last_device_error", "jattn_status_string", "jattn_version", "load_library", "forward",
@@ -25,7 +26,8 @@ __all__ = ["STATUS", "STATUS_CODE", "JattnError", "declared_symbols", "jattn_bwd
            "jattn_bwd_train_varlen", "forward_train", "backward_train", "jattn_qkv_norm", "jattn_fwd_saved",
            "qkv_norm", "TOKEN_KERNEL_KINDS", "jattn_add_norm", "jattn_add_norm_fp8", "jattn_quant_rows",
            "jattn_add_norm_bwd_bytes", "jattn_add_norm_bwd", "add_norm", "add_norm_fp8", "add_norm_backward",
-           "quant_rows"]
+           "quant_rows", "jattn_qkv_norm_fp8", "jattn_qkv_norm_lora", "jattn_qkv_norm_lora_bytes", "qkv_norm_fp8",
+           "qkv_norm_lora"]
 
 
 def forward(q, k, v, gq, gk, n_txt: int, stream=None):
@@ -188,3 +190,46 @@ def quant_rows(x, stream=None):
         scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     jattn_quant_rows(x, scale.numel(), x.shape[-1], x8, scale, stream)
     return x8, scale
+
+
+def _projected(x_img, x_txt, H: int, d: int):
+    """q, k, v and `saved` of a projection call, and its sizes."""
+    import torch
+
+    B, N_img, C = x_img.shape
+    N_txt = x_txt.shape[1]
+    dev = x_img.device
+    q, k, v = (torch.empty((B, H, N_img + N_txt, d), dtype=torch.bfloat16, device=dev) for _ in range(3))
+    saved = torch.empty(jattn_saved_bytes(B, H, N_img, N_txt, d), dtype=torch.uint8, device=dev)
+    return (q, k, v, saved), (B, H, N_img, N_txt, d, C)
+
+
+def qkv_norm_fp8(x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt, sw_txt, b_txt, gq, gk, H: int,
+                 stream=None):
+    """q, k, v, saved: qkv_norm from 8-bit tokens and weights (float8_e4m3fn) with the fp32 scales of their
+    rows, as add_norm_fp8 and quant_rows give them: x_* [B, N_*, C], sx_* [B, N_*], w_* [3 H d, C],
+    sw_* [3 H d]."""
+    with _outputs_on(stream, x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt, sw_txt, b_txt, gq, gk):
+        out, sizes = _projected(x_img, x_txt, H, gq.shape[0])
+    jattn_qkv_norm_fp8(x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt, sw_txt, b_txt, gq, gk, *sizes,
+                       *out, stream)
+    return out
+
+
+def qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, H: int, down_img, up_img, down_txt, up_txt,
+                  scale, index, stream=None):
+    """q, k, v, saved: qkv_norm with low-rank adapters of the batch items' own: item b adds
+    scale[a] (x A_a^T) B_a^T, a = index[b] (int32 on the device; outside 0 .. n - 1: none), with A in
+    down_* [n, 3 rank, C] and B in up_* [n, 3 H d, rank], q, k and v each with a rank of their own
+    (both None: no adapters in that stream)."""
+    import torch
+
+    n = scale.numel()
+    rank = next((u.shape[-1] for u in (up_img, up_txt) if u is not None), 8)
+    with _outputs_on(stream, x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_img, up_img, down_txt, up_txt,
+                     scale, index):
+        out, sizes = _projected(x_img, x_txt, H, gq.shape[0])
+        work = torch.empty(jattn_qkv_norm_lora_bytes(*sizes[:5], rank), dtype=torch.uint8, device=x_img.device)
+    jattn_qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_img, up_img, down_txt, up_txt, scale,
+                        index, n, rank, *sizes, *out, work, stream)
+    return out

@@ -115,13 +115,19 @@ def load_library(path: str | None = None, build_if_missing: bool = False) -> cty
     lib.jattn_add_norm_bwd_bytes.restype = sz
     lib.jattn_add_norm_bwd.argtypes = [vp] * 5 + [i32, i32] + [vp] * 4
     lib.jattn_add_norm_bwd.restype = i32
+    lib.jattn_qkv_norm_fp8.argtypes = [vp] * 12 + [i32] * 6 + [vp] * 5
+    lib.jattn_qkv_norm_fp8.restype = i32
+    lib.jattn_qkv_norm_lora_bytes.argtypes = [i32] * 6
+    lib.jattn_qkv_norm_lora_bytes.restype = sz
+    lib.jattn_qkv_norm_lora.argtypes = [vp] * 14 + [i32] * 8 + [vp] * 6
+    lib.jattn_qkv_norm_lora.restype = i32
     if path is None:
         _lib = lib
     return lib
 
 
 KERNEL_KINDS = 6
-TOKEN_KERNEL_KINDS = range(16, 20)  # the token-row kernels' kinds, numbered apart
+TOKEN_KERNEL_KINDS = range(16, 21)  # the token-row kernels' kinds, numbered apart
 
 
 def jattn_profile_enable(on: bool = True) -> int:
@@ -499,6 +505,64 @@ def jattn_add_norm_bwd(dy, dh, h, r, g, T: int, C: int, dx, dg, work, stream=Non
                                 _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_add_norm_bwd")
+    return rc
+
+
+def jattn_qkv_norm_fp8(x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt, sw_txt, b_txt, gq, gk, B: int,
+                       H: int, N_img: int, N_txt: int, d: int, C: int, q, k, v, saved, stream=None,
+                       check: bool = True) -> int:
+    """C ABI jattn_qkv_norm_fp8: jattn_qkv_norm with tokens and weights in float8_e4m3fn and the fp32 scales
+    of their rows, sx_* [B, N_*] and sw_* [3 H d]."""
+    import torch
+
+    e = B * H * (N_img + N_txt) * d
+    bf, f32, f8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+    yc = 3 * H * d
+    nb = jattn_saved_bytes(B, H, N_img, N_txt, d)
+    args = []
+    for n, N_s, x, sx, w, sw, b in (("img", N_img, x_img, sx_img, w_img, sw_img, b_img),
+                                    ("txt", N_txt, x_txt, sx_txt, w_txt, sw_txt, b_txt)):
+        args += [_ptr(x, "x_" + n, f8, B * N_s * C), _ptr(sx, "sx_" + n, f32, B * N_s),
+                 _ptr(w, "w_" + n, f8, yc * C if N_s else None), _ptr(sw, "sw_" + n, f32, yc if N_s else None),
+                 _ptr(b, "b_" + n, f32, yc)]
+    rc = load_library().jattn_qkv_norm_fp8(*args, _ptr(gq, "gq", f32, d), _ptr(gk, "gk", f32, d), B, H, N_img,
+                                           N_txt, d, C, _ptr(q, "q", bf, e), _ptr(k, "k", bf, e),
+                                           _ptr(v, "v", bf, e), _saved_ptr(saved, nb), _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_qkv_norm_fp8")
+    return rc
+
+
+def jattn_qkv_norm_lora_bytes(B: int, H: int, N_img: int, N_txt: int, d: int, rank: int) -> int:
+    """C ABI jattn_qkv_norm_lora_bytes: size of the work buffer of jattn_qkv_norm_lora (0: it rejects the sizes)."""
+    return int(load_library().jattn_qkv_norm_lora_bytes(B, H, N_img, N_txt, d, rank))
+
+
+def jattn_qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_img, up_img, down_txt, up_txt, scale,
+                        index, n_adapters: int, rank: int, B: int, H: int, N_img: int, N_txt: int, d: int, C: int,
+                        q, k, v, saved, work, stream=None, check: bool = True) -> int:
+    """C ABI jattn_qkv_norm_lora: jattn_qkv_norm with the batch items' adapters.  down_* [n, 3 rank, C] and up_*
+    [n, 3 H d, rank] bf16 (None: none in that stream), scale [n] fp32, index [B] int32 (outside 0 .. n - 1:
+    no adapter), work jattn_qkv_norm_lora_bytes(...) bytes."""
+    import torch
+
+    e = B * H * (N_img + N_txt) * d
+    bf, f32 = torch.bfloat16, torch.float32
+    yc = 3 * H * d
+    nb = jattn_saved_bytes(B, H, N_img, N_txt, d)
+    args = []
+    for n, N_s, x, w, b in (("img", N_img, x_img, w_img, b_img), ("txt", N_txt, x_txt, w_txt, b_txt)):
+        args += [_ptr(x, "x_" + n, bf, B * N_s * C), _ptr(w, "w_" + n, bf, yc * C if N_s else None),
+                 _ptr(b, "b_" + n, f32, yc)]
+    args += [_ptr(gq, "gq", f32, d), _ptr(gk, "gk", f32, d)]
+    for n, down, up in (("img", down_img, up_img), ("txt", down_txt, up_txt)):
+        args += [_ptr(down, "down_" + n, bf, n_adapters * 3 * rank * C), _ptr(up, "up_" + n, bf, n_adapters * yc * rank)]
+    rc = load_library().jattn_qkv_norm_lora(
+        *args, _ptr(scale, "scale", f32, n_adapters), _ptr(index, "index", torch.int32, B), n_adapters, rank, B, H,
+        N_img, N_txt, d, C, _ptr(q, "q", bf, e), _ptr(k, "k", bf, e), _ptr(v, "v", bf, e), _saved_ptr(saved, nb),
+        _work_ptr(work, jattn_qkv_norm_lora_bytes(B, H, N_img, N_txt, d, rank)), _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_qkv_norm_lora")
     return rc
 
 

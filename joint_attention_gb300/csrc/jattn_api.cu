@@ -273,15 +273,30 @@ bool encode_bhnd_map_rows(CUtensorMap* map, const void* base, int BH, int N, int
   return r == CUDA_SUCCESS;
 }
 
-bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows) {
+bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool e4m3) {
   auto fn = encode_fn();
   if (!fn) return false;
+  const int size = e4m3 ? 1 : 2;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * size};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t es[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  CUresult r = fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                  const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_pair_map(CUtensorMap* map, const void* base, int planes, int64_t rows, int cols, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(planes)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(rows) * cols * 2};
+  cuuint32_t box[3] = {16, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -660,85 +675,227 @@ extern "C" int jattn_bwd_train_varlen(const jattn_bf16* q, const jattn_bf16* k, 
   return bwd_body(s, q, k, v, gq, gk, out, lse, dout, saved, dq, dk, dv, dgq, dgk, stream);
 }
 
-extern "C" int jattn_qkv_norm(const jattn_bf16* x_img, const jattn_bf16* w_img, const float* b_img,
-                              const jattn_bf16* x_txt, const jattn_bf16* w_txt, const float* b_txt, const float* gq,
-                              const float* gk, int B, int H, int N_img, int N_txt, int d, int C, jattn_bf16* q,
-                              jattn_bf16* k, jattn_bf16* v, void* saved, void* stream) {
-  if (!gq || !gk || !q || !k || !v || !saved) return JATTN_ERR_INVALID_ARG;
-  if ((N_img > 0 && (!x_img || !w_img)) || (N_txt > 0 && (!x_txt || !w_txt))) return JATTN_ERR_INVALID_ARG;
+namespace {
+
+// One projection call: the image (0) and caption (1) streams' operands, and
+// what the 8-bit or the adapter form adds.
+struct QkvCall {
+  const void* x[2];
+  const void* w[2];
+  const float* bias[2];
+  const float *gq, *gk;
+  int B, H, N_img, N_txt, d, C;
+  jattn_bf16 *q, *k, *v;
+  void* saved;
+  void* stream;
+  bool e4m3 = false;
+  const float* sx[2] = {nullptr, nullptr};
+  const float* sw[2] = {nullptr, nullptr};
+  bool lora = false;
+  const jattn_bf16* down[2] = {nullptr, nullptr};
+  const jattn_bf16* up[2] = {nullptr, nullptr};
+  const float* scale = nullptr;
+  const int* index = nullptr;
+  int n_adapters = 0, rank = 0;
+  void* work = nullptr;
+};
+
+size_t lora_u_bytes(int64_t rows, int rank) {
+  const int64_t r16 = (rank + 15) / 16 * 16;
+  return (static_cast<size_t>(rows) * 3 * r16 * 2 + 255) & ~static_cast<size_t>(255);
+}
+
+int check_lora(int rank) {
+  if (rank <= 0) return JATTN_ERR_INVALID_ARG;
+  return rank % 8 != 0 || rank > JATTN_MAX_RANK ? JATTN_ERR_UNSUPPORTED : JATTN_OK;
+}
+
+int qkv_body(const QkvCall& c) {
+  const int n_s[2] = {c.N_img, c.N_txt};
+  if (!c.gq || !c.gk || !c.q || !c.k || !c.v || !c.saved) return JATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i) {
+    if (n_s[i] > 0 && (!c.x[i] || !c.w[i])) return JATTN_ERR_INVALID_ARG;
+    if (c.e4m3 && n_s[i] > 0 && (!c.sx[i] || !c.sw[i])) return JATTN_ERR_INVALID_ARG;
+    if ((c.down[i] == nullptr) != (c.up[i] == nullptr)) return JATTN_ERR_INVALID_ARG;
+  }
+  if (c.lora && (!c.scale || !c.index || !c.work || c.n_adapters <= 0)) return JATTN_ERR_INVALID_ARG;
   Shape s;
-  int rc = check_shape(B, H, N_img, N_txt, d, &s);
+  int rc = check_shape(c.B, c.H, c.N_img, c.N_txt, c.d, &s);
   if (rc != JATTN_OK) return rc;
+  const int d = c.d, C = c.C;
   if (C <= 0) return JATTN_ERR_INVALID_ARG;
-  if (C % 8 != 0) return JATTN_ERR_UNSUPPORTED;  // TMA row stride: a multiple of 16 bytes
-  const int64_t ycols = 3 * static_cast<int64_t>(H) * d;
-  if (ycols * C >= (int64_t{1} << 31) || static_cast<int64_t>(B) * N_img * C >= (int64_t{1} << 31) ||
-      static_cast<int64_t>(B) * N_txt * C >= (int64_t{1} << 31))
+  // TMA row stride: a multiple of 16 bytes.
+  const int size = c.e4m3 ? 1 : 2;
+  if (C * static_cast<int64_t>(size) % 16 != 0) return JATTN_ERR_UNSUPPORTED;
+  if (c.lora && (rc = check_lora(c.rank)) != JATTN_OK) return rc;
+  const int64_t ycols = 3 * static_cast<int64_t>(c.H) * d;
+  const int64_t limit = int64_t{1} << 31;
+  if (ycols * C >= limit || static_cast<int64_t>(c.B) * c.N_img * C >= limit ||
+      static_cast<int64_t>(c.B) * c.N_txt * C >= limit)
     return JATTN_ERR_INVALID_ARG;
-  const void* ptrs[] = {x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, q, k, v, saved};
+  if (c.lora && (3 * static_cast<int64_t>(c.n_adapters) >= limit)) return JATTN_ERR_INVALID_ARG;
+  const void* ptrs[] = {c.x[0], c.w[0],  c.bias[0], c.x[1],    c.w[1],    c.bias[1], c.gq,      c.gk,
+                        c.q,    c.k,     c.v,       c.saved,   c.sx[0],   c.sx[1],   c.sw[0],   c.sw[1],
+                        c.scale, c.index, c.work,   c.down[0], c.down[1], c.up[0],   c.up[1]};
   for (const void* p : ptrs)
     if (!aligned16(p)) return JATTN_ERR_MISALIGNED;
   const size_t tb = s.elems * 2;
   const SavedLayout sl = saved_layout(s);
-  const size_t xb_img = static_cast<size_t>(B) * N_img * C * 2, xb_txt = static_cast<size_t>(B) * N_txt * C * 2;
-  const size_t wb = static_cast<size_t>(ycols) * C * 2, bb = static_cast<size_t>(ycols) * 4;
-  const Range ins[] = {range_of(x_img, N_img ? xb_img : 0), range_of(w_img, N_img ? wb : 0),
-                       range_of(b_img, N_img && b_img ? bb : 0), range_of(x_txt, N_txt ? xb_txt : 0),
-                       range_of(w_txt, N_txt ? wb : 0), range_of(b_txt, N_txt && b_txt ? bb : 0),
-                       range_of(gq, d * 4), range_of(gk, d * 4)};
-  const Range outs[] = {range_of(q, tb), range_of(k, tb), range_of(v, tb), range_of(saved, sl.total)};
+  const size_t wb = static_cast<size_t>(ycols) * C * size, bb = static_cast<size_t>(ycols) * 4;
+  auto bytes_if = [](bool on, size_t b) { return on ? b : size_t{0}; };
+  Range ins[20];
+  int n_in = 0;
+  for (int i = 0; i < 2; ++i) {
+    const bool on = n_s[i] > 0;
+    const size_t rows = static_cast<size_t>(c.B) * n_s[i], n = static_cast<size_t>(c.n_adapters);
+    ins[n_in++] = range_of(c.x[i], rows * C * size);
+    ins[n_in++] = range_of(c.w[i], bytes_if(on, wb));
+    ins[n_in++] = range_of(c.bias[i], bytes_if(on && c.bias[i], bb));
+    ins[n_in++] = range_of(c.sx[i], bytes_if(c.sx[i], rows * 4));
+    ins[n_in++] = range_of(c.sw[i], bytes_if(on && c.sw[i], bb));
+    ins[n_in++] = range_of(c.down[i], bytes_if(on && c.down[i], n * 3 * c.rank * C * 2));
+    ins[n_in++] = range_of(c.up[i], bytes_if(on && c.up[i], n * ycols * c.rank * 2));
+  }
+  ins[n_in++] = range_of(c.gq, d * 4);
+  ins[n_in++] = range_of(c.gk, d * 4);
+  ins[n_in++] = range_of(c.scale, bytes_if(c.lora, static_cast<size_t>(c.n_adapters) * 4));
+  ins[n_in++] = range_of(c.index, bytes_if(c.lora, static_cast<size_t>(c.B) * 4));
+  const size_t u_img = c.lora ? lora_u_bytes(static_cast<int64_t>(c.B) * c.N_img, c.rank) : 0;
+  const size_t u_txt = c.lora ? lora_u_bytes(static_cast<int64_t>(c.B) * c.N_txt, c.rank) : 0;
+  const Range outs[] = {range_of(c.q, tb), range_of(c.k, tb), range_of(c.v, tb), range_of(c.saved, sl.total),
+                        range_of(c.work, u_img + u_txt)};
   for (size_t a = 0; a < sizeof(outs) / sizeof(outs[0]); ++a) {
-    for (const Range& i : ins)
-      if (overlaps(outs[a], i)) return JATTN_ERR_ALIAS;
+    for (int i = 0; i < n_in; ++i)
+      if (overlaps(outs[a], ins[i])) return JATTN_ERR_ALIAS;
     for (size_t b = a + 1; b < sizeof(outs) / sizeof(outs[0]); ++b)
       if (overlaps(outs[a], outs[b])) return JATTN_ERR_ALIAS;
   }
 
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStream_t st = static_cast<cudaStream_t>(c.stream);
   uint32_t* err = dev_err_ptr();
   if (!err) return fail(JATTN_ERR_CUDA, "device error word", cudaGetLastError());
-  uint8_t* base = static_cast<uint8_t*>(saved);
+  uint8_t* base = static_cast<uint8_t*>(c.saved);
   QkvLaunch a;
-  a.H = H;
+  a.H = c.H;
   a.C = C;
   a.N = s.N;
   a.d = d;
+  a.e4m3 = c.e4m3;
   // Stream 0: the image rows (after the caption rows); stream 1: the caption rows.
-  a.M[0] = B * N_img;
-  a.N_s[0] = N_img;
-  a.row0[0] = N_txt;
-  a.bias[0] = b_img;
-  a.M[1] = B * N_txt;
-  a.N_s[1] = N_txt;
-  a.row0[1] = 0;
-  a.bias[1] = b_txt;
-  a.gq = gq;
-  a.gk = gk;
-  a.out[0] = q;
-  a.out[1] = k;
-  a.out[2] = v;
+  for (int i = 0; i < 2; ++i) {
+    a.M[i] = c.B * n_s[i];
+    a.N_s[i] = n_s[i];
+    a.row0[i] = i == 0 ? c.N_txt : 0;
+    a.bias[i] = c.bias[i];
+    a.sx[i] = c.sx[i];
+    a.sw[i] = c.sw[i];
+  }
+  a.gq = c.gq;
+  a.gk = c.gk;
+  a.out[0] = c.q;
+  a.out[1] = c.k;
+  a.out[2] = c.v;
   a.hat[0] = reinterpret_cast<uint16_t*>(base + sl.qhat);
   a.hat[1] = reinterpret_cast<uint16_t*>(base + sl.khat);
   a.r[0] = reinterpret_cast<float*>(base + sl.rq);
   a.r[1] = reinterpret_cast<float*>(base + sl.rk);
   CUtensorMap maps[4];
-  const jattn_bf16* xs[2] = {N_img ? x_img : x_txt, N_txt ? x_txt : x_img};
-  const jattn_bf16* ws[2] = {N_img ? w_img : w_txt, N_txt ? w_txt : w_img};
-  const int64_t ms[2] = {N_img ? a.M[0] : a.M[1], N_txt ? a.M[1] : a.M[0]};
-  for (int i = 0; i < 2; ++i)
-    if (!encode_rows_map(&maps[2 * i], xs[i], ms[i], C, 128) || !encode_rows_map(&maps[2 * i + 1], ws[i], ycols, C, 256))
+  for (int i = 0; i < 2; ++i) {
+    const int j = n_s[i] ? i : 1 - i;  // a stream without rows launches no tiles: any valid map
+    if (!encode_rows_map(&maps[2 * i], c.x[j], a.M[j], C, 128, c.e4m3) ||
+        !encode_rows_map(&maps[2 * i + 1], c.w[j], ycols, C, 256, c.e4m3))
       return fail(JATTN_ERR_CUDA, "cuTensorMapEncodeTiled");
+  }
   CUtensorMap out_maps[5];
-  const void* outs_p[5] = {q, k, v, a.hat[0], a.hat[1]};
+  const void* outs_p[5] = {c.q, c.k, c.v, a.hat[0], a.hat[1]};
   for (int i = 0; i < 5; ++i)
     if (!encode_bhnd_map_rows(&out_maps[i], outs_p[i], s.BH, s.N, d, 32)) return fail(JATTN_ERR_CUDA, "cuTensorMapEncodeTiled");
   cudaError_t ce;
+  LoraLaunch l;
+  CUtensorMap lora_maps[4], down_maps[2], item_maps[2];
+  if (c.lora) {
+    l.n_adapters = c.n_adapters;
+    l.rank = c.rank;
+    l.index = c.index;
+    l.scale = c.scale;
+    l.u[0] = static_cast<uint16_t*>(c.work);
+    l.u[1] = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(c.work) + u_img);
+    const int r16 = (c.rank + 15) / 16 * 16;
+    for (int i = 0; i < 2; ++i) {
+      l.on[i] = c.down[i] && n_s[i] > 0;
+      if (!l.on[i]) {
+        lora_maps[i] = lora_maps[2 + i] = down_maps[i] = item_maps[i] = maps[0];
+      } else if (!encode_pair_map(&lora_maps[i], l.u[i], 0, a.M[i], 3 * r16, 128) ||
+                 !encode_pair_map(&lora_maps[2 + i], c.up[i], c.n_adapters, ycols, c.rank, 256) ||
+                 !encode_bhnd_map_rows(&down_maps[i], c.down[i], 3 * c.n_adapters, c.rank, C, r16) ||
+                 !encode_bhnd_map(&item_maps[i], c.x[i], c.B, n_s[i], C)) {
+        return fail(JATTN_ERR_CUDA, "cuTensorMapEncodeTiled");
+      }
+    }
+    {
+      Timed t(JATTN_KERNEL_LORA_DOWN, st);
+      ce = launch_lora_down(item_maps, down_maps, l, a, c.B, err, st);
+    }
+    if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "lora_down launch", ce);
+  }
   {
     Timed t(JATTN_KERNEL_QKV_NORM, st);
-    ce = launch_qkv_norm(maps, out_maps, a, err, st);
+    ce = launch_qkv_norm(maps, out_maps, a, err, st, c.lora ? &l : nullptr, lora_maps);
   }
   if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "qkv_norm launch", ce);
   return JATTN_OK;
+}
+
+}  // namespace
+
+extern "C" int jattn_qkv_norm(const jattn_bf16* x_img, const jattn_bf16* w_img, const float* b_img,
+                              const jattn_bf16* x_txt, const jattn_bf16* w_txt, const float* b_txt, const float* gq,
+                              const float* gk, int B, int H, int N_img, int N_txt, int d, int C, jattn_bf16* q,
+                              jattn_bf16* k, jattn_bf16* v, void* saved, void* stream) {
+  return qkv_body(QkvCall{{x_img, x_txt}, {w_img, w_txt}, {b_img, b_txt}, gq, gk, B, H, N_img, N_txt, d, C, q, k, v,
+                          saved, stream});
+}
+
+extern "C" int jattn_qkv_norm_fp8(const uint8_t* x_img, const float* sx_img, const uint8_t* w_img,
+                                  const float* sw_img, const float* b_img, const uint8_t* x_txt,
+                                  const float* sx_txt, const uint8_t* w_txt, const float* sw_txt,
+                                  const float* b_txt, const float* gq, const float* gk, int B, int H, int N_img,
+                                  int N_txt, int d, int C, jattn_bf16* q, jattn_bf16* k, jattn_bf16* v, void* saved,
+                                  void* stream) {
+  QkvCall c{{x_img, x_txt}, {w_img, w_txt}, {b_img, b_txt}, gq, gk, B, H, N_img, N_txt, d, C, q, k, v, saved, stream};
+  c.e4m3 = true;
+  c.sx[0] = sx_img;
+  c.sx[1] = sx_txt;
+  c.sw[0] = sw_img;
+  c.sw[1] = sw_txt;
+  return qkv_body(c);
+}
+
+extern "C" size_t jattn_qkv_norm_lora_bytes(int B, int H, int N_img, int N_txt, int d, int rank) {
+  Shape s;
+  if (check_shape(B, H, N_img, N_txt, d, &s) != JATTN_OK || check_lora(rank) != JATTN_OK) return 0;
+  return lora_u_bytes(static_cast<int64_t>(B) * N_img, rank) + lora_u_bytes(static_cast<int64_t>(B) * N_txt, rank);
+}
+
+extern "C" int jattn_qkv_norm_lora(const jattn_bf16* x_img, const jattn_bf16* w_img, const float* b_img,
+                                   const jattn_bf16* x_txt, const jattn_bf16* w_txt, const float* b_txt,
+                                   const float* gq, const float* gk, const jattn_bf16* down_img,
+                                   const jattn_bf16* up_img, const jattn_bf16* down_txt, const jattn_bf16* up_txt,
+                                   const float* scale, const int* index, int n_adapters, int rank, int B, int H,
+                                   int N_img, int N_txt, int d, int C, jattn_bf16* q, jattn_bf16* k, jattn_bf16* v,
+                                   void* saved, void* work, void* stream) {
+  QkvCall c{{x_img, x_txt}, {w_img, w_txt}, {b_img, b_txt}, gq, gk, B, H, N_img, N_txt, d, C, q, k, v, saved, stream};
+  c.lora = true;
+  c.down[0] = down_img;
+  c.down[1] = down_txt;
+  c.up[0] = up_img;
+  c.up[1] = up_txt;
+  c.scale = scale;
+  c.index = index;
+  c.n_adapters = n_adapters;
+  c.rank = rank;
+  c.work = work;
+  return qkv_body(c);
 }
 
 extern "C" int jattn_fwd_saved(const jattn_bf16* v, int B, int H, int N_img, int N_txt, int d, jattn_bf16* out,
@@ -993,6 +1150,7 @@ extern "C" const char* jattn_kernel_name(int kind) {
     case JATTN_KERNEL_ADD_NORM_BWD: return "add_norm_bwd";
     case JATTN_KERNEL_ADD_NORM_DG: return "add_norm_dg";
     case JATTN_KERNEL_QUANT_ROWS: return "quant_rows";
+    case JATTN_KERNEL_LORA_DOWN: return "lora_down";
     default: return "unknown";
   }
 }
@@ -1002,7 +1160,8 @@ extern "C" const char* jattn_status_string(int status) {
     case JATTN_OK: return "ok";
     case JATTN_ERR_INVALID_ARG: return "invalid argument (null pointer, non-positive or overflowing size)";
     case JATTN_ERR_UNSUPPORTED:
-      return "unsupported size (d must be 64 or 128; C a multiple of 8, and for token rows at most 16384)";
+      return "unsupported size (d must be 64 or 128; C a multiple of 8, or of 16 for 8-bit tokens, and for token "
+             "rows at most 16384; a rank a multiple of 8, at most 128)";
     case JATTN_ERR_MISALIGNED: return "pointer not 16-byte aligned";
     case JATTN_ERR_ALIAS: return "an output buffer overlaps another buffer";
     case JATTN_ERR_CUDA: return "CUDA launch or allocation failed";

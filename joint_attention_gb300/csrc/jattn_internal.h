@@ -160,17 +160,41 @@ struct QkvLaunch {
   int N_s[2];   // tokens per batch item
   int row0[2];  // first row in the joint sequence
   const float* bias[2];  // [3 H d] fp32 or null
+  bool e4m3;             // 8-bit tokens and weights, with the scales of their rows:
+  const float *sx[2], *sw[2];
   const float *gq, *gk;
   uint16_t* out[3];  // q, k, v
   uint16_t* hat[2];  // q_hat, k_hat
   float* r[2];       // rq, rk
 };
+// Low-rank adapters of the batch items beside the projection (bf16 only).
+struct LoraLaunch {
+  int n_adapters, rank;
+  const int* index;    // [B] the items' adapters
+  const float* scale;  // [n_adapters]
+  bool on[2];          // whether a stream has adapters (and rows)
+  uint16_t* u[2];      // scratch [M, 3 * 16 ceil(rank / 16)]
+};
 // out_maps: q, k, v, q_hat, k_hat as encode_bhnd_map_rows(..., 32) maps.
+// lora_maps (with lora): encode_pair_map maps of both streams' U (128-row
+// boxes), then of their up weights [n, 3 H d, rank] (256-row boxes); a stream
+// without adapters: any valid map.
 cudaError_t launch_qkv_norm(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
-                            uint32_t* dev_err, cudaStream_t st);
-// A 2-D TMA map over a row-major [rows, cols] bf16 matrix with a
-// (64, box_rows) box and 128-byte swizzle (cols * 2 a multiple of 16).
-bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows);
+                            uint32_t* dev_err, cudaStream_t st, const LoraLaunch* lora = nullptr,
+                            const CUtensorMap* lora_maps = nullptr);
+// U = bf16(scale X A^T), before launch_qkv_norm.  x: [B, N_s, C] as
+// encode_bhnd_map maps; down: the adapters' [3 n, rank, C] as
+// encode_bhnd_map_rows(..., 16 ceil(rank / 16)) maps.
+cudaError_t launch_lora_down(const CUtensorMap (&x)[2], const CUtensorMap (&down)[2], const LoraLaunch& l,
+                             const QkvLaunch& a, int B, uint32_t* dev_err, cudaStream_t st);
+// A 2-D TMA map over a row-major [rows, cols] matrix of bf16 (or, with e4m3,
+// 8-bit) values with a (128 bytes, box_rows) box and 128-byte swizzle (a
+// row's bytes a multiple of 16).
+bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows,
+                     bool e4m3 = false);
+// TMA maps with (16, box_rows) boxes of bf16 and 32-byte swizzle over
+// [planes, rows, cols]; planes 0: a 2-D map over [rows, cols].
+bool encode_pair_map(CUtensorMap* map, const void* base, int planes, int64_t rows, int cols, int box_rows);
 
 // Encodes a 3-D TMA map over a [BH, N, d] bf16 tensor with a (64, 128, 1)
 // box and 128-byte swizzle.  Returns false if the driver rejects it.

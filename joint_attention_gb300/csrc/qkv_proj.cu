@@ -38,6 +38,20 @@
 // Heads past 3 H in the last column tile, and token rows past the stream's
 // end in its last row tile, read the TMA's zero fill and are not stored.
 //
+// The same kernel takes two other forms of the products (template kMode):
+//   kE4m3  X and W in e4m3 with fp32 scales of their rows: a K step of 128
+//          values in the same 128-byte rows, kind::f8f6f4 products, and
+//          Y = bf16(sx sw acc + bias).
+//   kLora  low-rank adapters of the batch items' own beside the shared
+//          weights: Y = bf16(X W^T + U B^T + bias), U = scale X A^T (one
+//          launch of lora_down_kernel before, rounded to bf16), as further K
+//          steps of 16 into the same accumulator.  A row tile that holds items
+//          with different adapters takes each run of items in turn, with the
+//          other rows' lanes disabled in the MMA, so that no row mask or copy of
+//          U is needed; a column tile over a q / k / v boundary takes each part
+//          with its own columns of U.  Four such (U, B) pairs of 4 + 8 KB fill
+//          one ring stage.
+//
 // Correct rounding: the per-thread sum of the d squares is a balanced tree
 // (at most 7 roundings per term, within the 8 that the rounding window of the
 // norm kernels allows for), and elements in the bf16-midpoint window are
@@ -76,7 +90,9 @@ struct QkvCfg {
   static constexpr int kBiasBytes = 128 * 4;  // per epilogue warp: the bias of its 128 columns
   static constexpr int kOffStaging = kQkvStages * kStageBytes;
   static constexpr int kOffBias = kOffStaging + kEpiWarps * kStaging;
-  static constexpr int kDynSmem = kOffBias + kEpiWarps * kBiasBytes + 1024;
+  static constexpr int kOffScale = kOffBias + kEpiWarps * kBiasBytes;  // kE4m3: their weight scales, likewise
+  static constexpr int kDynSmem = kOffScale + 1024;
+  static constexpr int kDynSmemE4m3 = kOffScale + kEpiWarps * kBiasBytes + 1024;
 };
 
 struct QkvBars {
@@ -233,12 +249,19 @@ __device__ __forceinline__ void fix_stored_rows(unsigned todo, const uint32_t (&
   }
 }
 
+enum QkvMode { kBf16 = 0, kE4m3 = 1, kLora = 2 };
+
+// One (U, B) pair of a kLora stage: 128 rows and 256 columns, 16 of the rank.
+constexpr int kPairA = kBM * 32, kPairB = kBN * 32, kPairBytes = kPairA + kPairB;
+constexpr int kStagePairs = kStageBytes / kPairBytes;
+
 struct QkvStream {
   int M;       // token rows (B * N_s)
   int N_s;     // tokens per batch item
   int row0;    // the stream's first row in the joint sequence
   int tile0;   // its first tile
   const float* bias;  // [3 H d] or null
+  const float *sx, *sw;  // kE4m3: scales of the token rows and of the weight's rows
 };
 
 struct QkvParams {
@@ -249,7 +272,38 @@ struct QkvParams {
   uint16_t* out[3];   // q, k, v: [B, H, N, d]
   uint16_t* hat[2];   // q_hat, k_hat
   float* r[2];        // rq, rk: [B, H, N]
+  // kLora: the batch items' adapters (none where outside 0 .. n_adapters - 1),
+  // pairs of 16 of the rank, and whether a stream has adapters.
+  const int* index;
+  int n_adapters, rank_pairs;
+  bool lora[2];
 };
+
+// kLora: U [M, 3 * 16 rank_pairs] and the adapters' up weights [n, 3 H d, rank], image then caption stream.
+struct QkvLoraMaps {
+  CUtensorMap u[2], up[2];
+};
+
+// The next run of consecutive batch items with one adapter among rows m0 ..
+// m1 - 1 of a stream, from item b on: the adapter and the rows lo .. hi - 1
+// of the tile.  Items without an adapter are passed over.
+__device__ __forceinline__ bool next_run(const QkvParams& p, int N_s, int m0, int m1, int& b, int& adapter, int& lo,
+                                         int& hi) {
+  while (b * N_s < m1) {
+    adapter = __ldg(p.index + b);
+    lo = max(b * N_s, m0) - m0;
+    do ++b;
+    while (b * N_s < m1 && __ldg(p.index + b) == adapter);
+    hi = min(b * N_s, m1) - m0;
+    if (adapter >= 0 && adapter < p.n_adapters) return true;
+  }
+  return false;
+}
+// The q, k, v parts that columns n0 .. n0 + 255 meet.
+__device__ __forceinline__ void parts_of(int n0, int hd, int& first, int& last) {
+  first = n0 / hd;
+  last = min((n0 + kBN - 1) / hd, 2);
+}
 
 // TMA maps over the five outputs ([B H, N, d] bf16, box 64 columns x 32 rows,
 // 128-byte swizzle: the staging buffers' layout), for warps whose 32 rows lie
@@ -313,6 +367,8 @@ __device__ __forceinline__ QkvStream stream_of(const QkvParams& p, int si) {
   s.row0 = si ? p.s[1].row0 : p.s[0].row0;
   s.tile0 = si ? p.s[1].tile0 : p.s[0].tile0;
   s.bias = si ? p.s[1].bias : p.s[0].bias;
+  s.sx = si ? p.s[1].sx : p.s[0].sx;
+  s.sw = si ? p.s[1].sw : p.s[0].sw;
   return s;
 }
 
@@ -370,11 +426,12 @@ __device__ __forceinline__ void stage_hat_row(uint32_t buf, const uint32_t* y, u
 // One head of the warp's 32 token rows: D accumulator columns at taddr
 // (this lane's row).  row: head 0's row index (b H N + n) of this lane; the
 // head's is row + h N.  bias: this head's D bias values in shared memory.
-template <int D>
+// kE4m3: sx, the row's scale, and wscale, the D columns' in shared memory.
+template <int D, int kMode>
 __device__ __forceinline__ void qkv_emit_head(uint32_t taddr, int ocol, bool live, size_t row,
                                               const uint32_t (&rows)[8], const RowsOut& ro, uint32_t stg,
-                                              uint32_t bias, const QkvParams& p, const QkvOutMaps& om,
-                                              const QkvBars& bars, int lane) {
+                                              uint32_t bias, float sx, uint32_t wscale, const QkvParams& p,
+                                              const QkvOutMaps& om, const QkvBars& bars, int lane) {
   const int hd = p.H * D;
   const int which = ocol / hd;  // 0 q, 1 k, 2 v
   const int h = (ocol - which * hd) / D;
@@ -391,6 +448,13 @@ __device__ __forceinline__ void qkv_emit_head(uint32_t taddr, int ocol, bool liv
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
       const float4 bv = ld_shared_f4(bias + (c32 * 32 + e) * 4);
+      if constexpr (kMode == kE4m3) {
+        const float4 sv = ld_shared_f4(wscale + (c32 * 32 + e) * 4);
+        acc[e] = __float_as_uint(__uint_as_float(acc[e]) * sx * sv.x);
+        acc[e + 1] = __float_as_uint(__uint_as_float(acc[e + 1]) * sx * sv.y);
+        acc[e + 2] = __float_as_uint(__uint_as_float(acc[e + 2]) * sx * sv.z);
+        acc[e + 3] = __float_as_uint(__uint_as_float(acc[e + 3]) * sx * sv.w);
+      }
       yb[c32 * 16 + e / 2] = pack_bf16x2(__uint_as_float(acc[e]) + bv.x, __uint_as_float(acc[e + 1]) + bv.y);
       yb[c32 * 16 + e / 2 + 1] = pack_bf16x2(__uint_as_float(acc[e + 2]) + bv.z, __uint_as_float(acc[e + 3]) + bv.w);
     }
@@ -446,13 +510,15 @@ __device__ __forceinline__ void qkv_emit_head(uint32_t taddr, int ocol, bool liv
   }
 }
 
-template <int D>
+template <int D, int kMode>
 __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
     qkv_norm_kernel(const __grid_constant__ CUtensorMap map_x0, const __grid_constant__ CUtensorMap map_w0,
                     const __grid_constant__ CUtensorMap map_x1, const __grid_constant__ CUtensorMap map_w1,
-                    const __grid_constant__ QkvOutMaps om, const __grid_constant__ QkvParams p,
-                    const float* __restrict__ gq, const float* __restrict__ gk, uint32_t* dev_err) {
+                    const __grid_constant__ QkvOutMaps om, const __grid_constant__ QkvLoraMaps lm,
+                    const __grid_constant__ QkvParams p, const float* __restrict__ gq,
+                    const float* __restrict__ gk, uint32_t* dev_err) {
   using Cfg = QkvCfg<D>;
+  constexpr int kStepK = kMode == kE4m3 ? 2 * kBK : kBK;  // values in a K step's 128-byte rows
   constexpr int kWarpProd = Cfg::kWarpProd, kWarpIssue = Cfg::kWarpIssue;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) QkvBars bars;
@@ -487,7 +553,7 @@ __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
-  const int ksteps = (p.C + kBK - 1) / kBK;
+  const int ksteps = (p.C + kStepK - 1) / kStepK;
 
   if (warp == kWarpProd) {
     if (lane == 0) {
@@ -509,9 +575,41 @@ __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
             break;
           uint8_t* st = sm + s * kStageBytes;
           mbar_arrive_expect_tx(&bars.full[s], kStageBytes);
-          tma_load_2d(st, mx, &bars.full[s], kb * kBK, mt * kBM);
-          tma_load_2d(st + kATile, mw, &bars.full[s], kb * kBK, nt * kBN);
+          tma_load_2d(st, mx, &bars.full[s], kb * kStepK, mt * kBM);
+          tma_load_2d(st + kATile, mw, &bars.full[s], kb * kStepK, nt * kBN);
           ++it;
+        }
+        if constexpr (kMode == kLora) {
+          if (!ok || !(si ? p.lora[1] : p.lora[0])) continue;
+          const int N_s = si ? p.s[1].N_s : p.s[0].N_s, M = si ? p.s[1].M : p.s[0].M;
+          const int m0 = mt * kBM, m1 = min(m0 + kBM, M);
+          const CUtensorMap* mu = si ? &lm.u[1] : &lm.u[0];
+          const CUtensorMap* mup = si ? &lm.up[1] : &lm.up[0];
+          int p0, p1, b = m0 / N_s, adapter, lo, hi, left = 0;
+          parts_of(nt * kBN, p.H * D, p0, p1);
+          const int per_run = (p1 - p0 + 1) * p.rank_pairs;
+          while (next_run(p, N_s, m0, m1, b, adapter, lo, hi)) left += per_run;
+          int in_stage = 0;
+          b = m0 / N_s;
+          while (ok && left > 0 && next_run(p, N_s, m0, m1, b, adapter, lo, hi)) {
+            for (int j = 0; ok && j < per_run; ++j, --left) {
+              const int s = it % kQkvStages;
+              if (in_stage == 0) {
+                if (it >= kQkvStages &&
+                    !(ok = mbar_wait(&bars.empty[s], ((it / kQkvStages) - 1) & 1, ab, dev_err)))
+                  break;
+                mbar_arrive_expect_tx(&bars.full[s], min(left, kStagePairs) * kPairBytes);
+              }
+              uint8_t* st = sm + s * kStageBytes + in_stage * kPairBytes;
+              const int part = p0 + j / p.rank_pairs, kc = j % p.rank_pairs;
+              tma_load_2d(st, mu, &bars.full[s], (part * p.rank_pairs + kc) * 16, m0);
+              tma_load_3d(st + kPairA, mup, &bars.full[s], kc * 16, nt * kBN, adapter);
+              if (++in_stage == kStagePairs || left == 1) {
+                in_stage = 0;
+                ++it;
+              }
+            }
+          }
         }
       }
       if (*ab) {  // aborted: the copies in flight land before the CTA exits
@@ -521,7 +619,8 @@ __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
     }
   } else if (warp == kWarpIssue) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(kBM, kBN, false, false);
+      constexpr uint32_t idesc =
+          kMode == kE4m3 ? idesc_e4m3_f32(kBM, kBN) : idesc_bf16_f32(kBM, kBN, false, false);
       int it = 0, lt = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++lt) {
@@ -536,9 +635,58 @@ __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
           const uint32_t st = smem_u32(sm + s * kStageBytes);
           const uint64_t a = sdesc_sw128(st, 16, 1024), b = sdesc_sw128(st + kATile, 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            umma_bf16_ss(acc, desc_add(a, kk * 32), desc_add(b, kk * 32), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kBK / 16; ++kk) {  // 32 bytes of each row: 16 bf16 or 32 e4m3 values
+            const uint32_t add = (kb > 0 || kk > 0) ? 1u : 0u;
+            if constexpr (kMode == kE4m3)
+              umma_f8_ss(acc, desc_add(a, kk * 32), desc_add(b, kk * 32), idesc, add);
+            else
+              umma_bf16_ss(acc, desc_add(a, kk * 32), desc_add(b, kk * 32), idesc, add);
+          }
           umma_commit(&bars.empty[s]);
+        }
+        if constexpr (kMode == kLora) {
+          const int si = t >= p.s[1].tile0 ? 1 : 0;
+          if (ok && (si ? p.lora[1] : p.lora[0])) {
+            const int tl = t - (si ? p.s[1].tile0 : p.s[0].tile0);
+            const int mt = tl / p.n_tiles, n0 = (tl - mt * p.n_tiles) * kBN;
+            const int N_s = si ? p.s[1].N_s : p.s[0].N_s, M = si ? p.s[1].M : p.s[0].M;
+            const int m0 = mt * kBM, m1 = min(m0 + kBM, M), hd = p.H * D;
+            int p0, p1, b = m0 / N_s, adapter, lo, hi, in_stage = 0;
+            parts_of(n0, hd, p0, p1);
+            while (ok && next_run(p, N_s, m0, m1, b, adapter, lo, hi)) {
+              uint32_t off[4];  // the lanes (rows) that the run does not hold
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const int l = min(max(lo - 32 * w, 0), 32), h = min(max(hi - 32 * w, 0), 32);
+                const uint32_t below = l >= 32 ? 0xFFFFFFFFu : (1u << l) - 1u;
+                const uint32_t upto = h >= 32 ? 0xFFFFFFFFu : (1u << h) - 1u;
+                off[w] = ~(upto & ~below);
+              }
+              for (int part = p0; ok && part <= p1; ++part) {
+                const int c0 = max(part * hd, n0) - n0, c1 = min((part + 1) * hd, n0 + kBN) - n0;
+                const uint32_t desc = idesc_bf16_f32(kBM, c1 - c0, false, false);
+                for (int kc = 0; kc < p.rank_pairs; ++kc) {
+                  const int s = it % kQkvStages;
+                  if (in_stage == 0) {
+                    if (!(ok = mbar_wait(&bars.full[s], (it / kQkvStages) & 1, ab, dev_err))) break;
+                    tc_fence_after();
+                  }
+                  const uint32_t st = smem_u32(sm + s * kStageBytes + in_stage * kPairBytes);
+                  umma_bf16_ss_lanes(acc + c0, sdesc_sw32_kmajor(st, 256),
+                                     sdesc_sw32_kmajor(st + kPairA + c0 * 32, 256), desc, off, 1u);
+                  if (++in_stage == kStagePairs) {
+                    in_stage = 0;
+                    umma_commit(&bars.empty[s]);
+                    ++it;
+                  }
+                }
+              }
+            }
+            if (ok && in_stage > 0) {
+              umma_commit(&bars.empty[it % kQkvStages]);
+              ++it;
+            }
+          }
         }
         if (ok) umma_commit(&bars.acc_full[abuf]);
       }
@@ -551,6 +699,7 @@ __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
     const int lg = warp & 3, wcol = (warp >> 2) * 128;
     const uint32_t stg = smem_u32(sm + Cfg::kOffStaging + warp * Cfg::kStaging);
     const uint32_t bias_w = smem_u32(sm + Cfg::kOffBias + warp * Cfg::kBiasBytes);
+    const uint32_t wscale_w = smem_u32(sm + Cfg::kOffScale + warp * Cfg::kBiasBytes);  // kE4m3
     const uint32_t lane_base = static_cast<uint32_t>(lg * 32) << 16;
     const int hd3 = 3 * p.H * D;
     int lt = 0;
@@ -568,12 +717,22 @@ __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
       __syncwarp();  // the previous tile's reads of the slice are done
       st_shared_v4(bias_w + lane * 16, __float_as_uint(bq.x), __float_as_uint(bq.y), __float_as_uint(bq.z),
                    __float_as_uint(bq.w));
+      if constexpr (kMode == kE4m3) {
+        float4 sq = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col0 + lane * 4 < hd3) sq = __ldg(reinterpret_cast<const float4*>(S.sw + col0) + lane);
+        st_shared_v4(wscale_w + lane * 16, __float_as_uint(sq.x), __float_as_uint(sq.y), __float_as_uint(sq.z),
+                     __float_as_uint(sq.w));
+      }
       const bool ok = mbar_wait(&bars.acc_full[abuf], (lt >> 1) & 1, ab, dev_err);
       if (!__all_sync(0xffffffffu, ok)) break;
       __syncwarp();
       tc_fence_after();
       const int m = mt * kBM + lg * 32 + lane;
       const bool live = m < S.M;
+      float sx = 0.f;
+      if constexpr (kMode == kE4m3) {
+        if (live) sx = __ldg(S.sx + m);
+      }
       const int bi = live ? m / S.N_s : 0;
       const int n = live ? S.row0 + (m - bi * S.N_s) : 0;
       const size_t row = static_cast<size_t>(bi) * p.H * p.N + n;  // < B H N < 2^31 / d
@@ -592,8 +751,8 @@ __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
       for (int j = 0; j < 128 / D; ++j) {
         const int ocol = col0 + j * D;  // the head's first column in Y
         if (ocol < hd3)
-          qkv_emit_head<D>(tmem + lane_base + abuf * kBN + wcol + j * D, ocol, live, row, rows, ro, stg,
-                           bias_w + j * D * 4, p, om, bars, lane);
+          qkv_emit_head<D, kMode>(tmem + lane_base + abuf * kBN + wcol + j * D, ocol, live, row, rows, ro, stg,
+                                  bias_w + j * D * 4, sx, wscale_w + j * D * 4, p, om, bars, lane);
       }
       tc_fence_before();
       mbar_arrive(&bars.acc_empty[abuf]);
@@ -608,13 +767,193 @@ __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
   }
 }
 
+
+// --- U = scale X A^T, rounded to bf16 ---------------------------------------
+// One CTA per batch item, stream and block of 128 of its token rows: an item
+// has one adapter, whose down weights [3 rank, C] are the product's other
+// operand, N = 3 * 16 rank_pairs columns (a rank that is not a multiple of 16
+// reads the TMA's zero fill).  Items without an adapter write nothing (the
+// projection reads nothing of theirs).  The rounding of U to bf16 is that of
+// the projection's own operands: U is the left operand of the second product.
+// Warps 0-3 read the accumulator out (a row a thread), warp 4 loads, warp 5
+// issues.
+constexpr int kDownThreads = 192;
+constexpr int kDownMaxStages = 6;
+constexpr int kDownSmem = 200 * 1024;
+
+struct DownStream {
+  int N_s, blocks, cta0;  // rows per item, its 128-row blocks, the stream's first CTA
+  uint16_t* u;            // [B N_s, 3 * 16 rank_pairs]
+};
+struct DownParams {
+  DownStream s[2];
+  int C, rank_pairs, n_adapters, stages, tmem_cols;
+  const int* index;
+  const float* scale;
+};
+struct DownMaps {
+  CUtensorMap x[2], down[2];  // [B, N_s, C] with 128-row boxes; [3 n, rank, C] with 16 rank_pairs rows
+};
+struct DownBars {
+  uint64_t full[kDownMaxStages], empty[kDownMaxStages], done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__global__ void __launch_bounds__(kDownThreads, 1)
+    lora_down_kernel(const __grid_constant__ DownMaps maps, const __grid_constant__ DownParams p,
+                     uint32_t* dev_err) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) DownBars bars;
+  uint8_t* sm = align1024(smem_raw);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile int* ab = &bars.abort;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int si = static_cast<int>(blockIdx.x) >= p.s[1].cta0 ? 1 : 0;
+  const int N_s = si ? p.s[1].N_s : p.s[0].N_s, blocks = si ? p.s[1].blocks : p.s[0].blocks;
+  const int local = blockIdx.x - (si ? p.s[1].cta0 : p.s[0].cta0);
+  const int item = local / blocks, row0 = (local - item * blocks) * kBM;
+  const int adapter = __ldg(p.index + item);
+  if (adapter < 0 || adapter >= p.n_adapters) return;  // the whole CTA
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+    }
+    mbar_init(&bars.done, 1);
+    bars.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(&bars.tmem_base, p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  const int ksteps = (p.C + kBK - 1) / kBK;
+  const int r16 = 16 * p.rank_pairs;
+  const int stage_bytes = kATile + 3 * r16 * 128;
+  if (warp == 4) {
+    if (lane == 0) {
+      const CUtensorMap* mx = si ? &maps.x[1] : &maps.x[0];
+      const CUtensorMap* md = si ? &maps.down[1] : &maps.down[0];
+      int kb = 0;
+      for (; kb < ksteps; ++kb) {
+        const int s = kb % p.stages;
+        if (kb >= p.stages && !mbar_wait(&bars.empty[s], ((kb / p.stages) - 1) & 1, ab, dev_err)) break;
+        uint8_t* st = sm + s * stage_bytes;
+        mbar_arrive_expect_tx(&bars.full[s], stage_bytes);
+        tma_load_3d(st, mx, &bars.full[s], kb * kBK, row0, item);
+        for (int part = 0; part < 3; ++part)
+          tma_load_3d(st + kATile + part * r16 * 128, md, &bars.full[s], kb * kBK, 0, 3 * adapter + part);
+      }
+      if (*ab) {  // aborted: the copies in flight land before the CTA exits
+        for (int i = (kb > p.stages ? kb - p.stages : 0); i < kb; ++i)
+          mbar_wait_drain(&bars.full[i % p.stages], (i / p.stages) & 1);
+      }
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      const bool one = 3 * r16 <= 256;
+      const uint32_t idesc = idesc_bf16_f32(kBM, one ? 3 * r16 : r16, false, false);
+      for (int kb = 0; kb < ksteps; ++kb) {
+        const int s = kb % p.stages;
+        if (!mbar_wait(&bars.full[s], (kb / p.stages) & 1, ab, dev_err)) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(sm + s * stage_bytes);
+        const uint64_t a = sdesc_sw128(st, 16, 1024), b = sdesc_sw128(st + kATile, 16, 1024);
+        for (int kk = 0; kk < kBK / 16; ++kk) {
+          const uint32_t add = (kb > 0 || kk > 0) ? 1u : 0u;
+          for (int part = 0; part < (one ? 1 : 3); ++part)
+            umma_bf16_ss(tmem + part * r16, desc_add(a, kk * 32), desc_add(b, kk * 32 + part * r16 * 128), idesc,
+                         add);
+        }
+        umma_commit(&bars.empty[s]);
+      }
+      // Every MMA this thread issued has completed once this barrier flips.
+      umma_commit(&bars.done);
+      mbar_wait_drain(&bars.done, 0);
+    }
+  } else {
+    bool ok = mbar_wait(&bars.done, 0, ab, dev_err);
+    ok = __all_sync(0xffffffffu, ok) && !*ab;
+    __syncwarp();
+    if (__all_sync(0xffffffffu, ok)) {
+      tc_fence_after();
+      const float scale = __ldg(p.scale + adapter);
+      const int n = row0 + warp * 32 + lane;
+      uint16_t* u = (si ? p.s[1].u : p.s[0].u) + (static_cast<size_t>(item) * N_s + n) * (3 * r16);
+      for (int c = 0; c < 3 * p.rank_pairs; ++c) {
+        uint32_t v[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c * 16, v);
+        tmem_wait_ld();
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * scale, __uint_as_float(v[2 * i + 1]) * scale);
+        if (n < N_s) {
+          uint4* o = reinterpret_cast<uint4*>(u + c * 16);
+          o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
 }  // namespace
 
+cudaError_t launch_lora_down(const CUtensorMap (&x)[2], const CUtensorMap (&down)[2], const LoraLaunch& l,
+                             const QkvLaunch& a, int B, uint32_t* dev_err, cudaStream_t st) {
+  DownMaps maps;
+  DownParams p;
+  const int r16 = (l.rank + 15) / 16 * 16;
+  int ctas = 0;
+  for (int i = 0; i < 2; ++i) {
+    maps.x[i] = x[i];
+    maps.down[i] = down[i];
+    p.s[i].N_s = a.N_s[i];
+    p.s[i].blocks = l.on[i] ? (a.N_s[i] + kBM - 1) / kBM : 0;
+    p.s[i].cta0 = ctas;
+    p.s[i].u = l.u[i];
+    ctas += B * p.s[i].blocks;
+  }
+  if (ctas == 0) return cudaSuccess;
+  p.C = a.C;
+  p.rank_pairs = r16 / 16;
+  p.n_adapters = l.n_adapters;
+  const int stage_bytes = kATile + 3 * r16 * 128;
+  p.stages = kDownSmem / stage_bytes < kDownMaxStages ? kDownSmem / stage_bytes : kDownMaxStages;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < 3 * r16) p.tmem_cols *= 2;
+  p.index = l.index;
+  p.scale = l.scale;
+  const int smem = p.stages * stage_bytes + 1024;
+  cudaError_t e = cudaFuncSetAttribute(lora_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(lora_down_kernel, dim3(ctas), dim3(kDownThreads), smem, st, maps, p, dev_err);
+}
+
 cudaError_t launch_qkv_norm(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
-                            uint32_t* dev_err, cudaStream_t st) {
+                            uint32_t* dev_err, cudaStream_t st, const LoraLaunch* lora,
+                            const CUtensorMap* lora_maps) {
   QkvOutMaps om;
   for (int i = 0; i < 3; ++i) om.out[i] = out_maps[i];
   for (int i = 0; i < 2; ++i) om.hat[i] = out_maps[3 + i];
+  QkvLoraMaps lm;
+  for (int i = 0; i < 2; ++i) {
+    lm.u[i] = lora ? lora_maps[i] : maps[0];
+    lm.up[i] = lora ? lora_maps[2 + i] : maps[0];
+  }
   QkvParams p;
   p.H = a.H;
   p.C = a.C;
@@ -627,7 +966,10 @@ cudaError_t launch_qkv_norm(const CUtensorMap (&maps)[4], const CUtensorMap (&ou
     p.s[i].row0 = a.row0[i];
     p.s[i].tile0 = tile0;
     p.s[i].bias = a.bias[i];
+    p.s[i].sx = a.sx[i];
+    p.s[i].sw = a.sw[i];
     tile0 += ((a.M[i] + kBM - 1) / kBM) * p.n_tiles;
+    p.lora[i] = lora && lora->on[i];
   }
   p.tiles = tile0;
   for (int i = 0; i < 3; ++i) p.out[i] = a.out[i];
@@ -635,17 +977,27 @@ cudaError_t launch_qkv_norm(const CUtensorMap (&maps)[4], const CUtensorMap (&ou
     p.hat[i] = a.hat[i];
     p.r[i] = a.r[i];
   }
+  p.index = lora ? lora->index : nullptr;
+  p.n_adapters = lora ? lora->n_adapters : 0;
+  p.rank_pairs = lora ? (lora->rank + 15) / 16 : 0;
   if (p.tiles == 0) return cudaSuccess;
   const int sms = device_sm_count();
   const int grid = p.tiles < sms ? p.tiles : sms;
   auto go = [&](auto kernel, int threads, int smem) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(grid), dim3(threads), smem, st, maps[0], maps[1], maps[2], maps[3], om, p, a.gq,
-                      a.gk, dev_err);
+    return launch_pdl(kernel, dim3(grid), dim3(threads), smem, st, maps[0], maps[1], maps[2], maps[3], om, lm, p,
+                      a.gq, a.gk, dev_err);
   };
-  if (a.d == 64) return go(qkv_norm_kernel<64>, QkvCfg<64>::kThreads, QkvCfg<64>::kDynSmem);
-  return go(qkv_norm_kernel<128>, QkvCfg<128>::kThreads, QkvCfg<128>::kDynSmem);
+  auto go_d = [&](auto cfg, auto plain, auto e4m3, auto with_lora) {
+    using Cfg = decltype(cfg);
+    if (lora) return go(with_lora, Cfg::kThreads, Cfg::kDynSmem);
+    if (a.e4m3) return go(e4m3, Cfg::kThreads, Cfg::kDynSmemE4m3);
+    return go(plain, Cfg::kThreads, Cfg::kDynSmem);
+  };
+  if (a.d == 64)
+    return go_d(QkvCfg<64>(), qkv_norm_kernel<64, kBf16>, qkv_norm_kernel<64, kE4m3>, qkv_norm_kernel<64, kLora>);
+  return go_d(QkvCfg<128>(), qkv_norm_kernel<128, kBf16>, qkv_norm_kernel<128, kE4m3>, qkv_norm_kernel<128, kLora>);
 }
 
 }  // namespace jattn
