@@ -6,6 +6,8 @@ plus small conveniences that allocate the output tensors with torch.
 """
 from __future__ import annotations
 
+import contextlib
+
 from ._binding import (KERNEL_KINDS, STATUS, STATUS_CODE, JattnError, declared_symbols, jattn_bwd, jattn_fwd,
                        jattn_fwd_noalloc, jattn_fwd_varlen, jattn_bwd_varlen, jattn_selftest_wait_timeout, jattn_set_sm_limit,
                        jattn_set_deterministic, jattn_kernel_name, jattn_last_device_error, jattn_last_error_message, jattn_profile_enable, jattn_profile_read,
@@ -122,11 +124,12 @@ def qkv_norm(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, H: int, stream=No
     return q, k, v, saved
 
 
+_no_context = contextlib.nullcontext()
+
+
 def _outputs_on(stream, *tensors):
     """Context in which a call's outputs are allocated: the launching stream's, so that the allocator
     orders their reuse by it.  The call runs on the current device, where its tensors must be."""
-    import contextlib
-
     import torch
 
     dev = torch.cuda.current_device()
@@ -134,8 +137,12 @@ def _outputs_on(stream, *tensors):
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
     if stream is None:
-        return contextlib.nullcontext()
+        return _no_context
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+# The functions below hand the raw pointers of the outputs that they have just allocated to the
+# binding: only a caller's tensors need its checks.
 
 
 def add_norm(x, g, residual=None, eps: float = 1e-6, stream=None):
@@ -144,12 +151,12 @@ def add_norm(x, g, residual=None, eps: float = 1e-6, stream=None):
     for add_norm_backward."""
     import torch
 
-    C = g.numel()
     with _outputs_on(stream, x, g, residual):
         y = torch.empty_like(x)
         h = x if residual is None else torch.empty_like(x)
         r = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    jattn_add_norm(x, residual, g, r.numel(), C, eps, None if residual is None else h, y, r, stream)
+    jattn_add_norm(x, residual, g, r.numel(), g.numel(), eps, None if residual is None else h.data_ptr(),
+                   y.data_ptr(), r.data_ptr(), stream)
     return y, h, r
 
 
@@ -158,13 +165,13 @@ def add_norm_fp8(x, g, residual=None, eps: float = 1e-6, stream=None):
     standing for scale * y8 (what qkv_norm_fp8 reads)."""
     import torch
 
-    C = g.numel()
     with _outputs_on(stream, x, g, residual):
         y8 = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         h = x if residual is None else torch.empty_like(x)
         r = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         scale = torch.empty_like(r)
-    jattn_add_norm_fp8(x, residual, g, r.numel(), C, eps, None if residual is None else h, y8, scale, r, stream)
+    jattn_add_norm_fp8(x, residual, g, r.numel(), g.numel(), eps, None if residual is None else h.data_ptr(),
+                       y8.data_ptr(), scale.data_ptr(), r.data_ptr(), stream)
     return y8, scale, h, r
 
 
@@ -177,7 +184,7 @@ def add_norm_backward(dy, h, r, g, dh=None, stream=None):
     with _outputs_on(stream, dy, h, r, g, dh):
         dx, dg = torch.empty_like(dy), torch.empty_like(g)
         work = torch.empty(jattn_add_norm_bwd_bytes(T, C), dtype=torch.uint8, device=dy.device)
-    jattn_add_norm_bwd(dy, dh, h, r, g, T, C, dx, dg, work, stream)
+    jattn_add_norm_bwd(dy, dh, h, r, g, T, C, dx.data_ptr(), dg.data_ptr(), work.data_ptr(), stream)
     return dx, dg
 
 
@@ -188,7 +195,7 @@ def quant_rows(x, stream=None):
     with _outputs_on(stream, x):
         x8 = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    jattn_quant_rows(x, scale.numel(), x.shape[-1], x8, scale, stream)
+    jattn_quant_rows(x, scale.numel(), x.shape[-1], x8.data_ptr(), scale.data_ptr(), stream)
     return x8, scale
 
 
@@ -199,7 +206,7 @@ def _projected(x_img, x_txt, H: int, d: int):
     B, N_img, C = x_img.shape
     N_txt = x_txt.shape[1]
     dev = x_img.device
-    q, k, v = (torch.empty((B, H, N_img + N_txt, d), dtype=torch.bfloat16, device=dev) for _ in range(3))
+    q, k, v = torch.empty((3, B, H, N_img + N_txt, d), dtype=torch.bfloat16, device=dev).unbind(0)
     saved = torch.empty(jattn_saved_bytes(B, H, N_img, N_txt, d), dtype=torch.uint8, device=dev)
     return (q, k, v, saved), (B, H, N_img, N_txt, d, C)
 
@@ -212,7 +219,7 @@ def qkv_norm_fp8(x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt, sw_t
     with _outputs_on(stream, x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt, sw_txt, b_txt, gq, gk):
         out, sizes = _projected(x_img, x_txt, H, gq.shape[0])
     jattn_qkv_norm_fp8(x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt, sw_txt, b_txt, gq, gk, *sizes,
-                       *out, stream)
+                       *(t.data_ptr() for t in out), stream)
     return out
 
 
@@ -224,12 +231,11 @@ def qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, H: int, down
     (both None: no adapters in that stream)."""
     import torch
 
-    n = scale.numel()
     rank = next((u.shape[-1] for u in (up_img, up_txt) if u is not None), 8)
     with _outputs_on(stream, x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_img, up_img, down_txt, up_txt,
                      scale, index):
         out, sizes = _projected(x_img, x_txt, H, gq.shape[0])
         work = torch.empty(jattn_qkv_norm_lora_bytes(*sizes[:5], rank), dtype=torch.uint8, device=x_img.device)
     jattn_qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_img, up_img, down_txt, up_txt, scale,
-                        index, n, rank, *sizes, *out, work, stream)
+                        index, scale.numel(), rank, *sizes, *(t.data_ptr() for t in out), work.data_ptr(), stream)
     return out

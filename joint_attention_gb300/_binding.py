@@ -164,10 +164,14 @@ def declared_symbols(header: str = HEADER) -> list[str]:
 
 def _ptr(x, name: str, dtype=None, numel: int | None = None):
     """Raw pointer of a tensor (checked) or an int / None passed through."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
+    try:  # the checks in one line first: a projection call has two dozen arguments
+        if (x.is_cuda and x.is_contiguous() and (dtype is None or x.dtype is dtype)
+                and (numel is None or x.numel() == numel)):
+            return x.data_ptr()
+    except AttributeError:
+        pass
     import torch
 
     if not isinstance(x, torch.Tensor):
@@ -178,16 +182,15 @@ def _ptr(x, name: str, dtype=None, numel: int | None = None):
         raise ValueError(f"{name}: must be contiguous")
     if dtype is not None and x.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {x.dtype}")
-    if numel is not None and x.numel() != numel:
-        raise ValueError(f"{name}: expected {numel} elements, got {x.numel()}")
-    return x.data_ptr()
+    raise ValueError(f"{name}: expected {numel} elements, got {x.numel()}")
 
 
 def _stream(stream):
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same handle without a Stream object
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -479,12 +482,13 @@ def jattn_add_norm_bwd_bytes(T: int, C: int) -> int:
     return int(load_library().jattn_add_norm_bwd_bytes(T, C))
 
 
-def _work_ptr(work, nbytes: int):
-    """Raw pointer of a work buffer of at least nbytes bytes (any dtype)."""
-    import torch
-
+def _work_ptr(work, bytes_of, *sizes):
+    """Raw pointer of a work buffer of at least bytes_of(*sizes) bytes (any dtype)."""
     if work is None or isinstance(work, int):
         return work
+    import torch
+
+    nbytes = bytes_of(*sizes)
     if not isinstance(work, torch.Tensor) or not work.is_cuda or not work.is_contiguous():
         raise ValueError("work: expected a contiguous CUDA tensor")
     if work.numel() * work.element_size() < nbytes:
@@ -501,11 +505,16 @@ def jattn_add_norm_bwd(dy, dh, h, r, g, T: int, C: int, dx, dg, work, stream=Non
     lib = load_library()
     rc = lib.jattn_add_norm_bwd(_ptr(dy, "dy", bf, e), _ptr(dh, "dh", bf, e), _ptr(h, "h", bf, e),
                                 _ptr(r, "r", f32, T), _ptr(g, "g", f32, C), T, C, _ptr(dx, "dx", bf, e),
-                                _ptr(dg, "dg", f32, C), _work_ptr(work, lib.jattn_add_norm_bwd_bytes(T, C)),
+                                _ptr(dg, "dg", f32, C), _work_ptr(work, jattn_add_norm_bwd_bytes, T, C),
                                 _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_add_norm_bwd")
     return rc
+
+
+def _saved(saved, *sizes):
+    """Raw pointer of a training pair's buffer for a [B, H, N, d] shape."""
+    return saved if saved is None or isinstance(saved, int) else _saved_ptr(saved, jattn_saved_bytes(*sizes))
 
 
 def jattn_qkv_norm_fp8(x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt, sw_txt, b_txt, gq, gk, B: int,
@@ -518,7 +527,6 @@ def jattn_qkv_norm_fp8(x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt
     e = B * H * (N_img + N_txt) * d
     bf, f32, f8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
     yc = 3 * H * d
-    nb = jattn_saved_bytes(B, H, N_img, N_txt, d)
     args = []
     for n, N_s, x, sx, w, sw, b in (("img", N_img, x_img, sx_img, w_img, sw_img, b_img),
                                     ("txt", N_txt, x_txt, sx_txt, w_txt, sw_txt, b_txt)):
@@ -527,7 +535,7 @@ def jattn_qkv_norm_fp8(x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt
                  _ptr(b, "b_" + n, f32, yc)]
     rc = load_library().jattn_qkv_norm_fp8(*args, _ptr(gq, "gq", f32, d), _ptr(gk, "gk", f32, d), B, H, N_img,
                                            N_txt, d, C, _ptr(q, "q", bf, e), _ptr(k, "k", bf, e),
-                                           _ptr(v, "v", bf, e), _saved_ptr(saved, nb), _stream(stream))
+                                           _ptr(v, "v", bf, e), _saved(saved, B, H, N_img, N_txt, d), _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_qkv_norm_fp8")
     return rc
@@ -549,7 +557,6 @@ def jattn_qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_i
     e = B * H * (N_img + N_txt) * d
     bf, f32 = torch.bfloat16, torch.float32
     yc = 3 * H * d
-    nb = jattn_saved_bytes(B, H, N_img, N_txt, d)
     args = []
     for n, N_s, x, w, b in (("img", N_img, x_img, w_img, b_img), ("txt", N_txt, x_txt, w_txt, b_txt)):
         args += [_ptr(x, "x_" + n, bf, B * N_s * C), _ptr(w, "w_" + n, bf, yc * C if N_s else None),
@@ -559,8 +566,8 @@ def jattn_qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_i
         args += [_ptr(down, "down_" + n, bf, n_adapters * 3 * rank * C), _ptr(up, "up_" + n, bf, n_adapters * yc * rank)]
     rc = load_library().jattn_qkv_norm_lora(
         *args, _ptr(scale, "scale", f32, n_adapters), _ptr(index, "index", torch.int32, B), n_adapters, rank, B, H,
-        N_img, N_txt, d, C, _ptr(q, "q", bf, e), _ptr(k, "k", bf, e), _ptr(v, "v", bf, e), _saved_ptr(saved, nb),
-        _work_ptr(work, jattn_qkv_norm_lora_bytes(B, H, N_img, N_txt, d, rank)), _stream(stream))
+        N_img, N_txt, d, C, _ptr(q, "q", bf, e), _ptr(k, "k", bf, e), _ptr(v, "v", bf, e), _saved(saved, B, H, N_img, N_txt, d),
+        _work_ptr(work, jattn_qkv_norm_lora_bytes, B, H, N_img, N_txt, d, rank), _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_qkv_norm_lora")
     return rc

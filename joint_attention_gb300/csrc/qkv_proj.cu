@@ -77,20 +77,22 @@ constexpr uint32_t kDeadRow = 0xFFFFFFFFu;
 // Eight epilogue warps (warps w and w + 4 take the TMEM lanes of warp w % 4
 // and columns 0-127 / 128-255 of the tile: two heads of d = 64, or one of
 // d = 128), then the TMA producer and the MMA issuer.  Each epilogue warp
-// stages its rows in shared memory: at d = 64 raw rows and q_hat / k_hat rows
-// in two buffers, at d = 128 one buffer used for each 64-column half.
+// stages its rows in shared memory, in two buffers: at d = 64 raw rows and
+// q_hat / k_hat rows, at d = 128 the two 64-column halves, raw, then q_hat /
+// k_hat.
 template <int D>
 struct QkvCfg {
   static constexpr int kEpiWarps = 8;
   static constexpr int kEpiThreads = 32 * kEpiWarps;
   static constexpr int kWarpProd = kEpiWarps, kWarpIssue = kEpiWarps + 1;
   static constexpr int kThreads = 32 * (kEpiWarps + 2);
-  static constexpr int kBuffers = D == 64 ? 2 : 1;
-  static constexpr int kStaging = kBuffers * kStagingBytes;
+  static constexpr int kStaging = 2 * kStagingBytes;
   static constexpr int kBiasBytes = 128 * 4;  // per epilogue warp: the bias of its 128 columns
   static constexpr int kOffStaging = kQkvStages * kStageBytes;
   static constexpr int kOffBias = kOffStaging + kEpiWarps * kStaging;
-  static constexpr int kOffScale = kOffBias + kEpiWarps * kBiasBytes;  // kE4m3: their weight scales, likewise
+  static constexpr int kSpareBytes = D == 128 ? 256 : 0;  // per epilogue warp: fix_staged_halves' row
+  static constexpr int kOffSpare = kOffBias + kEpiWarps * kBiasBytes;
+  static constexpr int kOffScale = kOffSpare + kEpiWarps * kSpareBytes;  // kE4m3: their weight scales, likewise
   static constexpr int kDynSmem = kOffScale + 1024;
   static constexpr int kDynSmemE4m3 = kOffScale + kEpiWarps * kBiasBytes + 1024;
 };
@@ -210,42 +212,43 @@ __device__ __forceinline__ void fix_staged_rows(unsigned todo, uint32_t raw, uin
     st_shared_u32(staged(hat, o, lane >> 2) + off, pack_bf16x2(f[0], f[1]));
   }
 }
-// d = 128 (fix_stored_rows): the row's raw values come from the owner's
-// registers (yb, by shuffles) and the corrected elements are stored again
-// over the owner's q_hat / k_hat row, which is already written.
-__device__ __forceinline__ void fix_stored_rows(unsigned todo, const uint32_t (&yb)[64], float r, size_t hrow,
-                                                uint16_t* hat_base, const float* g, int lane) {
+// d = 128 (fix_staged_halves): the row's raw values no longer are in a buffer
+// (both hold a half of q_hat / k_hat): the owner writes them to its warp's
+// spare row, each lane takes four and writes its words (re-rounded where
+// needed) over the staged halves.
+__device__ __forceinline__ void fix_staged_halves(unsigned todo, const uint32_t (&yb)[64], uint32_t spare,
+                                                  uint32_t hat, float r, const float* g, int lane) {
   while (todo) {
     const int o = __ffs(todo) - 1;
     todo &= todo - 1;
-    uint32_t mine[2];
+    if (lane == o) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      const uint32_t t = __shfl_sync(0xffffffffu, yb[i], o);
-      if ((i & 31) == lane) mine[i >> 5] = t;
+      for (int c = 0; c < 16; ++c)
+        st_shared_v4(spare + c * 16, yb[4 * c], yb[4 * c + 1], yb[4 * c + 2], yb[4 * c + 3]);
     }
     const float ro = __shfl_sync(0xffffffffu, r, o);
-    const uint32_t lo = __shfl_sync(0xffffffffu, static_cast<uint32_t>(hrow), o);
-    const uint32_t hi = __shfl_sync(0xffffffffu, static_cast<uint32_t>(hrow >> 32), o);
-    uint16_t* hat = hat_base + ((static_cast<size_t>(hi) << 32) | lo) * 128;
+    __syncwarp();
+    // Words 2 lane, 2 lane + 1 of row o: elements 4 lane .. 4 lane + 3.
+    const uint32_t w0 = ld_shared_u32(spare + lane * 8), w1 = ld_shared_u32(spare + lane * 8 + 4);
     float s = 0.f, c = 0.f;
-    add_sq_df(mine[0], s, c);
-    add_sq_df(mine[1], s, c);
+    add_sq_df(w0, s, c);
+    add_sq_df(w1, s, c);
     warp_sum_df(s, c);
     float rh, rl;
     rsqrt_mean_eps_df(s, c, 1.f / 128, rh, rl);
+    float f[4];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int e0 = 2 * (lane + 32 * w);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float x = j ? bf_hi(mine[w]) : bf_lo(mine[w]);
-        if (near_bf16_midpoint(__fmul_rn(__fmul_rn(g[e0 + j], x), ro))) {
-          const float z = round_bf16_df(g[e0 + j], x, rh, rl);
-          hat[e0 + j] = static_cast<uint16_t>(pack_bf16x2(z, 0.f) & 0xFFFFu);
-        }
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int e = 4 * lane + j;
+      const uint32_t w = j < 2 ? w0 : w1;
+      const float x = (j & 1) ? bf_hi(w) : bf_lo(w);
+      const float z = __fmul_rn(__fmul_rn(g[e], x), ro);
+      f[j] = near_bf16_midpoint(z) ? round_bf16_df(g[e], x, rh, rl) : z;
     }
+    const uint32_t at = staged(hat + (lane >> 4) * kStagingBytes, o, (lane & 15) >> 1) + (lane & 1) * 8;
+    st_shared_u32(at, pack_bf16x2(f[0], f[1]));
+    st_shared_u32(at + 4, pack_bf16x2(f[2], f[3]));
+    __syncwarp();  // the spare row is free again
   }
 }
 
@@ -374,23 +377,25 @@ __device__ __forceinline__ QkvStream stream_of(const QkvParams& p, int si) {
 
 // r of one row from its bf16 values (packed pairs; exact squares): a
 // balanced tree, built block by block (16 values, then across the D / 16
-// blocks) so that few partial sums are live at once.
+// blocks) so that few partial sums are live at once.  Two neighbouring sums at
+// a time in packed fp32 arithmetic; the fma adds two exact squares with one
+// rounding, as an addition of them does.
 template <int D>
 __device__ __forceinline__ float row_rsqrt(const uint32_t (&yb)[D / 2]) {
   float blk[D / 16];
 #pragma unroll
   for (int b = 0; b < D / 16; ++b) {
-    float t[8];
+    uint64_t t[4];  // sums of the words (0, 1), (2, 3), (4, 5), (6, 7)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t u = yb[b * 8 + i];
-      t[i] = __fadd_rn(__fmul_rn(bf_lo(u), bf_lo(u)), __fmul_rn(bf_hi(u), bf_hi(u)));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = yb[b * 8 + 2 * i], v = yb[b * 8 + 2 * i + 1];
+      const uint64_t lo = f2_make(bf_lo(u), bf_lo(v)), hi = f2_make(bf_hi(u), bf_hi(v));
+      t[i] = f2_fma(lo, lo, f2_mul(hi, hi));
     }
-#pragma unroll
-    for (int w = 4; w >= 1; w >>= 1)
-#pragma unroll
-      for (int i = 0; i < w; ++i) t[i] = __fadd_rn(t[i], t[i + w]);
-    blk[b] = t[0];
+    const uint64_t s = f2_add(f2_add(t[0], t[2]), f2_add(t[1], t[3]));
+    float s0, s1;
+    f2_split(s, s0, s1);
+    blk[b] = __fadd_rn(s0, s1);
   }
 #pragma unroll
   for (int w = D / 32; w >= 1; w >>= 1)
@@ -399,24 +404,37 @@ __device__ __forceinline__ float row_rsqrt(const uint32_t (&yb)[D / 2]) {
   return rsqrtf(__fadd_rn(__fmul_rn(blk[0], 1.f / D), kEps));
 }
 
+// Elements near a bf16 midpoint, two at a time: the smaller of the low halves'
+// distances above the window's start, per half of m, starting from kNoneNear
+// (the test of near_bf16_midpoint).
+constexpr uint32_t kNoneNear = 0xFFFFFFFFu;
+__device__ __forceinline__ void near_pair(float z0, float z1, uint32_t& m) {
+  constexpr uint32_t kFrom = (0x10000u + kTieWindow / 2 - 0x8000u) & 0xFFFFu;
+  m = __viaddmin_u16x2(__byte_perm(__float_as_uint(z0), __float_as_uint(z1), 0x5410), kFrom * 0x10001u, m);
+}
+__device__ __forceinline__ bool any_near(uint32_t m) {
+  return (m & 0xFFFFu) < kTieWindow || (m >> 16) < kTieWindow;
+}
+
 // 64 columns of this lane's q_hat / k_hat row, (g x) r per element, staged
 // 16 bytes at a time into its row of the staging buffer; `near` collects the
 // elements within the midpoint window.
-__device__ __forceinline__ void stage_hat_row(uint32_t buf, const uint32_t* y, uint32_t g, float r, bool& near,
+__device__ __forceinline__ void stage_hat_row(uint32_t buf, const uint32_t* y, uint32_t g, float r, uint32_t& near,
                                               int lane) {
+  const uint64_t r2 = f2_make(r, r);
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     // The gains through ordered shared loads: loaded chunk by chunk, not all
     // at once ahead of the loop.
     const float4 ga = ld_shared_f4(g + c * 32), gb = ld_shared_f4(g + c * 32 + 16);
-    const float gv[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
+    const uint64_t gv[4] = {f2_make(ga.x, ga.y), f2_make(ga.z, ga.w), f2_make(gb.x, gb.y), f2_make(gb.z, gb.w)};
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t yv = y[4 * c + i];
-      const float z0 = __fmul_rn(__fmul_rn(gv[2 * i], bf_lo(yv)), r);
-      const float z1 = __fmul_rn(__fmul_rn(gv[2 * i + 1], bf_hi(yv)), r);
-      near |= near_bf16_midpoint(z0) | near_bf16_midpoint(z1);
+      float z0, z1;
+      f2_split(f2_mul(f2_mul(gv[i], f2_make(bf_lo(yv), bf_hi(yv))), r2), z0, z1);
+      near_pair(z0, z1, near);
       w[i] = pack_bf16x2(z0, z1);
     }
     st_shared_v4(staged(buf, lane, c), w[0], w[1], w[2], w[3]);
@@ -430,7 +448,7 @@ __device__ __forceinline__ void stage_hat_row(uint32_t buf, const uint32_t* y, u
 template <int D, int kMode>
 __device__ __forceinline__ void qkv_emit_head(uint32_t taddr, int ocol, bool live, size_t row,
                                               const uint32_t (&rows)[8], const RowsOut& ro, uint32_t stg,
-                                              uint32_t bias, float sx, uint32_t wscale, const QkvParams& p,
+                                              uint32_t bias, float sx, uint32_t wscale, uint32_t spare, const QkvParams& p,
                                               const QkvOutMaps& om, const QkvBars& bars, int lane) {
   const int hd = p.H * D;
   const int which = ocol / hd;  // 0 q, 1 k, 2 v
@@ -440,6 +458,7 @@ __device__ __forceinline__ void qkv_emit_head(uint32_t taddr, int ocol, bool liv
   const uint32_t raw = stg;
   // Y = bf16(acc + bias), 32 columns at a time (packed pairs).
   uint32_t yb[D / 2];
+  const uint64_t sx2 = f2_make(sx, sx);
 #pragma unroll
   for (int c32 = 0; c32 < D / 32; ++c32) {
     uint32_t acc[32];
@@ -448,15 +467,21 @@ __device__ __forceinline__ void qkv_emit_head(uint32_t taddr, int ocol, bool liv
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
       const float4 bv = ld_shared_f4(bias + (c32 * 32 + e) * 4);
+      uint64_t y0 = f2_make(__uint_as_float(acc[e]), __uint_as_float(acc[e + 1]));
+      uint64_t y1 = f2_make(__uint_as_float(acc[e + 2]), __uint_as_float(acc[e + 3]));
       if constexpr (kMode == kE4m3) {
         const float4 sv = ld_shared_f4(wscale + (c32 * 32 + e) * 4);
-        acc[e] = __float_as_uint(__uint_as_float(acc[e]) * sx * sv.x);
-        acc[e + 1] = __float_as_uint(__uint_as_float(acc[e + 1]) * sx * sv.y);
-        acc[e + 2] = __float_as_uint(__uint_as_float(acc[e + 2]) * sx * sv.z);
-        acc[e + 3] = __float_as_uint(__uint_as_float(acc[e + 3]) * sx * sv.w);
+        y0 = f2_fma(f2_mul(y0, sx2), f2_make(sv.x, sv.y), f2_make(bv.x, bv.y));
+        y1 = f2_fma(f2_mul(y1, sx2), f2_make(sv.z, sv.w), f2_make(bv.z, bv.w));
+      } else {
+        y0 = f2_add(y0, f2_make(bv.x, bv.y));
+        y1 = f2_add(y1, f2_make(bv.z, bv.w));
       }
-      yb[c32 * 16 + e / 2] = pack_bf16x2(__uint_as_float(acc[e]) + bv.x, __uint_as_float(acc[e + 1]) + bv.y);
-      yb[c32 * 16 + e / 2 + 1] = pack_bf16x2(__uint_as_float(acc[e + 2]) + bv.z, __uint_as_float(acc[e + 3]) + bv.w);
+      float a0, a1, a2, a3;
+      f2_split(y0, a0, a1);
+      f2_split(y1, a2, a3);
+      yb[c32 * 16 + e / 2] = pack_bf16x2(a0, a1);
+      yb[c32 * 16 + e / 2 + 1] = pack_bf16x2(a2, a3);
     }
   }
   const float* g = which == 0 ? bars.gq : bars.gk;
@@ -470,9 +495,9 @@ __device__ __forceinline__ void qkv_emit_head(uint32_t taddr, int ocol, bool liv
       return;
     }
     const float r = row_rsqrt<D>(yb);
-    bool near = false;
+    uint32_t near = kNoneNear;
     stage_hat_row(hat, yb, smem_u32(g), r, near, lane);
-    const unsigned todo = __ballot_sync(0xffffffffu, near && live);
+    const unsigned todo = __ballot_sync(0xffffffffu, any_near(near) && live);
     __syncwarp();
     if (todo) {
       fix_staged_rows(todo, raw, hat, r, g, lane);
@@ -483,30 +508,31 @@ __device__ __forceinline__ void qkv_emit_head(uint32_t taddr, int ocol, bool liv
     if (live) r_of(p, which)[hrow] = r;
     __syncwarp();
   } else {
-    // d = 128: each 64-column half through the raw staging buffer.
+    // d = 128: a 64-column half in each buffer, raw, then q_hat / k_hat.
+    staging_free(lane);
 #pragma unroll
     for (int h64 = 0; h64 < 2; ++h64) {
-      staging_free(lane);
-      stage_row(raw, yb + h64 * 32, lane);
-      emit_rows<D>(raw, out_map(om, which), out_of(p, which), ro, rows, head_rows, h, h64 * 64, lane);
-      __syncwarp();
+      const uint32_t buf = raw + h64 * kStagingBytes;
+      stage_row(buf, yb + h64 * 32, lane);
+      emit_rows<D>(buf, out_map(om, which), out_of(p, which), ro, rows, head_rows, h, h64 * 64, lane);
     }
+    __syncwarp();
     if (which == 2) return;
     const float r = row_rsqrt<D>(yb);
-    bool near = false;
-#pragma unroll
-    for (int h64 = 0; h64 < 2; ++h64) {
-      staging_free(lane);
-      stage_hat_row(raw, yb + h64 * 32, smem_u32(g + h64 * 64), r, near, lane);
-      emit_rows<D>(raw, hat_map(om, which), hat_of(p, which), ro, rows, head_rows, h, h64 * 64, lane);
-      __syncwarp();
-    }
-    // The row re-rounding below stores over these rows: the tile stores first.
-    if (lane == 0) bulk_wait_group0();
+    uint32_t near = kNoneNear;
+    staging_free(lane);
+    stage_hat_row(raw, yb, smem_u32(g), r, near, lane);
+    stage_hat_row(raw + kStagingBytes, yb + 32, smem_u32(g + 64), r, near, lane);
+    const unsigned todo = __ballot_sync(0xffffffffu, any_near(near) && live);
     __syncwarp();
+    if (todo)
+      fix_staged_halves(todo, *reinterpret_cast<const uint32_t(*)[64]>(yb), spare, raw, r, g, lane);
+#pragma unroll
+    for (int h64 = 0; h64 < 2; ++h64)
+      emit_rows<D>(raw + h64 * kStagingBytes, hat_map(om, which), hat_of(p, which), ro, rows, head_rows, h, h64 * 64,
+                   lane);
     if (live) r_of(p, which)[hrow] = r;
-    const unsigned todo = __ballot_sync(0xffffffffu, near && live);
-    if (todo) fix_stored_rows(todo, *reinterpret_cast<const uint32_t(*)[64]>(yb), r, hrow, hat_of(p, which), g, lane);
+    __syncwarp();
   }
 }
 
@@ -700,6 +726,7 @@ __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
     const uint32_t stg = smem_u32(sm + Cfg::kOffStaging + warp * Cfg::kStaging);
     const uint32_t bias_w = smem_u32(sm + Cfg::kOffBias + warp * Cfg::kBiasBytes);
     const uint32_t wscale_w = smem_u32(sm + Cfg::kOffScale + warp * Cfg::kBiasBytes);  // kE4m3
+    const uint32_t spare_w = smem_u32(sm + Cfg::kOffSpare + warp * Cfg::kSpareBytes);
     const uint32_t lane_base = static_cast<uint32_t>(lg * 32) << 16;
     const int hd3 = 3 * p.H * D;
     int lt = 0;
@@ -752,7 +779,7 @@ __global__ void __launch_bounds__(QkvCfg<D>::kThreads, 1)
         const int ocol = col0 + j * D;  // the head's first column in Y
         if (ocol < hd3)
           qkv_emit_head<D, kMode>(tmem + lane_base + abuf * kBN + wcol + j * D, ocol, live, row, rows, ro, stg,
-                                  bias_w + j * D * 4, sx, wscale_w + j * D * 4, p, om, bars, lane);
+                                  bias_w + j * D * 4, sx, wscale_w + j * D * 4, spare_w, p, om, bars, lane);
       }
       tc_fence_before();
       mbar_arrive(&bars.acc_empty[abuf]);
