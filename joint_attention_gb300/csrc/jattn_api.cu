@@ -287,7 +287,7 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t c
   return r == CUDA_SUCCESS;
 }
 
-bool encode_pair_map(CUtensorMap* map, const void* base, int planes, int64_t rows, int cols, int box_rows) {
+bool encode_unit_map(CUtensorMap* map, const void* base, int planes, int64_t rows, int cols, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
@@ -702,7 +702,7 @@ struct QkvCall {
 
 size_t lora_u_bytes(int64_t rows, int rank) {
   const int64_t r16 = (rank + 15) / 16 * 16;
-  return (static_cast<size_t>(rows) * 3 * r16 * 2 + 255) & ~static_cast<size_t>(255);
+  return (static_cast<size_t>(rows) * 2 * 3 * r16 * 2 + 255) & ~static_cast<size_t>(255);
 }
 
 int check_lora(int rank) {
@@ -799,11 +799,13 @@ int qkv_body(const QkvCall& c) {
   a.hat[1] = reinterpret_cast<uint16_t*>(base + sl.khat);
   a.r[0] = reinterpret_cast<float*>(base + sl.rq);
   a.r[1] = reinterpret_cast<float*>(base + sl.rk);
+  a.pair = qkv_uses_pairs(a);
+  const int w_rows = kQkvWRows(d, a.pair);
   CUtensorMap maps[4];
   for (int i = 0; i < 2; ++i) {
     const int j = n_s[i] ? i : 1 - i;  // a stream without rows launches no tiles: any valid map
     if (!encode_rows_map(&maps[2 * i], c.x[j], a.M[j], C, 128, c.e4m3) ||
-        !encode_rows_map(&maps[2 * i + 1], c.w[j], ycols, C, 256, c.e4m3))
+        !encode_rows_map(&maps[2 * i + 1], c.w[j], ycols, C, w_rows, c.e4m3))
       return fail(JATTN_ERR_CUDA, "cuTensorMapEncodeTiled");
   }
   CUtensorMap out_maps[5];
@@ -825,8 +827,8 @@ int qkv_body(const QkvCall& c) {
       l.on[i] = c.down[i] && n_s[i] > 0;
       if (!l.on[i]) {
         lora_maps[i] = lora_maps[2 + i] = down_maps[i] = item_maps[i] = maps[0];
-      } else if (!encode_pair_map(&lora_maps[i], l.u[i], 0, a.M[i], 3 * r16, 128) ||
-                 !encode_pair_map(&lora_maps[2 + i], c.up[i], c.n_adapters, ycols, c.rank, 256) ||
+      } else if (!encode_unit_map(&lora_maps[i], l.u[i], 0, a.M[i], 6 * r16, 128) ||
+                 !encode_unit_map(&lora_maps[2 + i], c.up[i], c.n_adapters, ycols, c.rank, w_rows) ||
                  !encode_bhnd_map_rows(&down_maps[i], c.down[i], 3 * c.n_adapters, c.rank, C, r16) ||
                  !encode_bhnd_map(&item_maps[i], c.x[i], c.B, n_s[i], C)) {
         return fail(JATTN_ERR_CUDA, "cuTensorMapEncodeTiled");

@@ -27,6 +27,27 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// The same with thread-block clusters of `cluster` CTAs (1: none).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), int cluster, dim3 grid, dim3 block, size_t smem,
+                               cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 // Tile sizes of the tensor-core kernels: 128 query rows per tile (the
 // tcgen05 M = 128 accumulator, one row per TMEM lane), 128 keys per tile.
 constexpr int kTileM = 128;
@@ -152,10 +173,15 @@ int attn_bwd_counter_words(const AttnShape& s);
 // --- QKV projection with the QK-RMSNorm epilogue ---------------------------
 // Stream 0 is the image stream, stream 1 the caption stream; maps holds the
 // TMA maps of x0, w0, x1, w1 (encode_rows_map: x with 128-row boxes, w with
-// 256-row boxes).  A stream with M = 0 rows launches no tiles (its maps are
+// kQkvWRows boxes).  A stream with M = 0 rows launches no tiles (its maps are
 // then any valid map).
+// Tiles: 256 rows x 256 columns by a pair of CTAs (qkv_uses_pairs), each
+// loading half of the weight rows, or 128 rows x one head by one CTA.
+constexpr int kQkvCols(int d, bool pair) { return pair ? 256 : d; }
+constexpr int kQkvWRows(int d, bool pair) { return pair ? 128 : d; }
 struct QkvLaunch {
   int H, C, N, d;
+  bool pair;    // the tiles, as the weights' maps were made for (qkv_uses_pairs)
   int M[2];     // token rows B * N_s
   int N_s[2];   // tokens per batch item
   int row0[2];  // first row in the joint sequence
@@ -173,16 +199,22 @@ struct LoraLaunch {
   const int* index;    // [B] the items' adapters
   const float* scale;  // [n_adapters]
   bool on[2];          // whether a stream has adapters (and rows)
-  uint16_t* u[2];      // scratch [M, 3 * 16 ceil(rank / 16)]
+  uint16_t* u[2];      // scratch [M, 2 * 3 * 16 ceil(rank / 16)]
 };
 // out_maps: q, k, v, q_hat, k_hat as encode_bhnd_map_rows(..., 32) maps.
-// lora_maps (with lora): encode_pair_map maps of both streams' U (128-row
-// boxes), then of their up weights [n, 3 H d, rank] (256-row boxes); a stream
-// without adapters: any valid map.
+// lora_maps (with lora): encode_unit_map maps of both streams' U (128-row
+// boxes), then of their up weights [n, 3 H d, rank] (kQkvWRows boxes); a
+// stream without adapters: any valid map.
 cudaError_t launch_qkv_norm(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
                             uint32_t* dev_err, cudaStream_t st, const LoraLaunch* lora = nullptr,
                             const CUtensorMap* lora_maps = nullptr);
-// U = bf16(scale X A^T), before launch_qkv_norm.  x: [B, N_s, C] as
+bool qkv_uses_pairs(const QkvLaunch& a);
+cudaError_t launch_qkv_norm_e4m3(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
+                                 uint32_t* dev_err, cudaStream_t st);
+cudaError_t launch_qkv_norm_lora(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
+                                 uint32_t* dev_err, cudaStream_t st, const LoraLaunch* lora,
+                                 const CUtensorMap* lora_maps);
+// U = scale X A^T in two bf16 terms, before launch_qkv_norm.  x: [B, N_s, C] as
 // encode_bhnd_map maps; down: the adapters' [3 n, rank, C] as
 // encode_bhnd_map_rows(..., 16 ceil(rank / 16)) maps.
 cudaError_t launch_lora_down(const CUtensorMap (&x)[2], const CUtensorMap (&down)[2], const LoraLaunch& l,
@@ -194,7 +226,7 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t c
                      bool e4m3 = false);
 // TMA maps with (16, box_rows) boxes of bf16 and 32-byte swizzle over
 // [planes, rows, cols]; planes 0: a 2-D map over [rows, cols].
-bool encode_pair_map(CUtensorMap* map, const void* base, int planes, int64_t rows, int cols, int box_rows);
+bool encode_unit_map(CUtensorMap* map, const void* base, int planes, int64_t rows, int cols, int box_rows);
 
 // Encodes a 3-D TMA map over a [BH, N, d] bf16 tensor with a (64, 128, 1)
 // box and 128-byte swizzle.  Returns false if the driver rejects it.

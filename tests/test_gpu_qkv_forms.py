@@ -7,8 +7,8 @@ Tolerances, from the arithmetic:
   off by at most one ulp (2^-23) of the terms' summed magnitudes, a few fp32 products and the bias
   included (K + 8 roundings), then rounds once to bf16 (half a step, at most 2^-8 relative):
   |got - exact| <= (K + 8) 2^-23 mag + 2^-8 |exact|, mag the sum of the terms' magnitudes.
-* U = scale X A^T is rounded to bf16 between the two products of an adapter: another
-  sum_j 2^-8 |U_j B_oj|, and its own accumulation (C + 2) 2^-23 sum_j mag(U_j) |B_oj|.
+* U = scale X A^T is kept as two bf16 terms between the two products of an adapter (2^-8 of 2^-8): another
+  sum_j 2^-16 |U_j B_oj|, and its own accumulation (C + 2) 2^-23 sum_j mag(U_j) |B_oj|.
 * q_hat, k_hat, 1/rms: bit for bit (1/rms to 2^-21) what jattn_fwd_train keeps for the same q, k.
 """
 import numpy as np
@@ -94,6 +94,8 @@ FP8_CASES = [
     (33, 2, 1, 2, 64, 64, False),      # single tokens of many items
     (3, 12, 256, 77, 64, 768, True),
     (1, 16, 300, 77, 128, 2048, True),
+    (3, 1, 50, 0, 64, 64, True),       # one head, one stream: an item's rows follow the last one's on in memory
+    (5, 12, 1024, 77, 64, 192, True),  # more tiles than CTAs
 ]
 
 
@@ -172,6 +174,10 @@ LORA_CASES = [
     (3, 12, 256, 77, 64, 768, 16, 4, True),
     (2, 16, 2, 77, 128, 2048, 64, 2, True),
     (70, 5, 2, 3, 64, 320, 80, 9, True),
+    (3, 1, 50, 0, 64, 64, 16, 3, False),       # one head, one stream
+    (5, 12, 1000, 77, 64, 192, 24, 4, True),   # more tiles than CTAs, row tiles over two items
+    (3, 7, 1100, 33, 128, 72, 48, 2, True),
+    (600, 8, 3, 1, 64, 64, 8, 600, True),      # 86 items in a row tile of 256
 ]
 
 
@@ -219,7 +225,7 @@ def lora_exact(t, rank):
             mu = part(x.abs() @ down.abs().transpose(1, 2)) * sc[:, None, None, None].abs()
             y = y + join(u @ up)
             mag = mag + join(u.abs() @ up.abs())
-            off = join((2.0 ** -8 * u.abs() + (C + 2) * 2.0 ** -23 * mu) @ up.abs())
+            off = join((2.0 ** -16 * u.abs() + (C + 2) * 2.0 ** -23 * mu) @ up.abs())
         ys.append(y), mags.append(mag), offs.append(off)
     return torch.cat(ys, 1), torch.cat(mags, 1), torch.cat(offs, 1)
 
@@ -243,6 +249,24 @@ def test_qkv_norm_lora(ja, case):
     again = lora_call(ja, t, H)
     for a, b in zip(out[:3], again[:3]):
         assert torch.equal(a, b)
+
+
+@gpu
+@pytest.mark.parametrize("B,H,N_img,N_txt,d", [(3, 1, 50, 0, 64), (4, 1, 0, 40, 128), (9, 1, 700, 0, 64)])
+def test_qkv_norm_with_one_head_and_one_stream(ja, B, H, N_img, N_txt, d):
+    """The rows of an item then follow the last one's on in memory, and a warp's 32 rows may be of two items:
+    every row of q, k, v, q_hat and k_hat is written."""
+    C = 64
+    t = lora_inputs(B, H, N_img, N_txt, d, C, 8, 1, True, 33, streams=())
+    q, k, v = (torch.full((B, H, N_img + N_txt, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+               for _ in range(3))
+    saved = torch.full((ja.jattn_saved_bytes(B, H, N_img, N_txt, d),), 0xFF, dtype=torch.uint8, device="cuda")
+    ja.jattn_qkv_norm(t["x_img"] if N_img else None, t["w_img"], t["b_img"], t["x_txt"] if N_txt else None,
+                      t["w_txt"], t["b_txt"], t["gq"], t["gk"], B, H, N_img, N_txt, d, C, q, k, v, saved)
+    ok(ja)
+    y, mag, _ = lora_exact(t, 8)
+    check_y((q, k, v), y, (C + 8) * 2.0 ** -23 * mag, H, d)
+    check_norms(ja, q, k, v, saved, t["gq"], t["gk"], N_txt)
 
 
 @gpu
