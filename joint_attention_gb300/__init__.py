@@ -206,7 +206,9 @@ def _projected(x_img, x_txt, H: int, d: int):
     B, N_img, C = x_img.shape
     N_txt = x_txt.shape[1]
     dev = x_img.device
-    q, k, v = torch.empty((3, B, H, N_img + N_txt, d), dtype=torch.bfloat16, device=dev).unbind(0)
+    shape = (B, H, N_img + N_txt, d)
+    q = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    k, v = torch.empty_like(q), torch.empty_like(q)
     saved = torch.empty(jattn_saved_bytes(B, H, N_img, N_txt, d), dtype=torch.uint8, device=dev)
     return (q, k, v, saved), (B, H, N_img, N_txt, d, C)
 

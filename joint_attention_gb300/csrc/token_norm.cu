@@ -15,9 +15,13 @@
 //     dx = bf16(dh + r (u - n mean_c(u n))),   dg_c = sum_t dy n
 //
 // Row layout: a row's 16-byte chunks (8 values) are dealt round-robin to the
-// lanes that share it, one warp (C <= 1024) or one block, V chunks a lane,
-// kept in registers between the reduction and the output: every array is
-// read and written once.
+// lanes of the G warps that share it (1 for C <= 1024, 2 up to 2048, ...), at
+// most four chunks a lane, kept in registers between the reduction and the
+// output: every array is read and written once.  A block of 8 warps holds 8 / G
+// rows (16 warps for G = 16); warps of a row join their sums through shared
+// memory and a barrier of their own.  The arithmetic is in packed fp32 pairs:
+// with three reads and two writes of 16 bits a value the kernels are bound by
+// HBM only while they spend some 10 instructions on it.
 #include <cuda_bf16.h>
 
 #include "jattn_internal.h"
@@ -28,55 +32,65 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxFloor = 0x1p-80f;  // smallest row maximum a scale is made from
-constexpr int kRowThreads = 256;        // warp rows: 8 rows per block
-constexpr int kWarpRowMaxC = 1024;      // wider rows take a block each
-constexpr int kMaxBlockRow = 512;       // threads of a block row: 4 chunks a lane cover JATTN_MAX_WIDTH
-constexpr int kBwdParts = 304;          // blocks of the backward at most: two for each of 152 SMs
+constexpr int kMaxWarps = 16;         // sharing a row: 4 chunks a lane cover JATTN_MAX_WIDTH
+constexpr int kBwdParts = 304;        // blocks of the backward at most: two for each of 152 SMs
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
+// Warps of a block: 8 (8 / G rows), or one row's.
+constexpr int block_warps(int G) { return G > 8 ? G : 8; }
+
+// 8 bf16 values and packed fp32 pairs.
+struct F8 {
+  uint64_t p[4];
+};
+__device__ __forceinline__ F8 unpack8(const uint4& w) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  F8 f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f.p[i] = f2_make(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+  return f;
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint32_t pack2(uint64_t p) {
+  float a, b;
+  f2_split(p, a, b);
+  return pack_bf16x2(a, b);
+}
+__device__ __forceinline__ uint4 pack8(const F8& f) {
+  return make_uint4(pack2(f.p[0]), pack2(f.p[1]), pack2(f.p[2]), pack2(f.p[3]));
+}
+__device__ __forceinline__ F8 load8f(const float* g, int chunk) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(g) + 2 * chunk);
+  const float4 b = __ldg(reinterpret_cast<const float4*>(g) + 2 * chunk + 1);
+  return F8{{f2_make(a.x, a.y), f2_make(a.z, a.w), f2_make(b.x, b.y), f2_make(b.z, b.w)}};
 }
 // Four fp32 values as e4m3 bytes, lowest first (nearest even; beyond 448: 448; NaN stays NaN).
-__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t pack_e4m3x4(uint64_t ab, uint64_t cd) {
+  float a, b, c, d;
+  f2_split(ab, a, b);
+  f2_split(cd, c, d);
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
-__device__ __forceinline__ void load8f(const float* g, int chunk, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(g) + 2 * chunk);
-  const float4 b = __ldg(reinterpret_cast<const float4*>(g) + 2 * chunk + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
 
-// Reduction over the lanes that share a row: the warp, or the whole block
-// (red: one float per warp; the buffer is free again after the next call's
-// first barrier, so two buffers used in turn need no third barrier).
+// Reduction over the G warps that share a row (red: a float for each warp of
+// the block; free again after the next call's barrier, so two used in turn need
+// no second barrier).
 template <bool kMax>
 __device__ __forceinline__ float combine(float a, float b) {
   return kMax ? fmaxf(a, b) : a + b;
 }
-template <bool kBlock, bool kMax>
+template <int G, bool kMax>
 __device__ __forceinline__ float row_reduce(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = combine<kMax>(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if constexpr (kBlock) {
-    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if constexpr (G > 1) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, group = warp / G;
     if (lane == 0) red[warp] = v;
-    __syncthreads();
-    v = lane < warps ? red[lane] : 0.f;  // maxima are of magnitudes
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * G) : "memory");
+    v = red[group * G + (lane & (G - 1))];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v = combine<kMax>(v, __shfl_xor_sync(0xffffffffu, v, o));
-    v = __shfl_sync(0xffffffffu, v, 0);
+    for (int o = G / 2; o > 0; o >>= 1) v = combine<kMax>(v, __shfl_xor_sync(0xffffffffu, v, o));
   }
   return v;
 }
@@ -97,84 +111,87 @@ struct NormArgs {
 
 enum class RowOp { kNorm, kNormE4m3, kQuant };
 
-template <int V, bool kBlock, RowOp kOp>
-__global__ void __launch_bounds__(kBlock ? kMaxBlockRow : kRowThreads) token_rows_kernel(const NormArgs a) {
-  __shared__ float red[2][16];
+template <int V, int G, RowOp kOp>
+__global__ void __launch_bounds__(32 * block_warps(G)) token_rows_kernel(const NormArgs a) {
+  __shared__ float red[2][kMaxWarps];
   griddep_launch_dependents();
   griddep_wait();
-  const int lanes = kBlock ? blockDim.x : 32;
-  const int lane = kBlock ? threadIdx.x : threadIdx.x % 32;
-  const int64_t row = kBlock ? static_cast<int64_t>(blockIdx.x)
-                             : static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + threadIdx.x / 32;
-  if (row >= a.T) return;  // a whole warp (kBlock: never)
+  constexpr int kLanes = 32 * G, kRows = block_warps(G) / G;
+  const int lane = threadIdx.x % kLanes;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kLanes;
+  if (row >= a.T) return;  // all warps of a row
   const int64_t base = row * a.chunks;
   uint4 w[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = i * lanes + lane;
+    const int c = i * kLanes + lane;
     w[i] = c < a.chunks ? a.x[base + c] : make_uint4(0u, 0u, 0u, 0u);
   }
   if (kOp != RowOp::kQuant && a.res) {
+    uint4 e[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = i * lanes + lane;
-      if (c < a.chunks) {
-        float u[8], v[8];
-        unpack8(w[i], u);
-        unpack8(a.res[base + c], v);
+      const int c = i * kLanes + lane;
+      e[i] = c < a.chunks ? a.res[base + c] : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = __fadd_rn(u[j], v[j]);
-        w[i] = pack8(u);
-        a.h[base + c] = w[i];
-      }
+    for (int i = 0; i < V; ++i) {
+      const int c = i * kLanes + lane;
+      F8 u = unpack8(w[i]), v = unpack8(e[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u.p[j] = f2_add(u.p[j], v.p[j]);
+      w[i] = pack8(u);
+      if (c < a.chunks) a.h[base + c] = w[i];
     }
   }
   float r = 1.f;
   if constexpr (kOp != RowOp::kQuant) {
-    float ss = 0.f;
+    uint64_t s2 = 0;  // (0, 0)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float u[8];
-      unpack8(w[i], u);
+      const F8 u = unpack8(w[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(u[j], u[j], ss);
+      for (int j = 0; j < 4; ++j) s2 = f2_fma(u.p[j], u.p[j], s2);
     }
-    ss = row_reduce<kBlock, false>(ss, red[0]);
+    float s0, s1;
+    f2_split(s2, s0, s1);
+    const float ss = row_reduce<G, false>(s0 + s1, red[0]);
     r = __frsqrt_rn(fmaf(ss, a.inv_c, a.eps));
     if (lane == 0 && a.r) a.r[row] = r;
   }
-  auto z8 = [&](int i, int c, float (&z)[8]) {
-    unpack8(w[i], z);
+  const uint64_t r2 = f2_make(r, r);
+  auto z_of = [&](int i, int c) {  // (h r) g
+    F8 z = unpack8(w[i]);
     if constexpr (kOp != RowOp::kQuant) {
-      float g[8];
-      load8f(a.g, c, g);
+      const F8 g = load8f(a.g, c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = __fmul_rn(__fmul_rn(z[j], r), g[j]);
+      for (int j = 0; j < 4; ++j) z.p[j] = f2_mul(f2_mul(z.p[j], r2), g.p[j]);
     }
+    return z;
   };
   if constexpr (kOp == RowOp::kNorm) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = i * lanes + lane;
-      if (c < a.chunks) {
-        float z[8];
-        z8(i, c, z);
-        a.y[base + c] = pack8(z);
-      }
+      const int c = i * kLanes + lane;
+      if (c < a.chunks) a.y[base + c] = pack8(z_of(i, c));
     }
   } else {
+    F8 z[V];
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = i * lanes + lane;
+      const int c = i * kLanes + lane;
       if (c < a.chunks) {
-        float z[8];
-        z8(i, c, z);
+        z[i] = z_of(i, c);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(z[j]));
+        for (int j = 0; j < 4; ++j) {
+          float u, v;
+          f2_split(z[i].p[j], u, v);
+          m = fmax3(m, fabsf(u), fabsf(v));
+        }
       }
     }
-    m = row_reduce<kBlock, true>(m, red[1]);
+    m = row_reduce<G, true>(m, red[1]);
     // 448 z / m as 0.875 z over m / 512, which stays in range for every z and is exact for a bf16 z:
     // midpoints of e4m3 (common then) stay midpoints.  The product with the reciprocal and one residual
     // correction (Markstein, 1990) rounds as the quotient does.
@@ -182,18 +199,18 @@ __global__ void __launch_bounds__(kBlock ? kMaxBlockRow : kRowThreads) token_row
     if (lane == 0) a.s[row] = __fdiv_rn(m, kE4m3Max);
     m = __fmul_rn(m, 1.f / 512);
     const float inv = __frcp_rn(m);
+    const uint64_t inv2 = f2_make(inv, inv), neg_m2 = f2_make(-m, -m);
+    const uint64_t k2 = f2_make(kE4m3Max / 512, kE4m3Max / 512);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = i * lanes + lane;
+      const int c = i * kLanes + lane;
       if (c < a.chunks) {
-        float z[8];
-        z8(i, c, z);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float v = __fmul_rn(z[j], kE4m3Max / 512), q = __fmul_rn(v, inv);
-          z[j] = fmaf(fmaf(-q, m, v), inv, q);
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t v = f2_mul(z[i].p[j], k2), q = f2_mul(v, inv2);
+          z[i].p[j] = f2_fma(f2_fma(q, neg_m2, v), inv2, q);
         }
-        a.y8[base + c] = make_uint2(pack_e4m3x4(z[0], z[1], z[2], z[3]), pack_e4m3x4(z[4], z[5], z[6], z[7]));
+        a.y8[base + c] = make_uint2(pack_e4m3x4(z[i].p[0], z[i].p[1]), pack_e4m3x4(z[i].p[2], z[i].p[3]));
       }
     }
   }
@@ -213,138 +230,192 @@ struct NormBwdArgs {
 };
 
 // Rows in a fixed stride per block; each lane sums dy n of its columns over
-// the rows it meets, then the block's warps are added in order.
-template <int V, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? kMaxBlockRow : kRowThreads) token_norm_bwd_kernel(const NormBwdArgs a) {
-  extern __shared__ float sums[];  // warp rows: [warps][chunks * 8]
-  __shared__ float red[2][16];
+// the rows it meets, then the block's rows are added in order.  The three
+// operands of a row arrive by bulk copies in one of two buffers of its warps'
+// own, two rows ahead of the arithmetic: 17616 x 768 in 23.1 us with the rows
+// loaded to registers when they are needed, 26.4 us loaded one row ahead.
+constexpr int kBwdBufs = 2;
+
+template <int V, int G>
+__global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 1 : 2) token_norm_bwd_kernel(const NormBwdArgs a,
+                                                                                            uint32_t* dev_err) {
+  constexpr int kLanes = 32 * G, kRows = block_warps(G) / G;
+  extern __shared__ __align__(16) uint4 ring[];  // [row of the block][buffer][dy, h, dh][chunks]; then the sums
+  __shared__ float red[2][kMaxWarps];
+  __shared__ uint64_t full[kRows][kBwdBufs];
+  __shared__ int abort_flag;
+  volatile int* ab = &abort_flag;
+  const int lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
   griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < kRows * kBwdBufs; ++i) mbar_init(&full[0][0] + i, 1);
+    fence_mbar_init();
+  }
   griddep_wait();
-  const int lanes = kBlock ? blockDim.x : 32;
-  const int lane = kBlock ? threadIdx.x : threadIdx.x % 32;
-  const int rows_per_pass = kBlock ? 1 : kRowThreads / 32;
-  float acc[V][8];
+  __syncthreads();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows + slot;
+  const uint32_t bytes = a.chunks * 16;
+  auto buffer = [&](int buf) { return ring + static_cast<size_t>((slot * kBwdBufs + buf) * 3) * a.chunks; };
+  auto fetch = [&](int64_t row, int buf) {  // one lane of the row's warps
+    uint4* to = buffer(buf);
+    uint64_t* bar = &full[slot][buf];
+    const int64_t base = row * a.chunks;
+    mbar_arrive_expect_tx(bar, a.dh ? 3 * bytes : 2 * bytes);
+    bulk_load(to, a.dy + base, bytes, bar);
+    bulk_load(to + a.chunks, a.h + base, bytes, bar);
+    if (a.dh) bulk_load(to + 2 * a.chunks, a.dh + base, bytes, bar);
+  };
+  int fetched = 0;
+  if (lane == 0)
+    for (; fetched < kBwdBufs && first + fetched * step < a.T; ++fetched) fetch(first + fetched * step, fetched);
+  uint64_t acc[V][4];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-  int which = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_pass + (kBlock ? 0 : threadIdx.x / 32); row < a.T;
-       row += static_cast<int64_t>(gridDim.x) * rows_per_pass) {
-    const int64_t base = row * a.chunks;
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+  int it = 0;
+  float next_r = first < a.T ? a.r[first] : 0.f;
+  for (int64_t row = first; row < a.T; row += step, ++it) {
+    const int buf = it % kBwdBufs;
+    const float r = next_r;
+    next_r = row + step < a.T ? a.r[row + step] : 0.f;
+    // A wait that gave up is recorded; the loop goes on over what the buffer holds (without new copies), so
+    // that the warps of a row still meet at their barrier.
+    mbar_wait(&full[slot][buf], (it / kBwdBufs) & 1, ab, dev_err);
+    const uint4* from = buffer(buf);
     uint4 wy[V], wh[V], wd[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = i * lanes + lane;
+      const int c = i * kLanes + lane;
       const bool in = c < a.chunks;
-      wy[i] = in ? a.dy[base + c] : make_uint4(0u, 0u, 0u, 0u);
-      wh[i] = in ? a.h[base + c] : make_uint4(0u, 0u, 0u, 0u);
-      wd[i] = in && a.dh ? a.dh[base + c] : make_uint4(0u, 0u, 0u, 0u);
+      wy[i] = in ? from[c] : make_uint4(0u, 0u, 0u, 0u);
+      wh[i] = in ? from[a.chunks + c] : make_uint4(0u, 0u, 0u, 0u);
+      wd[i] = in && a.dh ? from[2 * a.chunks + c] : make_uint4(0u, 0u, 0u, 0u);
     }
-    const float r = a.r[row];
-    float un = 0.f;
+    const int64_t base = row * a.chunks;
+    const uint64_t r2 = f2_make(r, r);
+    F8 n[V], u[V];  // h r and g dy
+    uint64_t un2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = i * lanes + lane;
-      if (c < a.chunks) {
-        float y[8], h[8], g[8];
-        unpack8(wy[i], y);
-        unpack8(wh[i], h);
-        load8f(a.g, c, g);
+      const int c = i * kLanes + lane;
+      const bool in = c < a.chunks;
+      const F8 y = unpack8(wy[i]), g = load8f(a.g, in ? c : 0);
+      n[i] = unpack8(wh[i]);
+      u[i] = y;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float dn = y[j] * (h[j] * r);
-          acc[i][j] += dn;
-          un = fmaf(dn, g[j], un);
-        }
+      for (int j = 0; j < 4; ++j) {
+        n[i].p[j] = f2_mul(n[i].p[j], r2);
+        u[i].p[j] = f2_mul(y.p[j], g.p[j]);
+        acc[i][j] = f2_fma(y.p[j], n[i].p[j], acc[i][j]);
+        un2 = f2_fma(u[i].p[j], n[i].p[j], un2);
       }
     }
-    const float m = row_reduce<kBlock, false>(un, red[which]) * a.inv_c;
-    which ^= 1;
+    float u0, u1;
+    f2_split(un2, u0, u1);
+    const float m = -row_reduce<G, false>(u0 + u1, red[it & 1]) * a.inv_c;
+    // Every lane of the row has its values in registers (they are in the sum, or were read before it).
+    __syncwarp();
+    if (lane == 0 && row + kBwdBufs * step < a.T && !*ab) {
+      fetch(row + kBwdBufs * step, buf);
+      ++fetched;
+    }
+    const uint64_t m2 = f2_make(m, m);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = i * lanes + lane;
-      if (c < a.chunks) {
-        float y[8], h[8], g[8], d[8];
-        unpack8(wy[i], y);
-        unpack8(wh[i], h);
-        unpack8(wd[i], d);
-        load8f(a.g, c, g);
+      const int c = i * kLanes + lane;
+      F8 d = unpack8(wd[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = fmaf(r, fmaf(-(h[j] * r), m, y[j] * g[j]), d[j]);
-        a.dx[base + c] = pack8(d);
-      }
+      for (int j = 0; j < 4; ++j) d.p[j] = f2_fma(r2, f2_fma(n[i].p[j], m2, u[i].p[j]), d.p[j]);
+      if (c < a.chunks) a.dx[base + c] = pack8(d);
     }
+  }
+  if (lane == 0 && *ab) {  // the copies in flight land before the block exits
+    for (int i = fetched > kBwdBufs ? fetched - kBwdBufs : 0; i < fetched; ++i)
+      mbar_wait_drain(&full[slot][i % kBwdBufs], (i / kBwdBufs) & 1);
   }
   const int C = a.chunks * 8;
   float* out = a.part + static_cast<size_t>(blockIdx.x) * C;
-  if constexpr (kBlock) {
+  float* sums = reinterpret_cast<float*>(ring);  // [rows of the block][C]: every copy has landed and been read
+  if constexpr (kRows > 1) __syncthreads();
+  ulonglong2* mine = reinterpret_cast<ulonglong2*>(kRows > 1 ? sums + static_cast<size_t>(slot) * C : out);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = i * lanes + lane;
-      if (c < a.chunks) {
-        float4* o = reinterpret_cast<float4*>(out) + 2 * c;
-        o[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        o[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
-      }
+  for (int i = 0; i < V; ++i) {
+    const int c = i * kLanes + lane;
+    if (c < a.chunks) {
+      mine[2 * c] = make_ulonglong2(acc[i][0], acc[i][1]);
+      mine[2 * c + 1] = make_ulonglong2(acc[i][2], acc[i][3]);
     }
-  } else {
-    float4* mine = reinterpret_cast<float4*>(sums + static_cast<size_t>(threadIdx.x / 32) * C);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = i * lanes + lane;
-      if (c < a.chunks) {
-        mine[2 * c] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        mine[2 * c + 1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
-      }
-    }
+  }
+  if constexpr (kRows > 1) {
     __syncthreads();
-    for (int c = threadIdx.x; c < C; c += kRowThreads) {
+    for (int c = threadIdx.x; c < C; c += 32 * block_warps(G)) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kRowThreads / 32; ++w) s += sums[w * C + c];
+      for (int i = 0; i < kRows; ++i) s += sums[i * C + c];
       out[c] = s;
     }
   }
 }
 
-// dg = the sum of the blocks' partial sums, in a fixed order: 32 columns a
-// block, 8 threads a column.
+// dg = the sum of the blocks' partial sums, in a fixed order: 8 columns (a
+// 32-byte sector of each partial) a block, 32 threads a column.
 __global__ void __launch_bounds__(256) dg_sum_kernel(const float* part, int parts, int C, float* dg) {
-  __shared__ float sums[8][33];
+  __shared__ float sums[32][9];
   griddep_launch_dependents();
   griddep_wait();
-  const int col = threadIdx.x % 32, grp = threadIdx.x / 32;
-  const int c = blockIdx.x * 32 + col;
-  float s = 0.f;
-  if (c < C)
-    for (int p = grp; p < parts; p += 8) s += part[static_cast<size_t>(p) * C + c];
+  const int col = threadIdx.x % 8, grp = threadIdx.x / 8;
+  const float* from = part + blockIdx.x * 8 + col;  // C is a multiple of 8
+  float v[(kBwdParts + 31) / 32];  // all on their way at once
+#pragma unroll
+  for (int i = 0; i < (kBwdParts + 31) / 32; ++i) {
+    const int p = grp + 32 * i;
+    v[i] = p < parts ? from[static_cast<size_t>(p) * C] : 0.f;
+  }
+  float s = v[0];
+#pragma unroll
+  for (int i = 1; i < (kBwdParts + 31) / 32; ++i) s += v[i];
   sums[grp][col] = s;
   __syncthreads();
-  if (grp == 0 && c < C) {
+  if (grp == 0) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sums[i][col];
-    dg[c] = s;
+    for (int i = 1; i < 32; ++i) s += sums[i][col];
+    dg[blockIdx.x * 8 + col] = s;
   }
 }
 
-int block_row_threads(int chunks, int per_lane) { return ((chunks + per_lane - 1) / per_lane + 31) / 32 * 32; }
+// Calls f(V, G) with the row layout of a width: as few warps as hold it at
+// four chunks a lane.
+template <int kV, int kG>
+struct Layout {
+  static constexpr int V = kV, G = kG;
+};
+template <typename F>
+cudaError_t with_layout(int chunks, F f) {
+  if (chunks <= 32) return f(Layout<1, 1>());
+  if (chunks <= 64) return f(Layout<2, 1>());
+  if (chunks <= 96) return f(Layout<3, 1>());
+  if (chunks <= 128) return f(Layout<4, 1>());
+  if (chunks <= 192) return f(Layout<3, 2>());
+  if (chunks <= 256) return f(Layout<4, 2>());
+  if (chunks <= 384) return f(Layout<3, 4>());
+  if (chunks <= 512) return f(Layout<4, 4>());
+  if (chunks <= 768) return f(Layout<3, 8>());
+  if (chunks <= 1024) return f(Layout<4, 8>());
+  if (chunks <= 1536) return f(Layout<3, 16>());
+  return f(Layout<4, 16>());
+}
 
 template <RowOp kOp>
 cudaError_t launch_rows(const NormArgs& a, cudaStream_t st) {
-  if (a.chunks * 8 <= kWarpRowMaxC) {
-    constexpr int kRows = kRowThreads / 32;
-    const int64_t blocks = (a.T + kRows - 1) / kRows;
-    const dim3 grid(static_cast<unsigned>(blocks));
-    switch ((a.chunks + 31) / 32) {
-      case 1: return launch_pdl(token_rows_kernel<1, false, kOp>, grid, dim3(kRowThreads), 0, st, a);
-      case 2: return launch_pdl(token_rows_kernel<2, false, kOp>, grid, dim3(kRowThreads), 0, st, a);
-      case 3: return launch_pdl(token_rows_kernel<3, false, kOp>, grid, dim3(kRowThreads), 0, st, a);
-      default: return launch_pdl(token_rows_kernel<4, false, kOp>, grid, dim3(kRowThreads), 0, st, a);
-    }
-  }
-  return launch_pdl(token_rows_kernel<4, true, kOp>, dim3(static_cast<unsigned>(a.T)),
-                    dim3(block_row_threads(a.chunks, 4)), 0, st, a);
+  return with_layout(a.chunks, [&](auto l) {
+    using L = decltype(l);
+    constexpr int kWarps = block_warps(L::G), kRows = kWarps / L::G;
+    return launch_pdl(token_rows_kernel<L::V, L::G, kOp>, dim3(static_cast<unsigned>((a.T + kRows - 1) / kRows)),
+                      dim3(32 * kWarps), 0, st, a);
+  });
 }
 
 }  // namespace
@@ -368,14 +439,18 @@ cudaError_t launch_add_norm(const TokenNorm& t, cudaStream_t st) {
 }
 
 int add_norm_bwd_parts(int T, int C) {
-  const int64_t rows = C <= kWarpRowMaxC ? kRowThreads / 32 : 1;
-  const int64_t blocks = (T + rows - 1) / rows;
+  int rows = 1;
+  with_layout(C / 8, [&](auto l) {
+    rows = block_warps(decltype(l)::G) / decltype(l)::G;
+    return cudaSuccess;
+  });
+  const int64_t blocks = (static_cast<int64_t>(T) + rows - 1) / rows;
   return static_cast<int>(blocks < kBwdParts ? blocks : kBwdParts);
 }
 
 cudaError_t launch_add_norm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const float* r,
                                 const float* g, int T, int C, uint16_t* dx, float* part, int parts,
-                                cudaStream_t st) {
+                                uint32_t* dev_err, cudaStream_t st) {
   NormBwdArgs a;
   a.dy = reinterpret_cast<const uint4*>(dy);
   a.dh = reinterpret_cast<const uint4*>(dh);
@@ -387,21 +462,21 @@ cudaError_t launch_add_norm_bwd(const uint16_t* dy, const uint16_t* dh, const ui
   a.inv_c = 1.f / static_cast<float>(C);
   a.dx = reinterpret_cast<uint4*>(dx);
   a.part = part;
-  const dim3 grid(static_cast<unsigned>(parts));
-  if (C <= kWarpRowMaxC) {
-    const size_t smem = static_cast<size_t>(kRowThreads / 32) * C * 4;  // at most 32 KB
-    switch ((a.chunks + 31) / 32) {
-      case 1: return launch_pdl(token_norm_bwd_kernel<1, false>, grid, dim3(kRowThreads), smem, st, a);
-      case 2: return launch_pdl(token_norm_bwd_kernel<2, false>, grid, dim3(kRowThreads), smem, st, a);
-      case 3: return launch_pdl(token_norm_bwd_kernel<3, false>, grid, dim3(kRowThreads), smem, st, a);
-      default: return launch_pdl(token_norm_bwd_kernel<4, false>, grid, dim3(kRowThreads), smem, st, a);
-    }
-  }
-  return launch_pdl(token_norm_bwd_kernel<4, true>, grid, dim3(block_row_threads(a.chunks, 4)), 0, st, a);
+  return with_layout(a.chunks, [&](auto l) {
+    using L = decltype(l);
+    constexpr int kWarps = block_warps(L::G), kRows = kWarps / L::G;
+    // 12 bytes a value for the rows of a block: 96 KB at most (two blocks on an SM), 192 KB for G = 16.
+    const size_t smem = static_cast<size_t>(kRows) * kBwdBufs * 3 * C * 2;
+    auto kernel = token_norm_bwd_kernel<L::V, L::G>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(parts)), dim3(32 * kWarps), smem, st, a, dev_err);
+  });
 }
 
 cudaError_t launch_dg_sum(const float* part, int parts, int C, float* dg, cudaStream_t st) {
-  return launch_pdl(dg_sum_kernel, dim3(static_cast<unsigned>((C + 31) / 32)), dim3(256), 0, st, part, parts, C, dg);
+  return launch_pdl(dg_sum_kernel, dim3(static_cast<unsigned>(C / 8)), dim3(256), 0, st, part, parts, C, dg);
 }
 
 }  // namespace jattn
