@@ -527,15 +527,14 @@ def jattn_qkv_norm_fp8(x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt
     e = B * H * (N_img + N_txt) * d
     bf, f32, f8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
     yc = 3 * H * d
-    args = []
-    for n, N_s, x, sx, w, sw, b in (("img", N_img, x_img, sx_img, w_img, sw_img, b_img),
-                                    ("txt", N_txt, x_txt, sx_txt, w_txt, sw_txt, b_txt)):
-        args += [_ptr(x, "x_" + n, f8, B * N_s * C), _ptr(sx, "sx_" + n, f32, B * N_s),
-                 _ptr(w, "w_" + n, f8, yc * C if N_s else None), _ptr(sw, "sw_" + n, f32, yc if N_s else None),
-                 _ptr(b, "b_" + n, f32, yc)]
-    rc = load_library().jattn_qkv_norm_fp8(*args, _ptr(gq, "gq", f32, d), _ptr(gk, "gk", f32, d), B, H, N_img,
-                                           N_txt, d, C, _ptr(q, "q", bf, e), _ptr(k, "k", bf, e),
-                                           _ptr(v, "v", bf, e), _saved(saved, B, H, N_img, N_txt, d), _stream(stream))
+    rc = load_library().jattn_qkv_norm_fp8(
+        _ptr(x_img, "x_img", f8, B * N_img * C), _ptr(sx_img, "sx_img", f32, B * N_img),
+        _ptr(w_img, "w_img", f8, yc * C if N_img else None), _ptr(sw_img, "sw_img", f32, yc if N_img else None),
+        _ptr(b_img, "b_img", f32, yc), _ptr(x_txt, "x_txt", f8, B * N_txt * C),
+        _ptr(sx_txt, "sx_txt", f32, B * N_txt), _ptr(w_txt, "w_txt", f8, yc * C if N_txt else None),
+        _ptr(sw_txt, "sw_txt", f32, yc if N_txt else None), _ptr(b_txt, "b_txt", f32, yc), _ptr(gq, "gq", f32, d),
+        _ptr(gk, "gk", f32, d), B, H, N_img, N_txt, d, C, _ptr(q, "q", bf, e), _ptr(k, "k", bf, e),
+        _ptr(v, "v", bf, e), _saved(saved, B, H, N_img, N_txt, d), _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_qkv_norm_fp8")
     return rc
@@ -557,16 +556,15 @@ def jattn_qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_i
     e = B * H * (N_img + N_txt) * d
     bf, f32 = torch.bfloat16, torch.float32
     yc = 3 * H * d
-    args = []
-    for n, N_s, x, w, b in (("img", N_img, x_img, w_img, b_img), ("txt", N_txt, x_txt, w_txt, b_txt)):
-        args += [_ptr(x, "x_" + n, bf, B * N_s * C), _ptr(w, "w_" + n, bf, yc * C if N_s else None),
-                 _ptr(b, "b_" + n, f32, yc)]
-    args += [_ptr(gq, "gq", f32, d), _ptr(gk, "gk", f32, d)]
-    for n, down, up in (("img", down_img, up_img), ("txt", down_txt, up_txt)):
-        args += [_ptr(down, "down_" + n, bf, n_adapters * 3 * rank * C), _ptr(up, "up_" + n, bf, n_adapters * yc * rank)]
     rc = load_library().jattn_qkv_norm_lora(
-        *args, _ptr(scale, "scale", f32, n_adapters), _ptr(index, "index", torch.int32, B), n_adapters, rank, B, H,
-        N_img, N_txt, d, C, _ptr(q, "q", bf, e), _ptr(k, "k", bf, e), _ptr(v, "v", bf, e), _saved(saved, B, H, N_img, N_txt, d),
+        _ptr(x_img, "x_img", bf, B * N_img * C), _ptr(w_img, "w_img", bf, yc * C if N_img else None),
+        _ptr(b_img, "b_img", f32, yc), _ptr(x_txt, "x_txt", bf, B * N_txt * C),
+        _ptr(w_txt, "w_txt", bf, yc * C if N_txt else None), _ptr(b_txt, "b_txt", f32, yc), _ptr(gq, "gq", f32, d),
+        _ptr(gk, "gk", f32, d), _ptr(down_img, "down_img", bf, n_adapters * 3 * rank * C),
+        _ptr(up_img, "up_img", bf, n_adapters * yc * rank), _ptr(down_txt, "down_txt", bf, n_adapters * 3 * rank * C),
+        _ptr(up_txt, "up_txt", bf, n_adapters * yc * rank), _ptr(scale, "scale", f32, n_adapters),
+        _ptr(index, "index", torch.int32, B), n_adapters, rank, B, H, N_img, N_txt, d, C, _ptr(q, "q", bf, e),
+        _ptr(k, "k", bf, e), _ptr(v, "v", bf, e), _saved(saved, B, H, N_img, N_txt, d),
         _work_ptr(work, jattn_qkv_norm_lora_bytes, B, H, N_img, N_txt, d, rank), _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_qkv_norm_lora")

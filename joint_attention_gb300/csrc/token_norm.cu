@@ -159,7 +159,12 @@ __global__ void __launch_bounds__(32 * block_warps(G)) token_rows_kernel(const N
     r = __frsqrt_rn(fmaf(ss, a.inv_c, a.eps));
     if (lane == 0 && a.r) a.r[row] = r;
   }
-  const uint64_t r2 = f2_make(r, r);
+  // 8 bits: r cancels in 448 z / m, so that z and m need it only to its power of two, whose product with h
+  // is exact; s gets the rest of it, rho in [1, 2).
+  const float pow2 = __uint_as_float(__float_as_uint(r) & 0x7F800000u);
+  const float rho = kOp == RowOp::kNormE4m3 ? __uint_as_float((__float_as_uint(r) & 0x007FFFFFu) | 0x3F800000u) : 1.f;
+  const float rz = kOp == RowOp::kNormE4m3 ? pow2 : r;
+  const uint64_t r2 = f2_make(rz, rz);
   auto z_of = [&](int i, int c) {  // (h r) g
     F8 z = unpack8(w[i]);
     if constexpr (kOp != RowOp::kQuant) {
@@ -195,9 +200,9 @@ __global__ void __launch_bounds__(32 * block_warps(G)) token_rows_kernel(const N
     // 448 z / m as 0.875 z over m / 512, which stays in range for every z and is exact for a bf16 z:
     // midpoints of e4m3 (common then) stay midpoints.  The product with the reciprocal and one residual
     // correction (Markstein, 1990) rounds as the quotient does.
-    m = fmaxf(m, kAmaxFloor);
-    if (lane == 0) a.s[row] = __fdiv_rn(m, kE4m3Max);
-    m = __fmul_rn(m, 1.f / 512);
+    const float mz = __fmul_rn(m, rho);
+    if (lane == 0) a.s[row] = __fdiv_rn(fmaxf(mz, kAmaxFloor), kE4m3Max);
+    m = __fmul_rn(mz < kAmaxFloor ? __fdiv_rn(kAmaxFloor, rho) : m, 1.f / 512);
     const float inv = __frcp_rn(m);
     const uint64_t inv2 = f2_make(inv, inv), neg_m2 = f2_make(-m, -m);
     const uint64_t k2 = f2_make(kE4m3Max / 512, kE4m3Max / 512);
