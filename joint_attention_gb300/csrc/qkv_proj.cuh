@@ -331,20 +331,47 @@ struct QkvLoraMaps {
   CUtensorMap u[2], up[2];
 };
 
-// The next run of consecutive batch items with one adapter among rows m0 ..
-// m1 - 1 of a stream, from item b on: the adapter and the rows lo .. hi - 1
-// of the tile.  Items without an adapter are passed over.
-__device__ __forceinline__ bool next_run(const QkvParams& p, int N_s, int m0, int m1, int& b, int& adapter, int& lo,
-                                         int& hi) {
-  while (b * N_s < m1) {
-    adapter = __ldg(p.index + b);
-    lo = max(b * N_s, m0) - m0;
-    do ++b;
-    while (b * N_s < m1 && __ldg(p.index + b) == adapter);
-    hi = min(b * N_s, m1) - m0;
-    if (adapter >= 0 && adapter < p.n_adapters) return true;
+// The runs of consecutive batch items with one adapter among rows m0 .. m1 - 1
+// of a stream: next() gives the next one's adapter and its rows lo .. hi - 1 of
+// the tile, passing over items without an adapter.  Two items' indexes are on
+// their way ahead of the one that is looked at.
+struct Runs {
+  const int* index;
+  int n_adapters, N_s, m0, m1;
+  int b, row;      // the next item, and its first row
+  int here, then;  // its index, and the next one's
+  int adapter, lo, hi;
+  __device__ __forceinline__ Runs(const QkvParams& p, int N_s_, int m0_, int m1_)
+      : index(p.index), n_adapters(p.n_adapters), N_s(N_s_), m0(m0_), m1(m1_) {
+    b = m0 / N_s;
+    row = b * N_s;
+    here = __ldg(index + b);
+    then = row + N_s < m1 ? __ldg(index + b + 1) : 0;
   }
-  return false;
+  __device__ __forceinline__ void step() {
+    ++b;
+    row += N_s;
+    here = then;
+    if (row + N_s < m1) then = __ldg(index + b + 1);  // row + N_s < m1 <= B N_s: item b + 1 exists
+  }
+  __device__ __forceinline__ bool next() {
+    while (row < m1) {
+      adapter = here;
+      lo = max(row, m0) - m0;
+      do step();
+      while (row < m1 && here == adapter);
+      hi = min(row, m1) - m0;
+      if (adapter >= 0 && adapter < n_adapters) return true;
+    }
+    return false;
+  }
+};
+// Rows lo .. hi - 1 of words of 32 rows: the bits of word w.
+__device__ __forceinline__ uint32_t rows_of_word(int lo, int hi, int w) {
+  const int from = max(lo - 32 * w, 0), to = min(hi - 32 * w, 32);
+  uint32_t m;
+  asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(m) : "r"(from), "r"(max(to - from, 0)));
+  return m;
 }
 // The q, k, v parts that columns n0 .. n0 + cols - 1 meet.
 __device__ __forceinline__ void parts_of(int n0, int cols, int hd, int& first, int& last) {
@@ -701,8 +728,8 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
           for (int part = p0; ok && part <= p1; ++part) {
             const int c0 = max(part * hd, n0), width = min((part + 1) * hd, n0 + kCols) - c0;
             for (int kc = 0; ok && kc < p.rank_units; ++kc) {
-              int b = m0 / N_s, adapter, lo, hi;
-              bool more = next_run(p, N_s, m0, m1, b, adapter, lo, hi);
+              Runs runs(p, N_s, m0, m1);
+              bool more = runs.next();
               while (ok && more) {
                 if (used + 2 * Cfg::kUnitA + Cfg::kUnitB > Cfg::kStageBytes) close();
                 const int s = it % kStages;
@@ -720,9 +747,9 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
                 used += 2 * Cfg::kUnitA;
                 do {
                   if (rank == 0) mbar_expect_tx(&bars.full[s], kCtas * Cfg::kUnitB);
-                  tma_load_3d_to<kPair>(st + used, mup, full, kc * 16, c0 + rank * (width / kCtas), adapter);
+                  tma_load_3d_to<kPair>(st + used, mup, full, kc * 16, c0 + rank * (width / kCtas), runs.adapter);
                   used += Cfg::kUnitB;
-                  more = next_run(p, N_s, m0, m1, b, adapter, lo, hi);
+                  more = runs.next();
                 } while (more && used + Cfg::kUnitB <= Cfg::kStageBytes);
               }
             }
@@ -783,8 +810,8 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
               const int c0 = max(part * hd, n0) - n0, c1 = min((part + 1) * hd, n0 + kCols) - n0;
               const uint32_t desc = idesc_bf16_f32(kRows, c1 - c0, false, false);
               for (int kc = 0; ok && kc < p.rank_units; ++kc) {
-                int b = m0 / N_s, adapter, lo, hi;
-                bool more = next_run(p, N_s, m0, m1, b, adapter, lo, hi);
+                Runs runs(p, N_s, m0, m1);
+                bool more = runs.next();
                 while (ok && more) {
                   if (used + 2 * Cfg::kUnitA + Cfg::kUnitB > Cfg::kStageBytes) close();
                   const int s = it % kStages;
@@ -799,17 +826,12 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
                   do {
                     uint32_t off[4 * kCtas];  // the lanes (rows) that the run does not hold
 #pragma unroll
-                    for (int w = 0; w < 4 * kCtas; ++w) {
-                      const int l = min(max(lo - 32 * w, 0), 32), h = min(max(hi - 32 * w, 0), 32);
-                      const uint32_t below = l >= 32 ? 0xFFFFFFFFu : (1u << l) - 1u;
-                      const uint32_t upto = h >= 32 ? 0xFFFFFFFFu : (1u << h) - 1u;
-                      off[w] = ~(upto & ~below);
-                    }
+                    for (int w = 0; w < 4 * kCtas; ++w) off[w] = ~rows_of_word(runs.lo, runs.hi, w);
                     const uint64_t up = sdesc_sw32_kmajor(st + used, 256);
                     umma_bf16_ss_lanes(acc + c0, u_hi, up, desc, off, 1u);
                     umma_bf16_ss_lanes(acc + c0, u_lo, up, desc, off, 1u);
                     used += Cfg::kUnitB;
-                    more = next_run(p, N_s, m0, m1, b, adapter, lo, hi);
+                    more = runs.next();
                   } while (more && used + Cfg::kUnitB <= Cfg::kStageBytes);
                 }
               }
@@ -913,22 +935,19 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
   }
 }
 
-// How many pairs of a kernel the current device runs at once (asked once per
-// device and kernel): not every SM finds a free neighbour, and a pair beyond
-// that number would start when the others have finished.
+// How many pairs of a kernel the current device runs at once (a pair beyond
+// that number would start when the others have finished), after a check of the
+// registers its setmaxnreg split was sized for; asked once per device and
+// kernel (`known`: the kernel's own, by device, 0 where not asked yet).
 template <typename K>
-cudaError_t resident_pairs(K kernel, int threads, int smem, int regs, int* pairs) {
-  constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices];  // one array per kernel type: the kernel is checked too
-  static std::atomic<K> of[kDevices];
+cudaError_t resident_pairs(K kernel, int threads, int smem, int regs, std::atomic<int>* known, int devices,
+                           int* pairs) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const bool slot = dev >= 0 && dev < kDevices;
-  if (slot && of[dev].load(std::memory_order_acquire) == kernel) {
-    *pairs = known[dev].load(std::memory_order_relaxed);
-    return cudaSuccess;
-  }
+  const bool slot = dev >= 0 && dev < devices;
+  *pairs = slot ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*pairs > 0) return cudaSuccess;
   cudaFuncAttributes fa;
   e = cudaFuncGetAttributes(&fa, kernel);
   if (e != cudaSuccess) return e;
@@ -947,10 +966,7 @@ cudaError_t resident_pairs(K kernel, int threads, int smem, int regs, int* pairs
   e = cudaOccupancyMaxActiveClusters(pairs, kernel, &cfg);
   if (e != cudaSuccess) return e;
   if (*pairs < 1) return cudaErrorInvalidConfiguration;
-  if (slot) {
-    known[dev].store(*pairs, std::memory_order_relaxed);
-    of[dev].store(kernel, std::memory_order_release);
-  }
+  if (slot) known[dev].store(*pairs, std::memory_order_relaxed);
   return cudaSuccess;
 }
 
@@ -965,8 +981,9 @@ cudaError_t launch_qkv_kernel(const CUtensorMap (&maps)[4], const QkvOutMaps& om
   const int sms = device_sm_count();
   int groups = sms > Cfg::kCtas ? sms / Cfg::kCtas : 1;
   if constexpr (kPair) {
+    static std::atomic<int> known[64];
     int fit = 0;
-    e = resident_pairs(kernel, Cfg::kThreads, Cfg::kDynSmem, QkvRegs<D>::kLaunch, &fit);
+    e = resident_pairs(kernel, Cfg::kThreads, Cfg::kDynSmem, QkvRegs<D>::kLaunch, known, 64, &fit);
     if (e != cudaSuccess) return e;
     if (fit < groups) groups = fit;
   }
