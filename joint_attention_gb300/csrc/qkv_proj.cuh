@@ -76,6 +76,7 @@
 #include "jattn_internal.h"
 #include "sm103_ptx.cuh"
 #include "bf16_round.cuh"
+#include "fastdiv.cuh"
 
 namespace jattn {
 namespace {
@@ -313,6 +314,7 @@ struct QkvParams {
   QkvStream s[2];     // 0: image stream, 1: caption stream
   int H, C, N;        // heads, model width (K of the product), joint sequence length
   int n_tiles;        // column tiles
+  DivU31 by_tiles;    // division by n_tiles
   int tiles;          // all tiles of both streams
   uint16_t* out[3];   // q, k, v: [B, H, N, d]
   uint16_t* hat[2];   // q_hat, k_hat
@@ -570,7 +572,7 @@ __device__ __forceinline__ void qkv_emit(uint32_t taddr, uint64_t* acc_empty, in
   int which[kHeads], head[kHeads];  // 0 q, 1 k, 2 v (3: past the last head)
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
-    which[i] = (col0 + i * D) / hd;
+    which[i] = (col0 + i * D >= hd) + (col0 + i * D >= 2 * hd) + (col0 + i * D >= 3 * hd);
     head[i] = (col0 + i * D - which[i] * hd) / D;
   }
   auto part = [&](int i) { return D == 64 ? which[i < kHeads ? i : 0] : which[0]; };  // of half i
@@ -862,7 +864,7 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
     // without a bias); kE4m3: their scales, and those of its rows.
     auto fetch = [&](int t, int buf) {
       const QkvStream S = stream_of(p, t >= p.s[1].tile0 ? 1 : 0);
-      const int tl = t - S.tile0, mt = tl / p.n_tiles, col = (tl - mt * p.n_tiles) * kCols + wcol + lane * 4;
+      const int tl = t - S.tile0, mt = static_cast<int>(p.by_tiles.div(tl)), col = (tl - mt * p.n_tiles) * kCols + wcol + lane * 4;
       if (lane * 4 < Cfg::kWarpCols) {
         const uint32_t to = bias_w + buf * Cfg::kBiasBytes + lane * 16;
         if (S.bias && col < hd3)
@@ -893,7 +895,7 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
       const int abuf = lt & 1;
       const QkvStream S = stream_of(p, t >= p.s[1].tile0 ? 1 : 0);
       const int tl = t - S.tile0;
-      const int mt = tl / p.n_tiles, nt = tl - mt * p.n_tiles;
+      const int mt = static_cast<int>(p.by_tiles.div(tl)), nt = tl - mt * p.n_tiles;
       const int col0 = nt * kCols + wcol;  // the warp's first column in Y
       const int m = mt * kRows + rank * kBM + lg * 32 + lane;
       const bool live = m < S.M;
@@ -1014,6 +1016,7 @@ cudaError_t launch_qkv_form(const CUtensorMap (&maps)[4], const CUtensorMap (&ou
   p.C = a.C;
   p.N = a.N;
   p.n_tiles = (3 * a.H * a.d + cols - 1) / cols;
+  p.by_tiles = make_div_u31(p.n_tiles);
   int tile0 = 0;
   for (int i = 0; i < 2; ++i) {
     p.s[i].M = a.M[i];
