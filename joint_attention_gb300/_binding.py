@@ -8,6 +8,7 @@ library is missing the import of a call fails loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -293,6 +294,7 @@ def jattn_bwd_varlen(q, k, v, gq, gk, out, lse, dout, dq, dk, dv, dgq, dgk, cu_s
     return rc
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone, and a library call of 0.8 us
 def jattn_saved_bytes(B: int, H: int, N_img: int, N_txt: int, d: int) -> int:
     """C ABI jattn_saved_bytes: size of the activation buffer of jattn_fwd_train / jattn_bwd_train."""
     return int(load_library().jattn_saved_bytes(B, H, N_img, N_txt, d))
@@ -477,6 +479,7 @@ def jattn_quant_rows(x, T: int, C: int, x8, s, stream=None, check: bool = True) 
     return rc
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone, and a library call of 0.8 us
 def jattn_add_norm_bwd_bytes(T: int, C: int) -> int:
     """C ABI jattn_add_norm_bwd_bytes: size of the work buffer of jattn_add_norm_bwd (0: it rejects the sizes)."""
     return int(load_library().jattn_add_norm_bwd_bytes(T, C))
@@ -540,6 +543,7 @@ def jattn_qkv_norm_fp8(x_img, sx_img, w_img, sw_img, b_img, x_txt, sx_txt, w_txt
     return rc
 
 
+@functools.lru_cache(maxsize=1024)
 def jattn_qkv_norm_lora_bytes(B: int, H: int, N_img: int, N_txt: int, d: int, rank: int) -> int:
     """C ABI jattn_qkv_norm_lora_bytes: size of the work buffer of jattn_qkv_norm_lora (0: it rejects the sizes)."""
     return int(load_library().jattn_qkv_norm_lora_bytes(B, H, N_img, N_txt, d, rank))

@@ -1025,14 +1025,12 @@ extern "C" int jattn_add_norm_bwd(const jattn_bf16* dy, const jattn_bf16* dh, co
   const Range outs[] = {range_of(dx, tb), range_of(dg, gb), range_of(work, jattn_add_norm_bwd_bytes(T, C))};
   if (any_alias(ins, outs, outs[0], ins[1])) return JATTN_ERR_ALIAS;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  uint32_t* err = dev_err_ptr();
-  if (!err) return fail(JATTN_ERR_CUDA, "device error word", cudaGetLastError());
   float* part = static_cast<float*>(work);
   const int parts = add_norm_bwd_parts(T, C);
   cudaError_t ce;
   {
     Timed t(JATTN_KERNEL_ADD_NORM_BWD, st);
-    ce = launch_add_norm_bwd(dy, dh, h, r, g, T, C, dx, part, parts, err, st);
+    ce = launch_add_norm_bwd(dy, dh, h, r, g, T, C, dx, part, parts, st);
   }
   if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "add_norm_bwd launch", ce);
   {

@@ -132,7 +132,7 @@ cudaError_t launch_add_norm(const TokenNorm& t, cudaStream_t st);
 int add_norm_bwd_parts(int T, int C);
 cudaError_t launch_add_norm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const float* r,
                                 const float* g, int T, int C, uint16_t* dx, float* part, int parts,
-                                uint32_t* dev_err, cudaStream_t st);
+                                cudaStream_t st);
 cudaError_t launch_dg_sum(const float* part, int parts, int C, float* dg, cudaStream_t st);
 
 // --- tensor-core attention kernels ------------------------------------------

@@ -11,10 +11,15 @@ namespace {
 // operand, N = 3 * 16 rank_units columns (a rank that is not a multiple of 16
 // reads the TMA's zero fill).  Items without an adapter write nothing (the
 // projection reads nothing of theirs).  U is kept as two bf16 terms, the value
-// rounded and the rest rounded (2^-17 of it is lost), so that Y has one
+// rounded and the rest rounded (at most 2^-16 of it is lost), so that Y has one
 // rounding: with one term q_hat's error against 64 bits was 1.2 to 1.35 times
-// that of fp32 arithmetic.  Warps 0-3 read the accumulator out (a row a thread), warp 4 loads, warp 5
-// issues.
+// that of fp32 arithmetic.  Warps 0-3 read the accumulator out (a row a
+// thread), warp 4 loads, warp 5 issues.
+//
+// What bounds it: its own start and end.  At 512 px (16 items, rank 16) it reads
+// 27 MB in 13 us under ncu, with 4 stages of the ring as with 12; the projection
+// starts behind its first wait, so that the call takes 72 us where the
+// projection alone takes 57 and, with no item having an adapter, 64.
 constexpr int kDownThreads = 192;
 constexpr int kDownK = 64;
 constexpr int kDownMaxStages = 6;

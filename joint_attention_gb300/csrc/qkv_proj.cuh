@@ -22,11 +22,10 @@
 //   kPair   256 token rows x 256 output columns by a pair of CTAs
 //           (cta_group::2): each CTA keeps 128 rows, all 256 columns of its
 //           accumulator in its TMEM, and half of the weight tile in its shared
-//           memory.  One CTA alone would load and read the whole weight tile:
-//           96 KB of shared-memory traffic a K step and 128 x 256 products
-//           instead of 64 KB, and shared memory (with the epilogue's staging)
-//           is what bounds this kernel: 512 px from e4m3 rows 46.6 us so
-//           (128 x 256 tiles), see kPair's own times at qkv_uses_pairs.
+//           memory.  One CTA alone with 256 columns would load and read the
+//           whole weight tile: 96 KB of shared-memory traffic a K step and 128
+//           x 256 products instead of 64 KB (the products alone, 768 px from
+//           e4m3 rows: 71.9 us so, 66.2 us by pairs).
 //   !kPair  128 token rows x one head's columns by one CTA: for few rows,
 //           whose tiles are then four (two) times as many.
 // K in steps of 128 bytes a row; persistent, the image stream's tiles then the
@@ -47,6 +46,14 @@
 //               store, or four rows per store instruction).
 // Heads past 3 H in the last column tile, and token rows past the stream's
 // end in its last row tile, read the TMA's zero fill and are not stored.
+//
+// What bounds it (512 px, C = 768, 12 heads of 64; 57 us from bf16, 39 us from
+// e4m3): from bf16 a third of the issuer's time goes to waiting for loads, whose
+// latency the ring's 128 KB cover only while nothing is written (with the
+// stores left out in a timing copy 48 us; 3 stages 62.5, 2 stages 78 us); from
+// e4m3 the epilogue's instructions (issue slots 51 % busy, the products alone
+// 22.9 us).  16 epilogue warps of 64 columns at d = 64 took 39.4 us where 8 of
+// 128 columns took 42.7 (e4m3); at d = 128 a row is a whole head, 8 warps.
 //
 // The same kernel takes two other forms of the products (template kMode):
 //   kE4m3  X and W in e4m3 with fp32 scales of their rows: a K step of 128
@@ -864,7 +871,8 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
     // without a bias); kE4m3: their scales, and those of its rows.
     auto fetch = [&](int t, int buf) {
       const QkvStream S = stream_of(p, t >= p.s[1].tile0 ? 1 : 0);
-      const int tl = t - S.tile0, mt = static_cast<int>(p.by_tiles.div(tl)), col = (tl - mt * p.n_tiles) * kCols + wcol + lane * 4;
+      const int tl = t - S.tile0, mt = static_cast<int>(p.by_tiles.div(tl));
+      const int col = (tl - mt * p.n_tiles) * kCols + wcol + lane * 4;
       if (lane * 4 < Cfg::kWarpCols) {
         const uint32_t to = bias_w + buf * Cfg::kBiasBytes + lane * 16;
         if (S.bias && col < hd3)

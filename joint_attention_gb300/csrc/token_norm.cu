@@ -19,9 +19,17 @@
 // most four chunks a lane, kept in registers between the reduction and the
 // output: every array is read and written once.  A block of 8 warps holds 8 / G
 // rows (16 warps for G = 16); warps of a row join their sums through shared
-// memory and a barrier of their own.  The arithmetic is in packed fp32 pairs:
-// with three reads and two writes of 16 bits a value the kernels are bound by
-// HBM only while they spend some 10 instructions on it.
+// memory and a barrier of their own.  The arithmetic is in packed fp32 pairs: the
+// kernels are bound by HBM only while they spend some 10 instructions on a
+// value.  Four chunks a lane, that is few warps a row and much in flight for
+// each, measured best (9524 x 2048 to 8 bits 26.3 us with 4, 29.0 with 2, 33.6
+// with 1, 27.9 with 8).
+//
+// Measured (device time, inputs out of L2; the copy rate is 6.77 TB/s): forward
+// 17616 x 768 17.7 us (6.1 TB/s), 32768 x 4096 155 us (6.9 TB/s); to 8 bits 9524
+// x 2048 26.3 us (5.2 TB/s: 16 instructions a value); rows to 8 bits 9524 x 2048
+// 10.0 us (5.9 TB/s); backward 17616 x 768 20.3 us with the sum of dg (5.3 TB/s:
+// two launches, and 7.2 rows a warp).
 #include <cuda_bf16.h>
 
 #include "jattn_internal.h"
@@ -235,69 +243,37 @@ struct NormBwdArgs {
 };
 
 // Rows in a fixed stride per block; each lane sums dy n of its columns over
-// the rows it meets, then the block's rows are added in order.  The three
-// operands of a row arrive by bulk copies in one of two buffers of its warps'
-// own, two rows ahead of the arithmetic: 17616 x 768 in 23.1 us with the rows
-// loaded to registers when they are needed, 26.4 us loaded one row ahead.
-constexpr int kBwdBufs = 2;
-
+// the rows it meets, then the block's rows are added in order.  n and u stay in
+// registers between the two uses, 13 instructions a value instead of 20.  (The
+// next rows' operands by bulk copies through shared memory, two rows ahead: 22.2
+// us for 17616 x 768 instead of 20.3; to registers, one row ahead: slower still.)
 template <int V, int G>
-__global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 1 : 2) token_norm_bwd_kernel(const NormBwdArgs a,
-                                                                                            uint32_t* dev_err) {
+__global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 1 : 2) token_norm_bwd_kernel(const NormBwdArgs a) {
   constexpr int kLanes = 32 * G, kRows = block_warps(G) / G;
-  extern __shared__ __align__(16) uint4 ring[];  // [row of the block][buffer][dy, h, dh][chunks]; then the sums
+  extern __shared__ float sums[];  // [rows of a block][C]
   __shared__ float red[2][kMaxWarps];
-  __shared__ uint64_t full[kRows][kBwdBufs];
-  __shared__ int abort_flag;
-  volatile int* ab = &abort_flag;
   const int lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
   griddep_launch_dependents();
-  if (threadIdx.x == 0) {
-    abort_flag = 0;
-    for (int i = 0; i < kRows * kBwdBufs; ++i) mbar_init(&full[0][0] + i, 1);
-    fence_mbar_init();
-  }
   griddep_wait();
-  __syncthreads();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows + slot;
-  const uint32_t bytes = a.chunks * 16;
-  auto buffer = [&](int buf) { return ring + static_cast<size_t>((slot * kBwdBufs + buf) * 3) * a.chunks; };
-  auto fetch = [&](int64_t row, int buf) {  // one lane of the row's warps
-    uint4* to = buffer(buf);
-    uint64_t* bar = &full[slot][buf];
-    const int64_t base = row * a.chunks;
-    mbar_arrive_expect_tx(bar, a.dh ? 3 * bytes : 2 * bytes);
-    bulk_load(to, a.dy + base, bytes, bar);
-    bulk_load(to + a.chunks, a.h + base, bytes, bar);
-    if (a.dh) bulk_load(to + 2 * a.chunks, a.dh + base, bytes, bar);
-  };
-  int fetched = 0;
-  if (lane == 0)
-    for (; fetched < kBwdBufs && first + fetched * step < a.T; ++fetched) fetch(first + fetched * step, fetched);
   uint64_t acc[V][4];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0;
   int it = 0;
-  float next_r = first < a.T ? a.r[first] : 0.f;
-  for (int64_t row = first; row < a.T; row += step, ++it) {
-    const int buf = it % kBwdBufs;
-    const float r = next_r;
-    next_r = row + step < a.T ? a.r[row + step] : 0.f;
-    // A wait that gave up is recorded; the loop goes on over what the buffer holds (without new copies), so
-    // that the warps of a row still meet at their barrier.
-    mbar_wait(&full[slot][buf], (it / kBwdBufs) & 1, ab, dev_err);
-    const uint4* from = buffer(buf);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + slot; row < a.T; row += step, ++it) {
+    const uint4 *dy = a.dy + row * a.chunks, *h = a.h + row * a.chunks;
+    const uint4* dh = a.dh ? a.dh + row * a.chunks : nullptr;
+    const float r = a.r[row];
     uint4 wy[V], wh[V], wd[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * kLanes + lane;
       const bool in = c < a.chunks;
-      wy[i] = in ? from[c] : make_uint4(0u, 0u, 0u, 0u);
-      wh[i] = in ? from[a.chunks + c] : make_uint4(0u, 0u, 0u, 0u);
-      wd[i] = in && a.dh ? from[2 * a.chunks + c] : make_uint4(0u, 0u, 0u, 0u);
+      wy[i] = in ? dy[c] : make_uint4(0u, 0u, 0u, 0u);
+      wh[i] = in ? h[c] : make_uint4(0u, 0u, 0u, 0u);
+      wd[i] = in && dh ? dh[c] : make_uint4(0u, 0u, 0u, 0u);
     }
     const int64_t base = row * a.chunks;
     const uint64_t r2 = f2_make(r, r);
@@ -321,12 +297,6 @@ __global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 1 : 2) token_norm
     float u0, u1;
     f2_split(un2, u0, u1);
     const float m = -row_reduce<G, false>(u0 + u1, red[it & 1]) * a.inv_c;
-    // Every lane of the row has its values in registers (they are in the sum, or were read before it).
-    __syncwarp();
-    if (lane == 0 && row + kBwdBufs * step < a.T && !*ab) {
-      fetch(row + kBwdBufs * step, buf);
-      ++fetched;
-    }
     const uint64_t m2 = f2_make(m, m);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -337,14 +307,8 @@ __global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 1 : 2) token_norm
       if (c < a.chunks) a.dx[base + c] = pack8(d);
     }
   }
-  if (lane == 0 && *ab) {  // the copies in flight land before the block exits
-    for (int i = fetched > kBwdBufs ? fetched - kBwdBufs : 0; i < fetched; ++i)
-      mbar_wait_drain(&full[slot][i % kBwdBufs], (i / kBwdBufs) & 1);
-  }
   const int C = a.chunks * 8;
   float* out = a.part + static_cast<size_t>(blockIdx.x) * C;
-  float* sums = reinterpret_cast<float*>(ring);  // [rows of the block][C]: every copy has landed and been read
-  if constexpr (kRows > 1) __syncthreads();
   ulonglong2* mine = reinterpret_cast<ulonglong2*>(kRows > 1 ? sums + static_cast<size_t>(slot) * C : out);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -455,7 +419,7 @@ int add_norm_bwd_parts(int T, int C) {
 
 cudaError_t launch_add_norm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const float* r,
                                 const float* g, int T, int C, uint16_t* dx, float* part, int parts,
-                                uint32_t* dev_err, cudaStream_t st) {
+                                cudaStream_t st) {
   NormBwdArgs a;
   a.dy = reinterpret_cast<const uint4*>(dy);
   a.dh = reinterpret_cast<const uint4*>(dh);
@@ -470,13 +434,9 @@ cudaError_t launch_add_norm_bwd(const uint16_t* dy, const uint16_t* dh, const ui
   return with_layout(a.chunks, [&](auto l) {
     using L = decltype(l);
     constexpr int kWarps = block_warps(L::G), kRows = kWarps / L::G;
-    // 12 bytes a value for the rows of a block: 96 KB at most (two blocks on an SM), 192 KB for G = 16.
-    const size_t smem = static_cast<size_t>(kRows) * kBwdBufs * 3 * C * 2;
-    auto kernel = token_norm_bwd_kernel<L::V, L::G>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(parts)), dim3(32 * kWarps), smem, st, a, dev_err);
+    const size_t smem = kRows > 1 ? static_cast<size_t>(kRows) * C * sizeof(float) : 0;  // at most 32 KB
+    return launch_pdl(token_norm_bwd_kernel<L::V, L::G>, dim3(static_cast<unsigned>(parts)), dim3(32 * kWarps), smem,
+                      st, a);
   });
 }
 
