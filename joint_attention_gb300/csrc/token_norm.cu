@@ -244,7 +244,7 @@ struct NormBwdArgs {
 
 // Rows in a fixed stride per block; each lane sums dy n of its columns over
 // the rows it meets, then the block's rows are added in order.  n and u stay in
-// registers between the two uses, 13 instructions a value instead of 20.  (The
+// registers between the two uses, 12 instructions a value instead of 20.  (The
 // next rows' operands by bulk copies through shared memory, two rows ahead: 22.2
 // us for 17616 x 768 instead of 20.3; to registers, one row ahead: slower still.)
 template <int V, int G>
