@@ -222,7 +222,7 @@ int jattn_fwd_saved(const jattn_bf16* v, int B, int H, int N_img, int N_txt, int
  *
  * e4m3 is 1 sign, 4 exponent and 3 mantissa bits, largest finite value 448,
  * one byte a value; a row stands for s * y8.  The sum of squares is fp32: a
- * row whose mean square passes the fp32 range comes out as zeros.  A row with
+ * row whose sum passes the fp32 range comes out as zeros.  A row with
  * a NaN comes out as NaN (jattn_quant_rows: the NaN values stay NaN and do not
  * enter the row's maximum); 8-bit rows with an infinite z read NaN.
  *   x     : [T, C] bf16
@@ -266,7 +266,7 @@ int jattn_add_norm_bwd(const jattn_bf16* dy, const jattn_bf16* dh, const jattn_b
  * no gradient).  jattn_qkv_norm with rows in e4m3 and their fp32 scales, as
  * jattn_add_norm_fp8 and jattn_quant_rows write them:
  *
- *   Y = bf16(sx_t sw_o sum_c x8_tc w8_oc + b_o)     fp32 accumulation
+ *   Y = bf16((sum_c x8_tc w8_oc) sx_t sw_o + b_o)   fp32, in this order
  *
  *   x_img, x_txt   : [B, N_img, C] and [B, N_txt, C] bytes
  *   sx_img, sx_txt : [B, N_img] and [B, N_txt] float32

@@ -141,6 +141,14 @@ def _outputs_on(stream, *tensors):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
+def _buffer(nbytes, device):
+    """A buffer of the size that the library asks for; 0 is for sizes that the call then refuses, which
+    says why only if it gets a pointer."""
+    import torch
+
+    return torch.empty(nbytes or 16, dtype=torch.uint8, device=device)
+
+
 # The functions below hand the raw pointers of the outputs that they have just allocated to the
 # binding: only a caller's tensors need its checks.
 
@@ -183,7 +191,7 @@ def add_norm_backward(dy, h, r, g, dh=None, stream=None):
     T, C = r.numel(), g.numel()
     with _outputs_on(stream, dy, h, r, g, dh):
         dx, dg = torch.empty_like(dy), torch.empty_like(g)
-        work = torch.empty(jattn_add_norm_bwd_bytes(T, C), dtype=torch.uint8, device=dy.device)
+        work = _buffer(jattn_add_norm_bwd_bytes(T, C), dy.device)
     jattn_add_norm_bwd(dy, dh, h, r, g, T, C, dx.data_ptr(), dg.data_ptr(), work.data_ptr(), stream)
     return dx, dg
 
@@ -209,7 +217,7 @@ def _projected(x_img, x_txt, H: int, d: int):
     shape = (B, H, N_img + N_txt, d)
     q = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     k, v = torch.empty_like(q), torch.empty_like(q)
-    saved = torch.empty(jattn_saved_bytes(B, H, N_img, N_txt, d), dtype=torch.uint8, device=dev)
+    saved = _buffer(jattn_saved_bytes(B, H, N_img, N_txt, d), dev)
     return (q, k, v, saved), (B, H, N_img, N_txt, d, C)
 
 
@@ -231,13 +239,11 @@ def qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, H: int, down
     scale[a] (x A_a^T) B_a^T, a = index[b] (int32 on the device; outside 0 .. n - 1: none), with A in
     down_* [n, 3 rank, C] and B in up_* [n, 3 H d, rank], q, k and v each with a rank of their own
     (both None: no adapters in that stream)."""
-    import torch
-
     rank = next((u.shape[-1] for u in (up_img, up_txt) if u is not None), 8)
     with _outputs_on(stream, x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_img, up_img, down_txt, up_txt,
                      scale, index):
         out, sizes = _projected(x_img, x_txt, H, gq.shape[0])
-        work = torch.empty(jattn_qkv_norm_lora_bytes(*sizes[:5], rank), dtype=torch.uint8, device=x_img.device)
+        work = _buffer(jattn_qkv_norm_lora_bytes(*sizes[:5], rank), x_img.device)
     jattn_qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_img, up_img, down_txt, up_txt, scale,
                         index, scale.numel(), rank, *sizes, *(t.data_ptr() for t in out), work.data_ptr(), stream)
     return out

@@ -190,7 +190,9 @@ cudaError_t launch_lora_down(const CUtensorMap (&x)[2], const CUtensorMap (&down
   p.index = l.index;
   p.scale = l.scale;
   const int smem = p.stages * stage_bytes + 1024;
-  cudaError_t e = cudaFuncSetAttribute(lora_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The limit for every rank: a call of another thread, or a captured one, may be of a higher rank.
+  cudaError_t e = cudaFuncSetAttribute(lora_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kDownSmem + 1024);
   if (e != cudaSuccess) return e;
   return launch_pdl(lora_down_kernel, dim3(ctas), dim3(kDownThreads), smem, st, maps, p, dev_err);
 }

@@ -11,6 +11,9 @@ Tolerances, from the arithmetic:
   sum_j 2^-16 |U_j B_oj|, and its own accumulation (C + 2) 2^-23 sum_j mag(U_j) |B_oj|.
 * q_hat, k_hat, 1/rms: bit for bit (1/rms to 2^-21) what jattn_fwd_train keeps for the same q, k.
 """
+import threading
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -421,6 +424,86 @@ def test_forms_on_another_stream(ja):
     side.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@gpu
+def test_adapters_of_several_ranks_in_one_graph(ja):
+    """A captured call keeps what its launch needs when calls of other ranks follow, in the graph and outside."""
+    ts = [lora_inputs(2, 2, 140, 9, 64, 128, rank, 2, True, 85) for rank in (128, 16, 8)]
+    want = [lora_call(ja, t, 2)[:3] for t in ts]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [lora_call(ja, t, 2)[:3] for t in ts]
+    lora_call(ja, ts[2], 2)
+    for t in (x for out in got for x in out):
+        t.fill_(float("nan"))
+    graph.replay()
+    ok(ja)
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@gpu
+def test_calls_at_once(ja):
+    """Host threads with a stream each: adapters of different ranks, 8-bit rows, the token rows with their
+    backward, and the attention; every call gives the bits that it gives alone."""
+    tl = [lora_inputs(2, 4, 200, 30, 64, 128, rank, 2, True, 86) for rank in (128, 8)]
+    t8 = fp8_inputs(2, 12, 1024, 77, 64, 768, True, 87)
+    g = gen(88)
+    q, k, v = (randn(g, 1, 4, 333, 64) for _ in range(3))
+    x, res, dy = (randn(g, 700, 768) for _ in range(3))
+    gain = torch.rand(768, generator=g, device="cuda") + 0.5
+
+    def rows(stream):
+        y, h, r = ja.add_norm(x, gain, res, stream=stream)
+        return y, h, *ja.add_norm_backward(dy, h, r, gain, stream=stream)
+
+    jobs = [lambda s, t=t: lora_call(ja, t, 4, s)[:3] for t in tl]
+    jobs += [lambda s: fp8_call(ja, t8, 12, s)[:3], rows, lambda s: ja.forward(q, k, v, t8["gq"], t8["gk"], 33, s)[:1]]
+    want = [job(None) for job in jobs]
+    ok(ja)
+    start = threading.Barrier(len(jobs))
+
+    def run(job):
+        side = torch.cuda.Stream()
+        start.wait()
+        outs = [job(side) for _ in range(30)]
+        side.synchronize()
+        return outs
+
+    with ThreadPoolExecutor(len(jobs)) as pool:
+        results = list(pool.map(run, jobs))
+    ok(ja)
+    for outs, one in zip(results, want):
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(out, one))
+
+
+@gpu
+def test_on_the_default_stream_by_its_handle(ja):
+    """Stream 0 is a stream as any other, with another one current."""
+    t = lora_inputs(2, 2, 140, 9, 64, 128, 16, 2, True, 89)
+    want = lora_call(ja, t, 2)[:3]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = lora_call(ja, t, 2, 0)[:3]
+        torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@gpu
+def test_wrappers_name_what_is_unsupported(ja):
+    code = STATUS_CODE["JATTN_ERR_UNSUPPORTED"]
+    x, gain = randn(gen(90), 4, 12), torch.ones(12, device="cuda")
+    r = torch.ones(4, device="cuda")
+    t8 = fp8_inputs(1, 2, 8, 0, 32, 64, False, 91)
+    tl = lora_inputs(1, 2, 8, 0, 64, 64, 12, 1, False, 92)
+    for call in (lambda: ja.add_norm(x, gain), lambda: ja.add_norm_backward(x, x, r, gain),
+                 lambda: fp8_call(ja, t8, 2), lambda: lora_call(ja, tl, 2)):
+        with pytest.raises(ja.JattnError) as e:
+            call()
+        assert e.value.status == code
 
 
 # Fake, never-dereferenced device addresses: validation happens first.
