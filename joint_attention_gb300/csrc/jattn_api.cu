@@ -273,13 +273,13 @@ bool encode_bhnd_map_rows(CUtensorMap* map, const void* base, int BH, int N, int
   return r == CUDA_SUCCESS;
 }
 
-bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool e4m3) {
+bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, bool e4m3) {
   auto fn = encode_fn();
   if (!fn) return false;
   const int size = e4m3 ? 1 : 2;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * size};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), 128};
   cuuint32_t es[2] = {1, 1};
   CUresult r = fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                   const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -287,17 +287,45 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t c
   return r == CUDA_SUCCESS;
 }
 
-bool encode_unit_map(CUtensorMap* map, const void* base, int planes, int64_t rows, int cols, int box_rows) {
+bool encode_heads_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool e4m3) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
-                        static_cast<cuuint64_t>(planes)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(rows) * cols * 2};
-  cuuint32_t box[3] = {16, static_cast<cuuint32_t>(box_rows), 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, const_cast<void*>(base), dims, strides, box,
-                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t size = e4m3 ? 1 : 2, row = static_cast<cuuint64_t>(cols) * size;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(cols), 4, 16, static_cast<cuuint64_t>(rows) / 64};
+  cuuint64_t strides[3] = {16 * row, row, 64 * row};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / size), 4, 16, static_cast<cuuint32_t>(box_rows) / 64};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_unit_map(CUtensorMap* map, const void* base, int64_t rows, int cols) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  cuuint32_t box[2] = {16, 128};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_up_map(CUtensorMap* map, const uint16_t* up, int n, int64_t rows, int rank, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(rank) * 2;
+  cuuint64_t dims[5] = {static_cast<cuuint64_t>(rank), 4, 16, static_cast<cuuint64_t>(rows) / 64,
+                        static_cast<cuuint64_t>(n)};
+  cuuint64_t strides[4] = {16 * row, row, 64 * row, static_cast<cuuint64_t>(rows) * row};
+  cuuint32_t box[5] = {16, 4, 16, static_cast<cuuint32_t>(box_rows) / 64, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint16_t*>(up), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -799,19 +827,18 @@ int qkv_body(const QkvCall& c) {
   a.hat[1] = reinterpret_cast<uint16_t*>(base + sl.khat);
   a.r[0] = reinterpret_cast<float*>(base + sl.rq);
   a.r[1] = reinterpret_cast<float*>(base + sl.rk);
+  a.wide = true;
+  for (const void* o : {a.out[0], a.out[1], a.out[2], a.hat[0], a.hat[1]})
+    a.wide = a.wide && reinterpret_cast<uintptr_t>(o) % 32 == 0;
   a.pair = qkv_uses_pairs(a);
   const int w_rows = kQkvWRows(d, a.pair);
   CUtensorMap maps[4];
   for (int i = 0; i < 2; ++i) {
     const int j = n_s[i] ? i : 1 - i;  // a stream without rows launches no tiles: any valid map
-    if (!encode_rows_map(&maps[2 * i], c.x[j], a.M[j], C, 128, c.e4m3) ||
-        !encode_rows_map(&maps[2 * i + 1], c.w[j], ycols, C, w_rows, c.e4m3))
+    if (!encode_rows_map(&maps[2 * i], c.x[j], a.M[j], C, c.e4m3) ||
+        !encode_heads_map(&maps[2 * i + 1], c.w[j], ycols, C, w_rows, c.e4m3))
       return fail(JATTN_ERR_CUDA, "cuTensorMapEncodeTiled");
   }
-  CUtensorMap out_maps[5];
-  const void* outs_p[5] = {c.q, c.k, c.v, a.hat[0], a.hat[1]};
-  for (int i = 0; i < 5; ++i)
-    if (!encode_bhnd_map_rows(&out_maps[i], outs_p[i], s.BH, s.N, d, 32)) return fail(JATTN_ERR_CUDA, "cuTensorMapEncodeTiled");
   cudaError_t ce;
   LoraLaunch l;
   CUtensorMap lora_maps[4], down_maps[2], item_maps[2];
@@ -827,8 +854,8 @@ int qkv_body(const QkvCall& c) {
       l.on[i] = c.down[i] && n_s[i] > 0;
       if (!l.on[i]) {
         lora_maps[i] = lora_maps[2 + i] = down_maps[i] = item_maps[i] = maps[0];
-      } else if (!encode_unit_map(&lora_maps[i], l.u[i], 0, a.M[i], 6 * r16, 128) ||
-                 !encode_unit_map(&lora_maps[2 + i], c.up[i], c.n_adapters, ycols, c.rank, w_rows) ||
+      } else if (!encode_unit_map(&lora_maps[i], l.u[i], a.M[i], 6 * r16) ||
+                 !encode_up_map(&lora_maps[2 + i], c.up[i], c.n_adapters, ycols, c.rank, w_rows) ||
                  !encode_bhnd_map_rows(&down_maps[i], c.down[i], 3 * c.n_adapters, c.rank, C, r16) ||
                  !encode_bhnd_map(&item_maps[i], c.x[i], c.B, n_s[i], C)) {
         return fail(JATTN_ERR_CUDA, "cuTensorMapEncodeTiled");
@@ -842,7 +869,7 @@ int qkv_body(const QkvCall& c) {
   }
   {
     Timed t(JATTN_KERNEL_QKV_NORM, st);
-    ce = launch_qkv_norm(maps, out_maps, a, err, st, c.lora ? &l : nullptr, lora_maps);
+    ce = launch_qkv_norm(maps, a, err, st, c.lora ? &l : nullptr, lora_maps);
   }
   if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "qkv_norm launch", ce);
   return JATTN_OK;

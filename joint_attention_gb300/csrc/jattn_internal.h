@@ -172,8 +172,8 @@ int attn_bwd_counter_words(const AttnShape& s);
 
 // --- QKV projection with the QK-RMSNorm epilogue ---------------------------
 // Stream 0 is the image stream, stream 1 the caption stream; maps holds the
-// TMA maps of x0, w0, x1, w1 (encode_rows_map: x with 128-row boxes, w with
-// kQkvWRows boxes).  A stream with M = 0 rows launches no tiles (its maps are
+// TMA maps of x0, w0, x1, w1 (encode_rows_map: x; encode_heads_map: w, boxes of
+// kQkvWRows rows).  A stream with M = 0 rows launches no tiles (its maps are
 // then any valid map).
 // Tiles: 256 rows x 256 columns by a pair of CTAs (qkv_uses_pairs), each
 // loading half of the weight rows, or 128 rows x one head by one CTA.
@@ -191,6 +191,7 @@ struct QkvLaunch {
   const float *gq, *gk;
   uint16_t* out[3];  // q, k, v
   uint16_t* hat[2];  // q_hat, k_hat
+  bool wide;         // those five at 32-byte boundaries
   float* r[2];       // rq, rk
 };
 // Low-rank adapters of the batch items beside the projection (bf16 only).
@@ -201,17 +202,16 @@ struct LoraLaunch {
   bool on[2];          // whether a stream has adapters (and rows)
   uint16_t* u[2];      // scratch [M, 2 * 3 * 16 ceil(rank / 16)]
 };
-// out_maps: q, k, v, q_hat, k_hat as encode_bhnd_map_rows(..., 32) maps.
-// lora_maps (with lora): encode_unit_map maps of both streams' U (128-row
-// boxes), then of their up weights [n, 3 H d, rank] (kQkvWRows boxes); a
-// stream without adapters: any valid map.
-cudaError_t launch_qkv_norm(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
+// lora_maps (with lora): encode_unit_map maps of both streams' U, then
+// encode_up_map maps of their up weights (boxes of kQkvWRows rows); a stream
+// without adapters: any valid map.
+cudaError_t launch_qkv_norm(const CUtensorMap (&maps)[4], const QkvLaunch& a,
                             uint32_t* dev_err, cudaStream_t st, const LoraLaunch* lora = nullptr,
                             const CUtensorMap* lora_maps = nullptr);
 bool qkv_uses_pairs(const QkvLaunch& a);
-cudaError_t launch_qkv_norm_e4m3(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
+cudaError_t launch_qkv_norm_e4m3(const CUtensorMap (&maps)[4], const QkvLaunch& a,
                                  uint32_t* dev_err, cudaStream_t st);
-cudaError_t launch_qkv_norm_lora(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
+cudaError_t launch_qkv_norm_lora(const CUtensorMap (&maps)[4], const QkvLaunch& a,
                                  uint32_t* dev_err, cudaStream_t st, const LoraLaunch* lora,
                                  const CUtensorMap* lora_maps);
 // U = scale X A^T in two bf16 terms, before launch_qkv_norm.  x: [B, N_s, C] as
@@ -220,13 +220,20 @@ cudaError_t launch_qkv_norm_lora(const CUtensorMap (&maps)[4], const CUtensorMap
 cudaError_t launch_lora_down(const CUtensorMap (&x)[2], const CUtensorMap (&down)[2], const LoraLaunch& l,
                              const QkvLaunch& a, int B, uint32_t* dev_err, cudaStream_t st);
 // A 2-D TMA map over a row-major [rows, cols] matrix of bf16 (or, with e4m3,
-// 8-bit) values with a (128 bytes, box_rows) box and 128-byte swizzle (a
-// row's bytes a multiple of 16).
-bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows,
-                     bool e4m3 = false);
-// TMA maps with (16, box_rows) boxes of bf16 and 32-byte swizzle over
-// [planes, rows, cols]; planes 0: a 2-D map over [rows, cols].
-bool encode_unit_map(CUtensorMap* map, const void* base, int planes, int64_t rows, int cols, int box_rows);
+// 8-bit) values with a (128 bytes, 128) box and 128-byte swizzle (a row's bytes
+// a multiple of 16).
+bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, bool e4m3);
+// The projection's order of columns: a box row 64 g + 4 j + b is matrix row 64 g
+// + 16 b + j, so that four lanes that read one row of the accumulator four
+// columns at a time end with 16 consecutive columns each.
+// Weights [rows, cols], rows a multiple of 64, in that order: a 4-D map
+// (cols, b, j, g) with box_rows (a multiple of 64) rows a box, otherwise as above.
+bool encode_heads_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool e4m3);
+// (16, 128) boxes of a [rows, cols] bf16 matrix, 32-byte swizzle.
+bool encode_unit_map(CUtensorMap* map, const void* base, int64_t rows, int cols);
+// n adapters' up weights [rows, rank] in that order: a 5-D map (rank, b, j, g,
+// adapter), 16 of the rank and box_rows rows a box, 32-byte swizzle.
+bool encode_up_map(CUtensorMap* map, const uint16_t* up, int n, int64_t rows, int rank, int box_rows);
 
 // Encodes a 3-D TMA map over a [BH, N, d] bf16 tensor with a (64, 128, 1)
 // box and 128-byte swizzle.  Returns false if the driver rejects it.

@@ -3,9 +3,9 @@
 
 namespace jattn {
 
-cudaError_t launch_qkv_norm_e4m3(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
+cudaError_t launch_qkv_norm_e4m3(const CUtensorMap (&maps)[4], const QkvLaunch& a,
                                  uint32_t* dev_err, cudaStream_t st) {
-  return launch_qkv_form<kE4m3>(maps, out_maps, a, dev_err, st, nullptr, nullptr);
+  return launch_qkv_form<kE4m3>(maps, a, dev_err, st, nullptr, nullptr);
 }
 
 }  // namespace jattn

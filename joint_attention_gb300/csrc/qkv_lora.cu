@@ -197,10 +197,10 @@ cudaError_t launch_lora_down(const CUtensorMap (&x)[2], const CUtensorMap (&down
   return launch_pdl(lora_down_kernel, dim3(ctas), dim3(kDownThreads), smem, st, maps, p, dev_err);
 }
 
-cudaError_t launch_qkv_norm_lora(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
+cudaError_t launch_qkv_norm_lora(const CUtensorMap (&maps)[4], const QkvLaunch& a,
                                  uint32_t* dev_err, cudaStream_t st, const LoraLaunch* lora,
                                  const CUtensorMap* lora_maps) {
-  return launch_qkv_form<kLora>(maps, out_maps, a, dev_err, st, lora, lora_maps);
+  return launch_qkv_form<kLora>(maps, a, dev_err, st, lora, lora_maps);
 }
 
 }  // namespace jattn

@@ -36,24 +36,27 @@
 //   issuer      (of a pair: the first CTA's) 4 MMAs per K step into one of two
 //               TMEM accumulators, so that a tile's epilogue overlaps the next
 //               tile's products.
-//   epilogue    one thread per token row (TMEM lane), two heads of d = 64 or
-//               one of d = 128 (!kPair: one head).  Per head: d fp32 values out
-//               of TMEM, + bias (the warp's slice, copied to shared memory
-//               while the products run), rounded to bf16 (the projection's
-//               output) for q / k / v; for q and k the row's RMSNorm from those
-//               bf16 values, q_hat / k_hat and r.  Rows are staged in shared
-//               memory and written out as whole 128-byte lines (a TMA tile
-//               store, or four rows per store instruction).
+//   epilogue    a head's columns of 16 or 32 token rows a warp: their values out
+//               of TMEM, + bias (the columns', copied to shared memory while the
+//               products run), rounded to bf16 (the projection's output) for q /
+//               k / v; for q and k the row's RMSNorm from those bf16 values,
+//               q_hat / k_hat and r.  Four lanes share a row, 16 neighbouring
+//               columns of each 64 a lane, and write it straight from registers
+//               as whole 128-byte lines: the weights' rows are loaded in an order
+//               that leaves each lane's columns next to each other (qkv_emit).
 // Heads past 3 H in the last column tile, and token rows past the stream's
 // end in its last row tile, read the TMA's zero fill and are not stored.
 //
-// What bounds it (512 px, C = 768, 12 heads of 64; 57 us from bf16, 39 us from
-// e4m3): from bf16 a third of the issuer's time goes to waiting for loads, whose
-// latency the ring's 128 KB cover only while nothing is written (with the
-// stores left out in a timing copy 48 us; 3 stages 62.5, 2 stages 78 us); from
-// e4m3 the epilogue's instructions (issue slots 51 % busy, the products alone
-// 22.9 us).  16 epilogue warps of 64 columns at d = 64 took 39.4 us where 8 of
-// 128 columns took 42.7 (e4m3); at d = 128 a row is a whole head, 8 warps.
+// What bounds it (512 px, C = 768, 12 heads of 64; 51.5 us from bf16, 38.9 us
+// from e4m3; 768 px, C = 2048, 16 heads of 128; 141 and 86.5 us): the epilogue
+// beside the products.  From e4m3 at 768 px the products alone take 66 us (the
+// rate of cuBLAS), the epilogue with one K step 50, without its stores 41; at
+// 512 px 24, 34 and 29: there the epilogue's instructions count (some 930 a
+// warp for 32 rows of 64 columns).  What the epilogue takes of shared memory's
+// bandwidth the products lack: rows staged there and written out by TMA stores,
+// with the ring at 128 KB for it instead of 192, took 57 and 38.8, 151 and 92
+// us; the gains, biases and scales read without a gap every 16 columns (two-way
+// bank conflicts), and anew for each row, 5 us more at 512 px.
 //
 // The same kernel takes two other forms of the products (template kMode):
 //   kE4m3  X and W in e4m3 with fp32 scales of their rows: a K step of 128
@@ -71,10 +74,10 @@
 //          as many runs as fit (2 or 4 KB each): two such groups when there
 //          is one run, and U loaded once for 6 to 8 runs when there are many.
 //
-// Correct rounding: the per-thread sum of the d squares is a balanced tree
-// (at most 7 roundings per term, within the 8 that the rounding window of the
-// norm kernels allows for), and elements in the bf16-midpoint window are
-// re-rounded from a double-float r.
+// Correct rounding: the sum of the d squares is a balanced tree over a lane's
+// columns and the four lanes (at most 7 roundings per term, within the 8 that
+// the rounding window of the norm kernels allows for), and elements in the
+// bf16-midpoint window are re-rounded from a double-float r.
 #pragma once
 #include <atomic>
 
@@ -93,25 +96,20 @@ enum QkvMode { kBf16 = 0, kE4m3 = 1, kLora = 2 };
 constexpr int kBM = 128;                            // token rows of one CTA
 constexpr int kStepBytes = 128;                     // of each row in a K step
 constexpr int kATile = kBM * kStepBytes;            // 16 KB
-constexpr int kStageRowBytes = 128;                 // 64 bf16 columns of one token row
-constexpr int kStagingBytes = 32 * kStageRowBytes;  // per epilogue warp: its 32 rows of 64 columns
 constexpr uint32_t kDeadRow = 0xFFFFFFFFu;
-constexpr int kMaxStages = 6;
+constexpr int kRingBytes = 192 * 1024;
+constexpr int kMaxStages = 8;
 
-// Epilogue warps (warps w and w + 4 take the TMEM lanes of warp w % 4, and
-// kWarpCols columns each), then the TMA producer and the MMA issuer.  Each
-// epilogue warp stages its rows in shared memory, a buffer for each 64 of its
-// columns: raw, then q_hat / k_hat.
+// Epilogue warps, then the TMA producer and the MMA issuer.  Warp w reads the TMEM
+// lanes (rows) of warp w % 4, a head's columns of 16 rows or (kHalves = 2) of 32.
 // kPair: registers per thread (setmaxnreg).  Each SM sub-partition holds the
 // epilogue warps w with one w % 4 and one other warp, and an increase draws only
-// on the registers those were launched with, so (epilogue warps / 4) x kEpi +
-// kOther must be at most (epilogue warps / 4 + 1) x the launch count (allocated
-// by eights).  The launcher refuses any build whose register count differs.
-template <int D>
+// on the registers those were launched with, so 4 kEpi + kOther must be at most 5
+// times the launch count (allocated by eights).  The launcher refuses any build
+// whose register count differs.
 struct QkvRegs {
-  static constexpr int kLaunch = D == 64 ? 96 : 168, kEpi = D == 64 ? 104 : 208, kOther = D == 64 ? 64 : 88;
-  static constexpr int kEpiWarps = D == 64 ? 16 : 8;
-  static_assert(kEpiWarps / 4 * kEpi + kOther == (kEpiWarps / 4 + 1) * kLaunch, "projection register split");
+  static constexpr int kLaunch = 96, kEpi = 104, kOther = 64;
+  static_assert(4 * kEpi + kOther == 5 * kLaunch, "projection register split");
 };
 
 template <int D, int kMode, bool kPair>
@@ -119,23 +117,19 @@ struct QkvCfg {
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kCols = kQkvCols(D, kPair);       // of a tile
   static constexpr int kBRows = kQkvWRows(D, kPair);     // weight rows that a CTA loads
-  static constexpr int kWarpCols = kPair && D == 128 ? 128 : D;
-  static constexpr int kEpiWarps = 4 * (kCols / kWarpCols);
+  static constexpr int kEpiWarps = kPair ? 16 : 8;
+  static constexpr int kGroupWarps = kEpiWarps * D / kCols;  // that share a head's columns
+  static constexpr int kHalves = 8 / kGroupWarps;
   static constexpr int kWarpProd = kEpiWarps, kWarpIssue = kEpiWarps + 1;
   static constexpr int kThreads = 32 * (kEpiWarps + (kPair ? 4 : 2));  // kPair: two warps idle
-  static_assert(!kPair || kEpiWarps == QkvRegs<D>::kEpiWarps, "register split");
   static constexpr int kStageBytes = kATile + kBRows * kStepBytes;
-  static constexpr int kStages = kPair ? 4 : D == 64 ? 6 : 5;
+  static constexpr int kStages = kRingBytes / kStageBytes;
   static constexpr int kTmemCols = 2 * kCols;
-  static constexpr int kStaging = kWarpCols / 64 * kStagingBytes;
-  static constexpr int kBiasBytes = kWarpCols * 4;       // per epilogue warp: the bias of its columns
-  static constexpr int kSpareBytes = D * 2;              // per epilogue warp: fix_staged_rows' row
-  static constexpr int kOffStaging = kStages * kStageBytes;
-  static constexpr int kOffBias = kOffStaging + kEpiWarps * kStaging;
-  static constexpr int kOffSpare = kOffBias + kEpiWarps * 2 * kBiasBytes;  // two tiles' each
-  // kE4m3: the scales of the columns, likewise, and of the rows.
-  static constexpr int kOffScale = kOffSpare + kEpiWarps * kSpareBytes;
-  static constexpr int kOffXScale = kOffScale + kEpiWarps * 2 * kBiasBytes;
+  static constexpr int kColBytes = kCols * 5;            // the bias of a tile's columns, by col_offset
+  static constexpr int kOffBias = kStages * kStageBytes;  // two tiles'
+  // kE4m3: the scales of the columns, likewise, and of each warp's 32 rows.
+  static constexpr int kOffScale = kOffBias + 2 * kColBytes;
+  static constexpr int kOffXScale = kOffScale + 2 * kColBytes;
   static constexpr int kDynSmem = (kMode == kE4m3 ? kOffXScale + kEpiWarps * 2 * 128 : kOffScale) + 1024;
   // kLora: a group of operands for 16 of the rank, both terms of U, then the up weights of a run each.
   static constexpr int kUnitA = kBM * 32, kUnitB = kBRows * 32;
@@ -148,8 +142,8 @@ struct QkvBars {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
-  __align__(16) float gq[128];
-  __align__(16) float gk[128];
+  __align__(16) float gq[160];  // by col_offset
+  __align__(16) float gk[160];
 };
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
@@ -171,34 +165,30 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
-// Staging of a warp's 32 token rows of 64 bf16 columns (128 bytes each) in
-// shared memory: row i at i * 128, its 16-byte chunk c at slot c ^ (i % 8),
-// so that a row written by one lane and a chunk column read across 8 lanes
-// both touch every bank once.
-__device__ __forceinline__ uint32_t staged(uint32_t buf, int row, int chunk) {
-  return buf + row * kStageRowBytes + ((chunk ^ (row & 7)) << 4);
-}
-// This lane's row: w[0..31] (packed pairs).
-__device__ __forceinline__ void stage_row(uint32_t buf, const uint32_t* w, int lane) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c) st_shared_v4(staged(buf, lane, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-}
-// Writes the 32 staged rows out, four whole rows (four 128-byte lines) per
-// store instruction: lanes 8 j' .. 8 j' + 7 take row 4 j + j', one chunk
-// each.  row: this lane's row's index (b H + n's) for head 0 (kDeadRow: past
-// the stream's end); head_rows = h N; col: the first column (0, or 64 within a
-// d = 128 head row).
-template <int D>
-__device__ __forceinline__ void store_rows(uint32_t buf, uint16_t* base, uint32_t row, uint32_t head_rows, int col,
-                                           int lane) {
-  const int ch = lane & 7;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t to = __shfl_sync(0xffffffffu, row, 4 * j + (lane >> 3));
-    const uint4 val = ld_shared_v4(staged(buf, 4 * j + (lane >> 3), ch));
-    if (to != kDeadRow)
-      *reinterpret_cast<uint4*>(base + (static_cast<size_t>(to) + head_rows) * D + col + ch * 8) = val;
+// 16 consecutive columns of a row, one 32-byte store when the outputs are so
+// aligned (wide; pairs of CTAs are used only then), else two of 16 bytes.
+__device__ __forceinline__ void store_cols16(uint16_t* to, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
+}
+// All `threads` threads of a named barrier: whether ok holds for every one.
+__device__ __forceinline__ bool barrier_all(int id, int threads, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return all != 0;
 }
 
 // Elements near a bf16 midpoint.  The norm kernels' bound on z = (g x) r with
@@ -222,6 +212,10 @@ __device__ __forceinline__ bool any_near(uint32_t m) {
   return (m & 0xFFFFu) < kNearWindow || (m >> 16) < kNearWindow;
 }
 
+// Floats by column in shared memory: 16 bytes left free after each 16 columns, so
+// that four lanes reading 16 columns apart meet different banks.
+__device__ __forceinline__ constexpr uint32_t col_offset(uint32_t col) { return col * 4 + col / 16 * 16; }
+
 // The double-float sum of squares of a row spread over the warp, the same
 // on every lane: each lane's own error-free sum (s, c), then a butterfly of
 // error-free additions (symmetric, so every lane forms the same values).
@@ -244,70 +238,6 @@ __device__ __forceinline__ void add_sq_df(uint32_t w, float& s, float& c) {
   c = __fadd_rn(c, e);
 }
 
-// The rare path.  The warp takes each of its rows that has an element near a
-// bf16 midpoint (about one a tile) together: the lane that holds the row writes
-// its raw values to the warp's spare row; each lane takes D / 32 of them, their
-// squares (exact) are summed by error-free additions over the warp, and each
-// lane re-rounds its elements that the fp32 path put near a midpoint, from the
-// double-float r, and writes its words over the staged q_hat / k_hat row,
-// before that is written out.  (Four rows at a time by 8 lanes each took 2500
-// cycles a pass at d = 64 and 3700 at d = 128.)
-//   todo: rows by head (bit i: lane i's row); at d = 64 head h's staged rows are
-//   in buffer h, at d = 128 the head's halves in both.
-template <int D, int kHeads>
-__device__ __forceinline__ void fix_staged_rows(const unsigned (&todo)[kHeads], const uint32_t (&yb)[kHeads * D / 2],
-                                                uint32_t spare, uint32_t hat, const float (&r)[kHeads],
-                                                const float* const (&g)[kHeads], int lane) {
-  uint64_t left = todo[0];
-  if constexpr (kHeads == 2) left |= static_cast<uint64_t>(todo[1]) << 32;
-  while (left) {
-    const int bit = __ffsll(static_cast<long long>(left)) - 1;
-    left &= left - 1;
-    const int o = bit & 31, h = kHeads == 2 ? bit >> 5 : 0;
-    if (lane == o) {
-#pragma unroll
-      for (int i = 0; i < kHeads; ++i) {
-        if (h == i) {
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint32_t* y = yb + i * (D / 2) + 4 * c;
-            st_shared_v4(spare + c * 16, y[0], y[1], y[2], y[3]);
-          }
-        }
-      }
-    }
-    const float ro = __shfl_sync(0xffffffffu, h ? r[kHeads - 1] : r[0], o);
-    const float* gv = h ? g[kHeads - 1] : g[0];
-    __syncwarp();
-    constexpr int kWords = D / 64;  // of a lane: elements 2 kWords lane ..
-    uint32_t w[kWords];
-    float s = 0.f, c = 0.f;
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      w[i] = ld_shared_u32(spare + (kWords * lane + i) * 4);
-      add_sq_df(w[i], s, c);
-    }
-    warp_sum_df(s, c);
-    float rh, rl;
-    rsqrt_mean_eps_df(s, c, 1.f / D, rh, rl);
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const int e = 2 * (kWords * lane + i);
-      float f[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float x = j ? bf_hi(w[i]) : bf_lo(w[i]);
-        const float z = __fmul_rn(__fmul_rn(gv[e + j], x), ro);
-        f[j] = near_midpoint(z) ? round_bf16_df(gv[e + j], x, rh, rl) : z;
-      }
-      const int chunk = e >> 3;  // at d = 128 chunks 8 .. 15 are in the second buffer
-      const uint32_t buf = hat + (D == 64 ? h : chunk >> 3) * kStagingBytes;
-      st_shared_u32(staged(buf, o, chunk & 7) + (e & 6) * 2, pack_bf16x2(f[0], f[1]));
-    }
-    __syncwarp();  // the spare row is free again
-  }
-}
-
 struct QkvStream {
   int M;       // token rows (B * N_s)
   int N_s;     // tokens per batch item
@@ -322,10 +252,13 @@ struct QkvParams {
   int H, C, N;        // heads, model width (K of the product), joint sequence length
   int n_tiles;        // column tiles
   DivU31 by_tiles;    // division by n_tiles
-  int tiles;          // all tiles of both streams
+  int whole;          // tiles of both streams that are taken whole
+  int parts_log;      // those after them are taken in 1 << parts_log parts of their columns
+  int items;          // whole tiles and parts
   uint16_t* out[3];   // q, k, v: [B, H, N, d]
   uint16_t* hat[2];   // q_hat, k_hat
   float* r[2];        // rq, rk: [B, H, N]
+  bool wide;          // q, k, v, q_hat, k_hat at 32-byte boundaries
   // kLora: the batch items' adapters (none where outside 0 .. n_adapters - 1),
   // units of 16 of the rank, and whether a stream has adapters.
   const int* index;
@@ -335,7 +268,7 @@ struct QkvParams {
 };
 
 // kLora: U [M, 2 * 3 * 16 rank_units] (the high terms of q, k, v, then the low
-// terms) and the adapters' up weights [n, 3 H d, rank], image then caption stream.
+// terms) and the adapters' up weights, image then caption stream.
 struct QkvLoraMaps {
   CUtensorMap u[2], up[2];
 };
@@ -382,101 +315,55 @@ __device__ __forceinline__ uint32_t rows_of_word(int lo, int hi, int w) {
   asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(m) : "r"(from), "r"(max(to - from, 0)));
   return m;
 }
-// The q, k, v parts that columns n0 .. n0 + cols - 1 meet.
-__device__ __forceinline__ void parts_of(int n0, int cols, int hd, int& first, int& last) {
-  first = n0 / hd;
-  last = min((n0 + cols - 1) / hd, 2);
-}
-
-// TMA maps over the five outputs ([B H, N, d] bf16, box 64 columns x 32 rows,
-// 128-byte swizzle: the staging buffers' layout), for warps whose 32 rows lie
-// in one batch item.
-struct QkvOutMaps {
-  CUtensorMap out[3];  // q, k, v
-  CUtensorMap hat[2];  // q_hat, k_hat
-};
-__device__ __forceinline__ void tma_store_3d_s(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
-}
-
-// Field selection by a runtime index through selects: indexing the kernel's
-// parameter arrays with a runtime value would copy them to local memory.
-__device__ __forceinline__ uint16_t* out_of(const QkvParams& p, int which) {
-  return which == 0 ? p.out[0] : which == 1 ? p.out[1] : p.out[2];
-}
-__device__ __forceinline__ uint16_t* hat_of(const QkvParams& p, int which) { return which == 0 ? p.hat[0] : p.hat[1]; }
-__device__ __forceinline__ float* r_of(const QkvParams& p, int which) { return which == 0 ? p.r[0] : p.r[1]; }
-__device__ __forceinline__ const CUtensorMap* out_map(const QkvOutMaps& m, int which) {
-  return which == 0 ? &m.out[0] : which == 1 ? &m.out[1] : &m.out[2];
-}
-__device__ __forceinline__ const CUtensorMap* hat_map(const QkvOutMaps& m, int which) {
-  return which == 0 ? &m.hat[0] : &m.hat[1];
-}
-
-// Where a warp's 32 staged rows go: one TMA tile store when they are 32
-// consecutive rows of one item (contig; n0 and bh0 = b H of the first row),
-// else the row-by-row stores of store_rows (row: this lane's, for head 0).
-struct RowsOut {
-  bool contig;
-  int n0, bh0;
-  uint32_t row;
-};
-// Writes out the buffers whose bit in `which` is set, after the lanes have
-// staged them: where buffer i goes comes from to(i, map, base, head, column).
-template <int D, int kBufs, typename To>
-__device__ __forceinline__ void emit_rows(uint32_t buf, unsigned which, const RowsOut& ro, uint32_t N, To to,
-                                          int lane) {
-  if (ro.contig) fence_proxy_async_smem();  // this lane's staged writes, to the TMA unit
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < kBufs; ++i) {
-    if ((which >> i) & 1u) {
-      const CUtensorMap* map;
-      uint16_t* base;
-      int h, col;
-      to(i, map, base, h, col);
-      if (!ro.contig)
-        store_rows<D>(buf + i * kStagingBytes, base, ro.row, static_cast<uint32_t>(h) * N, col, lane);
-      else if (lane == 0)
-        tma_store_3d_s(map, buf + i * kStagingBytes, col, ro.n0, ro.bh0 + h);
-    }
+// The pieces of columns n0 .. end - 1 for the adapters: of one of q, k and v, and
+// 64, 128 or 256 columns, so that two CTAs' halves of a piece are whole boxes of
+// the up weights' rows, or a box's first rows.  next() gives the next one, from
+// column c on.
+struct Pieces {
+  int hd, end, c, cols, part;
+  __device__ __forceinline__ Pieces(int H_d, int n0, int end_)
+      : hd(H_d), end(min(end_, 3 * H_d)), c(n0), cols(0), part(0) {}
+  __device__ __forceinline__ bool next() {
+    c += cols;
+    if (c >= end) return false;
+    part = c / hd;
+    const int left = min((part + 1) * hd, end) - c;
+    cols = left >= 256 ? 256 : left >= 128 ? 128 : 64;
+    return true;
   }
-  if (ro.contig && lane == 0) bulk_commit_group();
-}
-// Before a staging buffer is written again: the TMA stores have read it.
-__device__ __forceinline__ void staging_free(int lane) {
-  if (lane == 0) bulk_wait_group_read0();
-  __syncwarp();
-}
-__device__ __forceinline__ QkvStream stream_of(const QkvParams& p, int si) {
-  QkvStream s;
-  s.M = si ? p.s[1].M : p.s[0].M;
-  s.N_s = si ? p.s[1].N_s : p.s[0].N_s;
-  s.row0 = si ? p.s[1].row0 : p.s[0].row0;
-  s.tile0 = si ? p.s[1].tile0 : p.s[0].tile0;
-  s.bias = si ? p.s[1].bias : p.s[0].bias;
-  s.sx = si ? p.s[1].sx : p.s[0].sx;
-  s.sw = si ? p.s[1].sw : p.s[0].sw;
-  return s;
+};
+
+// An item of work: columns n0 .. n0 + cols - 1 of row tile mt of stream si.
+struct QkvItem {
+  int si, mt, n0, cols;
+};
+template <int kCols>
+__device__ __forceinline__ QkvItem item_at(const QkvParams& p, int t) {
+  QkvItem it;
+  int sub = 0;
+  it.cols = kCols;
+  if (t >= p.whole) {
+    sub = (t - p.whole) & ((1 << p.parts_log) - 1);
+    t = p.whole + ((t - p.whole) >> p.parts_log);
+    it.cols = kCols >> p.parts_log;
+  }
+  it.si = t >= p.s[1].tile0 ? 1 : 0;
+  t -= p.s[it.si].tile0;
+  it.mt = static_cast<int>(p.by_tiles.div(t));
+  it.n0 = (t - it.mt * p.n_tiles) * kCols + sub * it.cols;
+  return it;
 }
 
-// r of one row from its bf16 values (packed pairs; exact squares): a
-// balanced tree, built block by block (16 values, then across the D / 16
-// blocks) so that few partial sums are live at once.  Two neighbouring sums at
-// a time in packed fp32 arithmetic; the fma adds two exact squares with one
-// rounding, as an addition of them does.
-//
-// r is what is kept; rc, for q_hat / k_hat, takes one Newton step more: r (1 +
-// t / 2), t = 1 - m r^2 of order 2^-22, is the root of m to 2^-44 before its
-// rounding.
+// This lane's part of a row's sum of squares, from its bf16 values (packed
+// pairs; exact squares): a balanced tree over each block of 16 columns, and over
+// the lane's two blocks at d = 128.  Two neighbouring sums at a time in packed
+// fp32 arithmetic; the fma adds two exact squares with one rounding, as an
+// addition of them does.
 template <int D>
-__device__ __forceinline__ void row_rsqrt(const uint32_t* yb, float& r, float& rc) {
-  float blk[D / 16];
+__device__ __forceinline__ float lane_squares(const uint32_t (&yb)[D / 8]) {
+  float blk[D / 64];
 #pragma unroll
-  for (int b = 0; b < D / 16; ++b) {
+  for (int b = 0; b < D / 64; ++b) {
     uint64_t t[4];  // sums of the words (0, 1), (2, 3), (4, 5), (6, 7)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -489,163 +376,239 @@ __device__ __forceinline__ void row_rsqrt(const uint32_t* yb, float& r, float& r
     f2_split(s, s0, s1);
     blk[b] = __fadd_rn(s0, s1);
   }
-#pragma unroll
-  for (int w = D / 32; w >= 1; w >>= 1)
-#pragma unroll
-    for (int i = 0; i < w; ++i) blk[i] = __fadd_rn(blk[i], blk[i + w]);
-  const float m = __fadd_rn(__fmul_rn(blk[0], 1.f / D), kEps);
+  return D == 64 ? blk[0] : __fadd_rn(blk[0], blk[D / 64 - 1]);
+}
+
+// r of a row of d values from its sum of squares.  r is what is kept; rc, for
+// q_hat / k_hat, takes one Newton step more: r (1 + t / 2), t = 1 - m r^2 of
+// order 2^-22, is the root of m to 2^-44 before its rounding.
+template <int D>
+__device__ __forceinline__ void row_rsqrt(float sum, float& r, float& rc) {
+  const float m = __fadd_rn(__fmul_rn(sum, 1.f / D), kEps);
   r = rsqrtf(m);
   const float q = __fmul_rn(m, r);  // 1 - m r^2 = 1 - q r + (q - m r) r
   const float t = __fmaf_rn(__fmaf_rn(-m, r, q), r, __fmaf_rn(-q, r, 1.f));
   rc = __fmaf_rn(__fmul_rn(0.5f, r), t, r);
 }
 
-// 64 columns of this lane's q_hat / k_hat row, (g x) r per element, staged
-// 16 bytes at a time into its row of the staging buffer; `near` collects the
-// elements within the midpoint window.
-__device__ __forceinline__ void stage_hat_row(uint32_t buf, const uint32_t* y, uint32_t g, float r, uint32_t& near,
-                                              int lane) {
-  const uint64_t r2 = f2_make(r, r);
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    // The gains through ordered shared loads: loaded chunk by chunk, not all
-    // at once ahead of the loop.
-    const float4 ga = ld_shared_f4(g + c * 32), gb = ld_shared_f4(g + c * 32 + 16);
-    const uint64_t gv[4] = {f2_make(ga.x, ga.y), f2_make(ga.z, ga.w), f2_make(gb.x, gb.y), f2_make(gb.z, gb.w)};
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // Unpacked by other instructions than in row_rsqrt, so that the compiler does not keep the row
-      // unpacked in between (128 registers, and spills around the rare path).
-      const uint32_t yv = y[4 * c + i];
-      const float lo = __uint_as_float(__byte_perm(yv, 0u, 0x1044)), hi = __uint_as_float(__byte_perm(yv, 0u, 0x3244));
-      float z0, z1;
-      f2_split(f2_mul(f2_mul(gv[i], f2_make(lo, hi)), r2), z0, z1);
-      near_pair(z0, z1, near);
-      w[i] = pack_bf16x2(z0, z1);
-    }
-    st_shared_v4(staged(buf, lane, c), w[0], w[1], w[2], w[3]);
+// The four lanes' sums of their kRows (2 or 4) rows, joined (lanes 2 apart
+// first): lane b of the four ends with the whole sum of row b (2 rows: b / 2).
+template <int kRows>
+__device__ __forceinline__ float quad_row_sum(const float (&s)[kRows], int b) {
+  const bool up = b & 2;
+  if constexpr (kRows == 2) {
+    const float t = __fadd_rn(up ? s[1] : s[0], __shfl_xor_sync(0xffffffffu, up ? s[0] : s[1], 2));
+    return __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 1));
+  } else {
+    const float t0 = __fadd_rn(up ? s[2] : s[0], __shfl_xor_sync(0xffffffffu, up ? s[0] : s[2], 2));
+    const float t1 = __fadd_rn(up ? s[3] : s[1], __shfl_xor_sync(0xffffffffu, up ? s[1] : s[3], 2));
+    const bool odd = b & 1;
+    return __fadd_rn(odd ? t1 : t0, __shfl_xor_sync(0xffffffffu, odd ? t0 : t1, 1));
   }
 }
 
-// The warp's 32 token rows of a tile, 64 kHalves columns from taddr (this
-// lane's row) and col0 on.  bias, wscale: those columns' in shared memory; sx:
-// the row's scale (kE4m3).  The accumulator is handed back (acc_empty) once
-// its values are in registers.
+// 16 columns of a q_hat / k_hat row, (g x) r per element (y: 8 words of the
+// row, g: their gains); `near` collects the elements within the midpoint window.
+__device__ __forceinline__ void hat_cols16(const uint32_t* y, const uint64_t (&g)[8], float r, uint32_t (&w)[8],
+                                           uint32_t& near) {
+  const uint64_t r2 = f2_make(r, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // Unpacked by other instructions than in lane_squares, so that the compiler does not keep the row
+    // unpacked in between.
+    const float lo = __uint_as_float(__byte_perm(y[i], 0u, 0x1044)), hi = __uint_as_float(__byte_perm(y[i], 0u, 0x3244));
+    float z0, z1;
+    f2_split(f2_mul(f2_mul(g[i], f2_make(lo, hi)), r2), z0, z1);
+    near_pair(z0, z1, near);
+    w[i] = pack_bf16x2(z0, z1);
+  }
+}
+
+// The rare path: a row of four lanes (src the first) that has an element near a
+// bf16 midpoint, by the whole warp: each lane takes two columns of each 64 (word
+// lane % 8 of lane src + lane / 8), the squares (exact) are summed by error-free
+// additions, and elements that the fp32 arithmetic (r) puts near a midpoint are
+// rounded from the double-float r.  to: the row.
+template <int D>
+__device__ __forceinline__ void fix_row(const uint32_t (&yb)[D / 8], int src, float r, const float* g, uint16_t* to,
+                                        int lane) {
+  uint32_t w[D / 64];
+  float s = 0.f, e = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t v = __shfl_sync(0xffffffffu, yb[c * 8 + k], src + (lane >> 3));
+      if ((lane & 7) == k) w[c] = v;
+    }
+    add_sq_df(w[c], s, e);
+  }
+  warp_sum_df(s, e);
+  float rh, rl;
+  rsqrt_mean_eps_df(s, e, 1.f / D, rh, rl);
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    const int col = c * 64 + 2 * lane;
+    float f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float x = i ? bf_hi(w[c]) : bf_lo(w[c]);
+      const float gv = g[col_offset(col + i) / 4];
+      const float z = __fmul_rn(__fmul_rn(gv, x), r);
+      f[i] = near_midpoint(z) ? round_bf16_df(gv, x, rh, rl) : z;
+    }
+    *reinterpret_cast<uint32_t*>(to + col) = pack_bf16x2(f[0], f[1]);
+  }
+}
+
+// A head's columns (from col0 on) of 16 kHalves token rows, taddr their first
+// TMEM lane and column.  rows: lane i's is row i of the warp's 32 (its index
+// for head 0, kDeadRow past the stream's end), half0: the first 16 rows to take;
+// bias, wscale: the columns' in shared memory; xscale: the 32 rows' (kE4m3).
+// The accumulator is handed back (acc_empty) once its values are in registers.
+//
+// Lane 4 a + b holds rows a and a + 8 of each 16, columns 16 b .. 16 b + 15 of
+// each 64: TMEM column 4 j + b is output column 16 b + j, by the order in which
+// the weights' rows are loaded.  So four lanes write 128 consecutive bytes of a
+// row from registers.
 template <int D, int kMode, bool kPair, int kHalves>
-__device__ __forceinline__ void qkv_emit(uint32_t taddr, uint64_t* acc_empty, int col0, bool live, size_t row,
-                                         const RowsOut& ro, uint32_t stg, uint32_t bias, float sx, uint32_t wscale,
-                                         uint32_t spare, const QkvParams& p, const QkvOutMaps& om,
+__device__ __forceinline__ void qkv_emit(uint32_t taddr, uint64_t* acc_empty, int col0, uint32_t rows, int half0,
+                                         uint32_t bias, uint32_t wscale, uint32_t xscale, const QkvParams& p,
                                          const QkvBars& bars, int lane) {
-  constexpr int kHeads = kHalves * 64 / D;
-  const int hd = p.H * D;
-  const uint64_t sx2 = f2_make(sx, sx);
-  // Y = bf16(acc + bias), 16 columns at a time (packed pairs); the next 16 are on their way meanwhile.
-  uint32_t yb[kHalves * 32];
-  uint32_t acc[2][16];
-  tmem_ld16(taddr, acc[0]);
+  constexpr int kRows = 2 * kHalves, kUnits = (D / 32) * kHalves;  // of 32 columns x 16 rows
+  const int a = lane >> 2, b = lane & 3;
+  uint32_t row[kRows];
+  uint64_t sx2[kRows];
 #pragma unroll
-  for (int c16 = 0; c16 < 4 * kHalves; ++c16) {
-    tmem_wait_ld();
-    if (c16 + 1 < 4 * kHalves) {
-      tmem_ld16(taddr + (c16 + 1) * 16, acc[(c16 + 1) & 1]);
-    } else {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_to<kPair>(acc_empty);
+  for (int i = 0; i < kRows; ++i) {
+    row[i] = __shfl_sync(0xffffffffu, rows, half0 * 16 + a + 8 * i);
+    if constexpr (kMode == kE4m3) {
+      const float sx = __uint_as_float(ld_shared_u32(xscale + (half0 * 16 + a + 8 * i) * 4));
+      sx2[i] = f2_make(sx, sx);
     }
-    const uint32_t(&v)[16] = acc[c16 & 1];
+  }
+  uint32_t yb[kRows][D / 8];  // packed pairs
+  {
+    uint32_t acc[2][16];
+    tmem_ld_16x128b_x8(taddr, acc[0]);
+    float4 bv[2], sv[2];
 #pragma unroll
-    for (int e = 0; e < 16; e += 4) {
-      const float4 bv = ld_shared_f4(bias + (c16 * 16 + e) * 4);
-      uint64_t y0 = f2_make(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-      uint64_t y1 = f2_make(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-      if constexpr (kMode == kE4m3) {
-        const float4 sv = ld_shared_f4(wscale + (c16 * 16 + e) * 4);
-        y0 = f2_fma(f2_mul(y0, sx2), f2_make(sv.x, sv.y), f2_make(bv.x, bv.y));
-        y1 = f2_fma(f2_mul(y1, sx2), f2_make(sv.z, sv.w), f2_make(bv.z, bv.w));
-      } else {
-        y0 = f2_add(y0, f2_make(bv.x, bv.y));
-        y1 = f2_add(y1, f2_make(bv.z, bv.w));
+    for (int u = 0; u < kUnits; ++u) {
+      const int c32 = u / kHalves, h = u % kHalves;
+      if (h == 0) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t at = col_offset((c32 / 2) * 64 + b * 16 + (c32 % 2) * 8 + j * 4);
+          bv[j] = ld_shared_f4(bias + at);
+          if constexpr (kMode == kE4m3) sv[j] = ld_shared_f4(wscale + at);
+        }
       }
-      float a0, a1, a2, a3;
-      f2_split(y0, a0, a1);
-      f2_split(y1, a2, a3);
-      yb[c16 * 8 + e / 2] = pack_bf16x2(a0, a1);
-      yb[c16 * 8 + e / 2 + 1] = pack_bf16x2(a2, a3);
+      tmem_wait_ld();
+      if (u + 1 < kUnits) {
+        const int c1 = (u + 1) / kHalves, h1 = (u + 1) % kHalves;
+        tmem_ld_16x128b_x8(taddr + (static_cast<uint32_t>(16 * h1) << 16) + 32 * c1, acc[(u + 1) & 1]);
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_to<kPair>(acc_empty);
+      }
+      // Y = bf16(acc + bias), four columns of both rows at a time.
+      const uint32_t(&v)[16] = acc[u & 1];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint64_t y0 = f2_make(__uint_as_float(v[8 * j + i]), __uint_as_float(v[8 * j + 2 + i]));
+          uint64_t y1 = f2_make(__uint_as_float(v[8 * j + 4 + i]), __uint_as_float(v[8 * j + 6 + i]));
+          if constexpr (kMode == kE4m3) {
+            const uint64_t sx = sx2[2 * h + i];
+            y0 = f2_fma(f2_mul(y0, sx), f2_make(sv[j].x, sv[j].y), f2_make(bv[j].x, bv[j].y));
+            y1 = f2_fma(f2_mul(y1, sx), f2_make(sv[j].z, sv[j].w), f2_make(bv[j].z, bv[j].w));
+          } else {
+            y0 = f2_add(y0, f2_make(bv[j].x, bv[j].y));
+            y1 = f2_add(y1, f2_make(bv[j].z, bv[j].w));
+          }
+          float a0, a1, a2, a3;
+          f2_split(y0, a0, a1);
+          f2_split(y1, a2, a3);
+          yb[2 * h + i][c32 * 4 + 2 * j] = pack_bf16x2(a0, a1);
+          yb[2 * h + i][c32 * 4 + 2 * j + 1] = pack_bf16x2(a2, a3);
+        }
+      }
     }
   }
+  const int hd = p.H * D;
   if (col0 >= 3 * hd) return;  // past the last head
-  int which[kHeads], head[kHeads];  // 0 q, 1 k, 2 v (3: past the last head)
+  const int which = (col0 >= hd) + (col0 >= 2 * hd);  // 0 q, 1 k, 2 v
+  const size_t head_rows = static_cast<size_t>((col0 - which * hd) / D) * p.N;
+  {
+    uint16_t* raw = p.out[which] + head_rows * D + b * 16;
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    which[i] = (col0 + i * D >= hd) + (col0 + i * D >= 2 * hd) + (col0 + i * D >= 3 * hd);
-    head[i] = (col0 + i * D - which[i] * hd) / D;
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        if (row[i] != kDeadRow)
+          store_cols16(raw + static_cast<size_t>(row[i]) * D + c * 64, yb[i] + c * 8, kPair || p.wide);
   }
-  auto part = [&](int i) { return D == 64 ? which[i < kHeads ? i : 0] : which[0]; };  // of half i
-  auto to_raw = [&](int i, const CUtensorMap*& map, uint16_t*& base, int& h, int& col) {
-    map = out_map(om, part(i));
-    base = out_of(p, part(i));
-    h = head[D == 64 ? i : 0];
-    col = D == 64 ? 0 : i * 64;
-  };
-  auto to_hat = [&](int i, const CUtensorMap*& map, uint16_t*& base, int& h, int& col) {
-    map = hat_map(om, part(i));
-    base = hat_of(p, part(i));
-    h = head[D == 64 ? i : 0];
-    col = D == 64 ? 0 : i * 64;
-  };
-  unsigned raw = 0, normed = 0;  // halves to be written, and those with a norm
+  if (which == 2) return;
+  float rc[kRows];
+  {
+    float s[kRows];
 #pragma unroll
-  for (int i = 0; i < kHalves; ++i) {
-    raw |= part(i) < 3 ? 1u << i : 0u;
-    normed |= part(i) < 2 ? 1u << i : 0u;
+    for (int i = 0; i < kRows; ++i) s[i] = lane_squares<D>(yb[i]);
+    float r, mine;
+    row_rsqrt<D>(quad_row_sum<kRows>(s, b), r, mine);
+    constexpr int kLanesRow = 4 / kRows;  // that hold a row's r
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) rc[i] = __shfl_sync(0xffffffffu, mine, (lane & 28) + kLanesRow * i);
+    const uint32_t own = __shfl_sync(0xffffffffu, rows, half0 * 16 + a + 8 * (b / kLanesRow));
+    if (b % kLanesRow == 0 && own != kDeadRow) p.r[which][head_rows + own] = r;
   }
-  staging_free(lane);
+  const float* g = which == 0 ? bars.gq : bars.gk;
+  uint16_t* hat = p.hat[which] + head_rows * D;
+  uint32_t near[kRows];
 #pragma unroll
-  for (int i = 0; i < kHalves; ++i) stage_row(stg + i * kStagingBytes, yb + i * 32, lane);
-  emit_rows<D, kHalves>(stg, raw, ro, p.N, to_raw, lane);
-  if (normed == 0) {
-    __syncwarp();
-    return;
-  }
-  float r[kHeads], rc[kHeads];
-  const float* g[kHeads];
+  for (int i = 0; i < kRows; ++i) near[i] = kNoneNear;
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    row_rsqrt<D>(yb + i * (D / 2), r[i], rc[i]);
-    g[i] = which[i] == 0 ? bars.gq : bars.gk;
-  }
-  staging_free(lane);  // (and, after row-by-row stores, their reads: a barrier)
-  unsigned todo[kHeads];
+  for (int c = 0; c < D / 64; ++c) {
+    uint64_t gv[8];
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    uint32_t near = kNoneNear;
-    if (which[i] < 2) {
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j)
-        stage_hat_row(stg + (i + j) * kStagingBytes, yb + (i * D / 64 + j) * 32, smem_u32(g[i] + j * 64), rc[i], near,
-                      lane);
-      if (live) r_of(p, which[i])[row + static_cast<size_t>(head[i]) * p.N] = r[i];
+    for (int j = 0; j < 4; ++j) {
+      const float4 f = ld_shared_f4(smem_u32(g) + col_offset(c * 64 + b * 16 + j * 4));
+      gv[2 * j] = f2_make(f.x, f.y);
+      gv[2 * j + 1] = f2_make(f.z, f.w);
     }
-    todo[i] = __ballot_sync(0xffffffffu, any_near(near) && live);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      uint32_t w[8];
+      hat_cols16(yb[i] + c * 8, gv, rc[i], w, near[i]);
+      if (row[i] != kDeadRow) store_cols16(hat + static_cast<size_t>(row[i]) * D + c * 64 + b * 16, w, kPair || p.wide);
+    }
   }
-  unsigned any = todo[0];
-  if constexpr (kHeads == 2) any |= todo[1];
+  unsigned todo[kRows], any = 0;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    todo[i] = __ballot_sync(0xffffffffu, any_near(near[i]) && row[i] != kDeadRow);
+    any |= todo[i];
+  }
   if (any) {
-    __syncwarp();
-    fix_staged_rows<D, kHeads>(todo, yb, spare, stg, rc, g, lane);
+    __syncwarp();  // the rows' stores come before those of fix_row
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      while (todo[i]) {
+        const int src = (__ffs(todo[i]) - 1) & ~3;
+        todo[i] &= ~(15u << src);
+        const uint32_t to = __shfl_sync(0xffffffffu, row[i], src);
+        fix_row<D>(yb[i], src, __shfl_sync(0xffffffffu, rc[i], src), g, hat + static_cast<size_t>(to) * D, lane);
+      }
   }
-  emit_rows<D, kHalves>(stg, normed, ro, p.N, to_hat, lane);
-  __syncwarp();
 }
 
 template <int D, int kMode, bool kPair>
 __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
     qkv_norm_kernel(const __grid_constant__ CUtensorMap map_x0, const __grid_constant__ CUtensorMap map_w0,
                     const __grid_constant__ CUtensorMap map_x1, const __grid_constant__ CUtensorMap map_w1,
-                    const __grid_constant__ QkvOutMaps om, const __grid_constant__ QkvLoraMaps lm,
-                    const __grid_constant__ QkvParams p, const float* __restrict__ gq,
+                    const __grid_constant__ QkvLoraMaps lm, const __grid_constant__ QkvParams p, const float* __restrict__ gq,
                     const float* __restrict__ gk, uint32_t* dev_err) {
   using Cfg = QkvCfg<D, kMode, kPair>;
   constexpr int kStages = Cfg::kStages, kCtas = Cfg::kCtas, kCols = Cfg::kCols;
@@ -658,7 +621,7 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int* ab = &bars.abort;
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;  // within the pair
-  const int first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
+  const int first_item = blockIdx.x / kCtas, item_step = gridDim.x / kCtas;
 
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
@@ -683,8 +646,8 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
   // before itself is complete: only the loads of U wait for it (the producer).
   if (kMode != kLora || !p.after_down) griddep_wait();
   for (int i = threadIdx.x; i < D; i += blockDim.x) {
-    bars.gq[i] = gq[i];
-    bars.gk[i] = gk[i];
+    bars.gq[col_offset(i) / 4] = gq[i];
+    bars.gk[col_offset(i) / 4] = gk[i];
   }
   tc_fence_before();
   __syncthreads();
@@ -694,7 +657,7 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
   const int ksteps = (p.C + kStepK - 1) / kStepK;
 
   if (warp >= Cfg::kEpiWarps) {
-  if constexpr (kPair) setmaxnreg_dec<QkvRegs<D>::kOther>();
+  if constexpr (kPair) setmaxnreg_dec<QkvRegs::kOther>();
   if (warp == kWarpProd) {
     if (lane == 0) {
       tma_prefetch_desc(&map_x0);
@@ -703,10 +666,9 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
       tma_prefetch_desc(&map_w1);
       int it = 0;
       bool ok = true;
-      for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
-        const int si = t >= p.s[1].tile0 ? 1 : 0;
-        const int tl = t - (si ? p.s[1].tile0 : p.s[0].tile0);
-        const int mt = tl / p.n_tiles, nt = tl - mt * p.n_tiles;
+      for (int t = first_item; ok && t < p.items; t += item_step) {
+        const auto [si, mt, n0, cols] = item_at<kCols>(p, t);
+        const int w0 = n0 + rank * (cols / kCtas);  // this CTA's part of the weight rows
         const CUtensorMap* mx = si ? &map_x1 : &map_x0;
         const CUtensorMap* mw = si ? &map_w1 : &map_w0;
         for (int kb = 0; kb < ksteps; ++kb) {
@@ -716,17 +678,15 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
           const uint32_t full = pair_bar<kPair>(&bars.full[s]);
           if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], kCtas * Cfg::kStageBytes);
           tma_load_2d_to<kPair>(st, mx, full, kb * kStepK, mt * kRows + rank * kBM);
-          tma_load_2d_to<kPair>(st + kATile, mw, full, kb * kStepK, nt * kCols + rank * Cfg::kBRows);
+          tma_load_4d_to<kPair>(st + kATile, mw, full, kb * kStepK, 0, (w0 & 63) >> 2, w0 >> 6);
           ++it;
         }
         if constexpr (kMode == kLora) {
-          if (!ok || !(si ? p.lora[1] : p.lora[0])) continue;
-          const int N_s = si ? p.s[1].N_s : p.s[0].N_s, M = si ? p.s[1].M : p.s[0].M;
-          const int m0 = mt * kRows, m1 = min(m0 + kRows, M), n0 = nt * kCols, hd = p.H * D;
-          const CUtensorMap* mu = si ? &lm.u[1] : &lm.u[0];
-          const CUtensorMap* mup = si ? &lm.up[1] : &lm.up[0];
-          int p0, p1, used = 0;  // bytes of the open stage (0: none open)
-          parts_of(n0, kCols, hd, p0, p1);
+          if (!ok || !p.lora[si]) continue;
+          const int N_s = p.s[si].N_s, M = p.s[si].M;
+          const int m0 = mt * kRows, m1 = min(m0 + kRows, M);
+          const CUtensorMap* mu = &lm.u[si];
+          int used = 0;  // bytes of the open stage (0: none open)
           bool waited = false;
           // The stage is closed by its one arrival; until then each group's bytes are added to what it expects.
           auto close = [&] {
@@ -734,8 +694,9 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
             used = 0;
             ++it;
           };
-          for (int part = p0; ok && part <= p1; ++part) {
-            const int c0 = max(part * hd, n0), width = min((part + 1) * hd, n0 + kCols) - c0;
+          Pieces pc(p.H * D, n0, n0 + cols);
+          while (ok && pc.next()) {
+            const int up0 = pc.c + rank * (pc.cols / kCtas);
             for (int kc = 0; ok && kc < p.rank_units; ++kc) {
               Runs runs(p, N_s, m0, m1);
               bool more = runs.next();
@@ -749,14 +710,14 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
                 }
                 const uint32_t full = pair_bar<kPair>(&bars.full[s]);
                 uint8_t* st = sm + s * Cfg::kStageBytes;
-                const int col = (part * p.rank_units + kc) * 16;
+                const int col = (pc.part * p.rank_units + kc) * 16;
                 if (rank == 0) mbar_expect_tx(&bars.full[s], kCtas * 2 * Cfg::kUnitA);
                 tma_load_2d_to<kPair>(st + used, mu, full, col, m0 + rank * kBM);
                 tma_load_2d_to<kPair>(st + used + Cfg::kUnitA, mu, full, col + 3 * 16 * p.rank_units, m0 + rank * kBM);
                 used += 2 * Cfg::kUnitA;
                 do {
                   if (rank == 0) mbar_expect_tx(&bars.full[s], kCtas * Cfg::kUnitB);
-                  tma_load_3d_to<kPair>(st + used, mup, full, kc * 16, c0 + rank * (width / kCtas), runs.adapter);
+                  tma_load_5d_to<kPair>(st + used, &lm.up[si], full, kc * 16, 0, (up0 & 63) >> 2, up0 >> 6, runs.adapter);
                   used += Cfg::kUnitB;
                   more = runs.next();
                 } while (more && used + Cfg::kUnitB <= Cfg::kStageBytes);
@@ -776,11 +737,12 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
     }
   } else if (warp == kWarpIssue) {
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc =
-          kMode == kE4m3 ? idesc_e4m3_f32(kRows, kCols) : idesc_bf16_f32(kRows, kCols, false, false);
       int it = 0, lt = 0;
       bool ok = true;
-      for (int t = first_tile; ok && t < p.tiles; t += tile_step, ++lt) {
+      for (int t = first_item; ok && t < p.items; t += item_step, ++lt) {
+        const auto [si, mt, n0, cols] = item_at<kCols>(p, t);
+        const uint32_t idesc =
+            kMode == kE4m3 ? idesc_e4m3_f32(kRows, cols) : idesc_bf16_f32(kRows, cols, false, false);
         const int abuf = lt & 1;
         if (lt >= 2 && !(ok = mbar_wait(&bars.acc_empty[abuf], ((lt >> 1) - 1) & 1, ab, dev_err))) break;
         tc_fence_after();
@@ -802,22 +764,18 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
           umma_commit_to<kPair>(&bars.empty[s]);
         }
         if constexpr (kMode == kLora) {
-          const int si = t >= p.s[1].tile0 ? 1 : 0;
-          if (ok && (si ? p.lora[1] : p.lora[0])) {
-            const int tl = t - (si ? p.s[1].tile0 : p.s[0].tile0);
-            const int mt = tl / p.n_tiles, n0 = (tl - mt * p.n_tiles) * kCols;
-            const int N_s = si ? p.s[1].N_s : p.s[0].N_s, M = si ? p.s[1].M : p.s[0].M;
-            const int m0 = mt * kRows, m1 = min(m0 + kRows, M), hd = p.H * D;
-            int p0, p1, used = 0;  // as the producer counts
-            parts_of(n0, kCols, hd, p0, p1);
+          if (ok && p.lora[si]) {
+            const int N_s = p.s[si].N_s, M = p.s[si].M;
+            const int m0 = mt * kRows, m1 = min(m0 + kRows, M);
+            int used = 0;  // as the producer counts
             auto close = [&] {
               umma_commit_to<kPair>(&bars.empty[it % kStages]);
               used = 0;
               ++it;
             };
-            for (int part = p0; ok && part <= p1; ++part) {
-              const int c0 = max(part * hd, n0) - n0, c1 = min((part + 1) * hd, n0 + kCols) - n0;
-              const uint32_t desc = idesc_bf16_f32(kRows, c1 - c0, false, false);
+            Pieces pc(p.H * D, n0, n0 + cols);
+            while (ok && pc.next()) {
+              const uint32_t desc = idesc_bf16_f32(kRows, pc.cols, false, false), at = acc + (pc.c - n0);
               for (int kc = 0; ok && kc < p.rank_units; ++kc) {
                 Runs runs(p, N_s, m0, m1);
                 bool more = runs.next();
@@ -837,8 +795,8 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
 #pragma unroll
                     for (int w = 0; w < 4 * kCtas; ++w) off[w] = ~rows_of_word(runs.lo, runs.hi, w);
                     const uint64_t up = sdesc_sw32_kmajor(st + used, 256);
-                    umma_bf16_ss_lanes(acc + c0, u_hi, up, desc, off, 1u);
-                    umma_bf16_ss_lanes(acc + c0, u_lo, up, desc, off, 1u);
+                    umma_bf16_ss_lanes(at, u_hi, up, desc, off, 1u);
+                    umma_bf16_ss_lanes(at, u_lo, up, desc, off, 1u);
                     used += Cfg::kUnitB;
                     more = runs.next();
                   } while (more && used + Cfg::kUnitB <= Cfg::kStageBytes);
@@ -856,39 +814,33 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
     }
   }
   } else {
-    if constexpr (kPair) setmaxnreg_inc<QkvRegs<D>::kEpi>();
-    // Warp w: the TMEM lanes of warp w % 4, and kWarpCols columns of the tile from kWarpCols (w / 4) on.
-    const int lg = warp & 3, wcol = (warp >> 2) * Cfg::kWarpCols;
-    const uint32_t stg = smem_u32(sm + Cfg::kOffStaging + warp * Cfg::kStaging);
-    const uint32_t bias_w = smem_u32(sm + Cfg::kOffBias + warp * 2 * Cfg::kBiasBytes);
-    const uint32_t wscale_w = smem_u32(sm + Cfg::kOffScale + warp * 2 * Cfg::kBiasBytes);  // kE4m3
-    const uint32_t xscale_w = smem_u32(sm + Cfg::kOffXScale + warp * 256);                 // kE4m3
-    const uint32_t spare_w = smem_u32(sm + Cfg::kOffSpare + warp * Cfg::kSpareBytes);
-    const uint32_t lane_base = static_cast<uint32_t>(lg * 32) << 16;
+    if constexpr (kPair) setmaxnreg_inc<QkvRegs::kEpi>();
+    // Warps of a group share the tile's columns from wcol on: each takes the TMEM lanes of warp w % 4, all 32
+    // or one half of them.
+    const int lg = warp & 3, group = warp / Cfg::kGroupWarps, wcol = group * D;
+    const int half0 = Cfg::kHalves == 2 ? 0 : (warp >> 2) & 1;
+    const uint32_t bias_s = smem_u32(sm + Cfg::kOffBias) + wcol * 5;
+    const uint32_t wscale_s = smem_u32(sm + Cfg::kOffScale) + wcol * 5;      // kE4m3
+    const uint32_t xscale_w = smem_u32(sm + Cfg::kOffXScale + warp * 256);  // kE4m3
     const int hd3 = 3 * p.H * D;
-    // What the epilogue of a tile reads from global memory, copied to this warp's slices one tile ahead
-    // (its latency, some 700 cycles each, is not met): the bias of the warp's columns (zero past 3 H d, or
-    // without a bias); kE4m3: their scales, and those of its rows.
+    // What the epilogue of a tile reads from global memory, copied to shared memory one tile ahead (its
+    // latency, some 700 cycles each, is not met): the bias of the group's columns (zero past 3 H d, or without
+    // a bias) by its first warp; kE4m3: their scales by its second, and by each warp those of its rows.
     auto fetch = [&](int t, int buf) {
-      const QkvStream S = stream_of(p, t >= p.s[1].tile0 ? 1 : 0);
-      const int tl = t - S.tile0, mt = static_cast<int>(p.by_tiles.div(tl));
-      const int col = (tl - mt * p.n_tiles) * kCols + wcol + lane * 4;
-      if (lane * 4 < Cfg::kWarpCols) {
-        const uint32_t to = bias_w + buf * Cfg::kBiasBytes + lane * 16;
-        if (S.bias && col < hd3)
-          cp_async16(to, S.bias + col);
+      const QkvItem it = item_at<kCols>(p, t);
+      const QkvStream& S = p.s[it.si];
+      const int col = it.n0 + wcol + lane * 4;
+      auto cols = [&](uint32_t to, const float* from) {
+        if (lane * 4 >= D) return;
+        if (from && col < hd3)
+          cp_async16(to + buf * Cfg::kColBytes + col_offset(lane * 4), from + col);
         else
-          st_shared_v4(to, 0u, 0u, 0u, 0u);
-        if constexpr (kMode == kE4m3) {
-          const uint32_t ws = wscale_w + buf * Cfg::kBiasBytes + lane * 16;
-          if (col < hd3)
-            cp_async16(ws, S.sw + col);
-          else
-            st_shared_v4(ws, 0u, 0u, 0u, 0u);
-        }
-      }
+          st_shared_v4(to + buf * Cfg::kColBytes + col_offset(lane * 4), 0u, 0u, 0u, 0u);
+      };
+      if (warp % Cfg::kGroupWarps == 0) cols(bias_s, S.bias);
       if constexpr (kMode == kE4m3) {
-        const int m = mt * kRows + rank * kBM + lg * 32 + lane;
+        if (warp % Cfg::kGroupWarps == 1) cols(wscale_s, S.sw);
+        const int m = it.mt * kRows + rank * kBM + lg * 32 + lane;
         const uint32_t xs = xscale_w + buf * 128 + lane * 4;
         if (m < S.M)
           cp_async4(xs, S.sx + m);
@@ -898,42 +850,34 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
       cp_async_commit();
     };
     int lt = 0;
-    if (first_tile < p.tiles) fetch(first_tile, 0);
-    for (int t = first_tile; t < p.tiles; t += tile_step, ++lt) {
+    if (first_item < p.items) fetch(first_item, 0);
+    for (int t = first_item; t < p.items; t += item_step, ++lt) {
       const int abuf = lt & 1;
-      const QkvStream S = stream_of(p, t >= p.s[1].tile0 ? 1 : 0);
-      const int tl = t - S.tile0;
-      const int mt = static_cast<int>(p.by_tiles.div(tl)), nt = tl - mt * p.n_tiles;
-      const int col0 = nt * kCols + wcol;  // the warp's first column in Y
-      const int m = mt * kRows + rank * kBM + lg * 32 + lane;
-      const bool live = m < S.M;
-      const int bi = live ? m / S.N_s : 0;
-      const int n = live ? S.row0 + (m - bi * S.N_s) : 0;
-      const size_t row = static_cast<size_t>(bi) * p.H * p.N + n;  // < B H N < 2^31 / d
-      const uint32_t row32 = live ? static_cast<uint32_t>(row) : kDeadRow;
-      RowsOut ro;
-      {
-        const uint32_t first = __shfl_sync(0xffffffffu, row32, 0), last = __shfl_sync(0xffffffffu, row32, 31);
-        // Of one item: with one head and one stream the next item's rows follow on.
-        const int b0 = __shfl_sync(0xffffffffu, bi, 0), b31 = __shfl_sync(0xffffffffu, bi, 31);
-        ro.contig = first != kDeadRow && last != kDeadRow && last - first == 31u && b0 == b31;
-        ro.n0 = __shfl_sync(0xffffffffu, n, 0);
-        ro.bh0 = b0 * p.H;
-        ro.row = row32;
+      const QkvItem it = item_at<kCols>(p, t);
+      const QkvStream& S = p.s[it.si];
+      const int m = it.mt * kRows + rank * kBM + lg * 32 + lane;
+      uint32_t row = kDeadRow;
+      if (m < S.M) {
+        const int bi = m / S.N_s;
+        // < B H N < 2^31 / d
+        row = static_cast<uint32_t>(bi) * p.H * p.N + S.row0 + (m - bi * S.N_s);
       }
       cp_async_wait_all();
-      const bool ok = mbar_wait(&bars.acc_full[abuf], (lt >> 1) & 1, ab, dev_err);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      __syncwarp();
+      bool ok = mbar_wait(&bars.acc_full[abuf], (lt >> 1) & 1, ab, dev_err);
+      // The group's copies have landed, it is done with the other buffer, and it goes on as one.
+      ok = barrier_all(1 + group, 32 * Cfg::kGroupWarps, ok);
+      if (!ok) break;
       tc_fence_after();
-      if (t + tile_step < p.tiles) fetch(t + tile_step, abuf ^ 1);
-      float sx = 0.f;
-      if constexpr (kMode == kE4m3) sx = __uint_as_float(ld_shared_u32(xscale_w + abuf * 128 + lane * 4));
-      qkv_emit<D, kMode, kPair, Cfg::kWarpCols / 64>(tmem + lane_base + abuf * kCols + wcol, &bars.acc_empty[abuf],
-                                                     col0, live, row, ro, stg, bias_w + abuf * Cfg::kBiasBytes, sx,
-                                                     wscale_w + abuf * Cfg::kBiasBytes, spare_w, p, om, bars, lane);
+      if (t + item_step < p.items) fetch(t + item_step, abuf ^ 1);
+      if (wcol >= it.cols) {  // a part without this group's columns
+        if (lane == 0) mbar_arrive_to<kPair>(&bars.acc_empty[abuf]);
+        continue;
+      }
+      qkv_emit<D, kMode, kPair, Cfg::kHalves>(
+          tmem + (static_cast<uint32_t>(lg * 32 + half0 * 16) << 16) + abuf * kCols + wcol, &bars.acc_empty[abuf],
+          it.n0 + wcol, row, half0, bias_s + abuf * Cfg::kColBytes, wscale_s + abuf * Cfg::kColBytes,
+          xscale_w + abuf * 128, p, bars, lane);
     }
-    if (lane == 0) bulk_wait_group0();  // this warp's tile stores are complete
   }
   tc_fence_before();
   __syncthreads();
@@ -981,9 +925,8 @@ cudaError_t resident_pairs(K kernel, int threads, int smem, int regs, std::atomi
 }
 
 template <int D, int kMode, bool kPair>
-cudaError_t launch_qkv_kernel(const CUtensorMap (&maps)[4], const QkvOutMaps& om, const QkvLoraMaps& lm,
-                              const QkvParams& p, const float* gq, const float* gk, uint32_t* dev_err,
-                              cudaStream_t st) {
+cudaError_t launch_qkv_kernel(const CUtensorMap (&maps)[4], const QkvLoraMaps& lm, QkvParams& p, int tiles,
+                              const float* gq, const float* gk, uint32_t* dev_err, cudaStream_t st) {
   using Cfg = QkvCfg<D, kMode, kPair>;
   auto kernel = qkv_norm_kernel<D, kMode, kPair>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kDynSmem);
@@ -993,25 +936,33 @@ cudaError_t launch_qkv_kernel(const CUtensorMap (&maps)[4], const QkvOutMaps& om
   if constexpr (kPair) {
     static std::atomic<int> known[64];
     int fit = 0;
-    e = resident_pairs(kernel, Cfg::kThreads, Cfg::kDynSmem, QkvRegs<D>::kLaunch, known, 64, &fit);
+    e = resident_pairs(kernel, Cfg::kThreads, Cfg::kDynSmem, QkvRegs::kLaunch, known, 64, &fit);
     if (e != cudaSuccess) return e;
     if (fit < groups) groups = fit;
   }
-  const int grid = (p.tiles < groups ? p.tiles : groups) * Cfg::kCtas;
+  // The tiles left over once all pairs have taken as many: in parts of a head (d = 64) or of two, when there
+  // are enough pairs for each to take a part at most.  In parts / whole (bf16, d = 64, C = 768): 81 tiles on 76
+  // pairs 14.5 / 16.6 us, 108 tiles 15.5 / 17.0, 621 tiles 51.3 / 53.0; by one head / by two: 14.5 / 15.1 (81).
+  const int left = tiles % groups;
+  p.whole = tiles;
+  p.parts_log = 0;
+  if (kPair && left > 0) {
+    for (int l = D == 64 ? 2 : 1; l > 0 && p.parts_log == 0; --l)
+      if ((left << l) <= groups) p.parts_log = l;
+    if (p.parts_log > 0) p.whole = tiles - left;
+  }
+  p.items = p.whole + ((tiles - p.whole) << p.parts_log);
+  const int grid = (p.items < groups ? p.items : groups) * Cfg::kCtas;
   return launch_pdl_cluster(kernel, Cfg::kCtas, dim3(grid), dim3(Cfg::kThreads), Cfg::kDynSmem, st, maps[0], maps[1],
-                            maps[2], maps[3], om, lm, p, gq, gk, dev_err);
+                            maps[2], maps[3], lm, p, gq, gk, dev_err);
 }
 
 }  // namespace
 
 // One form of the projection (each is compiled in a file of its own).
 template <int kMode>
-cudaError_t launch_qkv_form(const CUtensorMap (&maps)[4], const CUtensorMap (&out_maps)[5], const QkvLaunch& a,
-                            uint32_t* dev_err, cudaStream_t st, const LoraLaunch* lora,
-                            const CUtensorMap* lora_maps) {
-  QkvOutMaps om;
-  for (int i = 0; i < 3; ++i) om.out[i] = out_maps[i];
-  for (int i = 0; i < 2; ++i) om.hat[i] = out_maps[3 + i];
+cudaError_t launch_qkv_form(const CUtensorMap (&maps)[4], const QkvLaunch& a, uint32_t* dev_err, cudaStream_t st,
+                            const LoraLaunch* lora, const CUtensorMap* lora_maps) {
   QkvLoraMaps lm;
   for (int i = 0; i < 2; ++i) {
     lm.u[i] = lora ? lora_maps[i] : maps[0];
@@ -1037,22 +988,22 @@ cudaError_t launch_qkv_form(const CUtensorMap (&maps)[4], const CUtensorMap (&ou
     tile0 += ((a.M[i] + rows - 1) / rows) * p.n_tiles;
     p.lora[i] = lora && lora->on[i];
   }
-  p.tiles = tile0;
   for (int i = 0; i < 3; ++i) p.out[i] = a.out[i];
   for (int i = 0; i < 2; ++i) {
     p.hat[i] = a.hat[i];
     p.r[i] = a.r[i];
   }
+  p.wide = a.wide;
   p.index = lora ? lora->index : nullptr;
   p.n_adapters = lora ? lora->n_adapters : 0;
   p.after_down = p.lora[0] || p.lora[1];
   p.rank_units = lora ? (lora->rank + 15) / 16 : 0;
-  if (p.tiles == 0) return cudaSuccess;
+  if (tile0 == 0) return cudaSuccess;
   if (a.d == 64)
-    return pair ? launch_qkv_kernel<64, kMode, true>(maps, om, lm, p, a.gq, a.gk, dev_err, st)
-                : launch_qkv_kernel<64, kMode, false>(maps, om, lm, p, a.gq, a.gk, dev_err, st);
-  return pair ? launch_qkv_kernel<128, kMode, true>(maps, om, lm, p, a.gq, a.gk, dev_err, st)
-              : launch_qkv_kernel<128, kMode, false>(maps, om, lm, p, a.gq, a.gk, dev_err, st);
+    return pair ? launch_qkv_kernel<64, kMode, true>(maps, lm, p, tile0, a.gq, a.gk, dev_err, st)
+                : launch_qkv_kernel<64, kMode, false>(maps, lm, p, tile0, a.gq, a.gk, dev_err, st);
+  return pair ? launch_qkv_kernel<128, kMode, true>(maps, lm, p, tile0, a.gq, a.gk, dev_err, st)
+              : launch_qkv_kernel<128, kMode, false>(maps, lm, p, tile0, a.gq, a.gk, dev_err, st);
 }
 
 }  // namespace jattn

@@ -350,6 +350,52 @@ def test_forms_under_a_cap_on_the_ctas(ja, sms):
 
 
 @gpu
+@pytest.mark.parametrize("H,d", [(5, 64), (3, 128)])
+@pytest.mark.parametrize("sms", [4, 6, 11, 18, 26, 151])
+def test_parts_of_the_last_tiles(ja, H, d, sms):
+    """However the last tiles are shared out (whole, by two heads or by one), the same bits: tiles over the
+    borders between q, k and v (H no multiple of the heads of a tile) and adapters of several items included."""
+    C = 72 if d == 64 else 80
+    t8 = fp8_inputs(3, H, 500, 77, d, 80, True, 63)
+    tl = lora_inputs(7, H, 220, 33, d, C, 24, 3, True, 64)
+    tl["index"] = torch.tensor([2, 2, 0, -1, 1, 1, 0], dtype=torch.int32, device="cuda")
+    want8, want = fp8_call(ja, t8, H), lora_call(ja, tl, H)
+    check_lora(ja, tl, want, H, d, 24)
+    ja.jattn_set_sm_limit(sms)
+    try:
+        got = fp8_call(ja, t8, H)[:3] + lora_call(ja, tl, H)[:3]
+        ok(ja)
+    finally:
+        ja.jattn_set_sm_limit(0)
+    for a, b in zip(got, want8[:3] + want[:3]):
+        assert torch.equal(a, b)
+
+
+@gpu
+@pytest.mark.parametrize("N_img", [40, 1100])
+def test_outputs_at_16_byte_boundaries(ja, N_img):
+    """Outputs that start at a multiple of 16 bytes, not of 32, for few and for many tokens."""
+    B, H, N_txt, d, C = 2, 4, 9, 64, 128
+    t = lora_inputs(B, H, N_img, N_txt, d, C, 16, 2, True, 65)
+    want = lora_call(ja, t, H)
+    n = want[0].numel()
+    buf = torch.full((3, n + 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q, k, v = (b[8:8 + n].view(want[0].shape) for b in buf)
+    assert q.data_ptr() % 32 == 16
+    saved = torch.empty_like(want[3])
+    work = torch.empty(ja.jattn_qkv_norm_lora_bytes(B, H, N_img, N_txt, d, 16), dtype=torch.uint8, device="cuda")
+    ja.jattn_qkv_norm_lora(t["x_img"], t["w_img"], t["b_img"], t["x_txt"], t["w_txt"], t["b_txt"], t["gq"], t["gk"],
+                           t["down_img"], t["up_img"], t["down_txt"], t["up_txt"], t["scale"], t["index"], 2, 16,
+                           B, H, N_img, N_txt, d, C, q, k, v, saved, work)
+    ok(ja)
+    for a, b in zip((q, k, v), want[:3]):
+        assert torch.equal(a, b)
+    for a, b in zip(saved_parts(saved, q), saved_parts(want[3], q)):
+        assert torch.equal(a, b)
+    assert buf[:, :8].isnan().all() and buf[:, 8 + n:].isnan().all()
+
+
+@gpu
 def test_run_from_the_residual_stream_to_the_gradients(ja):
     """A block's attention path as a program runs it: the residual's addition and norm, the projection
     (8-bit, and with adapters), the attention, its backward, and the norm's backward; eager, and captured
