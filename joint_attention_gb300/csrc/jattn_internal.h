@@ -200,7 +200,7 @@ struct LoraLaunch {
   const int* index;    // [B] the items' adapters
   const float* scale;  // [n_adapters]
   bool on[2];          // whether a stream has adapters (and rows)
-  uint16_t* u[2];      // scratch [M, 2 * 3 * 16 ceil(rank / 16)]
+  uint16_t* u[2];      // scratch [M, 3 ceil(rank / 16), 2, 16]
 };
 // lora_maps (with lora): encode_unit_map maps of both streams' U, then
 // encode_up_map maps of their up weights (boxes of kQkvWRows rows); a stream
@@ -229,7 +229,7 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t c
 // Weights [rows, cols], rows a multiple of 64, in that order: a 4-D map
 // (cols, b, j, g) with box_rows (a multiple of 64) rows a box, otherwise as above.
 bool encode_heads_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool e4m3);
-// (16, 128) boxes of a [rows, cols] bf16 matrix, 32-byte swizzle.
+// (32, 128) boxes of a [rows, cols] bf16 matrix, 64-byte swizzle.
 bool encode_unit_map(CUtensorMap* map, const void* base, int64_t rows, int cols);
 // n adapters' up weights [rows, rank] in that order: a 5-D map (rank, b, j, g,
 // adapter), 16 of the rank and box_rows rows a box, 32-byte swizzle.

@@ -18,8 +18,8 @@ namespace {
 //
 // What bounds it: its own start and end.  At 512 px (16 items, rank 16) it reads
 // 27 MB in 13 us under ncu, with 4 stages of the ring as with 12; the projection
-// starts behind its first wait, so that the call takes 72 us where the
-// projection alone takes 57 and, with no item having an adapter, 64.
+// starts behind its first wait, so that the call takes 67 us where the
+// projection alone takes 52 and, with no item having an adapter, 56.
 constexpr int kDownThreads = 192;
 constexpr int kDownK = 64;
 constexpr int kDownMaxStages = 6;
@@ -27,7 +27,7 @@ constexpr int kDownSmem = 200 * 1024;
 
 struct DownStream {
   int N_s, blocks, cta0;  // rows per item, its 128-row blocks, the stream's first CTA
-  uint16_t* u;            // [B N_s, 2 * 3 * 16 rank_units]: the high terms, then the low terms
+  uint16_t* u;            // [B N_s, 3 rank_units, 2, 16]: 16 high terms, then their low terms
 };
 struct DownParams {
   DownStream s[2];
@@ -144,12 +144,11 @@ __global__ void __launch_bounds__(kDownThreads, 1)
           lo[i] = pack_bf16x2(a - bf_lo(hi[i]), b - bf_hi(hi[i]));
         }
         if (n < N_s) {
-          uint4* o = reinterpret_cast<uint4*>(u + c * 16);
+          uint4* o = reinterpret_cast<uint4*>(u + c * 32);
           o[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           o[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-          o = reinterpret_cast<uint4*>(u + 3 * r16 + c * 16);
-          o[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          o[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+          o[2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          o[3] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
         }
       }
       tc_fence_before();

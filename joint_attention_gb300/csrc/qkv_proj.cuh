@@ -47,16 +47,17 @@
 // Heads past 3 H in the last column tile, and token rows past the stream's
 // end in its last row tile, read the TMA's zero fill and are not stored.
 //
-// What bounds it (512 px, C = 768, 12 heads of 64; 51.5 us from bf16, 38.9 us
-// from e4m3; 768 px, C = 2048, 16 heads of 128; 141 and 86.5 us): the epilogue
-// beside the products.  From e4m3 at 768 px the products alone take 66 us (the
-// rate of cuBLAS), the epilogue with one K step 50, without its stores 41; at
-// 512 px 24, 34 and 29: there the epilogue's instructions count (some 930 a
-// warp for 32 rows of 64 columns).  What the epilogue takes of shared memory's
-// bandwidth the products lack: rows staged there and written out by TMA stores,
-// with the ring at 128 KB for it instead of 192, took 57 and 38.8, 151 and 92
-// us; the gains, biases and scales read without a gap every 16 columns (two-way
-// bank conflicts), and anew for each row, 5 us more at 512 px.
+// What bounds it (512 px, C = 768, 12 heads of 64; 52 us from bf16, 39 us from
+// e4m3; 768 px, C = 2048, 16 heads of 128; 141 and 87 us): the epilogue beside
+// the products.  The products alone take 38, 24, 120 and 66 us (the rate of
+// cuBLAS), the epilogue with one K step 30, 34, 43 and 50, of which 5 to 10 for
+// the stores.  From e4m3 at 512 px the epilogue's instructions count (some 930 a
+// warp for 32 rows of 64 columns); else the loads' latency beside the stores (a
+// ring of 128 KB 56 and 147 us from bf16, of 160 KB 52.7 and 141) and shared
+// memory's bandwidth, of which the products take most: rows staged there and
+// written out by TMA stores, with 128 KB left for the ring, took 57, 39, 151 and
+// 92 us; gains, biases and scales read without a gap every 16 columns (two-way
+// bank conflicts), and anew for each row, 5 us more from e4m3 at 512 px.
 //
 // The same kernel takes two other forms of the products (template kMode):
 //   kE4m3  X and W in e4m3 with fp32 scales of their rows: a K step of 128
@@ -118,6 +119,8 @@ struct QkvCfg {
   static constexpr int kCols = kQkvCols(D, kPair);       // of a tile
   static constexpr int kBRows = kQkvWRows(D, kPair);     // weight rows that a CTA loads
   static constexpr int kEpiWarps = kPair ? 16 : 8;
+  // Not with adapters, whose producer and issuer have more to keep (512 px 67.0 us without the split, 67.9 with).
+  static constexpr bool kSplitRegs = kPair && kMode != kLora;
   static constexpr int kGroupWarps = kEpiWarps * D / kCols;  // that share a head's columns
   static constexpr int kHalves = 8 / kGroupWarps;
   static constexpr int kWarpProd = kEpiWarps, kWarpIssue = kEpiWarps + 1;
@@ -132,7 +135,7 @@ struct QkvCfg {
   static constexpr int kOffXScale = kOffScale + 2 * kColBytes;
   static constexpr int kDynSmem = (kMode == kE4m3 ? kOffXScale + kEpiWarps * 2 * 128 : kOffScale) + 1024;
   // kLora: a group of operands for 16 of the rank, both terms of U, then the up weights of a run each.
-  static constexpr int kUnitA = kBM * 32, kUnitB = kBRows * 32;
+  static constexpr int kUnitU = kBM * 64, kUnitB = kBRows * 32;
   static_assert(kStages <= kMaxStages && kStageBytes % 1024 == 0 && kUnitB % 1024 == 0, "stage layout");
 };
 
@@ -241,6 +244,7 @@ __device__ __forceinline__ void add_sq_df(uint32_t w, float& s, float& c) {
 struct QkvStream {
   int M;       // token rows (B * N_s)
   int N_s;     // tokens per batch item
+  DivU31 by_items;  // division by N_s
   int row0;    // the stream's first row in the joint sequence
   int tile0;   // its first tile
   const float* bias;  // [3 H d] or null
@@ -267,8 +271,8 @@ struct QkvParams {
   bool after_down;  // the launch before this one is lora_down_kernel's
 };
 
-// kLora: U [M, 2 * 3 * 16 rank_units] (the high terms of q, k, v, then the low
-// terms) and the adapters' up weights, image then caption stream.
+// kLora: U [M, 3 rank_units, 2, 16] (for each 16 of the rank of q, k and v the high
+// terms, then the low terms) and the adapters' up weights, image then caption stream.
 struct QkvLoraMaps {
   CUtensorMap u[2], up[2];
 };
@@ -283,9 +287,11 @@ struct Runs {
   int b, row;      // the next item, and its first row
   int here, then;  // its index, and the next one's
   int adapter, lo, hi;
-  __device__ __forceinline__ Runs(const QkvParams& p, int N_s_, int m0_, int m1_)
-      : index(p.index), n_adapters(p.n_adapters), N_s(N_s_), m0(m0_), m1(m1_) {
-    b = m0 / N_s;
+  Runs() = default;
+  // Of row tile mt of stream si, kRows rows.
+  __device__ __forceinline__ Runs(const QkvParams& p, int si, int mt, int kRows)
+      : index(p.index), n_adapters(p.n_adapters), N_s(p.s[si].N_s), m0(mt * kRows), m1(min(m0 + kRows, p.s[si].M)) {
+    b = static_cast<int>(p.s[si].by_items.div(m0));
     row = b * N_s;
     here = __ldg(index + b);
     then = row + N_s < m1 ? __ldg(index + b + 1) : 0;
@@ -326,7 +332,7 @@ struct Pieces {
   __device__ __forceinline__ bool next() {
     c += cols;
     if (c >= end) return false;
-    part = c / hd;
+    part = (c >= hd) + (c >= 2 * hd);
     const int left = min((part + 1) * hd, end) - c;
     cols = left >= 256 ? 256 : left >= 128 ? 128 : 64;
     return true;
@@ -657,7 +663,7 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
   const int ksteps = (p.C + kStepK - 1) / kStepK;
 
   if (warp >= Cfg::kEpiWarps) {
-  if constexpr (kPair) setmaxnreg_dec<QkvRegs::kOther>();
+  if constexpr (Cfg::kSplitRegs) setmaxnreg_dec<QkvRegs::kOther>();
   if (warp == kWarpProd) {
     if (lane == 0) {
       tma_prefetch_desc(&map_x0);
@@ -665,12 +671,14 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
       tma_prefetch_desc(&map_x1);
       tma_prefetch_desc(&map_w1);
       int it = 0;
-      bool ok = true;
+      bool ok = true, waited = false;
       for (int t = first_item; ok && t < p.items; t += item_step) {
         const auto [si, mt, n0, cols] = item_at<kCols>(p, t);
         const int w0 = n0 + rank * (cols / kCtas);  // this CTA's part of the weight rows
         const CUtensorMap* mx = si ? &map_x1 : &map_x0;
         const CUtensorMap* mw = si ? &map_w1 : &map_w0;
+        Runs all;  // made early: the first indexes are on their way meanwhile
+        if constexpr (kMode == kLora) all = Runs(p, si, mt, kRows);
         for (int kb = 0; kb < ksteps; ++kb) {
           const int s = it % kStages;
           if (it >= kStages && !(ok = mbar_wait(&bars.empty[s], ((it / kStages) - 1) & 1, ab, dev_err))) break;
@@ -683,11 +691,8 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
         }
         if constexpr (kMode == kLora) {
           if (!ok || !p.lora[si]) continue;
-          const int N_s = p.s[si].N_s, M = p.s[si].M;
-          const int m0 = mt * kRows, m1 = min(m0 + kRows, M);
           const CUtensorMap* mu = &lm.u[si];
           int used = 0;  // bytes of the open stage (0: none open)
-          bool waited = false;
           // The stage is closed by its one arrival; until then each group's bytes are added to what it expects.
           auto close = [&] {
             if (rank == 0) mbar_arrive(&bars.full[it % kStages]);
@@ -698,10 +703,10 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
           while (ok && pc.next()) {
             const int up0 = pc.c + rank * (pc.cols / kCtas);
             for (int kc = 0; ok && kc < p.rank_units; ++kc) {
-              Runs runs(p, N_s, m0, m1);
+              Runs runs = all;
               bool more = runs.next();
               while (ok && more) {
-                if (used + 2 * Cfg::kUnitA + Cfg::kUnitB > Cfg::kStageBytes) close();
+                if (used + Cfg::kUnitU + Cfg::kUnitB > Cfg::kStageBytes) close();
                 const int s = it % kStages;
                 if (used == 0) {
                   if (it >= kStages && !(ok = mbar_wait(&bars.empty[s], ((it / kStages) - 1) & 1, ab, dev_err))) break;
@@ -710,11 +715,9 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
                 }
                 const uint32_t full = pair_bar<kPair>(&bars.full[s]);
                 uint8_t* st = sm + s * Cfg::kStageBytes;
-                const int col = (pc.part * p.rank_units + kc) * 16;
-                if (rank == 0) mbar_expect_tx(&bars.full[s], kCtas * 2 * Cfg::kUnitA);
-                tma_load_2d_to<kPair>(st + used, mu, full, col, m0 + rank * kBM);
-                tma_load_2d_to<kPair>(st + used + Cfg::kUnitA, mu, full, col + 3 * 16 * p.rank_units, m0 + rank * kBM);
-                used += 2 * Cfg::kUnitA;
+                if (rank == 0) mbar_expect_tx(&bars.full[s], kCtas * Cfg::kUnitU);
+                tma_load_2d_to<kPair>(st + used, mu, full, (pc.part * p.rank_units + kc) * 32, mt * kRows + rank * kBM);
+                used += Cfg::kUnitU;
                 do {
                   if (rank == 0) mbar_expect_tx(&bars.full[s], kCtas * Cfg::kUnitB);
                   tma_load_5d_to<kPair>(st + used, &lm.up[si], full, kc * 16, 0, (up0 & 63) >> 2, up0 >> 6, runs.adapter);
@@ -744,6 +747,8 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
         const uint32_t idesc =
             kMode == kE4m3 ? idesc_e4m3_f32(kRows, cols) : idesc_bf16_f32(kRows, cols, false, false);
         const int abuf = lt & 1;
+        Runs all;  // as the producer's
+        if constexpr (kMode == kLora) all = Runs(p, si, mt, kRows);
         if (lt >= 2 && !(ok = mbar_wait(&bars.acc_empty[abuf], ((lt >> 1) - 1) & 1, ab, dev_err))) break;
         tc_fence_after();
         const uint32_t acc = tmem + abuf * kCols;
@@ -765,8 +770,6 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
         }
         if constexpr (kMode == kLora) {
           if (ok && p.lora[si]) {
-            const int N_s = p.s[si].N_s, M = p.s[si].M;
-            const int m0 = mt * kRows, m1 = min(m0 + kRows, M);
             int used = 0;  // as the producer counts
             auto close = [&] {
               umma_commit_to<kPair>(&bars.empty[it % kStages]);
@@ -777,19 +780,18 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
             while (ok && pc.next()) {
               const uint32_t desc = idesc_bf16_f32(kRows, pc.cols, false, false), at = acc + (pc.c - n0);
               for (int kc = 0; ok && kc < p.rank_units; ++kc) {
-                Runs runs(p, N_s, m0, m1);
+                Runs runs = all;
                 bool more = runs.next();
                 while (ok && more) {
-                  if (used + 2 * Cfg::kUnitA + Cfg::kUnitB > Cfg::kStageBytes) close();
+                  if (used + Cfg::kUnitU + Cfg::kUnitB > Cfg::kStageBytes) close();
                   const int s = it % kStages;
                   if (used == 0) {
                     if (!(ok = mbar_wait(&bars.full[s], (it / kStages) & 1, ab, dev_err))) break;
                     tc_fence_after();
                   }
                   const uint32_t st = smem_u32(sm + s * Cfg::kStageBytes);
-                  const uint64_t u_hi = sdesc_sw32_kmajor(st + used, 256);
-                  const uint64_t u_lo = sdesc_sw32_kmajor(st + used + Cfg::kUnitA, 256);
-                  used += 2 * Cfg::kUnitA;
+                  const uint64_t u_hi = sdesc_sw64_kmajor(st + used, 512), u_lo = desc_add(u_hi, 32);
+                  used += Cfg::kUnitU;
                   do {
                     uint32_t off[4 * kCtas];  // the lanes (rows) that the run does not hold
 #pragma unroll
@@ -814,7 +816,7 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
     }
   }
   } else {
-    if constexpr (kPair) setmaxnreg_inc<QkvRegs::kEpi>();
+    if constexpr (Cfg::kSplitRegs) setmaxnreg_inc<QkvRegs::kEpi>();
     // Warps of a group share the tile's columns from wcol on: each takes the TMEM lanes of warp w % 4, all 32
     // or one half of them.
     const int lg = warp & 3, group = warp / Cfg::kGroupWarps, wcol = group * D;
@@ -980,6 +982,7 @@ cudaError_t launch_qkv_form(const CUtensorMap (&maps)[4], const QkvLaunch& a, ui
   for (int i = 0; i < 2; ++i) {
     p.s[i].M = a.M[i];
     p.s[i].N_s = a.N_s[i];
+    p.s[i].by_items = make_div_u31(a.N_s[i] > 0 ? a.N_s[i] : 1);
     p.s[i].row0 = a.row0[i];
     p.s[i].tile0 = tile0;
     p.s[i].bias = a.bias[i];

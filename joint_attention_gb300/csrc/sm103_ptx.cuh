@@ -544,6 +544,16 @@ __device__ __forceinline__ uint64_t sdesc_sw32_kmajor(uint32_t saddr, uint32_t s
   d |= static_cast<uint64_t>(6u) << 61;           // SWIZZLE_32B
   return d;
 }
+// The same with 64-byte swizzle (64-byte rows).
+__device__ __forceinline__ uint64_t sdesc_sw64_kmajor(uint32_t saddr, uint32_t sbo_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1u) << 16;           // leading offset: unused within one swizzle row
+  d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(4u) << 61;           // SWIZZLE_64B
+  return d;
+}
 
 // Instruction descriptor, kind::f16 with bf16 A/B and fp32 D.
 //   bits 4-5 D format (1 = f32); 7-9 A format (1 = bf16); 10-12 B format
