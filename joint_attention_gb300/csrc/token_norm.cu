@@ -27,7 +27,7 @@
 //
 // Measured (device time, inputs out of L2; the copy rate is 6.77 TB/s): forward
 // 17616 x 768 17.7 us (6.1 TB/s), 32768 x 4096 155 us (6.9 TB/s); to 8 bits 9524
-// x 2048 26.3 us (5.2 TB/s: 16 instructions a value); rows to 8 bits 9524 x 2048
+// x 2048 27.1 us (5.0 TB/s: 16 instructions a value); rows to 8 bits 9524 x 2048
 // 10.0 us (5.9 TB/s); backward 17616 x 768 20.3 us with the sum of dg (5.3 TB/s:
 // two launches, and 7.2 rows a warp).
 #include <cuda_bf16.h>
@@ -79,6 +79,74 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(uint64_t ab, uint64_t cd) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// The rare path of norm rows to 8 bits: values that the fp32 arithmetic cannot
+// place on one side of a midpoint of e4m3 (about one in 150 000).  r cancels in 448
+// z / m but for its power of two (rz), with which z = h rz g is exact as the sum of
+// two floats, and so is m, the largest of the row's: 2 * 448 |z| and the sum of the
+// neighbours times m are compared exactly.
+//
+// The second float of the row's largest |z| (m: the first).
+__device__ __noinline__ float max_low(const uint4* h, const float* g, int chunks, float rz, float m) {
+  float low = -m;  // below any
+#pragma unroll 4
+  for (int c = threadIdx.x % 32; c < chunks; c += 32) {
+    const F8 u = unpack8(h[c]), gv = load8f(g, c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x[2], y[2];
+      f2_split(u.p[j], x[0], x[1]);
+      f2_split(gv.p[j], y[0], y[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float xr = __fmul_rn(x[i], rz), z = __fmul_rn(xr, y[i]);
+        if (fabsf(z) == m) low = fmaxf(low, copysignf(1.f, z) * __fmaf_rn(xr, y[i], -z));
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) low = fmaxf(low, __shfl_xor_sync(0xffffffffu, low, o));
+  return low;
+}
+__device__ __forceinline__ float e4m3_magnitude(uint32_t code) {
+  const uint32_t e = code >> 3 & 15, f = code & 7;
+  return e ? __uint_as_float((e + 120) << 23 | f << 20) : f * 0x1p-9f;
+}
+// Eight values of a row: as both ends of the fp32 quotient's range (lo, hi) round
+// where they agree, else by the comparison with the midpoint.  m, low: the row's
+// largest |z|; false: low (then 0) is not known, and decides.
+__device__ __noinline__ bool exact_e4m3x8(uint4 h, const float* g, int chunk, float rz, float lo, float hi, float m,
+                                          float low, bool known, uint2* to) {
+  const F8 u = unpack8(h), gv = load8f(g, chunk);
+  uint32_t out[2] = {0u, 0u};
+  bool decided = true;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float x[2], y[2];
+    f2_split(u.p[j], x[0], x[1]);
+    f2_split(gv.p[j], y[0], y[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float xr = __fmul_rn(x[i], rz), z = __fmul_rn(xr, y[i]);
+      const uint32_t both = pack_e4m3x4(f2_make(__fmul_rn(z, lo), __fmul_rn(z, hi)), 0);
+      uint32_t code = both & 255u;
+      const uint32_t up = both >> 8 & 255u;
+      if (up != code) {
+        // Nearly equal products, in two floats each: every difference and sum below is exact.
+        const float zl = copysignf(1.f, z) * __fmaf_rn(xr, y[i], -z), za = fabsf(z);
+        const float mid = e4m3_magnitude(code & 127u) + e4m3_magnitude(up & 127u);
+        const float ah = __fmul_rn(896.f, za), al = __fmaf_rn(896.f, za, -ah);
+        const float bh = __fmul_rn(mid, m), bl = __fmaf_rn(mid, m, -bh);
+        const float d = (ah - bh) + ((al - bl) + (896.f * zl - mid * low));
+        if (!known && fabsf(d) <= bh * 0x1p-23f) decided = false;
+        if (d > 0.f || (d == 0.f && (code & 1u))) code = up;
+      }
+      out[j / 2] |= code << (8 * (2 * (j % 2) + i));
+    }
+  }
+  *to = make_uint2(out[0], out[1]);
+  return decided;
 }
 
 // Reduction over the G warps that share a row (red: a float for each warp of
@@ -205,25 +273,67 @@ __global__ void __launch_bounds__(32 * block_warps(G)) token_rows_kernel(const N
       }
     }
     m = row_reduce<G, true>(m, red[1]);
-    // 448 z / m as 0.875 z over m / 512, which stays in range for every z and is exact for a bf16 z:
-    // midpoints of e4m3 (common then) stay midpoints.  The product with the reciprocal and one residual
-    // correction (Markstein, 1990) rounds as the quotient does.
     const float mz = __fmul_rn(m, rho);
     if (lane == 0) a.s[row] = __fdiv_rn(fmaxf(mz, kAmaxFloor), kE4m3Max);
-    m = __fmul_rn(mz < kAmaxFloor ? __fdiv_rn(kAmaxFloor, rho) : m, 1.f / 512);
-    const float inv = __frcp_rn(m);
-    const uint64_t inv2 = f2_make(inv, inv), neg_m2 = f2_make(-m, -m);
-    const uint64_t k2 = f2_make(kE4m3Max / 512, kE4m3Max / 512);
+    if constexpr (kOp == RowOp::kNormE4m3) {
+      // z, m, 448 / m and the product round once each, 4 * 2^-24 in all: rounded from both ends of a range (5 *
+      // 2^-24 below, 6 above), which nearly always agree.  One product with 448 / m, rounded as it is, gave the
+      // other neighbour for one value in a million, in the same time (26.3 us for 9524 x 2048, 27.1 with the
+      // rare path).
+      const bool low = mz < kAmaxFloor;
+      const float most = low ? __fdiv_rn(kAmaxFloor, rho) : m;
+      const float by = __fdiv_rn(kE4m3Max, most);
+      const float lo = __fmul_rn(by, 1.f - 5 * 0x1p-24f), hi = __fmul_rn(by, 1.f + 6 * 0x1p-24f);
+      const uint64_t lo2 = f2_make(lo, lo), hi2 = f2_make(hi, hi);
+      unsigned open = 0;  // chunks with a value that is not decided
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = i * kLanes + lane;
-      if (c < a.chunks) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint64_t v = f2_mul(z[i].p[j], k2), q = f2_mul(v, inv2);
-          z[i].p[j] = f2_fma(f2_fma(q, neg_m2, v), inv2, q);
+      for (int i = 0; i < V; ++i) {
+        const int c = i * kLanes + lane;
+        if (c < a.chunks) {
+          const F8& v = z[i];
+          const uint32_t y0 = pack_e4m3x4(f2_mul(v.p[0], lo2), f2_mul(v.p[1], lo2));
+          const uint32_t y1 = pack_e4m3x4(f2_mul(v.p[2], lo2), f2_mul(v.p[3], lo2));
+          const uint32_t u0 = pack_e4m3x4(f2_mul(v.p[0], hi2), f2_mul(v.p[1], hi2));
+          const uint32_t u1 = pack_e4m3x4(f2_mul(v.p[2], hi2), f2_mul(v.p[3], hi2));
+          if ((y0 ^ u0) | (y1 ^ u1)) open |= 1u << i;
+          a.y8[base + c] = make_uint2(y0, y1);
         }
-        a.y8[base + c] = make_uint2(pack_e4m3x4(z[i].p[0], z[i].p[1]), pack_e4m3x4(z[i].p[2], z[i].p[3]));
+      }
+      if (__any_sync(0xffffffffu, open != 0)) {
+        // The row of h: complete, since its warps have met in row_reduce after their stores.
+        const uint4* h = (a.res ? a.h : a.x) + base;
+        unsigned left = 0;
+        for (unsigned o = open; o; o &= o - 1) {
+          const int c = (__ffs(o) - 1) * kLanes + lane;
+          if (!exact_e4m3x8(h[c], a.g, c, rz, lo, hi, most, 0.f, low, a.y8 + base + c)) left |= o & -o;
+        }
+        if (__any_sync(0xffffffffu, left != 0)) {
+          const float m_low = max_low(h, a.g, a.chunks, rz, m);
+          for (; left; left &= left - 1) {
+            const int c = (__ffs(left) - 1) * kLanes + lane;
+            exact_e4m3x8(h[c], a.g, c, rz, lo, hi, m, m_low, true, a.y8 + base + c);
+          }
+        }
+      }
+    } else {
+      // 448 x / m as 0.875 x over m / 512, which stays in range for every x and is exact: midpoints of e4m3
+      // (common here) stay midpoints.  The product with the reciprocal and one residual correction (Markstein,
+      // 1990) rounds as the quotient does.
+      m = __fmul_rn(fmaxf(m, kAmaxFloor), 1.f / 512);
+      const float inv = __frcp_rn(m);
+      const uint64_t inv2 = f2_make(inv, inv), neg_m2 = f2_make(-m, -m);
+      const uint64_t k2 = f2_make(kE4m3Max / 512, kE4m3Max / 512);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = i * kLanes + lane;
+        if (c < a.chunks) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t v = f2_mul(z[i].p[j], k2), q = f2_mul(v, inv2);
+            z[i].p[j] = f2_fma(f2_fma(q, neg_m2, v), inv2, q);
+          }
+          a.y8[base + c] = make_uint2(pack_e4m3x4(z[i].p[0], z[i].p[1]), pack_e4m3x4(z[i].p[2], z[i].p[3]));
+        }
       }
     }
   }

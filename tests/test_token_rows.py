@@ -126,6 +126,30 @@ def bwd64(dy, dh, h, r, g):
     return dx, dx_mag, (dy * n).sum(0), (dy * n).abs().sum(0)
 
 
+def e4m3_of(q):
+    """The e4m3 value nearest to q (float64, at most 448 in magnitude; ties to even), as float64."""
+    step = torch.exp2(torch.floor(torch.log2(q.abs().clamp_min(2.0 ** -6))) - 3)
+    return torch.round(q / step) * step
+
+
+@gpu
+@pytest.mark.parametrize("T,C", [(20000, 768), (4000, 2048), (3001, 1096), (500, 16384), (7000, 8)])
+@pytest.mark.parametrize("g_bits", [24, 3])
+def test_norm_rows_are_the_nearest_e4m3_values(ja, T, C, g_bits):
+    """448 z / max |z| does not depend on r: with the exact products h g (32 bits) in float64 the quotient is off by
+    2^-53, far below the distance of any two 32-bit products' quotient from a midpoint (2^-37) unless it is on it.
+    With gains of 3 bits many are."""
+    x, res, g = randn((T, C), 55), randn((T, C), 56, 2.0), gains(C, 57)
+    if g_bits < 24:
+        g = torch.round(g * 4) / 4
+        x[:, 0], res[:, 0] = 14.0, 0.0
+        g[0] = 2.0  # the row's maximum 28 = 448 / 16 (or a few larger ones): quotients are z times a power of two
+    y8, s, h, r = ja.add_norm_fp8(x, g, res)
+    z = h.double() * g.double()
+    want = e4m3_of(448 * z / z.abs().amax(-1, keepdim=True))
+    assert torch.equal(y8.float().double(), want)
+
+
 @gpu
 @pytest.mark.parametrize("T,C", SIZES + [(5000, 256), (1217, 2048)])
 @pytest.mark.parametrize("with_dh", [False, True])
