@@ -308,8 +308,8 @@ int jattn_qkv_norm_fp8(const uint8_t* x_img, const float* sx_img, const uint8_t*
  *   work               : jattn_qkv_norm_lora_bytes(...) bytes for U, contents of
  *                        no meaning before or after; calls that overlap on the
  *                        GPU need one each
- * Items that share an adapter are cheapest next to each other in the batch:
- * a tile of 128 tokens takes each run of equal index values in turn.
+ * A tile of 128 or 256 tokens takes each different adapter among its items in
+ * turn, wherever in the tile they lie.
  * jattn_qkv_norm_lora_bytes returns 0 for sizes the call would reject.
  */
 #define JATTN_MAX_RANK 128

@@ -18,8 +18,8 @@ namespace {
 //
 // What bounds it: its own start and end.  At 512 px (16 items, rank 16) it reads
 // 27 MB in 13 us under ncu, with 4 stages of the ring as with 12; the projection
-// starts behind its first wait, so that the call takes 67 us where the
-// projection alone takes 52 and, with no item having an adapter, 56.
+// starts behind its first wait, so that the call takes 66 us where the
+// projection alone takes 52 and, with no item having an adapter, 55.
 constexpr int kDownThreads = 192;
 constexpr int kDownK = 64;
 constexpr int kDownMaxStages = 6;

@@ -67,13 +67,14 @@
 //          weights: Y = bf16(X W^T + U B^T + bias), U = scale X A^T (one
 //          launch of lora_down_kernel before, kept as two bf16 terms) as
 //          further K steps of 16 into the same accumulator.  A row tile that
-//          holds items with different adapters takes each run of items in
-//          turn, with the other rows' lanes disabled in the MMA, so that no row
-//          mask or copy of U is needed; a column tile over a q / k / v boundary
+//          holds items with different adapters takes each adapter in turn, with
+//          the other rows' lanes disabled in the MMA, so that no copy of U is
+//          needed (a warp of its own lists the next tile's adapters and their
+//          rows); a column tile over a q / k / v boundary
 //          takes each part with its own columns of U.  A ring stage holds, for
 //          16 of the rank at a time, both terms of U (8 KB) and the B rows of
-//          as many runs as fit (2 or 4 KB each): two such groups when there
-//          is one run, and U loaded once for 6 to 8 runs when there are many.
+//          as many adapters as fit (2 or 4 KB each): two such groups when there
+//          is one, and U loaded once for 6 to 8 when there are many.
 //
 // Correct rounding: the sum of the d squares is a balanced tree over a lane's
 // columns and the four lanes (at most 7 roundings per term, within the 8 that
@@ -101,6 +102,16 @@ constexpr uint32_t kDeadRow = 0xFFFFFFFFu;
 constexpr int kRingBytes = 192 * 1024;
 constexpr int kMaxStages = 8;
 
+// The adapters that rows m0 .. m1 - 1 of a stream (one row tile) have, and each
+// one's rows of the tile (bit i of rows[g][w]: row 32 w + i), wherever its items
+// lie among them; in the order of their first rows.
+template <int kRows>
+struct Groups {
+  int count;
+  int adapter[kRows];
+  uint32_t rows[kRows][kRows / 32];
+};
+
 // Epilogue warps, then the TMA producer and the MMA issuer.  Warp w reads the TMEM
 // lanes (rows) of warp w % 4, a head's columns of 16 rows or (kHalves = 2) of 32.
 // kPair: registers per thread (setmaxnreg).  Each SM sub-partition holds the
@@ -124,7 +135,8 @@ struct QkvCfg {
   static constexpr int kGroupWarps = kEpiWarps * D / kCols;  // that share a head's columns
   static constexpr int kHalves = 8 / kGroupWarps;
   static constexpr int kWarpProd = kEpiWarps, kWarpIssue = kEpiWarps + 1;
-  static constexpr int kThreads = 32 * (kEpiWarps + (kPair ? 4 : 2));  // kPair: two warps idle
+  static constexpr int kWarpGroups = kEpiWarps + 2;  // kLora
+  static constexpr int kThreads = 32 * (kEpiWarps + (kPair ? 4 : kMode == kLora ? 3 : 2));  // kPair: one or two idle
   static constexpr int kStageBytes = kATile + kBRows * kStepBytes;
   static constexpr int kStages = kRingBytes / kStageBytes;
   static constexpr int kTmemCols = 2 * kCols;
@@ -133,8 +145,12 @@ struct QkvCfg {
   // kE4m3: the scales of the columns, likewise, and of each warp's 32 rows.
   static constexpr int kOffScale = kOffBias + 2 * kColBytes;
   static constexpr int kOffXScale = kOffScale + 2 * kColBytes;
-  static constexpr int kDynSmem = (kMode == kE4m3 ? kOffXScale + kEpiWarps * 2 * 128 : kOffScale) + 1024;
-  // kLora: a group of operands for 16 of the rank, both terms of U, then the up weights of a run each.
+  static constexpr int kOffGroups = kOffScale;  // kLora: two tiles'
+  static constexpr int kDynSmem = (kMode == kE4m3   ? kOffXScale + kEpiWarps * 2 * 128
+                                   : kMode == kLora ? kOffGroups + 2 * static_cast<int>(sizeof(Groups<kCtas * kBM>))
+                                                    : kOffScale) +
+                                  1024;
+  // kLora: a group of operands for 16 of the rank, both terms of U, then the up weights of an adapter each.
   static constexpr int kUnitU = kBM * 64, kUnitB = kBRows * 32;
   static_assert(kStages <= kMaxStages && kStageBytes % 1024 == 0 && kUnitB % 1024 == 0, "stage layout");
 };
@@ -143,6 +159,7 @@ struct QkvBars {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t mma_done;
+  uint64_t groups_full[2], groups_empty[2];  // kLora
   uint32_t tmem_base;
   int abort;
   __align__(16) float gq[160];  // by col_offset
@@ -244,7 +261,6 @@ __device__ __forceinline__ void add_sq_df(uint32_t w, float& s, float& c) {
 struct QkvStream {
   int M;       // token rows (B * N_s)
   int N_s;     // tokens per batch item
-  DivU31 by_items;  // division by N_s
   int row0;    // the stream's first row in the joint sequence
   int tile0;   // its first tile
   const float* bias;  // [3 H d] or null
@@ -277,49 +293,50 @@ struct QkvLoraMaps {
   CUtensorMap u[2], up[2];
 };
 
-// The runs of consecutive batch items with one adapter among rows m0 .. m1 - 1
-// of a stream: next() gives the next one's adapter and its rows lo .. hi - 1 of
-// the tile, passing over items without an adapter.  Two items' indexes are on
-// their way ahead of the one that is looked at.
-struct Runs {
-  const int* index;
-  int n_adapters, N_s, m0, m1;
-  int b, row;      // the next item, and its first row
-  int here, then;  // its index, and the next one's
-  int adapter, lo, hi;
-  Runs() = default;
-  // Of row tile mt of stream si, kRows rows.
-  __device__ __forceinline__ Runs(const QkvParams& p, int si, int mt, int kRows)
-      : index(p.index), n_adapters(p.n_adapters), N_s(p.s[si].N_s), m0(mt * kRows), m1(min(m0 + kRows, p.s[si].M)) {
-    b = static_cast<int>(p.s[si].by_items.div(m0));
-    row = b * N_s;
-    here = __ldg(index + b);
-    then = row + N_s < m1 ? __ldg(index + b + 1) : 0;
-  }
-  __device__ __forceinline__ void step() {
-    ++b;
-    row += N_s;
-    here = then;
-    if (row + N_s < m1) then = __ldg(index + b + 1);  // row + N_s < m1 <= B N_s: item b + 1 exists
-  }
-  __device__ __forceinline__ bool next() {
-    while (row < m1) {
-      adapter = here;
-      lo = max(row, m0) - m0;
-      do step();
-      while (row < m1 && here == adapter);
-      hi = min(row, m1) - m0;
-      if (adapter >= 0 && adapter < n_adapters) return true;
-    }
-    return false;
-  }
-};
 // Rows lo .. hi - 1 of words of 32 rows: the bits of word w.
 __device__ __forceinline__ uint32_t rows_of_word(int lo, int hi, int w) {
   const int from = max(lo - 32 * w, 0), to = min(hi - 32 * w, 32);
   uint32_t m;
   asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(m) : "r"(from), "r"(max(to - from, 0)));
   return m;
+}
+// Made by one warp, 32 items at a time.
+template <int kRows>
+__device__ __forceinline__ void make_groups(Groups<kRows>& out, const QkvParams& p, int si, int mt, int lane) {
+  const int N_s = p.s[si].N_s, m0 = mt * kRows, m1 = min(m0 + kRows, p.s[si].M);
+  int count = 0;
+  for (int first = m0 / N_s; first * N_s < m1; first += 32) {
+    const int b = first + lane;
+    const bool in = b * N_s < m1;
+    const int a = in ? __ldg(p.index + b) : -1;
+    const bool has = a >= 0 && a < p.n_adapters;
+    int g = -1;  // the item's group
+    for (int i = 0; i < count; ++i)
+      if (out.adapter[i] == a) g = i;
+    const unsigned peers = __match_any_sync(0xffffffffu, has ? a : -1);
+    const bool leads = has && g < 0 && lane == __ffs(peers) - 1;
+    const unsigned leaders = __ballot_sync(0xffffffffu, leads);
+    if (leads) {
+      g = count + __popc(leaders & ((1u << lane) - 1));
+      out.adapter[g] = a;
+#pragma unroll
+      for (int w = 0; w < kRows / 32; ++w) out.rows[g][w] = 0;
+    }
+    const int of_leader = __shfl_sync(0xffffffffu, g, __ffs(peers) - 1);
+    __syncwarp();
+    if (has) {
+      if (g < 0) g = of_leader;
+      const int lo = max(b * N_s, m0) - m0, hi = min(b * N_s + N_s, m1) - m0;
+#pragma unroll
+      for (int w = 0; w < kRows / 32; ++w) {
+        const uint32_t bits = rows_of_word(lo, hi, w);
+        if (bits) atomicOr(&out.rows[g][w], bits);
+      }
+    }
+    count += __popc(leaders);
+    __syncwarp();
+  }
+  if (lane == 0) out.count = count;
 }
 // The pieces of columns n0 .. end - 1 for the adapters: of one of q, k and v, and
 // 64, 128 or 256 columns, so that two CTAs' halves of a piece are whole boxes of
@@ -638,6 +655,8 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars.acc_full[b], 1);
       mbar_init(&bars.acc_empty[b], kCtas * Cfg::kEpiWarps);
+      mbar_init(&bars.groups_full[b], 1);
+      mbar_init(&bars.groups_empty[b], rank == 0 ? 2 : 1);  // the producer, and the issuer if it is here
     }
     mbar_init(&bars.mma_done, 1);
     bars.abort = 0;
@@ -670,15 +689,13 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
       tma_prefetch_desc(&map_w0);
       tma_prefetch_desc(&map_x1);
       tma_prefetch_desc(&map_w1);
-      int it = 0;
+      int it = 0, lists = 0;
       bool ok = true, waited = false;
       for (int t = first_item; ok && t < p.items; t += item_step) {
         const auto [si, mt, n0, cols] = item_at<kCols>(p, t);
         const int w0 = n0 + rank * (cols / kCtas);  // this CTA's part of the weight rows
         const CUtensorMap* mx = si ? &map_x1 : &map_x0;
         const CUtensorMap* mw = si ? &map_w1 : &map_w0;
-        Runs all;  // made early: the first indexes are on their way meanwhile
-        if constexpr (kMode == kLora) all = Runs(p, si, mt, kRows);
         for (int kb = 0; kb < ksteps; ++kb) {
           const int s = it % kStages;
           if (it >= kStages && !(ok = mbar_wait(&bars.empty[s], ((it / kStages) - 1) & 1, ab, dev_err))) break;
@@ -692,6 +709,10 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
         if constexpr (kMode == kLora) {
           if (!ok || !p.lora[si]) continue;
           const CUtensorMap* mu = &lm.u[si];
+          const int gb = lists & 1;
+          if (!(ok = mbar_wait(&bars.groups_full[gb], (lists >> 1) & 1, ab, dev_err))) break;
+          const Groups<kRows>& groups = reinterpret_cast<const Groups<kRows>*>(sm + Cfg::kOffGroups)[gb];
+          const int count = groups.count;
           int used = 0;  // bytes of the open stage (0: none open)
           // The stage is closed by its one arrival; until then each group's bytes are added to what it expects.
           auto close = [&] {
@@ -700,12 +721,11 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
             ++it;
           };
           Pieces pc(p.H * D, n0, n0 + cols);
-          while (ok && pc.next()) {
+          while (ok && count > 0 && pc.next()) {
             const int up0 = pc.c + rank * (pc.cols / kCtas);
             for (int kc = 0; ok && kc < p.rank_units; ++kc) {
-              Runs runs = all;
-              bool more = runs.next();
-              while (ok && more) {
+              int g = 0;
+              while (ok && g < count) {
                 if (used + Cfg::kUnitU + Cfg::kUnitB > Cfg::kStageBytes) close();
                 const int s = it % kStages;
                 if (used == 0) {
@@ -720,14 +740,16 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
                 used += Cfg::kUnitU;
                 do {
                   if (rank == 0) mbar_expect_tx(&bars.full[s], kCtas * Cfg::kUnitB);
-                  tma_load_5d_to<kPair>(st + used, &lm.up[si], full, kc * 16, 0, (up0 & 63) >> 2, up0 >> 6, runs.adapter);
+                  tma_load_5d_to<kPair>(st + used, &lm.up[si], full, kc * 16, 0, (up0 & 63) >> 2, up0 >> 6,
+                                        groups.adapter[g]);
                   used += Cfg::kUnitB;
-                  more = runs.next();
-                } while (more && used + Cfg::kUnitB <= Cfg::kStageBytes);
+                } while (++g < count && used + Cfg::kUnitB <= Cfg::kStageBytes);
               }
             }
           }
           if (used > 0) close();
+          mbar_arrive(&bars.groups_empty[gb]);
+          ++lists;
         }
       }
       if constexpr (kMode == kLora) griddep_wait();  // this grid ends after the one before it
@@ -740,15 +762,13 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
     }
   } else if (warp == kWarpIssue) {
     if (lane == 0 && rank == 0) {
-      int it = 0, lt = 0;
+      int it = 0, lt = 0, lists = 0;
       bool ok = true;
       for (int t = first_item; ok && t < p.items; t += item_step, ++lt) {
         const auto [si, mt, n0, cols] = item_at<kCols>(p, t);
         const uint32_t idesc =
             kMode == kE4m3 ? idesc_e4m3_f32(kRows, cols) : idesc_bf16_f32(kRows, cols, false, false);
         const int abuf = lt & 1;
-        Runs all;  // as the producer's
-        if constexpr (kMode == kLora) all = Runs(p, si, mt, kRows);
         if (lt >= 2 && !(ok = mbar_wait(&bars.acc_empty[abuf], ((lt >> 1) - 1) & 1, ab, dev_err))) break;
         tc_fence_after();
         const uint32_t acc = tmem + abuf * kCols;
@@ -770,6 +790,10 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
         }
         if constexpr (kMode == kLora) {
           if (ok && p.lora[si]) {
+            const int gb = lists & 1;
+            if (!(ok = mbar_wait(&bars.groups_full[gb], (lists >> 1) & 1, ab, dev_err))) break;
+            const Groups<kRows>& groups = reinterpret_cast<const Groups<kRows>*>(sm + Cfg::kOffGroups)[gb];
+            const int count = groups.count;
             int used = 0;  // as the producer counts
             auto close = [&] {
               umma_commit_to<kPair>(&bars.empty[it % kStages]);
@@ -777,12 +801,11 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
               ++it;
             };
             Pieces pc(p.H * D, n0, n0 + cols);
-            while (ok && pc.next()) {
+            while (ok && count > 0 && pc.next()) {
               const uint32_t desc = idesc_bf16_f32(kRows, pc.cols, false, false), at = acc + (pc.c - n0);
               for (int kc = 0; ok && kc < p.rank_units; ++kc) {
-                Runs runs = all;
-                bool more = runs.next();
-                while (ok && more) {
+                int g = 0;
+                while (ok && g < count) {
                   if (used + Cfg::kUnitU + Cfg::kUnitB > Cfg::kStageBytes) close();
                   const int s = it % kStages;
                   if (used == 0) {
@@ -793,19 +816,20 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
                   const uint64_t u_hi = sdesc_sw64_kmajor(st + used, 512), u_lo = desc_add(u_hi, 32);
                   used += Cfg::kUnitU;
                   do {
-                    uint32_t off[4 * kCtas];  // the lanes (rows) that the run does not hold
+                    uint32_t off[4 * kCtas];  // the lanes (rows) that are not the group's
 #pragma unroll
-                    for (int w = 0; w < 4 * kCtas; ++w) off[w] = ~rows_of_word(runs.lo, runs.hi, w);
+                    for (int w = 0; w < 4 * kCtas; ++w) off[w] = ~groups.rows[g][w];
                     const uint64_t up = sdesc_sw32_kmajor(st + used, 256);
                     umma_bf16_ss_lanes(at, u_hi, up, desc, off, 1u);
                     umma_bf16_ss_lanes(at, u_lo, up, desc, off, 1u);
                     used += Cfg::kUnitB;
-                    more = runs.next();
-                  } while (more && used + Cfg::kUnitB <= Cfg::kStageBytes);
+                  } while (++g < count && used + Cfg::kUnitB <= Cfg::kStageBytes);
                 }
               }
             }
             if (ok && used > 0) close();
+            mbar_arrive(&bars.groups_empty[gb]);
+            ++lists;
           }
         }
         if (ok) umma_commit_to<kPair>(&bars.acc_full[abuf]);
@@ -813,6 +837,19 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
       // Every MMA this thread issued has completed once this barrier flips.
       umma_commit<kCtas>(&bars.mma_done);
       mbar_wait_drain(&bars.mma_done, 0);
+    }
+  } else if (kMode == kLora && warp == Cfg::kWarpGroups) {
+    int lists = 0;
+    for (int t = first_item; t < p.items; t += item_step) {
+      const QkvItem item = item_at<kCols>(p, t);
+      if (!p.lora[item.si]) continue;
+      const int gb = lists & 1;
+      if (lists >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bars.groups_empty[gb], ((lists >> 1) - 1) & 1, ab, dev_err)))
+        break;
+      make_groups(reinterpret_cast<Groups<kRows>*>(sm + Cfg::kOffGroups)[gb], p, item.si, item.mt, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.groups_full[gb]);
+      ++lists;
     }
   }
   } else {
@@ -982,7 +1019,6 @@ cudaError_t launch_qkv_form(const CUtensorMap (&maps)[4], const QkvLaunch& a, ui
   for (int i = 0; i < 2; ++i) {
     p.s[i].M = a.M[i];
     p.s[i].N_s = a.N_s[i];
-    p.s[i].by_items = make_div_u31(a.N_s[i] > 0 ? a.N_s[i] : 1);
     p.s[i].row0 = a.row0[i];
     p.s[i].tile0 = tile0;
     p.s[i].bias = a.bias[i];

@@ -299,6 +299,18 @@ def test_lora_index_values(ja, index):
 
 
 @gpu
+@pytest.mark.parametrize("B,H,N_img,N_txt,d", [(150, 3, 3, 1, 64), (90, 2, 1, 2, 128), (70, 16, 9, 5, 64),
+                                               (40, 9, 40, 0, 128)])
+def test_lora_adapters_in_turn(ja, B, H, N_img, N_txt, d):
+    """Many short items that share few adapters, in turn: a tile has each adapter's rows all over it."""
+    t = lora_inputs(B, H, N_img, N_txt, d, 72, 24, 7, True, 34)
+    t["index"][::5] = -1
+    out = lora_call(ja, t, H)
+    ok(ja)
+    check_lora(ja, t, out, H, d, 24)
+
+
+@gpu
 @pytest.mark.parametrize("streams", [(), ("img",), ("txt",)])
 def test_lora_streams_without_adapters(ja, streams):
     case = (3, 2, 140, 30, 64, 128, 32, 3, True)
