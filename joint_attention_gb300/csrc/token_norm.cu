@@ -22,13 +22,13 @@
 // memory and a barrier of their own.  The arithmetic is in packed fp32 pairs: the
 // kernels are bound by HBM only while they spend some 10 instructions on a
 // value.  Four chunks a lane, that is few warps a row and much in flight for
-// each, measured best (9524 x 2048 to 8 bits 26.3 us with 4, 29.0 with 2, 33.6
-// with 1, 27.9 with 8).
+// each, measured best (9524 x 2048 to 8 bits, at an earlier state, 26.3 us with
+// 4, 29.0 with 2, 33.6 with 1, 27.9 with 8).
 //
 // Measured (device time, inputs out of L2; the copy rate is 6.77 TB/s): forward
 // 17616 x 768 17.7 us (6.1 TB/s), 32768 x 4096 155 us (6.9 TB/s); to 8 bits 9524
-// x 2048 27.1 us (5.0 TB/s: 16 instructions a value); rows to 8 bits 9524 x 2048
-// 10.0 us (5.9 TB/s); backward 17616 x 768 20.3 us with the sum of dg (5.3 TB/s:
+// x 2048 24.8 us (5.5 TB/s: 16 instructions a value; 29.6 us with gains of 1,
+// where ties of e4m3 are common); rows to 8 bits 9524 x 2048 10.0 us (5.9 TB/s); backward 17616 x 768 20.3 us with the sum of dg (5.3 TB/s:
 // two launches, and 7.2 rows a warp).
 #include <cuda_bf16.h>
 
@@ -87,21 +87,29 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(uint64_t ab, uint64_t cd) {
 // two floats, and so is m, the largest of the row's: 2 * 448 |z| and the sum of the
 // neighbours times m are compared exactly.
 //
-// The second float of the row's largest |z| (m: the first).
+// The second float of the row's largest |z| (m: the first): the largest of those
+// of the values that round to m.
 __device__ __noinline__ float max_low(const uint4* h, const float* g, int chunks, float rz, float m) {
+  const uint64_t r2 = f2_make(rz, rz);
   float low = -m;  // below any
 #pragma unroll 4
   for (int c = threadIdx.x % 32; c < chunks; c += 32) {
     const F8 u = unpack8(h[c]), gv = load8f(g, c);
+    float z[8];
+    bool here = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float x[2], y[2];
-      f2_split(u.p[j], x[0], x[1]);
-      f2_split(gv.p[j], y[0], y[1]);
+      f2_split(f2_mul(f2_mul(u.p[j], r2), gv.p[j]), z[2 * j], z[2 * j + 1]);
+      here |= fabsf(z[2 * j]) == m || fabsf(z[2 * j + 1]) == m;
+    }
+    if (here) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float xr = __fmul_rn(x[i], rz), z = __fmul_rn(xr, y[i]);
-        if (fabsf(z) == m) low = fmaxf(low, copysignf(1.f, z) * __fmaf_rn(xr, y[i], -z));
+      for (int j = 0; j < 8; ++j) {
+        float x[2], y[2];
+        f2_split(u.p[j / 2], x[0], x[1]);
+        f2_split(gv.p[j / 2], y[0], y[1]);
+        const float zl = __fmaf_rn(__fmul_rn(x[j % 2], rz), y[j % 2], -z[j]);
+        if (fabsf(z[j]) == m) low = fmaxf(low, copysignf(1.f, z[j]) * zl);
       }
     }
   }
@@ -113,40 +121,20 @@ __device__ __forceinline__ float e4m3_magnitude(uint32_t code) {
   const uint32_t e = code >> 3 & 15, f = code & 7;
   return e ? __uint_as_float((e + 120) << 23 | f << 20) : f * 0x1p-9f;
 }
-// Eight values of a row: as both ends of the fp32 quotient's range (lo, hi) round
-// where they agree, else by the comparison with the midpoint.  m, low: the row's
-// largest |z|; false: low (then 0) is not known, and decides.
-__device__ __noinline__ bool exact_e4m3x8(uint4 h, const float* g, int chunk, float rz, float lo, float hi, float m,
-                                          float low, bool known, uint2* to) {
-  const F8 u = unpack8(h), gv = load8f(g, chunk);
-  uint32_t out[2] = {0u, 0u};
-  bool decided = true;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float x[2], y[2];
-    f2_split(u.p[j], x[0], x[1]);
-    f2_split(gv.p[j], y[0], y[1]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float xr = __fmul_rn(x[i], rz), z = __fmul_rn(xr, y[i]);
-      const uint32_t both = pack_e4m3x4(f2_make(__fmul_rn(z, lo), __fmul_rn(z, hi)), 0);
-      uint32_t code = both & 255u;
-      const uint32_t up = both >> 8 & 255u;
-      if (up != code) {
-        // Nearly equal products, in two floats each: every difference and sum below is exact.
-        const float zl = copysignf(1.f, z) * __fmaf_rn(xr, y[i], -z), za = fabsf(z);
-        const float mid = e4m3_magnitude(code & 127u) + e4m3_magnitude(up & 127u);
-        const float ah = __fmul_rn(896.f, za), al = __fmaf_rn(896.f, za, -ah);
-        const float bh = __fmul_rn(mid, m), bl = __fmaf_rn(mid, m, -bh);
-        const float d = (ah - bh) + ((al - bl) + (896.f * zl - mid * low));
-        if (!known && fabsf(d) <= bh * 0x1p-23f) decided = false;
-        if (d > 0.f || (d == 0.f && (code & 1u))) code = up;
-      }
-      out[j / 2] |= code << (8 * (2 * (j % 2) + i));
-    }
-  }
-  *to = make_uint2(out[0], out[1]);
-  return decided;
+// Whether a value h whose fp32 quotient's range (lo, hi) holds a midpoint rounds
+// to the upper of its neighbours, code.  m, low: the row's largest |z|.
+__device__ __forceinline__ bool rounds_up(float h, float g, float rz, float lo, float hi, float m, float low,
+                                          uint32_t& code) {
+  const float x = __fmul_rn(h, rz), z = __fmul_rn(x, g), za = fabsf(z);
+  const uint32_t both = pack_e4m3x4(f2_make(__fmul_rn(z, lo), __fmul_rn(z, hi)), 0);
+  code = both >> 8 & 255u;
+  // Nearly equal products, in two floats each: every difference and sum below is exact.
+  const float zl = copysignf(1.f, z) * __fmaf_rn(x, g, -z);
+  const float mid = e4m3_magnitude(both & 127u) + e4m3_magnitude(code & 127u);
+  const float ah = __fmul_rn(896.f, za), al = __fmaf_rn(896.f, za, -ah);
+  const float bh = __fmul_rn(mid, m), bl = __fmaf_rn(mid, m, -bh);
+  const float d = (ah - bh) + ((al - bl) + (896.f * zl - mid * low));
+  return d > 0.f || (d == 0.f && (both & 1u));
 }
 
 // Reduction over the G warps that share a row (red: a float for each warp of
@@ -187,8 +175,11 @@ struct NormArgs {
 
 enum class RowOp { kNorm, kNormE4m3, kQuant };
 
+// To 8 bits the blocks an SM holds are kept at four (two of 16 warps) against the rare path's registers: 24.8
+// us for 9524 x 2048, 27.6 without.
 template <int V, int G, RowOp kOp>
-__global__ void __launch_bounds__(32 * block_warps(G)) token_rows_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(32 * block_warps(G), kOp != RowOp::kNormE4m3 ? 0 : G > 8 ? 2 : 4)
+    token_rows_kernel(const NormArgs a) {
   __shared__ float red[2][kMaxWarps];
   griddep_launch_dependents();
   griddep_wait();
@@ -277,15 +268,14 @@ __global__ void __launch_bounds__(32 * block_warps(G)) token_rows_kernel(const N
     if (lane == 0) a.s[row] = __fdiv_rn(fmaxf(mz, kAmaxFloor), kE4m3Max);
     if constexpr (kOp == RowOp::kNormE4m3) {
       // z, m, 448 / m and the product round once each, 4 * 2^-24 in all: rounded from both ends of a range (5 *
-      // 2^-24 below, 6 above), which nearly always agree.  One product with 448 / m, rounded as it is, gave the
-      // other neighbour for one value in a million, in the same time (26.3 us for 9524 x 2048, 27.1 with the
-      // rare path).
+      // 2^-24 below, 6 above), which nearly always agree.  (A corrected quotient, rounded as it is, took 26.3 us
+      // for 9524 x 2048 and gave the other neighbour for one value in a million.)
       const bool low = mz < kAmaxFloor;
       const float most = low ? __fdiv_rn(kAmaxFloor, rho) : m;
       const float by = __fdiv_rn(kE4m3Max, most);
       const float lo = __fmul_rn(by, 1.f - 5 * 0x1p-24f), hi = __fmul_rn(by, 1.f + 6 * 0x1p-24f);
       const uint64_t lo2 = f2_make(lo, lo), hi2 = f2_make(hi, hi);
-      unsigned open = 0;  // chunks with a value that is not decided
+      unsigned open = 0;  // undecided values: bit 8 b + 2 i + w for byte b of word w of chunk i
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = i * kLanes + lane;
@@ -295,24 +285,21 @@ __global__ void __launch_bounds__(32 * block_warps(G)) token_rows_kernel(const N
           const uint32_t y1 = pack_e4m3x4(f2_mul(v.p[2], lo2), f2_mul(v.p[3], lo2));
           const uint32_t u0 = pack_e4m3x4(f2_mul(v.p[0], hi2), f2_mul(v.p[1], hi2));
           const uint32_t u1 = pack_e4m3x4(f2_mul(v.p[2], hi2), f2_mul(v.p[3], hi2));
-          if ((y0 ^ u0) | (y1 ^ u1)) open |= 1u << i;
+          // (Neighbouring codes differ in their last bit.)
+          open |= (((y0 ^ u0) & 0x01010101u) | ((y1 ^ u1) & 0x01010101u) << 1) << (2 * i);
           a.y8[base + c] = make_uint2(y0, y1);
         }
       }
       if (__any_sync(0xffffffffu, open != 0)) {
         // The row of h: complete, since its warps have met in row_reduce after their stores.
         const uint4* h = (a.res ? a.h : a.x) + base;
-        unsigned left = 0;
-        for (unsigned o = open; o; o &= o - 1) {
-          const int c = (__ffs(o) - 1) * kLanes + lane;
-          if (!exact_e4m3x8(h[c], a.g, c, rz, lo, hi, most, 0.f, low, a.y8 + base + c)) left |= o & -o;
-        }
-        if (__any_sync(0xffffffffu, left != 0)) {
-          const float m_low = max_low(h, a.g, a.chunks, rz, m);
-          for (; left; left &= left - 1) {
-            const int c = (__ffs(left) - 1) * kLanes + lane;
-            exact_e4m3x8(h[c], a.g, c, rz, lo, hi, m, m_low, true, a.y8 + base + c);
-          }
+        const float m_low = low ? 0.f : max_low(h, a.g, a.chunks, rz, m);
+        for (; open; open &= open - 1) {
+          const int bit = __ffs(open) - 1, c = (bit >> 1 & 3) * kLanes + lane, e = 4 * (bit & 1) + (bit >> 3);
+          const uint32_t word = reinterpret_cast<const uint16_t*>(h + c)[e];
+          uint32_t code;
+          if (rounds_up(__uint_as_float(word << 16), __ldg(a.g + c * 8 + e), rz, lo, hi, most, m_low, code))
+            reinterpret_cast<uint8_t*>(a.y8 + base + c)[e] = static_cast<uint8_t>(code);
         }
       }
     } else {
