@@ -218,7 +218,7 @@ int jattn_fwd_saved(const jattn_bf16* v, int B, int H, int N_img, int N_txt, int
  *   r = (mean_c h_c^2 + eps)^(-1/2)         fp32
  *   z = g * h * r                           fp32
  *   y = bf16(z), or 8 bits: m = max(max_c |z_c|, 2^-80), s = m / 448 (fp32),
- *                           y8 = e4m3(448 z / m)
+ *                           y8 = e4m3(448 z / m), the real quotient in fp32 first
  *
  * e4m3 is 1 sign, 4 exponent and 3 mantissa bits, largest finite value 448,
  * one byte a value; a row stands for s * y8.  The sum of squares is fp32: a

@@ -82,10 +82,12 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(uint64_t ab, uint64_t cd) {
 }
 
 // The rare path of norm rows to 8 bits: values that the fp32 arithmetic cannot
-// place on one side of a midpoint of e4m3 (about one in 150 000).  r cancels in 448
+// place on one side of a midpoint of e4m3 (about one in 110 000).  r cancels in 448
 // z / m but for its power of two (rz), with which z = h rz g is exact as the sum of
 // two floats, and so is m, the largest of the row's: 2 * 448 |z| and the sum of the
-// neighbours times m are compared exactly.
+// neighbours times m are compared exactly.  y8 is the quotient of these rounded to
+// fp32 and then to e4m3, as a conversion from a wider type does it: up to half an
+// fp32 step from the midpoint is a tie.
 //
 // The second float of the row's largest |z| (m: the first): the largest of those
 // of the values that round to m.
@@ -130,11 +132,15 @@ __device__ __forceinline__ bool rounds_up(float h, float g, float rz, float lo, 
   code = both >> 8 & 255u;
   // Nearly equal products, in two floats each: every difference and sum below is exact.
   const float zl = copysignf(1.f, z) * __fmaf_rn(x, g, -z);
-  const float mid = e4m3_magnitude(both & 127u) + e4m3_magnitude(code & 127u);
+  const float mid = e4m3_magnitude(both & 127u) + e4m3_magnitude(code & 127u);  // twice the midpoint
   const float ah = __fmul_rn(896.f, za), al = __fmaf_rn(896.f, za, -ah);
   const float bh = __fmul_rn(mid, m), bl = __fmaf_rn(mid, m, -bh);
   const float d = (ah - bh) + ((al - bl) + (896.f * zl - mid * low));
-  return d > 0.f || (d == 0.f && (both & 1u));
+  // m times the fp32 step above the midpoint; below it half of that, if it is a power of two.
+  const uint32_t bits = __float_as_uint(mid);
+  float step = __fmul_rn(m, __uint_as_float(bits & 0x7F800000u) * 0x1p-24f);
+  if (d < 0.f && (bits & 0x007FFFFFu) == 0u) step *= 0.5f;
+  return fabsf(d) <= step ? both & 1u : d > 0.f;
 }
 
 // Reduction over the G warps that share a row (red: a float for each warp of
@@ -267,13 +273,13 @@ __global__ void __launch_bounds__(32 * block_warps(G), kOp != RowOp::kNormE4m3 ?
     const float mz = __fmul_rn(m, rho);
     if (lane == 0) a.s[row] = __fdiv_rn(fmaxf(mz, kAmaxFloor), kE4m3Max);
     if constexpr (kOp == RowOp::kNormE4m3) {
-      // z, m, 448 / m and the product round once each, 4 * 2^-24 in all: rounded from both ends of a range (5 *
-      // 2^-24 below, 6 above), which nearly always agree.  (A corrected quotient, rounded as it is, took 26.3 us
+      // z, m, 448 / m, the end of the range and the product round once each, 5 * 2^-24 in all, and a tie reaches
+      // 2^-24 far: rounded from both ends of a range (7 * 2^-24 below, 8 above), which nearly always agree.  (A corrected quotient, rounded as it is, took 26.3 us
       // for 9524 x 2048 and gave the other neighbour for one value in a million.)
       const bool low = mz < kAmaxFloor;
       const float most = low ? __fdiv_rn(kAmaxFloor, rho) : m;
       const float by = __fdiv_rn(kE4m3Max, most);
-      const float lo = __fmul_rn(by, 1.f - 5 * 0x1p-24f), hi = __fmul_rn(by, 1.f + 6 * 0x1p-24f);
+      const float lo = __fmul_rn(by, 1.f - 7 * 0x1p-24f), hi = __fmul_rn(by, 1.f + 8 * 0x1p-24f);
       const uint64_t lo2 = f2_make(lo, lo), hi2 = f2_make(hi, hi);
       unsigned open = 0;  // undecided values: bit 8 b + 2 i + w for byte b of word w of chunk i
 #pragma unroll

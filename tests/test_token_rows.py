@@ -137,8 +137,9 @@ def e4m3_of(q):
 @pytest.mark.parametrize("g_bits", [24, 3])
 def test_norm_rows_are_the_nearest_e4m3_values(ja, T, C, g_bits):
     """448 z / max |z| does not depend on r: with the exact products h g (32 bits) in float64 the quotient is off by
-    2^-53, far below the distance of any two 32-bit products' quotient from a midpoint (2^-37) unless it is on it.
-    With gains of 3 bits many are."""
+    2^-53; it is rounded to fp32 and then to e4m3, which that decides alike unless it lies within 2^-53 of the
+    midpoint of two fp32 values next to a midpoint of e4m3 (one in 2^48).  With gains of 3 bits many are midpoints
+    of e4m3."""
     x, res, g = randn((T, C), 55), randn((T, C), 56, 2.0), gains(C, 57)
     if g_bits < 24:
         g = torch.round(g * 4) / 4
@@ -146,7 +147,7 @@ def test_norm_rows_are_the_nearest_e4m3_values(ja, T, C, g_bits):
         g[0] = 2.0  # the row's maximum 28 = 448 / 16 (or a few larger ones): quotients are z times a power of two
     y8, s, h, r = ja.add_norm_fp8(x, g, res)
     z = h.double() * g.double()
-    want = e4m3_of(448 * z / z.abs().amax(-1, keepdim=True))
+    want = e4m3_of((448 * z / z.abs().amax(-1, keepdim=True)).float().double())
     assert torch.equal(y8.float().double(), want)
 
 
