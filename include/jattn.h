@@ -286,7 +286,7 @@ int jattn_qkv_norm_fp8(const uint8_t* x_img, const float* sx_img, const uint8_t*
  * many requests, each with its adapter, in one batch).  For item b with a =
  * index[b], per stream and part p of (q, k, v):
  *
- *   U_p = scale[a] X A_ap^T                         fp32 accumulation, kept to 2^-16
+ *   U_p = scale[a] X A_ap^T                         fp32, kept in full
  *   Y_p = bf16(X W_p^T + U_p B_ap^T + b_p)          fp32 accumulation, one rounding
  *
  * and for an item whose index is outside 0 .. n_adapters - 1, jattn_qkv_norm's

@@ -301,15 +301,15 @@ bool encode_heads_map(CUtensorMap* map, const void* base, int64_t rows, int64_t 
   return r == CUDA_SUCCESS;
 }
 
-bool encode_unit_map(CUtensorMap* map, const void* base, int64_t rows, int cols) {
+bool encode_u_map(CUtensorMap* map, const uint16_t* u, int64_t rows, int units) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  cuuint32_t box[2] = {32, 128};
-  cuuint32_t es[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  cuuint64_t dims[3] = {16, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(3 * units)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(units) * 96, 32};
+  cuuint32_t box[3] = {16, 128, 3};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(u), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -730,7 +730,7 @@ struct QkvCall {
 
 size_t lora_u_bytes(int64_t rows, int rank) {
   const int64_t r16 = (rank + 15) / 16 * 16;
-  return (static_cast<size_t>(rows) * 2 * 3 * r16 * 2 + 255) & ~static_cast<size_t>(255);
+  return (static_cast<size_t>(rows) * 3 * 3 * r16 * 2 + 255) & ~static_cast<size_t>(255);
 }
 
 int check_lora(int rank) {
@@ -854,7 +854,7 @@ int qkv_body(const QkvCall& c) {
       l.on[i] = c.down[i] && n_s[i] > 0;
       if (!l.on[i]) {
         lora_maps[i] = lora_maps[2 + i] = down_maps[i] = item_maps[i] = maps[0];
-      } else if (!encode_unit_map(&lora_maps[i], l.u[i], a.M[i], 6 * r16) ||
+      } else if (!encode_u_map(&lora_maps[i], l.u[i], a.M[i], 3 * r16 / 16) ||
                  !encode_up_map(&lora_maps[2 + i], c.up[i], c.n_adapters, ycols, c.rank, w_rows) ||
                  !encode_bhnd_map_rows(&down_maps[i], c.down[i], 3 * c.n_adapters, c.rank, C, r16) ||
                  !encode_bhnd_map(&item_maps[i], c.x[i], c.B, n_s[i], C)) {

@@ -200,9 +200,9 @@ struct LoraLaunch {
   const int* index;    // [B] the items' adapters
   const float* scale;  // [n_adapters]
   bool on[2];          // whether a stream has adapters (and rows)
-  uint16_t* u[2];      // scratch [M, 3 ceil(rank / 16), 2, 16]
+  uint16_t* u[2];      // scratch [M, 3 ceil(rank / 16), 3, 16]
 };
-// lora_maps (with lora): encode_unit_map maps of both streams' U, then
+// lora_maps (with lora): encode_u_map maps of both streams' U, then
 // encode_up_map maps of their up weights (boxes of kQkvWRows rows); a stream
 // without adapters: any valid map.
 cudaError_t launch_qkv_norm(const CUtensorMap (&maps)[4], const QkvLaunch& a,
@@ -214,7 +214,7 @@ cudaError_t launch_qkv_norm_e4m3(const CUtensorMap (&maps)[4], const QkvLaunch& 
 cudaError_t launch_qkv_norm_lora(const CUtensorMap (&maps)[4], const QkvLaunch& a,
                                  uint32_t* dev_err, cudaStream_t st, const LoraLaunch* lora,
                                  const CUtensorMap* lora_maps);
-// U = scale X A^T in two bf16 terms, before launch_qkv_norm.  x: [B, N_s, C] as
+// U = scale X A^T in three bf16 terms, before launch_qkv_norm.  x: [B, N_s, C] as
 // encode_bhnd_map maps; down: the adapters' [3 n, rank, C] as
 // encode_bhnd_map_rows(..., 16 ceil(rank / 16)) maps.
 cudaError_t launch_lora_down(const CUtensorMap (&x)[2], const CUtensorMap (&down)[2], const LoraLaunch& l,
@@ -229,8 +229,9 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t c
 // Weights [rows, cols], rows a multiple of 64, in that order: a 4-D map
 // (cols, b, j, g) with box_rows (a multiple of 64) rows a box, otherwise as above.
 bool encode_heads_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool e4m3);
-// (32, 128) boxes of a [rows, cols] bf16 matrix, 64-byte swizzle.
-bool encode_unit_map(CUtensorMap* map, const void* base, int64_t rows, int cols);
+// U [rows, units, 3, 16]: a 3-D map (16, rows, 3 units), the three terms of 16
+// columns of 128 rows a box, term by term, 32-byte swizzle.
+bool encode_u_map(CUtensorMap* map, const uint16_t* u, int64_t rows, int units);
 // n adapters' up weights [rows, rank] in that order: a 5-D map (rank, b, j, g,
 // adapter), 16 of the rank and box_rows rows a box, 32-byte swizzle.
 bool encode_up_map(CUtensorMap* map, const uint16_t* up, int n, int64_t rows, int rank, int box_rows);

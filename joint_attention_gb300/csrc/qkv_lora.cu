@@ -10,11 +10,12 @@ namespace {
 // has one adapter, whose down weights [3 rank, C] are the product's other
 // operand, N = 3 * 16 rank_units columns (a rank that is not a multiple of 16
 // reads the TMA's zero fill).  Items without an adapter write nothing (the
-// projection reads nothing of theirs).  U is kept as two bf16 terms, the value
-// rounded and the rest rounded (at most 2^-16 of it is lost), so that Y has one
-// rounding: with one term q_hat's error against 64 bits was 1.2 to 1.35 times
-// that of fp32 arithmetic.  Warps 0-3 read the accumulator out (a row a
-// thread), warp 4 loads, warp 5 issues.
+// projection reads nothing of theirs).  U is kept as three bf16 terms, each what
+// the ones before leave rounded: together they are the fp32 value, so that Y has
+// one rounding.  Of 10 000 values of q 4.5 are not the bf16 value nearest to the
+// exact one (512 px, rank 16), 4.1 without adapters; with two terms, which lose up
+// to 2^-17 of U, 8.4 were (and a call took 66.3 us instead of 67.3).  Warps 0-3
+// read the accumulator out (a row a thread), warp 4 loads, warp 5 issues.
 //
 // What bounds it: its own start and end.  At 512 px (16 items, rank 16) it reads
 // 27 MB in 13 us under ncu, with 4 stages of the ring as with 12; the projection
@@ -27,7 +28,7 @@ constexpr int kDownSmem = 200 * 1024;
 
 struct DownStream {
   int N_s, blocks, cta0;  // rows per item, its 128-row blocks, the stream's first CTA
-  uint16_t* u;            // [B N_s, 3 rank_units, 2, 16]: 16 high terms, then their low terms
+  uint16_t* u;            // [B N_s, 3 rank_units, 3, 16]: the first terms of 16 values, the second, the third
 };
 struct DownParams {
   DownStream s[2];
@@ -131,24 +132,29 @@ __global__ void __launch_bounds__(kDownThreads, 1)
       tc_fence_after();
       const float scale = __ldg(p.scale + adapter);
       const int n = row0 + warp * 32 + lane;
-      uint16_t* u = (si ? p.s[1].u : p.s[0].u) + (static_cast<size_t>(item) * N_s + n) * (6 * r16);
+      uint16_t* u = (si ? p.s[1].u : p.s[0].u) + (static_cast<size_t>(item) * N_s + n) * (9 * r16);
       for (int c = 0; c < 3 * p.rank_units; ++c) {
         uint32_t v[16];
         tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c * 16, v);
         tmem_wait_ld();
-        uint32_t hi[8], lo[8];
+        uint32_t w[3][8];  // (each remainder is exact in fp32)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float a = __uint_as_float(v[2 * i]) * scale, b = __uint_as_float(v[2 * i + 1]) * scale;
-          hi[i] = pack_bf16x2(a, b);
-          lo[i] = pack_bf16x2(a - bf_lo(hi[i]), b - bf_hi(hi[i]));
+          float a = __uint_as_float(v[2 * i]) * scale, b = __uint_as_float(v[2 * i + 1]) * scale;
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            w[k][i] = pack_bf16x2(a, b);
+            a -= bf_lo(w[k][i]);
+            b -= bf_hi(w[k][i]);
+          }
         }
         if (n < N_s) {
-          uint4* o = reinterpret_cast<uint4*>(u + c * 32);
-          o[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          o[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-          o[2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          o[3] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+          uint4* o = reinterpret_cast<uint4*>(u + c * 48);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            o[2 * k] = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+            o[2 * k + 1] = make_uint4(w[k][4], w[k][5], w[k][6], w[k][7]);
+          }
         }
       }
       tc_fence_before();

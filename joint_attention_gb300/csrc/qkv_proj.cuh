@@ -65,16 +65,16 @@
 //          Y = bf16(sx sw acc + bias).
 //   kLora  low-rank adapters of the batch items' own beside the shared
 //          weights: Y = bf16(X W^T + U B^T + bias), U = scale X A^T (one
-//          launch of lora_down_kernel before, kept as two bf16 terms) as
+//          launch of lora_down_kernel before, kept as three bf16 terms) as
 //          further K steps of 16 into the same accumulator.  A row tile that
 //          holds items with different adapters takes each adapter in turn, with
 //          the other rows' lanes disabled in the MMA, so that no copy of U is
 //          needed (a warp of its own lists the next tile's adapters and their
 //          rows); a column tile over a q / k / v boundary
 //          takes each part with its own columns of U.  A ring stage holds, for
-//          16 of the rank at a time, both terms of U (8 KB) and the B rows of
+//          16 of the rank at a time, the terms of U (12 KB) and the B rows of
 //          as many adapters as fit (2 or 4 KB each): two such groups when there
-//          is one, and U loaded once for 6 to 8 when there are many.
+//          is one, and U loaded once for 5 or 6 when there are many.
 //
 // Correct rounding: the sum of the d squares is a balanced tree over a lane's
 // columns and the four lanes (at most 7 roundings per term, within the 8 that
@@ -150,8 +150,8 @@ struct QkvCfg {
                                    : kMode == kLora ? kOffGroups + 2 * static_cast<int>(sizeof(Groups<kCtas * kBM>))
                                                     : kOffScale) +
                                   1024;
-  // kLora: a group of operands for 16 of the rank, both terms of U, then the up weights of an adapter each.
-  static constexpr int kUnitU = kBM * 64, kUnitB = kBRows * 32;
+  // kLora: a group of operands for 16 of the rank, the terms of U, then the up weights of an adapter each.
+  static constexpr int kTermU = kBM * 32, kUnitU = 3 * kTermU, kUnitB = kBRows * 32;
   static_assert(kStages <= kMaxStages && kStageBytes % 1024 == 0 && kUnitB % 1024 == 0, "stage layout");
 };
 
@@ -287,8 +287,8 @@ struct QkvParams {
   bool after_down;  // the launch before this one is lora_down_kernel's
 };
 
-// kLora: U [M, 3 rank_units, 2, 16] (for each 16 of the rank of q, k and v the high
-// terms, then the low terms) and the adapters' up weights, image then caption stream.
+// kLora: U [M, 3 rank_units, 3, 16] (for each 16 of the rank of q, k and v the first,
+// second and third terms) and the adapters' up weights, image then caption stream.
 struct QkvLoraMaps {
   CUtensorMap u[2], up[2];
 };
@@ -736,7 +736,8 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
                 const uint32_t full = pair_bar<kPair>(&bars.full[s]);
                 uint8_t* st = sm + s * Cfg::kStageBytes;
                 if (rank == 0) mbar_expect_tx(&bars.full[s], kCtas * Cfg::kUnitU);
-                tma_load_2d_to<kPair>(st + used, mu, full, (pc.part * p.rank_units + kc) * 32, mt * kRows + rank * kBM);
+                tma_load_3d_to<kPair>(st + used, mu, full, 0, mt * kRows + rank * kBM,
+                                      3 * (pc.part * p.rank_units + kc));
                 used += Cfg::kUnitU;
                 do {
                   if (rank == 0) mbar_expect_tx(&bars.full[s], kCtas * Cfg::kUnitB);
@@ -813,15 +814,16 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
                     tc_fence_after();
                   }
                   const uint32_t st = smem_u32(sm + s * Cfg::kStageBytes);
-                  const uint64_t u_hi = sdesc_sw64_kmajor(st + used, 512), u_lo = desc_add(u_hi, 32);
+                  const uint64_t u = sdesc_sw32_kmajor(st + used, 256);
                   used += Cfg::kUnitU;
                   do {
                     uint32_t off[4 * kCtas];  // the lanes (rows) that are not the group's
 #pragma unroll
                     for (int w = 0; w < 4 * kCtas; ++w) off[w] = ~groups.rows[g][w];
                     const uint64_t up = sdesc_sw32_kmajor(st + used, 256);
-                    umma_bf16_ss_lanes(at, u_hi, up, desc, off, 1u);
-                    umma_bf16_ss_lanes(at, u_lo, up, desc, off, 1u);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                      umma_bf16_ss_lanes(at, desc_add(u, k * Cfg::kTermU), up, desc, off, 1u);
                     used += Cfg::kUnitB;
                   } while (++g < count && used + Cfg::kUnitB <= Cfg::kStageBytes);
                 }

@@ -237,6 +237,22 @@ __device__ __forceinline__ void tma_load_2d_to(void* smem_dst, const CUtensorMap
         : "memory");
 }
 template <bool kPair>
+__device__ __forceinline__ void tma_load_3d_to(void* smem_dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                               int c2) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+template <bool kPair>
 __device__ __forceinline__ void tma_load_4d_to(void* smem_dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
                                                int c2, int c3) {
   if constexpr (kPair)
@@ -542,16 +558,6 @@ __device__ __forceinline__ uint64_t sdesc_sw32_kmajor(uint32_t saddr, uint32_t s
   d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(6u) << 61;           // SWIZZLE_32B
-  return d;
-}
-// The same with 64-byte swizzle (64-byte rows).
-__device__ __forceinline__ uint64_t sdesc_sw64_kmajor(uint32_t saddr, uint32_t sbo_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(1u) << 16;           // leading offset: unused within one swizzle row
-  d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(4u) << 61;           // SWIZZLE_64B
   return d;
 }
 

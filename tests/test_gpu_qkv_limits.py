@@ -1,0 +1,49 @@
+"""The QKV projections at the limits of their inputs and outputs: what the adapters' first product keeps, and
+rows past the fp32 range.
+
+Tolerances count the roundings that test_gpu_qkv_forms counts: each addition of a product off by at most
+2^-23 of the terms' summed magnitudes, bf16 by half a step (2^-8).
+"""
+import pytest
+import torch
+
+import joint_attention_gb300 as pkg
+from joint_attention_gb300.build import build
+from test_gpu_qkv_forms import lora_call, lora_inputs, ok
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ja():
+    build()
+    pkg.load_library()
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    return pkg
+
+
+@gpu
+@pytest.mark.parametrize("rank", [8, 16, 40, 128])
+@pytest.mark.parametrize("H,N,d", [(2, 40, 64), (6, 1100, 64), (6, 1100, 128)])
+def test_lora_first_product_is_kept_in_32_bits(ja, rank, H, N, d):
+    """Y = U B^T + b with each column of B one of U's columns and b the opposite of U rounded to fp32: what is
+    left is U's own error, of (C + 4) roundings of its terms' magnitudes, each at most 2^-23 (the sum, the scale, and the
+    term's and the bias's addition); U kept to 2^-16 would leave up to 2^-17 of U.  All tokens of an item are alike."""
+    B, C = 1, 16
+    t = lora_inputs(B, H, N, 0, d, C, rank, 1, True, 303, streams=("img",))
+    t["x_img"][:] = t["x_img"][:, :1].abs()
+    t["down_img"].abs_()
+    t["w_img"].zero_()
+    u = torch.einsum("c,pjc->pj", t["x_img"][0, 0].double(), t["down_img"].double().view(3, rank, C))
+    u = u * t["scale"].double()
+    col = torch.arange(H * d, device="cuda") % rank
+    t["up_img"].zero_()
+    t["up_img"].view(3, H * d, rank)[:, torch.arange(H * d, device="cuda"), col] = 1.0
+    want = u[:, col]
+    t["b_img"] = -want.float().reshape(-1)
+    q, k, v, _ = lora_call(ja, t, H)
+    ok(ja)
+    for y, w in zip((q, k, v), want.view(3, H, d)):
+        off = y[0].double() - (w - w.float().double())[:, None]  # y is rounded to bf16: at most 2^-8 of itself
+        assert (off.abs() <= ((C + 4) * 2.0 ** -23 * w + 2.0 ** -23 * w)[:, None] * (1 + 2.0 ** -8)).all()
