@@ -404,14 +404,15 @@ __device__ __forceinline__ float lane_squares(const uint32_t (&yb)[D / 8]) {
 
 // r of a row of d values from its sum of squares.  r is what is kept; rc, for
 // q_hat / k_hat, takes one Newton step more: r (1 + t / 2), t = 1 - m r^2 of
-// order 2^-22, is the root of m to 2^-44 before its rounding.
+// order 2^-22, is the root of m to 2^-44 before its rounding.  (r = 0, of a row
+// whose squares pass the fp32 range, stays: m r is then not a number.)
 template <int D>
 __device__ __forceinline__ void row_rsqrt(float sum, float& r, float& rc) {
   const float m = __fadd_rn(__fmul_rn(sum, 1.f / D), kEps);
   r = rsqrtf(m);
   const float q = __fmul_rn(m, r);  // 1 - m r^2 = 1 - q r + (q - m r) r
   const float t = __fmaf_rn(__fmaf_rn(-m, r, q), r, __fmaf_rn(-q, r, 1.f));
-  rc = __fmaf_rn(__fmul_rn(0.5f, r), t, r);
+  rc = r == 0.f ? r : __fmaf_rn(__fmul_rn(0.5f, r), t, r);
 }
 
 // The four lanes' sums of their kRows (2 or 4) rows, joined (lanes 2 apart

@@ -9,7 +9,7 @@ import torch
 
 import joint_attention_gb300 as pkg
 from joint_attention_gb300.build import build
-from test_gpu_qkv_forms import lora_call, lora_inputs, ok
+from test_gpu_qkv_forms import check_norms, fp8_call, fp8_inputs, lora_call, lora_inputs, ok, saved_parts
 
 gpu = pytest.mark.gpu
 
@@ -47,3 +47,34 @@ def test_lora_first_product_is_kept_in_32_bits(ja, rank, H, N, d):
     for y, w in zip((q, k, v), want.view(3, H, d)):
         off = y[0].double() - (w - w.float().double())[:, None]  # y is rounded to bf16: at most 2^-8 of itself
         assert (off.abs() <= ((C + 4) * 2.0 ** -23 * w + 2.0 ** -23 * w)[:, None] * (1 + 2.0 ** -8)).all()
+
+
+@gpu
+@pytest.mark.parametrize("form", ["bf16", "fp8", "lora"])
+@pytest.mark.parametrize("H,N_img,d", [(2, 40, 64), (2, 40, 128), (6, 1100, 64), (6, 1100, 128)])
+def test_rows_whose_squares_pass_fp32(ja, form, H, N_img, d):
+    """A q or k row whose sum of squares passes the fp32 range has 1/rms 0: its q_hat and k_hat are zeros, and
+    those of a row of infinities are NaN, as a training forward keeps them; other rows are as they were."""
+    B, N_txt, C = 2, 9, 64
+    if form == "fp8":
+        t = fp8_inputs(B, H, N_img, N_txt, d, C, True, 301)
+        t["sx_img"][0, 4], t["sx_img"][1, 7], t["sx_txt"][1, 3] = 1e20, float("inf"), 3e21
+        q, k, v, saved = fp8_call(ja, t, H)
+    else:
+        t = lora_inputs(B, H, N_img, N_txt, d, C, 16, 2, True, 302)
+        t["x_img"][0, 4] *= 1e20
+        t["x_img"][1, 7, 0] = float("inf")  # +-inf in every column
+        t["index"][1] = -1                  # (an adapter would add them to others of either sign)
+        t["x_txt"][1, 3] *= 3e21
+        if form == "lora":
+            q, k, v, saved = lora_call(ja, t, H)
+        else:
+            q, k, v, saved = ja.qkv_norm(t["x_img"], t["w_img"], t["b_img"], t["x_txt"], t["w_txt"], t["b_txt"],
+                                         t["gq"], t["gk"], H)
+    ok(ja)
+    check_norms(ja, q, k, v, saved, t["gq"], t["gk"], N_txt)
+    for hat, r in zip(*(saved_parts(saved, q)[i:i + 2] for i in (0, 2))):
+        for b, n in ((0, N_txt + 4), (1, 3)):
+            assert not hat[b, :, n].any() and not r[b, :, n].any()
+        assert hat[1, :, N_txt + 7].isnan().all()
+        assert hat.isnan().sum() == H * d
