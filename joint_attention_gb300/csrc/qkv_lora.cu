@@ -33,6 +33,7 @@ struct DownStream {
 struct DownParams {
   DownStream s[2];
   int C, rank_units, n_adapters, stages, tmem_cols;
+  bool half_unit;  // the rank is an odd multiple of 8: the last unit's second half stands for nothing
   const int* index;
   const float* scale;
 };
@@ -137,16 +138,24 @@ __global__ void __launch_bounds__(kDownThreads, 1)
         uint32_t v[16];
         tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c * 16, v);
         tmem_wait_ld();
-        uint32_t w[3][8];  // (each remainder is exact in fp32)
+        // Each remainder is exact in fp32.  The first two terms end at the largest bf16 value, so that a value
+        // above it keeps its rest and an infinity is the last term (not inf - inf).
+        uint32_t w[3][8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float a = __uint_as_float(v[2 * i]) * scale, b = __uint_as_float(v[2 * i + 1]) * scale;
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
-            w[k][i] = pack_bf16x2(a, b);
+            w[k][i] = k < 2 ? pack_bf16x2_sat(a, b) : pack_bf16x2(a, b);
             a -= bf_lo(w[k][i]);
             b -= bf_hi(w[k][i]);
           }
+        }
+        if (p.half_unit && c % p.rank_units == p.rank_units - 1) {  // past the rank: 0, for infinite tokens too
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int i = 4; i < 8; ++i) w[k][i] = 0u;
         }
         if (n < N_s) {
           uint4* o = reinterpret_cast<uint4*>(u + c * 48);
@@ -187,6 +196,7 @@ cudaError_t launch_lora_down(const CUtensorMap (&x)[2], const CUtensorMap (&down
   if (ctas == 0) return cudaSuccess;
   p.C = a.C;
   p.rank_units = r16 / 16;
+  p.half_unit = l.rank % 16 != 0;
   p.n_adapters = l.n_adapters;
   const int stage_bytes = kATile + 3 * r16 * 128;
   p.stages = kDownSmem / stage_bytes < kDownMaxStages ? kDownSmem / stage_bytes : kDownMaxStages;

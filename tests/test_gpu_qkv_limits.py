@@ -78,3 +78,33 @@ def test_rows_whose_squares_pass_fp32(ja, form, H, N_img, d):
             assert not hat[b, :, n].any() and not r[b, :, n].any()
         assert hat[1, :, N_txt + 7].isnan().all()
         assert hat.isnan().sum() == H * d
+
+
+@gpu
+@pytest.mark.parametrize("rank", [16, 24])
+@pytest.mark.parametrize("H,N", [(2, 40), (6, 1100)])
+def test_lora_with_infinities_and_the_largest_values(ja, rank, H, N):
+    """A token with an infinite value and positive weights is infinite, and not NaN, whatever the rank (one that is no
+    multiple of 16 included); a U near the end of the fp32 range, above the largest bf16, counts as it is."""
+    B, C, d = 2, 72, 64
+    t = lora_inputs(B, H, N, 0, d, C, rank, 2, True, 304, streams=("img",))
+    for name in ("x_img", "w_img", "down_img", "up_img"):
+        t[name].abs_().clamp_min_(2.0 ** -6)
+    t["x_img"][0, 5, 1] = float("inf")
+    q, k, v, _ = lora_call(ja, t, H)
+    ok(ja)
+    for y in (q, k, v):
+        assert (y[0, :, 5] == float("inf")).all()
+        assert y.isfinite().sum() == y.numel() - H * d
+    big = torch.finfo(torch.bfloat16).max  # 255 * 2^120
+    t["w_img"].zero_(), t["b_img"].zero_(), t["up_img"].zero_(), t["down_img"].zero_(), t["x_img"].zero_()
+    t["scale"][:] = 1.0
+    t["x_img"][1, 7, :2] = torch.tensor([1.0, 2.0 ** 119], device="cuda")
+    t["down_img"][:, :, :2] = torch.tensor([big, 1.5], device="cuda")  # U = 255.75 * 2^120
+    t["up_img"][:, :, 3] = 2.0 ** -20
+    q, k, v, _ = lora_call(ja, t, H)
+    ok(ja)
+    want = torch.tensor(255.75 * 2.0 ** 100, dtype=torch.float64).to(torch.bfloat16).item()
+    for y in (q, k, v):
+        assert (y[1, :, 7] == want).all()
+        assert (y != 0).sum() == H * d
