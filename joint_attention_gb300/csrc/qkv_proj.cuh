@@ -186,15 +186,20 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
 }
 
 // 16 consecutive columns of a row, one 32-byte store when the outputs are so
-// aligned (wide; pairs of CTAs are used only then), else two of 16 bytes.
-__device__ __forceinline__ void store_cols16(uint16_t* to, const uint32_t* w, bool wide) {
+// aligned (wide).  Else two of 16 bytes, with kTurn the upper half first in every other
+// lane: the lanes whose halves meet in a 32-byte sector then write them at once.
+template <bool kTurn>
+__device__ __forceinline__ void store_cols16(uint16_t* to, const uint32_t* w, bool wide, int lane) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
   } else {
-    reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    uint4* half = reinterpret_cast<uint4*>(to);
+    const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+    const bool turn = kTurn && (lane & 1) == 0;
+    half[turn ? 1 : 0] = turn ? hi : lo;
+    half[turn ? 0 : 1] = turn ? lo : hi;
   }
 }
 // All `threads` threads of a named barrier: whether ok holds for every one.
@@ -495,11 +500,16 @@ __device__ __forceinline__ void fix_row(const uint32_t (&yb)[D / 8], int src, fl
 // each 64: TMEM column 4 j + b is output column 16 b + j, by the order in which
 // the weights' rows are loaded.  So four lanes write 128 consecutive bytes of a
 // row from registers.
-template <int D, int kMode, bool kPair, int kHalves>
+template <int D, int kMode, bool kPair, bool kWide, int kHalves>
 __device__ __forceinline__ void qkv_emit(uint32_t taddr, uint64_t* acc_empty, int col0, uint32_t rows, int half0,
                                          uint32_t bias, uint32_t wscale, uint32_t xscale, const QkvParams& p,
                                          const QkvBars& bars, int lane) {
   constexpr int kRows = 2 * kHalves, kUnits = (D / 32) * kHalves;  // of 32 columns x 16 rows
+  const bool wide = kPair ? kWide : p.wide;
+  // Outputs at 16-byte boundaries, in turn / in one order (512 px at d = 64; 768 px, C = 1024, at d = 128): from bf16
+  // 53.3 / 56.6 and 85.2 / 92.5 us, with adapters 69.5 / 75.0 and 103.3 / 110.8, from e4m3 at d = 128 71.8 / 79.9;
+  // from e4m3 at d = 64, which has no instructions to spare, 50.0 / 48.3.  (At 32-byte boundaries 52, 83, 66, 99, 58, 38.)
+  constexpr bool kTurn = kMode != kE4m3 || D != 64;
   const int a = lane >> 2, b = lane & 3;
   uint32_t row[kRows];
   uint64_t sx2[kRows];
@@ -572,7 +582,7 @@ __device__ __forceinline__ void qkv_emit(uint32_t taddr, uint64_t* acc_empty, in
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
         if (row[i] != kDeadRow)
-          store_cols16(raw + static_cast<size_t>(row[i]) * D + c * 64, yb[i] + c * 8, kPair || p.wide);
+          store_cols16<kTurn>(raw + static_cast<size_t>(row[i]) * D + c * 64, yb[i] + c * 8, wide, lane);
   }
   if (which == 2) return;
   float rc[kRows];
@@ -606,7 +616,8 @@ __device__ __forceinline__ void qkv_emit(uint32_t taddr, uint64_t* acc_empty, in
     for (int i = 0; i < kRows; ++i) {
       uint32_t w[8];
       hat_cols16(yb[i] + c * 8, gv, rc[i], w, near[i]);
-      if (row[i] != kDeadRow) store_cols16(hat + static_cast<size_t>(row[i]) * D + c * 64 + b * 16, w, kPair || p.wide);
+      if (row[i] != kDeadRow)
+        store_cols16<kTurn>(hat + static_cast<size_t>(row[i]) * D + c * 64 + b * 16, w, wide, lane);
     }
   }
   unsigned todo[kRows], any = 0;
@@ -628,7 +639,9 @@ __device__ __forceinline__ void qkv_emit(uint32_t taddr, uint64_t* acc_empty, in
   }
 }
 
-template <int D, int kMode, bool kPair>
+// kWide: of a pair, whether the outputs are at 32-byte boundaries (a kernel of its own for those that are not: with
+// both in one 512 px from e4m3 rows took 42.2 us instead of 39.2); single CTAs look at p.wide.
+template <int D, int kMode, bool kPair, bool kWide>
 __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
     qkv_norm_kernel(const __grid_constant__ CUtensorMap map_x0, const __grid_constant__ CUtensorMap map_w0,
                     const __grid_constant__ CUtensorMap map_x1, const __grid_constant__ CUtensorMap map_w1,
@@ -915,7 +928,7 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
         if (lane == 0) mbar_arrive_to<kPair>(&bars.acc_empty[abuf]);
         continue;
       }
-      qkv_emit<D, kMode, kPair, Cfg::kHalves>(
+      qkv_emit<D, kMode, kPair, kWide, Cfg::kHalves>(
           tmem + (static_cast<uint32_t>(lg * 32 + half0 * 16) << 16) + abuf * kCols + wcol, &bars.acc_empty[abuf],
           it.n0 + wcol, row, half0, bias_s + abuf * Cfg::kColBytes, wscale_s + abuf * Cfg::kColBytes,
           xscale_w + abuf * 128, p, bars, lane);
@@ -966,11 +979,11 @@ cudaError_t resident_pairs(K kernel, int threads, int smem, int regs, std::atomi
   return cudaSuccess;
 }
 
-template <int D, int kMode, bool kPair>
+template <int D, int kMode, bool kPair, bool kWide>
 cudaError_t launch_qkv_kernel(const CUtensorMap (&maps)[4], const QkvLoraMaps& lm, QkvParams& p, int tiles,
                               const float* gq, const float* gk, uint32_t* dev_err, cudaStream_t st) {
   using Cfg = QkvCfg<D, kMode, kPair>;
-  auto kernel = qkv_norm_kernel<D, kMode, kPair>;
+  auto kernel = qkv_norm_kernel<D, kMode, kPair, kWide>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kDynSmem);
   if (e != cudaSuccess) return e;
   const int sms = device_sm_count();
@@ -997,6 +1010,14 @@ cudaError_t launch_qkv_kernel(const CUtensorMap (&maps)[4], const QkvLoraMaps& l
   const int grid = (p.items < groups ? p.items : groups) * Cfg::kCtas;
   return launch_pdl_cluster(kernel, Cfg::kCtas, dim3(grid), dim3(Cfg::kThreads), Cfg::kDynSmem, st, maps[0], maps[1],
                             maps[2], maps[3], lm, p, gq, gk, dev_err);
+}
+
+template <int D, int kMode>
+cudaError_t launch_qkv_tiles(const CUtensorMap (&maps)[4], const QkvLoraMaps& lm, QkvParams& p, int tiles,
+                             const QkvLaunch& a, uint32_t* dev_err, cudaStream_t st) {
+  if (!a.pair) return launch_qkv_kernel<D, kMode, false, false>(maps, lm, p, tiles, a.gq, a.gk, dev_err, st);
+  if (a.wide) return launch_qkv_kernel<D, kMode, true, true>(maps, lm, p, tiles, a.gq, a.gk, dev_err, st);
+  return launch_qkv_kernel<D, kMode, true, false>(maps, lm, p, tiles, a.gq, a.gk, dev_err, st);
 }
 
 }  // namespace
@@ -1041,11 +1062,8 @@ cudaError_t launch_qkv_form(const CUtensorMap (&maps)[4], const QkvLaunch& a, ui
   p.after_down = p.lora[0] || p.lora[1];
   p.rank_units = lora ? (lora->rank + 15) / 16 : 0;
   if (tile0 == 0) return cudaSuccess;
-  if (a.d == 64)
-    return pair ? launch_qkv_kernel<64, kMode, true>(maps, lm, p, tile0, a.gq, a.gk, dev_err, st)
-                : launch_qkv_kernel<64, kMode, false>(maps, lm, p, tile0, a.gq, a.gk, dev_err, st);
-  return pair ? launch_qkv_kernel<128, kMode, true>(maps, lm, p, tile0, a.gq, a.gk, dev_err, st)
-              : launch_qkv_kernel<128, kMode, false>(maps, lm, p, tile0, a.gq, a.gk, dev_err, st);
+  if (a.d == 64) return launch_qkv_tiles<64, kMode>(maps, lm, p, tile0, a, dev_err, st);
+  return launch_qkv_tiles<128, kMode>(maps, lm, p, tile0, a, dev_err, st);
 }
 
 }  // namespace jattn
