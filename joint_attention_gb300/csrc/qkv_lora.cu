@@ -98,10 +98,8 @@ __global__ void __launch_bounds__(kDownThreads, 1)
         for (int part = 0; part < 3; ++part)
           tma_load_3d(st + kATile + part * r16 * 128, md, &bars.full[s], kb * kDownK, 0, 3 * adapter + part);
       }
-      if (*ab) {  // aborted: the copies in flight land before the CTA exits
-        for (int i = (kb > p.stages ? kb - p.stages : 0); i < kb; ++i)
-          mbar_wait_drain(&bars.full[i % p.stages], (i / p.stages) & 1);
-      }
+      if (*ab)  // aborted: the copies in flight land before the CTA exits
+        drain_ring(kb, p.stages, true, [&](int s, uint32_t parity) { mbar_wait_drain(&bars.full[s], parity); });
     }
   } else if (warp == 5) {
     if (lane == 0) {

@@ -89,6 +89,7 @@
 #include "sm103_ptx.cuh"
 #include "bf16_round.cuh"
 #include "fastdiv.cuh"
+#include "ring.cuh"
 
 namespace jattn {
 namespace {
@@ -768,12 +769,11 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
         }
       }
       if constexpr (kMode == kLora) griddep_wait();  // this grid ends after the one before it
-      if (*ab) {
-        // Aborted: the copies in flight land before the CTA exits.  The second
-        // CTA's signal the first one's barriers: it waits out the limit.
-        for (int i = (it > kStages ? it - kStages : 0); i < it; ++i)
-          mbar_wait_drain(&bars.full[i % kStages], (i / kStages) & 1);
-      }
+      // Aborted: the copies in flight land before the CTA, or the pair, exits.  (A role that gives up later has
+      // waited a second for the issuer, which has then met every stage, or has itself waited that long for one of
+      // them: by then those copies have landed.  The pair's closing barrier keeps both CTAs until then.)
+      if (*ab)
+        drain_ring(it, kStages, rank == 0, [&](int s, uint32_t parity) { mbar_wait_drain(&bars.full[s], parity); });
     }
   } else if (warp == kWarpIssue) {
     if (lane == 0 && rank == 0) {
