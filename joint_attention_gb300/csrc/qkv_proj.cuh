@@ -119,10 +119,12 @@ struct Groups {
 // epilogue warps w with one w % 4 and one other warp, and an increase draws only
 // on the registers those were launched with, so 4 kEpi + kOther must be at most 5
 // times the launch count (allocated by eights).  The launcher refuses any build
-// whose register count differs.
+// whose register count differs (fits: used registers against the count that a form
+// is launched with, 0 for a form without a split).
 struct QkvRegs {
   static constexpr int kLaunch = 96, kEpi = 104, kOther = 64;
   static_assert(4 * kEpi + kOther == 5 * kLaunch, "projection register split");
+  static constexpr bool fits(int used, int launch) { return launch == 0 || (used + 7) / 8 * 8 == launch; }
 };
 
 template <int D, int kMode, bool kPair>
@@ -133,6 +135,7 @@ struct QkvCfg {
   static constexpr int kEpiWarps = kPair ? 16 : 8;
   // Not with adapters, whose producer and issuer have more to keep (512 px 67.0 us without the split, 67.9 with).
   static constexpr bool kSplitRegs = kPair && kMode != kLora;
+  static constexpr int kLaunchRegs = kSplitRegs ? QkvRegs::kLaunch : 0;
   static constexpr int kGroupWarps = kEpiWarps * D / kCols;  // that share a head's columns
   static constexpr int kHalves = 8 / kGroupWarps;
   static constexpr int kWarpProd = kEpiWarps, kWarpIssue = kEpiWarps + 1;
@@ -946,7 +949,7 @@ __global__ void __launch_bounds__(QkvCfg<D, kMode, kPair>::kThreads, 1)
 
 // How many pairs of a kernel the current device runs at once (a pair beyond
 // that number would start when the others have finished), after a check of the
-// registers its setmaxnreg split was sized for; asked once per device and
+// registers its setmaxnreg split (if regs is not 0) was sized for; asked once per device and
 // kernel (`known`: the kernel's own, by device, 0 where not asked yet).
 template <typename K>
 cudaError_t resident_pairs(K kernel, int threads, int smem, int regs, std::atomic<int>* known, int devices,
@@ -960,7 +963,7 @@ cudaError_t resident_pairs(K kernel, int threads, int smem, int regs, std::atomi
   cudaFuncAttributes fa;
   e = cudaFuncGetAttributes(&fa, kernel);
   if (e != cudaSuccess) return e;
-  if ((fa.numRegs + 7) / 8 * 8 != regs) return cudaErrorInvalidConfiguration;
+  if (!QkvRegs::fits(fa.numRegs, regs)) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(threads);
@@ -991,7 +994,7 @@ cudaError_t launch_qkv_kernel(const CUtensorMap (&maps)[4], const QkvLoraMaps& l
   if constexpr (kPair) {
     static std::atomic<int> known[64];
     int fit = 0;
-    e = resident_pairs(kernel, Cfg::kThreads, Cfg::kDynSmem, QkvRegs::kLaunch, known, 64, &fit);
+    e = resident_pairs(kernel, Cfg::kThreads, Cfg::kDynSmem, Cfg::kLaunchRegs, known, 64, &fit);
     if (e != cudaSuccess) return e;
     if (fit < groups) groups = fit;
   }
