@@ -353,7 +353,7 @@ struct NormBwdArgs {
 template <int V, int G>
 __global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 1 : 2) token_norm_bwd_kernel(const NormBwdArgs a) {
   constexpr int kLanes = 32 * G, kRows = block_warps(G) / G;
-  extern __shared__ float sums[];  // [rows of a block][C]
+  extern __shared__ __align__(16) float sums[];  // [rows of a block][C]
   __shared__ float red[2][kMaxWarps];
   const int lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
   griddep_launch_dependents();

@@ -1,10 +1,14 @@
 """Every layout of a token row (one to sixteen warps, one to four chunks a lane) in the forward, 8-bit, quant and
 backward kernels, with gains of both signs and zeros.  Tolerances: those of test_token_rows."""
+import glob
+import os
+import re
+
 import pytest
 import torch
 
 import joint_attention_gb300 as pkg
-from joint_attention_gb300.build import build
+from joint_attention_gb300.build import CSRC, build
 from test_token_rows import (FLOOR, SIZES, U, bwd64, check_e4m3, check_norm, check_quant, e4m3_of, gains, norm64,
                              randn)
 
@@ -66,3 +70,13 @@ def test_norm_rows_to_e4m3_by_the_exact_quotient(ja, T, C, g_bits):
     z = x.double() * g.double()
     want = e4m3_of((448 * z / z.abs().amax(-1, keepdim=True).clamp_min(FLOOR)).float().double())
     assert torch.equal(y8.float().double(), want)
+
+
+def test_dynamic_shared_arrays_state_their_alignment():
+    """They are written by 16-byte vectors: bytes that the kernel aligns itself, or an array declared at 16 bytes (a
+    narrower type's alignment would leave it to the size of the static arrays before it)."""
+    found = [d for name in glob.glob(os.path.join(CSRC, "*.cu*"))
+             for d in re.findall(r"extern __shared__ (.*)\[\];", open(name).read())]
+    assert found
+    for d in found:
+        assert d == "uint8_t smem_raw" or d.startswith("__align__(16) "), d
