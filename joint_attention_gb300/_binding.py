@@ -439,14 +439,19 @@ def jattn_fwd_saved(v, B: int, H: int, N_img: int, N_txt: int, d: int, out, lse,
     return rc
 
 
+def _size(n: int) -> int:
+    """n for a C int: 0, which the library refuses, where ctypes would keep the low 32 bits."""
+    return n if -(1 << 31) <= n < 1 << 31 else 0
+
+
 def jattn_add_norm(x, res, g, T: int, C: int, eps: float, h, y, r, stream=None, check: bool = True) -> int:
     """C ABI jattn_add_norm.  x / res / h / y [T, C] bf16 (res and h both or neither; h may be res),
     g [C] fp32, r [T] fp32 or None."""
     import torch
 
     bf, f32, e = torch.bfloat16, torch.float32, T * C
-    rc = load_library().jattn_add_norm(_ptr(x, "x", bf, e), _ptr(res, "res", bf, e), _ptr(g, "g", f32, C), T, C, eps,
-                                       _ptr(h, "h", bf, e), _ptr(y, "y", bf, e), _ptr(r, "r", f32, T),
+    rc = load_library().jattn_add_norm(_ptr(x, "x", bf, e), _ptr(res, "res", bf, e), _ptr(g, "g", f32, C), _size(T),
+                                       _size(C), eps, _ptr(h, "h", bf, e), _ptr(y, "y", bf, e), _ptr(r, "r", f32, T),
                                        _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_add_norm")
@@ -458,9 +463,10 @@ def jattn_add_norm_fp8(x, res, g, T: int, C: int, eps: float, h, y8, s, r, strea
     import torch
 
     bf, f32, e = torch.bfloat16, torch.float32, T * C
-    rc = load_library().jattn_add_norm_fp8(_ptr(x, "x", bf, e), _ptr(res, "res", bf, e), _ptr(g, "g", f32, C), T, C,
-                                           eps, _ptr(h, "h", bf, e), _ptr(y8, "y8", torch.float8_e4m3fn, e),
-                                           _ptr(s, "s", f32, T), _ptr(r, "r", f32, T), _stream(stream))
+    rc = load_library().jattn_add_norm_fp8(_ptr(x, "x", bf, e), _ptr(res, "res", bf, e), _ptr(g, "g", f32, C),
+                                           _size(T), _size(C), eps, _ptr(h, "h", bf, e),
+                                           _ptr(y8, "y8", torch.float8_e4m3fn, e), _ptr(s, "s", f32, T),
+                                           _ptr(r, "r", f32, T), _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_add_norm_fp8")
     return rc
@@ -471,7 +477,7 @@ def jattn_quant_rows(x, T: int, C: int, x8, s, stream=None, check: bool = True) 
     import torch
 
     e = T * C
-    rc = load_library().jattn_quant_rows(_ptr(x, "x", torch.bfloat16, e), T, C,
+    rc = load_library().jattn_quant_rows(_ptr(x, "x", torch.bfloat16, e), _size(T), _size(C),
                                          _ptr(x8, "x8", torch.float8_e4m3fn, e), _ptr(s, "s", torch.float32, T),
                                          _stream(stream))
     if check and rc != 0:
@@ -482,7 +488,7 @@ def jattn_quant_rows(x, T: int, C: int, x8, s, stream=None, check: bool = True) 
 @functools.lru_cache(maxsize=1024)  # a function of the sizes alone, and a library call of 0.8 us
 def jattn_add_norm_bwd_bytes(T: int, C: int) -> int:
     """C ABI jattn_add_norm_bwd_bytes: size of the work buffer of jattn_add_norm_bwd (0: it rejects the sizes)."""
-    return int(load_library().jattn_add_norm_bwd_bytes(T, C))
+    return int(load_library().jattn_add_norm_bwd_bytes(_size(T), _size(C)))
 
 
 def _work_ptr(work, bytes_of, *sizes):
@@ -507,7 +513,7 @@ def jattn_add_norm_bwd(dy, dh, h, r, g, T: int, C: int, dx, dg, work, stream=Non
     bf, f32, e = torch.bfloat16, torch.float32, T * C
     lib = load_library()
     rc = lib.jattn_add_norm_bwd(_ptr(dy, "dy", bf, e), _ptr(dh, "dh", bf, e), _ptr(h, "h", bf, e),
-                                _ptr(r, "r", f32, T), _ptr(g, "g", f32, C), T, C, _ptr(dx, "dx", bf, e),
+                                _ptr(r, "r", f32, T), _ptr(g, "g", f32, C), _size(T), _size(C), _ptr(dx, "dx", bf, e),
                                 _ptr(dg, "dg", f32, C), _work_ptr(work, jattn_add_norm_bwd_bytes, T, C),
                                 _stream(stream))
     if check and rc != 0:

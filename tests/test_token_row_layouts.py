@@ -80,3 +80,22 @@ def test_dynamic_shared_arrays_state_their_alignment():
     assert found
     for d in found:
         assert d == "uint8_t smem_raw" or d.startswith("__align__(16) "), d
+
+
+# Fake, never-dereferenced device addresses: the refusal comes first.
+A = [0x7F0000000000 + (i << 40) for i in range(10)]
+
+
+@pytest.mark.parametrize("T,C", [(2 ** 32 + 24, 64), (2 ** 31, 64), (24, 2 ** 32 + 64), (24, -2 ** 32 + 64)])
+def test_sizes_beyond_32_bits_are_refused(T, C):
+    """The library takes 32-bit sizes: one beyond them is refused, and not cut to its low bits (24 rows of 64 here)."""
+    build()
+    pkg.load_library()
+    for call in (lambda: pkg.jattn_quant_rows(A[0], T, C, A[1], A[2], stream=0),
+                 lambda: pkg.jattn_add_norm(A[0], A[1], A[2], T, C, 1e-6, A[3], A[4], A[5], stream=0),
+                 lambda: pkg.jattn_add_norm_fp8(A[0], A[1], A[2], T, C, 1e-6, A[3], A[4], A[5], A[6], stream=0),
+                 lambda: pkg.jattn_add_norm_bwd(A[0], A[1], A[2], A[3], A[4], T, C, A[5], A[6], A[7], stream=0)):
+        with pytest.raises(pkg.JattnError) as e:
+            call()
+        assert e.value.status == pkg.STATUS_CODE["JATTN_ERR_INVALID_ARG"]
+    assert pkg.jattn_add_norm_bwd_bytes(T, C) == 0
