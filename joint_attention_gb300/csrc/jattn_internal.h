@@ -116,7 +116,8 @@ void set_sm_limit(int n);  // n <= 0: no limit
 
 // --- token-row norm kernels (HBM-bound) ---------------------------------------
 // h = bf16(x + res), r = (mean h^2 + eps)^(-1/2), z = g h r; y = bf16(z), or
-// y8 = e4m3(z / s) with the rows' scales s.  g null (and y null): z = x.
+// y8 = e4m3(448 z / m) with the rows' scales s = m / 448, m = max |z| (the quotient
+// rounded to fp32 first).  g null (and y null): z = x.
 struct TokenNorm {
   const uint16_t *x, *res;  // res: or null (then h is null)
   const float* g;

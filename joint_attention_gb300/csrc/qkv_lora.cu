@@ -14,8 +14,9 @@ namespace {
 // the ones before leave rounded: together they are the fp32 value, so that Y has
 // one rounding.  Of 10 000 values of q 4.5 are not the bf16 value nearest to the
 // exact one (512 px, rank 16), 4.1 without adapters; with two terms, which lose up
-// to 2^-17 of U, 8.4 were (and a call took 66.3 us instead of 67.3).  Warps 0-3
-// read the accumulator out (a row a thread), warp 4 loads, warp 5 issues.
+// to 2^-17 of U, 8.4 were (and a call took 65.8 us instead of 66.4, of rank 128 110
+// instead of 119).  Warps 0-3 read the accumulator out (a row a thread), warp 4
+// loads, warp 5 issues.
 //
 // What bounds it: its own start and end.  At 512 px (16 items, rank 16) it reads
 // 27 MB in 13 us under ncu, with 4 stages of the ring as with 12; the projection

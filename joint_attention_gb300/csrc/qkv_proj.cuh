@@ -51,13 +51,16 @@
 // e4m3; 768 px, C = 2048, 16 heads of 128; 141 and 87 us): the epilogue beside
 // the products.  The products alone take 38, 24, 120 and 66 us (the rate of
 // cuBLAS), the epilogue with one K step 30, 34, 43 and 50, of which 5 to 10 for
-// the stores.  From e4m3 at 512 px the epilogue's instructions count (some 930 a
-// warp for 32 rows of 64 columns); else the loads' latency beside the stores (a
-// ring of 128 KB 56 and 147 us from bf16, of 160 KB 52.7 and 141) and shared
-// memory's bandwidth, of which the products take most: rows staged there and
-// written out by TMA stores, with 128 KB left for the ring, took 57, 39, 151 and
-// 92 us; gains, biases and scales read without a gap every 16 columns (two-way
-// bank conflicts), and anew for each row, 5 us more from e4m3 at 512 px.
+// the stores.  From e4m3 at 512 px it is the epilogue's latency, with the issue slots
+// 45 % and the tensor pipe 37 % busy: all 16 warps are in one phase of one tile (some
+// 930 instructions a warp for 32 rows of 64 columns; of 9.7 cycles between two of
+// them 2.6 are spent at the tile's barrier and 1.9 for TMEM and memory).  Else it is
+// the loads' latency beside the stores (a ring of 128 KB 56 and 147 us from bf16, of
+// 160 KB 52.7 and 141) and shared memory's bandwidth, of which the products take
+// most: rows staged there and written out by TMA stores, with 128 KB left for the
+// ring, took 57, 39, 151 and 92 us; gains, biases and scales read without a gap every
+// 16 columns (two-way bank conflicts), and anew for each row, 5 us more from e4m3 at
+// 512 px.
 //
 // The same kernel takes two other forms of the products (template kMode):
 //   kE4m3  X and W in e4m3 with fp32 scales of their rows: a K step of 128

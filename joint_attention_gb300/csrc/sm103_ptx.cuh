@@ -202,9 +202,13 @@ __device__ __forceinline__ uint32_t pair_bar(const uint64_t* bar) {
   if constexpr (kPair) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(a));
   return a;
 }
-// One arrival on that barrier.  A pair's is relaxed: it hands back TMEM, whose
-// reads tcgen05.wait::ld has completed, and publishes no memory (a release at
-// cluster scope cost some 500 cycles, and an acquire there the L1's contents).
+// One arrival on that barrier, by one lane for its warp.  A pair's is relaxed: it
+// hands back TMEM and publishes no memory (a release at cluster scope cost some 500
+// cycles, and an acquire there the L1's contents).  What it hands over is that every
+// lane's reads of TMEM have completed: each lane has waited for its own
+// (tcgen05.wait::ld) and fenced them (tc_fence_before), and the warp has met
+// (__syncwarp) before the lane arrives; the issuer fences (tc_fence_after) between
+// its wait and the products that overwrite the columns.
 template <bool kPair>
 __device__ __forceinline__ void mbar_arrive_to(uint64_t* bar) {
   if constexpr (kPair)
