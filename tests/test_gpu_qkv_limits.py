@@ -172,8 +172,9 @@ def test_every_form_at_16_byte_boundaries(ja, form, N_img, d):
 @pytest.mark.parametrize("form", ["bf16", "fp8", "lora"])
 @pytest.mark.parametrize("B,H,N_img,d,C", [(16, 12, 1024, 64, 768), (4, 16, 2304, 128, 1024)])
 def test_outputs_at_16_byte_boundaries_are_not_slow(ja, form, B, H, N_img, d, C):
-    """Such a call takes the tiles of the others: less than 1.3 times their time (tiles of one head by single CTAs took
-    1.5 to 2 times).  The best of several runs of each, taken in turn."""
+    """Such a call takes the tiles of the others: at these sizes 1.03 to 1.25 times their time, where tiles of one head by
+    single CTAs took 1.57 to 2.5 times.  The border is between the two, (1.25 1.57)^(1/2) = 1.4.  The best of several
+    runs of each, taken in turn."""
     N_txt, rank, n = 77, 16, 4
     t = form_inputs(form, B, H, N_img, N_txt, d, C, rank, n, 312)
     odd = misaligned(ja, form, t, B, H, N_img, N_txt, d, C, rank, n)[0]
@@ -198,4 +199,4 @@ def test_outputs_at_16_byte_boundaries_are_not_slow(ja, form, B, H, N_img, d, C)
             b.record()
             torch.cuda.synchronize()
             best[i] = min(best[i], a.elapsed_time(b))
-    assert best[0] < 1.3 * best[1], best
+    assert best[0] < 1.4 * best[1], best
