@@ -52,7 +52,8 @@ typedef enum {
   JATTN_OK = 0,
   JATTN_ERR_INVALID_ARG = 1, /* null pointer, B/H/d <= 0, N_img/N_txt < 0, N < 1, size overflow */
   JATTN_ERR_UNSUPPORTED = 2, /* d not in {64, 128}; projections and token rows: C not a multiple of 8 (8-bit tokens:
-                                of 16; token rows: or above JATTN_MAX_WIDTH), rank not as jattn_qkv_norm_lora says */
+                                of 16; token rows: or above JATTN_MAX_WIDTH), rank not as jattn_qkv_norm_lora says,
+                                rotary pairs not as jattn_rope says */
   JATTN_ERR_MISALIGNED = 3,  /* a pointer is not 16-byte aligned */
   JATTN_ERR_ALIAS = 4,       /* an output buffer overlaps an input or another output */
   JATTN_ERR_CUDA = 5,        /* a CUDA launch or allocation failed */
@@ -263,6 +264,93 @@ int jattn_add_norm_bwd(const jattn_bf16* dy, const jattn_bf16* dh, const jattn_b
                        const float* g, int T, int C, jattn_bf16* dx, float* dg, void* work, void* stream);
 
 /*
+ * LayerNorm of token rows, with the residual's addition and with a gain and a
+ * bias of the model's own (items = 1) or of each batch item's (the scales and
+ * shifts of a modulated norm: re-diffusion README, "design notes" table, row
+ * "adaLN-Zero"; the pages print no equations).  The T rows of C values are
+ * `items` runs of T / items rows; row t belongs to item i:
+ *
+ *   h = bf16(x + res)                               (without res: h is x)
+ *   mu = mean_c h_c,  r = (mean_c (h_c - mu)^2 + eps)^(-1/2)      fp32
+ *   y = bf16(g_i (h - mu) r + b_i)
+ *
+ * A row with a NaN or an infinity comes out as NaN; one whose squares' sum passes
+ * the fp32 range as b_i.
+ *   x, res, h : as for jattn_add_norm (h may be res itself)
+ *   g         : [items, C] float32
+ *   b         : [items, C] float32, or NULL for none
+ *   items     : >= 1, a divisor of T
+ *   T, C, eps : as for jattn_add_norm
+ *   y         : [T, C] bf16
+ *   mean, r   : [T] float32, or NULL each when no backward will run
+ *
+ * jattn_layer_norm_bwd: with n = (h - mu) r and u = g_i dy, for the gradients dy of
+ * y and dh of h (or NULL: none),
+ *
+ *   dx = dh + r (u - mean_c(u) - n mean_c(u n))
+ *   dg_i = sum over the item's rows of dy n,   db_i = sum of dy
+ *
+ * dx [T, C] bf16 is the gradient of x and of res alike, and may be dh itself; dg and
+ * db (or NULL) [items, C] float32 are summed in an order that items, T and C alone
+ * set, so that all repeat bit for bit.  h, mean and r are the forward's.
+ *   work  : jattn_layer_norm_bwd_bytes(items, T, C) bytes, contents of no meaning
+ *           before or after; calls that overlap on the GPU need one each.
+ * jattn_layer_norm_bwd_bytes returns 0 for sizes the call would reject.
+ */
+int jattn_layer_norm(const jattn_bf16* x, const jattn_bf16* res, const float* g, const float* b, int items, int T,
+                     int C, float eps, jattn_bf16* h, jattn_bf16* y, float* mean, float* r, void* stream);
+size_t jattn_layer_norm_bwd_bytes(int items, int T, int C);
+int jattn_layer_norm_bwd(const jattn_bf16* dy, const jattn_bf16* dh, const jattn_bf16* h, const float* mean,
+                         const float* r, const float* g, int items, int T, int C, jattn_bf16* dx, float* dg,
+                         float* db, void* work, void* stream);
+
+/*
+ * Rotary positions on one to JATTN_MAX_AXES axes (a token's place in a text; height
+ * and width in an image; time as well in a video), with or without the QK-RMSNorm
+ * before them.  (No counterpart on the pages, whose model adds learned position
+ * vectors; their roadmap's native aspect buckets want positions that need none.)
+ * For every row x of q and of k, at token n of item b with positions pos[n] (or
+ * pos[b, n]):
+ *
+ *   z = g x (mean_c x_c^2 + eps)^(-1/2)            (without gains: z = x)
+ *   (z_i, z_j) -> (z_i cos t - z_j sin t, z_i sin t + z_j cos t)
+ *
+ * for each rotary pair p = 0 .. P - 1 with angle t = pos[.., axis of p] freq[p], the
+ * real product of the two fp32 values, (i, j) = (2 p, 2 p + 1) if interleaved, else
+ * (p, p + P); channels from 2 P on stay z.  fp32, then one rounding to bf16.
+ *   q, q_rot : [B, Hq, N, d] bf16; q_rot may be q itself
+ *   k, k_rot : [B, Hk, N, d] bf16; k_rot may be k itself
+ *   gq, gk   : [d] float32, or both NULL: no norm (and eps is not looked at)
+ *   pos      : [N, axes] float32, or with per_item != 0 [B, N, axes]; an axis on
+ *              which a token has no place (a caption's height) gets 0
+ *   freq     : [P] float32, radians per unit of position
+ *   pairs    : HOST array [axes], >= 0 each: axis 0 has the first pairs[0] pairs, axis 1
+ *              the next, ...; their sum P is a multiple of 8 (else JATTN_ERR_UNSUPPORTED),
+ *              8 .. d / 2; read during the call only
+ *   axes     : 1 .. JATTN_MAX_AXES (more: JATTN_ERR_UNSUPPORTED)
+ *   B, Hq, Hk, N : >= 1, B Hq N and B Hk N below 2^31
+ *   d        : 64 or 128
+ * The [H, T, d] layout of packed sequences is B = 1, with the positions of every row.
+ *
+ * jattn_rope_bwd: dq and dk from the gradients dq_rot and dk_rot of q_rot and k_rot
+ * (which they may be themselves), and with gains, for the q and k that the forward
+ * got, dgq and dgk (summed over b, h, n in an order that the sizes alone set: all
+ * repeat bit for bit).  Without gains q, k, dgq, dgk and work are NULL.
+ *   work  : jattn_rope_bwd_bytes(...) bytes with gains, contents of no meaning before
+ *           or after; calls that overlap on the GPU need one each.
+ * jattn_rope_bwd_bytes returns 0 for sizes the call would reject.
+ */
+#define JATTN_MAX_AXES 4
+int jattn_rope(const jattn_bf16* q, const jattn_bf16* k, const float* gq, const float* gk, const float* pos,
+               const float* freq, const int* pairs, int axes, int per_item, int interleaved, int B, int Hq, int Hk,
+               int N, int d, float eps, jattn_bf16* q_rot, jattn_bf16* k_rot, void* stream);
+size_t jattn_rope_bwd_bytes(int per_item, int B, int Hq, int Hk, int N, int d);
+int jattn_rope_bwd(const jattn_bf16* dq_rot, const jattn_bf16* dk_rot, const jattn_bf16* q, const jattn_bf16* k,
+                   const float* gq, const float* gk, const float* pos, const float* freq, const int* pairs, int axes,
+                   int per_item, int interleaved, int B, int Hq, int Hk, int N, int d, float eps, jattn_bf16* dq,
+                   jattn_bf16* dk, float* dgq, float* dgk, void* work, void* stream);
+
+/*
  * The projection from 8-bit tokens and weights (serving; 8-bit tokens carry
  * no gradient).  jattn_qkv_norm with rows in e4m3 and their fp32 scales, as
  * jattn_add_norm_fp8 and jattn_quant_rows write them:
@@ -400,7 +488,13 @@ typedef enum {
   JATTN_KERNEL_ADD_NORM_DG = 18,   /* dg from the partial sums */
   JATTN_KERNEL_QUANT_ROWS = 19,    /* rows to 8 bits */
   JATTN_KERNEL_LORA_DOWN = 20,     /* the adapters' first product (the projections themselves: QKV_NORM) */
-  JATTN_TOKEN_KERNEL_END = 21
+  JATTN_KERNEL_LAYER_NORM = 21,
+  JATTN_KERNEL_LAYER_NORM_BWD = 22,  /* its backward: dx and partial sums of dg, db */
+  JATTN_KERNEL_LAYER_NORM_SUMS = 23, /* dg, db from the partial sums */
+  JATTN_KERNEL_ROPE = 24,            /* rotary positions, and their backward without gains */
+  JATTN_KERNEL_ROPE_NORM_BWD = 25,   /* their backward with gains: dq, dk and partial sums of dgq, dgk */
+  JATTN_KERNEL_ROPE_GAINS = 26,      /* dgq, dgk from the partial sums */
+  JATTN_TOKEN_KERNEL_END = 27
 } jattn_token_kernel_kind;
 
 int jattn_profile_enable(int on);

@@ -16,7 +16,8 @@ from ._binding import (KERNEL_KINDS, STATUS, STATUS_CODE, JattnError, declared_s
                        jattn_fwd_train_varlen, jattn_bwd_train_varlen, jattn_qkv_norm, jattn_fwd_saved,
                        TOKEN_KERNEL_KINDS, jattn_add_norm, jattn_add_norm_fp8, jattn_quant_rows,
                        jattn_add_norm_bwd_bytes, jattn_add_norm_bwd, jattn_qkv_norm_fp8, jattn_qkv_norm_lora,
-                       jattn_qkv_norm_lora_bytes)
+                       jattn_qkv_norm_lora_bytes, jattn_layer_norm, jattn_layer_norm_bwd_bytes, jattn_layer_norm_bwd,
+                       jattn_rope, jattn_rope_bwd_bytes, jattn_rope_bwd)
 
 __all__ = ["STATUS", "STATUS_CODE", "JattnError", "declared_symbols", "jattn_bwd", "jattn_fwd",
            "jattn_last_device_error", "jattn_status_string", "jattn_version", "load_library", "forward",
@@ -29,7 +30,8 @@ __all__ = ["STATUS", "STATUS_CODE", "JattnError", "declared_symbols", "jattn_bwd
            "qkv_norm", "TOKEN_KERNEL_KINDS", "jattn_add_norm", "jattn_add_norm_fp8", "jattn_quant_rows",
            "jattn_add_norm_bwd_bytes", "jattn_add_norm_bwd", "add_norm", "add_norm_fp8", "add_norm_backward",
            "quant_rows", "jattn_qkv_norm_fp8", "jattn_qkv_norm_lora", "jattn_qkv_norm_lora_bytes", "qkv_norm_fp8",
-           "qkv_norm_lora"]
+           "qkv_norm_lora", "jattn_layer_norm", "jattn_layer_norm_bwd_bytes", "jattn_layer_norm_bwd", "layer_norm",
+           "layer_norm_backward", "jattn_rope", "jattn_rope_bwd_bytes", "jattn_rope_bwd", "rope", "rope_backward"]
 
 
 def forward(q, k, v, gq, gk, n_txt: int, stream=None):
@@ -247,3 +249,78 @@ def qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, H: int, down
     jattn_qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_img, up_img, down_txt, up_txt, scale,
                         index, scale.numel(), rank, *sizes, *(t.data_ptr() for t in out), work.data_ptr(), stream)
     return out
+
+
+def layer_norm(x, g, b=None, residual=None, eps: float = 1e-6, stream=None):
+    """y, h, mean, r: LayerNorm of the token rows h = x + residual (h is x without a residual) over their
+    last axis.  x, residual, h, y [..., C] bf16; gain g and bias b (or None) fp32, [C], or [items, C] for
+    batch items of equally many rows each with their own; mean, r [...] fp32 for layer_norm_backward."""
+    import torch
+
+    with _outputs_on(stream, x, g, b, residual):
+        y = torch.empty_like(x)
+        h = x if residual is None else torch.empty_like(x)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        r = torch.empty_like(mean)
+    C = g.shape[-1]
+    jattn_layer_norm(x, residual, g, b, g.numel() // C, r.numel(), C, eps, None if residual is None else h.data_ptr(),
+                     y.data_ptr(), mean.data_ptr(), r.data_ptr(), stream)
+    return y, h, mean, r
+
+
+def layer_norm_backward(dy, h, mean, r, g, dh=None, bias: bool = True, stream=None):
+    """dx, dg, db from layer_norm's h, mean and r: dx is the gradient of x and of the residual alike, dg and
+    db (None without bias) have g's shape; dh is the gradient of h from later uses of it (None: none)."""
+    import torch
+
+    T, C = r.numel(), g.shape[-1]
+    items = g.numel() // C
+    with _outputs_on(stream, dy, h, mean, r, g, dh):
+        dx, dg = torch.empty_like(dy), torch.empty_like(g)
+        db = torch.empty_like(g) if bias else None
+        work = _buffer(jattn_layer_norm_bwd_bytes(items, T, C), dy.device)
+    jattn_layer_norm_bwd(dy, dh, h, mean, r, g, items, T, C, dx.data_ptr(), dg.data_ptr(),
+                         db.data_ptr() if bias else None, work.data_ptr(), stream)
+    return dx, dg, db
+
+
+def _rope_sizes(q, k, pos):
+    """Whether the positions are each item's own, and B, Hq, Hk, N, d of [B, H, N, d] or packed [H, T, d] tensors."""
+    if q.dim() not in (3, 4) or k.dim() != q.dim() or q.shape[-2:] != k.shape[-2:] or q.shape[:-3] != k.shape[:-3]:
+        raise ValueError(f"q and k: expected [B, H, N, d] or [H, T, d] with heads of their own, got {tuple(q.shape)} "
+                         f"and {tuple(k.shape)}")
+    B = q.shape[0] if q.dim() == 4 else 1
+    return pos.dim() == 3, B, q.shape[-3], k.shape[-3], q.shape[-2], q.shape[-1]
+
+
+def rope(q, k, pos, freq, pairs, gq=None, gk=None, interleaved: bool = False, eps: float = 1e-6, stream=None):
+    """q_rot, k_rot: rotary positions of q [B, Hq, N, d] and k [B, Hk, N, d] (or packed [H, T, d]) bf16, after
+    the QK-RMSNorm with gains gq, gk [d] fp32 if they are given.  pos [N, axes], or [B, N, axes] for
+    positions of each item's own, and freq [P] fp32 (radians per unit); pairs: host ints, how many of the
+    P channel pairs each axis has.  Pair p is channels (2 p, 2 p + 1) if interleaved, else (p, p + P)."""
+    import torch
+
+    with _outputs_on(stream, q, k, pos, freq, gq, gk):
+        q_rot, k_rot = torch.empty_like(q), torch.empty_like(k)
+    per_item, *sizes = _rope_sizes(q, k, pos)
+    jattn_rope(q, k, gq, gk, pos, freq, pairs, per_item, interleaved, *sizes, eps, q_rot.data_ptr(), k_rot.data_ptr(),
+               stream)
+    return q_rot, k_rot
+
+
+def rope_backward(dq_rot, dk_rot, pos, freq, pairs, q=None, k=None, gq=None, gk=None, interleaved: bool = False,
+                  eps: float = 1e-6, stream=None):
+    """dq, dk, dgq, dgk from the gradients of rope's outputs; q, k, gq, gk as rope got them with gains, and
+    None without (dgq and dgk are None then)."""
+    import torch
+
+    per_item, *sizes = _rope_sizes(dq_rot, dk_rot, pos)
+    norm = gq is not None
+    with _outputs_on(stream, dq_rot, dk_rot, pos, freq, q, k, gq, gk):
+        dq, dk = torch.empty_like(dq_rot), torch.empty_like(dk_rot)
+        dgq, dgk = (torch.empty_like(gq), torch.empty_like(gk)) if norm else (None, None)
+        work = _buffer(jattn_rope_bwd_bytes(per_item, *sizes), dq_rot.device) if norm else None
+    jattn_rope_bwd(dq_rot, dk_rot, q if norm else None, k if norm else None, gq, gk, pos, freq, pairs, per_item,
+                   interleaved, *sizes, eps, dq.data_ptr(), dk.data_ptr(), dgq.data_ptr() if norm else None,
+                   dgk.data_ptr() if norm else None, work, stream)
+    return dq, dk, dgq, dgk

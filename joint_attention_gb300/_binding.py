@@ -122,13 +122,25 @@ def load_library(path: str | None = None, build_if_missing: bool = False) -> cty
     lib.jattn_qkv_norm_lora_bytes.restype = sz
     lib.jattn_qkv_norm_lora.argtypes = [vp] * 14 + [i32] * 8 + [vp] * 6
     lib.jattn_qkv_norm_lora.restype = i32
+    lib.jattn_layer_norm.argtypes = [vp] * 4 + [i32] * 3 + [f32c] + [vp] * 5
+    lib.jattn_layer_norm.restype = i32
+    lib.jattn_layer_norm_bwd_bytes.argtypes = [i32] * 3
+    lib.jattn_layer_norm_bwd_bytes.restype = sz
+    lib.jattn_layer_norm_bwd.argtypes = [vp] * 6 + [i32] * 3 + [vp] * 5
+    lib.jattn_layer_norm_bwd.restype = i32
+    lib.jattn_rope.argtypes = [vp] * 6 + [i32p] + [i32] * 8 + [f32c] + [vp] * 3
+    lib.jattn_rope.restype = i32
+    lib.jattn_rope_bwd_bytes.argtypes = [i32] * 6
+    lib.jattn_rope_bwd_bytes.restype = sz
+    lib.jattn_rope_bwd.argtypes = [vp] * 8 + [i32p] + [i32] * 8 + [f32c] + [vp] * 6
+    lib.jattn_rope_bwd.restype = i32
     if path is None:
         _lib = lib
     return lib
 
 
 KERNEL_KINDS = 6
-TOKEN_KERNEL_KINDS = range(16, 21)  # the token-row kernels' kinds, numbered apart
+TOKEN_KERNEL_KINDS = range(16, 27)  # the token-row kernels' kinds, numbered apart
 
 
 def jattn_profile_enable(on: bool = True) -> int:
@@ -518,6 +530,97 @@ def jattn_add_norm_bwd(dy, dh, h, r, g, T: int, C: int, dx, dg, work, stream=Non
                                 _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_add_norm_bwd")
+    return rc
+
+
+def jattn_layer_norm(x, res, g, b, items: int, T: int, C: int, eps: float, h, y, mean, r, stream=None,
+                     check: bool = True) -> int:
+    """C ABI jattn_layer_norm.  x / res / h / y [T, C] bf16 (res and h both or neither; h may be res),
+    g / b (or None) [items, C] fp32, mean / r [T] fp32 or None."""
+    import torch
+
+    bf, f32, e = torch.bfloat16, torch.float32, T * C
+    rc = load_library().jattn_layer_norm(_ptr(x, "x", bf, e), _ptr(res, "res", bf, e), _ptr(g, "g", f32, items * C),
+                                         _ptr(b, "b", f32, items * C), _size(items), _size(T), _size(C), eps,
+                                         _ptr(h, "h", bf, e), _ptr(y, "y", bf, e), _ptr(mean, "mean", f32, T),
+                                         _ptr(r, "r", f32, T), _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_layer_norm")
+    return rc
+
+
+@functools.lru_cache(maxsize=1024)
+def jattn_layer_norm_bwd_bytes(items: int, T: int, C: int) -> int:
+    """C ABI jattn_layer_norm_bwd_bytes: size of the work buffer of jattn_layer_norm_bwd (0: it rejects the sizes)."""
+    return int(load_library().jattn_layer_norm_bwd_bytes(_size(items), _size(T), _size(C)))
+
+
+def jattn_layer_norm_bwd(dy, dh, h, mean, r, g, items: int, T: int, C: int, dx, dg, db, work, stream=None,
+                         check: bool = True) -> int:
+    """C ABI jattn_layer_norm_bwd.  dy / dh (or None) / h / dx [T, C] bf16 (dx may be dh), mean / r [T] fp32,
+    g / dg / db (or None) [items, C] fp32, work jattn_layer_norm_bwd_bytes(items, T, C) bytes."""
+    import torch
+
+    bf, f32, e = torch.bfloat16, torch.float32, T * C
+    rc = load_library().jattn_layer_norm_bwd(
+        _ptr(dy, "dy", bf, e), _ptr(dh, "dh", bf, e), _ptr(h, "h", bf, e), _ptr(mean, "mean", f32, T),
+        _ptr(r, "r", f32, T), _ptr(g, "g", f32, items * C), _size(items), _size(T), _size(C), _ptr(dx, "dx", bf, e),
+        _ptr(dg, "dg", f32, items * C), _ptr(db, "db", f32, items * C),
+        _work_ptr(work, jattn_layer_norm_bwd_bytes, items, T, C), _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_layer_norm_bwd")
+    return rc
+
+
+def _pairs_array(pairs):
+    """Host int array (ctypes) of the axes' pairs, the count of axes and of pairs."""
+    vals = [int(x) for x in pairs]
+    return (ctypes.c_int * len(vals))(*vals), len(vals), sum(vals)
+
+
+def jattn_rope(q, k, gq, gk, pos, freq, pairs, per_item: bool, interleaved: bool, B: int, Hq: int, Hk: int, N: int,
+               d: int, eps: float, q_rot, k_rot, stream=None, check: bool = True) -> int:
+    """C ABI jattn_rope.  q / q_rot [B, Hq, N, d] and k / k_rot [B, Hk, N, d] bf16 (in place: the same), gq / gk [d]
+    fp32 or both None, pos [N, axes] (per_item: [B, N, axes]) and freq [sum of pairs] fp32, pairs host ints."""
+    import torch
+
+    bf, f32 = torch.bfloat16, torch.float32
+    arr, axes, P = _pairs_array(pairs)
+    eq, ek = B * Hq * N * d, B * Hk * N * d
+    rc = load_library().jattn_rope(
+        _ptr(q, "q", bf, eq), _ptr(k, "k", bf, ek), _ptr(gq, "gq", f32, d), _ptr(gk, "gk", f32, d),
+        _ptr(pos, "pos", f32, (B if per_item else 1) * N * axes), _ptr(freq, "freq", f32, P), arr, axes, bool(per_item),
+        bool(interleaved), _size(B), _size(Hq), _size(Hk), _size(N), _size(d), eps, _ptr(q_rot, "q_rot", bf, eq),
+        _ptr(k_rot, "k_rot", bf, ek), _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_rope")
+    return rc
+
+
+@functools.lru_cache(maxsize=1024)
+def jattn_rope_bwd_bytes(per_item: bool, B: int, Hq: int, Hk: int, N: int, d: int) -> int:
+    """C ABI jattn_rope_bwd_bytes: size of the work buffer of jattn_rope_bwd with gains (0: it rejects the sizes)."""
+    return int(load_library().jattn_rope_bwd_bytes(bool(per_item), *map(_size, (B, Hq, Hk, N, d))))
+
+
+def jattn_rope_bwd(dq_rot, dk_rot, q, k, gq, gk, pos, freq, pairs, per_item: bool, interleaved: bool, B: int, Hq: int,
+                   Hk: int, N: int, d: int, eps: float, dq, dk, dgq, dgk, work, stream=None, check: bool = True) -> int:
+    """C ABI jattn_rope_bwd (layouts as jattn_rope; dq may be dq_rot, dk may be dk_rot).  Without gains q, k, gq, gk,
+    dgq, dgk and work are None; with gains work has jattn_rope_bwd_bytes(...) bytes."""
+    import torch
+
+    bf, f32 = torch.bfloat16, torch.float32
+    arr, axes, P = _pairs_array(pairs)
+    eq, ek = B * Hq * N * d, B * Hk * N * d
+    rc = load_library().jattn_rope_bwd(
+        _ptr(dq_rot, "dq_rot", bf, eq), _ptr(dk_rot, "dk_rot", bf, ek), _ptr(q, "q", bf, eq), _ptr(k, "k", bf, ek),
+        _ptr(gq, "gq", f32, d), _ptr(gk, "gk", f32, d), _ptr(pos, "pos", f32, (B if per_item else 1) * N * axes),
+        _ptr(freq, "freq", f32, P), arr, axes, bool(per_item), bool(interleaved), _size(B), _size(Hq), _size(Hk),
+        _size(N), _size(d), eps, _ptr(dq, "dq", bf, eq), _ptr(dk, "dk", bf, ek), _ptr(dgq, "dgq", f32, d),
+        _ptr(dgk, "dgk", f32, d), _work_ptr(work, jattn_rope_bwd_bytes, bool(per_item), B, Hq, Hk, N, d),
+        _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_rope_bwd")
     return rc
 
 

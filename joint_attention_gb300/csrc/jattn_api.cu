@@ -1068,6 +1068,237 @@ extern "C" int jattn_add_norm_bwd(const jattn_bf16* dy, const jattn_bf16* dh, co
   return JATTN_OK;
 }
 
+namespace {
+
+int check_items(int items, int T, int C) {
+  const int rc = check_rows(T, C);
+  if (rc != JATTN_OK) return rc;
+  return items <= 0 || T % items != 0 ? JATTN_ERR_INVALID_ARG : JATTN_OK;
+}
+
+}  // namespace
+
+extern "C" int jattn_layer_norm(const jattn_bf16* x, const jattn_bf16* res, const float* g, const float* b, int items,
+                                int T, int C, float eps, jattn_bf16* h, jattn_bf16* y, float* mean, float* r,
+                                void* stream) {
+  if (!x || !g || !y || (res == nullptr) != (h == nullptr) || !eps_ok(eps)) return JATTN_ERR_INVALID_ARG;
+  const int rc = check_items(items, T, C);
+  if (rc != JATTN_OK) return rc;
+  const void* ptrs[] = {x, res, g, b, h, y, mean, r};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return JATTN_ERR_MISALIGNED;
+  const size_t tb = static_cast<size_t>(T) * C * 2, rows = static_cast<size_t>(T) * 4;
+  const size_t gb = static_cast<size_t>(items) * C * 4;
+  const Range ins[] = {range_of(x, tb), range_of(res, res ? tb : 0), range_of(g, gb), range_of(b, b ? gb : 0)};
+  const Range outs[] = {range_of(h, h ? tb : 0), range_of(y, tb), range_of(mean, mean ? rows : 0),
+                        range_of(r, r ? rows : 0)};
+  if (any_alias(ins, outs, outs[0], ins[1])) return JATTN_ERR_ALIAS;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t ce;
+  {
+    Timed t(JATTN_KERNEL_LAYER_NORM, st);
+    ce = launch_layer_norm(LayerNorm{x, res, g, b, items, T, C, eps, h, y, mean, r}, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "layer_norm launch", ce);
+  return JATTN_OK;
+}
+
+extern "C" size_t jattn_layer_norm_bwd_bytes(int items, int T, int C) {
+  if (check_items(items, T, C) != JATTN_OK) return 0;
+  return static_cast<size_t>(items) * layer_norm_bwd_parts(items, T, C) * 2 * C * sizeof(float);
+}
+
+extern "C" int jattn_layer_norm_bwd(const jattn_bf16* dy, const jattn_bf16* dh, const jattn_bf16* h, const float* mean,
+                                    const float* r, const float* g, int items, int T, int C, jattn_bf16* dx,
+                                    float* dg, float* db, void* work, void* stream) {
+  if (!dy || !h || !mean || !r || !g || !dx || !dg || !work) return JATTN_ERR_INVALID_ARG;
+  const int rc = check_items(items, T, C);
+  if (rc != JATTN_OK) return rc;
+  const void* ptrs[] = {dy, dh, h, mean, r, g, dx, dg, db, work};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return JATTN_ERR_MISALIGNED;
+  const size_t tb = static_cast<size_t>(T) * C * 2, rows = static_cast<size_t>(T) * 4;
+  const size_t gb = static_cast<size_t>(items) * C * 4;
+  const Range ins[] = {range_of(dy, tb),     range_of(dh, dh ? tb : 0), range_of(h, tb),
+                       range_of(mean, rows), range_of(r, rows),         range_of(g, gb)};
+  const Range outs[] = {range_of(dx, tb), range_of(dg, gb), range_of(db, db ? gb : 0),
+                        range_of(work, jattn_layer_norm_bwd_bytes(items, T, C))};
+  if (any_alias(ins, outs, outs[0], ins[1])) return JATTN_ERR_ALIAS;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* part = static_cast<float*>(work);
+  const LayerNormBwd t{dy, dh, h, mean, r, g, items, T, C, dx, dg, db};
+  const int parts = layer_norm_bwd_parts(items, T, C);
+  cudaError_t ce;
+  {
+    Timed timed(JATTN_KERNEL_LAYER_NORM_BWD, st);
+    ce = launch_layer_norm_bwd(t, part, parts, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "layer_norm_bwd launch", ce);
+  {
+    Timed timed(JATTN_KERNEL_LAYER_NORM_SUMS, st);
+    ce = launch_layer_norm_sums(part, parts, t, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "layer_norm_sums launch", ce);
+  return JATTN_OK;
+}
+
+namespace {
+
+static_assert(kMaxAxes == JATTN_MAX_AXES, "the kernels' axes are the header's");
+
+// The sizes of a rotary call; positions and pairs by check_pairs.
+int check_rope(int per_item, int B, int Hq, int Hk, int N, int d, Rope* t) {
+  if (B <= 0 || Hq <= 0 || Hk <= 0 || N <= 0 || d <= 0) return JATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return JATTN_ERR_UNSUPPORTED;
+  const int64_t limit = int64_t{1} << 31, most = Hq > Hk ? Hq : Hk;
+  if (B * most >= limit || B * most * N >= limit) return JATTN_ERR_INVALID_ARG;
+  t->B = B;
+  t->Hq = Hq;
+  t->Hk = Hk;
+  t->N = N;
+  t->d = d;
+  t->per_item = per_item != 0;
+  return JATTN_OK;
+}
+
+int check_pairs(const int* pairs, int axes, Rope* t) {
+  if (!pairs || axes <= 0) return JATTN_ERR_INVALID_ARG;
+  if (axes > kMaxAxes) return JATTN_ERR_UNSUPPORTED;
+  int64_t sum = 0;
+  for (int i = 0; i < axes; ++i) {
+    if (pairs[i] < 0) return JATTN_ERR_INVALID_ARG;
+    sum += pairs[i];
+    t->pairs[i] = pairs[i];
+  }
+  t->axes = axes;
+  if (sum <= 0 || 2 * sum > t->d) return JATTN_ERR_INVALID_ARG;
+  return sum % 8 != 0 ? JATTN_ERR_UNSUPPORTED : JATTN_OK;
+}
+
+// Sizes in bytes of a rotary call's tensors.
+struct RopeBytes {
+  size_t q, k, pos, freq, g;
+  explicit RopeBytes(const Rope& t) {
+    const size_t row = static_cast<size_t>(t.d) * 2, tokens = static_cast<size_t>(t.B) * t.N;
+    q = tokens * t.Hq * row;
+    k = tokens * t.Hk * row;
+    pos = (t.per_item ? tokens : t.N) * t.axes * 4;
+    freq = 0;
+    for (int i = 0; i < t.axes; ++i) freq += static_cast<size_t>(t.pairs[i]) * 4;
+    g = static_cast<size_t>(t.d) * 4;
+  }
+};
+
+// As any_alias, with two outputs that may be exactly the inputs that they replace.
+template <size_t I, size_t O>
+bool any_alias2(const Range (&ins)[I], const Range (&outs)[O]) {
+  auto equal = [](Range a, Range b) { return a.lo == b.lo && a.hi == b.hi; };
+  for (size_t a = 0; a < O; ++a) {
+    for (size_t i = 0; i < I; ++i)
+      if (overlaps(outs[a], ins[i]) && !(a < 2 && a == i && equal(outs[a], ins[i]))) return true;
+    for (size_t b = a + 1; b < O; ++b)
+      if (overlaps(outs[a], outs[b])) return true;
+  }
+  return false;
+}
+
+}  // namespace
+
+extern "C" int jattn_rope(const jattn_bf16* q, const jattn_bf16* k, const float* gq, const float* gk,
+                          const float* pos, const float* freq, const int* pairs, int axes, int per_item,
+                          int interleaved, int B, int Hq, int Hk, int N, int d, float eps, jattn_bf16* q_rot,
+                          jattn_bf16* k_rot, void* stream) {
+  if (!q || !k || !pos || !freq || !q_rot || !k_rot || (gq == nullptr) != (gk == nullptr) || (gq && !eps_ok(eps)))
+    return JATTN_ERR_INVALID_ARG;
+  Rope t = {};
+  int rc = check_rope(per_item, B, Hq, Hk, N, d, &t);
+  if (rc == JATTN_OK) rc = check_pairs(pairs, axes, &t);
+  if (rc != JATTN_OK) return rc;
+  const void* ptrs[] = {q, k, gq, gk, pos, freq, q_rot, k_rot};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return JATTN_ERR_MISALIGNED;
+  const RopeBytes n(t);
+  const Range ins[] = {range_of(q, n.q),           range_of(k, n.k),     range_of(pos, n.pos), range_of(freq, n.freq),
+                       range_of(gq, gq ? n.g : 0), range_of(gk, gk ? n.g : 0)};
+  const Range outs[] = {range_of(q_rot, n.q), range_of(k_rot, n.k)};
+  if (any_alias2(ins, outs)) return JATTN_ERR_ALIAS;
+  t.pos = pos;
+  t.freq = freq;
+  t.interleaved = interleaved != 0;
+  t.gq = gq;
+  t.gk = gk;
+  t.eps = eps;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t ce;
+  {
+    Timed timed(JATTN_KERNEL_ROPE, st);
+    ce = launch_rope(t, q, k, q_rot, k_rot, false, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "rope launch", ce);
+  return JATTN_OK;
+}
+
+extern "C" size_t jattn_rope_bwd_bytes(int per_item, int B, int Hq, int Hk, int N, int d) {
+  Rope t = {};
+  if (check_rope(per_item, B, Hq, Hk, N, d, &t) != JATTN_OK) return 0;
+  int64_t of_q;
+  return static_cast<size_t>(rope_bwd_parts(t, &of_q)) * d * sizeof(float);
+}
+
+extern "C" int jattn_rope_bwd(const jattn_bf16* dq_rot, const jattn_bf16* dk_rot, const jattn_bf16* q,
+                              const jattn_bf16* k, const float* gq, const float* gk, const float* pos,
+                              const float* freq, const int* pairs, int axes, int per_item, int interleaved, int B,
+                              int Hq, int Hk, int N, int d, float eps, jattn_bf16* dq, jattn_bf16* dk, float* dgq,
+                              float* dgk, void* work, void* stream) {
+  if (!dq_rot || !dk_rot || !pos || !freq || !dq || !dk) return JATTN_ERR_INVALID_ARG;
+  const bool norm = gq != nullptr;
+  for (const void* p : {static_cast<const void*>(q), static_cast<const void*>(k), static_cast<const void*>(gk),
+                        static_cast<const void*>(dgq), static_cast<const void*>(dgk), static_cast<const void*>(work)})
+    if ((p != nullptr) != norm) return JATTN_ERR_INVALID_ARG;
+  if (norm && !eps_ok(eps)) return JATTN_ERR_INVALID_ARG;
+  Rope t = {};
+  int rc = check_rope(per_item, B, Hq, Hk, N, d, &t);
+  if (rc == JATTN_OK) rc = check_pairs(pairs, axes, &t);
+  if (rc != JATTN_OK) return rc;
+  const void* ptrs[] = {dq_rot, dk_rot, q, k, gq, gk, pos, freq, dq, dk, dgq, dgk, work};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return JATTN_ERR_MISALIGNED;
+  const RopeBytes n(t);
+  const size_t gb = norm ? n.g : 0, wb = norm ? jattn_rope_bwd_bytes(per_item, B, Hq, Hk, N, d) : 0;
+  const Range ins[] = {range_of(dq_rot, n.q),         range_of(dk_rot, n.k),         range_of(q, norm ? n.q : 0),
+                       range_of(k, norm ? n.k : 0),   range_of(pos, n.pos),          range_of(freq, n.freq),
+                       range_of(gq, gb),              range_of(gk, gb)};
+  const Range outs[] = {range_of(dq, n.q), range_of(dk, n.k), range_of(dgq, gb), range_of(dgk, gb),
+                        range_of(work, wb)};
+  if (any_alias2(ins, outs)) return JATTN_ERR_ALIAS;
+  t.pos = pos;
+  t.freq = freq;
+  t.interleaved = interleaved != 0;
+  t.gq = gq;
+  t.gk = gk;
+  t.eps = eps;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t ce;
+  if (!norm) {
+    Timed timed(JATTN_KERNEL_ROPE, st);
+    ce = launch_rope(t, dq_rot, dk_rot, dq, dk, true, st);
+    if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "rope backward launch", ce);
+    return JATTN_OK;
+  }
+  float* part = static_cast<float*>(work);
+  {
+    Timed timed(JATTN_KERNEL_ROPE_NORM_BWD, st);
+    ce = launch_rope_norm_bwd(t, dq_rot, dk_rot, q, k, dq, dk, part, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "rope_norm_bwd launch", ce);
+  {
+    Timed timed(JATTN_KERNEL_ROPE_GAINS, st);
+    ce = launch_rope_gains(t, part, dgq, dgk, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "rope_gains launch", ce);
+  return JATTN_OK;
+}
+
 namespace jattn {
 
 // One thread waits on an mbarrier that nothing arrives at, through the same
@@ -1180,6 +1411,12 @@ extern "C" const char* jattn_kernel_name(int kind) {
     case JATTN_KERNEL_ADD_NORM_DG: return "add_norm_dg";
     case JATTN_KERNEL_QUANT_ROWS: return "quant_rows";
     case JATTN_KERNEL_LORA_DOWN: return "lora_down";
+    case JATTN_KERNEL_LAYER_NORM: return "layer_norm";
+    case JATTN_KERNEL_LAYER_NORM_BWD: return "layer_norm_bwd";
+    case JATTN_KERNEL_LAYER_NORM_SUMS: return "layer_norm_sums";
+    case JATTN_KERNEL_ROPE: return "rope";
+    case JATTN_KERNEL_ROPE_NORM_BWD: return "rope_norm_bwd";
+    case JATTN_KERNEL_ROPE_GAINS: return "rope_gains";
     default: return "unknown";
   }
 }
@@ -1190,7 +1427,7 @@ extern "C" const char* jattn_status_string(int status) {
     case JATTN_ERR_INVALID_ARG: return "invalid argument (null pointer, non-positive or overflowing size)";
     case JATTN_ERR_UNSUPPORTED:
       return "unsupported size (d must be 64 or 128; C a multiple of 8, or of 16 for 8-bit tokens, and for token "
-             "rows at most 16384; a rank a multiple of 8, at most 128)";
+             "rows at most 16384; a rank a multiple of 8, at most 128; rotary pairs a multiple of 8 on at most 4 axes)";
     case JATTN_ERR_MISALIGNED: return "pointer not 16-byte aligned";
     case JATTN_ERR_ALIAS: return "an output buffer overlaps another buffer";
     case JATTN_ERR_CUDA: return "CUDA launch or allocation failed";

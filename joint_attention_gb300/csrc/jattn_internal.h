@@ -136,6 +136,53 @@ cudaError_t launch_add_norm_bwd(const uint16_t* dy, const uint16_t* dh, const ui
                                 cudaStream_t st);
 cudaError_t launch_dg_sum(const float* part, int parts, int C, float* dg, cudaStream_t st);
 
+// LayerNorm: h = bf16(x + res), mu = mean h, r = (mean (h - mu)^2 + eps)^(-1/2),
+// y = bf16(g (h - mu) r + b), with gain and bias rows of `items` equal runs of rows.
+struct LayerNorm {
+  const uint16_t *x, *res;  // res: or null (then h is null)
+  const float *g, *b;       // [items, C]; b: or null
+  int items, T, C;          // T a multiple of items; C as above
+  float eps;
+  uint16_t *h, *y;
+  float *mean, *r;  // or null
+};
+cudaError_t launch_layer_norm(const LayerNorm& t, cudaStream_t st);
+struct LayerNormBwd {
+  const uint16_t *dy, *dh, *h;  // dh: or null
+  const float *mean, *r, *g;
+  int items, T, C;
+  uint16_t* dx;
+  float *dg, *db;  // [items, C]; db: or null
+};
+// layer_norm_bwd_parts(items, T, C) blocks an item, each writing C partial sums of
+// dg, and of db if there is one, to part; launch_layer_norm_sums adds an item's in a
+// fixed order.
+int layer_norm_bwd_parts(int items, int T, int C);
+cudaError_t launch_layer_norm_bwd(const LayerNormBwd& t, float* part, int parts, cudaStream_t st);
+cudaError_t launch_layer_norm_sums(const float* part, int parts, const LayerNormBwd& t, cudaStream_t st);
+
+// --- rotary positions (HBM-bound) ---------------------------------------------
+constexpr int kMaxAxes = 4;
+struct Rope {
+  int B, Hq, Hk, N, d;  // q [B, Hq, N, d], k [B, Hk, N, d]
+  const float* pos;     // [N, axes], or with per_item [B, N, axes]
+  bool per_item;
+  const float* freq;    // [sum of pairs]
+  int axes, pairs[kMaxAxes];
+  bool interleaved;
+  const float *gq, *gk;  // [d] gains of the QK-RMSNorm, or both null
+  float eps;
+};
+// backward: the rotation's transpose (no gains).
+cudaError_t launch_rope(const Rope& t, const uint16_t* q, const uint16_t* k, uint16_t* q_out, uint16_t* k_out,
+                        bool backward, cudaStream_t st);
+// With gains: part holds d partial sums for each of rope_bwd_parts blocks, of_q of q
+// and the others of k, which launch_rope_gains adds in a fixed order.
+int64_t rope_bwd_parts(const Rope& t, int64_t* of_q);
+cudaError_t launch_rope_norm_bwd(const Rope& t, const uint16_t* dq_rot, const uint16_t* dk_rot, const uint16_t* q,
+                                 const uint16_t* k, uint16_t* dq, uint16_t* dk, float* part, cudaStream_t st);
+cudaError_t launch_rope_gains(const Rope& t, const float* part, float* dgq, float* dgk, cudaStream_t st);
+
 // --- tensor-core attention kernels ------------------------------------------
 struct AttnShape {
   int BH;        // heads (B*H, or H for a packed variable-length call)
@@ -153,6 +200,25 @@ cudaError_t launch_attn_fwd(const CUtensorMap& map_q, const CUtensorMap& map_k, 
                             const AttnShape& s, uint16_t* out, float* lse, uint32_t* dev_err, cudaStream_t st,
                             float* dq_zero = nullptr, uint32_t* zero_count = nullptr);
 int attn_fwd_grid(const AttnShape& s);
+
+// Packed sequences with grouped heads: q [Hq, T, d], k and v [Hk, T, d] as they are (no
+// norm), causal or not.  seg: the sequences that have rows (seg.rows = T, which may lie
+// behind the last one).
+struct GroupedShape {
+  int Hq, Hk, T, d;
+  bool causal;
+  float scale;
+  bool deterministic;  // backward: fixed dQ accumulation order
+  SegTable seg;
+};
+cudaError_t launch_attn_fwd_grouped(const GroupedShape& s, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                    uint16_t* out, float* lse, uint32_t* dev_err, cudaStream_t st);
+// After launch_bwd_prep on the query heads (stats, and dqacc [Hq, T, d] and counters zeroed:
+// one word per 128 padded rows of a query head); launch_grouped_dq then makes dq of dqacc.
+cudaError_t launch_attn_bwd_grouped(const GroupedShape& s, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                    const uint16_t* dout, const uint16_t* stats, float* dqacc, uint32_t* counters,
+                                    uint16_t* dk, uint16_t* dv, uint32_t* dev_err, cudaStream_t st);
+cudaError_t launch_grouped_dq(const GroupedShape& s, const float* dqacc, uint16_t* dq, cudaStream_t st);
 
 // map_stats: a TMA map over the bf16 statistics chunks (encode_stats_map);
 // map_dq one over the fp32 dQ accumulator (encode_dq_map).  The accumulator must be zeroed unless

@@ -1,0 +1,329 @@
+"""LayerNorm of token rows with the residual's addition, with gains and biases of the model's or of
+each item's own, and its backward, against their definitions in float64.
+
+Tolerances, from the arithmetic (u = 2^-24, one fp32 rounding; a sum over a row passes at most 28
+roundings on any path: at most 16 in a lane, 10 joining the lanes, and the mean's factor):
+* h is the exact sum rounded once to bf16: equal bits.
+* The first mean m0 is off by D = 28 u mean|h| at most.  With c = h - mu, h - m0 rounds once and its
+  mean is off by 28 u (mean|c| + D): the centred values are off by 30 u (mean|c| + D) + u |c|.
+  Below 2^-126 an addition rounds by 2^-150 at most whatever the terms: C 2^-149 for both means' sums.
+* r: the squares' sum 28 u, the mean and eps 2 u, halved by the root, which rounds once: 2^-19
+  relative, and 64 u D^2 / (var + eps) for the correction by the square of the second mean.
+* y: half a bf16 step (2^-8 relative), the centred values' error times r and g, and n = c r with r's.
+* dx: half a bf16 step and 64 u of the terms' magnitudes; dg, db: a fixed tree over the rows, at most
+  128 roundings on any path at these sizes: 128 u of the terms' magnitudes.
+"""
+import pytest
+import torch
+
+from joint_attention_gb300 import STATUS_CODE
+import joint_attention_gb300 as pkg
+from joint_attention_gb300.build import build
+
+U = 2.0 ** -24
+EPS = 1e-6
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build()
+    return pkg.load_library()
+
+
+@pytest.fixture(scope="module")
+def ja(lib):
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    return pkg
+
+
+def randn(shape, seed, scale=1.0, dtype=torch.bfloat16, shift=0.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale + shift).to(dtype)
+
+
+def gains(shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.rand(shape, generator=g, device="cuda") + 0.5
+
+
+def by_rows(p, T, C):
+    """A gain or bias [C] or [items, C] for each of T rows, float64."""
+    p = p.double().view(-1, C)
+    return p.repeat_interleave(T // p.shape[0], 0)
+
+
+def check_norm(out, x, res, g, b, eps=EPS):
+    y, h, mean, r = out
+    C = x.shape[-1]
+    x, h, y = x.reshape(-1, C), h.reshape(-1, C), y.reshape(-1, C)
+    h0 = x if res is None else (x.double() + res.reshape(-1, C).double()).to(torch.bfloat16)
+    assert torch.equal(h.view(torch.int16), h0.view(torch.int16))
+    h0 = h0.double()
+    mu = h0.mean(-1, keepdim=True)
+    c = h0 - mu
+    var = (c * c).mean(-1, keepdim=True)
+    r0 = 1.0 / torch.sqrt(var + eps)
+    D = 28 * U * h0.abs().mean(-1, keepdim=True)
+    off = 30 * U * (c.abs().mean(-1, keepdim=True) + D)
+    assert ((mean.double().view(-1, 1) - mu).abs() <= 2 * U * mu.abs() + off + C * 2.0 ** -149).all()
+    r_off = 2.0 ** -19 + 64 * U * D * D / (var + eps)
+    assert ((r.double().view(-1, 1) - r0).abs() <= r0 * r_off).all()
+    n, gr = c * r0, by_rows(g, len(x), C)
+    y0, tol = n * gr, gr.abs() * (r0 * (off + U * c.abs()) + n.abs() * (r_off + 4 * U))
+    if b is not None:
+        br = by_rows(b, len(x), C)
+        y0, tol = y0 + br, tol + 2 * U * br.abs()
+    assert ((y.double() - y0).abs() <= y0.abs() * 2.0 ** -8 + tol * 1.01 + 1e-38).all()
+
+
+SIZES = [(1, 8), (1, 768), (7, 200), (333, 776), (5, 1024), (3, 1032), (100, 1096), (9, 2048), (6, 4096),
+         (4, 8200), (2, 16384), (2305, 768)]
+
+
+@gpu
+@pytest.mark.parametrize("T,C", SIZES)
+@pytest.mark.parametrize("with_res", [False, True])
+def test_layer_norm(ja, T, C, with_res):
+    x, g, b = randn((T, C), 1, shift=0.5), gains(C, 2), randn((C,), 3, 0.3, torch.float32)
+    res = randn((T, C), 4, 4.0) if with_res else None
+    check_norm(ja.layer_norm(x, g, b, res), x, res, g, b)
+    check_norm(ja.layer_norm(x, g, None, res), x, res, g, None)
+
+
+@gpu
+@pytest.mark.parametrize("items,rows,C", [(2, 1, 8), (16, 77, 768), (3, 111, 1096), (400, 3, 256), (5, 9, 4096)])
+def test_gains_and_biases_of_each_item(ja, items, rows, C):
+    x, g, b = randn((items, rows, C), 5), gains((items, C), 6), randn((items, C), 7, 0.3, torch.float32)
+    out = ja.layer_norm(x, g, b)
+    check_norm(out, x, None, g, b)
+    y, h, mean, r = out
+    dy = randn(x.shape, 8)
+    check_backward(ja.layer_norm_backward(dy, h, mean, r, g), dy, None, h, mean, r, g, True)
+
+
+def bwd64(dy, dh, h, mean, r, g):
+    C = h.shape[-1]
+    dy, h = dy.reshape(-1, C).double(), h.reshape(-1, C).double()
+    mean, r = mean.double().view(-1, 1), r.double().view(-1, 1)
+    n, u = (h - mean) * r, dy * by_rows(g, len(h), C)
+    items = g.numel() // C
+    item = lambda t: t.view(items, -1, C).sum(1)  # noqa: E731
+    dx = r * (u - u.mean(-1, keepdim=True) - n * (u * n).mean(-1, keepdim=True))
+    mag = r * (u.abs() + u.abs().mean(-1, keepdim=True) + n.abs() * (u * n).abs().mean(-1, keepdim=True))
+    # the centred values round at h - mean, whose terms may be larger than they
+    wide = (h.abs() + mean.abs()) * r
+    mag = mag + r * (wide * (u * n).abs().mean(-1, keepdim=True) + n.abs() * (u.abs() * wide).mean(-1, keepdim=True)) / 16
+    if dh is not None:
+        dx, mag = dx + dh.reshape(-1, C).double(), mag + dh.reshape(-1, C).double().abs()
+    return dx, mag, item(dy * n), item(dy.abs() * (n.abs() + wide / 64)), item(dy), item(dy.abs())
+
+
+def check_backward(out, dy, dh, h, mean, r, g, bias):
+    dx, dg, db = out
+    C = h.shape[-1]
+    dx0, mag, dg0, dg_mag, db0, db_mag = bwd64(dy, dh, h, mean, r, g)
+    assert ((dx.reshape(-1, C).double() - dx0).abs() <= dx0.abs() * 2.0 ** -8 + 64 * U * mag + 1e-38).all()
+    assert dg.shape == g.shape
+    assert ((dg.view(-1, C).double() - dg0).abs() <= 128 * U * dg_mag + 1e-38).all()
+    if bias:
+        assert ((db.view(-1, C).double() - db0).abs() <= 128 * U * db_mag + 1e-38).all()
+    else:
+        assert db is None
+
+
+@gpu
+@pytest.mark.parametrize("T,C", SIZES + [(5000, 256), (1217, 2048), (700, 12288)])
+@pytest.mark.parametrize("with_dh", [False, True])
+@pytest.mark.parametrize("bias", [False, True])
+def test_layer_norm_backward(ja, T, C, with_dh, bias):
+    h, g, dy = randn((T, C), 10, 3.0, shift=1.0), gains(C, 11), randn((T, C), 12)
+    dh = randn((T, C), 13) if with_dh else None
+    _, _, mean, r = ja.layer_norm(h, g)
+    out = ja.layer_norm_backward(dy, h, mean, r, g, dh, bias)
+    check_backward(out, dy, dh, h, mean, r, g, bias)
+    again = ja.layer_norm_backward(dy, h, mean, r, g, dh, bias)
+    for a, b in zip(out, again):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
+@gpu
+def test_layer_norm_backward_is_the_gradient_by_differences(ja):
+    """<dx, v>, <dg, w> and <db, w> against central differences of L = sum(dy y) + sum(dh h) in float64,
+    where neither h nor y is rounded: dx differs by its bf16 rounding (and mean and r by theirs) alone."""
+    T, C = 13, 328
+    h, g, b = randn((T, C), 20, 2.0, shift=0.7), gains(C, 21), randn((C,), 22, 0.3, torch.float32)
+    dy, dh = randn((T, C), 23), randn((T, C), 24)
+    _, _, mean, r = ja.layer_norm(h, g, b)
+    dx, dg, db = ja.layer_norm_backward(dy, h, mean, r, g, dh)
+
+    def loss(t, gain, shift):
+        c = t - t.mean(-1, keepdim=True)
+        n = c / torch.sqrt((c * c).mean(-1, keepdim=True) + EPS)
+        return (dy.double() * (n * gain + shift)).sum() + (dh.double() * t).sum()
+
+    for k in range(4):
+        v, w, e = randn((T, C), 30 + k, dtype=torch.float64), randn((C,), 40 + k, dtype=torch.float64), 1e-5
+        t, gain, shift = h.double(), g.double(), b.double()
+        by = [(loss(t + e * v, gain, shift) - loss(t - e * v, gain, shift)) / (2 * e),
+              (loss(t, gain + e * w, shift) - loss(t, gain - e * w, shift)) / (2 * e),
+              (loss(t, gain, shift + e * w) - loss(t, gain, shift - e * w)) / (2 * e)]
+        # each dx is off by at most 2^-8 of itself, with signs of their own: four times their norm
+        tol = (2.0 ** -8 * dx.double() * v).norm() * 4
+        assert abs((dx.double() * v).sum() - by[0]) <= tol + 1e-4
+        for got, want in ((dg, by[1]), (db, by[2])):
+            assert abs((got.double() * w).sum() - want) <= 128 * U * (got.double() * w).abs().sum() * 8 + 1e-4
+
+
+@gpu
+@pytest.mark.parametrize("C", [768, 2048])
+def test_in_place_forms_give_the_same_bits(ja, C):
+    T = 301
+    x, res, g, b = randn((T, C), 50), randn((T, C), 51, 2.0), gains(C, 52), gains(C, 53)
+    y, h, mean, r = ja.layer_norm(x, g, b, res)
+    y2, stream = torch.empty_like(y), res.clone()
+    ja.jattn_layer_norm(x, stream, g, b, 1, T, C, EPS, stream, y2, None, None)
+    assert torch.equal(y2, y) and torch.equal(stream, h)
+    dy, dh = randn((T, C), 54), randn((T, C), 55)
+    dx, dg, db = ja.layer_norm_backward(dy, h, mean, r, g, dh)
+    buf, dg2, db2 = dh.clone(), torch.empty_like(dg), torch.empty_like(db)
+    work = torch.full((ja.jattn_layer_norm_bwd_bytes(1, T, C),), 0xFF, dtype=torch.uint8, device="cuda")
+    ja.jattn_layer_norm_bwd(dy, buf, h, mean, r, g, 1, T, C, buf, dg2, db2, work)
+    assert torch.equal(buf, dx) and torch.equal(dg2, dg) and torch.equal(db2, db)
+
+
+@gpu
+@pytest.mark.parametrize("C", [776, 2048, 8200])
+def test_rows_of_equal_values_infinities_and_nan(ja, C):
+    T = 12
+    x, g, b = randn((T, C), 60), gains(C, 61), gains(C, 62)
+    x[1] = 0.0
+    x[2] = 12345.0       # every value the mean: y is b
+    x[3, 5] = float("nan")
+    x[5, 7] = float("inf")
+    x[7, :4] = torch.tensor([3e38, -3e38, 3e38, -3e38])  # squares pass the fp32 range: r = 0
+    x[8] = 3e38          # and a sum of the values would
+    x[9] = 1e-38
+    x[10] = 1000.0
+    x[10, 0] = 1008.0    # one bf16 step from the others
+    out = ja.layer_norm(x, g, b)
+    y, _, mean, r = out
+    fine = [0, 1, 2, 4, 6, 9, 10, 11]
+    check_norm([t[fine] for t in out], x[fine], None, g, b)
+    want = b.to(torch.bfloat16)
+    assert torch.equal(y[1], want) and torch.equal(y[7], want)
+    assert y[3].isnan().all() and y[5].isnan().all()
+    assert r[7] == 0 and mean[7].abs() <= 1e33 and torch.isfinite(mean[8])
+
+
+@gpu
+def test_offsets_beyond_32_bits(ja):
+    C, T = 16384, (1 << 17) + 3  # 2^31 + 49152 values
+    x = torch.zeros((T, C), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = randn((3, C), 70)
+    res = torch.zeros_like(x)
+    res[-2:] = randn((2, C), 71)
+    g, b = gains(C, 72), gains(C, 73)
+    y, h, mean, r = ja.layer_norm(x, g, b, res)
+    check_norm((y[-3:], h[-3:], mean[-3:], r[-3:]), x[-3:], res[-3:], g, b)
+    assert (y[:4] == b.to(torch.bfloat16)).all() and not h[:4].any()
+    del y, res
+    dx, dg, db = ja.layer_norm_backward(x, h, mean, r, g)  # zero but for the last rows
+    check_backward((dx[-3:], dg, db), x[-3:], None, h[-3:], mean[-3:], r[-3:], g, True)
+
+
+@gpu
+def test_on_another_stream_and_captured(ja):
+    """The calls on a stream of their own, and captured into a graph that is replayed on new inputs."""
+    items, rows, C = 7, 111, 768
+    shape = (items, rows, C)
+    x, res, g, b = randn(shape, 80), randn(shape, 81), gains((items, C), 82), gains((items, C), 83)
+    dy = randn(shape, 84)
+
+    def both(**kw):
+        y, h, mean, r = ja.layer_norm(x, g, b, res, **kw)
+        return (y, h, mean, r, *ja.layer_norm_backward(dy, h, mean, r, g, **kw))
+
+    want = both()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = both(stream=stream)
+        side.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    x.copy_(randn(shape, 85))
+    dy.copy_(randn(shape, 86))
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(got, both()))
+
+
+@gpu
+def test_wrappers_refuse(ja):
+    x, g = randn((6, 768), 90), gains(768, 91)
+    with pytest.raises(ValueError):
+        ja.layer_norm(x[:, ::2], gains(384, 1))   # strides
+    with pytest.raises(ValueError):
+        ja.layer_norm(x, gains(760, 1))           # another width
+    with pytest.raises(ValueError):
+        ja.layer_norm(x, g, gains((2, 768), 1))   # a bias of another shape
+    with pytest.raises(ValueError):
+        ja.layer_norm(x, g, None, x[:3])          # another number of rows
+    with pytest.raises(ValueError):
+        ja.layer_norm(x.float(), g)
+    with pytest.raises(ValueError):
+        ja.layer_norm(x.cpu(), g)
+    with pytest.raises(ja.JattnError):
+        ja.layer_norm(x, gains((4, 768), 1))      # 6 rows of 4 items
+    with pytest.raises(ja.JattnError):
+        ja.layer_norm(randn((4, 12), 1), gains(12, 1))
+    with pytest.raises(ja.JattnError):
+        ja.layer_norm(x, g, eps=0.0)
+    y, h, mean, r = ja.layer_norm(x, g)
+    with pytest.raises(ValueError):
+        ja.jattn_layer_norm_bwd(y, None, h, mean, r, g, 1, 6, 768, torch.empty_like(y), torch.empty_like(g), None,
+                                torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+# Fake, never-dereferenced device addresses: validation happens first.
+A = 0x7F0000000000
+
+
+def at(i):
+    return A + (i << 33)
+
+
+def test_layer_norm_validation(lib):
+    code = STATUS_CODE
+    base = dict(x=at(0), res=at(1), g=at(2), b=at(3), items=2, T=24, C=64, eps=1e-6, h=at(4), y=at(5), mean=at(6),
+                r=at(7))
+    f = lambda **kw: lib.jattn_layer_norm(*{**base, **kw}.values(), None)  # noqa: E731
+    for kw in (dict(x=None), dict(g=None), dict(y=None), dict(res=None), dict(h=None), dict(T=0), dict(C=0),
+               dict(T=-1), dict(items=0), dict(items=-2), dict(items=5), dict(items=48), dict(eps=0.0), dict(eps=-1.0),
+               dict(eps=float("nan")), dict(eps=float("inf"))):
+        assert f(**kw) == code["JATTN_ERR_INVALID_ARG"], kw
+    for kw in (dict(C=60), dict(C=16392)):
+        assert f(**kw) == code["JATTN_ERR_UNSUPPORTED"], kw
+    for kw in (dict(x=A + 8), dict(r=at(7) + 4), dict(b=at(3) + 8), dict(mean=at(6) + 4)):
+        assert f(**kw) == code["JATTN_ERR_MISALIGNED"], kw
+    for kw in (dict(y=at(0)), dict(h=at(0)), dict(h=at(1) + 16), dict(y=at(1)), dict(r=at(4)), dict(y=at(4)),
+               dict(h=at(2)), dict(mean=at(7)), dict(y=at(3)), dict(r=at(2) + 256)):
+        assert f(**kw) == code["JATTN_ERR_ALIAS"], kw
+    baseb = dict(dy=at(0), dh=at(1), h=at(2), mean=at(3), r=at(4), g=at(5), items=3, T=24, C=64, dx=at(6), dg=at(7),
+                 db=at(8), work=at(9))
+    f = lambda **kw: lib.jattn_layer_norm_bwd(*{**baseb, **kw}.values(), None)  # noqa: E731
+    for k in ("dy", "h", "mean", "r", "g", "dx", "dg", "work"):
+        assert f(**{k: None}) == code["JATTN_ERR_INVALID_ARG"], k
+    assert f(T=0) == f(items=0) == f(items=7) == code["JATTN_ERR_INVALID_ARG"]
+    assert f(C=12) == code["JATTN_ERR_UNSUPPORTED"]
+    assert f(work=at(9) + 8) == f(db=at(8) + 4) == code["JATTN_ERR_MISALIGNED"]
+    for kw in (dict(dx=at(0)), dict(dx=at(2)), dict(dx=at(1) + 16), dict(dg=at(5)), dict(work=at(6)),
+               dict(work=at(2)), dict(db=at(7) + 512), dict(db=at(3))):
+        assert f(**kw) == code["JATTN_ERR_ALIAS"], kw
+    size = lib.jattn_layer_norm_bwd_bytes
+    assert size(3, 24, 64) > 0 and size(0, 24, 64) == size(5, 24, 64) == size(3, 24, 60) == size(3, 0, 64) == 0

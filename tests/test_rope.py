@@ -1,0 +1,316 @@
+"""Rotary positions on several axes, with or without the QK-RMSNorm, and their backward, against their
+definitions in float64.
+
+Tolerances, from the arithmetic (u = 2^-24, one fp32 rounding):
+* An angle's fraction of a turn is rounded once (2^-25 of a turn at most, and the low parts less while the
+  angle is below 2^22 turns) and sincospif is off by at most 2 u: cosines and sines are off by 2 pi 2^-25 +
+  2 u < 2^-21.  A rotated value has two products and a sum: (|z_i| + |z_j|) 2^-20 in all.
+* z = x r g: the sum of squares 20 u halved by the root, which rounds once, and two products: 14 u.
+* Every output: half a bf16 step, 2^-8 relative.
+* Backward with gains: the rotated gradient's error times g, r and the terms of dx, whose sums pass less than
+  24 roundings: 2^-18 of the terms' magnitudes; dg: at most 256 roundings on any path and those errors, 2^-15.
+"""
+import pytest
+import torch
+
+from joint_attention_gb300 import STATUS_CODE
+import joint_attention_gb300 as pkg
+from joint_attention_gb300.build import build
+
+EPS = 1e-6
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build()
+    return pkg.load_library()
+
+
+@pytest.fixture(scope="module")
+def ja(lib):
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    return pkg
+
+
+def randn(shape, seed, scale=1.0, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def gains(C, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.rand(C, generator=g, device="cuda") + 0.5
+
+
+def inputs(B, Hq, Hk, N, d, pairs, per_item, seed, far=5000.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    shape = (B, N, len(pairs)) if per_item else (N, len(pairs))
+    pos = (torch.rand(shape, generator=g, device="cuda") * 2 - 1) * far  # fractions and both signs
+    freq = torch.cat([10000.0 ** (-torch.arange(p, dtype=torch.float64) / max(p, 1)) for p in pairs]).float().cuda()
+    return randn((B, Hq, N, d), seed + 1), randn((B, Hk, N, d), seed + 2), pos, freq
+
+
+def turns64(pos, freq, pairs):
+    axis = [a for a, p in enumerate(pairs) for _ in range(p)]
+    angle = pos.double()[..., axis] * freq.double()
+    angle = angle[:, None] if pos.dim() == 3 else angle  # [.., N, P] beside [B, H, N, d]
+    return angle.cos(), angle.sin()
+
+
+def rotate64(x, cos, sin, interleaved, add=False):
+    """The rotation; with add its terms' magnitudes |z_i| + |z_j|."""
+    P, out = cos.shape[-1], x.clone()
+    i, j = (slice(0, 2 * P, 2), slice(1, 2 * P, 2)) if interleaved else (slice(0, P), slice(P, 2 * P))
+    a, b = x[..., i], x[..., j]
+    out[..., i], out[..., j] = (a + b, a + b) if add else (a * cos - b * sin, a * sin + b * cos)
+    return out
+
+
+def norm64(x, g):
+    x = x.double()
+    return x if g is None else x / torch.sqrt((x * x).mean(-1, keepdim=True) + EPS) * g.double()
+
+
+def check_rope(out, x, pos, freq, pairs, g, interleaved):
+    cos, sin = turns64(pos, freq, pairs)
+    z = norm64(x, g)
+    want, mag = rotate64(z, cos, sin, interleaved), rotate64(z.abs(), cos, sin, interleaved, add=True)
+    assert ((out.double() - want).abs() <= want.abs() * 2.0 ** -8 + mag * 2.0 ** -19 + 1e-38).all()
+    P = cos.shape[-1]
+    if g is None:  # the other channels are the input's bits
+        assert torch.equal(out[..., 2 * P:].contiguous().view(torch.int16), x[..., 2 * P:].contiguous().view(torch.int16))
+
+
+CASES = [
+    (1, 1, 1, 1, 64, (32,), False), (3, 4, 2, 1, 128, (64,), True), (2, 12, 12, 77, 64, (16, 16), False),
+    (2, 3, 1, 333, 128, (8, 28, 28), True), (1, 8, 2, 1101, 64, (5, 0, 11), False), (16, 12, 12, 65, 64, (10, 22), False),
+    (2, 5, 5, 129, 128, (3, 9, 20, 8), True), (1, 33, 7, 31, 128, (8,), False), (40, 6, 2, 3, 64, (7, 17), True),
+]
+
+
+@gpu
+@pytest.mark.parametrize("B,Hq,Hk,N,d,pairs,per_item", CASES)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+def test_rope(ja, B, Hq, Hk, N, d, pairs, per_item, interleaved, norm):
+    q, k, pos, freq = inputs(B, Hq, Hk, N, d, pairs, per_item, 1)
+    gq, gk = (gains(d, 2), gains(d, 3)) if norm else (None, None)
+    q_rot, k_rot = ja.rope(q, k, pos, freq, pairs, gq, gk, interleaved)
+    check_rope(q_rot, q, pos, freq, pairs, gq, interleaved)
+    check_rope(k_rot, k, pos, freq, pairs, gk, interleaved)
+    in_place = q.clone(), k.clone()
+    ja.jattn_rope(*in_place, gq, gk, pos, freq, pairs, per_item, interleaved, B, Hq, Hk, N, d, EPS, *in_place)
+    assert torch.equal(in_place[0], q_rot) and torch.equal(in_place[1], k_rot)
+
+
+@gpu
+def test_far_positions(ja):
+    """Whole positions up to 2^24, all exact in fp32, with an angle of as many radians."""
+    q, k, _, freq = inputs(1, 2, 2, 6, 64, (32,), False, 5)
+    pos = torch.tensor([[0.0], [1.0], [999999.0], [2.0 ** 20 + 1], [2.0 ** 24], [-(2.0 ** 24) + 1]], device="cuda")
+    q_rot, _ = ja.rope(q, k, pos, freq, (32,))
+    check_rope(q_rot, q, pos, freq, (32,), None, False)
+    assert torch.equal(q_rot[:, :, 0], q[:, :, 0])
+
+
+def bwd64(x, grad, pos, freq, pairs, g, interleaved):
+    cos, sin = turns64(pos, freq, pairs)
+    u = rotate64(grad.double(), cos, -sin, interleaved)
+    mag = rotate64(grad.double().abs(), cos, sin, interleaved, add=True)
+    if g is None:
+        return u, mag, None, None
+    x, g = x.double(), g.double()
+    r = 1.0 / torch.sqrt((x * x).mean(-1, keepdim=True) + EPS)
+    n = x * r
+    dx = r * (u * g - n * (u * g * n).mean(-1, keepdim=True))
+    dx_mag = r * (mag * g.abs() + n.abs() * (mag * g.abs() * n.abs()).mean(-1, keepdim=True))
+    return dx, dx_mag, (u * n).sum((0, 1, 2)), (mag * n.abs()).sum((0, 1, 2))
+
+
+@gpu
+@pytest.mark.parametrize("B,Hq,Hk,N,d,pairs,per_item", CASES)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+def test_rope_backward(ja, B, Hq, Hk, N, d, pairs, per_item, interleaved, norm):
+    q, k, pos, freq = inputs(B, Hq, Hk, N, d, pairs, per_item, 11)
+    gq, gk = (gains(d, 12), gains(d, 13)) if norm else (None, None)
+    dq_rot, dk_rot = randn(q.shape, 14), randn(k.shape, 15)
+    call = lambda: ja.rope_backward(dq_rot, dk_rot, pos, freq, pairs, q, k, gq, gk, interleaved)  # noqa: E731
+    out = call()
+    for x, grad, g, dx, dg in ((q, dq_rot, gq, out[0], out[2]), (k, dk_rot, gk, out[1], out[3])):
+        dx0, mag, dg0, dg_mag = bwd64(x, grad, pos, freq, pairs, g, interleaved)
+        assert ((dx.double() - dx0).abs() <= dx0.abs() * 2.0 ** -8 + mag * 2.0 ** -18 + 1e-38).all()
+        if norm:
+            assert ((dg.double() - dg0).abs() <= dg_mag * 2.0 ** -15 + 1e-38).all()
+        else:
+            assert dg is None
+    for a, b in zip(out, call()):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
+@gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_backward_is_the_gradient_by_differences(ja, interleaved):
+    """<dq, v> and <dgq, w> against central differences of L = sum(dq_rot q_rot) in float64 without roundings."""
+    B, Hq, Hk, N, d, pairs = 2, 3, 1, 17, 64, (9, 15)
+    q, k, pos, freq = inputs(B, Hq, Hk, N, d, pairs, True, 21)
+    gq, gk = gains(d, 22), gains(d, 23)
+    dq_rot, dk_rot = randn(q.shape, 24), randn(k.shape, 25)
+    dq, dk, dgq, dgk = ja.rope_backward(dq_rot, dk_rot, pos, freq, pairs, q, k, gq, gk, interleaved)
+    cos, sin = turns64(pos, freq, pairs)
+    for x, g, grad, dx, dg in ((q, gq, dq_rot, dq, dgq), (k, gk, dk_rot, dk, dgk)):
+        loss = lambda t, gain: (grad.double() * rotate64(norm64(t, gain), cos, sin, interleaved)).sum()  # noqa: E731
+        for i in range(3):
+            v, w, e = randn(x.shape, 30 + i, dtype=torch.float64), randn((d,), 40 + i, dtype=torch.float64), 1e-5
+            by_x = (loss(x.double() + e * v, g.double()) - loss(x.double() - e * v, g.double())) / (2 * e)
+            by_g = (loss(x.double(), g.double() + e * w) - loss(x.double(), g.double() - e * w)) / (2 * e)
+            # each dx is off by at most 2^-8 of itself, with signs of their own: four times their norm
+            assert abs((dx.double() * v).sum() - by_x) <= 4 * (2.0 ** -8 * dx.double() * v).norm() + 1e-4
+            assert abs((dg.double() * w).sum() - by_g) <= 2.0 ** -13 * (dg.double() * w).abs().sum() + 1e-3
+
+
+@gpu
+def test_packed_layout_is_one_item(ja):
+    q, k, pos, freq = inputs(1, 4, 2, 205, 64, (16, 16), False, 31)
+    want = ja.rope(q, k, pos, freq, (16, 16))
+    got = ja.rope(q[0], k[0], pos, freq, (16, 16))
+    assert torch.equal(got[0], want[0][0]) and torch.equal(got[1], want[1][0])
+
+
+@gpu
+@pytest.mark.parametrize("norm", [False, True])
+def test_infinities_and_nan_stay_in_their_rows_and_pairs(ja, norm):
+    B, H, N, d, pairs = 1, 2, 40, 64, (8, 8)  # channels from 32 on do not turn
+    q, k, pos, freq = inputs(B, H, H, N, d, pairs, False, 41)
+    q[0, 0, 3, 1], q[0, 1, 5, 50], k[0, 1, 7, 2] = float("nan"), float("inf"), float("-inf")
+    gq, gk = (gains(d, 42), gains(d, 43)) if norm else (None, None)
+    q_rot, k_rot = ja.rope(q, k, pos, freq, pairs, gq, gk)
+    for got, x, g, bad in ((q_rot, q, gq, [(0, 3), (1, 5)]), (k_rot, k, gk, [(1, 7)])):
+        fine = torch.ones(H, N, dtype=torch.bool)
+        for at in bad:
+            fine[at] = False
+        fine = fine.cuda()
+        assert got[0][fine].isfinite().all()
+    if not norm:
+        assert q_rot[0, 0, 3].isnan().nonzero().flatten().tolist() == [1, 17]
+        assert q_rot[0, 1, 5].isinf().nonzero().flatten().tolist() == [50] and not q_rot[0, 1, 5].isnan().any()
+    dgq = ja.rope_backward(q_rot.nan_to_num(0, 0, 0), k_rot.nan_to_num(0, 0, 0), pos, freq, pairs,
+                           q.nan_to_num(0, 0, 0), k.nan_to_num(0, 0, 0), gq, gk)[2]
+    assert dgq is None or dgq.isfinite().all()
+
+
+@gpu
+def test_offsets_beyond_32_bits(ja):
+    B, H, N, d, pairs = 2, 4, 2097169, 128, (64,)  # q: 2^31 + 17408 values
+    q = torch.zeros((B, H, N, d), dtype=torch.bfloat16, device="cuda")
+    q[-1, -1, -5:] = randn((5, d), 51)
+    k = q[:, :1].clone()
+    k[-1, -1, -5:] = randn((5, d), 52)
+    pos = torch.arange(N, device="cuda", dtype=torch.float32)[:, None]
+    freq = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float().cuda()
+    ja.jattn_rope(q, k, None, None, pos, freq, pairs, False, True, B, H, 1, N, d, EPS, q, k)
+    check_rope(q[-1:, -1:, -5:], cut(51), pos[-5:], freq, pairs, None, True)
+    check_rope(k[-1:, -1:, -5:], cut(52), pos[-5:], freq, pairs, None, True)
+    assert not q[0, 0, :9].any()
+
+
+def cut(seed):
+    return randn((5, 128), seed)[None, None]
+
+
+@gpu
+def test_on_another_stream_and_captured(ja):
+    pairs = (16, 24, 24)
+    q, k, pos, freq = inputs(3, 4, 2, 111, 128, pairs, True, 61)
+    gq, gk, dq_rot, dk_rot = gains(128, 62), gains(128, 63), randn(q.shape, 64), randn(k.shape, 65)
+
+    def both(**kw):
+        return (*ja.rope(q, k, pos, freq, pairs, gq, gk, **kw),
+                *ja.rope_backward(dq_rot, dk_rot, pos, freq, pairs, q, k, gq, gk, **kw))
+
+    want = both()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = both(stream=stream)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    q.copy_(randn(q.shape, 66))
+    pos.add_(3.0)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, both()))
+
+
+@gpu
+def test_wrappers_refuse(ja):
+    pairs = (16, 16)
+    q, k, pos, freq = inputs(2, 4, 2, 20, 64, pairs, True, 71)
+    g = gains(64, 72)
+    for bad in (dict(q=q[:, :, ::2], k=k[:, :, ::2]), dict(q=q.float()), dict(k=k[:1]), dict(k=k[..., :32]),
+                dict(pos=pos[:1]), dict(pos=pos.double()), dict(freq=freq[:16]), dict(pos=pos.cpu()),
+                dict(gq=g[:32], gk=g), dict(pairs=(16, 8)), dict(q=q[0])):
+        with pytest.raises(ValueError):
+            ja.rope(**{**dict(q=q, k=k, pos=pos, freq=freq, pairs=pairs), **bad})
+    for bad in (dict(gq=g), dict(gq=g, gk=g, eps=0.0), dict(pairs=(33, -1))):
+        with pytest.raises(ja.JattnError):
+            ja.rope(**{**dict(q=q, k=k, pos=pos, freq=freq, pairs=pairs), **bad})
+    with pytest.raises(ja.JattnError):
+        ja.rope_backward(q, k, pos, freq, pairs, None, k, g, g)
+
+
+# Fake, never-dereferenced device addresses: validation happens first.
+A = 0x7F0000000000
+
+
+def at(i):
+    return A + (i << 33)
+
+
+def ints(*v):
+    import ctypes
+
+    return (ctypes.c_int * len(v))(*v)
+
+
+def test_rope_validation(lib):
+    code = STATUS_CODE
+    base = dict(q=at(0), k=at(1), gq=at(2), gk=at(3), pos=at(4), freq=at(5), pairs=ints(8, 24), axes=2, per_item=0,
+                interleaved=0, B=2, Hq=4, Hk=2, N=24, d=64, eps=1e-6, q_rot=at(6), k_rot=at(7))
+    f = lambda **kw: lib.jattn_rope(*{**base, **kw}.values(), None)  # noqa: E731
+    for kw in (dict(q=None), dict(k=None), dict(gq=None), dict(gk=None), dict(pos=None), dict(freq=None),
+               dict(pairs=None), dict(q_rot=None), dict(k_rot=None), dict(axes=0), dict(axes=-1), dict(B=0), dict(Hq=0),
+               dict(Hk=-1), dict(N=0), dict(d=0), dict(eps=0.0), dict(eps=float("nan")), dict(pairs=ints(-8, 24)),
+               dict(pairs=ints(8, 32)), dict(pairs=ints(0, 0)), dict(pairs=ints(2 ** 31 - 1, 2 ** 31 - 1)),
+               dict(B=1 << 12, Hq=1 << 10, N=1 << 10), dict(B=1 << 16, Hk=1 << 16)):
+        assert f(**kw) == code["JATTN_ERR_INVALID_ARG"], kw
+    for kw in (dict(d=96), dict(pairs=ints(8, 20)), dict(pairs=ints(4, 4, 4, 4, 16), axes=5)):
+        assert f(**kw) == code["JATTN_ERR_UNSUPPORTED"], kw
+    for kw in (dict(q=A + 8), dict(freq=at(5) + 4), dict(gk=at(3) + 8)):
+        assert f(**kw) == code["JATTN_ERR_MISALIGNED"], kw
+    for kw in (dict(q_rot=at(1)), dict(q_rot=at(0) + 16), dict(k_rot=at(0)), dict(k_rot=at(6)), dict(q_rot=at(4)),
+               dict(k_rot=at(5)), dict(q_rot=at(2))):
+        assert f(**kw) == code["JATTN_ERR_ALIAS"], kw
+    baseb = dict(dq_rot=at(0), dk_rot=at(1), q=at(2), k=at(3), gq=at(4), gk=at(5), pos=at(6), freq=at(7),
+                 pairs=ints(8, 24), axes=2, per_item=0, interleaved=0, B=2, Hq=4, Hk=2, N=24, d=64, eps=1e-6, dq=at(8),
+                 dk=at(9), dgq=at(10), dgk=at(11), work=at(12))
+    f = lambda **kw: lib.jattn_rope_bwd(*{**baseb, **kw}.values(), None)  # noqa: E731
+    for key in ("dq_rot", "dk_rot", "q", "k", "gq", "gk", "pos", "freq", "pairs", "dq", "dk", "dgq", "dgk", "work"):
+        assert f(**{key: None}) == code["JATTN_ERR_INVALID_ARG"], key
+    plain = dict(q=None, k=None, gq=None, gk=None, dgq=None, dgk=None, work=None)
+    for key in plain:  # without gains none of these
+        assert f(**{**plain, key: baseb[key]}) == code["JATTN_ERR_INVALID_ARG"], key
+    assert f(eps=0.0) == f(N=-3) == code["JATTN_ERR_INVALID_ARG"]
+    assert f(d=80) == f(pairs=ints(1, 2)) == code["JATTN_ERR_UNSUPPORTED"]
+    assert f(work=at(12) + 8) == f(dgk=at(11) + 4) == code["JATTN_ERR_MISALIGNED"]
+    for kw in (dict(dq=at(1)), dict(dq=at(0) + 16), dict(dq=at(2)), dict(dk=at(3)), dict(dgq=at(4)), dict(dgk=at(10)),
+               dict(work=at(8)), dict(work=at(2)), dict(dk=at(8))):
+        assert f(**kw) == code["JATTN_ERR_ALIAS"], kw
+    size = lib.jattn_rope_bwd_bytes
+    assert size(0, 2, 4, 2, 24, 64) > 0 and size(0, 2, 4, 0, 24, 64) == size(0, 2, 4, 2, 24, 96) == 0
