@@ -411,6 +411,50 @@ int jattn_qkv_norm_lora(const jattn_bf16* x_img, const jattn_bf16* w_img, const 
                         jattn_bf16* k, jattn_bf16* v, void* saved, void* work, void* stream);
 
 /*
+ * Attention of packed sequences with grouped heads, causal or full, on q and k as they
+ * are: no QK-RMSNorm (jattn_rope applies it, with the positions, or none is wanted).
+ * (The caption tower before an MM-DiT is causal, re-diffusion README, "architecture
+ * flowchart": CLIP ViT-L/14; the pages print no code for it.)
+ *
+ *   S = scale q k^T  for the rows of one sequence, a query head h with kv head h / (Hq / Hk);
+ *       causal: row i sees the keys j <= i of its sequence
+ *   LSE_i = ln sum_j exp(S_ij),   O = exp(S - LSE) V
+ *
+ *   q, out, dout, dq : [Hq, T, d] bf16
+ *   k, v, dk, dv     : [Hk, T, d] bf16
+ *   lse              : [Hq, T] float32
+ *   cu_seqlens : HOST array of n_seqs + 1 ints, cu_seqlens[0] = 0, not decreasing: sequence
+ *           s is rows cu_seqlens[s] .. cu_seqlens[s+1]-1 of every head, and may be empty
+ *           (one sequence at least is not); read during the call only
+ *   n_seqs : 1 .. JATTN_MAX_SEQS (more: JATTN_ERR_UNSUPPORTED)
+ *   T      : rows of a head in memory, >= cu_seqlens[n_seqs].  Rows behind the last sequence
+ *           are read by no row's result, whatever they hold, and outputs leave theirs as
+ *           they were
+ *   Hq, Hk : heads, Hq a multiple of Hk;  d : 64 or 128;  Hq T d < 2^31
+ *   causal : 0 or not
+ *   scale  : 2^-20 .. 2^20
+ * A result does not depend on rows of other sequences, nor (forward, causal) on later
+ * rows, not even where these hold infinities or NaN.  In the backward a value that is not
+ * finite in q, k or dout of a row may make the gradients of rows of the same sequence in
+ * its 128-row tile NaN.
+ *
+ * jattn_bwd_grouped: the gradients of L = sum(dout * out), given the forward's out and
+ * lse.  dk and dv repeat bit for bit; dq as in jattn_bwd (with
+ * jattn_set_deterministic(1) bit for bit too).
+ *   work : jattn_bwd_grouped_bytes(...) bytes (fp32 dq, and the rows' statistics), contents of no meaning before or after; calls that
+ *           overlap on the GPU need one each.
+ * jattn_bwd_grouped_bytes returns 0 for sizes the call would reject.
+ */
+int jattn_fwd_grouped(const jattn_bf16* q, const jattn_bf16* k, const jattn_bf16* v, const int* cu_seqlens, int n_seqs,
+                      int Hq, int Hk, int T, int d, int causal, float scale, jattn_bf16* out, float* lse,
+                      void* stream);
+size_t jattn_bwd_grouped_bytes(const int* cu_seqlens, int n_seqs, int Hq, int Hk, int T, int d);
+int jattn_bwd_grouped(const jattn_bf16* q, const jattn_bf16* k, const jattn_bf16* v, const jattn_bf16* out,
+                      const float* lse, const jattn_bf16* dout, const int* cu_seqlens, int n_seqs, int Hq, int Hk,
+                      int T, int d, int causal, float scale, jattn_bf16* dq, jattn_bf16* dk, jattn_bf16* dv,
+                      void* work, void* stream);
+
+/*
  * Forward without any device allocation.  (No counterpart on the pages: an
  * integration entry point.)  Same arguments, layout and results as jattn_fwd,
  * but the scratch it needs (the normalised q_hat and k_hat, 2 * 2 * B*H*N*d
@@ -494,7 +538,8 @@ typedef enum {
   JATTN_KERNEL_ROPE = 24,            /* rotary positions, and their backward without gains */
   JATTN_KERNEL_ROPE_NORM_BWD = 25,   /* their backward with gains: dq, dk and partial sums of dgq, dgk */
   JATTN_KERNEL_ROPE_GAINS = 26,      /* dgq, dgk from the partial sums */
-  JATTN_TOKEN_KERNEL_END = 27
+  JATTN_KERNEL_GROUPED_DQ = 27,      /* dq of grouped heads from its accumulator (the others: ATTN_FWD, BWD_PREP, ATTN_BWD) */
+  JATTN_TOKEN_KERNEL_END = 28
 } jattn_token_kernel_kind;
 
 int jattn_profile_enable(int on);

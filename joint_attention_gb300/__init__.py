@@ -17,7 +17,8 @@ from ._binding import (KERNEL_KINDS, STATUS, STATUS_CODE, JattnError, declared_s
                        TOKEN_KERNEL_KINDS, jattn_add_norm, jattn_add_norm_fp8, jattn_quant_rows,
                        jattn_add_norm_bwd_bytes, jattn_add_norm_bwd, jattn_qkv_norm_fp8, jattn_qkv_norm_lora,
                        jattn_qkv_norm_lora_bytes, jattn_layer_norm, jattn_layer_norm_bwd_bytes, jattn_layer_norm_bwd,
-                       jattn_rope, jattn_rope_bwd_bytes, jattn_rope_bwd)
+                       jattn_rope, jattn_rope_bwd_bytes, jattn_rope_bwd, jattn_fwd_grouped, jattn_bwd_grouped_bytes,
+                       jattn_bwd_grouped)
 
 __all__ = ["STATUS", "STATUS_CODE", "JattnError", "declared_symbols", "jattn_bwd", "jattn_fwd",
            "jattn_last_device_error", "jattn_status_string", "jattn_version", "load_library", "forward",
@@ -31,7 +32,8 @@ __all__ = ["STATUS", "STATUS_CODE", "JattnError", "declared_symbols", "jattn_bwd
            "jattn_add_norm_bwd_bytes", "jattn_add_norm_bwd", "add_norm", "add_norm_fp8", "add_norm_backward",
            "quant_rows", "jattn_qkv_norm_fp8", "jattn_qkv_norm_lora", "jattn_qkv_norm_lora_bytes", "qkv_norm_fp8",
            "qkv_norm_lora", "jattn_layer_norm", "jattn_layer_norm_bwd_bytes", "jattn_layer_norm_bwd", "layer_norm",
-           "layer_norm_backward", "jattn_rope", "jattn_rope_bwd_bytes", "jattn_rope_bwd", "rope", "rope_backward"]
+           "layer_norm_backward", "jattn_rope", "jattn_rope_bwd_bytes", "jattn_rope_bwd", "rope", "rope_backward",
+           "jattn_fwd_grouped", "jattn_bwd_grouped_bytes", "jattn_bwd_grouped", "forward_grouped", "backward_grouped"]
 
 
 def forward(q, k, v, gq, gk, n_txt: int, stream=None):
@@ -324,3 +326,41 @@ def rope_backward(dq_rot, dk_rot, pos, freq, pairs, q=None, k=None, gq=None, gk=
                    interleaved, *sizes, eps, dq.data_ptr(), dk.data_ptr(), dgq.data_ptr() if norm else None,
                    dgk.data_ptr() if norm else None, work, stream)
     return dq, dk, dgq, dgk
+
+
+def _grouped_sizes(q, k, scale):
+    """Hq, Hk, T, d of q [Hq, T, d] and k, and the scale (None: 1 / sqrt(d))."""
+    if q.dim() != 3 or k.dim() != 3 or q.shape[1:] != k.shape[1:]:
+        raise ValueError(f"q and k: expected [Hq, T, d] and [Hk, T, d], got {tuple(q.shape)} and {tuple(k.shape)}")
+    Hq, T, d = q.shape
+    return (Hq, k.shape[0], T, d), d ** -0.5 if scale is None else scale
+
+
+def forward_grouped(q, k, v, cu_seqlens, causal: bool = True, scale: float | None = None, stream=None):
+    """out, lse: attention of packed sequences with grouped heads, causal or full, on q [Hq, T, d] and k, v
+    [Hk, T, d] bf16 as they are (no norm); query head h reads kv head h // (Hq // Hk).  Sequence s is rows
+    cu_seqlens[s] .. cu_seqlens[s+1]-1 of every head (host ints; it may be empty); rows of out and lse
+    behind the last one are left as they were allocated.  scale None: 1 / sqrt(d)."""
+    import torch
+
+    (Hq, Hk, T, d), scale = _grouped_sizes(q, k, scale)
+    with _outputs_on(stream, q, k, v):
+        out = torch.empty_like(q)
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    jattn_fwd_grouped(q, k, v, cu_seqlens, Hq, Hk, T, d, causal, scale, out.data_ptr(), lse.data_ptr(), stream)
+    return out, lse
+
+
+def backward_grouped(q, k, v, out, lse, dout, cu_seqlens, causal: bool = True, scale: float | None = None,
+                     stream=None):
+    """dq, dk, dv from forward_grouped's out and lse for the upstream gradient dout (the same causal and
+    scale)."""
+    import torch
+
+    sizes, scale = _grouped_sizes(q, k, scale)
+    with _outputs_on(stream, q, k, v, out, lse, dout):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        work = _buffer(jattn_bwd_grouped_bytes(cu_seqlens, *sizes), q.device)
+    jattn_bwd_grouped(q, k, v, out, lse, dout, cu_seqlens, *sizes, causal, scale, dq.data_ptr(), dk.data_ptr(),
+                      dv.data_ptr(), work.data_ptr(), stream)
+    return dq, dk, dv

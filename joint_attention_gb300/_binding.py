@@ -134,13 +134,19 @@ def load_library(path: str | None = None, build_if_missing: bool = False) -> cty
     lib.jattn_rope_bwd_bytes.restype = sz
     lib.jattn_rope_bwd.argtypes = [vp] * 8 + [i32p] + [i32] * 8 + [f32c] + [vp] * 6
     lib.jattn_rope_bwd.restype = i32
+    lib.jattn_fwd_grouped.argtypes = [vp] * 3 + [i32p] + [i32] * 6 + [f32c] + [vp] * 3
+    lib.jattn_fwd_grouped.restype = i32
+    lib.jattn_bwd_grouped_bytes.argtypes = [i32p] + [i32] * 5
+    lib.jattn_bwd_grouped_bytes.restype = sz
+    lib.jattn_bwd_grouped.argtypes = [vp] * 6 + [i32p] + [i32] * 6 + [f32c] + [vp] * 5
+    lib.jattn_bwd_grouped.restype = i32
     if path is None:
         _lib = lib
     return lib
 
 
 KERNEL_KINDS = 6
-TOKEN_KERNEL_KINDS = range(16, 27)  # the token-row kernels' kinds, numbered apart
+TOKEN_KERNEL_KINDS = range(16, 28)  # the token-row kernels' kinds, numbered apart
 
 
 def jattn_profile_enable(on: bool = True) -> int:
@@ -681,6 +687,46 @@ def jattn_qkv_norm_lora(x_img, w_img, b_img, x_txt, w_txt, b_txt, gq, gk, down_i
         _work_ptr(work, jattn_qkv_norm_lora_bytes, B, H, N_img, N_txt, d, rank), _stream(stream))
     if check and rc != 0:
         raise JattnError(rc, "jattn_qkv_norm_lora")
+    return rc
+
+
+def jattn_fwd_grouped(q, k, v, cu_seqlens, Hq: int, Hk: int, T: int, d: int, causal: bool, scale: float, out, lse,
+                      stream=None, check: bool = True) -> int:
+    """C ABI jattn_fwd_grouped.  q / out [Hq, T, d] and k / v [Hk, T, d] bf16, lse [Hq, T] fp32; cu_seqlens a host
+    sequence of n + 1 ints, not decreasing, the last at most T."""
+    import torch
+
+    bf, eq, ek = torch.bfloat16, Hq * T * d, Hk * T * d
+    arr, _, n = _cu_array(cu_seqlens)
+    rc = load_library().jattn_fwd_grouped(_ptr(q, "q", bf, eq), _ptr(k, "k", bf, ek), _ptr(v, "v", bf, ek), arr, n,
+                                          _size(Hq), _size(Hk), _size(T), _size(d), bool(causal), scale,
+                                          _ptr(out, "out", bf, eq), _ptr(lse, "lse", torch.float32, Hq * T),
+                                          _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_fwd_grouped")
+    return rc
+
+
+def jattn_bwd_grouped_bytes(cu_seqlens, Hq: int, Hk: int, T: int, d: int) -> int:
+    """C ABI jattn_bwd_grouped_bytes: size of the work buffer of jattn_bwd_grouped (0: it rejects the sizes)."""
+    arr, _, n = _cu_array(cu_seqlens)
+    return int(load_library().jattn_bwd_grouped_bytes(arr, n, *map(_size, (Hq, Hk, T, d))))
+
+
+def jattn_bwd_grouped(q, k, v, out, lse, dout, cu_seqlens, Hq: int, Hk: int, T: int, d: int, causal: bool,
+                      scale: float, dq, dk, dv, work, stream=None, check: bool = True) -> int:
+    """C ABI jattn_bwd_grouped (layouts as jattn_fwd_grouped), work jattn_bwd_grouped_bytes(...) bytes."""
+    import torch
+
+    bf, eq, ek = torch.bfloat16, Hq * T * d, Hk * T * d
+    arr, _, n = _cu_array(cu_seqlens)
+    rc = load_library().jattn_bwd_grouped(
+        _ptr(q, "q", bf, eq), _ptr(k, "k", bf, ek), _ptr(v, "v", bf, ek), _ptr(out, "out", bf, eq),
+        _ptr(lse, "lse", torch.float32, Hq * T), _ptr(dout, "dout", bf, eq), arr, n, _size(Hq), _size(Hk), _size(T),
+        _size(d), bool(causal), scale, _ptr(dq, "dq", bf, eq), _ptr(dk, "dk", bf, ek), _ptr(dv, "dv", bf, ek),
+        _work_ptr(work, jattn_bwd_grouped_bytes, cu_seqlens, Hq, Hk, T, d), _stream(stream))
+    if check and rc != 0:
+        raise JattnError(rc, "jattn_bwd_grouped")
     return rc
 
 

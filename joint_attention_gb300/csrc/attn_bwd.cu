@@ -58,7 +58,9 @@
 
 #include <type_traits>
 
+#include "grouped.cuh"
 #include "jattn_internal.h"
+#include "ring.cuh"
 #include "sm103_ptx.cuh"
 
 namespace jattn {
@@ -189,12 +191,43 @@ struct BwdUnit {
   // Ordered modes: contributions to that query tile's accumulator made before
   // this one.
   __device__ __forceinline__ int rank(int i) const { return ord == kDqAscending ? j : i; }
+  __device__ __forceinline__ int last_rank(int) const { return nkt - 1; }
   __device__ __forceinline__ int kv0() const { return row0 + 128 * j; }  // first key row
+  __device__ __forceinline__ int tiles() const { return nkt; }           // query tiles visited
+  __device__ __forceinline__ int head(int) const { return bh; }          // of the i-th query tile
+};
+
+// Grouped heads, causal or not: a key tile of one kv head visits the query tiles of
+// each of its query heads in turn (causal: from its own rows on).  Ordered modes add
+// each query tile's contributions by ascending key tiles; the units that hold the
+// lower key tiles of a segment come first (GroupedOrder), so no wait can deadlock.
+struct BwdUnitGrouped {
+  int bh;        // kv head
+  int h0;        // its first query head
+  int per_head;  // query tiles of each
+  int n;         // in all
+  int j, nkt, row0, end, prow0, ord;  // as in BwdUnit
+  bool causal;
+  __device__ __forceinline__ int query_tile(int i) const {
+    const int r = i % per_head;
+    if (ord == kDqAscending && !causal) return r;
+    const int q = r + j;
+    return q < nkt ? q : q - nkt;
+  }
+  __device__ __forceinline__ int rank(int) const { return j; }
+  __device__ __forceinline__ int last_rank(int i) const { return causal ? query_tile(i) : nkt - 1; }
+  __device__ __forceinline__ int kv0() const { return row0 + 128 * j; }
+  __device__ __forceinline__ int tiles() const { return n; }
+  __device__ __forceinline__ int head(int i) const { return h0 + i / per_head; }
+  // Whether the i-th query tile holds the key tile's own rows, of which each key
+  // reaches the queries from its own on.
+  __device__ __forceinline__ bool diagonal(int i) const { return causal && i % per_head == 0; }
 };
 
 // The [B, H, N, d] layout: one segment [0, N) per head, decoded without the
 // segment table.
 struct BwdWorkUniform {
+  static constexpr bool kGrouped = false;
   int upc;    // 128-row tiles per head
   int units;  // heads * upc
   int ord;    // dQ order
@@ -216,6 +249,7 @@ struct BwdWorkUniform {
 
 // Packed variable-length layout: segments from the table.
 struct BwdWork {
+  static constexpr bool kGrouped = false;
   int upc;    // units per head (padded rows per head / 128)
   int units;  // heads * upc
   int ord;    // dQ order
@@ -240,6 +274,36 @@ struct BwdWork {
   }
 };
 
+struct BwdWorkGrouped {
+  static constexpr bool kGrouped = true;
+  int units;
+  int heads, group;  // kv heads, and query heads of each
+  int ord;
+  bool causal;
+  struct {
+    int rows, prows;
+  } seg;
+  GroupedOrder order;
+  __device__ __forceinline__ BwdUnitGrouped unit(int u) const {
+    BwdUnitGrouped r;
+    const int k = u / heads;
+    r.bh = u - k * heads;
+    r.h0 = r.bh * group;
+    int s, level;
+    order.at(k, causal, &s, &level);
+    r.nkt = order.blocks[s];
+    r.j = causal ? r.nkt - 1 - level : level;
+    r.per_head = causal ? level + 1 : r.nkt;
+    r.n = r.per_head * group;
+    r.row0 = order.start[s];
+    r.end = r.row0 + order.len[s];
+    r.prow0 = order.prow[s];
+    r.ord = ord;
+    r.causal = causal;
+    return r;
+  }
+};
+
 struct BwdBars {
   uint64_t kv_full[2], kv_empty[2];
   uint64_t kv_mmadone[2];  // d = 64: the unit's MMAs are done with K/V buffer b
@@ -257,6 +321,7 @@ struct BwdBars {
   uint64_t drain_sync;  // the dQ drain threads' staging handshakes
   uint64_t kraw_full;   // d = 64: the unit's raw k tile has landed (epilogue)
   uint64_t drain[3];
+  uint64_t tail;  // grouped: a tile whose rows behind the segment are to be zeroed has landed
   uint32_t tmem_base;
   int abort;
   __align__(16) float gk[128];  // K-RMSNorm gain (d entries)
@@ -282,8 +347,8 @@ __device__ void bwd_producer(const CUtensorMap* mq, const CUtensorMap* mk, const
   int nkv_issued = 0, nq_issued = 0, ndo_issued = 0;
   bool ok = true;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u += gridDim.x, ++ui) {
-    const BwdUnit un = w.unit(u);
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+    const auto un = w.unit(u);
     const int bh = un.bh, kv0 = un.kv0();
     const int b = ui % C::kKVBufs;
     if (ui >= C::kKVBufs && !(ok = mbar_wait(&bars.kv_empty[b], ((ui / C::kKVBufs) - 1) & 1, ab, dev_err))) break;
@@ -323,6 +388,115 @@ __device__ void bwd_producer(const CUtensorMap* mq, const CUtensorMap* mk, const
       mbar_wait_drain(&bars.q_full[t % C::kQStages], (t / C::kQStages) & 1);
     for (int t = (ndo_issued > C::kDOStages ? ndo_issued - C::kDOStages : 0); t < ndo_issued; ++t)
       mbar_wait_drain(&bars.do_full[t % C::kDOStages], (t / C::kDOStages) & 1);
+  }
+}
+
+// The producer of grouped heads, a whole warp.  A ragged tile at a segment's end holds
+// the next sequence's rows (or anything, behind the last one), whose values times
+// probabilities of zero are no zeros if they are not finite; so such a tile, unless the
+// TMA unit fills in zeros at the tensor's end, comes in on a barrier of its own and its
+// rows behind the segment become zeros before the products may have it.
+template <int D>
+__device__ void bwd_producer_grouped(const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv,
+                                     const CUtensorMap* mdo, const CUtensorMap* mstats, uint8_t* sm, BwdBars& bars,
+                                     const BwdWorkGrouped& w, uint32_t* dev_err) {
+  using C = BwdCfg<D>;
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) {
+    tma_prefetch_desc(mq);
+    tma_prefetch_desc(mk);
+    tma_prefetch_desc(mv);
+    tma_prefetch_desc(mdo);
+    tma_prefetch_desc(mstats);
+  }
+  volatile int* ab = &bars.abort;
+  int nkv_issued = 0, nq_issued = 0, ndo_issued = 0;
+  uint32_t tails = 0;
+  // A tile's load on its own barrier, or, ragged, through `tail`.
+  auto load = [&](const CUtensorMap* m, uint8_t* dst, uint64_t* bar, int row, int head) {
+    for (int blk = 0; blk < D / 64; ++blk) tma_load_3d(dst + blk * 16384, m, bar, blk * 64, row, head);
+  };
+  auto clear = [&](uint8_t* tile, int valid) {  // rows from `valid` on of a landed tile
+    const uint32_t base = smem_u32(tile);
+    for (int i = valid * 8 + lane; i < 1024; i += 32)
+      for (int blk = 0; blk < D / 64; ++blk) st_shared_v4(base + blk * 16384 + i * 16, 0u, 0u, 0u, 0u);
+  };
+  auto landed = [&]() -> bool { return __all_sync(0xffffffffu, mbar_wait(&bars.tail, (tails++) & 1, ab, dev_err)); };
+  auto hand_over = [&](uint64_t* bar) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, dev_err));
+  };
+  bool ok = true;
+  int tb = 0;  // query tiles of the previous units
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<true>(u, ++ui)) {
+    const BwdUnitGrouped un = w.unit(u);
+    const int kv0 = un.kv0();
+    const int b = ui % C::kKVBufs;
+    const int ragged = un.end < w.seg.rows ? (un.end - un.row0) % 128 : 0;  // rows of such a last tile
+    if (ui >= C::kKVBufs && !(ok = wait(&bars.kv_empty[b], ((ui / C::kKVBufs) - 1) & 1))) break;
+    const bool kv_ragged = ragged && un.j == un.nkt - 1;
+    if (lane == 0) {
+      uint64_t* bar = kv_ragged ? &bars.tail : &bars.kv_full[b];
+      mbar_arrive_expect_tx(bar, 2u * C::kTile);
+      load(mk, sm + C::off_k(b), bar, kv0, un.bh);
+      load(mv, sm + C::off_v(b), bar, kv0, un.bh);
+    }
+    if (kv_ragged) {
+      if (!(ok = landed())) break;
+      clear(sm + C::off_k(b), ragged);
+      clear(sm + C::off_v(b), ragged);
+      hand_over(&bars.kv_full[b]);
+    }
+    ++nkv_issued;
+    for (int i = 0; i < un.n; ++i) {
+      const int t = tb + i;
+      const int qs = t % C::kQStages, ds = t % C::kDOStages;
+      const int qi = un.query_tile(i), head = un.head(i);
+      const bool q_ragged = ragged && qi == un.nkt - 1;
+      if (t >= C::kQStages && !(ok = wait(&bars.q_empty[qs], ((t / C::kQStages) - 1) & 1))) break;
+      uint8_t* q = sm + C::kOffQ + qs * C::kTile;
+      if (lane == 0) {
+        uint64_t* bar = q_ragged ? &bars.tail : &bars.q_full[qs];
+        mbar_arrive_expect_tx(bar, C::kTile + C::kStatsChunk);
+        tma_load_3d(sm + C::kOffStats + qs * C::kStatsChunk, mstats, bar, 0, un.prow0 + qi * 128, head);
+        load(mq, q, bar, un.row0 + qi * 128, head);
+      }
+      if (q_ragged) {
+        if (!(ok = landed())) break;
+        clear(q, ragged);
+        hand_over(&bars.q_full[qs]);
+      }
+      ++nq_issued;
+      if (t >= C::kDOStages && !(ok = wait(&bars.do_empty[ds], ((t / C::kDOStages) - 1) & 1))) break;
+      uint8_t* dout = sm + C::kOffDO + ds * C::kTile;
+      if (lane == 0) {
+        uint64_t* bar = q_ragged ? &bars.tail : &bars.do_full[ds];
+        mbar_arrive_expect_tx(bar, C::kTile);
+        load(mdo, dout, bar, un.row0 + qi * 128, head);
+      }
+      if (q_ragged) {
+        if (!(ok = landed())) break;
+        clear(dout, ragged);
+        hand_over(&bars.do_full[ds]);
+      }
+      ++ndo_issued;
+    }
+    tb += un.n;
+  }
+  __syncwarp();
+  if (*ab && lane == 0) {
+    // Aborted: let the copies already in flight land before the CTA exits.
+    if (tails > 0) mbar_wait_drain(&bars.tail, (tails - 1) & 1);
+    auto drain = [](int issued, int slots, uint64_t* bar) {
+      drain_ring(issued, slots, true, [&](int slot, uint32_t parity) { mbar_wait_drain(&bar[slot], parity); });
+    };
+    drain(nkv_issued, C::kKVBufs, bars.kv_full);
+    drain(nq_issued, C::kQStages, bars.q_full);
+    drain(ndo_issued, C::kDOStages, bars.do_full);
   }
 }
 
@@ -438,8 +612,8 @@ __device__ void bwd_mma_recompute(uint8_t* sm, BwdBars& bars, uint32_t tmem, con
   };
   bool ok = true;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u += gridDim.x, ++ui) {
-    const int nkt = w.unit(u).nkt;
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+    const int nkt = w.unit(u).tiles();
     const int b = ui % C::kKVBufs;
     if (!(ok = mbar_wait(&bars.kv_full[b], (ui / C::kKVBufs) & 1, ab, dev_err))) break;
     const uint64_t kK = sdesc_sw128(smem_u32(sm + C::off_k(b)), 16, 1024);
@@ -483,8 +657,8 @@ __device__ void bwd_mma_gradients(uint8_t* sm, BwdBars& bars, uint32_t tmem, con
   };
   bool ok = true;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u += gridDim.x, ++ui) {
-    const int nkt = w.unit(u).nkt;
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+    const int nkt = w.unit(u).tiles();
     for (int i = 0; i < nkt; ++i) {
       const int t = tb + i;
       if (!(ok = mbar_wait(&bars.p_ready, t & 1, ab, dev_err))) break;
@@ -512,8 +686,8 @@ __device__ void bwd_mma_dq(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& w
   const uint64_t mDS = sdesc_sw128(smem_u32(sm + C::kOffDS), 16384, 1024);
   bool ok = true;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u += gridDim.x, ++ui) {
-    const int nkt = w.unit(u).nkt;
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+    const int nkt = w.unit(u).tiles();
     const int b = ui % C::kKVBufs;
     if (!(ok = mbar_wait(&bars.kv_full[b], (ui / C::kKVBufs) & 1, ab, dev_err))) break;
     const uint64_t mK = sdesc_sw128(smem_u32(sm + C::off_k(b)), 16384, 1024);
@@ -559,8 +733,8 @@ __device__ void bwd_mma(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& w, u
 
   bool ok = true;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u += gridDim.x, ++ui) {
-    const int nkt = w.unit(u).nkt;
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+    const int nkt = w.unit(u).tiles();
     const int b = ui % C::kKVBufs;
     const int t0 = tb;
     tb += nkt;
@@ -626,6 +800,15 @@ __device__ void bwd_mma(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& w, u
   mbar_wait_drain(&bars.drain[0], 0);
 }
 
+// Of 2 N values packed in pairs, those before `first` become zeros (whatever they
+// are: a masked product with a value that is not finite is no zero by itself).
+template <int N>
+__device__ __forceinline__ void only_from(int first, uint32_t (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (2 * i < first) x[i] = 2 * i + 1 < first ? 0u : x[i] & 0xFFFF0000u;
+}
+
 // Key-row threads of one compute group (query columns 64g .. 64g+63).
 template <int D, class W>
 __device__ void bwd_compute(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, const W& w, float scale,
@@ -643,13 +826,15 @@ __device__ void bwd_compute(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, co
   volatile int* ab = &bars.abort;
 
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; u < w.units; u += gridDim.x, ++ui) {
-    const BwdUnit un = w.unit(u);
+  for (int u = blockIdx.x, ui = 0; u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+    const auto un = w.unit(u);
     const bool key_live = un.kv0() + kr < un.end;
     const int t0 = tb;
-    tb += un.nkt;
-    for (int i = 0; i < un.nkt; ++i) {
+    tb += un.tiles();
+    for (int i = 0; i < un.tiles(); ++i) {
       const int t = t0 + i;
+      bool diagonal = false;
+      if constexpr (W::kGrouped) diagonal = un.diagonal(i);
       bool ok = mbar_wait(&bars.s_full, t & 1, ab, dev_err);
       if (!__all_sync(0xffffffffu, ok)) return;
       tc_fence_after();
@@ -685,6 +870,9 @@ __device__ void bwd_compute(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, co
           for (int e = 0; e < 32; e += 2) pp[(c * 32 + e) / 2] = 0u;
         }
       }
+      if constexpr (W::kGrouped) {
+        if (diagonal) only_from<32>(kr - 64 * g, pp);
+      }
       if (C::kSplitIssuers && t > 0) {
         // dV(t-1) must be done reading P^T(t-1) before it is overwritten;
         // waited for after all the exponentials, so that they overlap dV(t-1).
@@ -715,6 +903,9 @@ __device__ void bwd_compute(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, co
           for (int e = 0; e < 32; e += 2)
             dsw[c][e / 2] = bf16x2_mul(pp[(c * 32 + e) / 2], pack_bf16x2(__uint_as_float(dpall[c][e]),
                                                                           __uint_as_float(dpall[c][e + 1])));
+          if constexpr (W::kGrouped) {
+            if (diagonal) only_from<16>(kr - 64 * g - 32 * c, dsw[c]);
+          }
           // d = 64: dS^T(t) also goes over this group's dP^T(t) columns
           // (packed like P^T), where dK(t) reads it; dP(t+1) is issued once
           // dK(t) is done.
@@ -739,6 +930,14 @@ __device__ void bwd_compute(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, co
       mbar_arrive(&bars.ds_ready);
     }
   }
+}
+
+// A grouped query row behind the segment adds zeros to the next one's: its dS are zeros,
+// but their products with keys that are not finite would be none.
+template <int N>
+__device__ __forceinline__ void zero_all(uint32_t (&a)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = 0u;
 }
 
 // d = 64, warps 8-11 (one thread per query row): per query tile, dQ_t out of
@@ -794,14 +993,14 @@ __device__ void bwd_drain64(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& 
   bool ok = true;
   const int tiles_per_head = w.seg.prows / 128;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x; ok && u < w.units; u += gridDim.x) {
-    const BwdUnit un = w.unit(u);
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+    const auto un = w.unit(u);
     const int t0 = tb;
-    tb += un.nkt;
-    for (int i = 0; i < un.nkt; ++i) {
+    tb += un.tiles();
+    for (int i = 0; i < un.tiles(); ++i) {
       const int t = t0 + i;
-      const int qt = un.query_tile(i), rank = un.rank(i);
-      uint32_t* cnt = counters + static_cast<size_t>(un.bh) * tiles_per_head + un.prow0 / 128 + qt;
+      const int qt = un.query_tile(i), rank = un.rank(i), head = un.head(i);
+      uint32_t* cnt = counters + static_cast<size_t>(head) * tiles_per_head + un.prow0 / 128 + qt;
       // Ordered modes: the counter read ahead (its latency overlaps the wait for dQ).
       const uint32_t seen = kOrd && leader && rank > 0 ? ld_acquire_gpu(cnt) : 0u;
       const bool store = kFirstStore && rank == 0;
@@ -812,6 +1011,9 @@ __device__ void bwd_drain64(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& 
       tmem_ld32(tQ, *reinterpret_cast<uint32_t(*)[32]>(a));
       tmem_ld32(tQ + 32, *reinterpret_cast<uint32_t(*)[32]>(a + 32));
       tmem_wait_ld();
+      if constexpr (W::kGrouped) {
+        if (un.row0 + qt * 128 + r128 >= un.end) zero_all(a);
+      }
       tc_fence_before();
       mbar_arrive(&bars.dq_free);
       if (leader) {
@@ -835,17 +1037,17 @@ __device__ void bwd_drain64(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& 
       if (leader) {
         const int row = un.row0 + qt * 128;
         if (store) {
-          tma_store_3d(mdq, stage, 0, row, un.bh);
-          tma_store_3d(mdq, stage + 16384, 32, row, un.bh);
+          tma_store_3d(mdq, stage, 0, row, head);
+          tma_store_3d(mdq, stage + 16384, 32, row, head);
         } else {
-          tma_reduce_add_3d(mdq, stage, 0, row, un.bh);
-          tma_reduce_add_3d(mdq, stage + 16384, 32, row, un.bh);
+          tma_reduce_add_3d(mdq, stage, 0, row, head);
+          tma_reduce_add_3d(mdq, stage + 16384, 32, row, head);
         }
         bulk_commit_group();
         if constexpr (kOrd) {
-          if (rank != un.nkt - 1) {
+          if (rank != un.last_rank(i)) {
             pend = cnt;
-            if (i == un.nkt - 1) complete_previous();
+            if (i == un.tiles() - 1) complete_previous();
           }
         }
       }
@@ -855,6 +1057,15 @@ __device__ void bwd_drain64(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& 
     if (ok) complete_previous();
     bulk_wait_group0();
   }
+}
+
+// 8 accumulator columns times `scale`, in bf16.
+__device__ __forceinline__ uint4 scaled8(const uint32_t (&a)[32], int at, float scale) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = pack_bf16x2(__uint_as_float(a[at + 2 * i]) * scale, __uint_as_float(a[at + 2 * i + 1]) * scale);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // d = 128, warps 8-11 (one thread per query row, then per key row).
@@ -936,15 +1147,15 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
   const size_t rows = static_cast<size_t>(w.seg.rows);
   const int tiles_per_head = w.seg.prows / 128;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u += gridDim.x, ++ui) {
-    const BwdUnit un = w.unit(u);
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+    const auto un = w.unit(u);
     const int bh = un.bh;
     const int t0 = tb;
-    tb += un.nkt;
-    for (int i = 0; i < un.nkt; ++i) {
+    tb += un.tiles();
+    for (int i = 0; i < un.tiles(); ++i) {
       const int t = t0 + i;
-      const int qt = un.query_tile(i), rank = un.rank(i);
-      uint32_t* cnt = counters + static_cast<size_t>(bh) * tiles_per_head + un.prow0 / 128 + qt;
+      const int qt = un.query_tile(i), rank = un.rank(i), head = un.head(i);
+      uint32_t* cnt = counters + static_cast<size_t>(head) * tiles_per_head + un.prow0 / 128 + qt;
       // Ordered modes: the counter read ahead (its latency overlaps the wait for dQ).
       const uint32_t seen = kOrd && leader && rank > 0 ? ld_acquire_gpu(cnt) : 0u;
       const bool store = kFirstStore && rank == 0;
@@ -958,12 +1169,15 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
       tc_fence_after();
       // Columns 32-95 into H1 / H2, whose reduces go first: the producer
       // reloads the Q stage once they have been read.
+      const bool behind = W::kGrouped && row + r128 >= un.end;  // the segment
       uint32_t a[32];
       tmem_ld32(tQ + 32, a);
       tmem_wait_ld();
+      if (behind) zero_all(a);
       stage32(h1, a);
       tmem_ld32(tQ + 64, a);
       tmem_wait_ld();
+      if (behind) zero_all(a);
       stage32(h2, a);
       fence_proxy_async_smem();
       if constexpr (kOrd) {
@@ -976,11 +1190,11 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
       if (!(ok = drain_sync())) break;
       if (leader) {
         if (store) {
-          tma_store_3d(mdq, h1, 32, row, bh);
-          tma_store_3d(mdq, h2, 64, row, bh);
+          tma_store_3d(mdq, h1, 32, row, head);
+          tma_store_3d(mdq, h2, 64, row, head);
         } else {
-          tma_reduce_add_3d(mdq, h1, 32, row, bh);
-          tma_reduce_add_3d(mdq, h2, 64, row, bh);
+          tma_reduce_add_3d(mdq, h1, 32, row, head);
+          tma_reduce_add_3d(mdq, h2, 64, row, head);
         }
         bulk_commit_group();
       }
@@ -989,6 +1203,10 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
       tmem_ld32(tQ, a);
       tmem_ld32(tQ + 96, b);
       tmem_wait_ld();
+      if (behind) {
+        zero_all(a);
+        zero_all(b);
+      }
       tc_fence_before();
       mbar_arrive(&bars.dq_free);
       // H0 is free once the previous tile's reduces from it have read it
@@ -999,8 +1217,8 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
       fence_proxy_async_smem();
       if (!(ok = drain_sync())) break;
       if (leader) {
-        if (store) tma_store_3d(mdq, h0, 0, row, bh);
-        else tma_reduce_add_3d(mdq, h0, 0, row, bh);
+        if (store) tma_store_3d(mdq, h0, 0, row, head);
+        else tma_reduce_add_3d(mdq, h0, 0, row, head);
         bulk_commit_group();
         bulk_wait_group_read<1>();                        // H1 and H2 have been read
         mbar_arrive(&bars.q_empty[t % C::kQStages]);  // the producer may reload the Q stage
@@ -1011,13 +1229,13 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
       fence_proxy_async_smem();
       if (!(ok = drain_sync())) break;
       if (leader) {
-        if (store) tma_store_3d(mdq, h0, 96, row, bh);
-        else tma_reduce_add_3d(mdq, h0, 96, row, bh);
+        if (store) tma_store_3d(mdq, h0, 96, row, head);
+        else tma_reduce_add_3d(mdq, h0, 96, row, head);
         bulk_commit_group();
         if constexpr (kOrd) {
-          if (rank != un.nkt - 1) {
+          if (rank != un.last_rank(i)) {
             pend = cnt;
-            if (i == un.nkt - 1) complete_previous();
+            if (i == un.tiles() - 1) complete_previous();
           }
         }
       }
@@ -1031,8 +1249,8 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
     const int n = un.kv0() + r128;  // key row of this thread
     const bool key_live = n < un.end;
     const size_t row_off = (static_cast<size_t>(bh) * rows + (key_live ? n : 0)) * D;
-    const float r = key_live ? rk[static_cast<size_t>(bh) * rows + n] : 0.f;
-    const uint4* krow = reinterpret_cast<const uint4*>(k_raw + row_off);
+    const float r = !W::kGrouped && key_live ? rk[static_cast<size_t>(bh) * rows + n] : 0.f;
+    const uint4* krow = W::kGrouped ? nullptr : reinterpret_cast<const uint4*>(k_raw + row_off);
     uint4* dvrow = reinterpret_cast<uint4*>(dv + row_off);
     uint4* dkrow = reinterpret_cast<uint4*>(dk + row_off);
 #pragma unroll
@@ -1056,6 +1274,23 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
         }
       }
     }
+    if constexpr (W::kGrouped) {  // no norm: dk = scale times the accumulator
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t a[32];
+        tmem_ld32(tDK + c * 32, a);
+        tmem_wait_ld();
+        if (c == D / 32 - 1) {
+          tc_fence_before();
+          mbar_arrive(&bars.acc_free_k);
+        }
+        if (key_live) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) dkrow[c * 4 + q] = scaled8(a, q * 8, scale);
+        }
+      }
+      continue;
+    } else {
     // The gain, 8 columns at a time (two 16-byte broadcasts).
     auto gain8 = [&](int col, float (&g)[8]) {
       const float4 g0 = *reinterpret_cast<const float4*>(&bars.gk[col]);
@@ -1145,12 +1380,13 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
     if (!(ok = epi_sync())) break;  // the warp sums are complete
     bars.dgk_cta[r128] += ((bars.wsum[0][r128] + bars.wsum[1][r128]) + bars.wsum[2][r128]) + bars.wsum[3][r128];
     if (!(ok = epi_sync())) break;  // ... and read before the next unit rewrites them
+    }
   }
   if (leader) {
     if (ok) complete_previous();
     bulk_wait_group0();
   }
-  dgk_part[static_cast<size_t>(blockIdx.x) * D + r128] = bars.dgk_cta[r128];
+  if constexpr (!W::kGrouped) dgk_part[static_cast<size_t>(blockIdx.x) * D + r128] = bars.dgk_cta[r128];
 }
 
 // d = 64 epilogue warps (warps 12-15, one thread per key row): per unit,
@@ -1181,7 +1417,7 @@ __device__ void bwd_epilogue_warps(uint8_t* sm, BwdBars& bars, uint32_t tmem, co
   uint32_t epi_uses = 0;
   uint32_t kraw_issued = 0, kraw_done = 0;  // thread 0 issues the raw k tile loads
   if (r128 == 0) {
-    tma_prefetch_desc(mkraw);
+    if (!W::kGrouped) tma_prefetch_desc(mkraw);
     tma_prefetch_desc(mdk);
     tma_prefetch_desc(mdv);
   }
@@ -1193,15 +1429,16 @@ __device__ void bwd_epilogue_warps(uint8_t* sm, BwdBars& bars, uint32_t tmem, co
   };
   bool ok = true;
   const size_t rows = static_cast<size_t>(w.seg.rows);
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u += gridDim.x, ++ui) {
-    const BwdUnit un = w.unit(u);
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+    const auto un = w.unit(u);
     const int bh = un.bh, kv0 = un.kv0();
     const int b = ui % C::kKVBufs;
     const int n = kv0 + r128;
     const bool key_live = n < un.end;
     const int live_rows = un.end - kv0 < 128 ? un.end - kv0 : 128;
     const size_t tile_off = (static_cast<size_t>(bh) * rows + kv0) * D;
-    const float r = key_live ? rk[static_cast<size_t>(bh) * rows + n] : 0.f;
+    float r = 0.f;
+    if constexpr (!W::kGrouped) r = key_live ? rk[static_cast<size_t>(bh) * rows + n] : 0.f;
     const uint32_t tile_k = smem_u32(sm + C::off_k(b));  // k, then dk
     const uint32_t tile_v = smem_u32(sm + C::off_v(b));  // dv
 
@@ -1214,7 +1451,7 @@ __device__ void bwd_epilogue_warps(uint8_t* sm, BwdBars& bars, uint32_t tmem, co
     // it), in the same 128-byte swizzled layout the tile had.  Rows past the
     // segment (zero-filled past the tensor's end, the next sequence's rows in
     // a packed call) have r = 0 and zero dK, so they contribute nothing.
-    if (r128 == 0) {
+    if (!W::kGrouped && r128 == 0) {
       mbar_arrive_expect_tx(&bars.kraw_full, C::kTile);
       tma_load_3d(sm + C::off_k(b), mkraw, &bars.kraw_full, 0, kv0, bh);
       ++kraw_issued;
@@ -1246,6 +1483,15 @@ __device__ void bwd_epilogue_warps(uint8_t* sm, BwdBars& bars, uint32_t tmem, co
     tmem_wait_ld();
     tc_fence_before();
     mbar_arrive(&bars.acc_free_k);
+    if constexpr (W::kGrouped) {  // no norm: dk = scale times the accumulator
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 o = scaled8(*reinterpret_cast<const uint32_t(*)[32]>(dkr + c * 32), q * 8, scale);
+          st_shared_v4(chunk_addr(tile_k, r128, c * 4 + q), o.x, o.y, o.z, o.w);
+        }
+    } else {
     ok = mbar_wait(&bars.kraw_full, ui & 1, ab, dev_err);
     if (!(ok = __all_sync(0xffffffffu, ok))) break;
     ++kraw_done;
@@ -1323,9 +1569,10 @@ __device__ void bwd_epilogue_warps(uint8_t* sm, BwdBars& bars, uint32_t tmem, co
       }
       bars.wsum[warp & 3][c * 32 + lane] = __uint_as_float(a[0]);
     }
+    }
     fence_proxy_async_smem();  // the dk / dv tiles, for the TMA stores
     if (!(ok = epi_sync())) break;  // dk tile, dv tile and warp sums complete
-    if (r128 < D)
+    if (!W::kGrouped && r128 < D)
       bars.dgk_cta[r128] += ((bars.wsum[0][r128] + bars.wsum[1][r128]) + bars.wsum[2][r128]) + bars.wsum[3][r128];
     if (live_rows == 128 || un.end == w.seg.rows) {
       // The tiles out by TMA (rows past the tensor's end are clipped).
@@ -1360,7 +1607,7 @@ __device__ void bwd_epilogue_warps(uint8_t* sm, BwdBars& bars, uint32_t tmem, co
     if (kraw_issued > kraw_done) mbar_wait_drain(&bars.kraw_full, kraw_done & 1);
     bulk_wait_group0();  // the dk / dv stores are complete
   }
-  if (r128 < D) dgk_part[static_cast<size_t>(blockIdx.x) * D + r128] = bars.dgk_cta[r128];
+  if (!W::kGrouped && r128 < D) dgk_part[static_cast<size_t>(blockIdx.x) * D + r128] = bars.dgk_cta[r128];
 }
 
 template <int D, class W, bool kOrd>
@@ -1416,6 +1663,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(&bars.drain[0], 1);
     mbar_init(&bars.drain[1], 1);
     mbar_init(&bars.drain[2], 1);
+    mbar_init(&bars.tail, 1);
     bars.abort = 0;
     fence_mbar_init();
   }
@@ -1448,9 +1696,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 
   griddep_wait();  // the previous grid's writes (q_hat, k_hat, statistics chunks, zeroed dQ) are visible
-  for (int c = threadIdx.x; c < D; c += blockDim.x) {
-    bars.gk[c] = gk[c];
-    bars.dgk_cta[c] = 0.f;
+  if constexpr (!W::kGrouped) {
+    for (int c = threadIdx.x; c < D; c += blockDim.x) {
+      bars.gk[c] = gk[c];
+      bars.dgk_cta[c] = 0.f;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -1469,8 +1719,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     } else if (warp < kWarpTma) {
       bwd_epilogue_warps<D>(sm, bars, tmem, w, scale, &map_kraw, &map_dk, &map_dv, rk, dk, dv, dgk_part, dev_err);
     } else if (warp == kWarpTma) {
-      if (lane == 0)
-        bwd_producer<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, sm, bars, w, dev_err);
+      if constexpr (W::kGrouped) {
+        bwd_producer_grouped<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, sm, bars, w, dev_err);
+      } else {
+        if (lane == 0) bwd_producer<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, sm, bars, w, dev_err);
+      }
     } else if (warp == kWarpMma0) {
       if (lane == 0) bwd_mma_recompute<D>(sm, bars, tmem, w, dev_err);
     } else if (warp == kWarpMma1) {
@@ -1489,8 +1742,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     } else if (warp < kWarpTma) {
       setmaxnreg_dec<kRegIdle128>();
     } else if (warp == kWarpTma) {
-      if (lane == 0)
-        bwd_producer<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, sm, bars, w, dev_err);
+      if constexpr (W::kGrouped) {
+        bwd_producer_grouped<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, sm, bars, w, dev_err);
+      } else {
+        if (lane == 0) bwd_producer<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, sm, bars, w, dev_err);
+      }
     } else if (warp == kWarpMma0) {
       if (lane == 0) bwd_mma<D>(sm, bars, tmem, w, dev_err);
     }
@@ -1506,7 +1762,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 template <int D, bool kOrd, class W>
 cudaError_t launch_bwd_w(const W& w, int grid, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                          const CUtensorMap& mdo, const CUtensorMap& mstats, const CUtensorMap& mdq,
-                         const CUtensorMap& mkraw, const CUtensorMap& mdk, const CUtensorMap& mdv, const AttnShape& s,
+                         const CUtensorMap& mkraw, const CUtensorMap& mdk, const CUtensorMap& mdv, float scale,
                          const uint16_t* k_raw, const float* rk, const float* gk, uint16_t* dk, uint16_t* dv,
                          float* dqacc, uint32_t* counters, float* dgk_part, uint32_t* dev_err, cudaStream_t st) {
   using C = BwdCfg<D>;
@@ -1520,7 +1776,7 @@ cudaError_t launch_bwd_w(const W& w, int grid, const CUtensorMap& mq, const CUte
   e = cudaFuncGetAttributes(&fa, kernel);
   if (e != cudaSuccess) return e;
   if (fa.numRegs < kRegLaunchMin || fa.numRegs > kRegLaunchMax) return cudaErrorInvalidConfiguration;
-  return launch_pdl(kernel, dim3(grid), dim3(kBwdThreads), C::kDynSmem, st, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, w, s.scale,
+  return launch_pdl(kernel, dim3(grid), dim3(kBwdThreads), C::kDynSmem, st, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, w, scale,
                     reinterpret_cast<const __nv_bfloat16*>(k_raw), rk, gk,
                     reinterpret_cast<__nv_bfloat16*>(dk), reinterpret_cast<__nv_bfloat16*>(dv), dqacc, counters,
                     dgk_part, dev_err);
@@ -1578,9 +1834,9 @@ cudaError_t launch_bwd_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
     w.units = s.BH * w.upc;
     w.ord = plan.ord;
     if (plan.ord == kDqArrival)
-      return launch_bwd_w<D, false>(w, plan.grid, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, s, k_raw, rk, gk, dk, dv,
+      return launch_bwd_w<D, false>(w, plan.grid, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, s.scale, k_raw, rk, gk, dk, dv,
                                     dqacc, counters, dgk_part, dev_err, st);
-    return launch_bwd_w<D, true>(w, plan.grid, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, s, k_raw, rk, gk, dk, dv,
+    return launch_bwd_w<D, true>(w, plan.grid, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, s.scale, k_raw, rk, gk, dk, dv,
                                  dqacc, counters, dgk_part, dev_err, st);
   }
   BwdWork w;
@@ -1589,13 +1845,73 @@ cudaError_t launch_bwd_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
   w.units = s.BH * w.upc;
   w.ord = plan.ord;
   if (plan.ord == kDqArrival)
-    return launch_bwd_w<D, false>(w, plan.grid, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, s, k_raw, rk, gk, dk, dv,
+    return launch_bwd_w<D, false>(w, plan.grid, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, s.scale, k_raw, rk, gk, dk, dv,
                                   dqacc, counters, dgk_part, dev_err, st);
-  return launch_bwd_w<D, true>(w, plan.grid, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, s, k_raw, rk, gk, dk, dv, dqacc,
+  return launch_bwd_w<D, true>(w, plan.grid, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, s.scale, k_raw, rk, gk, dk, dv, dqacc,
                                counters, dgk_part, dev_err, st);
 }
 
+// dq of grouped heads: bf16(scale dS K) from the fp32 accumulator, the rows of the
+// sequences alone.  Bound by HBM: 6 bytes a value, read and written once.
+constexpr int kDqThreads = 256, kDqChunks = 4;  // 8-value chunks of a thread
+__global__ void __launch_bounds__(kDqThreads) grouped_dq_kernel(const float4* __restrict__ acc, uint4* __restrict__ dq,
+                                                                int64_t head_chunks, int64_t chunks, float scale) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t head = static_cast<int64_t>(blockIdx.y) * head_chunks;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kDqThreads * kDqChunks) + threadIdx.x;
+  float4 a[kDqChunks][2];
+#pragma unroll
+  for (int i = 0; i < kDqChunks; ++i) {
+    const int64_t c = first + i * kDqThreads;
+    if (c < chunks) {
+      a[i][0] = acc[(head + c) * 2];
+      a[i][1] = acc[(head + c) * 2 + 1];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kDqChunks; ++i) {
+    const int64_t c = first + i * kDqThreads;
+    if (c < chunks)
+      dq[head + c] = make_uint4(pack_bf16x2(a[i][0].x * scale, a[i][0].y * scale),
+                                pack_bf16x2(a[i][0].z * scale, a[i][0].w * scale),
+                                pack_bf16x2(a[i][1].x * scale, a[i][1].y * scale),
+                                pack_bf16x2(a[i][1].z * scale, a[i][1].w * scale));
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_grouped_dq(const GroupedShape& s, const float* dqacc, uint16_t* dq, cudaStream_t st) {
+  const int64_t row = s.d / 8, chunks = s.seg.cu[s.seg.n] * row, block = kDqThreads * kDqChunks;
+  return launch_pdl(grouped_dq_kernel, dim3(static_cast<unsigned>((chunks + block - 1) / block), s.Hq),
+                    dim3(kDqThreads), 0, st, reinterpret_cast<const float4*>(dqacc), reinterpret_cast<uint4*>(dq),
+                    s.T * row, chunks, s.scale);
+}
+
+cudaError_t launch_attn_bwd_grouped(const GroupedShape& s, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                    const uint16_t* dout, const uint16_t* stats, float* dqacc, uint32_t* counters,
+                                    uint16_t* dk, uint16_t* dv, uint32_t* dev_err, cudaStream_t st) {
+  CUtensorMap mq, mk, mv, mdo, mstats, mdq, mdk, mdv;
+  if (!encode_bhnd_map(&mq, q, s.Hq, s.T, s.d) || !encode_bhnd_map(&mk, k, s.Hk, s.T, s.d) ||
+      !encode_bhnd_map(&mv, v, s.Hk, s.T, s.d) || !encode_bhnd_map(&mdo, dout, s.Hq, s.T, s.d) ||
+      !encode_stats_map(&mstats, stats, s.Hq, s.seg.prows) || !encode_dq_map(&mdq, dqacc, s.Hq, s.T, s.d) ||
+      !encode_bhnd_map(&mdk, dk, s.Hk, s.T, s.d) || !encode_bhnd_map(&mdv, dv, s.Hk, s.T, s.d))
+    return cudaErrorInvalidValue;
+  BwdWorkGrouped w;
+  w.heads = s.Hk;
+  w.group = s.Hq / s.Hk;
+  w.causal = s.causal;
+  w.ord = s.deterministic ? kDqAscending : kDqArrival;
+  w.seg.rows = s.T;
+  w.seg.prows = s.seg.prows;
+  w.units = s.Hk * w.order.make(s, kTileN);
+  const int sms = device_sm_count(), grid = w.units < sms ? w.units : sms;
+  auto launch = s.d == 64 ? (s.deterministic ? launch_bwd_w<64, true, BwdWorkGrouped> : launch_bwd_w<64, false, BwdWorkGrouped>)
+                          : (s.deterministic ? launch_bwd_w<128, true, BwdWorkGrouped> : launch_bwd_w<128, false, BwdWorkGrouped>);
+  return launch(w, grid, mq, mk, mv, mdo, mstats, mdq, mk, mdk, mdv, s.scale, k, nullptr, nullptr, dk, dv, dqacc,
+                counters, nullptr, dev_err, st);
+}
 
 // One dgk partial per CTA.
 int attn_bwd_dgk_parts(const AttnShape& s) { return bwd_plan(s).grid; }

@@ -37,6 +37,7 @@
 // key columns past N in the last key tile are masked to -inf.
 #include <cuda_bf16.h>
 
+#include "grouped.cuh"
 #include "jattn_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -108,16 +109,18 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 // tiles, ring slots and every per-tile barrier are counted on across units.
 struct FwdUnit {
   int bh;      // head
+  int kvh;     // the head of its keys and values
   int q0;      // first query row (tile A) in the head
   int kvb;     // the segment's first row
   int end;     // one past its last row
-  int nkv;     // its 128-key tiles
+  int nkv;     // 128-key tiles that the unit streams
   bool has_b;  // tile B has rows
 };
 
 // The [B, H, N, d] layout: one segment [0, N) per head, decoded without the
 // segment table.
 struct FwdWorkUniform {
+  static constexpr bool kGrouped = false;
   int upc;    // 256-row blocks per head
   int units;  // heads * upc
   int nkv;    // 128-key tiles per head
@@ -126,7 +129,7 @@ struct FwdWorkUniform {
   } seg;
   __device__ __forceinline__ FwdUnit unit(int u) const {
     FwdUnit r;
-    r.bh = u / upc;
+    r.bh = r.kvh = u / upc;
     r.q0 = (u - r.bh * upc) * 2 * kTileM;
     r.kvb = 0;
     r.end = seg.rows;
@@ -138,13 +141,14 @@ struct FwdWorkUniform {
 
 // Packed variable-length layout: segments from the table.
 struct FwdWork {
+  static constexpr bool kGrouped = false;
   int upc;    // units per head
   int units;  // heads * upc
   SegTable seg;
   int uf[kMaxSegments + 1];  // units before each segment (256-row blocks)
   __device__ __forceinline__ FwdUnit unit(int u) const {
     FwdUnit r;
-    r.bh = u / upc;
+    r.bh = r.kvh = u / upc;
     const int k = u - r.bh * upc;
     int lo = 0, hi = seg.n;  // uf[lo] <= k < uf[hi]
     while (hi - lo > 1) {
@@ -160,6 +164,43 @@ struct FwdWork {
     return r;
   }
 };
+
+// Grouped heads, causal or not (no QK-RMSNorm, rows as they are): units in
+// GroupedOrder's order, the longest first.  A causal unit ends with the key tile
+// of its own last rows, and tile A one key tile before tile B.
+struct FwdWorkGrouped {
+  static constexpr bool kGrouped = true;
+  int units;
+  int heads, group;  // query heads, and query heads of each kv head
+  bool causal;
+  struct {
+    int rows;
+  } seg;
+  GroupedOrder order;
+  __device__ __forceinline__ FwdUnit unit(int u) const {
+    FwdUnit r;
+    const int k = u / heads;
+    r.bh = u - k * heads;
+    r.kvh = r.bh / group;
+    int s, level;
+    order.at(k, causal, &s, &level);
+    r.kvb = order.start[s];
+    r.end = r.kvb + order.len[s];
+    r.q0 = r.kvb + level * 2 * kTileM;
+    r.has_b = r.q0 + kTileM < r.end;
+    r.nkv = causal ? 2 * level + (r.has_b ? 2 : 1) : (order.len[s] + kTileN - 1) / kTileN;
+    return r;
+  }
+  // Key tiles of tile x of the unit.
+  __device__ __forceinline__ int tiles(const FwdUnit& r, int x) const {
+    return causal && x == 0 && r.has_b ? r.nkv - 1 : r.nkv;
+  }
+};
+template <class W>
+__device__ __forceinline__ int tiles_of(const W& w, const FwdUnit& r, int x) {
+  if constexpr (W::kGrouped) return w.tiles(r, x);
+  else return r.nkv;
+}
 
 // Warp 11 (training pair): zeroes the backward's fp32 dQ accumulator rows of
 // this CTA's units, with HBM bandwidth the forward leaves idle, then counts
@@ -195,7 +236,7 @@ __device__ void fwd_producer(const CUtensorMap* map_q, const CUtensorMap* map_k,
   volatile int* ab = &bars.abort;
   int issued = 0, q_issued = 0;
   bool ok = true;
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u += gridDim.x, ++ui) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
     const FwdUnit un = w.unit(u);
     const int bh = un.bh, q0 = un.q0;
     const bool hasB = un.has_b;
@@ -216,7 +257,7 @@ __device__ void fwd_producer(const CUtensorMap* map_q, const CUtensorMap* map_k,
       const CUtensorMap* m = (i & 1) ? map_v : map_k;
       const int kv0 = un.kvb + (i >> 1) * kTileN;
       for (int blk = 0; blk < D / 64; ++blk)
-        tma_load_3d(sm + C::kOffRing + slot * C::kSlotBytes + blk * 16384, m, &bars.full[slot], blk * 64, kv0, bh);
+        tma_load_3d(sm + C::kOffRing + slot * C::kSlotBytes + blk * 16384, m, &bars.full[slot], blk * 64, kv0, un.kvh);
     }
   }
   if (*ab) {
@@ -275,12 +316,12 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
   // unit's epilogue.
   bool s0_issued = false;
   bool ok = true;
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u += gridDim.x, ++ui) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
     const int b = ui % C::kQBufs;
     const FwdUnit uo = w.unit(u);
-    const int nkv = uo.nkv;
+    const int nkv = tiles_of(w, uo, x);
     const int g0 = gb;  // first ring item of the unit
-    gb += 2 * nkv;
+    gb += 2 * uo.nkv;
     if (x == 1 && !uo.has_b) {
       // No tile B in this unit: only release the unit's slots and Q buffer.
       for (int i = 0; ok && i < 2 * nkv; ++i) {
@@ -305,9 +346,9 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
     s0_issued = false;
     // The next unit, if this issuer computes a tile of it (tile B may be
     // absent): its first score product goes out early (d = 64).
-    const int un = u + static_cast<int>(gridDim.x);
+    const int un = next_unit<W::kGrouped>(u, ui + 1);
     const bool early_next = C::kSepP && un < w.units && (x == 0 || w.unit(un).has_b);
-    const int bn = (ui + 1) % C::kQBufs, g0n = g0 + 2 * nkv;
+    const int bn = (ui + 1) % C::kQBufs, g0n = g0 + 2 * uo.nkv;
     for (int j = 0; ok && j < nkv; ++j) {
       const int jt = jx + j;
       const int iv = g0 + 2 * j + 1, ik = g0 + 2 * j + 2;
@@ -357,6 +398,13 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
       umma_commit(&bars.empty[slot_of(iv)]);
       if (more) umma_commit(&bars.empty[slot_of(ik)]);
     }
+    if constexpr (W::kGrouped) {
+      // Tile A of a causal unit: the key tile of tile B's own rows is only released.
+      for (int i = 2 * nkv; ok && i < 2 * uo.nkv; ++i) {
+        if (!(ok = mbar_wait(&bars.full[slot_of(g0 + i)], phase_of(g0 + i), ab, dev_err))) break;
+        umma_commit(&bars.empty[slot_of(g0 + i)]);
+      }
+    }
     jx += nkv;
   }
   // Every MMA this thread issued has completed once this barrier flips.
@@ -364,11 +412,97 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
   mbar_wait_drain(&bars.drain[x], 0);
 }
 
+// The tensors themselves, for grouped rows that the products cannot serve.
+struct FwdRaw {
+  const __nv_bfloat16 *q, *k, *v;
+};
+
+__device__ __forceinline__ void bf16x8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// A causal row's product covers the whole key tile of its own rows, and a value of
+// a later row there that is not finite, times a probability of zero, is NaN.  So
+// a row of O that is not finite, with such a value among its tile's later rows, is
+// computed again from the rows that it sees alone (rare, and slow), into the same
+// TMEM columns.  In common: O is read once more, some 0.1 us a unit.
+template <int D>
+__device__ __forceinline__ void restore_masked(uint32_t tO, const FwdUnit& un, int qt0, int n, bool live, float m_ref,
+                                               float scale_log2, int rows, const FwdRaw& raw) {
+  float zero = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld32(tO + c * 32, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) zero = fmaf(__uint_as_float(o[e]), 0.f, zero);  // NaN, once any is not finite
+  }
+  bool again = live && !(zero == 0.f);
+  if (!__any_sync(0xffffffffu, again)) return;
+  const size_t kv = static_cast<size_t>(un.kvh) * rows;
+  const uint4* k = reinterpret_cast<const uint4*>(raw.k + kv * D);
+  const uint4* v = reinterpret_cast<const uint4*>(raw.v + kv * D);
+  const uint4* q = reinterpret_cast<const uint4*>(raw.q + (static_cast<size_t>(un.bh) * rows + (live ? n : qt0)) * D);
+  if (again) {
+    float sum = 0.f;
+    for (size_t i = (n + 1) * static_cast<size_t>(D / 8); i < static_cast<size_t>(min(qt0 + 128, un.end)) * (D / 8); ++i) {
+      float f[8];
+      bf16x8(v[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(f[e], 0.f, sum);
+    }
+    again = !(sum == 0.f);
+  }
+  if (!__any_sync(0xffffffffu, again)) return;
+  const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld32(tO + c * 32, o);
+    tmem_wait_ld();
+    if (again) {
+      float acc[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+      for (int j = un.kvb; j <= n; ++j) {
+        float s = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < D / 8; ++i) {
+          float a[8], b[8];
+          bf16x8(q[i], a);
+          bf16x8(k[static_cast<size_t>(j) * (D / 8) + i], b);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+        }
+        const float p = ex2_approx(fmaf(s, scale_log2, neg_m));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float b[8];
+          bf16x8(v[static_cast<size_t>(j) * (D / 8) + c * 4 + i], b);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[8 * i + e] = fmaf(p, b[e], acc[8 * i + e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
+    }
+    __syncwarp();
+    tmem_st32(tO + c * 32, o);
+    tmem_wait_st();
+  }
+}
+
 // Softmax / epilogue of one 128-row query tile (x = 0: tile A, 1: tile B).
 template <int D, class W>
 __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const W& w, float scale_log2,
                             const CUtensorMap* map_o, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-                            uint32_t* dev_err) {
+                            const FwdRaw& raw, uint32_t* dev_err) {
   using C = FwdCfg<D>;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int wq = warp & 3;
@@ -382,12 +516,14 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
   int jx = 0;       // key tiles processed by this query-tile slot (barrier phases)
   uint32_t uc = 0;  // units processed by this slot (o_done phases)
   uint32_t us = 0;  // tiles stored through the staging buffer (epi phases)
+  int gb = 0;       // ring items of the units so far (grouped)
   bool ok = true;
-  for (int u = blockIdx.x; ok && u < w.units; u += gridDim.x) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
   const FwdUnit un = w.unit(u);
+  gb += 2 * un.nkv;
   if (x == 1 && !un.has_b) continue;
   // Per-unit values, so that the tile loop keeps few of them live.
-  const int nkv = un.nkv;
+  const int nkv = tiles_of(w, un, x);
   const int qt0 = un.q0 + x * 128;  // the tile's first row
   const int n = qt0 + row;
   const int nvalid_last = un.end - (un.kvb + (nkv - 1) * kTileN);  // keys of the last key tile
@@ -415,7 +551,34 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
       tc_fence_before();
       mbar_arrive(&bars.s_free[x]);
     }
-    const int nvalid = j + 1 < nkv ? kTileN : nvalid_last;
+    if constexpr (W::kGrouped) {
+      // The last key tile: a causal row sees the keys up to its own (which, as in
+      // every row that is stored, ends before the segment does).
+      if (j + 1 == nkv && (w.causal || nvalid_last < kTileN)) {
+        const int seen = w.causal ? row + 1 : nvalid_last;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c * 32 + e >= seen) s[c][e] = __float_as_uint(-INFINITY);
+        // Values behind the segment (another sequence's, or anything) times a
+        // probability of zero are no zeros if they are not finite: their rows of
+        // the shared tile become zeros before the product reads it.  (Behind the
+        // tensor's end the TMA unit has filled in zeros.)
+        if (nvalid_last < kTileN && un.end < w.seg.rows) {
+          const int iv = gb - 2 * un.nkv + 2 * j + 1;  // the tile's ring item
+          ok = mbar_wait(&bars.full[iv % C::kSlots], (iv / C::kSlots) & 1, ab, dev_err);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          if (row >= nvalid_last) {
+            const uint32_t vrow = smem_u32(sm + C::kOffRing + (iv % C::kSlots) * C::kSlotBytes) + row * 128;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) st_shared_v4(vrow + (i >> 3) * 16384 + (i & 7) * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+      }
+    }
+    const int nvalid = W::kGrouped || j + 1 < nkv ? kTileN : nvalid_last;
     if (nvalid < kTileN) {  // only the ragged last key tile needs the mask
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -439,7 +602,8 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
     const float alpha = need ? ex2_approx(m_ref - m_new) : 1.f;
     l *= alpha;
     m_ref = m_new;
-    const float neg_m = -m_ref;
+    // (A grouped row may have scores of -inf alone so far: their probabilities are zeros.)
+    const float neg_m = W::kGrouped && m_ref == -INFINITY ? 0.f : -m_ref;
     // Probabilities and row sum; P (bf16 pairs, 16 packed columns per 32
     // scores) into TMEM.  x = s * scale_log2 - m and the row sum in packed
     // f32x2 arithmetic (two scores per instruction), 2^x on the MUFU unit;
@@ -505,6 +669,9 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
   if (!ok) return;
   tc_fence_after();
   const float inv_l = 1.f / l;
+  if constexpr (W::kGrouped) {
+    if (w.causal) restore_masked<D>(tO, un, qt0, n, live, m_ref, scale_log2, w.seg.rows, raw);
+  }
   if (tile_store) {
     // O rows into the query tile's staging tile (128-byte swizzle: 16-byte
     // chunk c of row r at c ^ (r & 7)), then one TMA store of the tile; rows
@@ -572,7 +739,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
                     const __grid_constant__ W w, float scale_log2,
                     __nv_bfloat16* __restrict__ out, float* __restrict__ lse, float* dq_zero, uint32_t* zero_count,
-                    uint32_t* dev_err) {
+                    const FwdRaw raw, uint32_t* dev_err) {
   using C = FwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ FwdBars bars;
@@ -616,13 +783,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (warp == 8) {
       if (lane == 0) fwd_producer<D>(&map_q, &map_k, &map_v, sm, bars, w, dev_err);
     } else if (warp == 11) {
-      if (dq_zero) fwd_zero_dq<D>(w, dq_zero, zero_count, lane);
+      if constexpr (!W::kGrouped) {
+        if (dq_zero) fwd_zero_dq<D>(w, dq_zero, zero_count, lane);
+      }
     } else {
       if (lane == 0) fwd_mma<D>(sm, bars, tmem, warp - 9, w, dev_err);
     }
   } else {
     setmaxnreg_inc<kRegSoftmax>();
-    fwd_softmax<D>(sm, bars, tmem, warp >> 2, w, scale_log2, &map_o, out, lse, dev_err);
+    fwd_softmax<D>(sm, bars, tmem, warp >> 2, w, scale_log2, &map_o, out, lse, raw, dev_err);
   }
   tc_fence_before();
   __syncthreads();
@@ -634,8 +803,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
 template <int D, class W>
 cudaError_t launch_fwd_w(const W& w, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                         const AttnShape& s, uint16_t* out, float* lse, float* dq_zero, uint32_t* zero_count,
-                         uint32_t* dev_err, cudaStream_t st) {
+                         int heads, int rows, float scale, uint16_t* out, float* lse, float* dq_zero,
+                         uint32_t* zero_count, uint32_t* dev_err, cudaStream_t st, const FwdRaw& raw = {}) {
   using C = FwdCfg<D>;
   static_assert(C::kDynSmem + static_cast<int>(sizeof(FwdBars)) <= 232448, "shared memory budget");
   auto kernel = attn_fwd_kernel<D, W>;
@@ -649,11 +818,11 @@ cudaError_t launch_fwd_w(const W& w, const CUtensorMap& mq, const CUtensorMap& m
   if (fa.numRegs != kRegLaunchFwd) return cudaErrorInvalidConfiguration;
   const int sms = device_sm_count();
   const int grid = w.units < sms ? w.units : sms;
-  const float scale_log2 = s.scale * 1.4426950408889634f;
+  const float scale_log2 = scale * 1.4426950408889634f;
   CUtensorMap mo;  // the output, for the staged tile stores (d = 64)
-  if (!encode_bhnd_map(&mo, out, s.BH, s.N, D)) return cudaErrorInvalidValue;
+  if (!encode_bhnd_map(&mo, out, heads, rows, D)) return cudaErrorInvalidValue;
   return launch_pdl(kernel, dim3(grid), dim3(kFwdThreads), C::kDynSmem, st, mq, mk, mv, mo, w, scale_log2,
-                    reinterpret_cast<__nv_bfloat16*>(out), lse, dq_zero, zero_count, dev_err);
+                    reinterpret_cast<__nv_bfloat16*>(out), lse, dq_zero, zero_count, raw, dev_err);
 }
 
 // Work units (256 query rows of one head's segment) of a launch.
@@ -673,7 +842,7 @@ cudaError_t launch_fwd_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
     w.upc = (s.seg.rows + 2 * kTileM - 1) / (2 * kTileM);
     w.nkv = (s.seg.rows + kTileN - 1) / kTileN;
     w.units = s.BH * w.upc;
-    return launch_fwd_w<D>(w, mq, mk, mv, s, out, lse, dq_zero, zero_count, dev_err, st);
+    return launch_fwd_w<D>(w, mq, mk, mv, s.BH, s.N, s.scale, out, lse, dq_zero, zero_count, dev_err, st);
   }
   FwdWork w;
   w.seg = s.seg;
@@ -682,7 +851,7 @@ cudaError_t launch_fwd_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
     w.uf[i + 1] = w.uf[i] + (s.seg.cu[i + 1] - s.seg.cu[i] + 2 * kTileM - 1) / (2 * kTileM);
   w.upc = w.uf[s.seg.n];
   w.units = s.BH * w.upc;
-  return launch_fwd_w<D>(w, mq, mk, mv, s, out, lse, dq_zero, zero_count, dev_err, st);
+  return launch_fwd_w<D>(w, mq, mk, mv, s.BH, s.N, s.scale, out, lse, dq_zero, zero_count, dev_err, st);
 }
 
 }  // namespace
@@ -693,6 +862,24 @@ cudaError_t launch_attn_fwd(const CUtensorMap& map_q, const CUtensorMap& map_k, 
   if (s.d == 64) return launch_fwd_d<64>(map_q, map_k, map_v, s, out, lse, dq_zero, zero_count, dev_err, st);
   if (s.d == 128) return launch_fwd_d<128>(map_q, map_k, map_v, s, out, lse, dq_zero, zero_count, dev_err, st);
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_attn_fwd_grouped(const GroupedShape& s, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                    uint16_t* out, float* lse, uint32_t* dev_err, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  if (!encode_bhnd_map(&mq, q, s.Hq, s.T, s.d) || !encode_bhnd_map(&mk, k, s.Hk, s.T, s.d) ||
+      !encode_bhnd_map(&mv, v, s.Hk, s.T, s.d))
+    return cudaErrorInvalidValue;
+  FwdWorkGrouped w;
+  w.heads = s.Hq;
+  w.group = s.Hq / s.Hk;
+  w.causal = s.causal;
+  w.seg.rows = s.T;
+  w.units = s.Hq * w.order.make(s, 2 * kTileM);
+  auto bf = [](const uint16_t* p) { return reinterpret_cast<const __nv_bfloat16*>(p); };
+  const FwdRaw raw{bf(q), bf(k), bf(v)};
+  auto launch = s.d == 64 ? launch_fwd_w<64, FwdWorkGrouped> : launch_fwd_w<128, FwdWorkGrouped>;
+  return launch(w, mq, mk, mv, s.Hq, s.T, s.scale, out, lse, nullptr, nullptr, dev_err, st, raw);
 }
 
 int attn_fwd_grid(const AttnShape& s) {

@@ -1299,6 +1299,135 @@ extern "C" int jattn_rope_bwd(const jattn_bf16* dq_rot, const jattn_bf16* dk_rot
   return JATTN_OK;
 }
 
+namespace {
+
+// Sizes of a grouped call; the segments are the sequences that have rows.
+int check_grouped(const int* cu, int n, int Hq, int Hk, int T, int d, GroupedShape* s) {
+  if (!cu || n < 1 || Hq <= 0 || Hk <= 0 || T <= 0 || d <= 0) return JATTN_ERR_INVALID_ARG;
+  if (n > kMaxSegments || (d != 64 && d != 128)) return JATTN_ERR_UNSUPPORTED;
+  if (Hq % Hk != 0 || Hq > 65535 || cu[0] != 0) return JATTN_ERR_INVALID_ARG;
+  int rows[kMaxSegments + 1], full = 0;
+  rows[0] = 0;
+  for (int i = 0; i < n; ++i) {
+    if (cu[i + 1] < cu[i] || cu[i + 1] > T) return JATTN_ERR_INVALID_ARG;
+    if (cu[i + 1] > cu[i]) rows[++full] = cu[i + 1];
+  }
+  if (full == 0 || !make_seg_table(&s->seg, rows, full)) return JATTN_ERR_INVALID_ARG;
+  const int64_t limit = int64_t{1} << 31;
+  if (static_cast<int64_t>(Hq) * T * d >= limit || static_cast<int64_t>(Hq) * s->seg.prows >= limit)
+    return JATTN_ERR_INVALID_ARG;
+  s->seg.rows = T;
+  s->Hq = Hq;
+  s->Hk = Hk;
+  s->T = T;
+  s->d = d;
+  return JATTN_OK;
+}
+
+bool scale_ok(float scale) { return scale >= 0x1p-20f && scale <= 0x1p20f; }
+
+// A grouped call's tensors in bytes, and its work buffer: the statistics chunks, the
+// fp32 dq accumulator, the dQ order counters (used in the deterministic mode alone).
+struct GroupedBytes {
+  size_t q, k, lse, stats, dq, counters, work;
+  explicit GroupedBytes(const GroupedShape& s) {
+    auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+    const size_t rows = static_cast<size_t>(s.Hq) * s.T, padded = static_cast<size_t>(s.Hq) * s.seg.prows;
+    q = rows * s.d * 2;
+    k = static_cast<size_t>(s.Hk) * s.T * s.d * 2;
+    lse = rows * 4;
+    stats = up(padded * 32);
+    dq = up(rows * s.d * 4);
+    counters = up(padded / 128 * 4);
+    work = stats + dq + counters;
+  }
+};
+
+}  // namespace
+
+extern "C" int jattn_fwd_grouped(const jattn_bf16* q, const jattn_bf16* k, const jattn_bf16* v, const int* cu_seqlens,
+                                 int n_seqs, int Hq, int Hk, int T, int d, int causal, float scale, jattn_bf16* out,
+                                 float* lse, void* stream) {
+  if (!q || !k || !v || !out || !lse || !scale_ok(scale)) return JATTN_ERR_INVALID_ARG;
+  GroupedShape s;
+  const int rc = check_grouped(cu_seqlens, n_seqs, Hq, Hk, T, d, &s);
+  if (rc != JATTN_OK) return rc;
+  const void* ptrs[] = {q, k, v, out, lse};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return JATTN_ERR_MISALIGNED;
+  const GroupedBytes n(s);
+  const Range ins[] = {range_of(q, n.q), range_of(k, n.k), range_of(v, n.k)};
+  const Range outs[] = {range_of(out, n.q), range_of(lse, n.lse)};
+  if (any_alias(ins, outs, Range{0, 0}, Range{0, 0})) return JATTN_ERR_ALIAS;
+  s.causal = causal != 0;
+  s.scale = scale;
+  s.deterministic = false;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint32_t* err = dev_err_ptr();
+  if (!err) return fail(JATTN_ERR_CUDA, "device error word", cudaGetLastError());
+  cudaError_t ce;
+  {
+    Timed t(JATTN_KERNEL_ATTN_FWD, st);
+    ce = launch_attn_fwd_grouped(s, q, k, v, out, lse, err, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "attn_fwd launch", ce);
+  return JATTN_OK;
+}
+
+extern "C" size_t jattn_bwd_grouped_bytes(const int* cu_seqlens, int n_seqs, int Hq, int Hk, int T, int d) {
+  GroupedShape s;
+  return check_grouped(cu_seqlens, n_seqs, Hq, Hk, T, d, &s) == JATTN_OK ? GroupedBytes(s).work : 0;
+}
+
+extern "C" int jattn_bwd_grouped(const jattn_bf16* q, const jattn_bf16* k, const jattn_bf16* v, const jattn_bf16* out,
+                                 const float* lse, const jattn_bf16* dout, const int* cu_seqlens, int n_seqs, int Hq,
+                                 int Hk, int T, int d, int causal, float scale, jattn_bf16* dq, jattn_bf16* dk,
+                                 jattn_bf16* dv, void* work, void* stream) {
+  if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv || !work || !scale_ok(scale))
+    return JATTN_ERR_INVALID_ARG;
+  GroupedShape s;
+  const int rc = check_grouped(cu_seqlens, n_seqs, Hq, Hk, T, d, &s);
+  if (rc != JATTN_OK) return rc;
+  const void* ptrs[] = {q, k, v, out, lse, dout, dq, dk, dv, work};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return JATTN_ERR_MISALIGNED;
+  const GroupedBytes n(s);
+  const Range ins[] = {range_of(q, n.q),     range_of(k, n.k),     range_of(v, n.k),
+                       range_of(out, n.q),   range_of(lse, n.lse), range_of(dout, n.q)};
+  const Range outs[] = {range_of(dq, n.q), range_of(dk, n.k), range_of(dv, n.k), range_of(work, n.work)};
+  if (any_alias(ins, outs, Range{0, 0}, Range{0, 0})) return JATTN_ERR_ALIAS;
+  s.causal = causal != 0;
+  s.scale = scale;
+  s.deterministic = g_deterministic.load(std::memory_order_relaxed) != 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint32_t* err = dev_err_ptr();
+  if (!err) return fail(JATTN_ERR_CUDA, "device error word", cudaGetLastError());
+  uint8_t* base = static_cast<uint8_t*>(work);
+  uint16_t* stats = reinterpret_cast<uint16_t*>(base);
+  float* dqacc = reinterpret_cast<float*>(base + n.stats);
+  uint32_t* counters = reinterpret_cast<uint32_t*>(base + n.stats + n.dq);
+  cudaError_t ce;
+  {
+    Timed t(JATTN_KERNEL_BWD_PREP, st);
+    // The statistics and the zeroing alone: no norm, and its operands are not looked at.
+    ce = launch_bwd_prep(nullptr, nullptr, dqacc, dqacc, out, dout, lse, nullptr, nullptr, nullptr, nullptr, stats,
+                         1.f / scale, dqacc, counters, s.deterministic ? s.Hq * (s.seg.prows / 128) : 0, s.Hq, s.seg,
+                         d, err, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "bwd_prep launch", ce);
+  {
+    Timed t(JATTN_KERNEL_ATTN_BWD, st);
+    ce = launch_attn_bwd_grouped(s, q, k, v, dout, stats, dqacc, counters, dk, dv, err, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "attn_bwd launch", ce);
+  {
+    Timed t(JATTN_KERNEL_GROUPED_DQ, st);
+    ce = launch_grouped_dq(s, dqacc, dq, st);
+  }
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "grouped_dq launch", ce);
+  return JATTN_OK;
+}
+
 namespace jattn {
 
 // One thread waits on an mbarrier that nothing arrives at, through the same
@@ -1417,6 +1546,7 @@ extern "C" const char* jattn_kernel_name(int kind) {
     case JATTN_KERNEL_ROPE: return "rope";
     case JATTN_KERNEL_ROPE_NORM_BWD: return "rope_norm_bwd";
     case JATTN_KERNEL_ROPE_GAINS: return "rope_gains";
+    case JATTN_KERNEL_GROUPED_DQ: return "grouped_dq";
     default: return "unknown";
   }
 }

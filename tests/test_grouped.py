@@ -1,0 +1,465 @@
+"""Attention of packed sequences with grouped heads, causal and full, forward and backward, against its
+definition in float64.
+
+Tolerances, element by element, from the arithmetic (h = 2^-8, half a bf16 step; sums of products in fp32
+on the tensor cores, at most 2^-17 of their terms' magnitudes):
+* A score is off by 2^-17 A, A the largest scale sum |q_c k_c|, a probability relative to its row by e = h
+  (its rounding to bf16) + 2^-16 A + 2^-20, and the row's sum by (2^-16 A + N 2^-28 + 2^-20).
+* out: h |out| + e sum P |v|; lse: 2^-16 A + N 2^-28 + 2^-18 (1 + |lse|).
+* Backward: D = sum dout out with out's error; dS = P (dP - D) has the probability's error (with lse's),
+  two more roundings of h, and dP's and D's errors: dq, dk and dv h of themselves and the sums of their
+  terms' errors.
+"""
+import ctypes
+
+import pytest
+import torch
+
+from joint_attention_gb300 import STATUS_CODE
+import joint_attention_gb300 as pkg
+from joint_attention_gb300.build import build
+
+gpu = pytest.mark.gpu
+HALF = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build()
+    return pkg.load_library()
+
+
+@pytest.fixture(scope="module")
+def ja(lib):
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    return pkg
+
+
+def randn(shape, seed, scale=1.0, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def offsets(lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+def inputs(lens, Hq, Hk, d, seed, behind=0):
+    cu = offsets(lens)
+    T = cu[-1] + behind
+    return (randn((Hq, T, d), seed, 1.5), randn((Hk, T, d), seed + 1), randn((Hk, T, d), seed + 2),
+            randn((Hq, T, d), seed + 3), cu)
+
+
+def probabilities(q, k, causal, scale):
+    """P and lse of one head and sequence in float64, and the largest scale sum |q_c k_c|."""
+    s = (q @ k.T) * scale
+    seen = torch.ones_like(s, dtype=torch.bool)
+    if causal:
+        seen = seen.tril()
+    s = s.masked_fill(~seen, float("-inf"))
+    lse = torch.logsumexp(s, 1)
+    return torch.exp(s - lse[:, None]), lse, float((q.abs() @ k.abs().T).max()) * scale
+
+
+def check_forward(out, lse, q, k, v, cu, causal, scale=None):
+    group, d = q.shape[0] // k.shape[0], q.shape[-1]
+    scale = d ** -0.5 if scale is None else scale
+    for a, b in zip(cu, cu[1:]):
+        for h in range(q.shape[0]):
+            qh, kh, vh = (t[i, a:b].double() for t, i in ((q, h), (k, h // group), (v, h // group)))
+            if a == b:
+                continue
+            p, l0, A = probabilities(qh, kh, causal, scale)
+            o0, mag, n = p @ vh, p @ vh.abs(), b - a
+            tol = HALF * o0.abs() + (HALF + 2.0 ** -15 * A + n * 2.0 ** -28 + 2.0 ** -19) * mag
+            assert ((out[h, a:b].double() - o0).abs() <= tol + 1e-30).all(), (a, b, h)
+            tol = 2.0 ** -16 * A + n * 2.0 ** -28 + 2.0 ** -18 * (1 + l0.abs())
+            assert ((lse[h, a:b].double() - l0).abs() <= tol).all(), (a, b, h)
+
+
+def check_backward(dq, dk, dv, q, k, v, out, dout, cu, causal, scale=None):
+    group, d = q.shape[0] // k.shape[0], q.shape[-1]
+    scale = d ** -0.5 if scale is None else scale
+    for a, b in zip(cu, cu[1:]):
+        if a == b:
+            continue
+        for hk in range(k.shape[0]):
+            kh, vh = k[hk, a:b].double(), v[hk, a:b].double()
+            dk0 = dv0 = dk_tol = dv_tol = 0.0
+            for h in range(hk * group, (hk + 1) * group):
+                qh, g = q[h, a:b].double(), dout[h, a:b].double()
+                p, l0, A = probabilities(qh, kh, causal, scale)
+                n = b - a
+                o0, o_mag = p @ vh, p @ vh.abs()
+                e = 2.0 ** -14 * A + n * 2.0 ** -27 + 2.0 ** -17 * (1 + l0.abs()[:, None])  # a probability's, with lse's
+                o_tol = HALF * o0.abs() + (HALF + e) * o_mag
+                D, D_tol = (g * o0).sum(1, keepdim=True), (g.abs() * (o_tol + 2.0 ** -20 * o0.abs())).sum(1, keepdim=True)
+                dp, dp_tol = g @ vh.T, 2.0 ** -17 * (g.abs() @ vh.abs().T)
+                ds = p * (dp - D)
+                ds_tol = (3.1 * HALF + e) * ds.abs() + p * (dp_tol + D_tol) * 1.02
+                dq0 = scale * (ds @ kh)
+                tol = HALF * dq0.abs() + scale * ((ds_tol + 2.0 ** -16 * ds.abs()) @ kh.abs())
+                assert ((dq[h, a:b].double() - dq0).abs() <= tol + 1e-30).all(), (a, b, h)
+                dk0 = dk0 + scale * (ds.T @ qh)
+                dk_tol = dk_tol + scale * ((ds_tol + 2.0 ** -16 * ds.abs()).T @ qh.abs())
+                dv0 = dv0 + p.T @ g
+                dv_tol = dv_tol + ((HALF + e + 2.0 ** -16) * p).T @ g.abs()
+            assert ((dk[hk, a:b].double() - dk0).abs() <= HALF * dk0.abs() + dk_tol + 1e-30).all(), (a, b, hk)
+            assert ((dv[hk, a:b].double() - dv0).abs() <= HALF * dv0.abs() + dv_tol + 1e-30).all(), (a, b, hk)
+
+
+LENS = [(1,), (2, 1), (24,), (128,), (129,), (77,) * 5, (1, 127, 128, 129, 300), (513, 2, 640), (1101,),
+        (256, 0, 257, 0), (40, 1000, 3)]
+HEADS = [(1, 1), (4, 2), (6, 1)]
+
+
+@gpu
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("Hq,Hk", HEADS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_forward_grouped(ja, lens, Hq, Hk, d, causal):
+    q, k, v, _, cu = inputs(lens, Hq, Hk, d, 1)
+    out, lse = ja.forward_grouped(q, k, v, cu, causal)
+    assert ja.jattn_last_device_error() == 0
+    check_forward(out, lse, q, k, v, cu, causal)
+
+
+@gpu
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("Hq,Hk", HEADS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_backward_grouped(ja, lens, Hq, Hk, d, causal):
+    q, k, v, dout, cu = inputs(lens, Hq, Hk, d, 11)
+    out, lse = ja.forward_grouped(q, k, v, cu, causal)
+    grads = ja.backward_grouped(q, k, v, out, lse, dout, cu, causal)
+    assert ja.jattn_last_device_error() == 0
+    check_backward(*grads, q, k, v, out, dout, cu, causal)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_behind_the_last_sequence_are_left_and_not_read(ja, d, causal):
+    lens, behind = (130, 1, 77), 55
+    q, k, v, dout, cu = inputs(lens, 4, 2, d, 21, behind)
+    T = cu[-1]
+    clean = [t[:, :T].contiguous() for t in (q, k, v, dout)]
+    out0, lse0 = ja.forward_grouped(*clean[:3], cu, causal)
+    grads0 = ja.backward_grouped(*clean[:3], out0, lse0, clean[3], cu, causal)
+    for t in (q, k, v, dout):
+        t[:, T:] = float("nan")
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    ja.jattn_fwd_grouped(q, k, v, cu, 4, 2, T + behind, d, causal, d ** -0.5, out, lse)
+    assert torch.equal(out[:, :T], out0) and torch.equal(lse[:, :T], lse0)
+    assert (out[:, T:] == 7.0).all() and (lse[:, T:] == 7.0).all()
+    out[:, T:] = lse[:, T:] = float("nan")
+    dq, dk, dv = (torch.full_like(t, 7.0) for t in (q, k, v))
+    work = torch.full((ja.jattn_bwd_grouped_bytes(cu, 4, 2, T + behind, d),), 0xFF, dtype=torch.uint8, device="cuda")
+    ja.jattn_bwd_grouped(q, k, v, out, lse, dout, cu, 4, 2, T + behind, d, causal, d ** -0.5, dq, dk, dv, work)
+    assert ja.jattn_last_device_error() == 0
+    for got, want in zip((dq, dk, dv), grads0):
+        assert (got[:, T:] == 7.0).all()
+        if got is not dq or want is None:
+            assert torch.equal(got[:, :T], want)
+        else:  # sums of contributions in the order of arrival
+            assert torch.allclose(got[:, :T].float(), want.float(), rtol=2.0 ** -6, atol=1e-5)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_other_sequences_values_that_are_not_finite_do_not_reach_a_result(ja, d, causal, bad):
+    lens = (60, 200, 131, 5)
+    q, k, v, dout, cu = inputs(lens, 4, 2, d, 31)
+    ja.jattn_set_deterministic(True)
+    try:
+        out0, lse0 = ja.forward_grouped(q, k, v, cu, causal)
+        grads0 = ja.backward_grouped(q, k, v, out0, lse0, dout, cu, causal)
+        for t in (q, k, v, dout):  # the second sequence and the fourth
+            t[:, 60:260] = bad
+            t[:, 391:] = bad
+        out, lse = ja.forward_grouped(q, k, v, cu, causal)
+        grads = ja.backward_grouped(q, k, v, out, lse, dout, cu, causal)
+    finally:
+        ja.jattn_set_deterministic(False)
+    assert ja.jattn_last_device_error() == 0
+    for rows in (slice(0, 60), slice(260, 391)):
+        for got, want in zip((out, lse, *grads), (out0, lse0, *grads0)):
+            assert torch.equal(got[:, rows], want[:, rows])
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+def test_later_rows_that_are_not_finite_do_not_reach_earlier_ones(ja, d, bad):
+    """Causal: keys and values from row 201 on (and a value alone at row 70 of another sequence)."""
+    lens = (300, 90)
+    q, k, v, _, cu = inputs(lens, 4, 2, d, 41)
+    out0, lse0 = ja.forward_grouped(q, k, v, cu)
+    k[:, 201:300], v[:, 201:300], v[:, 370, 3] = bad, bad, bad
+    out, lse = ja.forward_grouped(q, k, v, cu)
+    check_forward(out[:, :201], lse[:, :201], q[:, :201], k[:, :201], v[:, :201], [0, 201], True)
+    tail = slice(300, 370)
+    check_forward(out[:, tail], lse[:, tail], q[:, tail], k[:, tail], v[:, tail], [0, 70], True)
+    assert torch.equal(lse[:, :201], lse0[:, :201]) and torch.equal(out[:, :128], out0[:, :128])
+    assert not out[:, 201:300].isfinite().any()
+    assert torch.equal(lse[:, 300:], lse0[:, 300:])
+    assert not out[:, 370:, 3].isfinite().any()
+    others = [c for c in range(d) if c != 3]
+    assert torch.allclose(out[:, 370:][..., others].float(), out0[:, 370:][..., others].float(), rtol=2.0 ** -6, atol=2.0 ** -8)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_and_large_scores(ja, d):
+    q, k, v, dout, cu = inputs((200, 33), 2, 1, d, 51)
+    for scale in (1.0, 0.01):
+        out, lse = ja.forward_grouped(q, k, v, cu, True, scale)
+        check_forward(out, lse, q, k, v, cu, True, scale)
+        check_backward(*ja.backward_grouped(q, k, v, out, lse, dout, cu, True, scale), q, k, v, out, dout, cu, True,
+                       scale)
+    k[0, 5] = float("-inf")  # scores of -inf or +inf: rows with -inf alone go without the key
+    q[:, :, :] = q.abs() + 2.0 ** -6
+    out, lse = ja.forward_grouped(q, k, v, cu)
+    keep = [i for i in range(200) if i != 5]
+    k2, v2 = k[:, keep], v[:, keep]
+    p, l0, _ = probabilities(q[0, 199:200].double(), k2[0].double(), False, d ** -0.5)
+    assert abs(lse[0, 199].item() - l0.item()) <= 1e-3
+    assert torch.allclose(out[0, 199].double(), (p @ v2[0].double())[0], rtol=2.0 ** -6, atol=2.0 ** -8)
+    assert out.isfinite().all()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("sms", [0, 3])
+def test_gradients_repeat_in_the_deterministic_mode(ja, d, causal, sms):
+    q, k, v, dout, cu = inputs((700, 129, 5, 260), 6, 2, d, 61)
+    ja.jattn_set_sm_limit(sms)
+    ja.jattn_set_deterministic(True)
+    try:
+        out, lse = ja.forward_grouped(q, k, v, cu, causal)
+        first = ja.backward_grouped(q, k, v, out, lse, dout, cu, causal)
+        for _ in range(3):
+            again = ja.backward_grouped(q, k, v, out, lse, dout, cu, causal)
+            assert all(torch.equal(a, b) for a, b in zip(first, again))
+        assert ja.jattn_last_device_error() == 0
+        check_backward(*first, q, k, v, out, dout, cu, causal)
+        ja.jattn_set_deterministic(False)
+        arrival = ja.backward_grouped(q, k, v, out, lse, dout, cu, causal)
+        again = ja.backward_grouped(q, k, v, out, lse, dout, cu, causal)  # (the modes may visit query tiles in other orders)
+        assert torch.equal(arrival[1], again[1]) and torch.equal(arrival[2], again[2])
+        check_backward(*arrival, q, k, v, out, dout, cu, causal)
+    finally:
+        ja.jattn_set_deterministic(False)
+        ja.jattn_set_sm_limit(0)
+
+
+@gpu
+def test_256_sequences(ja):
+    lens = [(7 * i) % 41 for i in range(256)]
+    for d in (64, 128):
+        q, k, v, dout, cu = inputs(lens, 2, 1, d, 71)
+        out, lse = ja.forward_grouped(q, k, v, cu)
+        grads = ja.backward_grouped(q, k, v, out, lse, dout, cu)
+        check_forward(out, lse, q, k, v, cu, True)
+        check_backward(*grads, q, k, v, out, dout, cu, True)
+    with pytest.raises(ja.JattnError):
+        ja.forward_grouped(q, k, v, [*cu, cu[-1]])
+
+
+@gpu
+def test_a_long_sequence(ja):
+    """70001 rows: the first, the last and some between against float64, and the values' gradients' sum."""
+    T, d = 70001, 64
+    q, k, v, dout, cu = inputs((T,), 2, 1, d, 81)
+    out, lse = ja.forward_grouped(q, k, v, cu)
+    for i in (0, 1, 127, 128, 4095, 33333, 65536, 69999, T - 1):
+        for h in range(2):
+            p, l0, A = probabilities(q[h, i:i + 1].double(), k[0, :i + 1].double(), False, d ** -0.5)
+            o0, mag = p @ v[0, :i + 1].double(), p @ v[0, :i + 1].double().abs()
+            tol = HALF * o0.abs() + (HALF + 2.0 ** -15 * A + i * 2.0 ** -28 + 2.0 ** -19) * mag
+            assert ((out[h, i].double() - o0).abs() <= tol).all()
+            assert abs(lse[h, i].item() - l0.item()) <= 2.0 ** -16 * A + i * 2.0 ** -28 + 2.0 ** -18 * (1 + l0.abs().item())
+    dq, dk, dv = ja.backward_grouped(q, k, v, out, lse, dout, cu)
+    assert ja.jattn_last_device_error() == 0
+    # every row of P sums to one: the values' gradients sum to dout's sum, but for 70001 roundings of dv
+    want = dout.double().sum((0, 1))
+    assert ((dv.double().sum((0, 1)) - want).abs() <= HALF * dv.double().abs().sum((0, 1))
+            + 2 * HALF * dout.double().abs().sum((0, 1)) * 2.0 ** -4).all()
+    assert dq.isfinite().all() and dk.isfinite().all()
+
+
+@gpu
+@pytest.mark.parametrize("causal", [True, False])
+def test_backward_is_the_gradient_by_differences(ja, causal):
+    q, k, v, dout, cu = inputs((37, 9), 4, 2, 64, 91)
+    out, lse = ja.forward_grouped(q, k, v, cu, causal)
+    grads = ja.backward_grouped(q, k, v, out, lse, dout, cu, causal)
+
+    def loss(q, k, v):
+        total = 0.0
+        for a, b in zip(cu, cu[1:]):
+            for h in range(4):
+                total = total + (dout[h, a:b].double() * (probabilities(q[h, a:b], k[h // 2, a:b], causal, 0.125)[0]
+                                                          @ v[h // 2, a:b])).sum()
+        return total
+
+    at = [t.double() for t in (q, k, v)]
+    for i, g in enumerate(grads):
+        for s in range(3):
+            w, e = randn(g.shape, 100 + s, dtype=torch.float64), 1e-5
+            up, down = list(at), list(at)
+            up[i], down[i] = at[i] + e * w, at[i] - e * w
+            by = (loss(*up) - loss(*down)) / (2 * e)
+            # each gradient is off by some 2^-7 of its terms, with signs of their own: four times their norm
+            assert abs((g.double() * w).sum() - by) <= 4 * 2.0 ** -7 * (g.double() * w).norm() + 1e-2
+
+
+@gpu
+def test_on_another_stream_and_captured(ja):
+    q, k, v, dout, cu = inputs((300, 41), 4, 2, 64, 111)
+    ja.jattn_set_deterministic(True)
+    try:
+        def both(**kw):
+            out, lse = ja.forward_grouped(q, k, v, cu, **kw)
+            return (out, lse, *ja.backward_grouped(q, k, v, out, lse, dout, cu, **kw))
+
+        want = both()
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        for stream in (side, side.cuda_stream):
+            got = both(stream=stream)
+            side.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = both()
+        q.copy_(randn(q.shape, 112))
+        dout.copy_(randn(q.shape, 113))
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, both()))
+    finally:
+        ja.jattn_set_deterministic(False)
+
+
+@gpu
+def test_a_block_of_the_operators(ja):
+    """As they are used together: norm with each item's scale and shift, projections, QK-RMSNorm with positions,
+    attention, and back; with all positions zero the joint attention with the same gains."""
+    B, N, H, d, C, pairs = 2, 205, 4, 64, 256, (16, 16)
+    x, res = randn((B, N, C), 121), randn((B, N, C), 122, 2.0)
+    scale, shift = randn((B, C), 123, 0.1, torch.float32) + 1, randn((B, C), 124, 0.1, torch.float32)
+    y, h, mean, r = ja.layer_norm(x, scale, shift, res)
+    w, none = randn((3 * H * d, C), 125, C ** -0.5), torch.empty((B, 0, C), dtype=torch.bfloat16, device="cuda")
+    gq, gk = (randn((d,), s, 0.1, torch.float32) + 1 for s in (126, 127))
+    q, k, v, saved = ja.qkv_norm(y, w, None, none, None, None, gq, gk, H)
+    pos = torch.zeros((N, 2), device="cuda")
+    freq = torch.ones(32, device="cuda")
+    packed = lambda t: t.transpose(0, 1).reshape(H, B * N, d).contiguous()  # noqa: E731
+    out0, lse0 = ja.forward(q, k, v, gq, gk, 0)
+    dout = randn(out0.shape, 128)
+    want = ja.backward(q, k, v, gq, gk, out0, lse0, dout, 0)
+    q_rot, k_rot = ja.rope(q, k, pos, freq, pairs, gq, gk)
+    cu = offsets([N] * B)
+    out, lse = ja.forward_grouped(packed(q_rot), packed(k_rot), packed(v), cu, causal=False)
+    grads = ja.backward_grouped(packed(q_rot), packed(k_rot), packed(v), out, lse, packed(dout), cu, causal=False)
+    back = lambda t: t.view(H, B, N, d).transpose(0, 1).contiguous()  # noqa: E731
+    dq, dk, dgq, dgk = ja.rope_backward(back(grads[0]), back(grads[1]), pos, freq, pairs, q, k, gq, gk)
+    rel = lambda a, b: ((a.double() - b.double()).norm() / b.double().norm()).item()  # noqa: E731
+    assert rel(back(out), out0) <= 2.0 ** -9 and (lse.view(H, B, N).transpose(0, 1) - lse0).abs().max() <= 2.0 ** -6
+    # one more rounding of the gradients to bf16, between attention and norm
+    for a, b in zip((dq, dk, back(grads[2]), dgq, dgk), want):
+        assert rel(a, b) <= 2.0 ** -7
+    dx, dg, db = ja.layer_norm_backward(y, h, mean, r, scale)
+    assert dx.isfinite().all() and dg.shape == scale.shape and db.shape == shift.shape
+
+
+@gpu
+def test_profile_counts_the_kernels(ja):
+    q, k, v, dout, cu = inputs((60,), 2, 1, 64, 131)
+    out, lse = ja.forward_grouped(q, k, v, cu)
+    ja.jattn_profile_reset()
+    ja.jattn_profile_enable(True)
+    ja.forward_grouped(q, k, v, cu)
+    ja.backward_grouped(q, k, v, out, lse, dout, cu)
+    torch.cuda.synchronize()
+    ja.jattn_profile_enable(False)
+    snap = ja.profile_snapshot()
+    assert [snap[n][0] for n in ("attn_fwd", "bwd_prep", "attn_bwd", "grouped_dq")] == [1, 1, 1, 1]
+    ja.jattn_profile_reset()
+
+
+@gpu
+def test_wrappers_refuse(ja):
+    q, k, v, dout, cu = inputs((20, 30), 4, 2, 64, 141)
+    for args in ((q[:, ::2], k[:, ::2], v, cu), (q.float(), k, v, cu), (q, k[:, :40], v, cu), (q, k, v[:1], cu),
+                 (q[0], k, v, cu), (q.cpu(), k, v, cu)):
+        with pytest.raises(ValueError):
+            ja.forward_grouped(*args)
+    for args, kw in (((q[:3].contiguous(), k, v, cu), {}), ((q, k, v, [0, 51]), {}), ((q, k, v, [0, 30, 20]), {}),
+                     ((q, k, v, [1, 50]), {}), ((q, k, v, [0]), {}), ((q, k, v, [0, 0]), {}),
+                     ((q, k, v, cu), dict(scale=0.0)), ((q, k, v, cu), dict(scale=float("nan")))):
+        with pytest.raises(ja.JattnError):
+            ja.forward_grouped(*args, **kw)
+    out, lse = ja.forward_grouped(q, k, v, cu)
+    with pytest.raises(ValueError):
+        ja.backward_grouped(q, k, v, out, lse.double(), dout, cu)
+    with pytest.raises(ValueError):
+        ja.jattn_bwd_grouped(q, k, v, out, lse, dout, cu, 4, 2, 50, 64, True, 0.125, torch.empty_like(q),
+                             torch.empty_like(k), torch.empty_like(v), torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+# Fake, never-dereferenced device addresses: validation happens first.
+A = 0x7F0000000000
+
+
+def at(i):
+    return A + (i << 34)
+
+
+def ints(*v):
+    return (ctypes.c_int * len(v))(*v)
+
+
+def test_grouped_validation(lib):
+    code = STATUS_CODE
+    base = dict(q=at(0), k=at(1), v=at(2), cu=ints(0, 5, 5, 24), n=3, Hq=4, Hk=2, T=30, d=64, causal=1, scale=0.125,
+                out=at(3), lse=at(4))
+    f = lambda **kw: lib.jattn_fwd_grouped(*{**base, **kw}.values(), None)  # noqa: E731
+    invalid = [dict(q=None), dict(k=None), dict(v=None), dict(cu=None), dict(n=0), dict(n=-1), dict(Hq=0), dict(Hk=0),
+               dict(Hq=3), dict(Hk=3), dict(Hq=-4), dict(T=0), dict(T=23), dict(d=0), dict(cu=ints(1, 5, 6, 24)),
+               dict(cu=ints(0, 5, 4, 24)), dict(cu=ints(0, 0, 0, 0)), dict(cu=ints(0, -1, 5, 24)), dict(Hq=70000, Hk=1),
+               dict(T=1 << 23), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf"))]
+    for kw in (*invalid, dict(out=None), dict(lse=None)):
+        assert f(**kw) == code["JATTN_ERR_INVALID_ARG"], kw
+    many = ints(*range(258))
+    for kw in (dict(d=96), dict(cu=many, n=257, T=300)):
+        assert f(**kw) == code["JATTN_ERR_UNSUPPORTED"], kw
+    for kw in (dict(q=A + 8), dict(lse=at(4) + 4)):
+        assert f(**kw) == code["JATTN_ERR_MISALIGNED"], kw
+    for kw in (dict(out=at(0)), dict(out=at(1)), dict(out=at(2) + 256), dict(lse=at(3)), dict(lse=at(1) + 128)):
+        assert f(**kw) == code["JATTN_ERR_ALIAS"], kw
+    baseb = dict(q=at(0), k=at(1), v=at(2), out=at(3), lse=at(4), dout=at(5), cu=ints(0, 5, 5, 24), n=3, Hq=4, Hk=2,
+                 T=30, d=64, causal=1, scale=0.125, dq=at(6), dk=at(7), dv=at(8), work=at(9))
+    f = lambda **kw: lib.jattn_bwd_grouped(*{**baseb, **kw}.values(), None)  # noqa: E731
+    for kw in (*invalid, *(dict([(key, None)]) for key in ("out", "lse", "dout", "dq", "dk", "dv", "work"))):
+        assert f(**kw) == code["JATTN_ERR_INVALID_ARG"], kw
+    assert f(d=32) == code["JATTN_ERR_UNSUPPORTED"]
+    assert f(work=at(9) + 8) == f(dout=at(5) + 2) == code["JATTN_ERR_MISALIGNED"]
+    for kw in (dict(dq=at(0)), dict(dq=at(5)), dict(dk=at(1)), dict(dv=at(7)), dict(work=at(6)), dict(work=at(3)),
+               dict(dv=at(2)), dict(dk=at(4))):
+        assert f(**kw) == code["JATTN_ERR_ALIAS"], kw
+    size = lambda cu, *a: lib.jattn_bwd_grouped_bytes(cu, len(cu) - 1, *a)  # noqa: E731
+    assert size(ints(0, 24), 4, 2, 30, 64) >= 4 * (128 * 32 + 30 * 64 * 4)
+    assert size(ints(0, 24), 4, 3, 30, 64) == size(ints(0, 31), 4, 2, 30, 64) == size(ints(0, 24), 4, 2, 30, 80) == 0
