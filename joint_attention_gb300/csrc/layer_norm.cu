@@ -11,13 +11,15 @@
 //     dx = bf16(dh + r (u - mean_c(u) - n mean_c(u n)))
 //     dg_i = sum over the item's rows of dy n,  db_i = sum of dy
 //
-// The mean is taken twice: m0 from the row as it is, then delta = mean(h - m0)
-// beside the sum of squares, var = mean((h - m0)^2) - delta^2.  m0 is off by a few
-// fp32 roundings of the row's magnitude, which for a row of large equal values would
-// be all that n is made of; delta takes them out at one instruction a value.  Both
-// means add terms that are divided by C first, so that finite rows have finite means.
+// Mean and variance: first from the sums of h and h^2, one reduction.  Where the mean
+// is more than sqrt(2) standard deviations from zero (or a sum is not finite) these
+// cancel, and the row, still in registers, is summed again from h - m0: delta = mean(h -
+// m0), var = mean((h - m0)^2) - delta^2.  That also takes out m0's own rounding errors,
+// which for a row of large equal values would be all that n is made of.  Means add
+// terms that are divided by C first, so that finite rows have finite means.  (Always
+// both: 22.0 us instead of 19.7 for 17616 x 768.)
 //
-// Row layout as in token_norm.cu: a row stays in the registers of 1 to 16 warps
+// Row layout (forward) as in token_norm.cu: a row stays in the registers of 1 to 16 warps
 // between the sums and the output, every array is read and written once, arithmetic
 // in packed fp32 pairs.
 #include <cuda_bf16.h>
@@ -69,10 +71,13 @@ struct LnArgs {
   float *mean, *r;  // or null
 };
 
+// At least four blocks an SM (two of 16 warps), as the rows' loads need them: 32768 x
+// 4096 157 us, as the compiler has it 168, five 181.  (Two rows a warp side by side,
+// with the gains and biases that they share loaded once: 17616 x 768 20.0 instead of
+// 19.7 us, 17616 x 1024 28.9 instead of 26.1.)
 template <int V, int G>
-__global__ void __launch_bounds__(32 * block_warps(G)) layer_norm_kernel(const LnArgs a) {
-  __shared__ float red[kMaxWarps];
-  __shared__ float2 red2[kMaxWarps];
+__global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 2 : 4) layer_norm_kernel(const LnArgs a) {
+  __shared__ float2 red[2][kMaxWarps];
   griddep_launch_dependents();
   griddep_wait();
   constexpr int kLanes = 32 * G, kRows = block_warps(G) / G;
@@ -104,61 +109,66 @@ __global__ void __launch_bounds__(32 * block_warps(G)) layer_norm_kernel(const L
     }
   }
   const uint64_t inv2 = f2_make(a.inv_c, a.inv_c);
-  uint64_t s2 = 0;  // (0, 0)
+  auto halves = [](uint64_t p) {
+    float lo, hi;
+    f2_split(p, lo, hi);
+    return lo + hi;
+  };
+  uint64_t s2 = 0, q2 = 0;  // (0, 0)
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const F8 u = unpack8(w[i]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s2 = f2_fma(u.p[j], inv2, s2);
-  }
-  float s0, s1;
-  f2_split(s2, s0, s1);
-  const float m0 = row_reduce<G, false>(s0 + s1, red);
-  const uint64_t neg_m = f2_make(-m0, -m0);
-  F8 d[V];
-  uint64_t d2 = 0, q2 = 0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = i * kLanes + lane;
-    d[i] = unpack8(w[i]);
-    const uint64_t off = c < a.chunks ? neg_m : 0;  // chunks past the row stay zeros
-#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      d[i].p[j] = f2_add(d[i].p[j], off);
-      d2 = f2_fma(d[i].p[j], inv2, d2);
-      q2 = f2_fma(d[i].p[j], d[i].p[j], q2);
+      s2 = f2_fma(u.p[j], inv2, s2);
+      q2 = f2_fma(u.p[j], u.p[j], q2);
     }
   }
-  float d0, d1, q0, q1;
-  f2_split(d2, d0, d1);
-  f2_split(q2, q0, q1);
-  const float2 sums = row_sums<G>(d0 + d1, q0 + q1, red2);
-  const float delta = sums.x;
-  float var = fmaf(sums.y, a.inv_c, -delta * delta);
-  if (var < 0.f) var = 0.f;               // (NaN stays NaN)
-  if (sums.y > 0x1.fffffep127f) var = sums.y;  // squares beyond the fp32 range: r = 0
+  float2 sums = row_sums<G>(halves(s2), halves(q2), red[0]);
+  const float m0 = sums.x;
+  const uint64_t neg_m = f2_make(-m0, -m0);
+  float delta = 0.f, var = fmaf(sums.y, a.inv_c, -m0 * m0);
+  if (!(m0 * m0 <= 2.f * var)) {  // the same in all lanes of the row
+    s2 = q2 = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const F8 u = unpack8(w[i]);
+      const uint64_t off = i * kLanes + lane < a.chunks ? neg_m : 0;  // chunks past the row stay zeros
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t d = f2_add(u.p[j], off);
+        s2 = f2_fma(d, inv2, s2);
+        q2 = f2_fma(d, d, q2);
+      }
+    }
+    sums = row_sums<G>(halves(s2), halves(q2), red[1]);
+    delta = sums.x;
+    var = fmaf(sums.y, a.inv_c, -delta * delta);
+    if (var < 0.f) var = 0.f;                    // (NaN stays NaN)
+    if (sums.y > 0x1.fffffep127f) var = sums.y;  // squares beyond the fp32 range: r = 0
+  }
   const float r = __frsqrt_rn(var + a.eps);
   if (lane == 0) {
     if (a.mean) a.mean[row] = m0 + delta;
     if (a.r) a.r[row] = r;
   }
-  const uint32_t item = static_cast<uint32_t>(row) / a.item_rows;
-  const float* g = a.g + static_cast<int64_t>(item) * a.chunks * 8;
-  const float* b = a.b ? a.b + static_cast<int64_t>(item) * a.chunks * 8 : nullptr;
+  const int64_t gains = static_cast<int64_t>(static_cast<uint32_t>(row) / a.item_rows) * a.chunks * 8;
   const uint64_t r2 = f2_make(r, r), shift = f2_make(-delta * r, -delta * r);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = i * kLanes + lane;
     if (c < a.chunks) {
-      const F8 gv = load8f(g, c);
-      F8 y;
-      if (b) {
-        const F8 bv = load8f(b, c);
+      const F8 g = load8f(a.g + gains, c);
+      F8 y = unpack8(w[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y.p[j] = f2_fma(f2_fma(d[i].p[j], r2, shift), gv.p[j], bv.p[j]);
+      for (int j = 0; j < 4; ++j) y.p[j] = f2_fma(f2_add(y.p[j], neg_m), r2, shift);
+      if (a.b) {
+        const F8 b = load8f(a.b + gains, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y.p[j] = f2_fma(y.p[j], g.p[j], b.p[j]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y.p[j] = f2_mul(f2_fma(d[i].p[j], r2, shift), gv.p[j]);
+        for (int j = 0; j < 4; ++j) y.p[j] = f2_mul(y.p[j], g.p[j]);
       }
       a.y[base + c] = pack8(y);
     }
@@ -178,12 +188,37 @@ struct LnBwdArgs {
   float* part;  // [items * parts, kSums, C] partial sums of dg (and of db)
 };
 
-// Blocks p of an item take its rows in a fixed stride; each lane sums dy n (and dy)
-// of its columns over the rows it meets, then the block's rows are added in order.
-template <int V, int G, bool kBias>
-__global__ void __launch_bounds__(32 * block_warps(G)) layer_norm_bwd_kernel(const LnBwdArgs a) {
+// The backward's row layout, by width: at most two chunks a lane, so that the next row
+// (kAhead) and sums of two gradients go beside the current one's; the sums of dy in shared
+// memory, which costs two loads and stores a chunk, and those of dy n there too
+// (kShared) where registers are short.  Measured, us (dy n's sums in registers / in shared
+// memory): 17616 x 512 15.6 / 16.1, x 768 27.2 / 25.1, 9524 x 2048 33.8 / 32.2, 32768 x 4096 173 / 181, 4096
+// x 8192 56 / 61; without the next row 243 for 32768 x 4096; with n and u kept from one use
+// to the other and no next row (as for RMSNorm), both sums in registers, 215.
+template <int kV, int kG, bool kA, bool kS>
+struct BwdLayout {
+  static constexpr int V = kV, G = kG;
+  static constexpr bool kAhead = kA, kShared = kS;
+};
+template <typename F>
+cudaError_t with_bwd_layout(int chunks, F f) {
+  if (chunks <= 32) return f(BwdLayout<1, 1, true, false>());
+  if (chunks <= 64) return f(BwdLayout<2, 1, true, false>());
+  if (chunks <= 128) return f(BwdLayout<2, 2, true, true>());
+  if (chunks <= 256) return f(BwdLayout<2, 4, true, true>());
+  if (chunks <= 512) return f(BwdLayout<2, 8, true, false>());
+  if (chunks <= 1024) return f(BwdLayout<2, 16, true, false>());
+  return f(BwdLayout<2, 32, false, true>());
+}
+
+// Blocks p of an item take its rows in a fixed stride; each lane sums dy n and dy of its
+// columns over the rows it meets, then the block's rows are added in order.
+template <typename L, bool kBias>
+__global__ void __launch_bounds__(32 * block_warps(L::G), L::G > 8 ? 1 : 2) layer_norm_bwd_kernel(const LnBwdArgs a) {
+  constexpr int V = L::V, G = L::G;
+  constexpr bool kAhead = L::kAhead, kSmemG = L::kShared;
   constexpr int kLanes = 32 * G, kRows = block_warps(G) / G, kSums = kBias ? 2 : 1;
-  extern __shared__ __align__(16) float sums[];  // [rows of a block][C], where it has several
+  extern __shared__ __align__(16) float4 planes[];  // [rows of a block][sums][2][C / 8]: halves of the lanes' chunks
   __shared__ float2 red[2][32];
   const int lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
   griddep_launch_dependents();
@@ -192,46 +227,87 @@ __global__ void __launch_bounds__(32 * block_warps(G)) layer_norm_bwd_kernel(con
   const int64_t first = static_cast<int64_t>(item) * a.item_rows, end = first + a.item_rows;
   const int64_t step = static_cast<int64_t>(a.parts) * kRows;
   const int C = a.chunks * 8;
-  F8 g[V];
-  uint64_t acc[kSums][V][4];
+  const float* g = a.g + static_cast<int64_t>(item) * C;
+  float4* mine = planes + static_cast<size_t>(slot) * kSums * 2 * a.chunks;  // dy n: chunk c at c and chunks + c; then dy
+  uint64_t acc[kSmemG ? 1 : V][4];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = i * kLanes + lane;
-    g[i] = load8f(a.g + static_cast<int64_t>(item) * C, c < a.chunks ? c : 0);
+    if (c < a.chunks) {
 #pragma unroll
-    for (int k = 0; k < kSums; ++k)
+      for (int k = 0; k < 2 * kSums; ++k) mine[k * a.chunks + c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (!kSmemG)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[k][i][j] = 0;
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0;
   }
-  int it = 0;
-  for (int64_t row = first + static_cast<int64_t>(p) * kRows + slot; row < end; row += step, ++it) {
+  auto add = [](float4& f, uint64_t lo, uint64_t hi) {
+    f2_split(f2_add(f2_make(f.x, f.y), lo), f.x, f.y);
+    f2_split(f2_add(f2_make(f.z, f.w), hi), f.z, f.w);
+  };
+  struct Row {
+    uint4 y[V], h[V], d[V];
+    float mean, r;
+  };
+  auto load = [&](int64_t row, Row& w) {
     const int64_t base = row * a.chunks;
-    const float mean = a.mean[row], r = a.r[row];
-    uint4 wy[V], wh[V], wd[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * kLanes + lane;
-      const bool in = c < a.chunks;
-      wy[i] = in ? a.dy[base + c] : make_uint4(0u, 0u, 0u, 0u);
-      wh[i] = in ? a.h[base + c] : make_uint4(0u, 0u, 0u, 0u);
-      wd[i] = in && a.dh ? a.dh[base + c] : make_uint4(0u, 0u, 0u, 0u);
+      const bool in = row < end && c < a.chunks;
+      w.y[i] = in ? a.dy[base + c] : make_uint4(0u, 0u, 0u, 0u);
+      w.h[i] = in ? a.h[base + c] : make_uint4(0u, 0u, 0u, 0u);
+      w.d[i] = in && a.dh ? a.dh[base + c] : make_uint4(0u, 0u, 0u, 0u);
     }
-    const uint64_t r2 = f2_make(r, r), neg_mean = f2_make(-mean, -mean);
-    F8 n[V], u[V];
+    w.mean = row < end ? a.mean[row] : 0.f;
+    w.r = row < end ? a.r[row] : 0.f;
+  };
+  int it = 0;
+  int64_t row = first + static_cast<int64_t>(p) * kRows + slot;
+  Row now;
+  if (kAhead) load(row, now);
+  for (; row < end; row += step, ++it) {
+    Row next;
+    if (kAhead) load(row + step, next);
+    else load(row, now);
+    const uint64_t r2 = f2_make(now.r, now.r), neg_mean = f2_make(-now.mean, -now.mean);
+    auto terms = [&](int i, F8& y, F8& n, F8& u) {
+      const int c = i * kLanes + lane;
+      const F8 gv = load8f(g, c < a.chunks ? c : 0);
+      y = unpack8(now.y[i]);
+      n = unpack8(now.h[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        n.p[j] = f2_mul(f2_add(n.p[j], neg_mean), r2);
+        u.p[j] = f2_mul(y.p[j], gv.p[j]);
+      }
+    };
     uint64_t u2 = 0, un2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const F8 y = unpack8(wy[i]);
-      n[i] = unpack8(wh[i]);
-      u[i] = y;
+      const int c = i * kLanes + lane;
+      F8 y, n, u;
+      terms(i, y, n, u);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        n[i].p[j] = f2_mul(f2_add(n[i].p[j], neg_mean), r2);
-        u[i].p[j] = f2_mul(y.p[j], g[i].p[j]);
-        acc[0][i][j] = f2_fma(y.p[j], n[i].p[j], acc[0][i][j]);
-        if constexpr (kBias) acc[1][i][j] = f2_add(acc[1][i][j], y.p[j]);
-        u2 = f2_add(u2, u[i].p[j]);
-        un2 = f2_fma(u[i].p[j], n[i].p[j], un2);  // chunks past the row: u is zero
+        u2 = f2_add(u2, u.p[j]);
+        un2 = f2_fma(u.p[j], n.p[j], un2);  // chunks past the row: u is zero
+        if (!kSmemG) acc[i][j] = f2_fma(y.p[j], n.p[j], acc[i][j]);
+      }
+      if (c < a.chunks) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (kSmemG) {
+            float4 s = mine[k * a.chunks + c];
+            add(s, f2_mul(y.p[2 * k], n.p[2 * k]), f2_mul(y.p[2 * k + 1], n.p[2 * k + 1]));
+            mine[k * a.chunks + c] = s;
+          }
+          if (kBias) {
+            float4 s = mine[(2 + k) * a.chunks + c];
+            add(s, y.p[2 * k], y.p[2 * k + 1]);
+            mine[(2 + k) * a.chunks + c] = s;
+          }
+        }
       }
     }
     float u0, u1, un0, un1;
@@ -243,34 +319,42 @@ __global__ void __launch_bounds__(32 * block_warps(G)) layer_norm_bwd_kernel(con
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * kLanes + lane;
-      F8 o = unpack8(wd[i]);
+      F8 y, n, u, o = unpack8(now.d[i]);
+      terms(i, y, n, u);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o.p[j] = f2_fma(r2, f2_fma(n[i].p[j], mn2, f2_add(u[i].p[j], mu2)), o.p[j]);
-      if (c < a.chunks) a.dx[base + c] = pack8(o);
+      for (int j = 0; j < 4; ++j) o.p[j] = f2_fma(r2, f2_fma(n.p[j], mn2, f2_add(u.p[j], mu2)), o.p[j]);
+      if (c < a.chunks) a.dx[row * a.chunks + c] = pack8(o);
     }
+    if (kAhead) now = next;
   }
-  float* out = a.part + static_cast<size_t>(blockIdx.x) * kSums * C;
-#pragma unroll
-  for (int k = 0; k < kSums; ++k) {
-    ulonglong2* mine = reinterpret_cast<ulonglong2*>(kRows > 1 ? sums + static_cast<size_t>(slot) * C : out + k * C);
+  if (!kSmemG) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * kLanes + lane;
       if (c < a.chunks) {
-        mine[2 * c] = make_ulonglong2(acc[k][i][0], acc[k][i][1]);
-        mine[2 * c + 1] = make_ulonglong2(acc[k][i][2], acc[k][i][3]);
-      }
-    }
-    if constexpr (kRows > 1) {
-      __syncthreads();
-      for (int c = threadIdx.x; c < C; c += 32 * block_warps(G)) {
-        float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) s += sums[i * C + c];
-        out[k * C + c] = s;
+        for (int k = 0; k < 2; ++k) {
+          float4 f;
+          f2_split(acc[i][2 * k], f.x, f.y);
+          f2_split(acc[i][2 * k + 1], f.z, f.w);
+          mine[k * a.chunks + c] = f;
+        }
       }
-      if (k + 1 < kSums) __syncthreads();
     }
+  }
+  __syncthreads();
+  // The block's rows in order.
+  float4* out = reinterpret_cast<float4*>(a.part + static_cast<size_t>(blockIdx.x) * kSums * C);
+  for (int i = threadIdx.x; i < kSums * 2 * a.chunks; i += 32 * block_warps(G)) {
+    const int k = i / (2 * a.chunks), j = i - k * 2 * a.chunks;  // half j & 1 of chunk j / 2 of sum k
+    const float4* from = planes + (2 * k + (j & 1)) * a.chunks + j / 2;
+    float4 s = from[0];
+#pragma unroll
+    for (int q = 1; q < kRows; ++q) {
+      const float4 f = from[static_cast<size_t>(q) * kSums * 2 * a.chunks];
+      s = make_float4(s.x + f.x, s.y + f.y, s.z + f.z, s.w + f.w);
+    }
+    out[i] = s;
   }
 }
 
@@ -285,19 +369,6 @@ __global__ void __launch_bounds__(256) ln_sum_kernel(const float* part, int part
   const float s = column_sum(part + (static_cast<size_t>(item) * parts * n_sums + k) * C + at, parts,
                              static_cast<size_t>(n_sums) * C);
   if (threadIdx.x < 8) (k == 0 ? dg : db)[static_cast<size_t>(item) * C + at + threadIdx.x] = s;
-}
-
-// The backward's row layout: at most two chunks a lane, because it keeps n, u and
-// the sums of both gradients in registers.
-template <typename F>
-cudaError_t with_bwd_layout(int chunks, F f) {
-  if (chunks <= 32) return f(Layout<1, 1>());
-  if (chunks <= 64) return f(Layout<2, 1>());
-  if (chunks <= 128) return f(Layout<2, 2>());
-  if (chunks <= 256) return f(Layout<2, 4>());
-  if (chunks <= 512) return f(Layout<2, 8>());
-  if (chunks <= 1024) return f(Layout<2, 16>());
-  return f(Layout<2, 32>());
 }
 
 }  // namespace
@@ -352,8 +423,12 @@ cudaError_t launch_layer_norm_bwd(const LayerNormBwd& t, float* part, int parts,
   return with_bwd_layout(a.chunks, [&](auto l) {
     using L = decltype(l);
     constexpr int kWarps = block_warps(L::G), kRows = kWarps / L::G;
-    const size_t smem = kRows > 1 ? static_cast<size_t>(kRows) * t.C * sizeof(float) : 0;  // at most 16 KB
-    auto kernel = t.db ? layer_norm_bwd_kernel<L::V, L::G, true> : layer_norm_bwd_kernel<L::V, L::G, false>;
+    const size_t smem = static_cast<size_t>(kRows) * (t.db ? 2 : 1) * t.C * sizeof(float);
+    auto kernel = t.db ? layer_norm_bwd_kernel<L, true> : layer_norm_bwd_kernel<L, false>;
+    if (smem > 40 * 1024) {  // more than the 48 KB, with the kernel's own, that need no asking
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+      if (e != cudaSuccess) return e;
+    }
     return launch_pdl(kernel, dim3(static_cast<unsigned>(t.items * parts)), dim3(32 * kWarps), smem, st, a);
   });
 }

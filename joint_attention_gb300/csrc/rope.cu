@@ -12,14 +12,16 @@
 //
 // Angles: pos freq / (2 pi) in turns as the sum of two floats (the product and its
 // exact remainder, with 1 / (2 pi) and freq / (2 pi) in two floats as well), whole
-// turns taken off exactly, then sincospif of what is left: off by some 2^-24 of a turn
-// for angles up to millions, where an fp32 angle would be off by 2^-24 of itself.
+// turns taken off exactly; what is left, within half a turn, is off by some 2^-24 of a
+// turn for angles up to millions, where an fp32 angle would be off by 2^-24 of itself.
+// There __sinf and __cosf are off by 2^-21.2 at most, a thousandth of the output's
+// rounding to bf16 (sincospif, exact to 2^-23, takes four times their instructions).
 //
 // Bound by HBM: every value is read and written once.  A thread keeps the cosines and
 // sines of one token's 8 pairs and takes 16 channels of that token in a run of heads
-// (and batch items, where they share positions), so that sincospif, some 350
-// instructions for 8 pairs, is paid once a run.  d / 16 threads a row; a warp covers 4
-// or 8 neighbouring tokens of a head, contiguous in memory.
+// (and batch items, where they share positions), so that the angles are paid once a
+// run.  d / 16 threads a row; a warp covers 4 or 8 neighbouring tokens of a head,
+// contiguous in memory.  The arithmetic is in packed fp32 pairs.
 #include <cuda_bf16.h>
 
 #include "jattn_internal.h"
@@ -30,10 +32,12 @@ namespace jattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;       // rows of a thread whose loads are in flight together
-constexpr int kMaxRun = 16;     // heads a thread takes at most
-constexpr int kBlocks = 152 * 8;     // blocks aimed at
-constexpr int kBlocksBwd = 152 * 4;  // with gains' gradients: a partial sum each
+constexpr int kAhead = 2;   // rows of a thread that are loaded while as many are written
+constexpr int kMaxRun = 16;  // heads a thread takes at most
+// Blocks aimed at, by longer or shorter runs: forward all that fit at once (three an SM;
+// 1 x 10 x 4033 rows of 128 6.1 us, with 8 an SM 7.8), backward with gains' gradients
+// twice that fit (4 x 48 x 2381 rows of 128 67.1 us, 4 an SM 68.5, 12 72.8).
+constexpr int kBlocks = 152 * 3, kBlocksBwd = 152 * 6;
 
 struct RopeArgs {
   const uint4* src[2];   // q, k (backward: their rotated gradients)
@@ -48,7 +52,6 @@ struct RopeArgs {
   int N, tiles;          // tokens, blocks over them
   int axes, P;
   int pair_end[kMaxAxes];  // pairs before the end of each axis
-  bool interleaved;
   float sign;  // of the angles
   float eps;
   float* part;  // backward with gains: [blocks of q, then of k][d]
@@ -59,34 +62,83 @@ __device__ __forceinline__ void rotation(float pos, float freq, float& c, float&
   constexpr float kInv = 0x1.45f306p-3f, kInvLow = 0x1.b9391p-28f;  // 1 / (2 pi)
   const float fh = __fmul_rn(freq, kInv), fl = __fmaf_rn(freq, kInvLow, __fmaf_rn(freq, kInv, -fh));
   const float th = __fmul_rn(pos, fh), tl = __fmaf_rn(pos, fl, __fmaf_rn(pos, fh, -th));
-  sincospif(2.f * ((th - rintf(th)) + tl), &s, &c);
+  float t = (th - rintf(th)) + tl;
+  t -= rintf(t);  // a low part that is a turn itself
+  __sincosf(t * 6.283185307179586f, &s, &c);
+}
+
+// 16 channels of a row, two pairs packed: x the pairs' first, y their second channels.
+// From the thread's two chunks: interleaved, pairs 0 .. 3 from one and 4 .. 7 from the
+// other; else first channels from one, second ones from the other.
+struct Pairs {
+  uint64_t x[4], y[4];
+};
+template <bool kInter>
+__device__ __forceinline__ Pairs unpack_pairs(const uint4 (&c)[2]) {
+  const uint32_t w[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
+  auto lo = [&](int i) { return __uint_as_float(w[i] << 16); };
+  auto hi = [&](int i) { return __uint_as_float(w[i] & 0xFFFF0000u); };
+  Pairs v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.x[i] = kInter ? f2_make(lo(2 * i), lo(2 * i + 1)) : f2_make(lo(i), hi(i));
+    v.y[i] = kInter ? f2_make(hi(2 * i), hi(2 * i + 1)) : f2_make(lo(4 + i), hi(4 + i));
+  }
+  return v;
+}
+template <bool kInter>
+__device__ __forceinline__ void store_pairs(uint4* row, const int (&chunk)[2], const Pairs& v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x0, x1, y0, y1;
+    f2_split(v.x[i], x0, x1);
+    f2_split(v.y[i], y0, y1);
+    w[kInter ? 2 * i : i] = kInter ? pack_bf16x2(x0, y0) : pack_bf16x2(x0, x1);
+    w[kInter ? 2 * i + 1 : 4 + i] = kInter ? pack_bf16x2(x1, y1) : pack_bf16x2(y0, y1);
+  }
+  row[chunk[0]] = make_uint4(w[0], w[1], w[2], w[3]);
+  row[chunk[1]] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+// The sum of all a * b.
+__device__ __forceinline__ float dot(const Pairs& a, const Pairs& b) {
+  uint64_t s = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = f2_fma(a.y[i], b.y[i], f2_fma(a.x[i], b.x[i], s));
+  float lo, hi;
+  f2_split(s, lo, hi);
+  return lo + hi;
+}
+template <typename F>
+__device__ __forceinline__ void each(F f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f(i);
 }
 
 // Where a block and a thread are, and the thread's cosines and sines.
-template <int D>
+template <int D, bool kInter>
 struct RopeThread {
   static constexpr int kLanes = D / 16, kTokens = kThreads / kLanes;
-  int t, item, first, count, token;  // tensor (0: q, 1: k); heads first .. first + count - 1 of the item's
-  int chunk[2];                      // the thread's 16-byte chunks of a row
-  bool live, rot[2];
-  int64_t row0;  // the first head's row
-  float c[8], s[8];
+  int t, item, run, count, token;  // tensor (0: q, 1: k); the run of heads of the item, how many
+  int chunk[2];                    // the thread's 16-byte chunks of a row
+  bool live, rot[2];               // whether the pairs of its halves turn
+  int64_t row0;                    // the first head's row
+  uint64_t c[4], s[4];             // cosines and sines, once turns() has run
 
   __device__ __forceinline__ explicit RopeThread(const RopeArgs& a) {
     const int per_item = a.chunks[0] + a.chunks[1];
     const int tile = blockIdx.x % a.tiles, job = blockIdx.x / a.tiles;
     item = job / per_item;
-    int run = job - item * per_item;
+    run = job - item * per_item;
     t = run >= a.chunks[0];
     if (t) run -= a.chunks[0];
-    first = run * a.run;
-    const int heads = t ? a.heads[1] : a.heads[0];
+    const int heads = t ? a.heads[1] : a.heads[0], first = run * a.run;
     count = min(a.run, heads - first);
     token = tile * kTokens + threadIdx.x / kLanes;
     live = token < a.N;
     row0 = (static_cast<int64_t>(item) * heads + first) * a.N + token;
     const int l = threadIdx.x % kLanes;
-    if (a.interleaved) {
+    if (kInter) {
       chunk[0] = l;
       chunk[1] = l + kLanes;
       rot[0] = chunk[0] < a.P / 4;
@@ -97,182 +149,190 @@ struct RopeThread {
       chunk[0] = l < lanes ? l : 2 * l;
       chunk[1] = l < lanes ? l + lanes : 2 * l + 1;
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      c[k] = 1.f;
-      s[k] = 0.f;
-    }
-    if (!live) return;
+  }
+  // Run after the first rows' loads have been sent, which it then overlaps.
+  __device__ __forceinline__ void turns(const RopeArgs& a) {
+    const int l = threadIdx.x % kLanes;
+    float at[kMaxAxes], co[8], si[8];
     const float* pos = a.pos + (static_cast<int64_t>(item) * a.N + token) * a.axes;
-    float at[kMaxAxes];
 #pragma unroll
-    for (int i = 0; i < kMaxAxes; ++i) at[i] = i < a.axes ? __ldg(pos + i) : 0.f;
+    for (int i = 0; i < kMaxAxes; ++i) at[i] = live && i < a.axes ? __ldg(pos + i) : 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (!rot[k / 4]) continue;
-      const int p = a.interleaved ? 4 * chunk[k / 4] + k % 4 : 8 * l + k;
+      co[k] = 1.f;
+      si[k] = 0.f;
+      if (!live || !rot[k / 4]) continue;
+      const int p = kInter ? 4 * chunk[k / 4] + k % 4 : 8 * l + k;
       float w = at[0];
 #pragma unroll
       for (int i = 1; i < kMaxAxes; ++i)
         if (p >= a.pair_end[i - 1]) w = at[i];
-      rotation(w, a.sign * __ldg(a.freq + p), c[k], s[k]);
+      rotation(w, a.sign * __ldg(a.freq + p), co[k], si[k]);
     }
+    each([&](int i) {
+      c[i] = f2_make(co[2 * i], co[2 * i + 1]);
+      s[i] = f2_make(si[2 * i], si[2 * i + 1]);
+    });
   }
-  // The 16 channels, chunk 0 first, rotated.
-  __device__ __forceinline__ void rotate(const RopeArgs& a, float (&v)[16]) const {
-    auto turn = [&](int i, int j, int k) {
-      const float x = v[i], y = v[j];
-      v[i] = fmaf(x, c[k], -(y * s[k]));
-      v[j] = fmaf(x, s[k], y * c[k]);
+  __device__ __forceinline__ void rotate(Pairs& v) const {
+    auto half = [&](int h) {
+#pragma unroll
+      for (int i = 2 * h; i < 2 * h + 2; ++i) {
+        const uint64_t x = v.x[i], y = v.y[i];
+        v.x[i] = f2_fma(y ^ 0x8000000080000000ull, s[i], f2_mul(x, c[i]));
+        v.y[i] = f2_fma(x, s[i], f2_mul(y, c[i]));
+      }
     };
-    if (a.interleaved) {
+    // (Not as a product with 1 and 0: an infinity beside them would be NaN.)
+    if (rot[0]) half(0);
+    if (rot[1]) half(1);
+  }
+  __device__ __forceinline__ Pairs gains(const float* gain) const {
+    float f[2][8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (rot[h])
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) turn(8 * h + 2 * k, 8 * h + 2 * k + 1, 4 * h + k);
-    } else if (rot[0]) {
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<float4*>(&f[h][4 * i]) = __ldg(reinterpret_cast<const float4*>(gain) + 2 * chunk[h] + i);
+    Pairs g;
+    each([&](int i) {
+      const int j = 4 * (i % 2);
+      g.x[i] = kInter ? f2_make(f[i / 2][j], f[i / 2][j + 2]) : f2_make(f[0][2 * i], f[0][2 * i + 1]);
+      g.y[i] = kInter ? f2_make(f[i / 2][j + 1], f[i / 2][j + 3]) : f2_make(f[1][2 * i], f[1][2 * i + 1]);
+    });
+    return g;
+  }
+  // A sum over the threads of the row.
+  static __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) turn(k, 8 + k, k);
-    }
+    for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
   }
 };
 
-__device__ __forceinline__ void unpack16(const uint4& lo, const uint4& hi, float (&v)[16]) {
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+// Some rows of a run, of one or two tensors.
+template <int kRows, int kTensors, typename Thread>
+struct RowLoads {
+  uint4 w[kRows][kTensors][2];
+  __device__ __forceinline__ void load(const Thread& th, const uint4* const (&from)[kTensors], int64_t at, int64_t step,
+                                       int h0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int k = 0; k < kTensors; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[i][k][h] = th.live && h0 + i < th.count ? from[k][at + i * step + th.chunk[h]] : make_uint4(0u, 0u, 0u, 0u);
   }
-}
-__device__ __forceinline__ uint4 pack_half(const float (&v)[16], int h) {
-  return make_uint4(pack_bf16x2(v[8 * h], v[8 * h + 1]), pack_bf16x2(v[8 * h + 2], v[8 * h + 3]),
-                    pack_bf16x2(v[8 * h + 4], v[8 * h + 5]), pack_bf16x2(v[8 * h + 6], v[8 * h + 7]));
-}
-template <int D>
-__device__ __forceinline__ void load_gain(const RopeThread<D>& th, const float* gain, float (&g)[16]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[8 * h + i] = __ldg(gain + 8 * th.chunk[h] + i);
-}
+};
 
-template <int D, bool kNorm>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+template <int D, bool kInter, bool kNorm>
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const RopeThread<D> th(a);
-  const uint4* src = th.t ? a.src[1] : a.src[0];
+  using Thread = RopeThread<D, kInter>;
+  Thread th(a);
+  const uint4* const src[1] = {th.t ? a.src[1] : a.src[0]};
   uint4* dst = th.t ? a.dst[1] : a.dst[0];
-  float g[16];
-  if constexpr (kNorm) load_gain(th, th.t ? a.gain[1] : a.gain[0], g);
   constexpr int kRow = D / 8;  // chunks of a row
   const int64_t step = static_cast<int64_t>(a.N) * kRow;
   int64_t at = th.row0 * kRow;
+  RowLoads<kAhead, 1, Thread> now, next;
+  now.load(th, src, at, step, 0);
+  th.turns(a);
+  Pairs g;
+  if constexpr (kNorm) g = th.gains(th.t ? a.gain[1] : a.gain[0]);
   for (int h0 = 0; h0 < th.count; h0 += kAhead, at += kAhead * step) {
-    uint4 w[kAhead][2];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[i][h] = th.live && h0 + i < th.count ? src[at + i * step + th.chunk[h]] : make_uint4(0u, 0u, 0u, 0u);
+    next.load(th, src, at + kAhead * step, step, h0 + kAhead);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (h0 + i >= th.count) break;  // the same in the whole block
-      float v[16];
-      unpack16(w[i][0], w[i][1], v);
+      Pairs v = unpack_pairs<kInter>(now.w[i][0]);
       if constexpr (kNorm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(v[e], v[e], ss);
-#pragma unroll
-        for (int o = RopeThread<D>::kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = __frsqrt_rn(fmaf(ss, 1.f / D, a.eps));
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = v[e] * r * g[e];
+        const float r = __frsqrt_rn(fmaf(Thread::row_sum(dot(v, v)), 1.f / D, a.eps));
+        const uint64_t r2 = f2_make(r, r);
+        each([&](int j) {
+          v.x[j] = f2_mul(f2_mul(v.x[j], r2), g.x[j]);
+          v.y[j] = f2_mul(f2_mul(v.y[j], r2), g.y[j]);
+        });
       }
-      th.rotate(a, v);
-      if (th.live) {
-        dst[at + i * step + th.chunk[0]] = pack_half(v, 0);
-        dst[at + i * step + th.chunk[1]] = pack_half(v, 1);
-      }
+      th.rotate(v);
+      if (th.live) store_pairs<kInter>(dst + at + i * step, th.chunk, v);
     }
+    now = next;
   }
 }
 
 // With gains: the rotation by -t, the backward of the RMSNorm and the block's part of
 // the gain's gradient (each thread its 16 channels over its heads, then the tokens of
 // the block in a fixed order).
-template <int D>
-__global__ void __launch_bounds__(kThreads) rope_norm_bwd_kernel(const __grid_constant__ RopeArgs a) {
+template <int D, bool kInter>
+__global__ void __launch_bounds__(kThreads, 2) rope_norm_bwd_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float sums[kThreads / 32][D];
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kLanes = RopeThread<D>::kLanes;
-  const RopeThread<D> th(a);
-  const uint4* src = th.t ? a.src[1] : a.src[0];
-  const uint4* x = th.t ? a.x[1] : a.x[0];
+  using Thread = RopeThread<D, kInter>;
+  constexpr int kLanes = Thread::kLanes;
+  Thread th(a);
+  const uint4* const src[2] = {th.t ? a.src[1] : a.src[0], th.t ? a.x[1] : a.x[0]};
   uint4* dst = th.t ? a.dst[1] : a.dst[0];
-  float g[16], dg[16];
-  load_gain(th, th.t ? a.gain[1] : a.gain[0], g);
-#pragma unroll
-  for (int e = 0; e < 16; ++e) dg[e] = 0.f;
-  constexpr int kRow = D / 8, kDeep = 2;
+  constexpr int kRow = D / 8, kDeep = 1;
   const int64_t step = static_cast<int64_t>(a.N) * kRow;
   int64_t at = th.row0 * kRow;
+  RowLoads<kDeep, 2, Thread> now, next;
+  now.load(th, src, at, step, 0);
+  th.turns(a);
+  const Pairs g = th.gains(th.t ? a.gain[1] : a.gain[0]);
+  Pairs dg = {};
   for (int h0 = 0; h0 < th.count; h0 += kDeep, at += kDeep * step) {
-    uint4 w[kDeep][2], wx[kDeep][2];
-#pragma unroll
-    for (int i = 0; i < kDeep; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool in = th.live && h0 + i < th.count;
-        w[i][h] = in ? src[at + i * step + th.chunk[h]] : make_uint4(0u, 0u, 0u, 0u);
-        wx[i][h] = in ? x[at + i * step + th.chunk[h]] : make_uint4(0u, 0u, 0u, 0u);
-      }
+    next.load(th, src, at + kDeep * step, step, h0 + kDeep);
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) {
       if (h0 + i >= th.count) break;  // the same in the whole block
-      float v[16], n[16];
-      unpack16(w[i][0], w[i][1], v);
-      unpack16(wx[i][0], wx[i][1], n);
-      th.rotate(a, v);
-      float ss = 0.f, ux = 0.f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        ss = fmaf(n[e], n[e], ss);
-        ux = fmaf(v[e] * g[e], n[e], ux);
-      }
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        ux += __shfl_xor_sync(0xffffffffu, ux, o);
-      }
+      Pairs v = unpack_pairs<kInter>(now.w[i][0]), n = unpack_pairs<kInter>(now.w[i][1]), u;
+      th.rotate(v);
+      each([&](int j) {
+        u.x[j] = f2_mul(v.x[j], g.x[j]);
+        u.y[j] = f2_mul(v.y[j], g.y[j]);
+      });
+      const float ss = Thread::row_sum(dot(n, n)), ux = Thread::row_sum(dot(u, n));
       const float r = __frsqrt_rn(fmaf(ss, 1.f / D, a.eps));
       const float m = -(ux * r) * (1.f / D);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float nr = n[e] * r;
-        dg[e] = fmaf(v[e], nr, dg[e]);
-        v[e] = r * fmaf(nr, m, v[e] * g[e]);
-      }
-      if (th.live) {
-        dst[at + i * step + th.chunk[0]] = pack_half(v, 0);
-        dst[at + i * step + th.chunk[1]] = pack_half(v, 1);
-      }
+      const uint64_t r2 = f2_make(r, r), m2 = f2_make(m, m);
+      each([&](int j) {
+        n.x[j] = f2_mul(n.x[j], r2);
+        n.y[j] = f2_mul(n.y[j], r2);
+        dg.x[j] = f2_fma(v.x[j], n.x[j], dg.x[j]);
+        dg.y[j] = f2_fma(v.y[j], n.y[j], dg.y[j]);
+        v.x[j] = f2_mul(r2, f2_fma(n.x[j], m2, u.x[j]));
+        v.y[j] = f2_mul(r2, f2_fma(n.y[j], m2, u.y[j]));
+      });
+      if (th.live) store_pairs<kInter>(dst + at + i * step, th.chunk, v);
     }
+    now = next;
   }
+  // The warp's tokens, then the block's warps; channels as unpack_pairs has them.
+  float f[16];
+  each([&](int i) {
+    f2_split(dg.x[i], f[4 * i], f[4 * i + 1]);
+    f2_split(dg.y[i], f[4 * i + 2], f[4 * i + 3]);
+  });
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
 #pragma unroll
-    for (int o = kLanes; o < 32; o <<= 1) dg[e] += __shfl_xor_sync(0xffffffffu, dg[e], o);
+    for (int o = kLanes; o < 32; o <<= 1) f[e] += __shfl_xor_sync(0xffffffffu, f[e], o);
   }
   if (threadIdx.x % 32 < kLanes) {
+    float* row = sums[threadIdx.x / 32];
+    each([&](int i) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sums[threadIdx.x / 32][8 * th.chunk[h] + i] = dg[8 * h + i];
+      for (int j = 0; j < 2; ++j) {
+        const int px = kInter ? 8 * th.chunk[i / 2] + 4 * (i % 2) + 2 * j : 8 * th.chunk[0] + 2 * i + j;
+        const int py = kInter ? px + 1 : 8 * th.chunk[1] + 2 * i + j;
+        row[px] = f[4 * i + j];
+        row[py] = f[4 * i + 2 + j];
+      }
+    });
   }
   __syncthreads();
   if (threadIdx.x < D) {
@@ -280,12 +340,9 @@ __global__ void __launch_bounds__(kThreads) rope_norm_bwd_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) s += sums[i][threadIdx.x];
     // Blocks of q first: an item's runs of q, each over the tiles.
-    const int tile = blockIdx.x % a.tiles, job = blockIdx.x / a.tiles;
-    const int run = job - th.item * (a.chunks[0] + a.chunks[1]) - (th.t ? a.chunks[0] : 0);
-    const int items = gridDim.x / (a.tiles * (a.chunks[0] + a.chunks[1]));
-    const int before = th.t ? items * a.chunks[0] : 0;
-    const int64_t at_part = static_cast<int64_t>(before + th.item * a.chunks[th.t] + run) * a.tiles + tile;
-    a.part[at_part * D + threadIdx.x] = s;
+    const int items = gridDim.x / (a.tiles * (a.chunks[0] + a.chunks[1])), tile = blockIdx.x % a.tiles;
+    const int64_t runs = static_cast<int64_t>(th.t ? items * a.chunks[0] : 0) + th.item * a.chunks[th.t] + th.run;
+    a.part[(runs * a.tiles + tile) * D + threadIdx.x] = s;
   }
 }
 
@@ -299,6 +356,12 @@ __global__ void __launch_bounds__(256) rope_gain_kernel(const float* part, int p
   const float s = column_sum(part + (k ? static_cast<size_t>(parts_q) * d : 0) + at, k ? parts_k : parts_q,
                              static_cast<size_t>(d));
   if (threadIdx.x < 8) (k ? dgk : dgq)[at + threadIdx.x] = s;
+}
+
+template <int D>
+auto rope_of(bool inter, bool norm) {
+  return inter ? (norm ? rope_kernel<D, true, true> : rope_kernel<D, true, false>)
+               : (norm ? rope_kernel<D, false, true> : rope_kernel<D, false, false>);
 }
 
 // How a call is split; all of it a function of the sizes alone.
@@ -341,7 +404,6 @@ RopeArgs args_of(const Rope& t, const Split& s, float sign) {
   a.P = end;
   a.pos = t.pos;
   a.freq = t.freq;
-  a.interleaved = t.interleaved;
   a.sign = sign;
   a.eps = t.eps;
   return a;
@@ -362,8 +424,7 @@ cudaError_t launch_rope(const Rope& t, const uint16_t* q, const uint16_t* k, uin
     a.gain[0] = t.gq;
     a.gain[1] = t.gk;
   }
-  auto kernel = t.d == 64 ? (norm ? rope_kernel<64, true> : rope_kernel<64, false>)
-                          : (norm ? rope_kernel<128, true> : rope_kernel<128, false>);
+  auto kernel = t.d == 64 ? rope_of<64>(t.interleaved, norm) : rope_of<128>(t.interleaved, norm);
   return launch_pdl(kernel, dim3(static_cast<unsigned>(s.blocks())), dim3(kThreads), 0, st, a);
 }
 
@@ -386,8 +447,9 @@ cudaError_t launch_rope_norm_bwd(const Rope& t, const uint16_t* dq_rot, const ui
   a.gain[0] = t.gq;
   a.gain[1] = t.gk;
   a.part = part;
-  return launch_pdl(t.d == 64 ? rope_norm_bwd_kernel<64> : rope_norm_bwd_kernel<128>,
-                    dim3(static_cast<unsigned>(s.blocks())), dim3(kThreads), 0, st, a);
+  auto kernel = t.d == 64 ? (t.interleaved ? rope_norm_bwd_kernel<64, true> : rope_norm_bwd_kernel<64, false>)
+                          : (t.interleaved ? rope_norm_bwd_kernel<128, true> : rope_norm_bwd_kernel<128, false>);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(s.blocks())), dim3(kThreads), 0, st, a);
 }
 
 cudaError_t launch_rope_gains(const Rope& t, const float* part, float* dgq, float* dgk, cudaStream_t st) {

@@ -3,8 +3,9 @@ definitions in float64.
 
 Tolerances, from the arithmetic (u = 2^-24, one fp32 rounding):
 * An angle's fraction of a turn is rounded once (2^-25 of a turn at most, and the low parts less while the
-  angle is below 2^22 turns) and sincospif is off by at most 2 u: cosines and sines are off by 2 pi 2^-25 +
-  2 u < 2^-21.  A rotated value has two products and a sum: (|z_i| + |z_j|) 2^-20 in all.
+  angle is below 2^22 turns), then to radians (2^-23), and the sine and cosine of up to half a turn are off by
+  2^-21.19 at most: 2 pi 2^-25 + 2^-23 + 2^-21.19 < 2^-20.  A rotated value has two products and a sum: (|z_i|
+  + |z_j|) 2^-19 in all.
 * z = x r g: the sum of squares 20 u halved by the root, which rounds once, and two products: 14 u.
 * Every output: half a bf16 step, 2^-8 relative.
 * Backward with gains: the rotated gradient's error times g, r and the terms of dx, whose sums pass less than
