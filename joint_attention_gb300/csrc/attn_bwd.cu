@@ -76,11 +76,13 @@ constexpr int kBwdThreads = 640;  // 5 warpgroups
 // the idle warps 12-15 24, TMA / issuer 96 (their launch count, no
 // setmaxnreg); 256 x 128 + 128 x (104 + 24 + 96) = 61440.  The issuers spill
 // below 96.
+// Grouped heads: compute 136 (P in fp32), d = 64: epilogue 72, d = 128: drain 88 (no norm).
 // setmaxnreg budgets.  An increase must not be below, a decrease not above,
 // the count the kernel launches with, and the sum must fit the launch's
 // registers (640 x that count); the launcher checks both against the
 // compiled kernel before every launch.
 constexpr int kRegCompute64 = 120, kRegDrain64 = 88, kRegEpi64 = 104, kRegMma64 = 48;
+constexpr int kRegComputeGrouped = 136, kRegEpiGrouped = 72, kRegDrain128Grouped = 88;
 constexpr int kRegCompute128 = 128, kRegDrain128 = 104, kRegIdle128 = 24, kRegMma128 = 96;
 // The split uses the whole launch allocation (640 x 96): the kernel must launch
 // with exactly 96 registers per thread.
@@ -103,6 +105,12 @@ static_assert(kRegEpi64 >= kRegLaunchMax && kRegMma64 <= kRegLaunchMin && kRegDr
                   kRegMma128 <= kRegLaunchMin &&
                   kRegDrain64 <= kRegLaunchMin && kRegCompute64 >= kRegLaunchMax && kRegCompute128 >= kRegLaunchMax,
               "setmaxnreg direction");
+static_assert(kRegComputeGrouped >= kRegLaunchMax && kRegEpiGrouped <= kRegLaunchMin &&
+                  kRegDrain128Grouped <= kRegLaunchMin,
+              "setmaxnreg direction");
+static_assert(32 * (2 * kRegComputeGrouped + kRegDrain64 + kRegEpiGrouped + kRegMma64) <= kSubPartRegs &&
+                  32 * (2 * kRegComputeGrouped + kRegDrain128Grouped + kRegIdle128 + kRegMma128) <= kSubPartRegs,
+              "the grouped register splits exceed a sub-partition's launch allocation");
 constexpr int kWarpEpi = 12;
 constexpr int kWarpTma = 16;
 constexpr int kWarpMma0 = 17;  // recompute issuer (d = 128: the only one)
@@ -191,10 +199,8 @@ struct BwdUnit {
   // Ordered modes: contributions to that query tile's accumulator made before
   // this one.
   __device__ __forceinline__ int rank(int i) const { return ord == kDqAscending ? j : i; }
-  __device__ __forceinline__ int last_rank(int) const { return nkt - 1; }
   __device__ __forceinline__ int kv0() const { return row0 + 128 * j; }  // first key row
   __device__ __forceinline__ int tiles() const { return nkt; }           // query tiles visited
-  __device__ __forceinline__ int head(int) const { return bh; }          // of the i-th query tile
 };
 
 // Grouped heads, causal or not: a key tile of one kv head visits the query tiles of
@@ -207,27 +213,30 @@ struct BwdUnitGrouped {
   int per_head;  // query tiles of each
   int n;         // in all
   int j, nkt, row0, end, prow0, ord;  // as in BwdUnit
-  bool causal;
-  __device__ __forceinline__ int query_tile(int i) const {
-    const int r = i % per_head;
+  bool causal;   // then the first query tile of each head holds the key tile's own rows,
+                 // of which a key reaches the queries from its own on
+  // The r-th query tile visited of a head.
+  __device__ __forceinline__ int query_tile(int r) const {
     if (ord == kDqAscending && !causal) return r;
     const int q = r + j;
     return q < nkt ? q : q - nkt;
   }
-  __device__ __forceinline__ int rank(int) const { return j; }
-  __device__ __forceinline__ int last_rank(int i) const { return causal ? query_tile(i) : nkt - 1; }
+  // The r of the segment's last query tile.
+  __device__ __forceinline__ int visit_of_last() const {
+    return ord == kDqAscending && !causal ? nkt - 1 : nkt - 1 - j;
+  }
   __device__ __forceinline__ int kv0() const { return row0 + 128 * j; }
   __device__ __forceinline__ int tiles() const { return n; }
-  __device__ __forceinline__ int head(int i) const { return h0 + i / per_head; }
-  // Whether the i-th query tile holds the key tile's own rows, of which each key
-  // reaches the queries from its own on.
-  __device__ __forceinline__ bool diagonal(int i) const { return causal && i % per_head == 0; }
+  // Rows of the segment's last tile, if it is a ragged one that the tensor goes on behind; else 0.
+  __device__ __forceinline__ int ragged(int rows) const { return end < rows ? (end - row0) & 127 : 0; }
 };
 
 // The [B, H, N, d] layout: one segment [0, N) per head, decoded without the
 // segment table.
+struct NoMaps {};
 struct BwdWorkUniform {
   static constexpr bool kGrouped = false;
+  using Ragged = NoMaps;
   int upc;    // 128-row tiles per head
   int units;  // heads * upc
   int ord;    // dQ order
@@ -250,6 +259,7 @@ struct BwdWorkUniform {
 // Packed variable-length layout: segments from the table.
 struct BwdWork {
   static constexpr bool kGrouped = false;
+  using Ragged = NoMaps;
   int upc;    // units per head (padded rows per head / 128)
   int units;  // heads * upc
   int ord;    // dQ order
@@ -274,8 +284,10 @@ struct BwdWork {
   }
 };
 
+struct RaggedMaps;
 struct BwdWorkGrouped {
   static constexpr bool kGrouped = true;
+  using Ragged = RaggedMaps;
   int units;
   int heads, group;  // kv heads, and query heads of each
   int ord;
@@ -286,11 +298,9 @@ struct BwdWorkGrouped {
   GroupedOrder order;
   __device__ __forceinline__ BwdUnitGrouped unit(int u) const {
     BwdUnitGrouped r;
-    const int k = u / heads;
-    r.bh = u - k * heads;
-    r.h0 = r.bh * group;
     int s, level;
-    order.at(k, causal, &s, &level);
+    order.unit(u, heads, causal, &s, &r.bh, &level);
+    r.h0 = r.bh * group;
     r.nkt = order.blocks[s];
     r.j = causal ? r.nkt - 1 - level : level;
     r.per_head = causal ? level + 1 : r.nkt;
@@ -321,7 +331,6 @@ struct BwdBars {
   uint64_t drain_sync;  // the dQ drain threads' staging handshakes
   uint64_t kraw_full;   // d = 64: the unit's raw k tile has landed (epilogue)
   uint64_t drain[3];
-  uint64_t tail;  // grouped: a tile whose rows behind the segment are to be zeroed has landed
   uint32_t tmem_base;
   int abort;
   __align__(16) float gk[128];  // K-RMSNorm gain (d entries)
@@ -391,106 +400,107 @@ __device__ void bwd_producer(const CUtensorMap* mq, const CUtensorMap* mk, const
   }
 }
 
-// The producer of grouped heads, a whole warp.  A ragged tile at a segment's end holds
-// the next sequence's rows (or anything, behind the last one), whose values times
-// probabilities of zero are no zeros if they are not finite; so such a tile, unless the
-// TMA unit fills in zeros at the tensor's end, comes in on a barrier of its own and its
-// rows behind the segment become zeros before the products may have it.
+// Maps with boxes of 16 rows and of one row, for a ragged tile.
+struct RowMaps {
+  CUtensorMap rows16, row1;
+};
+struct RaggedMaps {
+  RowMaps q, k, v, dout;
+};
+
+// A tile of 128 rows of which the segment has the first `valid` (1 .. 127): the others
+// become zeros, as boxes behind the tensor's last row `rows`, instead of the next
+// sequence's rows (or anything, behind the last one), whose values times probabilities of
+// zero would be no zeros if they were not finite.  Each part in boxes of 16 rows, the last
+// one over the end of the one before it (the same bytes), or of one row if it is shorter.
+// Nine boxes mostly, for each 64 columns.
+template <int D>
+__device__ __forceinline__ void load_ragged(const RowMaps& m, uint8_t* dst, uint64_t* bar, int row, int head, int valid,
+                                            int rows) {
+  auto part = [&](int first, int n, bool zeros) {
+    for (int r = 0; r < n;) {
+      const int at = first + (n < 16 ? r : min(r, n - 16));
+#pragma unroll
+      for (int blk = 0; blk < D / 64; ++blk)
+        tma_load_3d(dst + blk * 16384 + at * 128, n < 16 ? &m.row1 : &m.rows16, bar, blk * 64, zeros ? rows : row + at,
+                    head);
+      r += n < 16 ? 1 : 16;
+    }
+  };
+  part(0, valid, false);
+  part(valid, 128 - valid, true);
+}
+// The bytes that it counts on the barrier.
+template <int D>
+__device__ __forceinline__ uint32_t ragged_bytes(int valid) {
+  auto of = [](int n) { return n < 16 ? n : (n + 15) / 16 * 16; };
+  return static_cast<uint32_t>(of(valid) + of(128 - valid)) * D * 2;
+}
+
+// The producer of grouped heads.  Ragged tiles are code of their own, away from the
+// loop over the others: beside it they cost 20 to 30 of 210 us (16 x 1152 rows, 12 heads
+// of 64), though none was ragged; the loads of dO have two stages, and little time.
 template <int D>
 __device__ void bwd_producer_grouped(const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv,
-                                     const CUtensorMap* mdo, const CUtensorMap* mstats, uint8_t* sm, BwdBars& bars,
-                                     const BwdWorkGrouped& w, uint32_t* dev_err) {
+                                     const CUtensorMap* mdo, const CUtensorMap* mstats, const RaggedMaps& mr, uint8_t* sm,
+                                     BwdBars& bars, const BwdWorkGrouped& w, uint32_t* dev_err) {
   using C = BwdCfg<D>;
-  const int lane = threadIdx.x % 32;
-  if (lane == 0) {
-    tma_prefetch_desc(mq);
-    tma_prefetch_desc(mk);
-    tma_prefetch_desc(mv);
-    tma_prefetch_desc(mdo);
-    tma_prefetch_desc(mstats);
-  }
+  tma_prefetch_desc(mq);
+  tma_prefetch_desc(mk);
+  tma_prefetch_desc(mv);
+  tma_prefetch_desc(mdo);
+  tma_prefetch_desc(mstats);
   volatile int* ab = &bars.abort;
   int nkv_issued = 0, nq_issued = 0, ndo_issued = 0;
-  uint32_t tails = 0;
-  // A tile's load on its own barrier, or, ragged, through `tail`.
   auto load = [&](const CUtensorMap* m, uint8_t* dst, uint64_t* bar, int row, int head) {
+#pragma unroll
     for (int blk = 0; blk < D / 64; ++blk) tma_load_3d(dst + blk * 16384, m, bar, blk * 64, row, head);
   };
-  auto clear = [&](uint8_t* tile, int valid) {  // rows from `valid` on of a landed tile
-    const uint32_t base = smem_u32(tile);
-    for (int i = valid * 8 + lane; i < 1024; i += 32)
-      for (int blk = 0; blk < D / 64; ++blk) st_shared_v4(base + blk * 16384 + i * 16, 0u, 0u, 0u, 0u);
-  };
-  auto landed = [&]() -> bool { return __all_sync(0xffffffffu, mbar_wait(&bars.tail, (tails++) & 1, ab, dev_err)); };
-  auto hand_over = [&](uint64_t* bar) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-  };
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, dev_err));
+  // The query tile that is the t-th of all, Q with its statistics and dO; `valid` rows of it if it is ragged.
+  auto query_tile = [&](auto is_ragged, int t, const BwdUnitGrouped& un, int qi, int head, int valid) -> bool {
+    constexpr bool kRagged = decltype(is_ragged)::value;
+    const int qs = t % C::kQStages, ds = t % C::kDOStages, row = un.row0 + qi * 128;
+    uint8_t *q = sm + C::kOffQ + qs * C::kTile, *dout = sm + C::kOffDO + ds * C::kTile;
+    if (t >= C::kQStages && !mbar_wait(&bars.q_empty[qs], ((t / C::kQStages) - 1) & 1, ab, dev_err)) return false;
+    mbar_arrive_expect_tx(&bars.q_full[qs], (kRagged ? ragged_bytes<D>(valid) : C::kTile) + C::kStatsChunk);
+    tma_load_3d(sm + C::kOffStats + qs * C::kStatsChunk, mstats, &bars.q_full[qs], 0, un.prow0 + qi * 128, head);
+    if constexpr (kRagged) load_ragged<D>(mr.q, q, &bars.q_full[qs], row, head, valid, w.seg.rows);
+    else load(mq, q, &bars.q_full[qs], row, head);
+    ++nq_issued;
+    if (t >= C::kDOStages && !mbar_wait(&bars.do_empty[ds], ((t / C::kDOStages) - 1) & 1, ab, dev_err)) return false;
+    mbar_arrive_expect_tx(&bars.do_full[ds], kRagged ? ragged_bytes<D>(valid) : C::kTile);
+    if constexpr (kRagged) load_ragged<D>(mr.dout, dout, &bars.do_full[ds], row, head, valid, w.seg.rows);
+    else load(mdo, dout, &bars.do_full[ds], row, head);
+    ++ndo_issued;
+    return true;
   };
   bool ok = true;
-  int tb = 0;  // query tiles of the previous units
+  int t = 0;
   for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<true>(u, ++ui)) {
     const BwdUnitGrouped un = w.unit(u);
-    const int kv0 = un.kv0();
-    const int b = ui % C::kKVBufs;
-    const int ragged = un.end < w.seg.rows ? (un.end - un.row0) % 128 : 0;  // rows of such a last tile
-    if (ui >= C::kKVBufs && !(ok = wait(&bars.kv_empty[b], ((ui / C::kKVBufs) - 1) & 1))) break;
-    const bool kv_ragged = ragged && un.j == un.nkt - 1;
-    if (lane == 0) {
-      uint64_t* bar = kv_ragged ? &bars.tail : &bars.kv_full[b];
-      mbar_arrive_expect_tx(bar, 2u * C::kTile);
-      load(mk, sm + C::off_k(b), bar, kv0, un.bh);
-      load(mv, sm + C::off_v(b), bar, kv0, un.bh);
-    }
-    if (kv_ragged) {
-      if (!(ok = landed())) break;
-      clear(sm + C::off_k(b), ragged);
-      clear(sm + C::off_v(b), ragged);
-      hand_over(&bars.kv_full[b]);
+    const int kv0 = un.kv0(), b = ui % C::kKVBufs;
+    const int ragged = un.ragged(w.seg.rows);
+    if (ui >= C::kKVBufs && !(ok = mbar_wait(&bars.kv_empty[b], ((ui / C::kKVBufs) - 1) & 1, ab, dev_err))) break;
+    if (ragged && un.j == un.nkt - 1) {
+      mbar_arrive_expect_tx(&bars.kv_full[b], 2u * ragged_bytes<D>(ragged));
+      load_ragged<D>(mr.k, sm + C::off_k(b), &bars.kv_full[b], kv0, un.bh, ragged, w.seg.rows);
+      load_ragged<D>(mr.v, sm + C::off_v(b), &bars.kv_full[b], kv0, un.bh, ragged, w.seg.rows);
+    } else {
+      mbar_arrive_expect_tx(&bars.kv_full[b], 2u * C::kTile);
+      load(mk, sm + C::off_k(b), &bars.kv_full[b], kv0, un.bh);
+      load(mv, sm + C::off_v(b), &bars.kv_full[b], kv0, un.bh);
     }
     ++nkv_issued;
-    for (int i = 0; i < un.n; ++i) {
-      const int t = tb + i;
-      const int qs = t % C::kQStages, ds = t % C::kDOStages;
-      const int qi = un.query_tile(i), head = un.head(i);
-      const bool q_ragged = ragged && qi == un.nkt - 1;
-      if (t >= C::kQStages && !(ok = wait(&bars.q_empty[qs], ((t / C::kQStages) - 1) & 1))) break;
-      uint8_t* q = sm + C::kOffQ + qs * C::kTile;
-      if (lane == 0) {
-        uint64_t* bar = q_ragged ? &bars.tail : &bars.q_full[qs];
-        mbar_arrive_expect_tx(bar, C::kTile + C::kStatsChunk);
-        tma_load_3d(sm + C::kOffStats + qs * C::kStatsChunk, mstats, bar, 0, un.prow0 + qi * 128, head);
-        load(mq, q, bar, un.row0 + qi * 128, head);
+    const int r_ragged = ragged ? un.visit_of_last() : un.per_head;  // the ragged tile's place among a head's
+    for (int head = un.h0; ok && head < un.h0 + w.group; ++head)
+      for (int r = 0; ok && r < un.per_head;) {
+        const int stop = r <= r_ragged ? r_ragged : un.per_head;
+        for (; ok && r < stop; ++r, ++t) ok = query_tile(std::false_type(), t, un, un.query_tile(r), head, 128);
+        if (ok && r < un.per_head) ok = query_tile(std::true_type(), t++, un, un.query_tile(r++), head, ragged);
       }
-      if (q_ragged) {
-        if (!(ok = landed())) break;
-        clear(q, ragged);
-        hand_over(&bars.q_full[qs]);
-      }
-      ++nq_issued;
-      if (t >= C::kDOStages && !(ok = wait(&bars.do_empty[ds], ((t / C::kDOStages) - 1) & 1))) break;
-      uint8_t* dout = sm + C::kOffDO + ds * C::kTile;
-      if (lane == 0) {
-        uint64_t* bar = q_ragged ? &bars.tail : &bars.do_full[ds];
-        mbar_arrive_expect_tx(bar, C::kTile);
-        load(mdo, dout, bar, un.row0 + qi * 128, head);
-      }
-      if (q_ragged) {
-        if (!(ok = landed())) break;
-        clear(dout, ragged);
-        hand_over(&bars.do_full[ds]);
-      }
-      ++ndo_issued;
-    }
-    tb += un.n;
   }
-  __syncwarp();
-  if (*ab && lane == 0) {
+  if (*ab) {
     // Aborted: let the copies already in flight land before the CTA exits.
-    if (tails > 0) mbar_wait_drain(&bars.tail, (tails - 1) & 1);
     auto drain = [](int issued, int slots, uint64_t* bar) {
       drain_ring(issued, slots, true, [&](int slot, uint32_t parity) { mbar_wait_drain(&bar[slot], parity); });
     };
@@ -800,15 +810,6 @@ __device__ void bwd_mma(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& w, u
   mbar_wait_drain(&bars.drain[0], 0);
 }
 
-// Of 2 N values packed in pairs, those before `first` become zeros (whatever they
-// are: a masked product with a value that is not finite is no zero by itself).
-template <int N>
-__device__ __forceinline__ void only_from(int first, uint32_t (&x)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (2 * i < first) x[i] = 2 * i + 1 < first ? 0u : x[i] & 0xFFFF0000u;
-}
-
 // Key-row threads of one compute group (query columns 64g .. 64g+63).
 template <int D, class W>
 __device__ void bwd_compute(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, const W& w, float scale,
@@ -826,15 +827,13 @@ __device__ void bwd_compute(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, co
   volatile int* ab = &bars.abort;
 
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
-    const auto un = w.unit(u);
+  for (int u = blockIdx.x, ui = 0; u < w.units; u += gridDim.x, ++ui) {
+    const BwdUnit un = w.unit(u);
     const bool key_live = un.kv0() + kr < un.end;
     const int t0 = tb;
-    tb += un.tiles();
-    for (int i = 0; i < un.tiles(); ++i) {
+    tb += un.nkt;
+    for (int i = 0; i < un.nkt; ++i) {
       const int t = t0 + i;
-      bool diagonal = false;
-      if constexpr (W::kGrouped) diagonal = un.diagonal(i);
       bool ok = mbar_wait(&bars.s_full, t & 1, ab, dev_err);
       if (!__all_sync(0xffffffffu, ok)) return;
       tc_fence_after();
@@ -870,9 +869,6 @@ __device__ void bwd_compute(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, co
           for (int e = 0; e < 32; e += 2) pp[(c * 32 + e) / 2] = 0u;
         }
       }
-      if constexpr (W::kGrouped) {
-        if (diagonal) only_from<32>(kr - 64 * g, pp);
-      }
       if (C::kSplitIssuers && t > 0) {
         // dV(t-1) must be done reading P^T(t-1) before it is overwritten;
         // waited for after all the exponentials, so that they overlap dV(t-1).
@@ -903,9 +899,6 @@ __device__ void bwd_compute(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, co
           for (int e = 0; e < 32; e += 2)
             dsw[c][e / 2] = bf16x2_mul(pp[(c * 32 + e) / 2], pack_bf16x2(__uint_as_float(dpall[c][e]),
                                                                           __uint_as_float(dpall[c][e + 1])));
-          if constexpr (W::kGrouped) {
-            if (diagonal) only_from<16>(kr - 64 * g - 32 * c, dsw[c]);
-          }
           // d = 64: dS^T(t) also goes over this group's dP^T(t) columns
           // (packed like P^T), where dK(t) reads it; dP(t+1) is issued once
           // dK(t) is done.
@@ -928,6 +921,138 @@ __device__ void bwd_compute(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, co
       tc_fence_before();
       fence_proxy_async_smem();
       mbar_arrive(&bars.ds_ready);
+    }
+  }
+}
+
+// Of 32 values packed in pairs, those before `first` become zeros (whatever they are: a
+// masked product with a value that is not finite is no zero by itself).  Most warps have
+// none or only whole chunks to clear.
+__device__ __forceinline__ void only_from(int first, uint32_t* x) {
+  if (!__any_sync(0xffffffffu, first > 0)) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    // 16 bits a value; shl gives 0 from 32 on.
+    const int bits = max(16 * first - 32 * i, 0);
+    uint32_t keep;
+    asm("shl.b32 %0, %1, %2;" : "=r"(keep) : "r"(0xFFFFFFFFu), "r"(bits));
+    x[i] &= keep;
+  }
+}
+
+// The same for grouped heads.  P stays in fp32 for dS = P (dP - D), which then rounds
+// once (bf16 values of P and of dP - D and their bf16 product, as above, leave dq and dk
+// with 1.4 times the error).  A causal unit's diagonal tiles are code of their own:
+// their masks beside the others' arithmetic, though not executed there, cost 45 of 245 us
+// (16 x 1101 rows, 12 heads of 64): this loop is bound by instruction issue.
+template <int D, class W>
+__device__ void bwd_compute_grouped(uint8_t* sm, BwdBars& bars, uint32_t tmem, int g, const W& w, float scale,
+                                    uint32_t* dev_err) {
+  using C = BwdCfg<D>;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int kr = (warp & 3) * 32 + lane;  // key row in the tile == TMEM lane
+  const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t tS = tmem + lane_base + C::kColS + 64 * g;
+  const uint32_t tP = C::kSplitIssuers ? tmem + lane_base + C::kColP + 32 * g : tS;
+  const uint32_t tDP = tmem + lane_base + C::kColDP + 64 * g;
+  const uint32_t swz = static_cast<uint32_t>(kr & 7);
+  const uint32_t ds_row = smem_u32(sm + C::kOffDS) + g * 16384 + kr * 128;
+  static_assert(C::kDSBufs == 1, "one dS^T tile");
+  volatile int* ab = &bars.abort;
+  uint64_t sc2 = 0;  // s log2e
+
+  auto tile = [&](int t, auto diag) -> bool {
+    constexpr bool kDiagonal = decltype(diag)::value;
+    bool ok = mbar_wait(&bars.s_full, t & 1, ab, dev_err);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc_fence_after();
+    uint64_t p2[32];  // P^T in fp32 pairs
+    {
+      uint32_t s[2][32];
+      tmem_ld32(tS, s[0]);
+      tmem_ld32(tS + 32, s[1]);
+      tmem_wait_ld();
+      if (C::kSplitIssuers) {  // S^T is in registers: S(t+1) may overwrite it
+        tc_fence_before();
+        mbar_arrive(&bars.s_free);
+      }
+      uint32_t pp[32];
+#pragma unroll
+      for (int e = 0; e < 64; e += 2) {
+        float x0, x1;
+        f2_split(f2_mul(f2_make(__uint_as_float(s[e / 32][e % 32]), __uint_as_float(s[e / 32][e % 32 + 1])), sc2), x0,
+                 x1);
+        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+        p2[e / 2] = f2_make(p0, p1);
+        pp[e / 2] = pack_bf16x2(p0, p1);
+      }
+      if constexpr (kDiagonal) {
+        only_from(kr - 64 * g, pp);
+        only_from(kr - 64 * g - 32, pp + 16);
+      }
+      if (C::kSplitIssuers && t > 0) {
+        ok = mbar_wait(&bars.dv_done, (t - 1) & 1, ab, dev_err);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_st16(tP + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pp[c * 16]));
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(&bars.p_ready);
+
+    ok = mbar_wait(&bars.dp_full, t & 1, ab, dev_err);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc_fence_after();
+    uint32_t dsw[2][16];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t dp[32];
+      tmem_ld32(tDP + c * 32, dp);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        float x0, x1;
+        f2_split(f2_mul(p2[(c * 32 + e) / 2], f2_make(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]))), x0, x1);
+        dsw[c][e / 2] = pack_bf16x2(x0, x1);
+      }
+      if constexpr (kDiagonal) only_from(kr - 64 * g - 32 * c, dsw[c]);
+      if (C::kSplitIssuers) tmem_st16(tDP + c * 16, dsw[c]);
+    }
+    if (t > 0) {
+      ok = mbar_wait(&bars.ds_free[0], (t - 1) & 1, ab, dev_err);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int e = 0; e < 32; e += 8)
+        st_shared_v4(ds_row + ((static_cast<uint32_t>((c * 32 + e) >> 3) ^ swz) << 4), dsw[c][e / 2], dsw[c][e / 2 + 1],
+                     dsw[c][e / 2 + 2], dsw[c][e / 2 + 3]);
+    if (C::kSplitIssuers) tmem_wait_st();
+    tc_fence_before();
+    fence_proxy_async_smem();
+    mbar_arrive(&bars.ds_ready);
+    return true;
+  };
+
+  int t = 0;
+  for (int u = blockIdx.x, ui = 0; u < w.units; u = next_unit<true>(u, ++ui)) {
+    const BwdUnitGrouped un = w.unit(u);
+    // For a key behind the segment, whose rows in the tiles are zeros, 0: P is 1 and dS = -D
+    // there, which nothing but the products with those zeros sees (and dk and dv of the
+    // key, which are not stored).
+    const float sc = un.kv0() + kr < un.end ? scale * kLog2e : 0.f;
+    sc2 = f2_make(sc, sc);
+    for (int h = 0; h < w.group; ++h) {
+      int r = 0;
+      if (un.causal) {
+        if (!tile(t++, std::true_type())) return;
+        r = 1;
+      }
+      for (; r < un.per_head; ++r)
+        if (!tile(t++, std::false_type())) return;
     }
   }
 }
@@ -997,9 +1122,25 @@ __device__ void bwd_drain64(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& 
     const auto un = w.unit(u);
     const int t0 = tb;
     tb += un.tiles();
+    int vh = 0, vr = 0;  // grouped: query head of the kv head's, query tile of the head's visited ones
     for (int i = 0; i < un.tiles(); ++i) {
       const int t = t0 + i;
-      const int qt = un.query_tile(i), rank = un.rank(i), head = un.head(i);
+      int qt, rank, head, last_rank;  // the query tile, this contribution's place among the tile's and the last one's
+      if constexpr (W::kGrouped) {
+        qt = un.query_tile(vr);
+        head = un.h0 + vh;
+        rank = un.j;
+        last_rank = un.causal ? qt : un.nkt - 1;
+        if (++vr == un.per_head) {
+          vr = 0;
+          ++vh;
+        }
+      } else {
+        qt = un.query_tile(i);
+        head = un.bh;
+        rank = un.rank(i);
+        last_rank = un.nkt - 1;
+      }
       uint32_t* cnt = counters + static_cast<size_t>(head) * tiles_per_head + un.prow0 / 128 + qt;
       // Ordered modes: the counter read ahead (its latency overlaps the wait for dQ).
       const uint32_t seen = kOrd && leader && rank > 0 ? ld_acquire_gpu(cnt) : 0u;
@@ -1012,7 +1153,7 @@ __device__ void bwd_drain64(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& 
       tmem_ld32(tQ + 32, *reinterpret_cast<uint32_t(*)[32]>(a + 32));
       tmem_wait_ld();
       if constexpr (W::kGrouped) {
-        if (un.row0 + qt * 128 + r128 >= un.end) zero_all(a);
+        if (qt == un.nkt - 1 && un.row0 + qt * 128 + r128 >= un.end) zero_all(a);
       }
       tc_fence_before();
       mbar_arrive(&bars.dq_free);
@@ -1045,7 +1186,7 @@ __device__ void bwd_drain64(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& 
         }
         bulk_commit_group();
         if constexpr (kOrd) {
-          if (rank != un.last_rank(i)) {
+          if (rank != last_rank) {
             pend = cnt;
             if (i == un.tiles() - 1) complete_previous();
           }
@@ -1152,9 +1293,25 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
     const int bh = un.bh;
     const int t0 = tb;
     tb += un.tiles();
+    int vh = 0, vr = 0;  // grouped: query head of the kv head's, query tile of the head's visited ones
     for (int i = 0; i < un.tiles(); ++i) {
       const int t = t0 + i;
-      const int qt = un.query_tile(i), rank = un.rank(i), head = un.head(i);
+      int qt, rank, head, last_rank;  // the query tile, this contribution's place among the tile's and the last one's
+      if constexpr (W::kGrouped) {
+        qt = un.query_tile(vr);
+        head = un.h0 + vh;
+        rank = un.j;
+        last_rank = un.causal ? qt : un.nkt - 1;
+        if (++vr == un.per_head) {
+          vr = 0;
+          ++vh;
+        }
+      } else {
+        qt = un.query_tile(i);
+        head = un.bh;
+        rank = un.rank(i);
+        last_rank = un.nkt - 1;
+      }
       uint32_t* cnt = counters + static_cast<size_t>(head) * tiles_per_head + un.prow0 / 128 + qt;
       // Ordered modes: the counter read ahead (its latency overlaps the wait for dQ).
       const uint32_t seen = kOrd && leader && rank > 0 ? ld_acquire_gpu(cnt) : 0u;
@@ -1169,7 +1326,7 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
       tc_fence_after();
       // Columns 32-95 into H1 / H2, whose reduces go first: the producer
       // reloads the Q stage once they have been read.
-      const bool behind = W::kGrouped && row + r128 >= un.end;  // the segment
+      const bool behind = W::kGrouped && qt == un.nkt - 1 && row + r128 >= un.end;  // the segment
       uint32_t a[32];
       tmem_ld32(tQ + 32, a);
       tmem_wait_ld();
@@ -1233,7 +1390,7 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
         else tma_reduce_add_3d(mdq, h0, 96, row, head);
         bulk_commit_group();
         if constexpr (kOrd) {
-          if (rank != un.last_rank(i)) {
+          if (rank != last_rank) {
             pend = cnt;
             if (i == un.tiles() - 1) complete_previous();
           }
@@ -1474,6 +1631,23 @@ __device__ void bwd_epilogue_warps(uint8_t* sm, BwdBars& bars, uint32_t tmem, co
                      pack_bf16x2(__uint_as_float(a[q * 8 + 4]), __uint_as_float(a[q * 8 + 5])),
                      pack_bf16x2(__uint_as_float(a[q * 8 + 6]), __uint_as_float(a[q * 8 + 7])));
     }
+    if constexpr (W::kGrouped) {  // no norm: dk = scale times the accumulator
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t a[32];
+        tmem_ld32(tDK + c * 32, a);
+        tmem_wait_ld();
+        if (c == D / 32 - 1) {
+          tc_fence_before();
+          mbar_arrive(&bars.acc_free_k);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 o = scaled8(a, q * 8, scale);
+          st_shared_v4(chunk_addr(tile_k, r128, c * 4 + q), o.x, o.y, o.z, o.w);
+        }
+      }
+    } else {
     // dK out of TMEM into registers and its columns released at once: the
     // next unit's first dK product (and through it the next dP product)
     // waits for this read only.
@@ -1483,15 +1657,6 @@ __device__ void bwd_epilogue_warps(uint8_t* sm, BwdBars& bars, uint32_t tmem, co
     tmem_wait_ld();
     tc_fence_before();
     mbar_arrive(&bars.acc_free_k);
-    if constexpr (W::kGrouped) {  // no norm: dk = scale times the accumulator
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint4 o = scaled8(*reinterpret_cast<const uint32_t(*)[32]>(dkr + c * 32), q * 8, scale);
-          st_shared_v4(chunk_addr(tile_k, r128, c * 4 + q), o.x, o.y, o.z, o.w);
-        }
-    } else {
     ok = mbar_wait(&bars.kraw_full, ui & 1, ab, dev_err);
     if (!(ok = __all_sync(0xffffffffu, ok))) break;
     ++kraw_done;
@@ -1620,7 +1785,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     const __nv_bfloat16* __restrict__ k_raw,
                     const float* __restrict__ rk, const float* __restrict__ gk, __nv_bfloat16* __restrict__ dk,
                     __nv_bfloat16* __restrict__ dv, float* __restrict__ dqacc, uint32_t* __restrict__ counters,
-                    float* __restrict__ dgk_part, uint32_t* dev_err) {
+                    float* __restrict__ dgk_part, const __grid_constant__ typename W::Ragged ragged,
+                    uint32_t* dev_err) {
   using C = BwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) BwdBars bars;
@@ -1663,7 +1829,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(&bars.drain[0], 1);
     mbar_init(&bars.drain[1], 1);
     mbar_init(&bars.drain[2], 1);
-    mbar_init(&bars.tail, 1);
     bars.abort = 0;
     fence_mbar_init();
   }
@@ -1708,11 +1873,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tmem = bars.tmem_base;
 
   if (warp < 8) {
-    setmaxnreg_inc<D == 64 ? kRegCompute64 : kRegCompute128>();
-    bwd_compute<D>(sm, bars, tmem, warp >> 2, w, scale, dev_err);
+    setmaxnreg_inc<W::kGrouped ? kRegComputeGrouped : D == 128 ? kRegCompute128 : kRegCompute64>();
+    if constexpr (W::kGrouped) bwd_compute_grouped<D>(sm, bars, tmem, warp >> 2, w, scale, dev_err);
+    else bwd_compute<D>(sm, bars, tmem, warp >> 2, w, scale, dev_err);
   } else if constexpr (D == 64) {
     if (warp < kWarpEpi) setmaxnreg_dec<kRegDrain64>();
-    else if (warp < kWarpTma) setmaxnreg_inc<kRegEpi64>();
+    else if (warp < kWarpTma) {
+      if constexpr (W::kGrouped) setmaxnreg_dec<kRegEpiGrouped>();
+      else setmaxnreg_inc<kRegEpi64>();
+    }
     else setmaxnreg_dec<kRegMma64>();
     if (warp < kWarpEpi) {
       bwd_drain64<D, kOrd>(sm, bars, tmem, w, &map_dq, counters, dev_err);
@@ -1720,7 +1889,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bwd_epilogue_warps<D>(sm, bars, tmem, w, scale, &map_kraw, &map_dk, &map_dv, rk, dk, dv, dgk_part, dev_err);
     } else if (warp == kWarpTma) {
       if constexpr (W::kGrouped) {
-        bwd_producer_grouped<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, sm, bars, w, dev_err);
+        if (lane == 0) bwd_producer_grouped<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, ragged, sm, bars, w, dev_err);
       } else {
         if (lane == 0) bwd_producer<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, sm, bars, w, dev_err);
       }
@@ -1737,13 +1906,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // warps keep their launch count.
     static_assert(kRegMma128 == kRegLaunchMin, "d = 128: the TMA / issuer warps keep their launch count");
     if (warp < kWarpEpi) {
-      setmaxnreg_inc<kRegDrain128>();
+      if constexpr (W::kGrouped) setmaxnreg_dec<kRegDrain128Grouped>();
+      else setmaxnreg_inc<kRegDrain128>();
       bwd_drain128<D, kOrd>(sm, bars, tmem, w, scale, &map_dq, counters, k_raw, rk, dk, dv, dgk_part, dev_err);
     } else if (warp < kWarpTma) {
       setmaxnreg_dec<kRegIdle128>();
     } else if (warp == kWarpTma) {
       if constexpr (W::kGrouped) {
-        bwd_producer_grouped<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, sm, bars, w, dev_err);
+        if (lane == 0) bwd_producer_grouped<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, ragged, sm, bars, w, dev_err);
       } else {
         if (lane == 0) bwd_producer<D>(&map_q, &map_k, &map_v, &map_do, &map_stats, sm, bars, w, dev_err);
       }
@@ -1764,7 +1934,8 @@ cudaError_t launch_bwd_w(const W& w, int grid, const CUtensorMap& mq, const CUte
                          const CUtensorMap& mdo, const CUtensorMap& mstats, const CUtensorMap& mdq,
                          const CUtensorMap& mkraw, const CUtensorMap& mdk, const CUtensorMap& mdv, float scale,
                          const uint16_t* k_raw, const float* rk, const float* gk, uint16_t* dk, uint16_t* dv,
-                         float* dqacc, uint32_t* counters, float* dgk_part, uint32_t* dev_err, cudaStream_t st) {
+                         float* dqacc, uint32_t* counters, float* dgk_part, uint32_t* dev_err, cudaStream_t st,
+                         const typename W::Ragged& ragged = {}) {
   using C = BwdCfg<D>;
   static_assert(C::kDynSmem + static_cast<int>(sizeof(BwdBars)) <= 232448, "shared memory budget");
   auto kernel = attn_bwd_kernel<D, W, kOrd>;
@@ -1779,7 +1950,7 @@ cudaError_t launch_bwd_w(const W& w, int grid, const CUtensorMap& mq, const CUte
   return launch_pdl(kernel, dim3(grid), dim3(kBwdThreads), C::kDynSmem, st, mq, mk, mv, mdo, mstats, mdq, mkraw, mdk, mdv, w, scale,
                     reinterpret_cast<const __nv_bfloat16*>(k_raw), rk, gk,
                     reinterpret_cast<__nv_bfloat16*>(dk), reinterpret_cast<__nv_bfloat16*>(dv), dqacc, counters,
-                    dgk_part, dev_err);
+                    dgk_part, ragged, dev_err);
 }
 
 // The dQ order and grid of a launch.  Arrival order unless the deterministic
@@ -1906,11 +2077,20 @@ cudaError_t launch_attn_bwd_grouped(const GroupedShape& s, const uint16_t* q, co
   w.seg.rows = s.T;
   w.seg.prows = s.seg.prows;
   w.units = s.Hk * w.order.make(s, kTileN);
+  RaggedMaps mr;
+  auto rows = [&](RowMaps& m, const uint16_t* x, int heads) {
+    return encode_bhnd_map_rows(&m.rows16, x, heads, s.T, s.d, 16) && encode_bhnd_map_rows(&m.row1, x, heads, s.T, s.d, 1);
+  };
+  // (Behind the tensor's end the TMA unit fills in zeros.)
+  bool ragged = false;
+  for (int i = 0; i < w.order.n; ++i) ragged |= w.order.len[i] % 128 != 0 && w.order.start[i] + w.order.len[i] < s.T;
+  if (ragged && (!rows(mr.q, q, s.Hq) || !rows(mr.k, k, s.Hk) || !rows(mr.v, v, s.Hk) || !rows(mr.dout, dout, s.Hq)))
+    return cudaErrorInvalidValue;
   const int sms = device_sm_count(), grid = w.units < sms ? w.units : sms;
   auto launch = s.d == 64 ? (s.deterministic ? launch_bwd_w<64, true, BwdWorkGrouped> : launch_bwd_w<64, false, BwdWorkGrouped>)
                           : (s.deterministic ? launch_bwd_w<128, true, BwdWorkGrouped> : launch_bwd_w<128, false, BwdWorkGrouped>);
   return launch(w, grid, mq, mk, mv, mdo, mstats, mdq, mk, mdk, mdv, s.scale, k, nullptr, nullptr, dk, dv, dqacc,
-                counters, nullptr, dev_err, st);
+                counters, nullptr, dev_err, st, mr);
 }
 
 // One dgk partial per CTA.

@@ -179,11 +179,9 @@ struct FwdWorkGrouped {
   GroupedOrder order;
   __device__ __forceinline__ FwdUnit unit(int u) const {
     FwdUnit r;
-    const int k = u / heads;
-    r.bh = u - k * heads;
-    r.kvh = r.bh / group;
     int s, level;
-    order.at(k, causal, &s, &level);
+    order.unit(u, heads, causal, &s, &r.bh, &level);
+    r.kvh = r.bh / group;
     r.kvb = order.start[s];
     r.end = r.kvb + order.len[s];
     r.q0 = r.kvb + level * 2 * kTileM;

@@ -20,6 +20,7 @@ struct GroupedOrder {
   int prow[kMaxSegments];  // their first rows in the padded scratch (SegTable)
   int first[kMaxSegments + 1];   // causal: blocks before the levels that just segments 0 .. i have; else before segment i
   int blocks[kMaxSegments];  // of segment i
+  int pre[kMaxSegments];
 
   // Segment and level of block k.
   __host__ __device__ __forceinline__ void at(int k, bool causal, int* seg, int* level) const {
@@ -39,6 +40,29 @@ struct GroupedOrder {
       *level = off;
     }
   }
+#ifndef ORDER
+#define ORDER 1
+#endif
+  __host__ __device__ __forceinline__ void unit(int u, int heads, bool causal, int* seg, int* head, int* level) const {
+    if (ORDER == 1) {
+      const int k = u / heads;
+      *head = u - k * heads;
+      at(k, causal, seg, level);
+      return;
+    }
+    // segments, heads, levels
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] * heads <= u) lo = mid;
+      else hi = mid;
+    }
+    const int off = u - pre[lo] * heads;
+    *seg = lo;
+    *head = off / blocks[lo];
+    const int l = off - *head * blocks[lo];
+    *level = causal ? blocks[lo] - 1 - l : l;
+  }
   // From the segments of s, in blocks of that many rows; returns how many blocks.
   int make(const GroupedShape& s, int block) {
     n = s.seg.n;
@@ -52,6 +76,8 @@ struct GroupedOrder {
       prow[i] = s.seg.pcu[by[i]];
       blocks[i] = (len[i] + block - 1) / block;
     }
+    pre[0] = 0;
+    for (int i = 1; i < n; ++i) pre[i] = pre[i - 1] + blocks[i - 1];
     first[0] = 0;
     for (int i = 0; i < n; ++i)
       first[i + 1] = first[i] + (s.causal ? (blocks[i] - (i + 1 < n ? blocks[i + 1] : 0)) * (i + 1) : blocks[i]);
@@ -65,7 +91,11 @@ template <bool kGrouped>
 __device__ __forceinline__ int next_unit(int u, int ui) {
   if constexpr (kGrouped) {
     const int grid = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-    return ui * grid + (ui & 1 ? grid - 1 - c : c);
+#ifndef SNAKE
+#define SNAKE 1
+#endif
+    if (SNAKE) return ui * grid + (ui & 1 ? grid - 1 - c : c);
+    return u + grid;
   } else {
     return u + static_cast<int>(gridDim.x);
   }

@@ -71,12 +71,12 @@ struct LnArgs {
   float *mean, *r;  // or null
 };
 
-// At least four blocks an SM (two of 16 warps), as the rows' loads need them: 32768 x
+// At least four blocks an SM (five of rows up to 512, two of 16 warps), as the rows' loads need them: 32768 x
 // 4096 157 us, as the compiler has it 168, five 181.  (Two rows a warp side by side,
 // with the gains and biases that they share loaded once: 17616 x 768 20.0 instead of
 // 19.7 us, 17616 x 1024 28.9 instead of 26.1.)
 template <int V, int G>
-__global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 2 : 4) layer_norm_kernel(const LnArgs a) {
+__global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 2 : V > 2 ? 4 : 5) layer_norm_kernel(const LnArgs a) {
   __shared__ float2 red[2][kMaxWarps];
   griddep_launch_dependents();
   griddep_wait();
