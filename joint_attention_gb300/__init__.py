@@ -288,11 +288,14 @@ def layer_norm_backward(dy, h, mean, r, g, dh=None, bias: bool = True, stream=No
 
 def _rope_sizes(q, k, pos):
     """Whether the positions are each item's own, and B, Hq, Hk, N, d of [B, H, N, d] or packed [H, T, d] tensors."""
-    if q.dim() not in (3, 4) or k.dim() != q.dim() or q.shape[-2:] != k.shape[-2:] or q.shape[:-3] != k.shape[:-3]:
+    qs, ks = q.shape, k.shape
+    if len(qs) == 3 == len(ks):
+        qs, ks = (1, *qs), (1, *ks)
+    if len(qs) != 4 or len(ks) != 4 or (ks[0], ks[2], ks[3]) != (qs[0], qs[2], qs[3]):
         raise ValueError(f"q and k: expected [B, H, N, d] or [H, T, d] with heads of their own, got {tuple(q.shape)} "
                          f"and {tuple(k.shape)}")
-    B = q.shape[0] if q.dim() == 4 else 1
-    return pos.dim() == 3, B, q.shape[-3], k.shape[-3], q.shape[-2], q.shape[-1]
+    B, Hq, N, d = qs
+    return pos.dim() == 3, B, Hq, ks[1], N, d
 
 
 def rope(q, k, pos, freq, pairs, gq=None, gk=None, interleaved: bool = False, eps: float = 1e-6, stream=None):
@@ -304,9 +307,9 @@ def rope(q, k, pos, freq, pairs, gq=None, gk=None, interleaved: bool = False, ep
 
     with _outputs_on(stream, q, k, pos, freq, gq, gk):
         q_rot, k_rot = torch.empty_like(q), torch.empty_like(k)
-    per_item, *sizes = _rope_sizes(q, k, pos)
-    jattn_rope(q, k, gq, gk, pos, freq, pairs, per_item, interleaved, *sizes, eps, q_rot.data_ptr(), k_rot.data_ptr(),
-               stream)
+    per_item, B, Hq, Hk, N, d = _rope_sizes(q, k, pos)
+    jattn_rope(q, k, gq, gk, pos, freq, pairs, per_item, interleaved, B, Hq, Hk, N, d, eps, q_rot.data_ptr(),
+               k_rot.data_ptr(), stream)
     return q_rot, k_rot
 
 

@@ -578,10 +578,21 @@ def jattn_layer_norm_bwd(dy, dh, h, mean, r, g, items: int, T: int, C: int, dx, 
     return rc
 
 
+@functools.lru_cache(maxsize=1024)  # arrays that the library reads during a call, made once for equal values
+def _ints(vals: tuple):
+    return (ctypes.c_int * len(vals))(*vals)
+
+
 def _pairs_array(pairs):
     """Host int array (ctypes) of the axes' pairs, the count of axes and of pairs."""
-    vals = [int(x) for x in pairs]
-    return (ctypes.c_int * len(vals))(*vals), len(vals), sum(vals)
+    vals = tuple(map(int, pairs))
+    return _ints(vals), len(vals), sum(vals)
+
+
+def _offsets(cu_seqlens):
+    """Host int array (ctypes) of the sequence offsets, and the count of sequences."""
+    vals = tuple(map(int, cu_seqlens))
+    return _ints(vals), len(vals) - 1
 
 
 def jattn_rope(q, k, gq, gk, pos, freq, pairs, per_item: bool, interleaved: bool, B: int, Hq: int, Hk: int, N: int,
@@ -697,7 +708,7 @@ def jattn_fwd_grouped(q, k, v, cu_seqlens, Hq: int, Hk: int, T: int, d: int, cau
     import torch
 
     bf, eq, ek = torch.bfloat16, Hq * T * d, Hk * T * d
-    arr, _, n = _cu_array(cu_seqlens)
+    arr, n = _offsets(cu_seqlens)
     rc = load_library().jattn_fwd_grouped(_ptr(q, "q", bf, eq), _ptr(k, "k", bf, ek), _ptr(v, "v", bf, ek), arr, n,
                                           _size(Hq), _size(Hk), _size(T), _size(d), bool(causal), scale,
                                           _ptr(out, "out", bf, eq), _ptr(lse, "lse", torch.float32, Hq * T),
@@ -709,7 +720,7 @@ def jattn_fwd_grouped(q, k, v, cu_seqlens, Hq: int, Hk: int, T: int, d: int, cau
 
 def jattn_bwd_grouped_bytes(cu_seqlens, Hq: int, Hk: int, T: int, d: int) -> int:
     """C ABI jattn_bwd_grouped_bytes: size of the work buffer of jattn_bwd_grouped (0: it rejects the sizes)."""
-    arr, _, n = _cu_array(cu_seqlens)
+    arr, n = _offsets(cu_seqlens)
     return int(load_library().jattn_bwd_grouped_bytes(arr, n, *map(_size, (Hq, Hk, T, d))))
 
 
@@ -719,7 +730,7 @@ def jattn_bwd_grouped(q, k, v, out, lse, dout, cu_seqlens, Hq: int, Hk: int, T: 
     import torch
 
     bf, eq, ek = torch.bfloat16, Hq * T * d, Hk * T * d
-    arr, _, n = _cu_array(cu_seqlens)
+    arr, n = _offsets(cu_seqlens)
     rc = load_library().jattn_bwd_grouped(
         _ptr(q, "q", bf, eq), _ptr(k, "k", bf, ek), _ptr(v, "v", bf, ek), _ptr(out, "out", bf, eq),
         _ptr(lse, "lse", torch.float32, Hq * T), _ptr(dout, "dout", bf, eq), arr, n, _size(Hq), _size(Hk), _size(T),
