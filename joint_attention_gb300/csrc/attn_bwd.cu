@@ -207,23 +207,24 @@ struct BwdUnit {
 // each of its query heads in turn (causal: from its own rows on).  Ordered modes add
 // each query tile's contributions by ascending key tiles; the units that hold the
 // lower key tiles of a segment come first (GroupedOrder), so no wait can deadlock.
+template <bool kCausal>
 struct BwdUnitGrouped {
   int bh;        // kv head
   int h0;        // its first query head
   int per_head;  // query tiles of each
   int n;         // in all
   int j, nkt, row0, end, prow0, ord;  // as in BwdUnit
-  bool causal;   // then the first query tile of each head holds the key tile's own rows,
-                 // of which a key reaches the queries from its own on
+  // (Causal: the first query tile of each head holds the key tile's own rows, of which a
+  // key reaches the queries from its own on.)
   // The r-th query tile visited of a head.
   __device__ __forceinline__ int query_tile(int r) const {
-    if (ord == kDqAscending && !causal) return r;
+    if (ord == kDqAscending && !kCausal) return r;
     const int q = r + j;
     return q < nkt ? q : q - nkt;
   }
   // The r of the segment's last query tile.
   __device__ __forceinline__ int visit_of_last() const {
-    return ord == kDqAscending && !causal ? nkt - 1 : nkt - 1 - j;
+    return ord == kDqAscending && !kCausal ? nkt - 1 : nkt - 1 - j;
   }
   __device__ __forceinline__ int kv0() const { return row0 + 128 * j; }
   __device__ __forceinline__ int tiles() const { return n; }
@@ -285,31 +286,30 @@ struct BwdWork {
 };
 
 struct RaggedMaps;
+template <bool kC>
 struct BwdWorkGrouped {
-  static constexpr bool kGrouped = true;
+  static constexpr bool kGrouped = true, kCausal = kC;
   using Ragged = RaggedMaps;
   int units;
-  int heads, group;  // kv heads, and query heads of each
+  int group;  // query heads of each kv head
   int ord;
-  bool causal;
   struct {
     int rows, prows;
   } seg;
-  GroupedOrder order;
-  __device__ __forceinline__ BwdUnitGrouped unit(int u) const {
-    BwdUnitGrouped r;
+  GroupedOrder<kC, true> order;
+  __device__ __forceinline__ BwdUnitGrouped<kC> unit(int u) const {
+    BwdUnitGrouped<kC> r;
     int s, level;
-    order.unit(u, heads, causal, &s, &r.bh, &level);
+    order.unit(u, &s, &r.bh, &level);
     r.h0 = r.bh * group;
     r.nkt = order.blocks[s];
-    r.j = causal ? r.nkt - 1 - level : level;
-    r.per_head = causal ? level + 1 : r.nkt;
+    r.j = kC ? r.nkt - 1 - level : level;
+    r.per_head = kC ? level + 1 : r.nkt;
     r.n = r.per_head * group;
     r.row0 = order.start[s];
     r.end = r.row0 + order.len[s];
     r.prow0 = order.prow[s];
     r.ord = ord;
-    r.causal = causal;
     return r;
   }
 };
@@ -356,7 +356,7 @@ __device__ void bwd_producer(const CUtensorMap* mq, const CUtensorMap* mk, const
   int nkv_issued = 0, nq_issued = 0, ndo_issued = 0;
   bool ok = true;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const auto un = w.unit(u);
     const int bh = un.bh, kv0 = un.kv0();
     const int b = ui % C::kKVBufs;
@@ -440,10 +440,10 @@ __device__ __forceinline__ uint32_t ragged_bytes(int valid) {
 // The producer of grouped heads.  Ragged tiles are code of their own, away from the
 // loop over the others: beside it they cost 20 to 30 of 210 us (16 x 1152 rows, 12 heads
 // of 64), though none was ragged; the loads of dO have two stages, and little time.
-template <int D>
+template <int D, class W>
 __device__ void bwd_producer_grouped(const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv,
                                      const CUtensorMap* mdo, const CUtensorMap* mstats, const RaggedMaps& mr, uint8_t* sm,
-                                     BwdBars& bars, const BwdWorkGrouped& w, uint32_t* dev_err) {
+                                     BwdBars& bars, const W& w, uint32_t* dev_err) {
   using C = BwdCfg<D>;
   tma_prefetch_desc(mq);
   tma_prefetch_desc(mk);
@@ -457,7 +457,7 @@ __device__ void bwd_producer_grouped(const CUtensorMap* mq, const CUtensorMap* m
     for (int blk = 0; blk < D / 64; ++blk) tma_load_3d(dst + blk * 16384, m, bar, blk * 64, row, head);
   };
   // The query tile that is the t-th of all, Q with its statistics and dO; `valid` rows of it if it is ragged.
-  auto query_tile = [&](auto is_ragged, int t, const BwdUnitGrouped& un, int qi, int head, int valid) -> bool {
+  auto query_tile = [&](auto is_ragged, int t, const auto& un, int qi, int head, int valid) -> bool {
     constexpr bool kRagged = decltype(is_ragged)::value;
     const int qs = t % C::kQStages, ds = t % C::kDOStages, row = un.row0 + qi * 128;
     uint8_t *q = sm + C::kOffQ + qs * C::kTile, *dout = sm + C::kOffDO + ds * C::kTile;
@@ -476,8 +476,8 @@ __device__ void bwd_producer_grouped(const CUtensorMap* mq, const CUtensorMap* m
   };
   bool ok = true;
   int t = 0;
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<true>(u, ++ui)) {
-    const BwdUnitGrouped un = w.unit(u);
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
+    const auto un = w.unit(u);
     const int kv0 = un.kv0(), b = ui % C::kKVBufs;
     const int ragged = un.ragged(w.seg.rows);
     if (ui >= C::kKVBufs && !(ok = mbar_wait(&bars.kv_empty[b], ((ui / C::kKVBufs) - 1) & 1, ab, dev_err))) break;
@@ -622,7 +622,7 @@ __device__ void bwd_mma_recompute(uint8_t* sm, BwdBars& bars, uint32_t tmem, con
   };
   bool ok = true;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const int nkt = w.unit(u).tiles();
     const int b = ui % C::kKVBufs;
     if (!(ok = mbar_wait(&bars.kv_full[b], (ui / C::kKVBufs) & 1, ab, dev_err))) break;
@@ -667,7 +667,7 @@ __device__ void bwd_mma_gradients(uint8_t* sm, BwdBars& bars, uint32_t tmem, con
   };
   bool ok = true;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const int nkt = w.unit(u).tiles();
     for (int i = 0; i < nkt; ++i) {
       const int t = tb + i;
@@ -696,7 +696,7 @@ __device__ void bwd_mma_dq(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& w
   const uint64_t mDS = sdesc_sw128(smem_u32(sm + C::kOffDS), 16384, 1024);
   bool ok = true;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const int nkt = w.unit(u).tiles();
     const int b = ui % C::kKVBufs;
     if (!(ok = mbar_wait(&bars.kv_full[b], (ui / C::kKVBufs) & 1, ab, dev_err))) break;
@@ -743,7 +743,7 @@ __device__ void bwd_mma(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& w, u
 
   bool ok = true;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const int nkt = w.unit(u).tiles();
     const int b = ui % C::kKVBufs;
     const int t0 = tb;
@@ -1038,8 +1038,8 @@ __device__ void bwd_compute_grouped(uint8_t* sm, BwdBars& bars, uint32_t tmem, i
   };
 
   int t = 0;
-  for (int u = blockIdx.x, ui = 0; u < w.units; u = next_unit<true>(u, ++ui)) {
-    const BwdUnitGrouped un = w.unit(u);
+  for (int u = blockIdx.x, ui = 0; u < w.units; u = next_unit(w, u, ++ui)) {
+    const auto un = w.unit(u);
     // For a key behind the segment, whose rows in the tiles are zeros, 0: P is 1 and dS = -D
     // there, which nothing but the products with those zeros sees (and dk and dv of the
     // key, which are not stored).
@@ -1047,7 +1047,7 @@ __device__ void bwd_compute_grouped(uint8_t* sm, BwdBars& bars, uint32_t tmem, i
     sc2 = f2_make(sc, sc);
     for (int h = 0; h < w.group; ++h) {
       int r = 0;
-      if (un.causal) {
+      if (W::kCausal) {
         if (!tile(t++, std::true_type())) return;
         r = 1;
       }
@@ -1118,7 +1118,7 @@ __device__ void bwd_drain64(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& 
   bool ok = true;
   const int tiles_per_head = w.seg.prows / 128;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const auto un = w.unit(u);
     const int t0 = tb;
     tb += un.tiles();
@@ -1130,7 +1130,7 @@ __device__ void bwd_drain64(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W& 
         qt = un.query_tile(vr);
         head = un.h0 + vh;
         rank = un.j;
-        last_rank = un.causal ? qt : un.nkt - 1;
+        last_rank = W::kCausal ? qt : un.nkt - 1;
         if (++vr == un.per_head) {
           vr = 0;
           ++vh;
@@ -1288,7 +1288,7 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
   const size_t rows = static_cast<size_t>(w.seg.rows);
   const int tiles_per_head = w.seg.prows / 128;
   int tb = 0;  // query tiles of the previous units
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const auto un = w.unit(u);
     const int bh = un.bh;
     const int t0 = tb;
@@ -1301,7 +1301,7 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
         qt = un.query_tile(vr);
         head = un.h0 + vh;
         rank = un.j;
-        last_rank = un.causal ? qt : un.nkt - 1;
+        last_rank = W::kCausal ? qt : un.nkt - 1;
         if (++vr == un.per_head) {
           vr = 0;
           ++vh;
@@ -1586,7 +1586,7 @@ __device__ void bwd_epilogue_warps(uint8_t* sm, BwdBars& bars, uint32_t tmem, co
   };
   bool ok = true;
   const size_t rows = static_cast<size_t>(w.seg.rows);
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const auto un = w.unit(u);
     const int bh = un.bh, kv0 = un.kv0();
     const int b = ui % C::kKVBufs;
@@ -2069,28 +2069,30 @@ cudaError_t launch_attn_bwd_grouped(const GroupedShape& s, const uint16_t* q, co
       !encode_stats_map(&mstats, stats, s.Hq, s.seg.prows) || !encode_dq_map(&mdq, dqacc, s.Hq, s.T, s.d) ||
       !encode_bhnd_map(&mdk, dk, s.Hk, s.T, s.d) || !encode_bhnd_map(&mdv, dv, s.Hk, s.T, s.d))
     return cudaErrorInvalidValue;
-  BwdWorkGrouped w;
-  w.heads = s.Hk;
-  w.group = s.Hq / s.Hk;
-  w.causal = s.causal;
-  w.ord = s.deterministic ? kDqAscending : kDqArrival;
-  w.seg.rows = s.T;
-  w.seg.prows = s.seg.prows;
-  w.units = s.Hk * w.order.make(s, kTileN);
   RaggedMaps mr;
   auto rows = [&](RowMaps& m, const uint16_t* x, int heads) {
     return encode_bhnd_map_rows(&m.rows16, x, heads, s.T, s.d, 16) && encode_bhnd_map_rows(&m.row1, x, heads, s.T, s.d, 1);
   };
   // (Behind the tensor's end the TMA unit fills in zeros.)
   bool ragged = false;
-  for (int i = 0; i < w.order.n; ++i) ragged |= w.order.len[i] % 128 != 0 && w.order.start[i] + w.order.len[i] < s.T;
+  for (int i = 0; i < s.seg.n; ++i) ragged |= (s.seg.cu[i + 1] - s.seg.cu[i]) % 128 != 0 && s.seg.cu[i + 1] < s.T;
   if (ragged && (!rows(mr.q, q, s.Hq) || !rows(mr.k, k, s.Hk) || !rows(mr.v, v, s.Hk) || !rows(mr.dout, dout, s.Hq)))
     return cudaErrorInvalidValue;
-  const int sms = device_sm_count(), grid = w.units < sms ? w.units : sms;
-  auto launch = s.d == 64 ? (s.deterministic ? launch_bwd_w<64, true, BwdWorkGrouped> : launch_bwd_w<64, false, BwdWorkGrouped>)
-                          : (s.deterministic ? launch_bwd_w<128, true, BwdWorkGrouped> : launch_bwd_w<128, false, BwdWorkGrouped>);
-  return launch(w, grid, mq, mk, mv, mdo, mstats, mdq, mk, mdk, mdv, s.scale, k, nullptr, nullptr, dk, dv, dqacc,
-                counters, nullptr, dev_err, st, mr);
+  auto run = [&](auto causal) {
+    using W = BwdWorkGrouped<decltype(causal)::value>;
+    W w;
+    w.group = s.Hq / s.Hk;
+    w.ord = s.deterministic ? kDqAscending : kDqArrival;
+    w.seg.rows = s.T;
+    w.seg.prows = s.seg.prows;
+    w.units = w.order.make(s, kTileN, s.Hk);
+    const int sms = device_sm_count(), grid = w.units < sms ? w.units : sms;
+    auto launch = s.d == 64 ? (s.deterministic ? launch_bwd_w<64, true, W> : launch_bwd_w<64, false, W>)
+                            : (s.deterministic ? launch_bwd_w<128, true, W> : launch_bwd_w<128, false, W>);
+    return launch(w, grid, mq, mk, mv, mdo, mstats, mdq, mk, mdk, mdv, s.scale, k, nullptr, nullptr, dk, dv, dqacc,
+                  counters, nullptr, dev_err, st, mr);
+  };
+  return s.causal ? run(std::true_type()) : run(std::false_type());
 }
 
 // One dgk partial per CTA.

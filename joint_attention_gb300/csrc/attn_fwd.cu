@@ -37,6 +37,8 @@
 // key columns past N in the last key tile are masked to -inf.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "grouped.cuh"
 #include "jattn_internal.h"
 #include "sm103_ptx.cuh"
@@ -166,32 +168,32 @@ struct FwdWork {
 };
 
 // Grouped heads, causal or not (no QK-RMSNorm, rows as they are): units in
-// GroupedOrder's order, the longest first.  A causal unit ends with the key tile
-// of its own last rows, and tile A one key tile before tile B.
+// GroupedOrder's order.  A causal unit ends with the key tile of its own last rows,
+// and tile A one key tile before tile B.
+template <bool kC>
 struct FwdWorkGrouped {
-  static constexpr bool kGrouped = true;
+  static constexpr bool kGrouped = true, kCausal = kC;
   int units;
-  int heads, group;  // query heads, and query heads of each kv head
-  bool causal;
+  DivU31 by_group;  // query heads of each kv head
   struct {
     int rows;
   } seg;
-  GroupedOrder order;
+  GroupedOrder<kC, kC> order;
   __device__ __forceinline__ FwdUnit unit(int u) const {
     FwdUnit r;
     int s, level;
-    order.unit(u, heads, causal, &s, &r.bh, &level);
-    r.kvh = r.bh / group;
+    order.unit(u, &s, &r.bh, &level);
+    r.kvh = static_cast<int>(by_group.div(static_cast<uint32_t>(r.bh)));
     r.kvb = order.start[s];
     r.end = r.kvb + order.len[s];
     r.q0 = r.kvb + level * 2 * kTileM;
     r.has_b = r.q0 + kTileM < r.end;
-    r.nkv = causal ? 2 * level + (r.has_b ? 2 : 1) : (order.len[s] + kTileN - 1) / kTileN;
+    r.nkv = kC ? 2 * level + (r.has_b ? 2 : 1) : (order.len[s] + kTileN - 1) / kTileN;
     return r;
   }
   // Key tiles of tile x of the unit.
   __device__ __forceinline__ int tiles(const FwdUnit& r, int x) const {
-    return causal && x == 0 && r.has_b ? r.nkv - 1 : r.nkv;
+    return kC && x == 0 && r.has_b ? r.nkv - 1 : r.nkv;
   }
 };
 template <class W>
@@ -234,7 +236,7 @@ __device__ void fwd_producer(const CUtensorMap* map_q, const CUtensorMap* map_k,
   volatile int* ab = &bars.abort;
   int issued = 0, q_issued = 0;
   bool ok = true;
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const FwdUnit un = w.unit(u);
     const int bh = un.bh, q0 = un.q0;
     const bool hasB = un.has_b;
@@ -314,7 +316,7 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
   // unit's epilogue.
   bool s0_issued = false;
   bool ok = true;
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const int b = ui % C::kQBufs;
     const FwdUnit uo = w.unit(u);
     const int nkv = tiles_of(w, uo, x);
@@ -344,7 +346,7 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
     s0_issued = false;
     // The next unit, if this issuer computes a tile of it (tile B may be
     // absent): its first score product goes out early (d = 64).
-    const int un = next_unit<W::kGrouped>(u, ui + 1);
+    const int un = next_unit(w, u, ui + 1);
     const bool early_next = C::kSepP && un < w.units && (x == 0 || w.unit(un).has_b);
     const int bn = (ui + 1) % C::kQBufs, g0n = g0 + 2 * uo.nkv;
     for (int j = 0; ok && j < nkv; ++j) {
@@ -516,7 +518,7 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
   uint32_t us = 0;  // tiles stored through the staging buffer (epi phases)
   int gb = 0;       // ring items of the units so far (grouped)
   bool ok = true;
-  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit<W::kGrouped>(u, ++ui)) {
+  for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
   const FwdUnit un = w.unit(u);
   gb += 2 * un.nkv;
   if (x == 1 && !un.has_b) continue;
@@ -552,8 +554,8 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
     if constexpr (W::kGrouped) {
       // The last key tile: a causal row sees the keys up to its own (which, as in
       // every row that is stored, ends before the segment does).
-      if (j + 1 == nkv && (w.causal || nvalid_last < kTileN)) {
-        const int seen = w.causal ? row + 1 : nvalid_last;
+      if (j + 1 == nkv && (W::kCausal || nvalid_last < kTileN)) {
+        const int seen = W::kCausal ? row + 1 : nvalid_last;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -668,7 +670,7 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
   tc_fence_after();
   const float inv_l = 1.f / l;
   if constexpr (W::kGrouped) {
-    if (w.causal) restore_masked<D>(tO, un, qt0, n, live, m_ref, scale_log2, w.seg.rows, raw);
+    if constexpr (W::kCausal) restore_masked<D>(tO, un, qt0, n, live, m_ref, scale_log2, w.seg.rows, raw);
   }
   if (tile_store) {
     // O rows into the query tile's staging tile (128-byte swizzle: 16-byte
@@ -868,16 +870,18 @@ cudaError_t launch_attn_fwd_grouped(const GroupedShape& s, const uint16_t* q, co
   if (!encode_bhnd_map(&mq, q, s.Hq, s.T, s.d) || !encode_bhnd_map(&mk, k, s.Hk, s.T, s.d) ||
       !encode_bhnd_map(&mv, v, s.Hk, s.T, s.d))
     return cudaErrorInvalidValue;
-  FwdWorkGrouped w;
-  w.heads = s.Hq;
-  w.group = s.Hq / s.Hk;
-  w.causal = s.causal;
-  w.seg.rows = s.T;
-  w.units = s.Hq * w.order.make(s, 2 * kTileM);
   auto bf = [](const uint16_t* p) { return reinterpret_cast<const __nv_bfloat16*>(p); };
   const FwdRaw raw{bf(q), bf(k), bf(v)};
-  auto launch = s.d == 64 ? launch_fwd_w<64, FwdWorkGrouped> : launch_fwd_w<128, FwdWorkGrouped>;
-  return launch(w, mq, mk, mv, s.Hq, s.T, s.scale, out, lse, nullptr, nullptr, dev_err, st, raw);
+  auto run = [&](auto causal) {
+    using W = FwdWorkGrouped<decltype(causal)::value>;
+    W w;
+    w.by_group = make_div_u31(static_cast<uint32_t>(s.Hq / s.Hk));
+    w.seg.rows = s.T;
+    w.units = w.order.make(s, 2 * kTileM, s.Hq);
+    auto launch = s.d == 64 ? launch_fwd_w<64, W> : launch_fwd_w<128, W>;
+    return launch(w, mq, mk, mv, s.Hq, s.T, s.scale, out, lse, nullptr, nullptr, dev_err, st, raw);
+  };
+  return s.causal ? run(std::true_type()) : run(std::false_type());
 }
 
 int attn_fwd_grid(const AttnShape& s) {

@@ -3,68 +3,71 @@
 #pragma once
 #include <algorithm>
 
+#include "fastdiv.cuh"
 #include "jattn_internal.h"
 
 namespace jattn {
 
-// The segments' blocks of `block` rows.  A block's level is its place in its segment,
-// and the work of a causal block grows by one with its level (counted from the
-// segment's start for queries, from its end for keys).  Segments are sorted by length,
-// the longest first; causal: by levels, the highest first, each with all the segments
-// that have it, so that the work falls from first to last; not causal, where all
-// blocks of a segment cost the same: by segments.
+// The segments' blocks of `block` rows, for each of `heads` heads, as units 0, 1, ...  A
+// block's level is its place in its segment, and the work of a causal block grows by one
+// with its level (counted from the segment's start for queries, from its end for keys).
+// Segments are sorted by length, the longest first.
+//
+// falling: by levels, the highest first, each with all the segments that have it and all
+// heads, so that the work falls from first to last, and the CTAs take each round's units in
+// turn from the one and the other end.  Else by segments, heads, levels, and every CTA the
+// one gridDim.x further on: CTAs side by side then share a head's keys and values.
+// Measured: forward, causal, 16 heads of 128, 16384 rows 924 us falling, 1089 else (8192
+// rows 254, 323); not causal, 4 x 2381 rows, 24 heads of 128 315 us falling, 296 else.
+// Backward, causal, 8192 rows, 590 and 966 us, not causal, 16 x 1101 rows, 12 heads of 64
+// 245 and 265: its units of one head at once would add to the same dQ.
+template <bool kCausal, bool kFalling>
 struct GroupedOrder {
+  static_assert(kFalling || !kCausal, "causal blocks of other work one after the other");
   int n;                    // segments
   int start[kMaxSegments];  // their first rows, and rows
   int len[kMaxSegments];
   int prow[kMaxSegments];  // their first rows in the padded scratch (SegTable)
-  int first[kMaxSegments + 1];   // causal: blocks before the levels that just segments 0 .. i have; else before segment i
-  int blocks[kMaxSegments];  // of segment i
-  int pre[kMaxSegments];
+  // Blocks before those of segment i; causal: before the levels that just segments 0 .. i
+  // have.
+  int first[kMaxSegments + 1];
+  int blocks[kMaxSegments];   // of segment i
+  DivU31 div[kMaxSegments];   // causal: by i + 1; else by segment i's blocks
+  DivU31 by_heads;
+  int heads;
 
-  // Segment and level of block k.
-  __host__ __device__ __forceinline__ void at(int k, bool causal, int* seg, int* level) const {
-    int lo = 0, hi = n;  // first[lo] <= k < first[hi]
+  __device__ __forceinline__ void unit(int u, int* seg, int* head, int* level) const {
+    int k = u, each = heads;
+    if (kFalling) {
+      k = static_cast<int>(by_heads.div(static_cast<uint32_t>(u)));
+      each = 1;
+      *head = u - k * heads;
+    }
+    int lo = 0, hi = n;  // first[lo] * each <= k < first[hi] * each
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (first[mid] <= k) lo = mid;
+      if (first[mid] * each <= k) lo = mid;
       else hi = mid;
     }
-    const int off = k - first[lo];
-    if (causal) {
-      const int row = off / (lo + 1);
+    const int off = k - first[lo] * each;
+    *seg = lo;
+    *level = off;
+    if (kCausal) {
+      const int row = static_cast<int>(div[lo].div(static_cast<uint32_t>(off)));
       *seg = off - row * (lo + 1);
       *level = blocks[lo] - 1 - row;
-    } else {
-      *seg = lo;
-      *level = off;
+    } else if (!kFalling) {
+      *head = static_cast<int>(div[lo].div(static_cast<uint32_t>(off)));
+      *level = off - *head * blocks[lo];
     }
   }
-#ifndef ORDER
-#define ORDER 1
-#endif
-  __host__ __device__ __forceinline__ void unit(int u, int heads, bool causal, int* seg, int* head, int* level) const {
-    if (ORDER == 1) {
-      const int k = u / heads;
-      *head = u - k * heads;
-      at(k, causal, seg, level);
-      return;
-    }
-    // segments, heads, levels
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] * heads <= u) lo = mid;
-      else hi = mid;
-    }
-    const int off = u - pre[lo] * heads;
-    *seg = lo;
-    *head = off / blocks[lo];
-    const int l = off - *head * blocks[lo];
-    *level = causal ? blocks[lo] - 1 - l : l;
+  // The unit after u of a CTA, its ui-th.
+  __device__ __forceinline__ int next(int u, int ui) const {
+    const int grid = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+    return kFalling ? ui * grid + (ui & 1 ? grid - 1 - c : c) : u + grid;
   }
-  // From the segments of s, in blocks of that many rows; returns how many blocks.
-  int make(const GroupedShape& s, int block) {
+  // From the segments of s, in blocks of that many rows, for each of the heads; returns how many units.
+  int make(const GroupedShape& s, int block, int of_heads) {
     n = s.seg.n;
     int by[kMaxSegments];
     for (int i = 0; i < n; ++i) by[i] = i;
@@ -76,29 +79,22 @@ struct GroupedOrder {
       prow[i] = s.seg.pcu[by[i]];
       blocks[i] = (len[i] + block - 1) / block;
     }
-    pre[0] = 0;
-    for (int i = 1; i < n; ++i) pre[i] = pre[i - 1] + blocks[i - 1];
     first[0] = 0;
-    for (int i = 0; i < n; ++i)
-      first[i + 1] = first[i] + (s.causal ? (blocks[i] - (i + 1 < n ? blocks[i + 1] : 0)) * (i + 1) : blocks[i]);
-    return first[n];
+    for (int i = 0; i < n; ++i) {
+      first[i + 1] = first[i] + (kCausal ? (blocks[i] - (i + 1 < n ? blocks[i + 1] : 0)) * (i + 1) : blocks[i]);
+      div[i] = make_div_u31(static_cast<uint32_t>(kCausal ? i + 1 : blocks[i]));
+    }
+    heads = of_heads;
+    by_heads = make_div_u31(static_cast<uint32_t>(heads));
+    return first[n] * heads;
   }
 };
 
-// The unit after u, a CTA's ui-th.  Where the work falls from first to last (grouped) the CTAs take
-// each round's units in turn from the one and the other end.
-template <bool kGrouped>
-__device__ __forceinline__ int next_unit(int u, int ui) {
-  if constexpr (kGrouped) {
-    const int grid = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-#ifndef SNAKE
-#define SNAKE 1
-#endif
-    if (SNAKE) return ui * grid + (ui & 1 ? grid - 1 - c : c);
-    return u + grid;
-  } else {
-    return u + static_cast<int>(gridDim.x);
-  }
+// The unit after u, a CTA's ui-th, of any work description.
+template <class W>
+__device__ __forceinline__ int next_unit(const W& w, int u, int ui) {
+  if constexpr (W::kGrouped) return w.order.next(u, ui);
+  else return u + static_cast<int>(gridDim.x);
 }
 
 }  // namespace jattn
