@@ -296,7 +296,7 @@ struct BwdWorkGrouped {
   struct {
     int rows, prows;
   } seg;
-  GroupedOrder<kC, true> order;
+  GroupedOrder<kC> order;
   __device__ __forceinline__ BwdUnitGrouped<kC> unit(int u) const {
     BwdUnitGrouped<kC> r;
     int s, level;

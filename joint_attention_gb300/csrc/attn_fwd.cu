@@ -178,7 +178,7 @@ struct FwdWorkGrouped {
   struct {
     int rows;
   } seg;
-  GroupedOrder<kC, kC> order;
+  GroupedOrder<kC> order;
   __device__ __forceinline__ FwdUnit unit(int u) const {
     FwdUnit r;
     int s, level;
@@ -568,7 +568,8 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
         if (nvalid_last < kTileN && un.end < w.seg.rows) {
           const int iv = gb - 2 * un.nkv + 2 * j + 1;  // the tile's ring item
           ok = mbar_wait(&bars.full[iv % C::kSlots], (iv / C::kSlots) & 1, ab, dev_err);
-          if (!__all_sync(0xffffffffu, ok)) break;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           if (row >= nvalid_last) {
             const uint32_t vrow = smem_u32(sm + C::kOffRing + (iv % C::kSlots) * C::kSlotBytes) + row * 128;
 #pragma unroll

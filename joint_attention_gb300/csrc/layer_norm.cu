@@ -359,16 +359,17 @@ __global__ void __launch_bounds__(32 * block_warps(L::G), L::G > 8 ? 1 : 2) laye
 }
 
 // dg and db of an item: its blocks' partial sums, 8 columns a block.
-__global__ void __launch_bounds__(256) ln_sum_kernel(const float* part, int parts, int C, int n_sums, float* dg,
-                                                     float* db) {
+__global__ void __launch_bounds__(256) ln_sum_kernel(const float* part, int items, int parts, int C, int n_sums,
+                                                     float* dg, float* db) {
   griddep_launch_dependents();
   griddep_wait();
-  const int blocks_c = C / 8;
-  const int job = blockIdx.x / blocks_c, at = (blockIdx.x - job * blocks_c) * 8;
-  const int item = job / n_sums, k = job - item * n_sums;
-  const float s = column_sum(part + (static_cast<size_t>(item) * parts * n_sums + k) * C + at, parts,
-                             static_cast<size_t>(n_sums) * C);
-  if (threadIdx.x < 8) (k == 0 ? dg : db)[static_cast<size_t>(item) * C + at + threadIdx.x] = s;
+  const int k = blockIdx.y, at = blockIdx.x * 8;
+  for (int item = blockIdx.z; item < items; item += gridDim.z) {
+    const float s = column_sum(part + (static_cast<size_t>(item) * parts * n_sums + k) * C + at, parts,
+                               static_cast<size_t>(n_sums) * C);
+    if (threadIdx.x < 8) (k == 0 ? dg : db)[static_cast<size_t>(item) * C + at + threadIdx.x] = s;
+    __syncthreads();  // column_sum's memory is free again
+  }
 }
 
 }  // namespace
@@ -435,7 +436,8 @@ cudaError_t launch_layer_norm_bwd(const LayerNormBwd& t, float* part, int parts,
 
 cudaError_t launch_layer_norm_sums(const float* part, int parts, const LayerNormBwd& t, cudaStream_t st) {
   const int n_sums = t.db ? 2 : 1;
-  return launch_pdl(ln_sum_kernel, dim3(static_cast<unsigned>(t.C / 8 * n_sums * t.items)), dim3(256), 0, st, part,
+  const unsigned z = t.items < 65535 ? static_cast<unsigned>(t.items) : 65535u;
+  return launch_pdl(ln_sum_kernel, dim3(static_cast<unsigned>(t.C / 8), n_sums, z), dim3(256), 0, st, part, t.items,
                     parts, t.C, n_sums, t.dg, t.db);
 }
 

@@ -24,6 +24,7 @@
 // contiguous in memory.  The arithmetic is in packed fp32 pairs.
 #include <cuda_bf16.h>
 
+#include "fastdiv.cuh"
 #include "jattn_internal.h"
 #include "sm103_ptx.cuh"
 #include "token_rows.cuh"
@@ -46,10 +47,12 @@ struct RopeArgs {
   const float* gain[2];  // or null
   const float* pos;      // [N, axes], or [B, N, axes]
   const float* freq;     // [P]
-  int heads[2];          // heads that share a token's positions: of its batch item, or of all items
+  int heads[2];          // heads of a token: its batch item's, or, where they share positions, all items'
   int chunks[2];         // runs of them
   int run;               // heads of a run
-  int N, tiles;          // tokens, blocks over them
+  int N;                 // tokens of an item
+  int tokens, tiles;     // tokens with positions of their own (N, or B N), blocks over them
+  DivU31 by_n;
   int axes, P;
   int pair_end[kMaxAxes];  // pairs before the end of each axis
   float sign;  // of the angles
@@ -119,24 +122,23 @@ __device__ __forceinline__ void each(F f) {
 template <int D, bool kInter>
 struct RopeThread {
   static constexpr int kLanes = D / 16, kTokens = kThreads / kLanes;
-  int t, item, run, count, token;  // tensor (0: q, 1: k); the run of heads of the item, how many
+  int t, run, count, token;        // tensor (0: q, 1: k); the run of heads, how many
   int chunk[2];                    // the thread's 16-byte chunks of a row
   bool live, rot[2];               // whether the pairs of its halves turn
   int64_t row0;                    // the first head's row
   uint64_t c[4], s[4];             // cosines and sines, once turns() has run
 
   __device__ __forceinline__ explicit RopeThread(const RopeArgs& a) {
-    const int per_item = a.chunks[0] + a.chunks[1];
-    const int tile = blockIdx.x % a.tiles, job = blockIdx.x / a.tiles;
-    item = job / per_item;
-    run = job - item * per_item;
+    run = blockIdx.x / a.tiles;
+    const int tile = blockIdx.x - run * a.tiles;
     t = run >= a.chunks[0];
     if (t) run -= a.chunks[0];
     const int heads = t ? a.heads[1] : a.heads[0], first = run * a.run;
     count = min(a.run, heads - first);
     token = tile * kTokens + threadIdx.x / kLanes;
-    live = token < a.N;
-    row0 = (static_cast<int64_t>(item) * heads + first) * a.N + token;
+    live = token < a.tokens;
+    const int item = static_cast<int>(a.by_n.div(static_cast<uint32_t>(token)));
+    row0 = (static_cast<int64_t>(item) * heads + first) * a.N + (token - item * a.N);
     const int l = threadIdx.x % kLanes;
     if (kInter) {
       chunk[0] = l;
@@ -154,7 +156,7 @@ struct RopeThread {
   __device__ __forceinline__ void turns(const RopeArgs& a) {
     const int l = threadIdx.x % kLanes;
     float at[kMaxAxes], co[8], si[8];
-    const float* pos = a.pos + (static_cast<int64_t>(item) * a.N + token) * a.axes;
+    const float* pos = a.pos + static_cast<int64_t>(token) * a.axes;
 #pragma unroll
     for (int i = 0; i < kMaxAxes; ++i) at[i] = live && i < a.axes ? __ldg(pos + i) : 0.f;
 #pragma unroll
@@ -339,10 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_norm_bwd_kernel(const __grid
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) s += sums[i][threadIdx.x];
-    // Blocks of q first: an item's runs of q, each over the tiles.
-    const int items = gridDim.x / (a.tiles * (a.chunks[0] + a.chunks[1])), tile = blockIdx.x % a.tiles;
-    const int64_t runs = static_cast<int64_t>(th.t ? items * a.chunks[0] : 0) + th.item * a.chunks[th.t] + th.run;
-    a.part[(runs * a.tiles + tile) * D + threadIdx.x] = s;
+    a.part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = s;
   }
 }
 
@@ -366,23 +365,19 @@ auto rope_of(bool inter, bool norm) {
 
 // How a call is split; all of it a function of the sizes alone.
 struct Split {
-  int items, heads[2], run, chunks[2], tiles;
-  int64_t blocks() const { return static_cast<int64_t>(items) * tiles * (chunks[0] + chunks[1]); }
+  int tokens, heads[2], run, chunks[2], tiles;
+  int64_t blocks() const { return static_cast<int64_t>(tiles) * (static_cast<int64_t>(chunks[0]) + chunks[1]); }
 };
 Split split_of(const Rope& t, int aim) {
   Split s;
-  const int tokens = kThreads / (t.d / 16);
-  s.items = t.per_item ? t.B : 1;
+  const int block = kThreads / (t.d / 16);
+  s.tokens = t.per_item ? t.B * t.N : t.N;
   s.heads[0] = t.per_item ? t.Hq : t.B * t.Hq;
   s.heads[1] = t.per_item ? t.Hk : t.B * t.Hk;
-  s.tiles = static_cast<int>((static_cast<int64_t>(t.N) + tokens - 1) / tokens);
-  const int64_t each = static_cast<int64_t>(s.items) * s.tiles * (static_cast<int64_t>(s.heads[0]) + s.heads[1]);
-  const int64_t run = each / aim;
-  // Beyond 2^31 blocks of the longest run aimed at, runs grow instead.
-  const int64_t least = each / (int64_t{1} << 30) + 1;
+  s.tiles = static_cast<int>((static_cast<int64_t>(s.tokens) + block - 1) / block);
+  const int64_t run = s.tiles * (static_cast<int64_t>(s.heads[0]) + s.heads[1]) / aim;
   s.run = static_cast<int>(run < 1 ? 1 : run > kMaxRun ? kMaxRun : run);
-  if (s.run < least) s.run = static_cast<int>(least);
-  for (int i = 0; i < 2; ++i) s.chunks[i] = (s.heads[i] + s.run - 1) / s.run;
+  for (int i = 0; i < 2; ++i) s.chunks[i] = static_cast<int>((static_cast<int64_t>(s.heads[i]) + s.run - 1) / s.run);
   return s;
 }
 
@@ -394,7 +389,9 @@ RopeArgs args_of(const Rope& t, const Split& s, float sign) {
   }
   a.run = s.run;
   a.N = t.N;
+  a.tokens = s.tokens;
   a.tiles = s.tiles;
+  a.by_n = make_div_u31(static_cast<uint32_t>(t.N));
   a.axes = t.axes;
   int end = 0;
   for (int i = 0; i < kMaxAxes; ++i) {
@@ -430,7 +427,7 @@ cudaError_t launch_rope(const Rope& t, const uint16_t* q, const uint16_t* k, uin
 
 int64_t rope_bwd_parts(const Rope& t, int64_t* of_q) {
   const Split s = split_of(t, kBlocksBwd);
-  *of_q = static_cast<int64_t>(s.items) * s.tiles * s.chunks[0];
+  *of_q = static_cast<int64_t>(s.tiles) * s.chunks[0];
   return s.blocks();
 }
 
