@@ -194,7 +194,8 @@ struct LnBwdArgs {
 // (kShared) where registers are short.  Measured, us (dy n's sums in registers / in shared
 // memory): 17616 x 512 15.6 / 16.1, x 768 27.2 / 25.1, 9524 x 2048 33.8 / 32.2, 32768 x 4096 173 / 181, 4096
 // x 8192 56 / 61; without the next row 243 for 32768 x 4096; with n and u kept from one use
-// to the other and no next row (as for RMSNorm), both sums in registers, 215.
+// to the other and no next row (as for RMSNorm), both sums in registers, 215; the next rows
+// through a ring in shared memory, which leaves less of L1 to the gains, 191.
 template <int kV, int kG, bool kA, bool kS>
 struct BwdLayout {
   static constexpr int V = kV, G = kG;

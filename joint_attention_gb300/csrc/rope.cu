@@ -267,7 +267,12 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
 
 // With gains: the rotation by -t, the backward of the RMSNorm and the block's part of
 // the gain's gradient (each thread its 16 channels over its heads, then the tokens of
-// the block in a fixed order).
+// the block in a fixed order).  The sums' registers leave none for loads ahead: these go
+// through shared memory, each thread's own 64 bytes of kRing heads (4 x 48 x 2381 rows of
+// 128, 351 MB: 54.8 us, 6.4 TB/s; rings of 2, 3 and 6 59.8, 56.0 and 57.1; the next head in
+// registers 65.3).
+constexpr int kRing = 4;
+constexpr int kRingBytes = kRing * 4 * kThreads * 16;
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, 2) rope_norm_bwd_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float sums[kThreads / 32][D];
@@ -278,40 +283,53 @@ __global__ void __launch_bounds__(kThreads, 2) rope_norm_bwd_kernel(const __grid
   Thread th(a);
   const uint4* const src[2] = {th.t ? a.src[1] : a.src[0], th.t ? a.x[1] : a.x[0]};
   uint4* dst = th.t ? a.dst[1] : a.dst[0];
-  constexpr int kRow = D / 8, kDeep = 1;
+  extern __shared__ uint4 ring[];  // [kRing][gradient, x][chunk][thread]
+  constexpr int kRow = D / 8;
   const int64_t step = static_cast<int64_t>(a.N) * kRow;
   int64_t at = th.row0 * kRow;
-  RowLoads<kDeep, 2, Thread> now, next;
-  now.load(th, src, at, step, 0);
+  auto slot = [&](int head, int k, int h) { return &ring[((head % kRing * 2 + k) * 2 + h) * kThreads + threadIdx.x]; };
+  auto load = [&](int head) {  // of the run, one group each (empty behind the last)
+    if (th.live && head < th.count) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          cp_async16(smem_u32(slot(head, k, h)), src[k] + th.row0 * kRow + head * step + th.chunk[h]);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) load(i);
   th.turns(a);
   const Pairs g = th.gains(th.t ? a.gain[1] : a.gain[0]);
   Pairs dg = {};
-  for (int h0 = 0; h0 < th.count; h0 += kDeep, at += kDeep * step) {
-    next.load(th, src, at + kDeep * step, step, h0 + kDeep);
+  for (int head = 0; head < th.count; ++head, at += step) {
+    load(head + kRing - 1);
+    cp_async_wait<kRing - 1>();
+    uint4 w[2][2];
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i) {
-      if (h0 + i >= th.count) break;  // the same in the whole block
-      Pairs v = unpack_pairs<kInter>(now.w[i][0]), n = unpack_pairs<kInter>(now.w[i][1]), u;
-      th.rotate(v);
-      each([&](int j) {
-        u.x[j] = f2_mul(v.x[j], g.x[j]);
-        u.y[j] = f2_mul(v.y[j], g.y[j]);
-      });
-      const float ss = Thread::row_sum(dot(n, n)), ux = Thread::row_sum(dot(u, n));
-      const float r = __frsqrt_rn(fmaf(ss, 1.f / D, a.eps));
-      const float m = -(ux * r) * (1.f / D);
-      const uint64_t r2 = f2_make(r, r), m2 = f2_make(m, m);
-      each([&](int j) {
-        n.x[j] = f2_mul(n.x[j], r2);
-        n.y[j] = f2_mul(n.y[j], r2);
-        dg.x[j] = f2_fma(v.x[j], n.x[j], dg.x[j]);
-        dg.y[j] = f2_fma(v.y[j], n.y[j], dg.y[j]);
-        v.x[j] = f2_mul(r2, f2_fma(n.x[j], m2, u.x[j]));
-        v.y[j] = f2_mul(r2, f2_fma(n.y[j], m2, u.y[j]));
-      });
-      if (th.live) store_pairs<kInter>(dst + at + i * step, th.chunk, v);
-    }
-    now = next;
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[k][h] = th.live ? *slot(head, k, h) : make_uint4(0u, 0u, 0u, 0u);
+    Pairs v = unpack_pairs<kInter>(w[0]), n = unpack_pairs<kInter>(w[1]), u;
+    th.rotate(v);
+    each([&](int j) {
+      u.x[j] = f2_mul(v.x[j], g.x[j]);
+      u.y[j] = f2_mul(v.y[j], g.y[j]);
+    });
+    const float ss = Thread::row_sum(dot(n, n)), ux = Thread::row_sum(dot(u, n));
+    const float r = __frsqrt_rn(fmaf(ss, 1.f / D, a.eps));
+    const float m = -(ux * r) * (1.f / D);
+    const uint64_t r2 = f2_make(r, r), m2 = f2_make(m, m);
+    each([&](int j) {
+      n.x[j] = f2_mul(n.x[j], r2);
+      n.y[j] = f2_mul(n.y[j], r2);
+      dg.x[j] = f2_fma(v.x[j], n.x[j], dg.x[j]);
+      dg.y[j] = f2_fma(v.y[j], n.y[j], dg.y[j]);
+      v.x[j] = f2_mul(r2, f2_fma(n.x[j], m2, u.x[j]));
+      v.y[j] = f2_mul(r2, f2_fma(n.y[j], m2, u.y[j]));
+    });
+    if (th.live) store_pairs<kInter>(dst + at, th.chunk, v);
   }
   // The warp's tokens, then the block's warps; channels as unpack_pairs has them.
   float f[16];
@@ -446,7 +464,9 @@ cudaError_t launch_rope_norm_bwd(const Rope& t, const uint16_t* dq_rot, const ui
   a.part = part;
   auto kernel = t.d == 64 ? (t.interleaved ? rope_norm_bwd_kernel<64, true> : rope_norm_bwd_kernel<64, false>)
                           : (t.interleaved ? rope_norm_bwd_kernel<128, true> : rope_norm_bwd_kernel<128, false>);
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(s.blocks())), dim3(kThreads), 0, st, a);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(s.blocks())), dim3(kThreads), kRingBytes, st, a);
 }
 
 cudaError_t launch_rope_gains(const Rope& t, const float* part, float* dgq, float* dgk, cudaStream_t st) {
