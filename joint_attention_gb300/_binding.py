@@ -146,7 +146,7 @@ def load_library(path: str | None = None, build_if_missing: bool = False) -> cty
 
 
 KERNEL_KINDS = 6
-TOKEN_KERNEL_KINDS = range(16, 28)  # the token-row kernels' kinds, numbered apart
+TOKEN_KERNEL_KINDS = range(16, 29)  # the token-row kernels' kinds, numbered apart
 
 
 def jattn_profile_enable(on: bool = True) -> int:

@@ -213,6 +213,7 @@ struct BwdUnitGrouped {
   int h0;        // its first query head
   int per_head;  // query tiles of each
   int n;         // in all
+  int part;      // which part of the kv head's query heads these are
   int j, nkt, row0, end, prow0, ord;  // as in BwdUnit
   // (Causal: the first query tile of each head holds the key tile's own rows, of which a
   // key reaches the queries from its own on.)
@@ -291,21 +292,33 @@ struct BwdWorkGrouped {
   static constexpr bool kGrouped = true, kCausal = kC;
   using Ragged = RaggedMaps;
   int units;
-  int group;  // query heads of each kv head
+  int parts;  // of a kv head's query heads, a unit of each key tile for each part
+  int group;  // query heads of a part
   int ord;
   struct {
     int rows, prows;
   } seg;
-  GroupedOrder<kC> order;
+  GroupedOrder<kC> order;  // its heads: the kv heads' parts
+  // Where parts are joined, fp32 [parts][dk, dv][kv heads][rows][d].
+  __device__ __forceinline__ size_t tensor(size_t rows, int d) const { return order.heads / parts * rows * d; }
+  __device__ __forceinline__ size_t part_row(const BwdUnitGrouped<kC>& un, size_t rows, int d) const {
+    return 2 * un.part * tensor(rows, d);
+  }
   __device__ __forceinline__ BwdUnitGrouped<kC> unit(int u) const {
     BwdUnitGrouped<kC> r;
     int s, level;
     order.unit(u, &s, &r.bh, &level);
-    r.h0 = r.bh * group;
     r.nkt = order.blocks[s];
     r.j = kC ? r.nkt - 1 - level : level;
     r.per_head = kC ? level + 1 : r.nkt;
     r.n = r.per_head * group;
+    r.h0 = r.bh * group;
+    r.part = 0;
+    if (parts > 1) {
+      const int kv = r.bh / parts;
+      r.part = r.bh - kv * parts;
+      r.bh = kv;
+    }
     r.row0 = order.start[s];
     r.end = r.row0 + order.len[s];
     r.prow0 = order.prow[s];
@@ -1209,6 +1222,29 @@ __device__ __forceinline__ uint4 scaled8(const uint32_t (&a)[32], int at, float 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// A part's dK or dV row, times `scale`, in fp32 to where the parts are joined: 32 columns
+// of the accumulator at a time, its last ones released through `freed`.
+template <int D>
+__device__ __forceinline__ void store_part(uint32_t t, float* row, bool live, float scale, uint64_t* freed) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t a[32];
+    tmem_ld32(t + c * 32, a);
+    tmem_wait_ld();
+    if (c == D / 32 - 1) {
+      tc_fence_before();
+      mbar_arrive(freed);
+    }
+    if (live) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        *reinterpret_cast<float4*>(row + c * 32 + e) =
+            make_float4(__uint_as_float(a[e]) * scale, __uint_as_float(a[e + 1]) * scale,
+                        __uint_as_float(a[e + 2]) * scale, __uint_as_float(a[e + 3]) * scale);
+    }
+  }
+}
+
 // d = 128, warps 8-11 (one thread per query row, then per key row).
 // Per query tile: dQ_t out of TMEM in four 32-column quarters, staged as
 // 128 x 32 fp32 tiles with the 128-byte swizzle (16-byte chunk c of row r at
@@ -1406,6 +1442,14 @@ __device__ void bwd_drain128(uint8_t* sm, BwdBars& bars, uint32_t tmem, const W&
     const int n = un.kv0() + r128;  // key row of this thread
     const bool key_live = n < un.end;
     const size_t row_off = (static_cast<size_t>(bh) * rows + (key_live ? n : 0)) * D;
+    if constexpr (W::kGrouped) {
+      if (w.parts > 1) {
+        float* part = dgk_part + w.part_row(un, rows, D) + row_off;
+        store_part<D>(tmem + lane_base + C::kColDV, part + w.tensor(rows, D), key_live, 1.f, &bars.acc_free_v);
+        store_part<D>(tDK, part, key_live, scale, &bars.acc_free_k);
+        continue;
+      }
+    }
     const float r = !W::kGrouped && key_live ? rk[static_cast<size_t>(bh) * rows + n] : 0.f;
     const uint4* krow = W::kGrouped ? nullptr : reinterpret_cast<const uint4*>(k_raw + row_off);
     uint4* dvrow = reinterpret_cast<uint4*>(dv + row_off);
@@ -1604,6 +1648,15 @@ __device__ void bwd_epilogue_warps(uint8_t* sm, BwdBars& bars, uint32_t tmem, co
     if (ok) ok = mbar_wait(&bars.kv_mmadone[b], (ui / C::kKVBufs) & 1, ab, dev_err);
     if (!(ok = __all_sync(0xffffffffu, ok))) break;
     tc_fence_after();
+    if constexpr (W::kGrouped) {
+      if (w.parts > 1) {
+        float* part = dgk_part + w.part_row(un, rows, D) + tile_off + static_cast<size_t>(r128) * D;
+        store_part<D>(tmem + lane_base + C::kColDV, part + w.tensor(rows, D), key_live, 1.f, &bars.acc_free_v);
+        store_part<D>(tDK, part, key_live, scale, &bars.acc_free_k);
+        if (r128 == 0) mbar_arrive(&bars.kv_empty[b]);
+        continue;
+      }
+    }
     // The raw k tile into the unit's K buffer by TMA (the MMAs are done with
     // it), in the same 128-byte swizzled layout the tile had.  Rows past the
     // segment (zero-filled past the tensor's end, the next sequence's rows in
@@ -2022,47 +2075,118 @@ cudaError_t launch_bwd_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
                                counters, dgk_part, dev_err, st);
 }
 
-// dq of grouped heads: bf16(scale dS K) from the fp32 accumulator, the rows of the
-// sequences alone.  Bound by HBM: 6 bytes a value, read and written once.
-constexpr int kDqThreads = 256, kDqChunks = 4;  // 8-value chunks of a thread
-__global__ void __launch_bounds__(kDqThreads) grouped_dq_kernel(const float4* __restrict__ acc, uint4* __restrict__ dq,
-                                                                int64_t head_chunks, int64_t chunks, float scale) {
+// bf16(scale (the sum of the parts)) of fp32 accumulators, the rows of the sequences
+// alone: dq of grouped heads, and their dk and dv (blockIdx.z) where these come in parts.
+// Bound by HBM: every value is read and written once.
+constexpr int kRoundThreads = 256, kRoundChunks = 4;  // 8-value chunks of a thread
+struct RoundArgs {
+  const float4* acc[2];
+  uint4* out[2];
+  int parts;
+  int64_t part_chunks;  // from one part to the next
+  int64_t head_chunks, chunks;  // of a head in memory; of its rows that are wanted
+  float scale;
+};
+__global__ void __launch_bounds__(kRoundThreads) grouped_round_kernel(const __grid_constant__ RoundArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t head = static_cast<int64_t>(blockIdx.y) * head_chunks;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kDqThreads * kDqChunks) + threadIdx.x;
-  float4 a[kDqChunks][2];
+  const float4* acc = blockIdx.z ? a.acc[1] : a.acc[0];
+  uint4* out = blockIdx.z ? a.out[1] : a.out[0];
+  const int64_t head = static_cast<int64_t>(blockIdx.y) * a.head_chunks;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kRoundThreads * kRoundChunks) + threadIdx.x;
+  float4 v[kRoundChunks][2];
+  auto load = [&](int part, int i, int h) { return acc[(part * a.part_chunks + head + first + i * kRoundThreads) * 2 + h]; };
 #pragma unroll
-  for (int i = 0; i < kDqChunks; ++i) {
-    const int64_t c = first + i * kDqThreads;
-    if (c < chunks) {
-      a[i][0] = acc[(head + c) * 2];
-      a[i][1] = acc[(head + c) * 2 + 1];
+  for (int i = 0; i < kRoundChunks; ++i)
+    if (first + i * kRoundThreads < a.chunks) {
+      v[i][0] = load(0, i, 0);
+      v[i][1] = load(0, i, 1);
     }
-  }
+  for (int p = 1; p < a.parts; ++p)
 #pragma unroll
-  for (int i = 0; i < kDqChunks; ++i) {
-    const int64_t c = first + i * kDqThreads;
-    if (c < chunks)
-      dq[head + c] = make_uint4(pack_bf16x2(a[i][0].x * scale, a[i][0].y * scale),
-                                pack_bf16x2(a[i][0].z * scale, a[i][0].w * scale),
-                                pack_bf16x2(a[i][1].x * scale, a[i][1].y * scale),
-                                pack_bf16x2(a[i][1].z * scale, a[i][1].w * scale));
+    for (int i = 0; i < kRoundChunks; ++i)
+      if (first + i * kRoundThreads < a.chunks) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 x = load(p, i, h);
+          v[i][h] = make_float4(v[i][h].x + x.x, v[i][h].y + x.y, v[i][h].z + x.z, v[i][h].w + x.w);
+        }
+      }
+#pragma unroll
+  for (int i = 0; i < kRoundChunks; ++i) {
+    const float4 lo = v[i][0], hi = v[i][1];
+    if (first + i * kRoundThreads < a.chunks)
+      out[head + first + i * kRoundThreads] =
+          make_uint4(pack_bf16x2(lo.x * a.scale, lo.y * a.scale), pack_bf16x2(lo.z * a.scale, lo.w * a.scale),
+                     pack_bf16x2(hi.x * a.scale, hi.y * a.scale), pack_bf16x2(hi.z * a.scale, hi.w * a.scale));
   }
 }
 
 }  // namespace
 
-cudaError_t launch_grouped_dq(const GroupedShape& s, const float* dqacc, uint16_t* dq, cudaStream_t st) {
-  const int64_t row = s.d / 8, chunks = s.seg.cu[s.seg.n] * row, block = kDqThreads * kDqChunks;
-  return launch_pdl(grouped_dq_kernel, dim3(static_cast<unsigned>((chunks + block - 1) / block), s.Hq),
-                    dim3(kDqThreads), 0, st, reinterpret_cast<const float4*>(dqacc), reinterpret_cast<uint4*>(dq),
-                    s.T * row, chunks, s.scale);
+int grouped_parts(const GroupedShape& s) {
+  // In query tiles: of a CTA if all were equally busy, and of the heaviest unit.  152 CTAs
+  // whatever the device and its limit are, because the work buffer's size goes by it.
+  const int group = s.Hq / s.Hk;
+  int64_t all = 0, most = 0;
+  for (int i = 0; i < s.seg.n; ++i) {
+    const int64_t nkt = (s.seg.pcu[i + 1] - s.seg.pcu[i]) / 128;
+    all += s.causal ? nkt * (nkt + 1) / 2 : nkt * nkt;
+    most = nkt * group > most ? nkt * group : most;
+  }
+  const double even = static_cast<double>(all) * s.Hq / 152;
+  // A query tile takes some 2.4 us at d = 128, half at 64, the time of 122 d KB of HBM
+  // traffic; a part writes and reads 16 bytes for each value of k, and the join is a
+  // launch more.
+  const double tile = 122e3 * s.d, part = 16.0 * s.Hk * s.T * s.d, launch = 2e7;
+  int best = 1;
+  double least = (most > even ? most : even) * tile;
+  for (int p = 2; p <= group && p <= 16; ++p) {
+    if (group % p != 0) continue;
+    const double unit = static_cast<double>(most) / p;
+    const double cost = (unit > even ? unit : even) * tile + p * part + launch;
+    if (cost < least) {
+      least = cost;
+      best = p;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_grouped_round(const GroupedShape& s, const float* dqacc, uint16_t* dq, cudaStream_t st) {
+  const int64_t row = s.d / 8, block = kRoundThreads * kRoundChunks;
+  RoundArgs a = {};
+  a.acc[0] = reinterpret_cast<const float4*>(dqacc);
+  a.out[0] = reinterpret_cast<uint4*>(dq);
+  a.parts = 1;
+  a.head_chunks = s.T * row;
+  a.chunks = s.seg.cu[s.seg.n] * row;
+  a.scale = s.scale;
+  return launch_pdl(grouped_round_kernel, dim3(static_cast<unsigned>((a.chunks + block - 1) / block), s.Hq, 1),
+                    dim3(kRoundThreads), 0, st, a);
+}
+
+cudaError_t launch_grouped_join(const GroupedShape& s, const float* part, int parts, uint16_t* dk, uint16_t* dv,
+                                cudaStream_t st) {
+  const int64_t row = s.d / 8, block = kRoundThreads * kRoundChunks, tensor = static_cast<int64_t>(s.Hk) * s.T * row;
+  RoundArgs a = {};
+  a.acc[0] = reinterpret_cast<const float4*>(part);
+  a.acc[1] = a.acc[0] + 2 * tensor;
+  a.out[0] = reinterpret_cast<uint4*>(dk);
+  a.out[1] = reinterpret_cast<uint4*>(dv);
+  a.parts = parts;
+  a.part_chunks = 2 * tensor;
+  a.head_chunks = s.T * row;
+  a.chunks = s.seg.cu[s.seg.n] * row;
+  a.scale = 1.f;
+  return launch_pdl(grouped_round_kernel, dim3(static_cast<unsigned>((a.chunks + block - 1) / block), s.Hk, 2),
+                    dim3(kRoundThreads), 0, st, a);
 }
 
 cudaError_t launch_attn_bwd_grouped(const GroupedShape& s, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                     const uint16_t* dout, const uint16_t* stats, float* dqacc, uint32_t* counters,
-                                    uint16_t* dk, uint16_t* dv, uint32_t* dev_err, cudaStream_t st) {
+                                    uint16_t* dk, uint16_t* dv, float* part, int parts, uint32_t* dev_err,
+                                    cudaStream_t st) {
   CUtensorMap mq, mk, mv, mdo, mstats, mdq, mdk, mdv;
   if (!encode_bhnd_map(&mq, q, s.Hq, s.T, s.d) || !encode_bhnd_map(&mk, k, s.Hk, s.T, s.d) ||
       !encode_bhnd_map(&mv, v, s.Hk, s.T, s.d) || !encode_bhnd_map(&mdo, dout, s.Hq, s.T, s.d) ||
@@ -2081,16 +2205,17 @@ cudaError_t launch_attn_bwd_grouped(const GroupedShape& s, const uint16_t* q, co
   auto run = [&](auto causal) {
     using W = BwdWorkGrouped<decltype(causal)::value>;
     W w;
-    w.group = s.Hq / s.Hk;
+    w.group = s.Hq / (s.Hk * parts);
     w.ord = s.deterministic ? kDqAscending : kDqArrival;
     w.seg.rows = s.T;
     w.seg.prows = s.seg.prows;
-    w.units = w.order.make(s, kTileN, s.Hk);
+    w.parts = parts;
+    w.units = w.order.make(s, kTileN, s.Hk * parts);
     const int sms = device_sm_count(), grid = w.units < sms ? w.units : sms;
     auto launch = s.d == 64 ? (s.deterministic ? launch_bwd_w<64, true, W> : launch_bwd_w<64, false, W>)
                             : (s.deterministic ? launch_bwd_w<128, true, W> : launch_bwd_w<128, false, W>);
     return launch(w, grid, mq, mk, mv, mdo, mstats, mdq, mk, mdk, mdv, s.scale, k, nullptr, nullptr, dk, dv, dqacc,
-                  counters, nullptr, dev_err, st, mr);
+                  counters, part, dev_err, st, mr);
   };
   return s.causal ? run(std::true_type()) : run(std::false_type());
 }

@@ -1327,9 +1327,10 @@ int check_grouped(const int* cu, int n, int Hq, int Hk, int T, int d, GroupedSha
 bool scale_ok(float scale) { return scale >= 0x1p-20f && scale <= 0x1p20f; }
 
 // A grouped call's tensors in bytes, and its work buffer: the statistics chunks, the
-// fp32 dq accumulator, the dQ order counters (used in the deterministic mode alone).
+// fp32 dq accumulator, the dQ order counters (used in the deterministic mode alone), dk
+// and dv in parts (as many as a causal or a full call has).
 struct GroupedBytes {
-  size_t q, k, lse, stats, dq, counters, work;
+  size_t q, k, lse, stats, dq, counters, parts, work;
   explicit GroupedBytes(const GroupedShape& s) {
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     const size_t rows = static_cast<size_t>(s.Hq) * s.T, padded = static_cast<size_t>(s.Hq) * s.seg.prows;
@@ -1339,7 +1340,14 @@ struct GroupedBytes {
     stats = up(padded * 32);
     dq = up(rows * s.d * 4);
     counters = up(padded / 128 * 4);
-    work = stats + dq + counters;
+    GroupedShape c = s;
+    c.causal = true;
+    int p = grouped_parts(c);
+    c.causal = false;
+    const int full = grouped_parts(c);
+    p = p > full ? p : full;
+    parts = p > 1 ? static_cast<size_t>(p) * 4 * k : 0;  // two tensors, twice k's bytes each
+    work = stats + dq + counters + parts;
   }
 };
 
@@ -1406,6 +1414,8 @@ extern "C" int jattn_bwd_grouped(const jattn_bf16* q, const jattn_bf16* k, const
   uint16_t* stats = reinterpret_cast<uint16_t*>(base);
   float* dqacc = reinterpret_cast<float*>(base + n.stats);
   uint32_t* counters = reinterpret_cast<uint32_t*>(base + n.stats + n.dq);
+  float* part = reinterpret_cast<float*>(base + n.stats + n.dq + n.counters);
+  const int parts = grouped_parts(s);
   cudaError_t ce;
   {
     Timed t(JATTN_KERNEL_BWD_PREP, st);
@@ -1417,14 +1427,19 @@ extern "C" int jattn_bwd_grouped(const jattn_bf16* q, const jattn_bf16* k, const
   if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "bwd_prep launch", ce);
   {
     Timed t(JATTN_KERNEL_ATTN_BWD, st);
-    ce = launch_attn_bwd_grouped(s, q, k, v, dout, stats, dqacc, counters, dk, dv, err, st);
+    ce = launch_attn_bwd_grouped(s, q, k, v, dout, stats, dqacc, counters, dk, dv, part, parts, err, st);
   }
   if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "attn_bwd launch", ce);
   {
-    Timed t(JATTN_KERNEL_GROUPED_DQ, st);
-    ce = launch_grouped_dq(s, dqacc, dq, st);
+    Timed t(JATTN_KERNEL_GROUPED_ROUND, st);
+    ce = launch_grouped_round(s, dqacc, dq, st);
   }
-  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "grouped_dq launch", ce);
+  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "grouped_round launch", ce);
+  if (parts > 1) {
+    Timed t(JATTN_KERNEL_GROUPED_JOIN, st);
+    ce = launch_grouped_join(s, part, parts, dk, dv, st);
+    if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "grouped_join launch", ce);
+  }
   return JATTN_OK;
 }
 
@@ -1546,7 +1561,8 @@ extern "C" const char* jattn_kernel_name(int kind) {
     case JATTN_KERNEL_ROPE: return "rope";
     case JATTN_KERNEL_ROPE_NORM_BWD: return "rope_norm_bwd";
     case JATTN_KERNEL_ROPE_GAINS: return "rope_gains";
-    case JATTN_KERNEL_GROUPED_DQ: return "grouped_dq";
+    case JATTN_KERNEL_GROUPED_ROUND: return "grouped_round";
+    case JATTN_KERNEL_GROUPED_JOIN: return "grouped_join";
     default: return "unknown";
   }
 }

@@ -144,6 +144,28 @@ def test_backward_grouped(ja, lens, Hq, Hk, d, causal):
 
 
 @gpu
+@pytest.mark.parametrize("lens,Hq,Hk", [((1024,), 16, 1), ((700, 333), 12, 1), ((1500,), 10, 2), ((900, 0, 77), 14, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_kv_heads_whose_query_heads_are_split(ja, lens, Hq, Hk, d, causal):
+    """Few kv heads with many query heads: their gradients come in parts of the query heads, which are joined
+    in order (bit for bit again)."""
+    q, k, v, dout, cu = inputs(lens, Hq, Hk, d, 15, behind=9)
+    out, lse = ja.forward_grouped(q, k, v, cu, causal)
+    ja.jattn_profile_reset()
+    ja.jattn_profile_enable(True)
+    grads = ja.backward_grouped(q, k, v, out, lse, dout, cu, causal)
+    torch.cuda.synchronize()
+    ja.jattn_profile_enable(False)
+    joined = ja.profile_snapshot()["grouped_join"][0]
+    ja.jattn_profile_reset()
+    assert joined == 1 and ja.jattn_last_device_error() == 0
+    check_backward(*grads, q, k, v, out, dout, cu, causal)
+    again = ja.backward_grouped(q, k, v, out, lse, dout, cu, causal)
+    assert all(torch.equal(a[:, :cu[-1]], b[:, :cu[-1]]) for a, b in zip(grads[1:], again[1:]))
+
+
+@gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [True, False])
 def test_rows_behind_the_last_sequence_are_left_and_not_read(ja, d, causal):
@@ -396,7 +418,7 @@ def test_profile_counts_the_kernels(ja):
     torch.cuda.synchronize()
     ja.jattn_profile_enable(False)
     snap = ja.profile_snapshot()
-    assert [snap[n][0] for n in ("attn_fwd", "bwd_prep", "attn_bwd", "grouped_dq")] == [1, 1, 1, 1]
+    assert [snap[n][0] for n in ("attn_fwd", "bwd_prep", "attn_bwd", "grouped_round")] == [1, 1, 1, 1]
     ja.jattn_profile_reset()
 
 
