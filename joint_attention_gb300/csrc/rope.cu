@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_norm_bwd_kernel(const __grid
   Thread th(a);
   const uint4* const src[2] = {th.t ? a.src[1] : a.src[0], th.t ? a.x[1] : a.x[0]};
   uint4* dst = th.t ? a.dst[1] : a.dst[0];
-  extern __shared__ uint4 ring[];  // [kRing][gradient, x][chunk][thread]
+  extern __shared__ __align__(16) uint4 ring[];  // [kRing][gradient, x][chunk][thread]
   constexpr int kRow = D / 8;
   const int64_t step = static_cast<int64_t>(a.N) * kRow;
   int64_t at = th.row0 * kRow;
