@@ -441,8 +441,9 @@ int jattn_qkv_norm_lora(const jattn_bf16* x_img, const jattn_bf16* w_img, const 
  * jattn_bwd_grouped: the gradients of L = sum(dout * out), given the forward's out and
  * lse.  dk and dv repeat bit for bit; dq as in jattn_bwd (with
  * jattn_set_deterministic(1) bit for bit too).
- *   work : jattn_bwd_grouped_bytes(...) bytes (fp32 dq, and the rows' statistics), contents of no meaning before or after; calls that
- *           overlap on the GPU need one each.
+ *   work : jattn_bwd_grouped_bytes(...) bytes (fp32 dq, the rows' statistics, and dk and dv
+ *           in fp32 parts where query heads are split), contents of no meaning before or
+ *           after; calls that overlap on the GPU need one each.
  * jattn_bwd_grouped_bytes returns 0 for sizes the call would reject.
  */
 int jattn_fwd_grouped(const jattn_bf16* q, const jattn_bf16* k, const jattn_bf16* v, const int* cu_seqlens, int n_seqs,

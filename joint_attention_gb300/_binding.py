@@ -580,7 +580,8 @@ def jattn_layer_norm_bwd(dy, dh, h, mean, r, g, items: int, T: int, C: int, dx, 
 
 @functools.lru_cache(maxsize=1024)  # arrays that the library reads during a call, made once for equal values
 def _ints(vals: tuple):
-    return (ctypes.c_int * len(vals))(*vals)
+    # (-1, which the library refuses, where ctypes would keep the low 32 bits.)
+    return (ctypes.c_int * len(vals))(*(n if 0 <= n < 1 << 31 else -1 for n in vals))
 
 
 def _pairs_array(pairs):

@@ -365,10 +365,10 @@ __global__ void __launch_bounds__(256) ln_sum_kernel(const float* part, int item
   griddep_launch_dependents();
   griddep_wait();
   const int k = blockIdx.y, at = blockIdx.x * 8;
-  for (int item = blockIdx.z; item < items; item += gridDim.z) {
-    const float s = column_sum(part + (static_cast<size_t>(item) * parts * n_sums + k) * C + at, parts,
+  for (int64_t item = blockIdx.z; item < items; item += gridDim.z) {
+    const float s = column_sum(part + (item * parts * n_sums + k) * C + at, parts,
                                static_cast<size_t>(n_sums) * C);
-    if (threadIdx.x < 8) (k == 0 ? dg : db)[static_cast<size_t>(item) * C + at + threadIdx.x] = s;
+    if (threadIdx.x < 8) (k == 0 ? dg : db)[item * C + at + threadIdx.x] = s;
     __syncthreads();  // column_sum's memory is free again
   }
 }
@@ -404,8 +404,9 @@ int layer_norm_bwd_parts(int items, int T, int C) {
     rows = block_warps(decltype(l)::G) / decltype(l)::G;
     return cudaSuccess;
   });
-  const int most = (T / items + rows - 1) / rows, want = (kLnBwdBlocks + items - 1) / items;
-  return most < want ? most : want;
+  const int64_t most = (static_cast<int64_t>(T) / items + rows - 1) / rows;
+  const int64_t want = (static_cast<int64_t>(items) + kLnBwdBlocks - 1) / items;
+  return static_cast<int>(most < want ? most : want);
 }
 
 cudaError_t launch_layer_norm_bwd(const LayerNormBwd& t, float* part, int parts, cudaStream_t st) {

@@ -485,3 +485,17 @@ def test_grouped_validation(lib):
     size = lambda cu, *a: lib.jattn_bwd_grouped_bytes(cu, len(cu) - 1, *a)  # noqa: E731
     assert size(ints(0, 24), 4, 2, 30, 64) >= 4 * (128 * 32 + 30 * 64 * 4)
     assert size(ints(0, 24), 4, 3, 30, 64) == size(ints(0, 31), 4, 2, 30, 64) == size(ints(0, 24), 4, 2, 30, 80) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(cu=(0, 5, 2 ** 32 + 24)), dict(cu=(0, 2 ** 32, 24)), dict(cu=(2 ** 32, 5, 24)),
+                                dict(cu=(0, 5 - 2 ** 32, 24)), dict(T=2 ** 32 + 30), dict(Hq=2 ** 32 + 4), dict(d=2 ** 32 + 64)])
+def test_sizes_beyond_32_bits_are_refused(lib, kw):
+    a = {**dict(cu=(0, 5, 24), Hq=4, Hk=2, T=30, d=64), **kw}
+    sizes = a["Hq"], a["Hk"], a["T"], a["d"]
+    for call in (lambda: pkg.jattn_fwd_grouped(at(0), at(1), at(2), a["cu"], *sizes, True, 0.125, at(3), at(4), stream=0),
+                 lambda: pkg.jattn_bwd_grouped(at(0), at(1), at(2), at(3), at(4), at(5), a["cu"], *sizes, True, 0.125,
+                                               at(6), at(7), at(8), at(9), stream=0)):
+        with pytest.raises(pkg.JattnError) as e:
+            call()
+        assert e.value.status == STATUS_CODE["JATTN_ERR_INVALID_ARG"]
+    assert pkg.jattn_bwd_grouped_bytes(a["cu"], *sizes) == 0

@@ -330,3 +330,21 @@ def test_layer_norm_validation(lib):
         assert f(**kw) == code["JATTN_ERR_ALIAS"], kw
     size = lib.jattn_layer_norm_bwd_bytes
     assert size(3, 24, 64) > 0 and size(0, 24, 64) == size(5, 24, 64) == size(3, 24, 60) == size(3, 0, 64) == 0
+
+
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 8])
+def test_work_of_the_longest_calls(lib, T):
+    """304 blocks' sums of two gradients, however many the rows."""
+    assert lib.jattn_layer_norm_bwd_bytes(1, T, 64) == 304 * 2 * 64 * 4
+
+
+@pytest.mark.parametrize("T,C,items", [(2 ** 32 + 24, 64, 1), (24, 2 ** 32 + 64, 1), (24, 64, 2 ** 32 + 1)])
+def test_sizes_beyond_32_bits_are_refused(lib, T, C, items):
+    a = at
+    for call in (lambda: pkg.jattn_layer_norm(a(0), None, a(1), None, items, T, C, EPS, None, a(2), a(3), a(4), stream=0),
+                 lambda: pkg.jattn_layer_norm_bwd(a(0), None, a(1), a(2), a(3), a(4), items, T, C, a(5), a(6), a(7), a(8),
+                                                  stream=0)):
+        with pytest.raises(pkg.JattnError) as e:
+            call()
+        assert e.value.status == STATUS_CODE["JATTN_ERR_INVALID_ARG"]
+    assert pkg.jattn_layer_norm_bwd_bytes(items, T, C) == 0

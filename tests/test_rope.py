@@ -315,3 +315,17 @@ def test_rope_validation(lib):
         assert f(**kw) == code["JATTN_ERR_ALIAS"], kw
     size = lib.jattn_rope_bwd_bytes
     assert size(0, 2, 4, 2, 24, 64) > 0 and size(0, 2, 4, 0, 24, 64) == size(0, 2, 4, 2, 24, 96) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(N=2 ** 32 + 24), dict(d=2 ** 32 + 64), dict(B=2 ** 32 + 2), dict(Hk=2 ** 32 + 2),
+                                dict(pairs=(8, 2 ** 32 + 24)), dict(pairs=(8 - 2 ** 32, 24))])
+def test_sizes_beyond_32_bits_are_refused(lib, kw):
+    a = {**dict(pairs=(8, 24), B=2, Hq=4, Hk=2, N=24, d=64), **kw}
+    sizes = a["B"], a["Hq"], a["Hk"], a["N"], a["d"]
+    for call in (lambda: pkg.jattn_rope(at(0), at(1), None, None, at(2), at(3), a["pairs"], False, False, *sizes, EPS,
+                                        at(4), at(5), stream=0),
+                 lambda: pkg.jattn_rope_bwd(at(0), at(1), None, None, None, None, at(2), at(3), a["pairs"], False, False,
+                                            *sizes, EPS, at(4), at(5), None, None, None, stream=0)):
+        with pytest.raises(pkg.JattnError) as e:
+            call()
+        assert e.value.status == STATUS_CODE["JATTN_ERR_INVALID_ARG"]
