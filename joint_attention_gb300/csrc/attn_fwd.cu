@@ -99,6 +99,9 @@ struct FwdBars {
   uint64_t epi[2];  // d = 64: the query tile's O rows are staged (one arrival per warp)
   uint32_t tmem_base;
   int abort;
+  // Causal, of tile slot x: 1 + the last unit (counted by the slot) whose diagonal tile is
+  // left to the softmax threads, by the unit's parity: warps are up to one unit apart.
+  int by_rows[2][2];
 };
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
@@ -308,6 +311,14 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
   auto phase_of = [](int i) { return (uint32_t)((i / C::kSlots) & 1); };
   auto k_desc = [=](int i) { return sdesc_sw128(ring + slot_of(i) * C::kSlotBytes, 16, 1024); };
   auto v_desc = [=](int i) { return sdesc_sw128(ring + slot_of(i) * C::kSlotBytes, 16384, 1024); };
+  // A causal unit's last tile with values that no product may meet (set before its p_full).
+  int uc = 0;  // units of this slot
+  auto left_to_threads = [&](bool more) {
+    if constexpr (W::kGrouped) {
+      if constexpr (W::kCausal) return !more && *const_cast<volatile int*>(&bars.by_rows[x][uc & 1]) == uc + 1;
+    }
+    return false;
+  };
   volatile int* ab = &bars.abort;
   int jx = 0;  // key tiles this issuer has processed (its barrier phases)
   int gb = 0;  // ring items of the previous units
@@ -378,13 +389,13 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
         }
         if (!(ok = mbar_wait(&bars.p_full[x], jt & 1, ab, dev_err))) break;
         tc_fence_after();
-        issue_pv<D>(tO, tP, v_desc(iv), j > 0);
+        if (!left_to_threads(more)) issue_pv<D>(tO, tP, v_desc(iv), j > 0);
         umma_commit(&bars.pv_done[x]);
       } else {
         // P lives in the S columns: PV_X(j) must be issued before S_X(j+1).
         if (!(ok = mbar_wait(&bars.p_full[x], jt & 1, ab, dev_err))) break;
         tc_fence_after();
-        issue_pv<D>(tO, tP, v_desc(iv), j > 0);
+        if (!left_to_threads(more)) issue_pv<D>(tO, tP, v_desc(iv), j > 0);
         umma_commit(&bars.pv_done[x]);
         if (more) {
           issue_qk<D>(tS, q_desc, k_desc(ik));
@@ -406,6 +417,7 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
       }
     }
     jx += nkv;
+    ++uc;
   }
   // Every MMA this thread issued has completed once this barrier flips.
   umma_commit(&bars.drain[x]);
@@ -426,72 +438,66 @@ __device__ __forceinline__ void bf16x8(const uint4& u, float (&f)[8]) {
   }
 }
 
-// A causal row's product covers the whole key tile of its own rows, and a value of
-// a later row there that is not finite, times a probability of zero, is NaN.  So
-// a row of O that is not finite, with such a value among its tile's later rows, is
-// computed again from the rows that it sees alone (rare, and slow), into the same
-// TMEM columns.  In common: O is read once more, some 0.1 us a unit.
+// Whether a row of the V tile has a value that is not finite.
 template <int D>
-__device__ __forceinline__ void restore_masked(uint32_t tO, const FwdUnit& un, int qt0, int n, bool live, float m_ref,
-                                               float scale_log2, int rows, const FwdRaw& raw) {
-  float zero = 0.f;
+__device__ __forceinline__ bool row_not_finite(uint32_t vrow, int row) {
+  const __nv_bfloat162 zeros = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 z[4] = {zeros, zeros, zeros, zeros};
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    uint32_t o[32];
-    tmem_ld32(tO + c * 32, o);
-    tmem_wait_ld();
+  for (int i = 0; i < D / 8; ++i) {  // (in an order that keeps a warp's rows in different banks)
+    const uint4 v = ld_shared_v4(vrow + (i >> 3) * 16384 + (((i ^ row) & 7) << 4));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 32; ++e) zero = fmaf(__uint_as_float(o[e]), 0.f, zero);  // NaN, once any is not finite
+    for (int e = 0; e < 4; ++e) z[e] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), zeros, z[e]);
   }
-  bool again = live && !(zero == 0.f);
-  if (!__any_sync(0xffffffffu, again)) return;
+  const __nv_bfloat162 all = __hadd2(__hadd2(z[0], z[1]), __hadd2(z[2], z[3]));  // NaN, once any is not finite
+  return !(__low2float(all) == 0.f && __high2float(all) == 0.f);
+}
+
+// A causal row's product covers the whole key tile of its own rows, and a value of a
+// later row there that is not finite, times a probability of zero, is NaN.  So a
+// diagonal tile with such values is not multiplied (FwdBars::by_rows): each thread adds
+// its row's probabilities times the values of the rows that it sees to O in TMEM, or
+// starts O with them.  Rare, and slow (1.4 ms for such a tile of 128 channels, however
+// long the sequence is); to know costs a reading of the V tile out of shared memory for
+// each unit (64 x 77 rows, 12 heads of 64, 9.7 us instead of 9.4; 16384 rows, 910 instead of 905).
+template <int D>
+__device__ __forceinline__ void add_diagonal(uint32_t tO, const FwdUnit& un, int first, int n, bool live, bool start,
+                                             float m_ref, float scale_log2, int rows, const FwdRaw& raw) {
   const size_t kv = static_cast<size_t>(un.kvh) * rows;
   const uint4* k = reinterpret_cast<const uint4*>(raw.k + kv * D);
   const uint4* v = reinterpret_cast<const uint4*>(raw.v + kv * D);
-  const uint4* q = reinterpret_cast<const uint4*>(raw.q + (static_cast<size_t>(un.bh) * rows + (live ? n : qt0)) * D);
-  if (again) {
-    float sum = 0.f;
-    for (size_t i = (n + 1) * static_cast<size_t>(D / 8); i < static_cast<size_t>(min(qt0 + 128, un.end)) * (D / 8); ++i) {
-      float f[8];
-      bf16x8(v[i], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(f[e], 0.f, sum);
-    }
-    again = !(sum == 0.f);
-  }
-  if (!__any_sync(0xffffffffu, again)) return;
+  const uint4* q = reinterpret_cast<const uint4*>(raw.q + (static_cast<size_t>(un.bh) * rows + (live ? n : first)) * D);
   const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     uint32_t o[32];
     tmem_ld32(tO + c * 32, o);
     tmem_wait_ld();
-    if (again) {
-      float acc[32];
+    float acc[32];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-      for (int j = un.kvb; j <= n; ++j) {
-        float s = 0.f;
+    for (int e = 0; e < 32; ++e) acc[e] = start ? 0.f : __uint_as_float(o[e]);
+    for (int j = first; live && j <= n; ++j) {
+      float s = 0.f;
 #pragma unroll 1
-        for (int i = 0; i < D / 8; ++i) {
-          float a[8], b[8];
-          bf16x8(q[i], a);
-          bf16x8(k[static_cast<size_t>(j) * (D / 8) + i], b);
+      for (int i = 0; i < D / 8; ++i) {
+        float a[8], b[8];
+        bf16x8(q[i], a);
+        bf16x8(k[static_cast<size_t>(j) * (D / 8) + i], b);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
-        }
-        const float p = ex2_approx(fmaf(s, scale_log2, neg_m));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float b[8];
-          bf16x8(v[static_cast<size_t>(j) * (D / 8) + c * 4 + i], b);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[8 * i + e] = fmaf(p, b[e], acc[8 * i + e]);
-        }
+        for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
       }
+      const float p = ex2_approx(fmaf(s, scale_log2, neg_m));
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
+      for (int i = 0; i < 4; ++i) {
+        float b[8];
+        bf16x8(v[static_cast<size_t>(j) * (D / 8) + c * 4 + i], b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[8 * i + e] = fmaf(p, b[e], acc[8 * i + e]);
+      }
     }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
     __syncwarp();
     tmem_st32(tO + c * 32, o);
     tmem_wait_st();
@@ -538,6 +544,28 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
   float l = 0.f;
   for (int j = 0; j < nkv; ++j) {
     const int jt = jx + j;
+    if constexpr (W::kGrouped) {
+      // The last key tile's values, while its scores are computed: those behind the
+      // segment (another sequence's, or anything) times a probability of zero are no
+      // zeros if they are not finite, so their rows of the shared tile become zeros
+      // before the product reads it (behind the tensor's end the TMA unit has filled
+      // in zeros); causal, those of later rows likewise (add_diagonal).
+      const bool behind = nvalid_last < kTileN && un.end < w.seg.rows;
+      if (j + 1 == nkv && (W::kCausal || behind)) {
+        const int iv = gb - 2 * un.nkv + 2 * j + 1;  // the tile's ring item
+        ok = mbar_wait(&bars.full[iv % C::kSlots], (iv / C::kSlots) & 1, ab, dev_err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t vrow = smem_u32(sm + C::kOffRing + (iv % C::kSlots) * C::kSlotBytes) + row * 128;
+        if (behind && row >= nvalid_last) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) st_shared_v4(vrow + (i >> 3) * 16384 + (i & 7) * 16, 0u, 0u, 0u, 0u);
+        } else if (W::kCausal && row > 0 && row_not_finite<D>(vrow, row)) {
+          *const_cast<volatile int*>(&bars.by_rows[x][uc & 1]) = static_cast<int>(uc) + 1;
+        }
+        if (behind) fence_proxy_async_smem();
+      }
+    }
     ok = mbar_wait(&bars.s_full[x], jt & 1, ab, dev_err);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
@@ -561,22 +589,6 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (c * 32 + e >= seen) s[c][e] = __float_as_uint(-INFINITY);
-        // Values behind the segment (another sequence's, or anything) times a
-        // probability of zero are no zeros if they are not finite: their rows of
-        // the shared tile become zeros before the product reads it.  (Behind the
-        // tensor's end the TMA unit has filled in zeros.)
-        if (nvalid_last < kTileN && un.end < w.seg.rows) {
-          const int iv = gb - 2 * un.nkv + 2 * j + 1;  // the tile's ring item
-          ok = mbar_wait(&bars.full[iv % C::kSlots], (iv / C::kSlots) & 1, ab, dev_err);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (row >= nvalid_last) {
-            const uint32_t vrow = smem_u32(sm + C::kOffRing + (iv % C::kSlots) * C::kSlotBytes) + row * 128;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) st_shared_v4(vrow + (i >> 3) * 16384 + (i & 7) * 16, 0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
       }
     }
     const int nvalid = W::kGrouped || j + 1 < nkv ? kTileN : nvalid_last;
@@ -671,7 +683,10 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
   tc_fence_after();
   const float inv_l = 1.f / l;
   if constexpr (W::kGrouped) {
-    if constexpr (W::kCausal) restore_masked<D>(tO, un, qt0, n, live, m_ref, scale_log2, w.seg.rows, raw);
+    if constexpr (W::kCausal) {
+      if (*const_cast<volatile int*>(&bars.by_rows[x][uc & 1]) == static_cast<int>(uc) + 1)
+        add_diagonal<D>(tO, un, qt0, n, live, nkv == 1, m_ref, scale_log2, w.seg.rows, raw);
+    }
   }
   if (tile_store) {
     // O rows into the query tile's staging tile (128-byte swizzle: 16-byte
@@ -767,6 +782,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(&bars.epi[x], 4);
     }
     bars.abort = 0;
+    for (int x = 0; x < 2; ++x) bars.by_rows[x][0] = bars.by_rows[x][1] = 0;
     fence_mbar_init();
   }
   if (warp == 9) {

@@ -241,6 +241,42 @@ def test_later_rows_that_are_not_finite_do_not_reach_earlier_ones(ja, d, bad):
 
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("sms", [0, 3])
+def test_values_that_are_not_finite_in_every_tile(ja, d, bad, sms):
+    """Causal: one value of each 128-row tile, at its first, a middle and its last row, in units with one and two
+    tiles: rows before a sequence's first, and the other channels of all rows, are as without them."""
+    lens, at = (700, 40, 130, 257, 1), (0, 77, 127)
+    q, k, v, _, cu = inputs(lens, 6, 2, d, 43)
+    out0, lse0 = ja.forward_grouped(q, k, v, cu)
+    channel, first = d - 7, []
+    for s, n in enumerate(lens):
+        rows = [t * 128 + at[(t + s) % 3] for t in range((n + 127) // 128) if t * 128 + at[(t + s) % 3] < n]
+        first.append(cu[s] + (rows[0] if rows else n))
+        for r in rows:
+            v[:, cu[s] + r, channel] = bad
+    if sms:
+        ja.jattn_set_sm_limit(sms)
+    try:
+        out, lse = ja.forward_grouped(q, k, v, cu)
+        torch.cuda.synchronize()
+    finally:
+        ja.jattn_set_sm_limit(0)
+    assert ja.jattn_last_device_error() == 0 and torch.equal(lse, lse0)
+    for s in range(len(lens)):
+        seen = slice(first[s], cu[s + 1])
+        assert not out[:, seen, channel].isfinite().any()
+    others = [c for c in range(d) if c != channel]
+    check_forward(out[..., others], lse, q, k, v[..., others], cu, True, d ** -0.5)
+    for s in range(len(lens)):
+        rows = slice(cu[s], first[s])
+        n = first[s] - cu[s]
+        if n:
+            check_forward(out[:, rows], lse[:, rows], q[:, rows], k[:, rows], v[:, rows], [0, n], True)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
 def test_scales_and_large_scores(ja, d):
     q, k, v, dout, cu = inputs((200, 33), 2, 1, d, 51)
     for scale in (1.0, 0.01):
