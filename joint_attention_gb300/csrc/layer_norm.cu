@@ -17,11 +17,13 @@
 // m0), var = mean((h - m0)^2) - delta^2.  That also takes out m0's own rounding errors,
 // which for a row of large equal values would be all that n is made of.  Means add
 // terms that are divided by C first, so that finite rows have finite means.  (Always
-// both: 22.0 us instead of 19.7 for 17616 x 768.)
+// both: 2.3 us more of 19.7, 17616 x 768.)
 //
 // Row layout (forward) as in token_norm.cu: a row stays in the registers of 1 to 16 warps
 // between the sums and the output, every array is read and written once, arithmetic
-// in packed fp32 pairs.
+// in packed fp32 pairs.  Bound by HBM.  Measured: 16 x 1101 rows of 768 with a residual, gains
+// and biases of each item 18.2 us (108 MB, 6.0 TB/s), 8 rows 2.4; the backward of 32768 x
+// 4096 with dh 174 us (6.2 TB/s), of 333 x 1096 4.0 in two launches.
 #include <cuda_bf16.h>
 
 #include "jattn_internal.h"
@@ -71,43 +73,26 @@ struct LnArgs {
   float *mean, *r;  // or null
 };
 
-// At least four blocks an SM (five of rows up to 512, two of 16 warps), as the rows' loads need them: 32768 x
-// 4096 157 us, as the compiler has it 168, five 181.  (Two rows a warp side by side,
-// with the gains and biases that they share loaded once: 17616 x 768 20.0 instead of
-// 19.7 us, 17616 x 1024 28.9 instead of 26.1.)
-template <int V, int G>
-__global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 2 : V > 2 ? 4 : 5) layer_norm_kernel(const LnArgs a) {
-  __shared__ float2 red[2][kMaxWarps];
-  griddep_launch_dependents();
-  griddep_wait();
-  constexpr int kLanes = 32 * G, kRows = block_warps(G) / G;
-  const int lane = threadIdx.x % kLanes;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kLanes;
-  if (row >= a.T) return;  // all warps of a row
-  const int64_t base = row * a.chunks;
-  uint4 w[V];
+// w += e, rounded to bf16, is the row's h.
+template <int V>
+__device__ __forceinline__ void add_residual(const LnArgs& a, int64_t base, int lane, int lanes, uint4 (&w)[V],
+                                             const uint4 (&e)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = i * kLanes + lane;
-    w[i] = c < a.chunks ? a.x[base + c] : make_uint4(0u, 0u, 0u, 0u);
+    const int c = i * lanes + lane;
+    F8 u = unpack8(w[i]), v = unpack8(e[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u.p[j] = f2_add(u.p[j], v.p[j]);
+    w[i] = pack8(u);
+    if (c < a.chunks) a.h[base + c] = w[i];
   }
-  if (a.res) {
-    uint4 e[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = i * kLanes + lane;
-      e[i] = c < a.chunks ? a.res[base + c] : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = i * kLanes + lane;
-      F8 u = unpack8(w[i]), v = unpack8(e[i]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u.p[j] = f2_add(u.p[j], v.p[j]);
-      w[i] = pack8(u);
-      if (c < a.chunks) a.h[base + c] = w[i];
-    }
-  }
+}
+
+// Mean, r and y of a row that G warps hold in w (zeros behind its end).
+template <int V, int G>
+__device__ __forceinline__ void norm_row(const LnArgs& a, int64_t row, int lane, const uint4 (&w)[V], float2* red0,
+                                         float2* red1) {
+  constexpr int kLanes = 32 * G;
   const uint64_t inv2 = f2_make(a.inv_c, a.inv_c);
   auto halves = [](uint64_t p) {
     float lo, hi;
@@ -124,7 +109,7 @@ __global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 2 : V > 2 ? 4 : 5
       q2 = f2_fma(u.p[j], u.p[j], q2);
     }
   }
-  float2 sums = row_sums<G>(halves(s2), halves(q2), red[0]);
+  float2 sums = row_sums<G>(halves(s2), halves(q2), red0);
   const float m0 = sums.x;
   const uint64_t neg_m = f2_make(-m0, -m0);
   float delta = 0.f, var = fmaf(sums.y, a.inv_c, -m0 * m0);
@@ -141,7 +126,7 @@ __global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 2 : V > 2 ? 4 : 5
         q2 = f2_fma(d, d, q2);
       }
     }
-    sums = row_sums<G>(halves(s2), halves(q2), red[1]);
+    sums = row_sums<G>(halves(s2), halves(q2), red1);
     delta = sums.x;
     var = fmaf(sums.y, a.inv_c, -delta * delta);
     if (var < 0.f) var = 0.f;                    // (NaN stays NaN)
@@ -170,8 +155,85 @@ __global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 2 : V > 2 ? 4 : 5
 #pragma unroll
         for (int j = 0; j < 4; ++j) y.p[j] = f2_mul(y.p[j], g.p[j]);
       }
-      a.y[base + c] = pack8(y);
+      a.y[row * a.chunks + c] = pack8(y);
     }
+  }
+}
+
+// Rows of more than one warp: a row to a slot of G warps, as many blocks as that takes.
+// At least four blocks an SM (two of 16 warps), as the rows' loads need them: 32768 x 4096
+// 157 us, as the compiler has it 168, five 181.
+template <int V, int G>
+__global__ void __launch_bounds__(32 * block_warps(G), G > 8 ? 2 : 4) layer_norm_kernel(const LnArgs a) {
+  __shared__ float2 red[2][kMaxWarps];
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int kLanes = 32 * G, kRows = block_warps(G) / G;
+  const int lane = threadIdx.x % kLanes;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kLanes;
+  if (row >= a.T) return;  // all warps of a row
+  const int64_t base = row * a.chunks;
+  uint4 w[V], e[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = i * kLanes + lane;
+    w[i] = c < a.chunks ? a.x[base + c] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (a.res) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = i * kLanes + lane;
+      e[i] = c < a.chunks ? a.res[base + c] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    add_residual(a, base, lane, kLanes, w, e);
+  }
+  norm_row<V, G>(a, row, lane, w, red[0], red[1]);
+}
+
+// Rows of one warp: a block takes per_block neighbouring rows (and so the gains of one
+// item or two), its warps in turn, each with the next row on its way into its own part of
+// shared memory.  Three blocks an SM.  Measured, us (a row a warp as above / so): 16 x 1101 rows of
+// 768 with gains and biases of each item 21.5 / 18.2, 17616 x 768 with one 19.8 / 18.5, x 1024 26.2 /
+// 25.4, x 512 12.3 / 12.3; rings of 3 and 4 rows leave two blocks or one: 768 19.9 and
+// 21.1.  Of wider rows 9524 x 2048 28.4 / 28.0 but 32768 x 4096 157.6 / 166.
+constexpr int kLnRing = 2, kLnRingBlocks = 3;
+template <int V>
+constexpr int ln_ring_bytes() { return kLnRing * 2 * V * 256 * 16; }
+template <int V>
+__global__ void __launch_bounds__(256, kLnRingBlocks) layer_norm_ring_kernel(const LnArgs a, const int64_t per_block) {
+  extern __shared__ __align__(16) uint4 ring[];  // [kLnRing][x, res][V][thread]
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x % 32;
+  const int64_t start = blockIdx.x * per_block, end = min(start + per_block, a.T);
+  auto slot = [&](int s, int k, int i) { return &ring[((s * 2 + k) * V + i) * 256 + threadIdx.x]; };
+  auto load = [&](int64_t row, int s) {  // one group of copies (empty behind the last row)
+    if (row < end) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = i * 32 + lane;
+        if (c < a.chunks) {
+          cp_async16(smem_u32(slot(s, 0, i)), a.x + row * a.chunks + c);
+          if (a.res) cp_async16(smem_u32(slot(s, 1, i)), a.res + row * a.chunks + c);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  int64_t row = start + threadIdx.x / 32;
+  load(row, 0);
+  for (int s = 0; row < end; row += 8, s ^= 1) {
+    load(row + 8, s ^ 1);
+    cp_async_wait<1>();
+    uint4 w[V], e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = i * 32 + lane < a.chunks ? *slot(s, 0, i) : make_uint4(0u, 0u, 0u, 0u);
+    if (a.res) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) e[i] = i * 32 + lane < a.chunks ? *slot(s, 1, i) : make_uint4(0u, 0u, 0u, 0u);
+      add_residual(a, row * a.chunks, lane, 32, w, e);
+    }
+    norm_row<V, 1>(a, row, lane, w, nullptr, nullptr);
   }
 }
 
@@ -392,9 +454,19 @@ cudaError_t launch_layer_norm(const LayerNorm& t, cudaStream_t st) {
   a.r = t.r;
   return with_layout(a.chunks, [&](auto l) {
     using L = decltype(l);
-    constexpr int kWarps = block_warps(L::G), kRows = kWarps / L::G;
-    return launch_pdl(layer_norm_kernel<L::V, L::G>, dim3(static_cast<unsigned>((a.T + kRows - 1) / kRows)),
-                      dim3(32 * kWarps), 0, st, a);
+    if constexpr (L::G == 1) {
+      const int64_t most = (a.T + 7) / 8, grid = most < 152 * kLnRingBlocks ? most : 152 * kLnRingBlocks;
+      const int64_t per_block = (a.T + grid - 1) / grid;
+      const cudaError_t e = cudaFuncSetAttribute(layer_norm_ring_kernel<L::V>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, ln_ring_bytes<L::V>());
+      if (e != cudaSuccess) return e;
+      return launch_pdl(layer_norm_ring_kernel<L::V>, dim3(static_cast<unsigned>((a.T + per_block - 1) / per_block)),
+                        dim3(256), ln_ring_bytes<L::V>(), st, a, per_block);
+    } else {
+      constexpr int kWarps = block_warps(L::G), kRows = kWarps / L::G;
+      return launch_pdl(layer_norm_kernel<L::V, L::G>, dim3(static_cast<unsigned>((a.T + kRows - 1) / kRows)),
+                        dim3(32 * kWarps), 0, st, a);
+    }
   });
 }
 

@@ -15,13 +15,15 @@
 // turns taken off exactly; what is left, within half a turn, is off by some 2^-24 of a
 // turn for angles up to millions, where an fp32 angle would be off by 2^-24 of itself.
 // There __sinf and __cosf are off by 2^-21.2 at most, a thousandth of the output's
-// rounding to bf16 (sincospif, exact to 2^-23, takes four times their instructions).
+// rounding to bf16 (a sine exact to 2^-23 takes more instructions, for nothing here).
 //
 // Bound by HBM: every value is read and written once.  A thread keeps the cosines and
 // sines of one token's 8 pairs and takes 16 channels of that token in a run of heads
 // (and batch items, where they share positions), so that the angles are paid once a
 // run.  d / 16 threads a row; a warp covers 4 or 8 neighbouring tokens of a head,
-// contiguous in memory.  The arithmetic is in packed fp32 pairs.
+// contiguous in memory.  The arithmetic is in packed fp32 pairs.  Measured: 16 x 24 heads
+// of 64, 1101 rows, with gains 19.8 us (108 MB, 5.5 TB/s); 10 heads of 128, 4033 rows, without
+// 5.9 us; 32 tokens 2.0 us.
 #include <cuda_bf16.h>
 
 #include "fastdiv.cuh"
@@ -33,12 +35,11 @@ namespace jattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;   // rows of a thread that are loaded while as many are written
 constexpr int kMaxRun = 16;  // heads a thread takes at most
 // Blocks aimed at, by longer or shorter runs: forward all that fit at once (three an SM;
 // 1 x 10 x 4033 rows of 128 6.1 us, with 8 an SM 7.8), backward with gains' gradients
-// twice that fit (4 x 48 x 2381 rows of 128 67.1 us, 4 an SM 68.5, 12 72.8).
-constexpr int kBlocks = 152 * 3, kBlocksBwd = 152 * 6;
+// twice that fit (16 x 24 x 1101 rows of 64 31.0 us, 2 an SM 32.8, 6 32.2, 12 41.4).
+constexpr int kBlocks = 152 * 3, kBlocksBwd = 152 * 4;
 
 struct RopeArgs {
   const uint4* src[2];   // q, k (backward: their rotated gradients)
@@ -212,105 +213,101 @@ struct RopeThread {
   }
 };
 
-// Some rows of a run, of one or two tensors.
-template <int kRows, int kTensors, typename Thread>
-struct RowLoads {
-  uint4 w[kRows][kTensors][2];
-  __device__ __forceinline__ void load(const Thread& th, const uint4* const (&from)[kTensors], int64_t at, int64_t step,
-                                       int h0) {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
+// A thread's 16 channels of the rows of its run (of kTensors tensors), through shared
+// memory: kRing - 1 heads on their way while one is worked on, without registers for them.
+// (Two heads in registers loaded while two are written: 16 x 24 heads of 64, 1101 rows,
+// with gains 22.8 us instead of 19.8, 4 x 48 heads of 128, 2381 rows, 40.5 instead of 38.3;
+// backward with gains, one head ahead, 65.3 instead of 55.0, where rings of 2, 3 and 6 take
+// 59.8, 56.0 and 57.1.)
+constexpr int kRing = 4;
+template <int kTensors>
+constexpr int ring_bytes() { return kRing * kTensors * 2 * kThreads * 16; }
+template <int kTensors, typename Thread>
+struct RowRing {
+  uint4* ring;  // [kRing][kTensors][chunk][thread]
+  const uint4* from[kTensors];  // the first head's row
+  __device__ __forceinline__ uint4* slot(int head, int k, int h) const {
+    return &ring[((head % kRing * kTensors + k) * 2 + h) * kThreads + threadIdx.x];
+  }
+  // One head of the run, a group of copies of its own (empty behind the last).
+  __device__ __forceinline__ void load(const Thread& th, int head, int64_t step) const {
+    if (th.live && head < th.count) {
 #pragma unroll
       for (int k = 0; k < kTensors; ++k)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          w[i][k][h] = th.live && h0 + i < th.count ? from[k][at + i * step + th.chunk[h]] : make_uint4(0u, 0u, 0u, 0u);
+        for (int h = 0; h < 2; ++h) cp_async16(smem_u32(slot(head, k, h)), from[k] + head * step + th.chunk[h]);
+    }
+    cp_async_commit();
+  }
+  __device__ __forceinline__ void start(const Thread& th, int64_t step) const {
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) load(th, i, step);
+  }
+  // The head's values, once the load kRing - 1 heads ahead has been sent.
+  __device__ __forceinline__ void next(const Thread& th, int head, int64_t step, uint4 (&w)[kTensors][2]) const {
+    load(th, head + kRing - 1, step);
+    cp_async_wait<kRing - 1>();
+#pragma unroll
+    for (int k = 0; k < kTensors; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[k][h] = th.live ? *slot(head, k, h) : make_uint4(0u, 0u, 0u, 0u);
   }
 };
 
 template <int D, bool kInter, bool kNorm>
 __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ __align__(16) uint4 ring[];
   griddep_launch_dependents();
   griddep_wait();
   using Thread = RopeThread<D, kInter>;
   Thread th(a);
-  const uint4* const src[1] = {th.t ? a.src[1] : a.src[0]};
-  uint4* dst = th.t ? a.dst[1] : a.dst[0];
   constexpr int kRow = D / 8;  // chunks of a row
-  const int64_t step = static_cast<int64_t>(a.N) * kRow;
-  int64_t at = th.row0 * kRow;
-  RowLoads<kAhead, 1, Thread> now, next;
-  now.load(th, src, at, step, 0);
+  const int64_t step = static_cast<int64_t>(a.N) * kRow, at = th.row0 * kRow;
+  const RowRing<1, Thread> rows{ring, {(th.t ? a.src[1] : a.src[0]) + at}};
+  uint4* dst = (th.t ? a.dst[1] : a.dst[0]) + at;
+  rows.start(th, step);
   th.turns(a);
   Pairs g;
   if constexpr (kNorm) g = th.gains(th.t ? a.gain[1] : a.gain[0]);
-  for (int h0 = 0; h0 < th.count; h0 += kAhead, at += kAhead * step) {
-    next.load(th, src, at + kAhead * step, step, h0 + kAhead);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (h0 + i >= th.count) break;  // the same in the whole block
-      Pairs v = unpack_pairs<kInter>(now.w[i][0]);
-      if constexpr (kNorm) {
-        const float r = __frsqrt_rn(fmaf(Thread::row_sum(dot(v, v)), 1.f / D, a.eps));
-        const uint64_t r2 = f2_make(r, r);
-        each([&](int j) {
-          v.x[j] = f2_mul(f2_mul(v.x[j], r2), g.x[j]);
-          v.y[j] = f2_mul(f2_mul(v.y[j], r2), g.y[j]);
-        });
-      }
-      th.rotate(v);
-      if (th.live) store_pairs<kInter>(dst + at + i * step, th.chunk, v);
+  for (int head = 0; head < th.count; ++head, dst += step) {
+    uint4 w[1][2];
+    rows.next(th, head, step, w);
+    Pairs v = unpack_pairs<kInter>(w[0]);
+    if constexpr (kNorm) {
+      const float r = __frsqrt_rn(fmaf(Thread::row_sum(dot(v, v)), 1.f / D, a.eps));
+      const uint64_t r2 = f2_make(r, r);
+      each([&](int j) {
+        v.x[j] = f2_mul(f2_mul(v.x[j], r2), g.x[j]);
+        v.y[j] = f2_mul(f2_mul(v.y[j], r2), g.y[j]);
+      });
     }
-    now = next;
+    th.rotate(v);
+    if (th.live) store_pairs<kInter>(dst, th.chunk, v);
   }
 }
 
 // With gains: the rotation by -t, the backward of the RMSNorm and the block's part of
 // the gain's gradient (each thread its 16 channels over its heads, then the tokens of
-// the block in a fixed order).  The sums' registers leave none for loads ahead: these go
-// through shared memory, each thread's own 64 bytes of kRing heads (4 x 48 x 2381 rows of
-// 128, 351 MB: 54.8 us, 6.4 TB/s; rings of 2, 3 and 6 59.8, 56.0 and 57.1; the next head in
-// registers 65.3).
-constexpr int kRing = 4;
-constexpr int kRingBytes = kRing * 4 * kThreads * 16;
+// the block in a fixed order).  4 x 48 heads of 128, 2381 rows, 351 MB: 55.0 us, 6.4 TB/s.
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, 2) rope_norm_bwd_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float sums[kThreads / 32][D];
   griddep_launch_dependents();
   griddep_wait();
   using Thread = RopeThread<D, kInter>;
-  constexpr int kLanes = Thread::kLanes;
+  constexpr int kLanes = Thread::kLanes, kRow = D / 8;
   Thread th(a);
-  const uint4* const src[2] = {th.t ? a.src[1] : a.src[0], th.t ? a.x[1] : a.x[0]};
-  uint4* dst = th.t ? a.dst[1] : a.dst[0];
-  extern __shared__ __align__(16) uint4 ring[];  // [kRing][gradient, x][chunk][thread]
-  constexpr int kRow = D / 8;
-  const int64_t step = static_cast<int64_t>(a.N) * kRow;
-  int64_t at = th.row0 * kRow;
-  auto slot = [&](int head, int k, int h) { return &ring[((head % kRing * 2 + k) * 2 + h) * kThreads + threadIdx.x]; };
-  auto load = [&](int head) {  // of the run, one group each (empty behind the last)
-    if (th.live && head < th.count) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          cp_async16(smem_u32(slot(head, k, h)), src[k] + th.row0 * kRow + head * step + th.chunk[h]);
-    }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) load(i);
+  const int64_t step = static_cast<int64_t>(a.N) * kRow, at = th.row0 * kRow;
+  const RowRing<2, Thread> rows{ring, {(th.t ? a.src[1] : a.src[0]) + at, (th.t ? a.x[1] : a.x[0]) + at}};
+  uint4* dst = (th.t ? a.dst[1] : a.dst[0]) + at;
+  rows.start(th, step);
   th.turns(a);
   const Pairs g = th.gains(th.t ? a.gain[1] : a.gain[0]);
   Pairs dg = {};
-  for (int head = 0; head < th.count; ++head, at += step) {
-    load(head + kRing - 1);
-    cp_async_wait<kRing - 1>();
+  for (int head = 0; head < th.count; ++head, dst += step) {
     uint4 w[2][2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) w[k][h] = th.live ? *slot(head, k, h) : make_uint4(0u, 0u, 0u, 0u);
+    rows.next(th, head, step, w);
     Pairs v = unpack_pairs<kInter>(w[0]), n = unpack_pairs<kInter>(w[1]), u;
     th.rotate(v);
     each([&](int j) {
@@ -329,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_norm_bwd_kernel(const __grid
       v.x[j] = f2_mul(r2, f2_fma(n.x[j], m2, u.x[j]));
       v.y[j] = f2_mul(r2, f2_fma(n.y[j], m2, u.y[j]));
     });
-    if (th.live) store_pairs<kInter>(dst + at, th.chunk, v);
+    if (th.live) store_pairs<kInter>(dst, th.chunk, v);
   }
   // The warp's tokens, then the block's warps; channels as unpack_pairs has them.
   float f[16];
@@ -440,7 +437,7 @@ cudaError_t launch_rope(const Rope& t, const uint16_t* q, const uint16_t* k, uin
     a.gain[1] = t.gk;
   }
   auto kernel = t.d == 64 ? rope_of<64>(t.interleaved, norm) : rope_of<128>(t.interleaved, norm);
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(s.blocks())), dim3(kThreads), 0, st, a);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(s.blocks())), dim3(kThreads), ring_bytes<1>(), st, a);
 }
 
 int64_t rope_bwd_parts(const Rope& t, int64_t* of_q) {
@@ -464,9 +461,9 @@ cudaError_t launch_rope_norm_bwd(const Rope& t, const uint16_t* dq_rot, const ui
   a.part = part;
   auto kernel = t.d == 64 ? (t.interleaved ? rope_norm_bwd_kernel<64, true> : rope_norm_bwd_kernel<64, false>)
                           : (t.interleaved ? rope_norm_bwd_kernel<128, true> : rope_norm_bwd_kernel<128, false>);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes<2>());
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(s.blocks())), dim3(kThreads), kRingBytes, st, a);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(s.blocks())), dim3(kThreads), ring_bytes<2>(), st, a);
 }
 
 cudaError_t launch_rope_gains(const Rope& t, const float* part, float* dgq, float* dgk, cudaStream_t st) {

@@ -412,6 +412,31 @@ def test_on_another_stream_and_captured(ja):
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_calls_at_once_on_two_streams(ja, d):
+    """Each with its own tensors and work; dk and dv have no order to depend on."""
+    sets = [inputs((513, 70), 6, 1, d, 121), inputs((1, 1300), 4, 4, d, 131)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = []
+    for q, k, v, dout, cu in sets:
+        out, lse = ja.forward_grouped(q, k, v, cu)
+        want.append((out, lse, *ja.backward_grouped(q, k, v, out, lse, dout, cu)))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, (q, k, v, dout, cu) in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                out, lse = ja.forward_grouped(q, k, v, cu)
+                got[i].append((out, lse, *ja.backward_grouped(q, k, v, out, lse, dout, cu)))
+    torch.cuda.synchronize()
+    assert ja.jattn_last_device_error() == 0
+    for (q, k, v, dout, cu), ref, runs in zip(sets, want, got):
+        for run in runs:
+            assert all(torch.equal(a, b) for j, (a, b) in enumerate(zip(run, ref)) if j != 2)
+            check_backward(*run[2:], q, k, v, run[0], dout, cu, True)
+
+
+@gpu
 def test_a_block_of_the_operators(ja):
     """As they are used together: norm with each item's scale and shift, projections, QK-RMSNorm with positions,
     attention, and back; with all positions zero the joint attention with the same gains."""
