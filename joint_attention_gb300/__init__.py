@@ -333,10 +333,11 @@ def rope_backward(dq_rot, dk_rot, pos, freq, pairs, q=None, k=None, gq=None, gk=
 
 def _grouped_sizes(q, k, scale):
     """Hq, Hk, T, d of q [Hq, T, d] and k, and the scale (None: 1 / sqrt(d))."""
-    if q.dim() != 3 or k.dim() != 3 or q.shape[1:] != k.shape[1:]:
-        raise ValueError(f"q and k: expected [Hq, T, d] and [Hk, T, d], got {tuple(q.shape)} and {tuple(k.shape)}")
-    Hq, T, d = q.shape
-    return (Hq, k.shape[0], T, d), d ** -0.5 if scale is None else scale
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or qs[1] != ks[1] or qs[2] != ks[2]:
+        raise ValueError(f"q and k: expected [Hq, T, d] and [Hk, T, d], got {tuple(qs)} and {tuple(ks)}")
+    Hq, T, d = qs
+    return (Hq, ks[0], T, d), d ** -0.5 if scale is None else scale
 
 
 def forward_grouped(q, k, v, cu_seqlens, causal: bool = True, scale: float | None = None, stream=None):

@@ -719,10 +719,14 @@ def jattn_fwd_grouped(q, k, v, cu_seqlens, Hq: int, Hk: int, T: int, d: int, cau
     return rc
 
 
+@functools.lru_cache(maxsize=1024)
+def _bwd_grouped_bytes(vals: tuple, Hq: int, Hk: int, T: int, d: int) -> int:
+    return int(load_library().jattn_bwd_grouped_bytes(_ints(vals), len(vals) - 1, *map(_size, (Hq, Hk, T, d))))
+
+
 def jattn_bwd_grouped_bytes(cu_seqlens, Hq: int, Hk: int, T: int, d: int) -> int:
     """C ABI jattn_bwd_grouped_bytes: size of the work buffer of jattn_bwd_grouped (0: it rejects the sizes)."""
-    arr, n = _offsets(cu_seqlens)
-    return int(load_library().jattn_bwd_grouped_bytes(arr, n, *map(_size, (Hq, Hk, T, d))))
+    return _bwd_grouped_bytes(tuple(map(int, cu_seqlens)), Hq, Hk, T, d)
 
 
 def jattn_bwd_grouped(q, k, v, out, lse, dout, cu_seqlens, Hq: int, Hk: int, T: int, d: int, causal: bool,
