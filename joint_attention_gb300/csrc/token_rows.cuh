@@ -60,18 +60,21 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
   return v;
 }
 
-// The sum of `parts` partial sums, `step` floats apart, of each of 8 neighbouring
-// columns (a 32-byte sector) by a block of 256 threads, 32 a column, in a fixed
-// order: returned in the first 8 threads.
-__device__ __forceinline__ float column_sum(const float* from, int parts, size_t step) {
-  __shared__ float sums[32][9];
-  const int col = threadIdx.x % 8, grp = threadIdx.x / 8;
+// The sum of `parts` partial sums, `step` floats apart, of each of kCols neighbouring
+// columns (8: a 32-byte sector) by a block of 256 threads, 256 / kCols a column, in a fixed
+// order: returned in the first kCols threads.  Columns from `cols` on are not read.
+template <int kCols = 8>
+__device__ __forceinline__ float column_sum(const float* from, int parts, size_t step, int cols = kCols) {
+  constexpr int kGroups = 256 / kCols;
+  __shared__ float sums[kGroups][kCols + 1];
+  const int col = threadIdx.x % kCols, grp = threadIdx.x / kCols;
   constexpr int kAhead = 10;
+  if (kCols > 8 && col >= cols) parts = 0;
   float s = 0.f;
-  for (int p0 = grp; p0 < parts; p0 += 32 * kAhead) {
+  for (int p0 = grp; p0 < parts; p0 += kGroups * kAhead) {
     float v[kAhead];  // all on their way at once
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) v[i] = p0 + 32 * i < parts ? from[(p0 + 32 * i) * step + col] : 0.f;
+    for (int i = 0; i < kAhead; ++i) v[i] = p0 + kGroups * i < parts ? from[(p0 + kGroups * i) * step + col] : 0.f;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) s += v[i];
   }
@@ -79,7 +82,7 @@ __device__ __forceinline__ float column_sum(const float* from, int parts, size_t
   __syncthreads();
   if (grp == 0) {
 #pragma unroll
-    for (int i = 1; i < 32; ++i) s += sums[i][col];
+    for (int i = 1; i < kGroups; ++i) s += sums[i][col];
   }
   return s;
 }

@@ -96,7 +96,8 @@ def test_layer_norm(ja, T, C, with_res):
 
 
 @gpu
-@pytest.mark.parametrize("items,rows,C", [(2, 1, 8), (16, 77, 768), (3, 111, 1096), (400, 3, 256), (5, 9, 4096)])
+@pytest.mark.parametrize("items,rows,C", [(2, 1, 8), (16, 77, 768), (3, 111, 1096), (400, 3, 256), (5, 9, 4096),
+                                          (20, 40, 1000), (48, 367, 328)])
 def test_gains_and_biases_of_each_item(ja, items, rows, C):
     x, g, b = randn((items, rows, C), 5), gains((items, C), 6), randn((items, C), 7, 0.3, torch.float32)
     out = ja.layer_norm(x, g, b)
