@@ -48,11 +48,12 @@ struct RopeArgs {
   const float* gain[2];  // or null
   const float* pos;      // [N, axes], or [B, N, axes]
   const float* freq;     // [P]
-  int heads[2];          // heads of a token: its batch item's, or, where they share positions, all items'
+  int heads[2];          // heads of a token: its batch item's, or, where the blocks go over N, all items'
   int chunks[2];         // runs of them
   int run;               // heads of a run
   int N;                 // tokens of an item
-  int tokens, tiles;     // tokens with positions of their own (N, or B N), blocks over them
+  int tokens, tiles;     // tokens that the blocks go over (N, or B N), blocks over them
+  bool shared;           // an item's positions are all items'
   DivU31 by_n;
   int axes, P;
   int pair_end[kMaxAxes];  // pairs before the end of each axis
@@ -123,7 +124,7 @@ __device__ __forceinline__ void each(F f) {
 template <int D, bool kInter>
 struct RopeThread {
   static constexpr int kLanes = D / 16, kTokens = kThreads / kLanes;
-  int t, run, count, token;        // tensor (0: q, 1: k); the run of heads, how many
+  int t, run, count, token, pos;   // tensor (0: q, 1: k); the run of heads, how many; its positions' place
   int chunk[2];                    // the thread's 16-byte chunks of a row
   bool live, rot[2];               // whether the pairs of its halves turn
   int64_t row0;                    // the first head's row
@@ -140,6 +141,7 @@ struct RopeThread {
     live = token < a.tokens;
     const int item = static_cast<int>(a.by_n.div(static_cast<uint32_t>(token)));
     row0 = (static_cast<int64_t>(item) * heads + first) * a.N + (token - item * a.N);
+    pos = a.shared ? token - item * a.N : token;
     const int l = threadIdx.x % kLanes;
     if (kInter) {
       chunk[0] = l;
@@ -157,9 +159,9 @@ struct RopeThread {
   __device__ __forceinline__ void turns(const RopeArgs& a) {
     const int l = threadIdx.x % kLanes;
     float at[kMaxAxes], co[8], si[8];
-    const float* pos = a.pos + static_cast<int64_t>(token) * a.axes;
+    const float* from = a.pos + static_cast<int64_t>(pos) * a.axes;
 #pragma unroll
-    for (int i = 0; i < kMaxAxes; ++i) at[i] = live && i < a.axes ? __ldg(pos + i) : 0.f;
+    for (int i = 0; i < kMaxAxes; ++i) at[i] = live && i < a.axes ? __ldg(from + i) : 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       co[k] = 1.f;
@@ -386,9 +388,15 @@ struct Split {
 Split split_of(const Rope& t, int aim) {
   Split s;
   const int block = kThreads / (t.d / 16);
-  s.tokens = t.per_item ? t.B * t.N : t.N;
-  s.heads[0] = t.per_item ? t.Hq : t.B * t.Hq;
-  s.heads[1] = t.per_item ? t.Hk : t.B * t.Hk;
+  // Blocks over N tokens, whose angles then serve all items, unless a fifth of their places would be
+  // empty: with gains, forward and backward, us (so / blocks over all items' tokens): 256 items of one token, 20 heads
+  // of 128, 13.3 and 19.7 / 3.4 and 4.8; 256 of 77, 24 heads of 64, 26.8 and 41.6 / 21.5 and 35.0; of 140 38.2 and
+  // 59.2 / 36.2 and 53.7.
+  const int64_t places = (static_cast<int64_t>(t.N) + block - 1) / block * block;
+  const bool items = t.per_item || places * 4 >= static_cast<int64_t>(t.N) * 5;
+  s.tokens = items ? t.B * t.N : t.N;
+  s.heads[0] = items ? t.Hq : t.B * t.Hq;
+  s.heads[1] = items ? t.Hk : t.B * t.Hk;
   s.tiles = static_cast<int>((static_cast<int64_t>(s.tokens) + block - 1) / block);
   const int64_t run = s.tiles * (static_cast<int64_t>(s.heads[0]) + s.heads[1]) / aim;
   s.run = static_cast<int>(run < 1 ? 1 : run > kMaxRun ? kMaxRun : run);
@@ -406,6 +414,7 @@ RopeArgs args_of(const Rope& t, const Split& s, float sign) {
   a.N = t.N;
   a.tokens = s.tokens;
   a.tiles = s.tiles;
+  a.shared = !t.per_item;
   a.by_n = make_div_u31(static_cast<uint32_t>(t.N));
   a.axes = t.axes;
   int end = 0;

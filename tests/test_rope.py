@@ -88,6 +88,7 @@ CASES = [
     (1, 1, 1, 1, 64, (32,), False), (3, 4, 2, 1, 128, (64,), True), (2, 12, 12, 77, 64, (16, 16), False),
     (2, 3, 1, 333, 128, (8, 28, 28), True), (1, 8, 2, 1101, 64, (5, 0, 11), False), (16, 12, 12, 65, 64, (10, 22), False),
     (2, 5, 5, 129, 128, (3, 9, 20, 8), True), (1, 33, 7, 31, 128, (8,), False), (40, 6, 2, 3, 64, (7, 17), True),
+    (50, 6, 2, 3, 128, (8, 16), False), (3, 4, 1, 200, 64, (32,), False), (70, 2, 2, 1, 64, (3, 5), False),
 ]
 
 
