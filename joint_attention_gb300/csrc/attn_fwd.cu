@@ -547,12 +547,26 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
   float l = 0.f;
   for (int j = 0; j < nkv; ++j) {
     const int jt = jx + j;
+    ok = mbar_wait(&bars.s_full[x], jt & 1, ab, dev_err);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    tc_fence_after();
+    // The whole 128-score row in registers: four loads, one wait.
+    uint32_t s[4][32];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+    tmem_wait_ld();
+    if (C::kSepP) {  // the S columns may be overwritten by S(j+1) now
+      tc_fence_before();
+      mbar_arrive(&bars.s_free[x]);
+    }
     if constexpr (W::kGrouped) {
-      // The last key tile's values, while its scores are computed: those behind the
-      // segment (another sequence's, or anything) times a probability of zero are no
-      // zeros if they are not finite, so their rows of the shared tile become zeros
-      // before the product reads it (behind the tensor's end the TMA unit has filled
-      // in zeros); causal, those of later rows likewise (add_diagonal).
+      // The last key tile's values (looked at behind the wait for its scores, whose issuer
+      // has waited for all loads before: an older load's phase of the slot would pass for
+      // this one's): those behind the segment (another sequence's, or anything) times a
+      // probability of zero are no zeros if they are not finite, so their rows of the
+      // shared tile become zeros before the product reads it (behind the tensor's end the
+      // TMA unit has filled in zeros); causal, those of later rows likewise (add_diagonal).
       const bool behind = nvalid_last < kTileN && un.end < w.seg.rows;
       if (j + 1 == nkv && (W::kCausal || behind)) {
         const int iv = gb - 2 * un.nkv + 2 * j + 1;  // the tile's ring item
@@ -568,19 +582,6 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
         }
         if (behind) fence_proxy_async_smem();
       }
-    }
-    ok = mbar_wait(&bars.s_full[x], jt & 1, ab, dev_err);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    tc_fence_after();
-    // The whole 128-score row in registers: four loads, one wait.
-    uint32_t s[4][32];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
-    tmem_wait_ld();
-    if (C::kSepP) {  // the S columns may be overwritten by S(j+1) now
-      tc_fence_before();
-      mbar_arrive(&bars.s_free[x]);
     }
     if constexpr (W::kGrouped) {
       // The last key tile: a causal row sees the keys up to its own (which, as in
