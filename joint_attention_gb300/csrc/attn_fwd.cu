@@ -120,12 +120,19 @@ struct FwdUnit {
   int end;     // one past its last row
   int nkv;     // 128-key tiles that the unit streams
   bool has_b;  // tile B has rows
+  int kvh_b;   // grouped pairs: the kv head of tile B (else -1)
+};
+// A query tile of a unit, and the key tiles that it takes of those that the unit streams.
+struct FwdTile {
+  int bh, kvh;   // heads
+  int q0;        // first row
+  int first, n;  // key tiles
 };
 
 // The [B, H, N, d] layout: one segment [0, N) per head, decoded without the
 // segment table.
 struct FwdWorkUniform {
-  static constexpr bool kGrouped = false;
+  static constexpr bool kGrouped = false, kPairs = false;
   int upc;    // 256-row blocks per head
   int units;  // heads * upc
   int nkv;    // 128-key tiles per head
@@ -146,7 +153,7 @@ struct FwdWorkUniform {
 
 // Packed variable-length layout: segments from the table.
 struct FwdWork {
-  static constexpr bool kGrouped = false;
+  static constexpr bool kGrouped = false, kPairs = false;
   int upc;    // units per head
   int units;  // heads * upc
   SegTable seg;
@@ -175,12 +182,22 @@ struct FwdWork {
 // and tile A one key tile before tile B.  Bound as the other layouts are, by the chain of
 // a tile's scores, exponentials and product (the tensor pipe is busy for 46 % of 16 x 4096
 // causal rows of 128): 16 heads on 4 of 128, sequences of 16001, 2381, 333 and 1 rows,
-// causal, 910 us, 1180 TFLOP/s.
-template <bool kC>
+// causal, 880 us, 1218 TFLOP/s.
+//
+// Segments of one tile leave tile B free.  kP: where there are more units than CTAs, and at
+// least half of the blocks are such segments', two heads of one make a unit: tile A of the one, tile
+// B of the other, each with the key tile of its own kv head, or both with that of one.
+// Measured, us (one head a unit / two): causal, 16 x 77 rows of 12 heads of 64 9.7 / 6.9, 256 x 77
+// 72.8 / 50.7, 256 x 128 rows of 16 heads on 4 of 128 123 / 96.  (With kP for all calls, whose units take longer
+// to locate: 64 x 256 rows of 12 heads of 64 35.0 / 37.0.)
+template <bool kC, bool kP>
 struct FwdWorkGrouped {
-  static constexpr bool kGrouped = true, kCausal = kC;
+  static constexpr bool kGrouped = true, kCausal = kC, kPairs = kP;
   int units;
+  int singles;      // kP: units before the pairs
+  int short_seg;    // the first segment of those with pairs
   DivU31 by_group;  // query heads of each kv head
+  DivU31 by_pairs;  // pairs of heads
   struct {
     int rows;
   } seg;
@@ -188,24 +205,44 @@ struct FwdWorkGrouped {
   __device__ __forceinline__ FwdUnit unit(int u) const {
     FwdUnit r;
     int s, level;
-    order.unit(u, &s, &r.bh, &level);
+    r.kvh_b = -1;
+    if (!kP || u < singles) {
+      order.unit(u, &s, &r.bh, &level);
+    } else {
+      const int v = u - singles, pairs = (order.heads + 1) / 2;
+      s = static_cast<int>(by_pairs.div(static_cast<uint32_t>(v)));
+      r.bh = 2 * (v - s * pairs);
+      s += short_seg;
+      level = 0;
+    }
     r.kvh = static_cast<int>(by_group.div(static_cast<uint32_t>(r.bh)));
     r.kvb = order.start[s];
     r.end = r.kvb + order.len[s];
     r.q0 = r.kvb + level * 2 * kTileM;
     r.has_b = r.q0 + kTileM < r.end;
     r.nkv = kC ? 2 * level + (r.has_b ? 2 : 1) : (order.len[s] + kTileN - 1) / kTileN;
+    if (kP && u >= singles && r.bh + 1 < order.heads) {
+      r.has_b = true;
+      r.kvh_b = static_cast<int>(by_group.div(static_cast<uint32_t>(r.bh + 1)));
+      r.nkv = r.kvh_b != r.kvh ? 2 : 1;
+    }
     return r;
   }
-  // Key tiles of tile x of the unit.
-  __device__ __forceinline__ int tiles(const FwdUnit& r, int x) const {
-    return kC && x == 0 && r.has_b ? r.nkv - 1 : r.nkv;
+  __device__ __forceinline__ FwdTile tile(const FwdUnit& r, int x) const {
+    if (kP && r.kvh_b >= 0) return {r.bh + x, x ? r.kvh_b : r.kvh, r.q0, x && r.kvh_b != r.kvh ? 1 : 0, 1};
+    return {r.bh, r.kvh, r.q0 + x * kTileM, 0, kC && x == 0 && r.has_b ? r.nkv - 1 : r.nkv};
   }
 };
+// Segments of one tile.
+int segments_of_a_tile(const GroupedShape& s) {
+  int n = 0;
+  for (int i = 0; i < s.seg.n; ++i) n += s.seg.cu[i + 1] - s.seg.cu[i] <= kTileM;
+  return n;
+}
 template <class W>
-__device__ __forceinline__ int tiles_of(const W& w, const FwdUnit& r, int x) {
-  if constexpr (W::kGrouped) return w.tiles(r, x);
-  else return r.nkv;
+__device__ __forceinline__ FwdTile tile_of(const W& w, const FwdUnit& r, int x) {
+  if constexpr (W::kGrouped) return w.tile(r, x);
+  else return {r.bh, r.kvh, r.q0 + x * kTileM, 0, r.nkv};
 }
 
 // Warp 11 (training pair): zeroes the backward's fp32 dQ accumulator rows of
@@ -244,16 +281,17 @@ __device__ void fwd_producer(const CUtensorMap* map_q, const CUtensorMap* map_k,
   bool ok = true;
   for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const FwdUnit un = w.unit(u);
-    const int bh = un.bh, q0 = un.q0;
     const bool hasB = un.has_b;
     const int per_unit = 2 * un.nkv;
     const int b = ui % C::kQBufs;
     if (ui >= C::kQBufs && !(ok = mbar_wait(&bars.q_empty[b], ((ui / C::kQBufs) - 1) & 1, ab, dev_err))) break;
     mbar_arrive_expect_tx(&bars.q_full[b], (hasB ? 2u : 1u) * C::kQTileBytes);
-    for (int x = 0; x < (hasB ? 2 : 1); ++x)
+    for (int x = 0; x < (hasB ? 2 : 1); ++x) {
+      const FwdTile tile = tile_of(w, un, x);
       for (int blk = 0; blk < D / 64; ++blk)
         tma_load_3d(sm + C::kOffQ + (b * 2 + x) * C::kQTileBytes + blk * 16384, map_q, &bars.q_full[b], blk * 64,
-                    q0 + x * 128, bh);
+                    tile.q0, tile.bh);
+    }
     ++q_issued;
     for (int i = 0; i < per_unit; ++i, ++issued) {
       const int slot = issued % C::kSlots;
@@ -261,9 +299,15 @@ __device__ void fwd_producer(const CUtensorMap* map_q, const CUtensorMap* map_k,
         break;
       mbar_arrive_expect_tx(&bars.full[slot], C::kSlotBytes);
       const CUtensorMap* m = (i & 1) ? map_v : map_k;
-      const int kv0 = un.kvb + (i >> 1) * kTileN;
+      int kv0 = un.kvb + (i >> 1) * kTileN, kvh = un.kvh;
+      if constexpr (W::kPairs) {
+        if (un.kvh_b >= 0 && i > 1) {  // a pair: tile B's own key tile
+          kv0 = un.kvb;
+          kvh = un.kvh_b;
+        }
+      }
       for (int blk = 0; blk < D / 64; ++blk)
-        tma_load_3d(sm + C::kOffRing + slot * C::kSlotBytes + blk * 16384, m, &bars.full[slot], blk * 64, kv0, un.kvh);
+        tma_load_3d(sm + C::kOffRing + slot * C::kSlotBytes + blk * 16384, m, &bars.full[slot], blk * 64, kv0, kvh);
     }
   }
   if (*ab) {
@@ -330,20 +374,33 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
   // unit's epilogue.
   bool s0_issued = false;
   bool ok = true;
+  FwdUnit next = {};  // pairs: the next unit, located once
+  if (W::kPairs && blockIdx.x < w.units) next = w.unit(blockIdx.x);
   for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
     const int b = ui % C::kQBufs;
-    const FwdUnit uo = w.unit(u);
-    const int nkv = tiles_of(w, uo, x);
-    const int g0 = gb;  // first ring item of the unit
-    gb += 2 * uo.nkv;
-    if (x == 1 && !uo.has_b) {
-      // No tile B in this unit: only release the unit's slots and Q buffer.
-      for (int i = 0; ok && i < 2 * nkv; ++i) {
-        if (!(ok = mbar_wait(&bars.full[slot_of(g0 + i)], phase_of(g0 + i), ab, dev_err))) break;
-        umma_commit(&bars.empty[slot_of(g0 + i)]);
+    const FwdUnit uo = W::kPairs ? next : w.unit(u);
+    const int un = next_unit(w, u, ui + 1);
+    if (W::kPairs && un < w.units) next = w.unit(un);
+    const FwdTile tile = tile_of(w, uo, x);
+    const int nkv = tile.n, items = 2 * uo.nkv;
+    const int u0 = gb, g0 = gb + 2 * tile.first;  // first ring item of the unit, of this tile
+    gb += items;
+    // Ring items that this tile does not use are only released.
+    auto release = [&](int from, int to) {
+      for (int i = from; ok && i < to; ++i) {
+        if (!(ok = mbar_wait(&bars.full[slot_of(u0 + i)], phase_of(u0 + i), ab, dev_err))) break;
+        umma_commit(&bars.empty[slot_of(u0 + i)]);
       }
+    };
+    if (x == 1 && !uo.has_b) {
+      // No tile B in this unit: release all of its slots and the Q buffer.
+      release(0, items);
       if (ok) umma_commit(&bars.q_empty[b]);
       continue;
+    }
+    if constexpr (W::kPairs) {
+      release(0, 2 * tile.first);
+      if (!ok) break;
     }
     const uint64_t q_desc = sdesc_sw128(smem_u32(sm + C::kOffQ + (b * 2 + x) * C::kQTileBytes), 16, 1024);
     if (!s0_issued) {
@@ -360,9 +417,9 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
     s0_issued = false;
     // The next unit, if this issuer computes a tile of it (tile B may be
     // absent): its first score product goes out early (d = 64).
-    const int un = next_unit(w, u, ui + 1);
-    const bool early_next = C::kSepP && un < w.units && (x == 0 || w.unit(un).has_b);
-    const int bn = (ui + 1) % C::kQBufs, g0n = g0 + 2 * uo.nkv;
+    const bool early_next = C::kSepP && un < w.units && (x == 0 || (W::kPairs ? next : w.unit(un)).has_b);
+    const int bn = (ui + 1) % C::kQBufs;
+    const int g0n = gb + (W::kPairs ? 2 * tile_of(w, next, x).first : 0);
     for (int j = 0; ok && j < nkv; ++j) {
       const int jt = jx + j;
       const int iv = g0 + 2 * j + 1, ik = g0 + 2 * j + 2;
@@ -412,13 +469,7 @@ __device__ void fwd_mma(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, const 
       umma_commit(&bars.empty[slot_of(iv)]);
       if (more) umma_commit(&bars.empty[slot_of(ik)]);
     }
-    if constexpr (W::kGrouped) {
-      // Tile A of a causal unit: the key tile of tile B's own rows is only released.
-      for (int i = 2 * nkv; ok && i < 2 * uo.nkv; ++i) {
-        if (!(ok = mbar_wait(&bars.full[slot_of(g0 + i)], phase_of(g0 + i), ab, dev_err))) break;
-        umma_commit(&bars.empty[slot_of(g0 + i)]);
-      }
-    }
+    if constexpr (W::kGrouped) release(2 * (tile.first + nkv), items);
     jx += nkv;
     ++uc;
   }
@@ -463,14 +514,14 @@ __device__ __forceinline__ bool row_not_finite(uint32_t vrow, int row) {
 // its row's probabilities times the values of the rows that it sees to O in TMEM, or
 // starts O with them.  Rare, and slow (1.4 ms for such a tile of 128 channels, however
 // long the sequence is); to know costs a reading of the V tile out of shared memory for
-// each unit (16 x 77 rows, 12 heads of 64, 9.7 us instead of 9.4; 16001 rows, 16 of 128, 910 instead of 905).
+// each unit (16 x 77 rows, 12 heads of 64: 0.3 of 9.7 us).
 template <int D>
-__device__ __forceinline__ void add_diagonal(uint32_t tO, const FwdUnit& un, int first, int n, bool live, bool start,
+__device__ __forceinline__ void add_diagonal(uint32_t tO, const FwdTile& tile, int n, bool live, bool start,
                                              float m_ref, float scale_log2, int rows, const FwdRaw& raw) {
-  const size_t kv = static_cast<size_t>(un.kvh) * rows;
+  const size_t kv = static_cast<size_t>(tile.kvh) * rows;
   const uint4* k = reinterpret_cast<const uint4*>(raw.k + kv * D);
   const uint4* v = reinterpret_cast<const uint4*>(raw.v + kv * D);
-  const uint4* q = reinterpret_cast<const uint4*>(raw.q + (static_cast<size_t>(un.bh) * rows + (live ? n : first)) * D);
+  const uint4* q = reinterpret_cast<const uint4*>(raw.q + (static_cast<size_t>(tile.bh) * rows + (live ? n : tile.q0)) * D);
   const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
@@ -480,7 +531,7 @@ __device__ __forceinline__ void add_diagonal(uint32_t tO, const FwdUnit& un, int
     float acc[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) acc[e] = start ? 0.f : __uint_as_float(o[e]);
-    for (int j = first; live && j <= n; ++j) {
+    for (int j = tile.q0; live && j <= n; ++j) {
       float s = 0.f;
 #pragma unroll 1
       for (int i = 0; i < D / 8; ++i) {
@@ -527,13 +578,23 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
   uint32_t us = 0;  // tiles stored through the staging buffer (epi phases)
   int gb = 0;       // ring items of the units so far (grouped)
   bool ok = true;
+  FwdUnit next = {};  // pairs: the next unit, located while the last product runs
+  if (W::kPairs && blockIdx.x < w.units) next = w.unit(blockIdx.x);
   for (int u = blockIdx.x, ui = 0; ok && u < w.units; u = next_unit(w, u, ++ui)) {
-  const FwdUnit un = w.unit(u);
+  const FwdUnit un = W::kPairs ? next : w.unit(u);
+  auto locate_next = [&] {
+    const int nu = next_unit(w, u, ui + 1);
+    if (W::kPairs && nu < w.units) next = w.unit(nu);
+  };
   gb += 2 * un.nkv;
-  if (x == 1 && !un.has_b) continue;
+  if (x == 1 && !un.has_b) {
+    locate_next();
+    continue;
+  }
   // Per-unit values, so that the tile loop keeps few of them live.
-  const int nkv = tiles_of(w, un, x);
-  const int qt0 = un.q0 + x * 128;  // the tile's first row
+  const FwdTile tile = tile_of(w, un, x);
+  const int nkv = tile.n;
+  const int qt0 = tile.q0;  // the tile's first row
   const int n = qt0 + row;
   const int nvalid_last = un.end - (un.kvb + (nkv - 1) * kTileN);  // keys of the last key tile
   const bool live = n < un.end;
@@ -541,8 +602,8 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
   // head's last row: a tile that runs past its segment into the next one
   // stores rows instead.
   const bool tile_store = C::kStageO && (qt0 + 128 <= un.end || un.end == w.seg.rows);
-  const size_t orow = static_cast<size_t>(un.bh) * rows + (live ? n : 0);  // the row's index in O / LSE
-  const int bh = un.bh;
+  const int bh = tile.bh;
+  const size_t orow = static_cast<size_t>(bh) * rows + (live ? n : 0);  // the row's index in O / LSE
   float m_ref = -INFINITY;
   float l = 0.f;
   for (int j = 0; j < nkv; ++j) {
@@ -569,7 +630,7 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
       // TMA unit has filled in zeros); causal, those of later rows likewise (add_diagonal).
       const bool behind = nvalid_last < kTileN && un.end < w.seg.rows;
       if (j + 1 == nkv && (W::kCausal || behind)) {
-        const int iv = gb - 2 * un.nkv + 2 * j + 1;  // the tile's ring item
+        const int iv = gb - 2 * un.nkv + 2 * (tile.first + j) + 1;  // the tile's ring item
         ok = mbar_wait(&bars.full[iv % C::kSlots], (iv / C::kSlots) & 1, ab, dev_err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -681,6 +742,7 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
     mbar_arrive(&bars.p_full[x]);
   }
   if (!ok) return;
+  locate_next();
   ok = mbar_wait(&bars.o_done[x], uc & 1, ab, dev_err);
   ok = __all_sync(0xffffffffu, ok);
   if (!ok) return;
@@ -689,7 +751,7 @@ __device__ void fwd_softmax(uint8_t* sm, FwdBars& bars, uint32_t tmem, int x, co
   if constexpr (W::kGrouped) {
     if constexpr (W::kCausal) {
       if (*const_cast<volatile int*>(&bars.by_rows[x][uc & 1]) == static_cast<int>(uc) + 1)
-        add_diagonal<D>(tO, un, qt0, n, live, nkv == 1, m_ref, scale_log2, w.seg.rows, raw);
+        add_diagonal<D>(tO, tile, n, live, nkv == 1, m_ref, scale_log2, w.seg.rows, raw);
     }
   }
   if (tile_store) {
@@ -893,16 +955,29 @@ cudaError_t launch_attn_fwd_grouped(const GroupedShape& s, const uint16_t* q, co
     return cudaErrorInvalidValue;
   auto bf = [](const uint16_t* p) { return reinterpret_cast<const __nv_bfloat16*>(p); };
   const FwdRaw raw{bf(q), bf(k), bf(v)};
-  auto run = [&](auto causal) {
-    using W = FwdWorkGrouped<decltype(causal)::value>;
+  auto run = [&](auto causal, auto pairs) {
+    using W = FwdWorkGrouped<decltype(causal)::value, decltype(pairs)::value>;
     W w;
-    w.by_group = make_div_u31(static_cast<uint32_t>(s.Hq / s.Hk));
+    const int group = s.Hq / s.Hk, pairs_of = (s.Hq + 1) / 2, alone = segments_of_a_tile(s);
+    w.by_group = make_div_u31(static_cast<uint32_t>(group));
+    w.by_pairs = make_div_u31(static_cast<uint32_t>(pairs_of));
     w.seg.rows = s.T;
-    w.units = w.order.make(s, 2 * kTileM, s.Hq);
+    w.units = w.singles = w.order.make(s, 2 * kTileM, s.Hq);
+    // The segments are sorted by length: those of one tile are the last ones, and their
+    // blocks the last of all.
+    w.short_seg = s.seg.n - alone;
+    if (W::kPairs) {
+      w.singles -= alone * s.Hq;
+      w.units = w.singles + alone * pairs_of;
+    }
     auto launch = s.d == 64 ? launch_fwd_w<64, W> : launch_fwd_w<128, W>;
     return launch(w, mq, mk, mv, s.Hq, s.T, s.scale, out, lse, nullptr, nullptr, dev_err, st, raw);
   };
-  return s.causal ? run(std::true_type()) : run(std::false_type());
+  int64_t blocks = 0;
+  for (int i = 0; i < s.seg.n; ++i) blocks += (s.seg.cu[i + 1] - s.seg.cu[i] + 2 * kTileM - 1) / (2 * kTileM);
+  const bool pairs = s.Hq > 1 && blocks * s.Hq > device_sm_count() && 2 * segments_of_a_tile(s) >= blocks;
+  auto with = [&](auto causal) { return pairs ? run(causal, std::true_type()) : run(causal, std::false_type()); };
+  return s.causal ? with(std::true_type()) : with(std::false_type());
 }
 
 int attn_fwd_grid(const AttnShape& s) {

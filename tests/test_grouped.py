@@ -36,6 +36,14 @@ def ja(lib):
     return pkg
 
 
+@pytest.fixture
+def sm_limit(ja):
+    """Caps the CTAs; more units than those share CTAs (and short sequences' heads units)."""
+    yield ja.jattn_set_sm_limit
+    torch.cuda.synchronize()
+    ja.jattn_set_sm_limit(0)
+
+
 def randn(shape, seed, scale=1.0, dtype=torch.bfloat16):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
@@ -131,6 +139,26 @@ def test_forward_grouped(ja, lens, Hq, Hk, d, causal):
 
 
 @gpu
+@pytest.mark.parametrize("lens", [(77,) * 5, (1, 127, 128, 129, 300), (128,), (20, 0, 513, 3, 3, 90), (5, 256, 128, 640)])
+@pytest.mark.parametrize("Hq,Hk", [(2, 2), (5, 5), (4, 2), (6, 2), (3, 1), (1, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_forward_of_more_units_than_ctas(ja, lens, Hq, Hk, d, causal):
+    """Two heads of a short sequence share a unit there: the same bits."""
+    q, k, v, _, cu = inputs(lens, Hq, Hk, d, 17, behind=5)
+    want = ja.forward_grouped(q, k, v, cu, causal)
+    ja.jattn_set_sm_limit(2)
+    try:
+        out, lse = ja.forward_grouped(q, k, v, cu, causal)
+        torch.cuda.synchronize()
+    finally:
+        ja.jattn_set_sm_limit(0)
+    assert ja.jattn_last_device_error() == 0
+    assert torch.equal(out[:, :cu[-1]], want[0][:, :cu[-1]]) and torch.equal(lse[:, :cu[-1]], want[1][:, :cu[-1]])
+    check_forward(out, lse, q, k, v, cu, causal)
+
+
+@gpu
 @pytest.mark.parametrize("lens", LENS)
 @pytest.mark.parametrize("Hq,Hk", HEADS)
 @pytest.mark.parametrize("d", [64, 128])
@@ -168,7 +196,9 @@ def test_kv_heads_whose_query_heads_are_split(ja, lens, Hq, Hk, d, causal):
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [True, False])
-def test_rows_behind_the_last_sequence_are_left_and_not_read(ja, d, causal):
+@pytest.mark.parametrize("sms", [0, 2])
+def test_rows_behind_the_last_sequence_are_left_and_not_read(ja, sm_limit, d, causal, sms):
+    sm_limit(sms)
     lens, behind = (130, 1, 77), 55
     q, k, v, dout, cu = inputs(lens, 4, 2, d, 21, behind)
     T = cu[-1]
@@ -198,7 +228,9 @@ def test_rows_behind_the_last_sequence_are_left_and_not_read(ja, d, causal):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_other_sequences_values_that_are_not_finite_do_not_reach_a_result(ja, d, causal, bad):
+@pytest.mark.parametrize("sms", [0, 2])
+def test_other_sequences_values_that_are_not_finite_do_not_reach_a_result(ja, sm_limit, d, causal, bad, sms):
+    sm_limit(sms)
     lens = (60, 200, 131, 5)
     q, k, v, dout, cu = inputs(lens, 4, 2, d, 31)
     ja.jattn_set_deterministic(True)
@@ -242,11 +274,11 @@ def test_later_rows_that_are_not_finite_do_not_reach_earlier_ones(ja, d, bad):
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-@pytest.mark.parametrize("sms", [0, 3])
-def test_values_that_are_not_finite_in_every_tile(ja, d, bad, sms):
+@pytest.mark.parametrize("lens,sms", [((700, 40, 130, 257, 1), 0), ((700, 40, 130, 257, 1), 3), ((78, 128, 100, 1, 129), 2)])
+def test_values_that_are_not_finite_in_every_tile(ja, sm_limit, d, bad, lens, sms):
     """Causal: one value of each 128-row tile, at its first, a middle and its last row, in units with one and two
     tiles: rows before a sequence's first, and the other channels of all rows, are as without them."""
-    lens, at = (700, 40, 130, 257, 1), (0, 77, 127)
+    at = (0, 77, 127)
     q, k, v, _, cu = inputs(lens, 6, 2, d, 43)
     out0, lse0 = ja.forward_grouped(q, k, v, cu)
     channel, first = d - 7, []
@@ -255,13 +287,8 @@ def test_values_that_are_not_finite_in_every_tile(ja, d, bad, sms):
         first.append(cu[s] + (rows[0] if rows else n))
         for r in rows:
             v[:, cu[s] + r, channel] = bad
-    if sms:
-        ja.jattn_set_sm_limit(sms)
-    try:
-        out, lse = ja.forward_grouped(q, k, v, cu)
-        torch.cuda.synchronize()
-    finally:
-        ja.jattn_set_sm_limit(0)
+    sm_limit(sms)
+    out, lse = ja.forward_grouped(q, k, v, cu)
     assert ja.jattn_last_device_error() == 0 and torch.equal(lse, lse0)
     for s in range(len(lens)):
         seen = slice(first[s], cu[s + 1])
