@@ -440,6 +440,32 @@ def test_on_another_stream_and_captured(ja):
 
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_heads_far_apart(ja, d, causal):
+    """Almost 2^31 values (more bytes than 32 bits count) of which two sequences at the heads' starts are used."""
+    Hq, Hk, cu = 64, 8, [0, 130, 333]
+    T = (2 ** 31 - 1) // (Hq * d)
+    small = inputs((130, 203), Hq, Hk, d, 141)[:4]
+    q, k, v, dout = (torch.empty((t.shape[0], T, d), dtype=torch.bfloat16, device="cuda") for t in small)
+    for t, u in zip((q, k, v, dout), small):
+        t[:, :333] = u
+    ja.jattn_set_deterministic(True)
+    try:
+        want = ja.forward_grouped(*small[:3], cu, causal)
+        grads0 = ja.backward_grouped(*small[:3], *want, small[3], cu, causal)
+        got = ja.forward_grouped(q, k, v, cu, causal)
+        grads = ja.backward_grouped(q, k, v, *got, dout, cu, causal)
+    finally:
+        ja.jattn_set_deterministic(False)
+    assert ja.jattn_last_device_error() == 0
+    for a, b in zip((*got, *grads), (*want, *grads0)):
+        assert torch.equal(a[:, :333], b)
+    del q, k, v, dout, t, got, grads, a
+    torch.cuda.empty_cache()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
 def test_calls_at_once_on_two_streams(ja, d):
     """Each with its own tensors and work; dk and dv have no order to depend on."""
     sets = [inputs((513, 70), 6, 1, d, 121), inputs((1, 1300), 4, 4, d, 131)]

@@ -349,3 +349,26 @@ def test_sizes_beyond_32_bits_are_refused(lib, T, C, items):
             call()
         assert e.value.status == STATUS_CODE["JATTN_ERR_INVALID_ARG"]
     assert pkg.jattn_layer_norm_bwd_bytes(items, T, C) == 0
+
+
+@gpu
+@pytest.mark.parametrize("C", [512, 1024, 4096])
+def test_more_values_than_32_bits_count(ja, C):
+    """The last rows of more than 2^31 values are as in a call of their own."""
+    T = 2 ** 31 // C + 12
+    x = torch.zeros((T, C), dtype=torch.bfloat16, device="cuda")
+    res = torch.zeros_like(x)
+    x[-12:], res[-12:] = randn((12, C), 90), randn((12, C), 91)
+    g, b = gains(C, 92), randn((C,), 93, 0.3, torch.float32)
+    y, h, mean, r = ja.layer_norm(x, g, b, res)
+    for got, want in zip((y, h, mean, r), ja.layer_norm(x[-12:], g, b, res[-12:])):
+        assert torch.equal(got[-12:], want)
+    del res, y
+    dx, dg, db = ja.layer_norm_backward(x, h, mean, r, g, x)
+    own = ja.layer_norm_backward(x[-12:], h[-12:], mean[-12:], r[-12:], g, x[-12:])
+    assert torch.equal(dx[-12:], own[0])
+    # all other rows have dy = 0; the sums' order is another one
+    for got, want, mag in ((dg, own[1], (x[-12:].abs().double() * 8).sum(0)), (db, own[2], x[-12:].abs().double().sum(0))):
+        assert ((got.double() - want.double()).abs() <= 16 * U * mag).all()
+    del x, h, mean, r, dx, own
+    torch.cuda.empty_cache()

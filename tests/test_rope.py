@@ -330,3 +330,24 @@ def test_sizes_beyond_32_bits_are_refused(lib, kw):
         with pytest.raises(pkg.JattnError) as e:
             call()
         assert e.value.status == STATUS_CODE["JATTN_ERR_INVALID_ARG"]
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_values_than_32_bits_count(ja, d):
+    """The last tokens of more than 2^31 values are as in a call of their own."""
+    N = 2 ** 30 // d + 5
+    q, k = (torch.zeros((2, 1, N, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pos, freq = torch.arange(float(N), device="cuda")[:, None], torch.rand(d // 2, device="cuda")
+    gq, gk = gains(d, 2), gains(d, 3)
+    last = lambda t: t[1:, :, -7:].contiguous()  # noqa: E731
+    for i, t in enumerate((q, k)):
+        t[1, 0, -7:] = torch.randn((7, d), generator=torch.Generator(device="cuda").manual_seed(i), device="cuda")
+    args, tail = (freq, (d // 2,)), pos[-7:].clone()  # (of an aligned address)
+    got = ja.rope(q, k, pos, *args, gq, gk)
+    assert all(torch.equal(last(a), b) for a, b in zip(got, ja.rope(last(q), last(k), tail, *args, gq, gk)))
+    back = ja.rope_backward(*got, pos, *args, q, k, gq, gk)
+    own = ja.rope_backward(last(got[0]), last(got[1]), tail, *args, last(q), last(k), gq, gk)
+    assert all(torch.equal(last(a), b) for a, b in zip(back[:2], own[:2]))
+    del q, k, got, back, own
+    torch.cuda.empty_cache()
