@@ -2147,7 +2147,7 @@ int grouped_parts(const GroupedShape& s) {
   // launch more.  (Causal, 16 heads on 4, with parts and the join / without: 8192 and 1777
   // rows of 128 575 + 23 / 617 us, 8192 rows of 64 369 + 10 / 403; 16 x 1152 rows have no
   // parts.)
-  const double tile = 122e3 * s.d, part = 16.0 * s.Hk * s.T * s.d, launch = 2e7;
+  const double tile = 122e3 * s.d, part = 16.0 * s.Hk * s.seg.cu[s.seg.n] * s.d, launch = 2e7;
   int best = 1;
   double least = (most > even ? most : even) * tile;
   for (int p = 2; p <= group && p <= 16; ++p) {
