@@ -539,7 +539,8 @@ typedef enum {
   JATTN_KERNEL_ROPE = 24,            /* rotary positions, and their backward without gains */
   JATTN_KERNEL_ROPE_NORM_BWD = 25,   /* their backward with gains: dq, dk and partial sums of dgq, dgk */
   JATTN_KERNEL_ROPE_GAINS = 26,      /* dgq, dgk from the partial sums */
-  JATTN_KERNEL_GROUPED_ROUND = 27,   /* dq of grouped heads from its accumulator (the others: ATTN_FWD, BWD_PREP, ATTN_BWD) */
+  JATTN_KERNEL_GROUPED_ROUND = 27,   /* dq of grouped heads from its accumulator, where a sequence has more than 128
+                                        rows (the others: ATTN_FWD, BWD_PREP, ATTN_BWD) */
   JATTN_KERNEL_GROUPED_JOIN = 28,    /* their dk and dv from parts */
   JATTN_TOKEN_KERNEL_END = 29
 } jattn_token_kernel_kind;

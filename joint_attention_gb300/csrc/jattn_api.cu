@@ -1416,25 +1416,26 @@ extern "C" int jattn_bwd_grouped(const jattn_bf16* q, const jattn_bf16* k, const
   uint32_t* counters = reinterpret_cast<uint32_t*>(base + n.stats + n.dq);
   float* part = reinterpret_cast<float*>(base + n.stats + n.dq + n.counters);
   const int parts = grouped_parts(s);
+  const bool direct = grouped_direct(s);
   cudaError_t ce;
   {
     Timed t(JATTN_KERNEL_BWD_PREP, st);
     // The statistics and the zeroing alone: no norm, and its operands are not looked at.
     ce = launch_bwd_prep(nullptr, nullptr, dqacc, dqacc, out, dout, lse, nullptr, nullptr, nullptr, nullptr, stats,
-                         1.f / scale, dqacc, counters, s.deterministic ? s.Hq * (s.seg.prows / 128) : 0, s.Hq, s.seg,
-                         d, err, st);
+                         1.f / scale, direct ? nullptr : dqacc, counters,
+                         s.deterministic && !direct ? s.Hq * (s.seg.prows / 128) : 0, s.Hq, s.seg, d, err, st);
   }
   if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "bwd_prep launch", ce);
   {
     Timed t(JATTN_KERNEL_ATTN_BWD, st);
-    ce = launch_attn_bwd_grouped(s, q, k, v, dout, stats, dqacc, counters, dk, dv, part, parts, err, st);
+    ce = launch_attn_bwd_grouped(s, q, k, v, dout, stats, dqacc, counters, dq, dk, dv, part, parts, err, st);
   }
   if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "attn_bwd launch", ce);
-  {
+  if (!direct) {
     Timed t(JATTN_KERNEL_GROUPED_ROUND, st);
     ce = launch_grouped_round(s, dqacc, dq, st);
+    if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "grouped_round launch", ce);
   }
-  if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "grouped_round launch", ce);
   if (parts > 1) {
     Timed t(JATTN_KERNEL_GROUPED_JOIN, st);
     ce = launch_grouped_join(s, part, parts, dk, dv, st);

@@ -216,14 +216,16 @@ cudaError_t launch_attn_fwd_grouped(const GroupedShape& s, const uint16_t* q, co
 // Parts that a kv head's query heads are split into where few heads and long sequences
 // would leave CTAs idle (1: not split; a divisor of Hq / Hk); a function of the shape alone.
 int grouped_parts(const GroupedShape& s);
-// After launch_bwd_prep on the query heads (stats, and dqacc [Hq, T, d] and counters zeroed:
-// one word per 128 padded rows of a query head).  With parts > 1 dk and dv go to part, fp32
+// Whether no sequence has more than a tile's 128 rows: launch_attn_bwd_grouped then writes dq itself.
+bool grouped_direct(const GroupedShape& s);
+// After launch_bwd_prep on the query heads (stats, and unless grouped_direct dqacc [Hq, T, d] and
+// counters zeroed: one word per 128 padded rows of a query head).  With parts > 1 dk and dv go to part, fp32
 // [parts][dk, dv][Hk, T, d], and launch_grouped_join adds the parts in order; launch_grouped_round
-// makes dq of dqacc.
+// makes dq of dqacc (unless grouped_direct).
 cudaError_t launch_attn_bwd_grouped(const GroupedShape& s, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                     const uint16_t* dout, const uint16_t* stats, float* dqacc, uint32_t* counters,
-                                    uint16_t* dk, uint16_t* dv, float* part, int parts, uint32_t* dev_err,
-                                    cudaStream_t st);
+                                    uint16_t* dq, uint16_t* dk, uint16_t* dv, float* part, int parts,
+                                    uint32_t* dev_err, cudaStream_t st);
 cudaError_t launch_grouped_round(const GroupedShape& s, const float* dqacc, uint16_t* dq, cudaStream_t st);
 cudaError_t launch_grouped_join(const GroupedShape& s, const float* part, int parts, uint16_t* dk, uint16_t* dv,
                                 cudaStream_t st);
