@@ -1420,10 +1420,8 @@ extern "C" int jattn_bwd_grouped(const jattn_bf16* q, const jattn_bf16* k, const
   cudaError_t ce;
   {
     Timed t(JATTN_KERNEL_BWD_PREP, st);
-    // The statistics and the zeroing alone: no norm, and its operands are not looked at.
-    ce = launch_bwd_prep(nullptr, nullptr, dqacc, dqacc, out, dout, lse, nullptr, nullptr, nullptr, nullptr, stats,
-                         1.f / scale, direct ? nullptr : dqacc, counters,
-                         s.deterministic && !direct ? s.Hq * (s.seg.prows / 128) : 0, s.Hq, s.seg, d, err, st);
+    ce = launch_grouped_prep(s, out, dout, lse, stats, direct ? nullptr : dqacc,
+                             s.deterministic && !direct ? counters : nullptr, st);
   }
   if (ce != cudaSuccess) return fail(JATTN_ERR_CUDA, "bwd_prep launch", ce);
   {

@@ -218,8 +218,11 @@ cudaError_t launch_attn_fwd_grouped(const GroupedShape& s, const uint16_t* q, co
 int grouped_parts(const GroupedShape& s);
 // Whether no sequence has more than a tile's 128 rows: launch_attn_bwd_grouped then writes dq itself.
 bool grouped_direct(const GroupedShape& s);
-// After launch_bwd_prep on the query heads (stats, and unless grouped_direct dqacc [Hq, T, d] and
-// counters zeroed: one word per 128 padded rows of a query head).  With parts > 1 dk and dv go to part, fp32
+// The statistics (as launch_bwd_prep's); zeroes dqacc [Hq, T, d] (null: not; rows of the sequences) and
+// counters, one word per 128 padded rows of a query head (null: not).
+cudaError_t launch_grouped_prep(const GroupedShape& s, const uint16_t* out, const uint16_t* dout, const float* lse,
+                                uint16_t* stats, float* dqacc, uint32_t* counters, cudaStream_t st);
+// After launch_grouped_prep (with dqacc unless grouped_direct).  With parts > 1 dk and dv go to part, fp32
 // [parts][dk, dv][Hk, T, d], and launch_grouped_join adds the parts in order; launch_grouped_round
 // makes dq of dqacc (unless grouped_direct).
 cudaError_t launch_attn_bwd_grouped(const GroupedShape& s, const uint16_t* q, const uint16_t* k, const uint16_t* v,
