@@ -197,9 +197,10 @@ def test_kv_heads_whose_query_heads_are_split(ja, lens, Hq, Hk, d, causal):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("sms", [0, 2])
-def test_rows_behind_the_last_sequence_are_left_and_not_read(ja, sm_limit, d, causal, sms):
+@pytest.mark.parametrize("lens", [(130, 1, 77), (128, 1, 77)])
+def test_rows_behind_the_last_sequence_are_left_and_not_read(ja, sm_limit, d, causal, sms, lens):
     sm_limit(sms)
-    lens, behind = (130, 1, 77), 55
+    behind = 55
     q, k, v, dout, cu = inputs(lens, 4, 2, d, 21, behind)
     T = cu[-1]
     clean = [t[:, :T].contiguous() for t in (q, k, v, dout)]
@@ -248,6 +249,32 @@ def test_other_sequences_values_that_are_not_finite_do_not_reach_a_result(ja, sm
     for rows in (slice(0, 60), slice(260, 391)):
         for got, want in zip((out, lse, *grads), (out0, lse0, *grads0)):
             assert torch.equal(got[:, rows], want[:, rows])
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hk", [(4, 4), (6, 2), (8, 1)])
+def test_sequences_of_one_tile_and_values_that_are_not_finite(ja, d, causal, Hq, Hk):
+    """dq comes from one contribution there: the same bits in both modes, whatever the second and fourth hold."""
+    q, k, v, dout, cu = inputs((60, 128, 131 - 64, 5, 128), Hq, Hk, d, 33)
+    out0, lse0 = ja.forward_grouped(q, k, v, cu, causal)
+    want = ja.backward_grouped(q, k, v, out0, lse0, dout, cu, causal)
+    check_backward(*want, q, k, v, out0, dout, cu, causal)
+    for t in (q, k, v, dout):
+        t[:, cu[1]:cu[2]] = float("nan")
+        t[:, cu[3]:cu[4]] = float("inf")
+    for mode in (True, False):
+        ja.jattn_set_deterministic(mode)
+        try:
+            out, lse = ja.forward_grouped(q, k, v, cu, causal)
+            got = ja.backward_grouped(q, k, v, out, lse, dout, cu, causal)
+        finally:
+            ja.jattn_set_deterministic(False)
+        assert ja.jattn_last_device_error() == 0
+        for i in (0, 2, 4):
+            for a, b in zip((out, lse, *got), (out0, lse0, *want)):
+                assert torch.equal(a[:, cu[i]:cu[i + 1]], b[:, cu[i]:cu[i + 1]])
 
 
 @gpu
